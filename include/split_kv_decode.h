@@ -50,7 +50,13 @@ extern "C" {
 
 typedef struct CUstream_st *da_stream_t; /* same type as cudaStream_t */
 
-typedef enum { DA_F32 = 0, DA_F16 = 1, DA_BF16 = 2 } da_dtype_t;
+typedef enum {
+    DA_F32 = 0,
+    DA_F16 = 1,
+    DA_BF16 = 2,
+    DA_E4M3 = 3, /* 8-bit cache codes with scales (decode_attn_splitk_8bit): 1 sign,  */
+    DA_E5M2 = 4  /* 4 exponent, 3 mantissa bits up to 448; or 1, 5, 2 up to 57344     */
+} da_dtype_t;
 
 typedef enum {
     DA_OK = 0,
@@ -139,6 +145,9 @@ typedef enum {
 #define DA_KERNEL_MLA_TC 2  /* MLA (576/512 latent): the tcgen05/TMEM split kernel,
                                and the f32 CUDA-core one for sequences shorter
                                than DA_MLA_EXACT_BELOW                          */
+#define DA_KERNEL_GQA_8BIT 4 /* 8-bit GQA/MQA split kernel (decode_attn_splitk_8bit):
+                               e4m3 or e5m2 codes with a scale per (page, KV head),
+                               head_dim 128 or 256, groups of 1 to 128 query rows  */
 #define DA_KERNEL_GQA_TC 3  /* tcgen05/TMEM split kernel for GQA/MQA work items of
                                8 to 128 query rows ((n_heads / n_kv_heads) * q_len),
                                f16 or bf16 caches, head_dim 128 or 256; q and the
@@ -154,7 +163,8 @@ typedef struct {
     int32_t capacity;    /* positions allocated per sequence; seq_lens <= it   */
     int64_t k_batch_stride, k_pos_stride, k_head_stride; /* elements            */
     int64_t v_batch_stride, v_pos_stride, v_head_stride; /* elements            */
-    int32_t kv_dtype;    /* da_dtype_t of the cache                            */
+    int32_t kv_dtype;    /* da_dtype_t of the cache (DA_E4M3, DA_E5M2: only
+                            decode_attn_splitk_8bit runs such a plan)          */
     int32_t out_dtype;   /* da_dtype_t of out (DA_F32, DA_F16 or DA_BF16)      */
     float scale;         /* score scale, usually 1/sqrt(head_dim)              */
     int32_t force_splits;/* 0: heuristic; n > 0: n splits per sequence (capped
@@ -446,6 +456,168 @@ typedef struct {
 int decode_attn_splitk_dev(const da_args_t *args, const da_plan_t *plan, const da_dev_t *dev,
                            const float *q, const void *k_cache, const void *v_cache, void *out,
                            void *workspace, size_t workspace_bytes, da_stream_t stream);
+
+/*
+ * ---- an 8-bit paged KV cache --------------------------------------------
+ * Pools of 8-bit floating-point codes [num_blocks][block_size][n_kv_heads][dim]
+ * (any strides, as in da_dev_t) with one f32 scale per (block, KV head) for the
+ * keys and one for the values: the element a code c of block i and head h
+ * stands for is c * scale[i][h]. Three calls of a decode step, each
+ * capturable in a CUDA graph:
+ *   decode_attn_grow_tables   block table and slots of the new tokens
+ *   decode_attn_append_8bit   the new rows, quantised into their slots
+ *   decode_attn_splitk_8bit   attention over the pages
+ */
+
+/*
+ * The device state of a batch's block tables. A pool block is either in one
+ * sequence's table or on the free list. Set up once by the caller: seq_lens
+ * zero, free_list any order of the blocks 0 .. num_blocks - 1, state
+ * {num_blocks, 0, 0, 0}.
+ *   seq_lens     DEVICE int32[batch]: lengths before the call
+ *   seq_lens_out DEVICE int32[batch]: lengths after it; may be seq_lens itself
+ *   block_table  DEVICE int32[batch * max_blocks_per_seq]: as in da_dev_t. A call
+ *                writes the entries of the blocks it takes, and no others
+ *   free_list    DEVICE int32[num_blocks]: a stack of free blocks, entries
+ *                0 .. state[0] - 1
+ *   state        DEVICE int32[4]: {free blocks, status, 0, 0} before the call
+ *   state_out    DEVICE int32[4], the same after it; may be state itself, otherwise
+ *                zero before the first call (word 2 counts the CTAs of a call
+ *                that have read the state, and is zero between calls)
+ * batch is at most DA_MAX_BATCH, batch * max_blocks_per_seq below 2^31, and
+ * block_size any positive number.
+ */
+typedef struct da_tables_t {
+    const int32_t *seq_lens;
+    int32_t *seq_lens_out;
+    int32_t *block_table;
+    int32_t *free_list;
+    const int32_t *state;
+    int32_t *state_out;
+    int32_t batch;
+    int32_t max_blocks_per_seq;
+    int32_t block_size;
+    int32_t num_blocks;
+} da_tables_t;
+
+/*
+ * decode_attn_grow_tables -- block tables and slot map of a step, from the
+ * request lengths, on the device.
+ *   new_lens  DEVICE int32[batch]: tokens sequence b gets in this step (0: none);
+ *             a negative number releases the sequence: its blocks go back to
+ *             the free list and its length becomes 0
+ *   slot_map  DEVICE int64[slot_capacity]: out, the slots (block * block_size +
+ *             position in the block) of the new tokens, sequence by sequence in
+ *             the order of their positions; -1 past the last one, so that a
+ *             fixed number of rows can be appended from a captured graph
+ *   cu_new    DEVICE int32[batch + 1]: out, the rows of sequence b in slot_map are
+ *             cu_new[b] .. cu_new[b + 1] - 1 (NULL: not wanted)
+ * Sequence b takes ceil((L + n) / block_size) - ceil(L / block_size) blocks,
+ * in the order of the sequences and their positions, from the top of the
+ * stack; the call's released blocks are pushed before that, in the same
+ * order, so the last released is taken first. The result is a function of
+ * the inputs alone.
+ * All or nothing: when the blocks do not suffice (DA_ENOSPACE), or a length
+ * would pass max_blocks_per_seq * block_size, the tokens do not fit slot_map,
+ * or the state is not one of these tables (DA_EINVAL), the tables, lengths and
+ * free list stay as they are, every slot is -1, cu_new is zero, and state_out[1]
+ * holds the status, until decode_attn_tables_status reads and clears it (an
+ * earlier one is kept). One launch. seq_lens, state, new_lens and free_list must
+ * not change, and no second call run on the same state, while one is in flight.
+ */
+int decode_attn_grow_tables(const da_tables_t *tables, const int32_t *new_lens,
+                            int64_t *slot_map, int64_t slot_capacity, int32_t *cu_new,
+                            da_stream_t stream);
+
+/*
+ * decode_attn_tables_status -- synchronise `stream`, then read and clear the
+ * status word state[1]. DA_OK, DA_ENOSPACE (the free list ran out), DA_EINVAL
+ * (see above), or DA_ECUDA if the synchronisation itself failed.
+ */
+int decode_attn_tables_status(int32_t *state, da_stream_t stream);
+
+/*
+ * The shapes of decode_attn_append_8bit. Strides in elements.
+ *   new rows   (token, head, d) at base + token * *_src_stride + head *
+ *              *_src_head_stride + d, of type src_dtype (DA_F32, DA_F16 or
+ *              DA_BF16); the rows of every (token, head) start 16-byte aligned
+ *   pools      as in da_dev_t, of type code_dtype (DA_E4M3 or DA_E5M2); rows start
+ *              16-byte aligned
+ *   scales     (block, head) at base + block * *_scale_block_stride + head *
+ *              *_scale_head_stride
+ * head_dim and v_dim: multiples of 16, at most 1024.
+ */
+typedef struct da_append_t {
+    int32_t n_tokens;     /* rows of k_new, v_new and slot_map; 0: nothing to do  */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t v_dim;
+    int32_t block_size;   /* any positive number                                  */
+    int32_t num_blocks;
+    int32_t src_dtype;
+    int32_t code_dtype;
+    int64_t k_src_stride, k_src_head_stride, v_src_stride, v_src_head_stride;
+    int64_t k_block_stride, k_pos_stride, k_head_stride;
+    int64_t v_block_stride, v_pos_stride, v_head_stride;
+    int64_t k_scale_block_stride, k_scale_head_stride;
+    int64_t v_scale_block_stride, v_scale_head_stride;
+} da_append_t;
+
+/*
+ * decode_attn_append_8bit -- write new K/V rows into the pages their slots name.
+ *   slot_map  DEVICE int64[n_tokens]: block * block_size + position in the block of
+ *             every row; a negative slot, or one past the pool, skips its row.
+ *             The new rows of one block must be consecutive in slot_map, at
+ *             ascending consecutive positions (as decode_attn_grow_tables
+ *             writes them), and no block may appear twice otherwise: its
+ *             contents are then undefined (other blocks are not touched).
+ * For every (block, head) with new rows, at positions p0 .. p1 - 1, keys and
+ * values each for themselves: the rows before p0 are older ones and stay, the
+ * rows from p1 on stay as they are. The scale is a power of two 2^e, with the
+ * least e >= -100 for which every finite new value is at most MAX * 2^e
+ * (MAX = 448 for e4m3, 57344 for e5m2), and at least the block's scale when it
+ * has older rows; if it grows, the older rows' codes are rescaled (rounded to
+ * nearest even; exact unless a code becomes subnormal). The new codes are
+ * x / 2^e rounded to nearest even; an infinity becomes MAX of its sign, a NaN
+ * stays NaN. A power of two costs a floating-point code no precision, and
+ * growing scales add no error. One launch.
+ */
+int decode_attn_append_8bit(const da_append_t *shapes, const void *k_new, const void *v_new,
+                            const int64_t *slot_map, void *k_pool, void *v_pool,
+                            float *k_scale, float *v_scale, da_stream_t stream);
+
+/* The scales of 8-bit pools, strides in elements: (block, head) at base + block *
+ * *_block_stride + head * *_head_stride. Any finite positive f32 from 2^-100
+ * to 2^120 (smaller value scales, zero among them, count as 2^-100). */
+typedef struct da_scales_t {
+    const float *k_scale;
+    const float *v_scale;
+    int64_t k_block_stride, k_head_stride;
+    int64_t v_block_stride, v_head_stride;
+} da_scales_t;
+
+/*
+ * decode_attn_splitk_8bit -- decode_attn_splitk_dev over 8-bit paged pools.
+ * args->kv_dtype is DA_E4M3 or DA_E5M2, v_dim == head_dim (128 or 256), and the
+ * plan was made for these args; dev->block_table is required. A contiguous cache
+ * is a pool with an identity table. Keys and values are used as the codes stand,
+ * q and the probabilities carry 20 significant bits, sums are f32.
+ * Differences to decode_attn_splitk_dev:
+ *   - a device length is clamped to [0, plan->seq_lens[b]]. A sequence of length 0
+ *     gives zeros, and so does a new token before the sequence's start (length
+ *     < q_len); nothing is read for them.
+ *   - block_table entries of positions below the length must be in
+ *     [0, num_blocks); an entry outside reads as zeros.
+ *   - DA_FLAG_ONE_LAUNCH is accepted and the combine launch merges.
+ * Codes past a sequence's length may hold anything, NaN among them. With
+ * q_len > 1 a NaN in a new token's row reaches only the tokens that see it.
+ * decode_attn_combine, _combine_ranks and _combine_proj take its partials; the
+ * other split calls refuse an 8-bit plan (DA_EUNSUPPORTED).
+ */
+int decode_attn_splitk_8bit(const da_args_t *args, const da_plan_t *plan, const da_dev_t *dev,
+                            const da_scales_t *scales, const float *q, const void *k_pool,
+                            const void *v_pool, void *out, void *workspace,
+                            size_t workspace_bytes, da_stream_t stream);
 
 /* Thread-local description of the last failure on this thread ("" if none). */
 const char *decode_attn_last_error(void);

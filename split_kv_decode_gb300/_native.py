@@ -12,7 +12,7 @@ import threading
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libsplitkv.so")
 
-DA_F32, DA_F16, DA_BF16 = 0, 1, 2
+DA_F32, DA_F16, DA_BF16, DA_E4M3, DA_E5M2 = 0, 1, 2, 3, 4
 DA_OK, DA_EINVAL, DA_EUNSUPPORTED, DA_ENOSPACE, DA_ELAUNCH, DA_ETIMEOUT, DA_ECUDA = range(7)
 STATUS_NAMES = {0: "DA_OK", 1: "DA_EINVAL", 2: "DA_EUNSUPPORTED", 3: "DA_ENOSPACE",
                 4: "DA_ELAUNCH", 5: "DA_ETIMEOUT", 6: "DA_ECUDA"}
@@ -27,7 +27,7 @@ DA_FLAG_COMBINE_LOADS = 0x40
 DA_MLA_EXACT_BELOW = 2048
 DA_FLAG_TEST_NO_TMA = 0x100
 DA_FLAG_TEST_BAD_LAUNCH = 0x200
-DA_KERNEL_GQA_TMA, DA_KERNEL_MLA_TC, DA_KERNEL_GQA_TC = 1, 2, 3
+DA_KERNEL_GQA_TMA, DA_KERNEL_MLA_TC, DA_KERNEL_GQA_TC, DA_KERNEL_GQA_8BIT = 1, 2, 3, 4
 
 
 class DaArgs(ctypes.Structure):
@@ -80,6 +80,41 @@ class DaProj(ctypes.Structure):
     ]
 
 
+class DaTables(ctypes.Structure):
+    _fields_ = [
+        ("seq_lens", ctypes.c_void_p), ("seq_lens_out", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("free_list", ctypes.c_void_p),
+        ("state", ctypes.c_void_p), ("state_out", ctypes.c_void_p),
+        ("batch", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+    ]
+
+
+class DaAppend(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("v_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+        ("src_dtype", ctypes.c_int32), ("code_dtype", ctypes.c_int32),
+        ("k_src_stride", ctypes.c_int64), ("k_src_head_stride", ctypes.c_int64),
+        ("v_src_stride", ctypes.c_int64), ("v_src_head_stride", ctypes.c_int64),
+        ("k_block_stride", ctypes.c_int64), ("k_pos_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_block_stride", ctypes.c_int64), ("v_pos_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("k_scale_block_stride", ctypes.c_int64), ("k_scale_head_stride", ctypes.c_int64),
+        ("v_scale_block_stride", ctypes.c_int64), ("v_scale_head_stride", ctypes.c_int64),
+    ]
+
+
+class DaScales(ctypes.Structure):
+    _fields_ = [
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("k_block_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_block_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+    ]
+
+
 SIGNATURES = {
     "decode_attn_plan": (ctypes.c_int, [ctypes.POINTER(DaArgs), _P, ctypes.c_int,
                                         ctypes.POINTER(DaPlan)]),
@@ -104,6 +139,14 @@ SIGNATURES = {
     "decode_attn_splitk_proj": (ctypes.c_int, [ctypes.POINTER(DaArgs), ctypes.POINTER(DaPlan),
                                                ctypes.POINTER(DaProj), _P, _P, _P, _P, _P,
                                                ctypes.c_size_t, _P]),
+    "decode_attn_grow_tables": (ctypes.c_int, [ctypes.POINTER(DaTables), _P, _P, ctypes.c_int64,
+                                               _P, _P]),
+    "decode_attn_tables_status": (ctypes.c_int, [_P, _P]),
+    "decode_attn_append_8bit": (ctypes.c_int, [ctypes.POINTER(DaAppend), _P, _P, _P, _P, _P, _P,
+                                               _P, _P]),
+    "decode_attn_splitk_8bit": (ctypes.c_int, [ctypes.POINTER(DaArgs), ctypes.POINTER(DaPlan),
+                                               ctypes.POINTER(DaDev), ctypes.POINTER(DaScales),
+                                               _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "decode_attn_last_error": (ctypes.c_char_p, []),
     "decode_attn_release": (None, []),
     "decode_attn_version": (ctypes.c_char_p, []),

@@ -15,7 +15,8 @@ import torch
 
 from . import _native as N
 
-_DT = {torch.float32: N.DA_F32, torch.float16: N.DA_F16, torch.bfloat16: N.DA_BF16}
+_DT = {torch.float32: N.DA_F32, torch.float16: N.DA_F16, torch.bfloat16: N.DA_BF16,
+       torch.float8_e4m3fn: N.DA_E4M3, torch.float8_e5m2: N.DA_E5M2}
 
 
 class DecodeAttnError(RuntimeError):
@@ -280,3 +281,162 @@ def decode_attn_splitk_proj(args: N.DaArgs, plan: N.DaPlan, proj: N.DaProj, q: t
                                             _ptr(v_cache), _ptr(out), _ptr(workspace),
                                             workspace.numel() * workspace.element_size(),
                                             _stream(stream)))
+
+
+# ---- 8-bit paged caches ----------------------------------------------------------
+
+def _on(dev: torch.device, what: str, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: every tensor must be on {dev} (got one on {t.device})")
+
+
+def _launch(dev: torch.device, stream, call) -> None:
+    """call(stream handle) with `dev` current: the current stream of the tensors'
+    device, not of whichever device happens to be current."""
+    if dev.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(_stream(stream)))
+
+
+def make_tables(seq_lens: torch.Tensor, block_table: torch.Tensor, free_list: torch.Tensor,
+                state: torch.Tensor, block_size: int, *,
+                seq_lens_out: Optional[torch.Tensor] = None,
+                state_out: Optional[torch.Tensor] = None) -> N.DaTables:
+    """da_tables_t: the device state of a batch's block tables, all int32 on one
+    device: lengths [B], table [B, max_blocks], a stack of free blocks
+    [num_blocks] and state [4] = {free blocks, status, 0, 0}. Lengths and state are
+    updated in place unless *_out are given. The tensors must outlive every launch
+    (and every replay of a captured launch) that uses them."""
+    dev = seq_lens.device
+    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    state_out = state if state_out is None else state_out
+    for name, t, dims in (("seq_lens", seq_lens, 1), ("block_table", block_table, 2),
+                          ("free_list", free_list, 1), ("state", state, 1),
+                          ("seq_lens_out", seq_lens_out, 1), ("state_out", state_out, 1)):
+        if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims:
+            raise TypeError(f"{name} must be a {dims}-D int32 CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _on(dev, "make_tables", block_table, free_list, state, seq_lens_out, state_out)
+    B = seq_lens.shape[0]
+    if block_table.shape[0] != B or seq_lens_out.shape[0] != B:
+        raise ValueError("seq_lens, seq_lens_out and block_table must agree on the batch")
+    if state.shape[0] != 4 or state_out.shape[0] != 4:
+        raise ValueError("state must hold 4 words")
+    t = N.DaTables()
+    t.seq_lens, t.seq_lens_out = seq_lens.data_ptr(), seq_lens_out.data_ptr()
+    t.block_table, t.free_list = block_table.data_ptr(), free_list.data_ptr()
+    t.state, t.state_out = state.data_ptr(), state_out.data_ptr()
+    t.batch, t.max_blocks_per_seq = B, block_table.shape[1]
+    t.block_size, t.num_blocks = int(block_size), free_list.shape[0]
+    return t
+
+
+def decode_attn_grow_tables(tables: N.DaTables, new_lens: torch.Tensor,
+                            slot_map: torch.Tensor, cu_new: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """Give sequence b new_lens[b] more tokens (int32 [B] on the device; negative:
+    release it): takes the blocks, writes the tables, the slots of the new tokens
+    (slot_map int64, -1 past the last) and their row offsets (cu_new int32 [B + 1])."""
+    dev = new_lens.device
+    if new_lens.dtype != torch.int32 or not new_lens.is_cuda or not new_lens.is_contiguous() \
+            or new_lens.numel() != tables.batch:
+        raise TypeError("new_lens must be a contiguous int32 CUDA tensor of the batch's size")
+    if slot_map.dtype != torch.int64 or not slot_map.is_contiguous():
+        raise TypeError("slot_map must be a contiguous int64 tensor")
+    if cu_new is not None and (cu_new.dtype != torch.int32 or not cu_new.is_contiguous()
+                               or cu_new.numel() != tables.batch + 1):
+        raise TypeError("cu_new must be a contiguous int32 tensor of batch + 1 entries")
+    _on(dev, "decode_attn_grow_tables", slot_map, cu_new)
+    _launch(dev, stream, lambda st: N.load().decode_attn_grow_tables(
+        ctypes.byref(tables), _ptr(new_lens), _ptr(slot_map), slot_map.numel(), _ptr(cu_new), st))
+
+
+def decode_attn_tables_status(state: torch.Tensor, stream=None) -> None:
+    """Synchronises; raises if a decode_attn_grow_tables call on this state failed
+    since the last check (and clears the status)."""
+    _launch(state.device, stream,
+            lambda st: N.load().decode_attn_tables_status(_ptr(state), st))
+
+
+def make_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.Tensor,
+                v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> N.DaAppend:
+    """da_append_t for new rows [T, Hkv, D] (any token and head strides, e.g. the K and
+    V parts of a fused projection), pools [num_blocks, block_size, Hkv, D] of
+    float8_e4m3fn or float8_e5m2, and f32 scales [num_blocks, Hkv]."""
+    if k_new.dim() != 3 or v_new.dim() != 3 or k_pool.dim() != 4 or v_pool.dim() != 4 \
+            or k_scale.dim() != 2 or v_scale.dim() != 2:
+        raise ValueError("new rows must be [T, Hkv, D], pools [num_blocks, block_size, Hkv, D] "
+                         "and scales [num_blocks, Hkv]")
+    if k_new.shape[:2] != v_new.shape[:2] or k_pool.shape[:3] != v_pool.shape[:3] \
+            or k_new.dtype != v_new.dtype or k_pool.dtype != v_pool.dtype:
+        raise ValueError("keys and values must agree in their tokens, heads, blocks and types")
+    if k_new.shape[1:] != (k_pool.shape[2], k_pool.shape[3]) \
+            or v_new.shape[1:] != (v_pool.shape[2], v_pool.shape[3]):
+        raise ValueError("new rows and pools must agree in heads and width")
+    want = (k_pool.shape[0], k_pool.shape[2])
+    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want \
+            or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise ValueError("scales must be float32 [num_blocks, Hkv]")
+    if any(t.stride(-1) != 1 for t in (k_new, v_new, k_pool, v_pool)):
+        raise ValueError("the last dimension must be contiguous")
+    a = N.DaAppend()
+    a.n_tokens, a.n_kv_heads, a.head_dim = k_new.shape
+    a.v_dim = v_new.shape[2]
+    a.num_blocks, a.block_size = k_pool.shape[:2]
+    a.src_dtype, a.code_dtype = dtype_code(k_new.dtype), dtype_code(k_pool.dtype)
+    a.k_src_stride, a.k_src_head_stride = k_new.stride()[:2]
+    a.v_src_stride, a.v_src_head_stride = v_new.stride()[:2]
+    a.k_block_stride, a.k_pos_stride, a.k_head_stride = k_pool.stride()[:3]
+    a.v_block_stride, a.v_pos_stride, a.v_head_stride = v_pool.stride()[:3]
+    a.k_scale_block_stride, a.k_scale_head_stride = k_scale.stride()
+    a.v_scale_block_stride, a.v_scale_head_stride = v_scale.stride()
+    return a
+
+
+def decode_attn_append_8bit(append: N.DaAppend, k_new: torch.Tensor, v_new: torch.Tensor,
+                            slot_map: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                            k_scale: torch.Tensor, v_scale: torch.Tensor, stream=None) -> None:
+    """Quantise the new rows into the slots (int64 [T], negative: skip the row) of
+    the pools, one power-of-two scale per (block, KV head). `append` describes
+    tensors of these shapes and strides (make_append)."""
+    if slot_map.dtype != torch.int64 or not slot_map.is_contiguous() \
+            or slot_map.numel() != append.n_tokens:
+        raise TypeError("slot_map must be a contiguous int64 tensor with a slot per row")
+    dev = k_pool.device
+    if dev.type != "cuda":
+        raise TypeError("the pools must be CUDA tensors")
+    _on(dev, "decode_attn_append_8bit", k_new, v_new, slot_map, v_pool, k_scale, v_scale)
+    _launch(dev, stream, lambda st: N.load().decode_attn_append_8bit(
+        ctypes.byref(append), _ptr(k_new), _ptr(v_new), _ptr(slot_map), _ptr(k_pool),
+        _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), st))
+
+
+def make_scales(k_scale: torch.Tensor, v_scale: torch.Tensor) -> N.DaScales:
+    """da_scales_t for f32 scales [num_blocks, Hkv] (any strides). The tensors must
+    outlive every launch that uses the descriptor."""
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2:
+            raise TypeError("scales must be 2-D float32 CUDA tensors")
+    s = N.DaScales()
+    s.k_scale, s.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    s.k_block_stride, s.k_head_stride = k_scale.stride()
+    s.v_block_stride, s.v_head_stride = v_scale.stride()
+    return s
+
+
+def decode_attn_splitk_8bit(args: N.DaArgs, plan: N.DaPlan, dev: N.DaDev, scales: N.DaScales,
+                            q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                            out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """decode_attn_splitk_dev over 8-bit pools with scales (make_paged_args,
+    make_dev with a block table, make_scales)."""
+    _on(q.device, "decode_attn_splitk_8bit", k_pool, v_pool, out, workspace)
+    if q.dtype != torch.float32 or not q.is_contiguous() or not out.is_contiguous():
+        raise TypeError("q must be contiguous float32 and out contiguous")
+    _launch(q.device, stream, lambda st: N.load().decode_attn_splitk_8bit(
+        ctypes.byref(args), ctypes.byref(plan), ctypes.byref(dev), ctypes.byref(scales), _ptr(q),
+        _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), st))

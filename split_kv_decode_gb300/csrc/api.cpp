@@ -52,9 +52,13 @@ int dtype_size(int dt)
     case DA_F32: return 4;
     case DA_F16:
     case DA_BF16: return 2;
+    case DA_E4M3:
+    case DA_E5M2: return 1;
     default: return 0;
     }
 }
+
+bool is_8bit(int dt) { return dt == DA_E4M3 || dt == DA_E5M2; }
 
 const char *dtype_name(int dt)
 {
@@ -62,6 +66,8 @@ const char *dtype_name(int dt)
     case DA_F32: return "f32";
     case DA_F16: return "f16";
     case DA_BF16: return "bf16";
+    case DA_E4M3: return "e4m3";
+    case DA_E5M2: return "e5m2";
     default: return "?";
     }
 }
@@ -98,7 +104,7 @@ int check_args(const da_args_t *a)
                     a->v_dim);
     if (a->capacity < 1) return fail(DA_EINVAL, "args", "capacity %d < 1", a->capacity);
     if (!dtype_size(a->kv_dtype)) return fail(DA_EINVAL, "args", "kv_dtype %d", a->kv_dtype);
-    if (!dtype_size(a->out_dtype)) return fail(DA_EINVAL, "args", "out_dtype %d", a->out_dtype);
+    if (dtype_size(a->out_dtype) < 2) return fail(DA_EINVAL, "args", "out_dtype %d", a->out_dtype);
     if (!std::isfinite(a->scale)) return fail(DA_EINVAL, "args", "scale is not finite");
     if (a->k_pos_stride < 1 || a->k_head_stride < 1 || a->v_pos_stride < 1 ||
         a->v_head_stride < 1 || a->k_batch_stride < 0 || a->v_batch_stride < 0)
@@ -164,6 +170,23 @@ int select_kernel(const da_args_t *a, KernelChoice *kc)
     // the GQA kernel serves the q_len tokens of a group as extra rows
     const int G = a->n_heads / a->n_kv_heads * q_len_of(a);
     const int es = dtype_size(a->kv_dtype);
+    if (is_8bit(a->kv_dtype)) {
+        if (a->head_dim != a->v_dim || (a->head_dim != 128 && a->head_dim != 256) || G > 128)
+            return fail(DA_EUNSUPPORTED, "plan",
+                        "the 8-bit kernel serves v_dim == head_dim of 128 or 256 and groups of 1 "
+                        "to 128 rows (heads per KV head x q_len; got %d, %d, %d)",
+                        a->head_dim, a->v_dim, G);
+        if (a->k_pos_stride % 16 || a->k_head_stride % 16 || a->v_pos_stride % 16 ||
+            a->v_head_stride % 16)
+            return fail(DA_EUNSUPPORTED, "plan",
+                        "cache strides must be multiples of 16 bytes for TMA tiles");
+        kc->kernel = DA_KERNEL_GQA_8BIT;
+        kc->tile = kQ8Tile;
+        kc->ctas_per_sm = 1;
+        kc->cluster = 1;
+        kc->row_groups = (G + q8_rows_per_item(G) - 1) / q8_rows_per_item(G);
+        return DA_OK;
+    }
     if (a->head_dim == 576 && a->v_dim == 512 && a->n_kv_heads == 1) {
         // the rows of an item are (query token, head) pairs, like heads of MQA
         if (!mla_supported_heads(rows_of(a)))
@@ -502,17 +525,11 @@ int launch_mla(const da_args_t *a, const da_plan_t *pl, const float *q, const vo
     return DA_OK;
 }
 
-// Launches the split kernel(s). want_fuse: the kernels may merge their own
-// partials into `out` (no combine launch); *fused says whether they will.
-int launch_split(const da_args_t *a, const da_plan_t *pl, const float *q, const void *k,
-                 const void *v, void *ws, cudaStream_t st, const da_dev_t *dev, void *out,
-                 bool want_fuse, bool *fused)
+// Parameters that the GQA split kernels share.
+void split_params(const da_args_t *a, const da_plan_t *pl, const float *q, void *ws,
+                  SplitParams *out)
 {
-    *fused = false;
-    if (pl->kernel == DA_KERNEL_MLA_TC)
-        return launch_mla(a, pl, q, k, v, ws, st, dev, out, want_fuse, fused);
-
-    SplitParams p;
+    SplitParams &p = *out;
     std::memset(&p, 0, sizeof p);
     uint8_t *w = static_cast<uint8_t *>(ws);
     p.q = q;
@@ -534,6 +551,20 @@ int launch_split(const da_args_t *a, const da_plan_t *pl, const float *q, const 
         p.items.split_base[b] = pl->split_base[b];
     }
     p.items.split_base[a->batch] = pl->total_splits;
+}
+
+// Launches the split kernel(s). want_fuse: the kernels may merge their own
+// partials into `out` (no combine launch); *fused says whether they will.
+int launch_split(const da_args_t *a, const da_plan_t *pl, const float *q, const void *k,
+                 const void *v, void *ws, cudaStream_t st, const da_dev_t *dev, void *out,
+                 bool want_fuse, bool *fused)
+{
+    *fused = false;
+    if (pl->kernel == DA_KERNEL_MLA_TC)
+        return launch_mla(a, pl, q, k, v, ws, st, dev, out, want_fuse, fused);
+
+    SplitParams p;
+    split_params(a, pl, q, ws, &p);
     const bool tc = pl->kernel == DA_KERNEL_GQA_TC;
     // Both GQA kernels merge with every CTA of the launch waiting for its
     // groups, so they fuse only when the whole grid is resident at once (the
@@ -602,6 +633,32 @@ int launch_split(const da_args_t *a, const da_plan_t *pl, const float *q, const 
     return DA_OK;
 }
 
+// Launches the split kernel over 8-bit paged pools.
+int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
+                const da_scales_t *sc, const float *q, const void *k, const void *v, void *ws,
+                cudaStream_t st)
+{
+    SplitParams p;
+    split_params(a, pl, q, ws, &p);
+    p.dev_lens = dev->seq_lens;
+    p.block_table = dev->block_table;
+    p.max_blocks = dev->max_blocks_per_seq;
+    p.block_size = dev->block_size;
+    p.oob_block = dev->num_blocks;
+    p.box_rows = std::gcd(pl->tile, dev->block_size);
+    const int G = a->n_heads / a->n_kv_heads * q_len_of(a), per = q8_rows_per_item(G);
+    p.items.row_groups = (G + per - 1) / per;
+    const Scales8 s = {sc->k_scale,      sc->v_scale,       sc->k_block_stride, sc->k_head_stride,
+                       sc->v_block_stride, sc->v_head_stride, dev->num_blocks};
+    const Q8Pools pools = {static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(v),
+                           dev->k_block_stride, a->k_pos_stride, a->k_head_stride,
+                           dev->v_block_stride, a->v_pos_stride, a->v_head_stride};
+    const cudaError_t e =
+        launch_gqa_8bit(a->kv_dtype, a->head_dim, split_grid(a, pl), st, pools, s, p);
+    if (e != cudaSuccess) return fail(DA_ELAUNCH, "split", "%s", cudaGetErrorString(e));
+    return DA_OK;
+}
+
 // the projection's weights: element type, width, strides and alignment
 int check_proj(const da_args_t *a, const da_proj_t *pj, da_proj_t *norm)
 {
@@ -662,6 +719,53 @@ int launch_combine_phase(const da_args_t *a, const da_plan_t *pl, const void *ws
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DA_ELAUNCH, "combine", "%s", cudaGetErrorString(e));
+    return DA_OK;
+}
+
+// the calls without scales refuse an 8-bit cache
+int refuse_8bit(const da_args_t *a)
+{
+    if (is_8bit(a->kv_dtype))
+        return fail(DA_EUNSUPPORTED, "args",
+                    "an 8-bit cache has scales: call decode_attn_splitk_8bit");
+    return DA_OK;
+}
+
+// the block table of dev and the strides of its pools, and a plan whose chunks
+// start where a box of the tile's copies may
+int check_table(const da_args_t *a, const da_plan_t *plan, const da_dev_t *dev, bool box_chunks)
+{
+    const int es = dtype_size(a->kv_dtype);
+    if (!aligned(dev->block_table, 4))
+        return fail(DA_EINVAL, "args", "dev->block_table must be 4-byte aligned");
+    if (dev->block_size < 16 || dev->block_size % 16)
+        return fail(DA_EUNSUPPORTED, "args", "block_size %d: a positive multiple of 16",
+                    dev->block_size);
+    if (dev->max_blocks_per_seq < 1 || dev->num_blocks < 1)
+        return fail(DA_EINVAL, "args", "max_blocks_per_seq and num_blocks must be >= 1");
+    if ((dev->k_block_stride * es) % 16 || (dev->v_block_stride * es) % 16 ||
+        dev->k_block_stride < (int64_t)dev->block_size * a->k_pos_stride ||
+        dev->v_block_stride < (int64_t)dev->block_size * a->v_pos_stride)
+        return fail(DA_EUNSUPPORTED, "args",
+                    "block strides must hold block_size positions and be multiples of 16 "
+                    "bytes");
+    for (int b = 0; b < a->batch; ++b)
+        if ((int64_t)plan->seq_lens[b] > (int64_t)dev->max_blocks_per_seq * dev->block_size)
+            return fail(DA_EINVAL, "args",
+                        "seq_lens[%d] = %d exceeds max_blocks_per_seq x block_size", b,
+                        plan->seq_lens[b]);
+    // the GQA kernels copy a paged tile in boxes of multiples of gcd(tile,
+    // block_size) rows that start at multiples of that height, so a split
+    // must start at one
+    if (box_chunks) {
+        const int h = std::gcd(plan->tile, dev->block_size);
+        for (int b = 0; b < a->batch; ++b)
+            if (plan->chunk[b] % h)
+                return fail(DA_EINVAL, "plan",
+                            "chunk[%d] = %d: paged caches need chunks that are multiples "
+                            "of %d",
+                            b, plan->chunk[b], h);
+    }
     return DA_OK;
 }
 
@@ -770,6 +874,7 @@ int decode_attn_splitk_ex(const da_args_t *a, const da_plan_t *plan, const float
     KernelChoice kc;
     rc = check_plan(a, plan, &kc);
     if (rc) return rc;
+    if ((rc = refuse_8bit(a))) return rc;
     rc = check_buffers(kc.kernel, q, k, v, out);
     if (rc) return rc;
     if (!ws || !aligned(ws, 256))
@@ -798,6 +903,7 @@ int decode_attn_splitk_dev(const da_args_t *a, const da_plan_t *plan, const da_d
     KernelChoice kc;
     rc = check_plan(a, plan, &kc);
     if (rc) return rc;
+    if ((rc = refuse_8bit(a))) return rc;
     if (kc.kernel == DA_KERNEL_MLA_TC && dev->block_table &&
         (dev->v_block_stride != dev->k_block_stride ||
          (dev->k_block_stride * dtype_size(a->kv_dtype)) % 16))
@@ -808,39 +914,9 @@ int decode_attn_splitk_dev(const da_args_t *a, const da_plan_t *plan, const da_d
     if (rc) return rc;
     if (dev->seq_lens && !aligned(dev->seq_lens, 4))
         return fail(DA_EINVAL, "args", "dev->seq_lens must be 4-byte aligned");
-    if (dev->block_table) {
-        const int es = dtype_size(a->kv_dtype);
-        if (!aligned(dev->block_table, 4))
-            return fail(DA_EINVAL, "args", "dev->block_table must be 4-byte aligned");
-        if (dev->block_size < 16 || dev->block_size % 16)
-            return fail(DA_EUNSUPPORTED, "args", "block_size %d: a positive multiple of 16",
-                        dev->block_size);
-        if (dev->max_blocks_per_seq < 1 || dev->num_blocks < 1)
-            return fail(DA_EINVAL, "args", "max_blocks_per_seq and num_blocks must be >= 1");
-        if ((dev->k_block_stride * es) % 16 || (dev->v_block_stride * es) % 16 ||
-            dev->k_block_stride < (int64_t)dev->block_size * a->k_pos_stride ||
-            dev->v_block_stride < (int64_t)dev->block_size * a->v_pos_stride)
-            return fail(DA_EUNSUPPORTED, "args",
-                        "block strides must hold block_size positions and be multiples of 16 "
-                        "bytes");
-        for (int b = 0; b < a->batch; ++b)
-            if ((int64_t)plan->seq_lens[b] > (int64_t)dev->max_blocks_per_seq * dev->block_size)
-                return fail(DA_EINVAL, "args",
-                            "seq_lens[%d] = %d exceeds max_blocks_per_seq x block_size", b,
-                            plan->seq_lens[b]);
-        // the GQA kernels copy a paged tile in boxes of multiples of gcd(tile,
-        // block_size) rows that start at multiples of that height, so a split
-        // must start at one
-        if (kc.kernel != DA_KERNEL_MLA_TC) {
-            const int h = std::gcd(plan->tile, dev->block_size);
-            for (int b = 0; b < a->batch; ++b)
-                if (plan->chunk[b] % h)
-                    return fail(DA_EINVAL, "plan",
-                                "chunk[%d] = %d: paged caches need chunks that are multiples "
-                                "of %d",
-                                b, plan->chunk[b], h);
-        }
-    }
+    if (dev->block_table &&
+        (rc = check_table(a, plan, dev, kc.kernel != DA_KERNEL_MLA_TC)))
+        return rc;
     if (!ws || !aligned(ws, 256))
         return fail(DA_EINVAL, "args", "workspace must be non-NULL and 256-byte aligned");
     if ((int64_t)ws_bytes < plan->workspace_bytes)
@@ -854,6 +930,46 @@ int decode_attn_splitk_dev(const da_args_t *a, const da_plan_t *plan, const da_d
     rc = launch_split(a, plan, q, k, v, ws, st, dev, out, want_fuse(a), &fused);
     if (rc) return rc;
     if (fused || (a->flags & DA_FLAG_NO_COMBINE)) return DA_OK;
+    return launch_combine_phase(a, plan, ws, out, st);
+}
+
+int decode_attn_splitk_8bit(const da_args_t *a, const da_plan_t *plan, const da_dev_t *dev,
+                            const da_scales_t *sc, const float *q, const void *k, const void *v,
+                            void *out, void *ws, size_t ws_bytes, da_stream_t stream)
+{
+    int rc = check_args(a);
+    if (rc) return rc;
+    if (!is_8bit(a->kv_dtype))
+        return fail(DA_EUNSUPPORTED, "args", "kv_dtype must be DA_E4M3 or DA_E5M2 here (got %s)",
+                    dtype_name(a->kv_dtype));
+    if (!dev || !dev->block_table) return fail(DA_EINVAL, "args", "dev or its block_table is NULL");
+    if (!sc || !sc->k_scale || !sc->v_scale)
+        return fail(DA_EINVAL, "args", "scales or a scale pointer is NULL");
+    KernelChoice kc;
+    rc = check_plan(a, plan, &kc);
+    if (rc) return rc;
+    rc = check_buffers(kc.kernel, q, k, v, out);
+    if (rc) return rc;
+    if (dev->seq_lens && !aligned(dev->seq_lens, 4))
+        return fail(DA_EINVAL, "args", "dev->seq_lens must be 4-byte aligned");
+    if (!aligned(sc->k_scale, 4) || !aligned(sc->v_scale, 4))
+        return fail(DA_EINVAL, "args", "scales must be 4-byte aligned");
+    if (sc->k_block_stride < 1 || sc->k_head_stride < 1 || sc->v_block_stride < 1 ||
+        sc->v_head_stride < 1)
+        return fail(DA_EINVAL, "args", "scale strides must be positive");
+    if ((rc = check_table(a, plan, dev, true))) return rc;
+    if (!ws || !aligned(ws, 256))
+        return fail(DA_EINVAL, "args", "workspace must be non-NULL and 256-byte aligned");
+    if ((int64_t)ws_bytes < plan->workspace_bytes)
+        return fail(DA_ENOSPACE, "args", "workspace %zu bytes < %lld needed", ws_bytes,
+                    (long long)plan->workspace_bytes);
+    cudaError_t pre = cudaGetLastError();
+    if (pre != cudaSuccess)
+        return fail(DA_ECUDA, "before split", "pending CUDA error: %s", cudaGetErrorString(pre));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    rc = launch_8bit(a, plan, dev, sc, q, k, v, ws, st);
+    if (rc) return rc;
+    if (a->flags & DA_FLAG_NO_COMBINE) return DA_OK;
     return launch_combine_phase(a, plan, ws, out, st);
 }
 
@@ -909,6 +1025,7 @@ int decode_attn_splitk_proj(const da_args_t *a, const da_plan_t *plan, const da_
     KernelChoice kc;
     rc = check_plan(a, plan, &kc);
     if (rc) return rc;
+    if ((rc = refuse_8bit(a))) return rc;
     da_proj_t pj;
     rc = check_proj(a, proj, &pj);
     if (rc) return rc;
@@ -1011,6 +1128,7 @@ int decode_attn_device_status(void *ws, da_stream_t stream)
         return fail(DA_ETIMEOUT,
                     kernel == DA_KERNEL_MLA_TC   ? "split (mla)"
                     : kernel == DA_KERNEL_GQA_TC ? "split (gqa, tensor cores)"
+                    : kernel == DA_KERNEL_GQA_8BIT ? "split (gqa, 8 bits)"
                     : kernel == (kStatusTimeoutProj >> 8) ? "combine (projection)"
                     : kernel == (kStatusTimeoutCombine >> 8) ? "combine"
                                                           : "split (gqa)",
@@ -1036,7 +1154,7 @@ void decode_attn_release(void)
 
 const char *decode_attn_version(void)
 {
-    return "split_kv_decode_gb300 0.2 (sm_103a: SIMT and tcgen05 GQA, tcgen05 MLA, combine with projection)";
+    return "split_kv_decode_gb300 0.3 (sm_103a: SIMT and tcgen05 GQA, 8-bit paged GQA, tcgen05 MLA, combine with projection)";
 }
 
 } // extern "C"

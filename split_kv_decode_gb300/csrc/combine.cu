@@ -126,7 +126,7 @@ __device__ __forceinline__ float4 merge_columns(const CombineParams &p, int h, i
             const float4 u = part[w][lane];
             t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
         }
-        const float inv = 1.f / L;
+        const float inv = L == 0.f ? 0.f : 1.f / L; // no position at all: zeros
         t.x *= inv; t.y *= inv; t.z *= inv; t.w *= inv;
     }
     return t;

@@ -57,6 +57,7 @@ struct FusedOut {
 constexpr int kStatusTimeoutGqa = DA_ETIMEOUT | (DA_KERNEL_GQA_TMA << 8);
 constexpr int kStatusTimeoutMla = DA_ETIMEOUT | (DA_KERNEL_MLA_TC << 8);
 constexpr int kStatusTimeoutTc = DA_ETIMEOUT | (DA_KERNEL_GQA_TC << 8);
+constexpr int kStatusTimeoutQ8 = DA_ETIMEOUT | (DA_KERNEL_GQA_8BIT << 8);
 constexpr int kStatusTimeoutProj = DA_ETIMEOUT | (15 << 8); // combine with the projection
 constexpr int kStatusTimeoutCombine = DA_ETIMEOUT | (14 << 8); // staged combine
 
@@ -95,6 +96,13 @@ struct SplitParams {
     int32_t box_rows;        // paged: gcd(tile, block_size), so no box of box_rows rows
                              // that starts at a multiple of box_rows spans two blocks
     ItemTable items;
+};
+
+// 8-bit GQA kernel (gqa_8bit.cu): the scales of the pages, beside SplitParams.
+struct Scales8 {
+    const float *k, *v;
+    int64_t k_block, k_head, v_block, v_head; // strides, elements
+    int32_t num_blocks;
 };
 
 struct MlaParams {
@@ -241,6 +249,19 @@ __host__ __device__ inline TcLayout tc_layout(int D, int R)
 }
 cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
                           const CUtensorMap &km, const CUtensorMap &vm, const SplitParams &p);
+
+// 8-bit GQA kernel: tiles of kQ8Tile positions (a tile's positions are the 128 rows
+// of the score MMA); at most kQ8Rows query rows a work item, larger groups are
+// cut into row groups.
+constexpr int kQ8Tile = 128;
+constexpr int kQ8Rows = 8;
+int q8_rows_per_item(int rows);
+struct Q8Pools {
+    const uint8_t *k, *v;
+    int64_t k_block, k_pos, k_head, v_block, v_pos, v_head; // strides, bytes
+};
+cudaError_t launch_gqa_8bit(int code_dtype, int head_dim, int grid, cudaStream_t st,
+                            const Q8Pools &pools, const Scales8 &sc, const SplitParams &p);
 
 // TMA maps of the SIMT GQA kernel: k and v copy a whole tile of T rows; for a
 // paged pool kb and vb copy box_rows rows, the boxes of a tile that spans a

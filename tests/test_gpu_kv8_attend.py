@@ -1,0 +1,430 @@
+"""Split-KV attention over 8-bit paged pools (decode_attn_splitk_8bit) against attention
+in 64 bits over what the codes stand for.
+
+Tolerance, per output element, from the arithmetic (u = 2^-24):
+  * q is held to 20 significant bits (relative error 2^-20 at most, 2^-19 counted), and a
+    score is an f32 sum of at most 4 * 256 exact products, added 32 at a time, and four
+    more f32 operations: |error of a score| <= (2^-19 + 44 u) * M, M = scale * sum |q k|
+    of the position, under 2^-18 * M (natural units). A weight is off by e^error - 1, the
+    normalised output by twice that, times max |V|: 2^-17 M max|V|.
+  * probabilities are held to 20 significant bits and 2^-26 of the largest, 2^x is good to
+    2^-22, its f32 argument (at most 2^7 in size) to 2^-18: 2^-16.7 together; sums over
+    positions and splits are f32, for the lengths here at most 2^-17: 2^-15 max|V|.
+  * the output's rounding: half a step, eps / 2 of the value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from split_kv_decode_gb300 import _native as N
+from split_kv_decode_gb300 import api as A
+from tests.kv8_util import TDT, attention_reference, code_values, gathered, paged_cache
+
+pytestmark = pytest.mark.gpu
+
+OUT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def queries(seed, B, T, hq, d, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(B, T, hq, d, generator=g) * std
+
+
+def call(q, cache, page, scale, *, plan_lens, now=None, out="f32", splits=0, flags=0, num_sms=0,
+         stream=None, combine=True):
+    kp, vp, ks, vs, table = [t.cuda() for t in cache]
+    x = q.cuda()
+    x = x[:, 0].contiguous() if q.shape[1] == 1 else x
+    args = A.make_paged_args(x, kp, vp, scale, table.shape[1], out_dtype=OUT[out],
+                             force_splits=splits, flags=flags)
+    plan = A.decode_attn_plan(args, plan_lens, num_sms)
+    assert plan.kernel == N.DA_KERNEL_GQA_8BIT
+    lens = None if now is None else torch.tensor(now, dtype=torch.int32, device="cuda")
+    dev = A.make_dev(seq_lens=lens, block_table=table, k_pool=kp, v_pool=vp)
+    sc = A.make_scales(ks, vs)
+    ws = A.new_workspace(plan)
+    ws.fill_(0xFF)                                # poisoned: every partial must be written
+    o = torch.full(x.shape, math.nan, dtype=OUT[out], device="cuda")
+    torch.cuda.synchronize()
+    A.decode_attn_splitk_8bit(args, plan, dev, sc, x, kp, vp, o, ws, stream)
+    torch.cuda.synchronize()
+    A.decode_attn_device_status(ws)
+    return o.double().cpu().numpy().reshape(q.shape)
+
+
+def check(got, q, cache, lens, page, code, scale, out="f32", causal=True):
+    kp, vp, ks, vs, table = cache
+    k, v = gathered(kp, ks, table, lens, page, code), gathered(vp, vs, table, lens, page, code)
+    ref, mag = attention_reference(q.double().numpy(), k, v, lens, scale, causal)
+    assert np.all(np.isfinite(got))
+    for b in range(len(lens)):
+        vmax = np.abs(v[b]).max() if lens[b] else 0.0
+        tol = vmax * (2.0 ** -17 * mag[b][..., None] + 2.0 ** -15)
+        if out != "f32":
+            tol = tol + torch.finfo(OUT[out]).eps / 2 * np.abs(ref[b])
+            tol = tol + (6e-8 if out == "f16" else 0.0)      # half of f16's least step
+        worst = (np.abs(got[b] - ref[b]) / np.maximum(tol, 1e-300)).max()
+        assert worst <= 1, (b, worst, np.abs(got[b] - ref[b]).max(), vmax)
+    return ref
+
+
+def run_check(lens, page, hq, hkv, d, code, *, T=1, out="f32", seed=0, std=1.0, now=None,
+              splits=0, num_sms=0, flags=0, **kw):
+    cache = paged_cache(seed, lens if now is None else now, page, hkv, d, code,
+                        width_extra=2 + max(lens) // page, **kw)
+    q = queries(seed + 1, len(lens), T, hq, d, std)
+    scale = 1 / math.sqrt(d)
+    got = call(q, cache, page, scale, plan_lens=lens, now=now, out=out, splits=splits,
+               num_sms=num_sms, flags=flags)
+    at = lens if now is None else [min(max(n, 0), m) for n, m in zip(now, lens)]
+    ref = check(got, q, cache, at, page, code, scale, out, not flags & N.DA_FLAG_NO_CAUSAL)
+    return got, ref
+
+
+@pytest.mark.parametrize("code", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 256), (16, 4, 256), (32, 8, 128), (3, 3, 128),
+                                      (10, 2, 128), (24, 4, 256), (7, 1, 256), (8, 1, 128)])
+def test_groups_of_up_to_eight(hq, hkv, d, code):
+    run_check([1500, 1, 129, 128, 700], 16, hq, hkv, d, code, seed=hq)
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 80, 128, 256, 400])
+@pytest.mark.parametrize("d", [128, 256])
+def test_page_sizes(page, d):
+    run_check([2000, 17, 383], page, 8, 2, d, "e4m3", seed=page)
+
+
+@pytest.mark.parametrize("rows", [9, 12, 16, 20, 25, 31, 32, 33, 48, 64, 96, 100, 128])
+@pytest.mark.parametrize("d", [128, 256])
+def test_large_groups(rows, d):
+    run_check([900, 64], 64, rows, 1, d, "e4m3", seed=rows)
+
+
+@pytest.mark.parametrize("T,hq,hkv,d", [(2, 8, 2, 256), (4, 24, 4, 256), (3, 5, 5, 128),
+                                        (5, 16, 4, 128), (64, 2, 1, 128), (16, 8, 1, 256)])
+def test_several_new_tokens(T, hq, hkv, d):
+    # lengths down to the new tokens alone, and a causal limit that crosses tiles
+    run_check([T, T + 1, 130, 515, 128 + T // 2 + 1], 16, hq, hkv, d, "e4m3", T=T, seed=T)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40])
+def test_forced_splits(splits):
+    run_check([4000, 260], 48, 8, 2, 128, "e4m3", splits=splits, seed=3)
+    run_check([1000, 130], 48, 8, 2, 128, "e4m3", T=4, splits=splits, seed=4)
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+def test_output_types(out):
+    run_check([777, 300], 32, 12, 2, 256, "e4m3", out=out, seed=9)
+
+
+def test_few_ctas_walk_many_items():
+    run_check([3000, 1, 500, 129, 2048], 16, 16, 4, 128, "e4m3", num_sms=3, splits=5, seed=5)
+    run_check([600, 70], 64, 40, 2, 256, "e5m2", num_sms=2, splits=3, seed=6)
+
+
+def test_relative_accuracy_of_f32_output():
+    # the 2-norm of the error: every source above averages over hundreds of positions;
+    # 20-bit operands alone leave 2^-20 / sqrt(3) of the result
+    got, ref = run_check([6000], 64, 16, 4, 256, "e4m3", seed=11)
+    assert np.linalg.norm(got - ref) <= 2.0 ** -17 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("now", [[0, 1000, 5], [1000, 0, 0], [16, 15, 17], [-4, 10 ** 6, 128]])
+def test_device_lengths(now):
+    # lengths of zero give zeros; lengths are kept within [0, the plan's]
+    lens = [1000, 1000, 1000]
+    at = [min(max(n, 0), 1000) for n in now]
+    cache = paged_cache(2, at, 16, 2, 128, "e4m3", width_extra=64)
+    q = queries(3, 3, 1, 8, 128)
+    got = call(q, cache, 16, 0.1, plan_lens=lens, now=now)
+    check(got, q, cache, at, 16, "e4m3", 0.1)
+    for b in range(3):
+        assert at[b] or np.all(got[b] == 0)
+
+
+@pytest.mark.parametrize("now", [[0, 1, 2, 3, 200], [3, 0, 129, 4, 1]])
+def test_new_tokens_before_the_start_give_zeros(now):
+    cache = paged_cache(4, now, 16, 2, 128, "e4m3", width_extra=20)
+    q = queries(5, 5, 4, 4, 128)
+    got = call(q, cache, 16, 0.1, plan_lens=[256] * 5, now=now)
+    check(got, q, cache, now, 16, "e4m3", 0.1)
+    for b, n in enumerate(now):
+        for i in range(4):
+            assert n - 4 + 1 + i > 0 or np.all(got[b, i] == 0)
+
+
+def test_every_new_token_sees_everything_without_the_causal_limit():
+    run_check([300, 129], 16, 8, 2, 128, "e4m3", T=4, flags=N.DA_FLAG_NO_CAUSAL, seed=8)
+
+
+def test_value_scales_that_differ_by_eighty_powers_of_two():
+    run_check([2000, 300], 16, 8, 2, 128, "e4m3", uneven=True, seed=12)
+    run_check([2000, 300], 16, 40, 2, 128, "e4m3", uneven=True, seed=13, splits=3)
+
+
+def test_large_scores_and_a_rising_maximum():
+    # scores up to about +-60, and a cache whose later pages score higher and higher
+    run_check([3000], 16, 8, 2, 128, "e4m3", std=15.0, seed=14)
+    cache = paged_cache(15, [2000], 16, 1, 128, "e4m3", spread=0.0)
+    kp, vp, ks, vs, table = cache
+    for j in range(125):
+        ks[table[0, j]] *= 2.0 ** (j // 25)
+    q = queries(16, 1, 1, 4, 128)
+    got = call(q, cache, 16, 0.25, plan_lens=[2000], splits=1)
+    check(got, q, cache, [2000], 16, "e4m3", 0.25)
+
+
+def test_zero_scales_of_empty_pages():
+    # pages of zeros under another quantiser's rule: scale 0
+    cache = paged_cache(17, [500, 16], 16, 2, 128, "e4m3")
+    kp, vp, ks, vs, table = cache
+    for b, j in ((0, 3), (0, 7), (1, 0)):
+        blk = int(table[b, j])
+        kp.view(torch.uint8)[blk] = 0
+        vp.view(torch.uint8)[blk] = 0
+        ks[blk], vs[blk] = 0.0, 0.0
+    q = queries(18, 2, 1, 8, 128)
+    got = call(q, cache, 16, 0.1, plan_lens=[500, 16])
+    check(got, q, cache, [500, 16], 16, "e4m3", 0.1)
+    assert np.all(got[1] == 0)
+
+
+def test_scales_that_are_no_powers_of_two():
+    cache = paged_cache(19, [700], 32, 4, 256, "e4m3")
+    kp, vp, ks, vs, table = cache
+    g = torch.Generator().manual_seed(1)
+    ks *= 1 + 0.9 * torch.rand(ks.shape, generator=g)
+    vs *= 1 + 0.9 * torch.rand(vs.shape, generator=g)
+    q = queries(20, 1, 1, 16, 256)
+    got = call(q, cache, 32, 1 / 16, plan_lens=[700])
+    check(got, q, cache, [700], 32, "e4m3", 1 / 16)
+
+
+@pytest.mark.parametrize("code,nan", [("e4m3", 0x7F), ("e5m2", 0x7E), ("e5m2", 0x7C)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_nan_in_a_new_token_reaches_only_the_tokens_that_see_it(code, nan, splits):
+    # (e5m2's infinity too: it is no number either once weighted against others)
+    T, L, d = 4, 300, 128
+    cache = paged_cache(21, [L], 16, 1, d, code)
+    kp, vp, ks, vs, table = cache
+    q = queries(22, 1, T, 2, d)
+    clean = call(q, cache, 16, 0.1, plan_lens=[L], splits=splits)
+    for pool, at, cols in ((vp, L - 2, [5]), (kp, L - 1, range(d))):
+        pos, u = at, pool.view(torch.uint8)
+        old = u[table[0, pos // 16], pos % 16, 0, 5].item()
+        u[table[0, pos // 16], pos % 16, 0, 5] = nan
+        kp_, vp_, ks_, vs_, t_ = [t.cuda() for t in cache]
+        x = q.cuda()
+        a = A.make_paged_args(x, kp_, vp_, 0.1, t_.shape[1], force_splits=splits)
+        p = A.decode_attn_plan(a, [L])
+        dv = A.make_dev(block_table=t_, k_pool=kp_, v_pool=vp_)
+        ws, o = A.new_workspace(p), torch.empty_like(x)
+        A.decode_attn_splitk_8bit(a, p, dv, A.make_scales(ks_, vs_), x, kp_, vp_, o, ws)
+        got = o.double().cpu().numpy()
+        sees = [i for i in range(T) if L - T + i >= at]
+        blind = [i for i in range(T) if i not in sees]
+        np.testing.assert_array_equal(got[0, blind], clean[0, blind])
+        if nan != 0x7C or pool is vp:
+            assert not np.any(np.isfinite(got[0][sees][..., list(cols)]))
+        u[table[0, pos // 16], pos % 16, 0, 5] = old
+
+
+def test_head_major_pools_and_strided_scales():
+    lens, page, h, d = [500, 33], 16, 3, 128
+    cache = paged_cache(23, lens, page, h, d, "e4m3")
+    q = queries(24, 2, 1, 6, d)
+    want = call(q, cache, page, 0.1, plan_lens=lens)
+    kp, vp, ks, vs, table = cache
+    room = torch.full((2, kp.shape[0], h, page + 1, d + 16), 0x7F, dtype=torch.uint8, device="cuda")
+    pools = [r[:, :, :page, :d].permute(0, 2, 1, 3) for r in room]
+    for r, x in zip(pools, (kp, vp)):
+        r.copy_(x.view(torch.uint8))
+    pools = [r.view(TDT["e4m3"]) for r in pools]
+    scales = [s.t().contiguous().cuda().t() for s in (ks, vs)]
+    x = q[:, 0].contiguous().cuda()
+    t = table.cuda()
+    a = A.make_paged_args(x, *pools, 0.1, t.shape[1])
+    p = A.decode_attn_plan(a, lens)
+    dv = A.make_dev(block_table=t, k_pool=pools[0], v_pool=pools[1])
+    ws, o = A.new_workspace(p), torch.empty_like(x)
+    A.decode_attn_splitk_8bit(a, p, dv, A.make_scales(*scales), x, *pools, o, ws)
+    np.testing.assert_array_equal(o.double().cpu().numpy(), want[:, 0])
+
+
+def test_the_same_page_in_two_sequences_and_twice_in_one():
+    # a shared prefix, and a table that names a page again
+    cache = paged_cache(25, [160, 100], 16, 2, 128, "e4m3", poison=False)
+    table = cache[4]
+    table[1, :4] = table[0, :4]
+    table[0, 6] = table[0, 2]
+    q = queries(26, 2, 1, 8, 128)
+    got = call(q, cache, 16, 0.1, plan_lens=[160, 100])
+    check(got, q, cache, [160, 100], 16, "e4m3", 0.1)
+
+
+def test_table_entries_outside_the_pool_read_as_zeros():
+    cache = paged_cache(27, [64], 16, 1, 128, "e4m3")
+    table = cache[4]
+    zero = [t.clone() for t in cache]
+    for j, bad in ((1, -3), (2, 10 ** 9)):
+        zero[0].view(torch.uint8)[table[0, j]] = 0
+        zero[1].view(torch.uint8)[table[0, j]] = 0
+        zero[3][table[0, j]] = 1.0
+        table[0, j] = bad
+    q = queries(28, 1, 1, 4, 128)
+    got = call(q, cache, 16, 0.1, plan_lens=[64])
+    check(got, q, zero, [64], 16, "e4m3", 0.1)
+
+
+def test_pools_past_four_gigabytes():
+    nb, page, h, d = 2100, 64, 128, 256
+    kp = torch.zeros(nb, page, h, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vp = kp.clone()
+    ks = torch.ones(nb, h, device="cuda")
+    small = paged_cache(29, [100], page, h, d, "e4m3", spare=0)
+    for pool, x in ((kp, small[0]), (vp, small[1])):
+        pool.view(torch.uint8)[-2:] = x.view(torch.uint8).cuda()
+    ks[-2:], vs = small[2].cuda(), ks.clone()
+    vs[-2:] = small[3].cuda()
+    table = (small[4][:, :2] + nb - 2).cuda()
+    x = queries(30, 1, 1, h, d)
+    a = A.make_paged_args(x[:, 0].cuda(), kp, vp, 1 / 16, 2)
+    p = A.decode_attn_plan(a, [100])
+    dv = A.make_dev(block_table=table, k_pool=kp, v_pool=vp)
+    ws, o = A.new_workspace(p), torch.empty(1, h, d, device="cuda")
+    xq = x[:, 0].contiguous().cuda()
+    A.decode_attn_splitk_8bit(a, p, dv, A.make_scales(ks, vs), xq, kp, vp, o, ws)
+    check(o.double().cpu().numpy()[:, None], x, small, [100], page, "e4m3", 1 / 16)
+
+
+def test_a_long_context_sampled():
+    # one (row, head) of a 131072-position context against 64 bits; the other bound on the
+    # whole output: the same result from three times as many splits
+    L, page, h, d = 131072, 64, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(31)
+    nb = L // page
+    codes = [(torch.randn(nb, page, h, d, generator=g, device="cuda") * 40).clamp(-448, 448)
+             .to(torch.float8_e4m3fn) for _ in range(2)]
+    sc = [torch.full((nb, h), 2.0 ** -5, device="cuda") for _ in range(2)]
+    table = torch.randperm(nb, device="cuda", generator=g).int()[None].contiguous()
+    x = torch.randn(1, 8, d, generator=g, device="cuda")
+    outs = []
+    for s in (0, 300):
+        a = A.make_paged_args(x, *codes, d ** -0.5, nb, force_splits=s)
+        p = A.decode_attn_plan(a, [L])
+        dv = A.make_dev(block_table=table, k_pool=codes[0], v_pool=codes[1])
+        ws, o = A.new_workspace(p), torch.empty_like(x)
+        A.decode_attn_splitk_8bit(a, p, dv, A.make_scales(*sc), x, *codes, o, ws)
+        outs.append(o.double())
+    ids = table[0].long()
+    k, v = [(c.view(torch.uint8)[ids].view(c.dtype).double() * 2.0 ** -5).reshape(L, h, d)
+            for c in codes]
+    for head in (0, 5):
+        s = (k[:, head // 4] @ x[0, head].double()) * d ** -0.5
+        ref = torch.softmax(s, 0) @ v[:, head // 4]
+        assert (outs[0][0, head] - ref).norm() <= 2.0 ** -16 * ref.norm()
+    assert (outs[0] - outs[1]).norm() <= 2.0 ** -15 * outs[0].norm()
+
+
+def test_two_streams_at_once_and_captured():
+    lens = [900, 200]
+    caches = [paged_cache(s, lens, 16, 2, 128, "e4m3") for s in (32, 33)]
+    q = queries(34, 2, 1, 8, 128)
+    want = [call(q, c, 16, 0.1, plan_lens=lens) for c in caches]
+    streams, states = [torch.cuda.Stream() for _ in caches], []
+    x = q[:, 0].contiguous().cuda()
+    for c in caches:
+        kp, vp, ks, vs, t = [y.cuda() for y in c]
+        a = A.make_paged_args(x, kp, vp, 0.1, t.shape[1])
+        p = A.decode_attn_plan(a, lens)
+        states.append((a, p, A.make_dev(block_table=t, k_pool=kp, v_pool=vp),
+                       A.make_scales(ks, vs), x, kp, vp, torch.empty_like(x), A.new_workspace(p),
+                       (t, ks, vs)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, s in zip(streams, states):
+            A.decode_attn_splitk_8bit(*s[:9], stream=st)
+    torch.cuda.synchronize()
+    for w, s in zip(want, states):
+        np.testing.assert_array_equal(s[7].double().cpu().numpy(), w[:, 0])
+        s[7].fill_(math.nan)
+    graphs = []
+    for s in states:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            A.decode_attn_splitk_8bit(*s[:9])
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for w, s in zip(want, states):
+        np.testing.assert_array_equal(s[7].double().cpu().numpy(), w[:, 0])
+
+
+def test_partials_go_to_every_combine():
+    lens, d = [1200, 300], 128
+    cache = paged_cache(35, lens, 16, 2, d, "e4m3")
+    q = queries(36, 2, 1, 8, d)
+    want = call(q, cache, 16, 0.1, plan_lens=lens)[:, 0]
+    kp, vp, ks, vs, t = [y.cuda() for y in cache]
+    x = q[:, 0].contiguous().cuda()
+    a = A.make_paged_args(x, kp, vp, 0.1, t.shape[1], flags=N.DA_FLAG_NO_COMBINE)
+    p = A.decode_attn_plan(a, lens)
+    dv = A.make_dev(block_table=t, k_pool=kp, v_pool=vp)
+    ws, o = A.new_workspace(p), torch.empty_like(x)
+    A.decode_attn_splitk_8bit(a, p, dv, A.make_scales(ks, vs), x, kp, vp, o, ws)
+    A.decode_attn_combine(a, p, ws, o)
+    np.testing.assert_array_equal(o.double().cpu().numpy(), want)
+    # a second rank whose slice is empty changes nothing, with and without a projection
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dz = A.make_dev(seq_lens=zero, block_table=t, k_pool=kp, v_pool=vp)
+    n = A.decode_attn_workspace_bytes(p)
+    both = torch.empty(2 * n, dtype=torch.uint8, device="cuda")
+    both[:n] = ws
+    A.decode_attn_splitk_8bit(a, p, dz, A.make_scales(ks, vs), x, kp, vp, o, both[n:])
+    A.decode_attn_combine_ranks(a, p, both, 2, o)
+    # the ranks' merge adds in another order: f32 sums of at most 20 partials
+    np.testing.assert_allclose(o.double().cpu().numpy(), want, rtol=0, atol=2.0 ** -18 * 8)
+    w = torch.randn(8, 64, d, generator=torch.Generator().manual_seed(2)).cuda() / d ** 0.5
+    pr = torch.empty(2, 8, 64, device="cuda")
+    A.decode_attn_combine_proj(a, p, A.make_proj(w), ws, pr)
+    ref = np.einsum("hec,bhc->bhe", w.double().cpu().numpy(), want)
+    np.testing.assert_allclose(pr.double().cpu().numpy(), ref, rtol=0, atol=2.0 ** -14)
+    # two empty ranks: zeros
+    both[:n] = both[n:]
+    for r in (1, 2):
+        A.decode_attn_combine_ranks(a, p, both, r, o.fill_(math.nan))
+        assert torch.equal(o, torch.zeros_like(o))
+
+
+def test_one_launch_is_accepted_and_bad_launches_are_reported():
+    lens = [500]
+    cache = paged_cache(37, lens, 16, 2, 128, "e4m3")
+    q = queries(38, 1, 1, 8, 128)
+    want = call(q, cache, 16, 0.1, plan_lens=lens)
+    np.testing.assert_array_equal(
+        call(q, cache, 16, 0.1, plan_lens=lens, flags=N.DA_FLAG_ONE_LAUNCH), want)
+    with pytest.raises(A.DecodeAttnError) as e:
+        call(q, cache, 16, 0.1, plan_lens=lens, flags=N.DA_FLAG_TEST_BAD_LAUNCH)
+    assert e.value.status == N.DA_ELAUNCH and e.value.message.startswith("split")
+    np.testing.assert_array_equal(call(q, cache, 16, 0.1, plan_lens=lens), want)
+
+
+def test_codes_are_used_as_they_stand():
+    # one position: the output is its value row, every code of the type among the columns
+    for code in ("e4m3", "e5m2"):
+        vals = code_values(code)
+        finite = np.array([u for u in range(256) if np.isfinite(vals[u])], dtype=np.uint8)
+        for lo in range(0, len(finite), 128):
+            row = np.resize(finite[lo:lo + 128], 128)
+            kp = torch.zeros(1, 16, 1, 128, dtype=torch.uint8)
+            vp = torch.full((1, 16, 1, 128), 0x7F, dtype=torch.uint8)
+            vp[0, 0, 0] = torch.from_numpy(row)
+            cache = (kp.view(TDT[code]), vp.view(TDT[code]), torch.ones(1, 1),
+                     torch.full((1, 1), 0.375), torch.zeros(1, 1, dtype=torch.int32))
+            got = call(queries(1, 1, 1, 1, 128), cache, 16, 1.0, plan_lens=[1])
+            np.testing.assert_allclose(got[0, 0, 0], vals[row] * 0.375, rtol=2.0 ** -19, atol=0)
