@@ -274,6 +274,8 @@ CUtensorMapDataType tma_dtype(int dt)
     switch (dt) {
     case DA_F16: return CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     case DA_BF16: return CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    case DA_E4M3:
+    case DA_E5M2: return CU_TENSOR_MAP_DATA_TYPE_UINT8;
     default: return CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     }
 }
@@ -317,7 +319,7 @@ int encode_pool_map(CUtensorMap *map, const void *base, int dt, int D, int hkv, 
                           (cuuint64_t)num_blocks};
     cuuint64_t strides[3] = {(cuuint64_t)(head_st * es), (cuuint64_t)(pos_st * es),
                              (cuuint64_t)(block_st * es)};
-    cuuint32_t box[4] = {(cuuint32_t)(sw128 ? 64 : D), 1, (cuuint32_t)rows, 1};
+    cuuint32_t box[4] = {(cuuint32_t)(sw128 ? 128 / es : D), 1, (cuuint32_t)rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(map, tma_dtype(dt), 4, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -650,11 +652,17 @@ int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
     p.items.row_groups = (G + per - 1) / per;
     const Scales8 s = {sc->k_scale,      sc->v_scale,       sc->k_block_stride, sc->k_head_stride,
                        sc->v_block_stride, sc->v_head_stride, dev->num_blocks};
-    const Q8Pools pools = {static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(v),
-                           dev->k_block_stride, a->k_pos_stride, a->k_head_stride,
-                           dev->v_block_stride, a->v_pos_stride, a->v_head_stride};
-    const cudaError_t e =
-        launch_gqa_8bit(a->kv_dtype, a->head_dim, split_grid(a, pl), st, pools, s, p);
+    CUtensorMap km, vm;
+    int rc = encode_pool_map(&km, k, a->kv_dtype, a->head_dim, a->n_kv_heads, dev->block_size,
+                             dev->num_blocks, a->k_head_stride, a->k_pos_stride,
+                             dev->k_block_stride, p.box_rows, true);
+    if (rc) return rc;
+    rc = encode_pool_map(&vm, v, a->kv_dtype, a->v_dim, a->n_kv_heads, dev->block_size,
+                         dev->num_blocks, a->v_head_stride, a->v_pos_stride,
+                         dev->v_block_stride, p.box_rows, true);
+    if (rc) return rc;
+    const cudaError_t e = launch_gqa_8bit(a->kv_dtype, a->head_dim, split_grid(a, pl), st, km, vm,
+                                          s, p);
     if (e != cudaSuccess) return fail(DA_ELAUNCH, "split", "%s", cudaGetErrorString(e));
     return DA_OK;
 }

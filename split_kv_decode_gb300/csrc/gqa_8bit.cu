@@ -1,11 +1,39 @@
-// GQA / MQA split kernel over an 8-bit paged cache, sm_103a.
+// GQA / MQA split kernel over an 8-bit paged cache, tcgen05 tensor cores, sm_103a.
 //
-// The codes of a page (block i of block_size positions) stand for code *
-// scale[i][head], so with e4m3 or e5m2 codes Kc, Vc and page scales ks, vs
-//     score[r][pos] = scale * ks[page(pos)] * sum_d q[r][d] Kc[pos][d]
-//     out[r][d]     = sum_pos softmax(score)[r][pos] * vs[page(pos)] * Vc[pos][d].
-// An item is (sequence, KV head, split, row group), as for the SIMT kernel. One
-// warp takes one position at a time, its lanes the columns.
+// A page (block i of block_size positions) holds e4m3 or e5m2 codes Kc, Vc that
+// stand for code * scale[i][head]. With page scales ks, vs (lv = log2 vs) and
+// scores in log2 units,
+//     s[r][pos]  = ks[page] * sum_d q[r][d] Kc[pos][d]        (q times scale * log2 e)
+//     x[r][pos]  = 2^(s + lv[page] - m[r])
+//     acc[r][d]  = sum_pos x[r][pos] Vc[pos][d],   l[r] = sum_pos 2^(s - m[r])
+// so the value scales fold into the exponent and the codes go to the tensor cores
+// as they stand: TMA brings 128-position tiles of K and of V into shared memory
+// in the 128-byte swizzle the MMA reads, and nothing converts or re-reads them.
+//     S[pos][(j, r)]  = sum_d Kc[pos][d] q_j[r][d]      (M = 128 positions, K = D)
+//     O^T[d][(j, r)] += sum_pos Vc[pos][d] x_j[r][pos]  (M = 128 value columns, K = 128)
+//
+// The other operand of an 8-bit MMA is 8-bit too. q and x are split into four e4m3
+// terms, y = y_0 + 2^-4 y_1 + 2^-8 y_2 + 2^-12 y_3: a term rounds what the ones
+// before it left, and each takes 5 bits off (4 significant bits and the sign of
+// the rest), so four hold 20 bits; y is scaled to at most 256, so that the
+// smallest steps (e4m3's 2^-9, 2^-21 in the last term) are 2^-30 of the largest.
+// The terms are columns of the MMA (N = 4 x rows, at least 16), whose time for N <= 64
+// is that of reading the tile (46 to 48 cycles per 32-byte step); they are added in
+// f32 when S or O^T leave TMEM. The products are exact and the sums f32 (measured:
+// relative error 1e-7 on full-range codes).
+//
+// An item is (sequence, KV head, split, row group), rows (query token, head). The
+// roles of the 7 warps, one CTA per SM:
+//   warps 0-3  softmax and epilogue: a thread owns one position of the tile (TMEM lane),
+//              all rows; the reference m of a row moves only when a score outgrows it by
+//              2^8 (then O^T is rescaled), so most tiles take one vote. In the epilogue a
+//              thread owns a value column.
+//   warp 4     TMA producer: K and V tiles through one ring of slots, paged boxes as in the
+//              16-bit tensor-core kernel.
+//   warp 5     TMEM owner and the one thread that issues the MMAs.
+//   warp 6     the page scales of four tiles at a time, two batches ahead.
+// Every wait is bounded; a wait that runs out sets the status word and the CTA drains
+// and returns.
 #include <climits>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -17,106 +45,767 @@
 namespace skv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 224;
+constexpr int kProd = 4, kMma = 5, kScale = 6; // warps
+constexpr int T = kQ8Tile;
+constexpr int kTerms = 4;
+constexpr float kTermStep = 1.f / 16.f;
+constexpr float kHead = 4.f; // m is this much below the maximum that set it
+constexpr float kTau = 8.f;  // and moves when a score is this much above it
+constexpr int kMaxSlots = 12;
+constexpr float kMinScale = 7.8886090522101181e-31f; // 2^-100
 
-template <__nv_fp8_interpretation_t F, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-    gqa_8bit_kernel(const __grid_constant__ Q8Pools pools, const __grid_constant__ Scales8 sc,
-                    const __grid_constant__ SplitParams p)
+// barriers
+constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE = B_SFULL + 2,
+              B_PFULL = B_SFREE + 2, B_PFREE = B_PFULL + 2, B_PVDONE = B_PFREE + 2,
+              B_OREADY = B_PVDONE + 1, B_OFREE = B_OREADY + 1, B_QFULL = B_OFREE + 1,
+              B_QFREE = B_QFULL + 1, B_SCFULL = B_QFREE + 1, B_SCFREE = B_SCFULL + 2,
+              B_DRAIN = B_SCFREE + 2, B_N = B_DRAIN + 1;
+
+// shared memory of <D, RP>: RP rows an item at most, N = 4 RP columns
+template <int D, int RP> struct Layout {
+    static constexpr int N = kTerms * RP;
+    static constexpr int NCH = D / 128;        // 128-column chunks of a row
+    static constexpr int CHUNK = T * 128;      // bytes of a chunk of a tile
+    static constexpr int SLOT = NCH * CHUNK;   // a K or V tile
+    static constexpr int QCH = N * 128;        // a chunk of Q
+    static constexpr int PSLOT = N * 128;      // one P buffer
+    static constexpr int Q_OFF = 0;
+    static constexpr int P_OFF = Q_OFF + NCH * QCH;
+    static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
+    // after the slots: barriers, flags, page scales (2 batches of 4 tiles of 8 groups of
+    // 16 positions), per-row tables, warp maxima, columns with a NaN
+    static constexpr int BAR = 0, MISC = BAR + B_N * 8, SC = (MISC + 16 + 15) / 16 * 16,
+                         ROW = SC + 2 * 4 * 8 * 8, RED = ROW + 4 * RP * 4, NANC = RED + 4 * RP * 4,
+                         TAIL = NANC + D * 4;
+    static constexpr int SLOTS_FIT = (232448 - 1024 - SLOT_OFF - TAIL) / SLOT;
+    static constexpr int NS = SLOTS_FIT > kMaxSlots ? kMaxSlots : SLOTS_FIT;
+    static constexpr int TAIL_OFF = SLOT_OFF + NS * SLOT;
+    static constexpr int BYTES = TAIL_OFF + TAIL + 1024;
+    static_assert(NS >= 4, "K and V tiles of two steps in flight");
+    static_assert((2 + NCH) * N <= 512, "TMEM columns: two S slots and O^T");
+    static_assert(QCH % 1024 == 0 && BYTES <= 232448, "swizzle atoms, shared memory");
+};
+
+// byte offset of (row, byte) in a region of 128-byte rows with the 128-byte swizzle
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t byte)
 {
-    constexpr int E = D / 32; // columns of a lane
-    __shared__ float red[kWarps][kQ8Rows][D];
-    __shared__ float2 red_ml[kWarps][kQ8Rows];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const ItemTable &it = p.items;
-    const int Gh = p.hq / it.n_kv_heads, rows = Gh * p.q_len;
-    const int per = (rows + it.row_groups - 1) / it.row_groups;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-    for (int item = blockIdx.x; item < it.n_items; item += gridDim.x) {
-        int b, kvh, s, rg;
-        decode_item(it, item, b, kvh, s, rg);
-        const int L = p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), it.seq_lens[b]))
-                                 : it.seq_lens[b];
-        const int p0 = s * it.chunk[b], p1 = min(L, p0 + it.chunk[b]);
-        const int row0 = rg * per, R = min(per, rows - row0);
-        float q[kQ8Rows][E], acc[kQ8Rows][E], m[kQ8Rows], l[kQ8Rows];
-        int lim[kQ8Rows]; // positions row r sees: below lim
-        for (int r = 0; r < kQ8Rows; ++r) {
-            m[r] = kNeutralM;
-            l[r] = 0.f;
-            lim[r] = 0;
-            const int tok = (row0 + r) / Gh, g = (row0 + r) - tok * Gh;
-            if (r < R)
-                lim[r] = (p.flags & DA_FLAG_NO_CAUSAL) ? INT_MAX : L - p.q_len + 1 + tok;
-            for (int e = 0; e < E; ++e) {
-                acc[r][e] = 0.f;
-                q[r][e] = r < R ? p.q[((size_t)(b * p.q_len + tok) * p.hq + kvh * Gh + g) * D +
-                                      lane * E + e] * p.scale_log2
-                                : 0.f;
-            }
-        }
-        for (int pos = p0 + warp; pos < p1; pos += kWarps) {
-            const int i = pos / p.block_size;
-            const int blk = p.block_table[(size_t)b * p.max_blocks + i];
-            float k[E], v[E], ks = 0.f, vs = 0.f;
-            for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-            if (blk >= 0 && blk < sc.num_blocks) {
-                const int o = pos - i * p.block_size;
-                const uint8_t *kr = pools.k + blk * pools.k_block + o * pools.k_pos + kvh * pools.k_head;
-                const uint8_t *vr = pools.v + blk * pools.v_block + o * pools.v_pos + kvh * pools.v_head;
-                ks = sc.k[blk * sc.k_block + kvh * sc.k_head];
-                vs = sc.v[blk * sc.v_block + kvh * sc.v_head];
-                for (int e = 0; e < E; ++e) {
-                    k[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(kr[lane * E + e], F)));
-                    v[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(vr[lane * E + e], F)));
-                }
-            }
-            for (int r = 0; r < kQ8Rows; ++r) {
-                float d = 0.f;
-                for (int e = 0; e < E; ++e) d = fmaf(q[r][e], k[e], d);
-                for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                d *= ks;
-                if (pos < lim[r]) {
-                    const float mn = fmaxf(m[r], d), f = ex2(m[r] - mn), w = ex2(d - mn);
-                    m[r] = mn;
-                    l[r] = l[r] * f + w;
-                    for (int e = 0; e < E; ++e) acc[r][e] = acc[r][e] * f + w * vs * v[e];
-                }
-            }
-        }
-        for (int r = 0; r < kQ8Rows; ++r) {
-            for (int e = 0; e < E; ++e) red[warp][r][lane * E + e] = acc[r][e];
-            if (lane == 0) red_ml[warp][r] = make_float2(m[r], l[r]);
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < R * D; i += kWarps * 32) {
-            const int r = i / D, d = i - r * D;
-            float M = kNeutralM, A = 0.f, S = 0.f;
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_ml[w][r].x);
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(red_ml[w][r].x - M);
-                S += red_ml[w][r].y * f;
-                A += red[w][r][d] * f;
-            }
-            const int tok = (row0 + r) / Gh, g = (row0 + r) - tok * Gh;
-            const size_t wr = ((size_t)it.split_base[b] + s) * p.n_heads + kvh * Gh + tok * p.hq + g;
-            // a NaN score makes the row NaN whatever the other splits hold
-            const bool nan = isnan(S);
-            p.acc[wr * D + d] = nan ? S : A;
-            if (d == 0)
-                p.ml[wr] = nan ? make_float2(-kNeutralM, 1.f)
-                               : make_float2(S > 0.f ? M * kLn2 : kNeutralM, S);
-        }
-        __syncthreads();
-    }
+    return (row >> 3) * 1024 + (row & 7) * 128 + ((((byte >> 4) ^ row) & 7) << 4) + (byte & 15);
 }
 
-template <__nv_fp8_interpretation_t F, int D>
-cudaError_t launch_t(int grid, cudaStream_t st, const Q8Pools &pools, const Scales8 &sc,
-                     const SplitParams &p)
+__device__ __forceinline__ void sts_u8(uint32_t saddr, uint32_t v)
 {
-    gqa_8bit_kernel<F, D><<<grid, kWarps * 32, 0, st>>>(pools, sc, p);
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts_u32(uint32_t saddr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+// D[128][N] (+)= A . B, 8-bit operands, K = 32
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// f32 accumulation; A e4m3 or e5m2 (K-major, or MN-major with a_mn), B e4m3 K-major
+__device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn, bool a_e5m2)
+{
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((a_mn ? 1u : 0u) << 15) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// C consecutive 32-bit TMEM columns (C = 4 or 8) of this warp's lane quarter
+template <int C> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float *v);
+template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float *v)
+{
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, float *v)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ bool bar_or(bool pred) { return named_bar_or(1, 128, pred); }
+
+// two values to e4m3 (x in the low byte); *x, *y: what is left, times 16
+__device__ __forceinline__ uint32_t term2(float &x, float &y)
+{
+    const __nv_fp8x2_storage_t c =
+        __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+    x = (x - f.x) * 16.f;
+    y = (y - f.y) * 16.f;
+    return c;
+}
+
+// the length item items of sequence b attend over: the plan's, or the device's,
+// kept within [0, the plan's]
+__device__ __forceinline__ int len8(const SplitParams &p, int b)
+{
+    const int L = p.items.seq_lens[b];
+    return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
+}
+
+// The (item, tile) sequence of a CTA, the same for every role: items blockIdx.x,
+// blockIdx.x + gridDim.x, ..., each in tiles of T positions, the last one cut at the
+// item's end; items without positions have no tiles and are skipped.
+struct Walk8 {
+    int item, b, kvh, s, rg, p0, p1, t0, t1, gt, L;
+    bool done, first;
+    __device__ __forceinline__ void load_item(const SplitParams &p)
+    {
+        for (;;) {
+            done = item >= p.items.n_items;
+            if (done) return;
+            decode_item(p.items, item, b, kvh, s, rg);
+            p0 = s * p.items.chunk[b];
+            L = len8(p, b);
+            p1 = min(L, p0 + p.items.chunk[b]);
+            if (p1 > p0) break;
+            item += gridDim.x;
+        }
+        t0 = p0;
+        t1 = tile_end<T>(t0, p1);
+        first = true;
+    }
+    __device__ __forceinline__ void start(const SplitParams &p)
+    {
+        item = blockIdx.x;
+        gt = 0;
+        load_item(p);
+    }
+    __device__ __forceinline__ bool last() const { return t1 >= p1; }
+    __device__ __forceinline__ void next(const SplitParams &p)
+    {
+        ++gt;
+        if (t1 >= p1) {
+            item += gridDim.x;
+            load_item(p);
+        } else {
+            t0 = t1;
+            t1 = tile_end<T>(t0, p1);
+            first = false;
+        }
+    }
+};
+
+template <int D, int RP>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_8bit_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    const __grid_constant__ Scales8 sc, const __grid_constant__ SplitParams p,
+                    const int e5m2)
+{
+    using L = Layout<D, RP>;
+    constexpr int N = L::N, NCH = L::NCH, NS = L::NS;
+    constexpr int RC = RP < 8 ? RP : 8; // rows taken from TMEM at a time
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    uint8_t *tail = sm + L::TAIL_OFF;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(tail + L::BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + L::MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + L::MISC + 4);
+    float2 *sc_sm = reinterpret_cast<float2 *>(tail + L::SC); // (ks, log2 vs) of 16 positions
+    float *qf_sm = reinterpret_cast<float *>(tail + L::ROW);  // per row: 1 / (q's scaling)
+    float *alpha_sm = qf_sm + RP;                             // rescale factor
+    int *lim_sm = reinterpret_cast<int *>(alpha_sm + RP);     // positions seen: below lim
+    int *wrow_sm = lim_sm + RP;                               // workspace row
+    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // [4 warps][RP]
+    int *nan_sm = reinterpret_cast<int *>(tail + L::NANC);    // [D] first token that sees a NaN
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const ItemTable &it = p.items;
+    volatile int never = 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(bar + B_FULL + s, 1);
+            mbar_init(bar + B_EMPTY + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar + B_SFULL + s, 1);
+            mbar_init(bar + B_SFREE + s, 4);
+            mbar_init(bar + B_PFULL + s, 4);
+            mbar_init(bar + B_PFREE + s, 1);
+            mbar_init(bar + B_SCFULL + s, 1);
+            mbar_init(bar + B_SCFREE + s, 4);
+        }
+        mbar_init(bar + B_PVDONE, 1);
+        mbar_init(bar + B_OREADY, 1);
+        mbar_init(bar + B_OFREE, 4);
+        mbar_init(bar + B_QFULL, 4);
+        mbar_init(bar + B_QFREE, 1);
+        mbar_init(bar + B_DRAIN, 1);
+        *abort_flag = 0;
+        if (blockIdx.x == 0) *p.status = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMma) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == kProd) {
+        // =============================== TMA producer ===============================
+        // box j holds positions [t0 + j*h, t0 + (j+1)*h) of a 128-column chunk, h =
+        // box_rows (16 to 128: a divisor of the tile and of block_size), so no box spans
+        // two blocks and a tile spans blocks freely; h * 128 bytes is a multiple of the
+        // swizzle atom, so the boxes land as one box of the tile would
+        if (lane == 0) {
+            tma_prefetch_map(&kmap);
+            tma_prefetch_map(&vmap);
+        }
+        const uint64_t pol = l2_evict_first_policy();
+        const int bs = p.block_size, h = p.box_rows, nbox = T / h;
+        uint32_t eph = 0, issued = 0;
+        int win_b = -1, win_lo = 0, slot = 0;
+        int32_t win_entry = 0;
+        bool ok = true;
+        Walk8 w;
+        for (w.start(p); ok && !w.done; w.next(p)) {
+            const int lo = w.t0 / bs, hi = (w.t0 + T - 1) / bs;
+            if (w.b != win_b || lo < win_lo || hi >= win_lo + 32) {
+                win_b = w.b;
+                win_lo = lo;
+                win_entry = lo + lane < p.max_blocks
+                                ? p.block_table[(size_t)w.b * p.max_blocks + lo + lane]
+                                : p.oob_block;
+                if (win_entry < 0 || win_entry > p.oob_block) win_entry = p.oob_block;
+            }
+            const int pos = w.t0 + min(lane, nbox - 1) * h, idx = pos / bs;
+            const int blk = __shfl_sync(0xffffffffu, win_entry, idx - win_lo);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                // a slot's first use finds its barrier's previous phase complete
+                bool got = true;
+                if (lane == 0)
+                    got = mbar_wait_bounded(bar + B_EMPTY + slot, ((eph >> slot) & 1u) ^ 1u,
+                                            p.timeout_ns, abort_flag);
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    ok = false;
+                    break;
+                }
+                eph ^= 1u << slot;
+                if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
+                    issued |= 1u << slot;
+                    uint8_t *dst = sm + L::SLOT_OFF + slot * L::SLOT;
+                    if (lane == 0) mbar_arrive_expect_tx(bar + B_FULL + slot, L::SLOT);
+                    __syncwarp();
+                    if (lane < nbox) {
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_4d(dst + c * L::CHUNK + lane * h * 128, kv ? &vmap : &kmap,
+                                        bar + B_FULL + slot, c * 128, w.kvh, pos - idx * bs, blk,
+                                        pol);
+                    }
+                }
+                if (++slot == NS) slot = 0;
+            }
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            atomicCAS(p.status, 0, kStatusTimeoutQ8);
+        }
+        // nothing may be in flight when the CTA exits: wait (bounded) for the last copies
+        if (lane == 0)
+            for (int s = 0; s < NS; ++s)
+                if ((issued >> s) & 1u)
+                    (void)mbar_wait_bounded(bar + B_FULL + s, ((eph >> s) & 1u) ^ 1u,
+                                            p.timeout_ns, &never);
+    } else if (warp == kScale) {
+        // ====================== page scales, four tiles at a time ======================
+        const int g = lane & 7; // group of 16 positions of the tile
+        uint32_t fph = 0;
+        Walk8 w;
+        w.start(p);
+        for (int batch = 0; !w.done; ++batch) {
+            float2 v = make_float2(0.f, 0.f);
+            int b = -1, kvh = 0, pos = 0;
+            for (int i = 0; i < 4 && !w.done; ++i, w.next(p))
+                if ((lane >> 3) == i && w.t0 + 16 * g < w.t1) {
+                    b = w.b;
+                    kvh = w.kvh;
+                    pos = w.t0 + 16 * g;
+                }
+            if (b >= 0) {
+                const int blk = p.block_table[(size_t)b * p.max_blocks + pos / p.block_size];
+                float vs = 0.f;
+                if (blk >= 0 && blk < sc.num_blocks) {
+                    v.x = __ldg(sc.k + blk * sc.k_block + kvh * sc.k_head);
+                    vs = __ldg(sc.v + blk * sc.v_block + kvh * sc.v_head);
+                }
+                v.y = __log2f(fmaxf(vs, kMinScale));
+            }
+            const int half = batch & 1;
+            const bool got = mbar_wait_bounded(bar + B_SCFREE + half, ((fph >> half) & 1u) ^ 1u,
+                                               p.timeout_ns, abort_flag);
+            if (__any_sync(0xffffffffu, !got)) {
+                if (lane == 0) {
+                    *abort_flag = 1;
+                    atomicCAS(p.status, 0, kStatusTimeoutQ8);
+                }
+                break;
+            }
+            fph ^= 1u << half;
+            sc_sm[half * 32 + lane] = v;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + B_SCFULL + half);
+        }
+    } else if (warp == kMma) {
+        // ============================ MMA issue (1 thread) ============================
+        if (lane == 0) {
+            const uint32_t idesc_qk = idesc_f8(N, false, e5m2), idesc_pv = idesc_f8(N, true, e5m2);
+            uint32_t sph = 0, pph = 0, qph = 0, oph = 0;
+            bool ok = true, q_ready = false;
+            int items_pv = 0;
+            int kslot = 0, vslot = 1; // slots of tile t: 2t, 2t + 1 (mod NS)
+            uint32_t kph = 0, vph = 0;
+            Walk8 qk, pv;
+            qk.start(p);
+            pv.start(p);
+            uint64_t last = global_ns();
+            while (!pv.done) {
+                bool progress = false;
+                if (pv.gt < qk.gt) {
+                    // O^T += V^T . x^T once x(t) is written (V(t) is in by then or soon) and, at
+                    // an item's first tile, the previous item's epilogue has read O^T
+                    const int ps = pv.gt & 1;
+                    if (mbar_test(bar + B_PFULL + ps, (pph >> ps) & 1u) &&
+                        mbar_test(bar + B_FULL + vslot, vph) &&
+                        (!pv.first || items_pv == 0 || mbar_test(bar + B_OFREE, oph))) {
+                        pph ^= 1u << ps;
+                        if (pv.first && items_pv > 0) oph ^= 1u;
+                        if (pv.first) ++items_pv;
+                        tc_fence_after();
+                        const uint64_t vd =
+                            smem_desc_sw128(sb + L::SLOT_OFF + vslot * L::SLOT, 16, 1024);
+                        const uint64_t pd = smem_desc_sw128(sb + L::P_OFF + ps * L::PSLOT, 16, 1024);
+#pragma unroll
+                        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+                            for (int k = 0; k < T / 32; ++k)
+                                mma_f8(tmem + 2 * N + j * N,
+                                       vd + (uint64_t)((j * L::CHUNK + k * 4096) >> 4),
+                                       pd + (uint64_t)((k * 32) >> 4), idesc_pv,
+                                       (pv.first && k == 0) ? 0u : 1u);
+                        tc_commit(bar + B_EMPTY + vslot);
+                        tc_commit(bar + B_PFREE + ps);
+                        tc_commit(bar + B_PVDONE);
+                        if (pv.last()) tc_commit(bar + B_OREADY);
+                        if ((vslot += 2) >= NS) {
+                            vslot -= NS;
+                            vph ^= 1u;
+                        }
+                        progress = true;
+                        pv.next(p);
+                    }
+                }
+                if (!qk.done) {
+                    // S = K . q^T once q of the item and the K tile are in and the softmax has
+                    // released this S slot
+                    const int ss = qk.gt & 1;
+                    if (!q_ready && mbar_test(bar + B_QFULL, qph)) {
+                        qph ^= 1u;
+                        q_ready = true;
+                    }
+                    if (q_ready && mbar_test(bar + B_FULL + kslot, kph) &&
+                        mbar_test(bar + B_SFREE + ss, ((sph >> ss) & 1u) ^ 1u)) {
+                        sph ^= 1u << ss;
+                        tc_fence_after();
+                        const uint64_t kd =
+                            smem_desc_sw128(sb + L::SLOT_OFF + kslot * L::SLOT, 16, 1024);
+                        const uint64_t qd = smem_desc_sw128(sb + L::Q_OFF, 16, 1024);
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8(tmem + ss * N, kd + (uint64_t)((c * L::CHUNK + k * 32) >> 4),
+                                       qd + (uint64_t)((c * L::QCH + k * 32) >> 4), idesc_qk,
+                                       (c | k) != 0 ? 1u : 0u);
+                        tc_commit(bar + B_SFULL + ss);
+                        tc_commit(bar + B_EMPTY + kslot);
+                        if (qk.last()) {
+                            tc_commit(bar + B_QFREE);
+                            q_ready = false;
+                        }
+                        if ((kslot += 2) >= NS) {
+                            kslot -= NS;
+                            kph ^= 1u;
+                        }
+                        progress = true;
+                        qk.next(p);
+                    }
+                }
+                if (progress) {
+                    last = global_ns();
+                } else if (*abort_flag || global_ns() - last > p.timeout_ns) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok && !*abort_flag) {
+                *abort_flag = 1;
+                atomicCAS(p.status, 0, kStatusTimeoutQ8);
+            }
+            // no MMA may be in flight when TMEM is freed
+            tc_commit(bar + B_DRAIN);
+            (void)mbar_wait_bounded(bar + B_DRAIN, 0, p.timeout_ns, &never);
+        }
+        __syncwarp();
+    } else {
+        // ========================= softmax and epilogue (warps 0-3) ========================
+        const int tid = threadIdx.x; // position of the tile (TMEM lane), value column
+        const int Gh = p.hq / it.n_kv_heads, rows = Gh * p.q_len;
+        const int per = (rows + it.row_groups - 1) / it.row_groups;
+        const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+        const bool causal = p.q_len > 1 && !(p.flags & DA_FLAG_NO_CAUSAL);
+        uint32_t sph = 0, pfp = 0, qfp = 0, oph = 0, scp = 0;
+        bool ab = false;
+        int items = 0, gt = 0;
+        int vslot = 1;
+        uint32_t vph = 0;
+        for (int item = blockIdx.x; !ab && item < it.n_items; item += gridDim.x) {
+            int b, kvh, s, rg;
+            decode_item(it, item, b, kvh, s, rg);
+            const int Lb = len8(p, b);
+            const int p0 = s * it.chunk[b], p1 = min(Lb, p0 + it.chunk[b]);
+            const int row0 = rg * per, R = min(per, rows - row0);
+            const size_t wbase = ((size_t)it.split_base[b] + s) * p.n_heads + (size_t)kvh * Gh;
+            if (p1 <= p0) { // an empty item: a neutral partial, no MMA took part
+                if (tid < R) {
+                    const int tok = (row0 + tid) / Gh;
+                    p.ml[wbase + tok * p.hq + (row0 + tid - tok * Gh)] = make_float2(kNeutralM, 0.f);
+                }
+                continue;
+            }
+            // ---- q of this item's rows, once the previous item's QK is done with Q
+            if (items > 0) {
+                const bool okw = mbar_wait_bounded(bar + B_QFREE, qfp, p.timeout_ns, abort_flag);
+                if (bar_or(!okw)) {
+                    ab = true;
+                    break;
+                }
+                qfp ^= 1u;
+            }
+            // a warp takes every fourth row: scaled to [128, 256), cut into terms; a lane has
+            // 4 columns of every chunk
+            for (int r = warp; r < RP; r += 4) {
+                float4 x[NCH];
+                float a = 0.f;
+                const int tok = (row0 + r) / Gh, g = row0 + r - tok * Gh;
+                const float *qr =
+                    p.q + ((size_t)(b * p.q_len + tok) * p.hq + (size_t)kvh * Gh + g) * D + 4 * lane;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < R) x[c] = __ldg(reinterpret_cast<const float4 *>(qr + 128 * c));
+                    x[c].x *= p.scale_log2;
+                    x[c].y *= p.scale_log2;
+                    x[c].z *= p.scale_log2;
+                    x[c].w *= p.scale_log2;
+                    a = fmaxf(a, fmaxf(fmaxf(fabsf(x[c].x), fabsf(x[c].y)),
+                                       fmaxf(fabsf(x[c].z), fabsf(x[c].w))));
+                }
+                a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+                // 2^k with a * 2^k in [128, 256); k within what 2^k and 2^-k can be
+                int k = 134 - (int)(__float_as_uint(a) >> 23);
+                k = a > 0.f ? max(-120, min(120, k)) : 0;
+                const float f = __uint_as_float((uint32_t)(127 + k) << 23);
+                if (lane == 0) {
+                    qf_sm[r] = __uint_as_float((uint32_t)(127 - k) << 23);
+                    lim_sm[r] = r >= R ? 0 : causal ? Lb - p.q_len + 1 + tok : INT_MAX;
+                    wrow_sm[r] = r < R ? tok * p.hq + g : 0;
+                }
+                // an infinite q makes NaN scores, as infinities weighted against each other do
+                const bool nan = !(a <= 3.402823466e38f);
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    float y0 = x[c].x * f, y1 = x[c].y * f, y2 = x[c].z * f, y3 = x[c].w * f;
+                    if (nan) y0 = __int_as_float(0x7fffffff);
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) {
+                        const uint32_t lo = term2(y0, y1), hi = term2(y2, y3);
+                        sts_u32(sb + L::Q_OFF + c * L::QCH + swz(j * RP + r, 4 * lane),
+                                lo | (hi << 16));
+                    }
+                }
+            }
+            if (causal)
+                for (int i = tid; i < D; i += 128) nan_sm[i] = INT_MAX;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + B_QFULL);
+            named_bar_sync(1, 128); // the row tables
+            ++items;
+
+            // ---- tiles
+            float m[RP], l[RP]; // reference (uniform over the threads), this thread's share of l
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                m[r] = -INFINITY;
+                l[r] = 0.f;
+            }
+            const int lim0 = causal ? Lb - p.q_len + 1 : INT_MAX; // the first token's limit
+            bool firsttile = true;
+            for (int t0 = p0, t1; t0 < p1; t0 = t1, ++gt, firsttile = false) {
+                t1 = tile_end<T>(t0, p1);
+                const int ss = gt & 1, half = (gt >> 2) & 1;
+                bool okw = true;
+                if ((gt & 3) == 0) {
+                    okw = mbar_wait_bounded(bar + B_SCFULL + half, (scp >> half) & 1u, p.timeout_ns,
+                                            abort_flag);
+                    scp ^= 1u << half;
+                }
+                okw = okw && mbar_wait_bounded(bar + B_SFULL + ss, (sph >> ss) & 1u, p.timeout_ns,
+                                               abort_flag);
+                okw = okw && mbar_wait_bounded(bar + B_PFREE + ss, ((pfp >> ss) & 1u) ^ 1u,
+                                               p.timeout_ns, abort_flag);
+                sph ^= 1u << ss;
+                pfp ^= 1u << ss;
+                const bool short_tile = t1 - t0 < T, new_tokens = t1 > lim0;
+                if (short_tile || new_tokens)
+                    okw = okw && mbar_wait_bounded(bar + B_FULL + vslot, vph, p.timeout_ns,
+                                                   abort_flag);
+                tc_fence_after();
+                const float2 sv = sc_sm[half * 32 + (gt & 3) * 8 + (tid >> 4)];
+                const int pos = t0 + tid;
+                if (okw && (short_tile || new_tokens)) {
+                    const uint32_t vt = sb + L::SLOT_OFF + vslot * L::SLOT + tid * 128;
+                    if (pos >= t1) {
+                        // V rows past the tile hold whatever the pool has there: 0 * NaN would
+                        // reach O^T. (K rows past it only give scores that are masked.)
+#pragma unroll
+                        for (int i = 0; i < NCH * 8; ++i)
+                            sts_v4(vt + (i >> 3) * L::CHUNK + (((i + tid) & 7) << 4), 0u, 0u, 0u, 0u);
+                    } else if (pos >= lim0) {
+                        // a row that not every token sees: a NaN in it must not reach the others,
+                        // so it is taken out and the epilogue puts it where it belongs
+                        uint8_t *row = sm + L::SLOT_OFF + vslot * L::SLOT;
+                        const uint32_t least = e5m2 ? 0x7c7c7c7cu : 0x7f7f7f7fu;
+                        for (int i = 0; i < D; i += 4) {
+                            uint32_t *c = reinterpret_cast<uint32_t *>(
+                                row + (i >> 7) * L::CHUNK + swz(tid, i & 127));
+                            const uint32_t u = *c, bad = __vcmpgeu4(u & 0x7f7f7f7fu, least);
+                            if (bad) {
+                                *c = u & ~bad;
+                                for (int e = 0; e < 4; ++e)
+                                    if ((bad >> (8 * e)) & 1u)
+                                        atomicMin(nan_sm + i + e, pos - (Lb - p.q_len));
+                            }
+                        }
+                    }
+                }
+                // scores of this position, with the value scale in the exponent
+                float x[RP];
+#pragma unroll
+                for (int r0 = 0; r0 < RP; r0 += RC) {
+                    float v[kTerms][RC];
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) tmem_ld<RC>(tl + ss * N + j * RP + r0, v[j]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < RC; ++i) {
+                        float y = v[kTerms - 1][i];
+#pragma unroll
+                        for (int j = kTerms - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
+                        x[r0 + i] = y * (qf_sm[r0 + i] * sv.x);
+                    }
+                }
+                bool ex = false;
+                if (pos >= t1) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) x[r] = -INFINITY;
+                } else if (new_tokens) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        if (pos >= lim_sm[r]) x[r] = -INFINITY;
+                }
+#pragma unroll
+                for (int r = 0; r < RP; ++r) ex |= x[r] + sv.y > m[r] + kTau;
+                if (bar_or(ex || !okw)) {
+                    if (bar_or(!okw)) { // a wait ran out somewhere: leave together
+                        ab = true;
+                        break;
+                    }
+                    // move the references that scores outgrew; rescale l and O^T
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        // as ordered integers; a NaN counts as -inf
+                        const int u = __float_as_int(fmaxf(x[r] + sv.y, -INFINITY));
+                        const int o = __reduce_max_sync(0xffffffffu, u ^ ((u >> 31) & 0x7fffffff));
+                        if (lane == 0)
+                            red_sm[warp * RP + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
+                    }
+                    named_bar_sync(1, 128);
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const float tm = fmaxf(fmaxf(red_sm[r], red_sm[RP + r]),
+                                               fmaxf(red_sm[2 * RP + r], red_sm[3 * RP + r]));
+                        const float mn = tm > m[r] + kTau ? tm - kHead : m[r];
+                        const float al = mn == m[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
+                        if (tid == 0) alpha_sm[r] = al;
+                        l[r] *= al;
+                        m[r] = mn;
+                    }
+                    if (!firsttile) // PV(t-1) is done with O^T before it is rescaled
+                        okw = mbar_wait_bounded(bar + B_PVDONE, (uint32_t)(gt - 1) & 1u,
+                                                p.timeout_ns, abort_flag);
+                    if (bar_or(!okw)) { // also publishes the factors
+                        ab = true;
+                        break;
+                    }
+                    if (!firsttile) {
+                        tc_fence_after();
+                        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+                            for (int g = 0; g < N / 16; ++g) {
+                                float o[16];
+                                const uint32_t at = tl + 2 * N + j * N + 16 * g;
+                                tmem_ld16(at, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= alpha_sm[(16 * g + i) % RP];
+                                tmem_st16(at, o);
+                            }
+                        tmem_wait_st();
+                    }
+                    named_bar_sync(1, 128); // the factors and maxima are read before they change
+                }
+                // weights: l, and the terms of x into the P buffer
+                const uint32_t pt = sb + L::P_OFF + ss * L::PSLOT;
+#pragma unroll
+                for (int r = 0; r < RP; r += 2) {
+                    const float m0 = m[r] == -INFINITY ? 0.f : m[r];
+                    const float m1 = m[r + 1] == -INFINITY ? 0.f : m[r + 1];
+                    l[r] += ex2(x[r] - m0);
+                    l[r + 1] += ex2(x[r + 1] - m1);
+                    float y0 = ex2(x[r] + sv.y - m0), y1 = ex2(x[r + 1] + sv.y - m1);
+#pragma unroll
+                    for (int j = 0; j < kTerms; ++j) {
+                        const uint32_t c = term2(y0, y1);
+                        sts_u8(pt + swz(j * RP + r, tid), c & 0xff);
+                        sts_u8(pt + swz(j * RP + r + 1, tid), c >> 8);
+                    }
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar + B_SFREE + ss);
+                    mbar_arrive(bar + B_PFULL + ss);
+                    if ((gt & 3) == 3) mbar_arrive(bar + B_SCFREE + half);
+                }
+                if ((vslot += 2) >= NS) {
+                    vslot -= NS;
+                    vph ^= 1u;
+                }
+            }
+            if (ab) break;
+            // ------------------------------- epilogue -------------------------------
+            // l over the threads: lanes by a transposing reduce, then the four warps
+            tr_reduce<RP, 16>(l, lane);
+            if (tr_writer<RP, 16>(lane)) {
+#pragma unroll
+                for (int i = 0; i < tr_out<RP, 16>(); ++i)
+                    red_sm[warp * RP + tr_base<RP, 16>(lane) + i] = l[i];
+            }
+            float mr = -INFINITY; // m of row `tid`
+#pragma unroll
+            for (int r = 0; r < RP; ++r)
+                if (tid == r) mr = m[r];
+            const bool okw = mbar_wait_bounded(bar + B_OREADY, oph, p.timeout_ns, abort_flag);
+            if (bar_or(!okw)) {
+                ab = true;
+                break;
+            }
+            oph ^= 1u;
+            tc_fence_after();
+            for (int j = 0; j < NCH; ++j) {
+                const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
+#pragma unroll
+                for (int r0 = 0; r0 < RP; r0 += RC) {
+                    float v[kTerms][RC];
+#pragma unroll
+                    for (int k = 0; k < kTerms; ++k)
+                        tmem_ld<RC>(tl + 2 * N + j * N + k * RP + r0, v[k]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < RC; ++i) {
+                        float y = v[kTerms - 1][i];
+#pragma unroll
+                        for (int k = kTerms - 2; k >= 0; --k) y = fmaf(y, kTermStep, v[k][i]);
+                        if (r0 + i < R) {
+                            if (nan_from != INT_MAX && (row0 + r0 + i) / Gh >= nan_from)
+                                y = __int_as_float(0x7fffffff);
+                            p.acc[(wbase + wrow_sm[r0 + i]) * D + 128 * j + tid] = y;
+                        }
+                    }
+                }
+            }
+            if (tid < R) {
+                const float lr = red_sm[tid] + red_sm[RP + tid] + red_sm[2 * RP + tid] +
+                                 red_sm[3 * RP + tid];
+                // a NaN score makes the row NaN whatever the other splits hold
+                p.ml[wbase + wrow_sm[tid]] =
+                    isnan(lr) ? make_float2(-kNeutralM, 1.f)
+                              : make_float2(lr > 0.f ? mr * kLn2 : kNeutralM, lr);
+            }
+            tc_fence_before();
+            named_bar_sync(1, 128); // the tables are read before they change
+            if (lane == 0) mbar_arrive(bar + B_OFREE);
+        }
+        if (ab && tid == 0 && !*abort_flag) {
+            *abort_flag = 1;
+            atomicCAS(p.status, 0, kStatusTimeoutQ8);
+        }
+    }
+
+    // ---------------------------------- teardown ----------------------------------
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMma) tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0) griddep_launch_dependents();
+}
+
+template <int D, int RP>
+cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
+                     const Scales8 &sc, const SplitParams &p, int e5m2)
+{
+    auto *fn = gqa_8bit_kernel<D, RP>;
+    constexpr int bytes = Layout<D, RP>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    fn<<<grid, kThreads, bytes, st>>>(km, vm, sc, p, e5m2);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(int rows, int grid, cudaStream_t st, const CUtensorMap &km,
+                     const CUtensorMap &vm, const Scales8 &sc, const SplitParams &p, int e5m2)
+{
+    // the narrowest instantiation that holds the item's rows
+    if (rows <= 4) return launch_t<D, 4>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 8) return launch_t<D, 8>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 16) return launch_t<D, 16>(grid, st, km, vm, sc, p, e5m2);
+    return launch_t<D, 32>(grid, st, km, vm, sc, p, e5m2);
 }
 
 } // namespace
@@ -128,13 +817,14 @@ int q8_rows_per_item(int rows)
 }
 
 cudaError_t launch_gqa_8bit(int code_dtype, int head_dim, int grid, cudaStream_t st,
-                            const Q8Pools &pools, const Scales8 &sc, const SplitParams &p)
+                            const CUtensorMap &km, const CUtensorMap &vm, const Scales8 &sc,
+                            const SplitParams &p)
 {
-    if (head_dim == 128)
-        return code_dtype == DA_E4M3 ? launch_t<__NV_E4M3, 128>(grid, st, pools, sc, p)
-                                     : launch_t<__NV_E5M2, 128>(grid, st, pools, sc, p);
-    return code_dtype == DA_E4M3 ? launch_t<__NV_E4M3, 256>(grid, st, pools, sc, p)
-                                 : launch_t<__NV_E5M2, 256>(grid, st, pools, sc, p);
+    const int rows = p.n_heads / p.items.n_kv_heads;
+    const int per = (rows + p.items.row_groups - 1) / p.items.row_groups;
+    const int e5m2 = code_dtype == DA_E5M2;
+    if (head_dim == 128) return launch_d<128>(per, grid, st, km, vm, sc, p, e5m2);
+    return launch_d<256>(per, grid, st, km, vm, sc, p, e5m2);
 }
 
 } // namespace skv

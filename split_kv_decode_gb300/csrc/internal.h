@@ -250,18 +250,15 @@ __host__ __device__ inline TcLayout tc_layout(int D, int R)
 cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
                           const CUtensorMap &km, const CUtensorMap &vm, const SplitParams &p);
 
-// 8-bit GQA kernel: tiles of kQ8Tile positions (a tile's positions are the 128 rows
-// of the score MMA); at most kQ8Rows query rows a work item, larger groups are
-// cut into row groups.
+// 8-bit GQA kernel: tiles of kQ8Tile positions (the 128 rows of the score MMA); at
+// most kQ8Rows query rows a work item (four terms each, 128 MMA columns), larger
+// groups are cut into row groups.
 constexpr int kQ8Tile = 128;
-constexpr int kQ8Rows = 8;
+constexpr int kQ8Rows = 32;
 int q8_rows_per_item(int rows);
-struct Q8Pools {
-    const uint8_t *k, *v;
-    int64_t k_block, k_pos, k_head, v_block, v_pos, v_head; // strides, bytes
-};
 cudaError_t launch_gqa_8bit(int code_dtype, int head_dim, int grid, cudaStream_t st,
-                            const Q8Pools &pools, const Scales8 &sc, const SplitParams &p);
+                            const CUtensorMap &km, const CUtensorMap &vm, const Scales8 &sc,
+                            const SplitParams &p);
 
 // TMA maps of the SIMT GQA kernel: k and v copy a whole tile of T rows; for a
 // paged pool kb and vb copy box_rows rows, the boxes of a tile that spans a

@@ -428,3 +428,26 @@ def test_codes_are_used_as_they_stand():
                      torch.full((1, 1), 0.375), torch.zeros(1, 1, dtype=torch.int32))
             got = call(queries(1, 1, 1, 1, 128), cache, 16, 1.0, plan_lens=[1])
             np.testing.assert_allclose(got[0, 0, 0], vals[row] * 0.375, rtol=2.0 ** -19, atol=0)
+
+
+def test_a_wait_that_runs_out_is_reported():
+    # the copies are never issued; the next call on the same workspace is sound
+    lens = [500, 2000]
+    cache = paged_cache(39, lens, 16, 2, 128, "e4m3")
+    q = queries(40, 2, 1, 8, 128)
+    kp, vp, ks, vs, t = [y.cuda() for y in cache]
+    x = q[:, 0].contiguous().cuda()
+    dv = A.make_dev(block_table=t, k_pool=kp, v_pool=vp)
+    ws = o = None
+    for flags in (N.DA_FLAG_TEST_NO_TMA, 0):
+        a = A.make_paged_args(x, kp, vp, 0.1, t.shape[1], flags=flags, timeout_us=20000)
+        p = A.decode_attn_plan(a, lens)
+        ws = A.new_workspace(p) if ws is None else ws
+        o = torch.empty_like(x)
+        A.decode_attn_splitk_8bit(a, p, dv, A.make_scales(ks, vs), x, kp, vp, o, ws)
+        if flags:
+            with pytest.raises(A.DecodeAttnError) as e:
+                A.decode_attn_device_status(ws)
+            assert e.value.status == N.DA_ETIMEOUT and "8 bits" in e.value.message
+    A.decode_attn_device_status(ws)
+    check(o.double().cpu().numpy()[:, None], q, cache, lens, 16, "e4m3", 0.1)
