@@ -22,16 +22,16 @@
 // f32 when S or O^T leave TMEM. The products are exact and the sums f32 (measured:
 // relative error 1e-7 on full-range codes).
 //
-// An item is (sequence, KV head, split, row group), rows (query token, head). The
-// roles of the 7 warps, one CTA per SM:
-//   warps 0-3  softmax and epilogue: a thread owns one position of the tile (TMEM lane),
-//              all rows; the reference m of a row moves only when a score outgrows it by
-//              2^8 (then O^T is rescaled), so most tiles take one vote. In the epilogue a
+// An item is (sequence, KV head, split, row group), rows (query token, head). Roles, one
+// CTA per SM:
+//   softmax warpgroups (1, 2 or 4, up to 8 rows each): a thread owns one position of the
+//              tile (TMEM lane); the reference m of a row moves only when a score outgrows it
+//              by 2^8 (then O^T is rescaled), so most tiles take one vote. In the epilogue a
 //              thread owns a value column.
-//   warp 4     TMA producer: K and V tiles through one ring of slots, paged boxes as in the
+//   two warps  TMA producers, K and V tiles through one ring of slots, paged boxes as in the
 //              16-bit tensor-core kernel.
-//   warp 5     TMEM owner and the one thread that issues the MMAs.
-//   warp 6     the page scales of four tiles at a time, two batches ahead.
+//   two warps  MMA issue, one thread each for the scores and for the values.
+//   one warp   the page scales of four tiles at a time, two batches ahead.
 // Every wait is bounded; a wait that runs out sets the status word and the CTA drains
 // and returns.
 #include <climits>
@@ -45,8 +45,6 @@
 namespace skv {
 namespace {
 
-constexpr int kThreads = 224;
-constexpr int kProd = 4, kMma = 5, kScale = 6; // warps
 constexpr int T = kQ8Tile;
 constexpr int kTerms = 4;
 constexpr float kTermStep = 1.f / 16.f;
@@ -60,16 +58,28 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE 
               B_PFULL = B_SFREE + 2, B_PFREE = B_PFULL + 2, B_PVDONE = B_PFREE + 2,
               B_OREADY = B_PVDONE + 1, B_OFREE = B_OREADY + 1, B_QFULL = B_OFREE + 1,
               B_QFREE = B_QFULL + 1, B_SCFULL = B_QFREE + 1, B_SCFREE = B_SCFULL + 2,
-              B_DRAIN = B_SCFREE + 2, B_N = B_DRAIN + 1;
+              B_QKDRAIN = B_SCFREE + 2, B_PVDRAIN = B_QKDRAIN + 1, B_N = B_PVDRAIN + 1;
 
-// shared memory of <D, RP>: RP rows an item at most, N = 4 RP columns
+// Shape and shared memory of <D, RP>: RP rows an item at most, N = 4 RP columns. A
+// softmax warpgroup takes RPW rows of every tile (8, or 4 when there are no more): a
+// thread's share of a tile must not outlast the tile's time on the memory side, and 32
+// rows in one thread took 5200 cycles against 2800.
 template <int D, int RP> struct Layout {
     static constexpr int N = kTerms * RP;
+    static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups
+    static constexpr int RPW = RP / W;
+    static constexpr int THREADS = W * 128 + 160;
+    // warps after the softmax warps
+    static constexpr int KPROD = 4 * W, VPROD = KPROD + 1, QK = KPROD + 2, PV = KPROD + 3,
+                         SCALE = KPROD + 4;
+    // weights as [row term][position] (K-major), or for wide items [position][row term]
+    // (MN-major, rows of 128 bytes): there a thread stores 8 bytes at a time
+    static constexpr bool PMN = N >= 64;
     static constexpr int NCH = D / 128;        // 128-column chunks of a row
     static constexpr int CHUNK = T * 128;      // bytes of a chunk of a tile
     static constexpr int SLOT = NCH * CHUNK;   // a K or V tile
     static constexpr int QCH = N * 128;        // a chunk of Q
-    static constexpr int PSLOT = N * 128;      // one P buffer
+    static constexpr int PSLOT = PMN ? T * 128 : N * 128; // one P buffer
     static constexpr int Q_OFF = 0;
     static constexpr int P_OFF = Q_OFF + NCH * QCH;
     static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
@@ -79,10 +89,12 @@ template <int D, int RP> struct Layout {
                          ROW = SC + 2 * 4 * 8 * 8, RED = ROW + 4 * RP * 4, NANC = RED + 4 * RP * 4,
                          TAIL = NANC + D * 4;
     static constexpr int SLOTS_FIT = (232448 - 1024 - SLOT_OFF - TAIL) / SLOT;
-    static constexpr int NS = SLOTS_FIT > kMaxSlots ? kMaxSlots : SLOTS_FIT;
+    // even: K tiles then use the even slots and V tiles the odd ones, so the two producers
+    // never wait for each other's slots (a barrier's parity tells one phase back, not two)
+    static constexpr int NS = (SLOTS_FIT > kMaxSlots ? kMaxSlots : SLOTS_FIT) / 2 * 2;
     static constexpr int TAIL_OFF = SLOT_OFF + NS * SLOT;
     static constexpr int BYTES = TAIL_OFF + TAIL + 1024;
-    static_assert(NS >= 4, "K and V tiles of two steps in flight");
+    static_assert(NS >= 4 && NS % 2 == 0, "K and V tiles of two steps in flight");
     static_assert((2 + NCH) * N <= 512, "TMEM columns: two S slots and O^T");
     static_assert(QCH % 1024 == 0 && BYTES <= 232448, "swizzle atoms, shared memory");
 };
@@ -112,17 +124,17 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
                  : "memory");
 }
 
-// f32 accumulation; A e4m3 or e5m2 (K-major, or MN-major with a_mn), B e4m3 K-major
-__device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn, bool a_e5m2)
+// f32 accumulation; A e4m3 or e5m2, B e4m3, each K-major or (a_mn, b_mn) MN-major
+__device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn, bool b_mn, bool a_e5m2)
 {
     return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((a_mn ? 1u : 0u) << 15) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// C consecutive 32-bit TMEM columns (C = 4 or 8) of this warp's lane quarter
-template <int C> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float *v);
-template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float *v)
+// C consecutive 32-bit TMEM columns of this warp's lane quarter
+template <int C> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float *v)
 {
+    static_assert(C == 4, "four columns");
     uint32_t r[4];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -130,18 +142,14 @@ template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float *v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, float *v)
-{
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
 
-__device__ __forceinline__ bool bar_or(bool pred) { return named_bar_or(1, 128, pred); }
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const float *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])),
+                 "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
+                 : "memory");
+}
 
 // two values to e4m3 (x in the low byte); *x, *y: what is left, times 16
 __device__ __forceinline__ uint32_t term2(float &x, float &y)
@@ -206,14 +214,14 @@ struct Walk8 {
 };
 
 template <int D, int RP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
     gqa_8bit_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ Scales8 sc, const __grid_constant__ SplitParams p,
                     const int e5m2)
 {
     using L = Layout<D, RP>;
-    constexpr int N = L::N, NCH = L::NCH, NS = L::NS;
-    constexpr int RC = RP < 8 ? RP : 8; // rows taken from TMEM at a time
+    constexpr int N = L::N, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW;
+    constexpr int RC = 4; // rows taken from TMEM at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -227,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *alpha_sm = qf_sm + RP;                             // rescale factor
     int *lim_sm = reinterpret_cast<int *>(alpha_sm + RP);     // positions seen: below lim
     int *wrow_sm = lim_sm + RP;                               // workspace row
-    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // [4 warps][RP]
+    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // [4 W warps][RPW]
     int *nan_sm = reinterpret_cast<int *>(tail + L::NANC);    // [D] first token that sees a NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ItemTable &it = p.items;
@@ -240,84 +248,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar + B_SFULL + s, 1);
-            mbar_init(bar + B_SFREE + s, 4);
-            mbar_init(bar + B_PFULL + s, 4);
+            mbar_init(bar + B_SFREE + s, 4 * W);
+            mbar_init(bar + B_PFULL + s, 4 * W);
             mbar_init(bar + B_PFREE + s, 1);
             mbar_init(bar + B_SCFULL + s, 1);
-            mbar_init(bar + B_SCFREE + s, 4);
+            mbar_init(bar + B_SCFREE + s, 4 * W);
         }
         mbar_init(bar + B_PVDONE, 1);
         mbar_init(bar + B_OREADY, 1);
-        mbar_init(bar + B_OFREE, 4);
-        mbar_init(bar + B_QFULL, 4);
+        mbar_init(bar + B_OFREE, 4 * W);
+        mbar_init(bar + B_QFULL, 4 * W);
         mbar_init(bar + B_QFREE, 1);
-        mbar_init(bar + B_DRAIN, 1);
+        mbar_init(bar + B_QKDRAIN, 1);
+        mbar_init(bar + B_PVDRAIN, 1);
         *abort_flag = 0;
         if (blockIdx.x == 0) *p.status = 0;
         fence_mbar_init();
     }
-    if (warp == kMma) tmem_alloc(tmem_slot, 512);
+    if (warp == L::QK) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == kProd) {
-        // =============================== TMA producer ===============================
+    if (warp == L::KPROD || warp == L::VPROD) {
+        // =================== TMA producers, one for K and one for V ===================
         // box j holds positions [t0 + j*h, t0 + (j+1)*h) of a 128-column chunk, h =
         // box_rows (16 to 128: a divisor of the tile and of block_size), so no box spans
         // two blocks and a tile spans blocks freely; h * 128 bytes is a multiple of the
-        // swizzle atom, so the boxes land as one box of the tile would
-        if (lane == 0) {
-            tma_prefetch_map(&kmap);
-            tma_prefetch_map(&vmap);
-        }
+        // swizzle atom, so the boxes land as one box of the tile would. A box costs its
+        // warp about 75 cycles to issue, and pages of 16 positions make 8 of each 16 KB:
+        // one warp for both tiles took 2100 cycles per 128 positions of 128 columns,
+        // the memory 1400.
+        const bool isv = warp == L::VPROD;
+        const CUtensorMap *map = isv ? &vmap : &kmap;
+        if (lane == 0) tma_prefetch_map(map);
         const uint64_t pol = l2_evict_first_policy();
         const int bs = p.block_size, h = p.box_rows, nbox = T / h;
-        uint32_t eph = 0, issued = 0;
-        int win_b = -1, win_lo = 0, slot = 0;
-        int32_t win_entry = 0;
+        // this lane's box of tile w: its block, the first slot in it
+        auto look_up = [&](const Walk8 &w, int &slot0) {
+            int blk = p.oob_block;
+            if (!w.done && lane < nbox) {
+                const int pos = w.t0 + lane * h, idx = pos / bs;
+                slot0 = pos - idx * bs;
+                if (idx < p.max_blocks) {
+                    blk = __ldg(p.block_table + (size_t)w.b * p.max_blocks + idx);
+                    if (blk < 0 || blk > p.oob_block) blk = p.oob_block;
+                }
+            }
+            return blk;
+        };
+        uint32_t ph = 0, issued = 0, last = 0; // slots with copies, their last phases
+        int slot = isv ? 1 : 0;                // slots of tile t: K 2t, V 2t + 1 (mod NS)
         bool ok = true;
         Walk8 w;
-        for (w.start(p); ok && !w.done; w.next(p)) {
-            const int lo = w.t0 / bs, hi = (w.t0 + T - 1) / bs;
-            if (w.b != win_b || lo < win_lo || hi >= win_lo + 32) {
-                win_b = w.b;
-                win_lo = lo;
-                win_entry = lo + lane < p.max_blocks
-                                ? p.block_table[(size_t)w.b * p.max_blocks + lo + lane]
-                                : p.oob_block;
-                if (win_entry < 0 || win_entry > p.oob_block) win_entry = p.oob_block;
+        w.start(p);
+        int slot0 = 0, blk = look_up(w, slot0);
+        while (!w.done) {
+            Walk8 nx = w; // the next tile's blocks are looked up while this one is issued
+            nx.next(p);
+            int nslot0 = 0;
+            const int nblk = look_up(nx, nslot0);
+            // a slot's first use finds its barrier's previous phase complete
+            bool got = true;
+            if (lane == 0)
+                got = mbar_wait_bounded(bar + B_EMPTY + slot, ph ^ 1u, p.timeout_ns, abort_flag);
+            if (!__shfl_sync(0xffffffffu, got, 0)) {
+                ok = false;
+                break;
             }
-            const int pos = w.t0 + min(lane, nbox - 1) * h, idx = pos / bs;
-            const int blk = __shfl_sync(0xffffffffu, win_entry, idx - win_lo);
+            if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
+                issued |= 1u << slot;
+                last = (last & ~(1u << slot)) | (ph << slot);
+                uint8_t *dst = sm + L::SLOT_OFF + slot * L::SLOT + lane * h * 128;
+                if (lane == 0) mbar_arrive_expect_tx(bar + B_FULL + slot, L::SLOT);
+                __syncwarp();
+                if (lane < nbox) {
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                // a slot's first use finds its barrier's previous phase complete
-                bool got = true;
-                if (lane == 0)
-                    got = mbar_wait_bounded(bar + B_EMPTY + slot, ((eph >> slot) & 1u) ^ 1u,
-                                            p.timeout_ns, abort_flag);
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
-                    ok = false;
-                    break;
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_4d(dst + c * L::CHUNK, map, bar + B_FULL + slot, c * 128, w.kvh,
+                                    slot0, blk, pol);
                 }
-                eph ^= 1u << slot;
-                if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
-                    issued |= 1u << slot;
-                    uint8_t *dst = sm + L::SLOT_OFF + slot * L::SLOT;
-                    if (lane == 0) mbar_arrive_expect_tx(bar + B_FULL + slot, L::SLOT);
-                    __syncwarp();
-                    if (lane < nbox) {
-#pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tma_load_4d(dst + c * L::CHUNK + lane * h * 128, kv ? &vmap : &kmap,
-                                        bar + B_FULL + slot, c * 128, w.kvh, pos - idx * bs, blk,
-                                        pol);
-                    }
-                }
-                if (++slot == NS) slot = 0;
             }
+            if ((slot += 2) >= NS) {
+                slot -= NS;
+                ph ^= 1u;
+            }
+            w = nx;
+            blk = nblk;
+            slot0 = nslot0;
         }
         if (!ok && lane == 0) {
             *abort_flag = 1;
@@ -327,9 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0)
             for (int s = 0; s < NS; ++s)
                 if ((issued >> s) & 1u)
-                    (void)mbar_wait_bounded(bar + B_FULL + s, ((eph >> s) & 1u) ^ 1u,
-                                            p.timeout_ns, &never);
-    } else if (warp == kScale) {
+                    (void)mbar_wait_bounded(bar + B_FULL + s, (last >> s) & 1u, p.timeout_ns,
+                                            &never);
+    } else if (warp == L::SCALE) {
         // ====================== page scales, four tiles at a time ======================
         const int g = lane & 7; // group of 16 positions of the tile
         uint32_t fph = 0;
@@ -368,115 +387,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_SCFULL + half);
         }
-    } else if (warp == kMma) {
-        // ============================ MMA issue (1 thread) ============================
+    } else if (warp == L::QK || warp == L::PV) {
+        // ================ MMA issue: one thread for S, one for O^T ================
+        // Two issuers, so that neither polls for the other's inputs.
         if (lane == 0) {
-            const uint32_t idesc_qk = idesc_f8(N, false, e5m2), idesc_pv = idesc_f8(N, true, e5m2);
-            uint32_t sph = 0, pph = 0, qph = 0, oph = 0;
-            bool ok = true, q_ready = false;
-            int items_pv = 0;
-            int kslot = 0, vslot = 1; // slots of tile t: 2t, 2t + 1 (mod NS)
-            uint32_t kph = 0, vph = 0;
-            Walk8 qk, pv;
-            qk.start(p);
-            pv.start(p);
-            uint64_t last = global_ns();
-            while (!pv.done) {
-                bool progress = false;
-                if (pv.gt < qk.gt) {
-                    // O^T += V^T . x^T once x(t) is written (V(t) is in by then or soon) and, at
-                    // an item's first tile, the previous item's epilogue has read O^T
-                    const int ps = pv.gt & 1;
-                    if (mbar_test(bar + B_PFULL + ps, (pph >> ps) & 1u) &&
-                        mbar_test(bar + B_FULL + vslot, vph) &&
-                        (!pv.first || items_pv == 0 || mbar_test(bar + B_OFREE, oph))) {
-                        pph ^= 1u << ps;
-                        if (pv.first && items_pv > 0) oph ^= 1u;
-                        if (pv.first) ++items_pv;
-                        tc_fence_after();
-                        const uint64_t vd =
-                            smem_desc_sw128(sb + L::SLOT_OFF + vslot * L::SLOT, 16, 1024);
-                        const uint64_t pd = smem_desc_sw128(sb + L::P_OFF + ps * L::PSLOT, 16, 1024);
-#pragma unroll
-                        for (int j = 0; j < NCH; ++j)
-#pragma unroll
-                            for (int k = 0; k < T / 32; ++k)
-                                mma_f8(tmem + 2 * N + j * N,
-                                       vd + (uint64_t)((j * L::CHUNK + k * 4096) >> 4),
-                                       pd + (uint64_t)((k * 32) >> 4), idesc_pv,
-                                       (pv.first && k == 0) ? 0u : 1u);
-                        tc_commit(bar + B_EMPTY + vslot);
-                        tc_commit(bar + B_PFREE + ps);
-                        tc_commit(bar + B_PVDONE);
-                        if (pv.last()) tc_commit(bar + B_OREADY);
-                        if ((vslot += 2) >= NS) {
-                            vslot -= NS;
-                            vph ^= 1u;
-                        }
-                        progress = true;
-                        pv.next(p);
-                    }
-                }
-                if (!qk.done) {
+            const bool qk = warp == L::QK;
+            const uint32_t idesc = idesc_f8(N, !qk, !qk && L::PMN, e5m2);
+            uint32_t ph = 0, iph = 0, sph = 0; // phases: tile slot, item, S or P buffer
+            int slot = qk ? 0 : 1, items = 0;  // slots of tile t: K 2t, V 2t + 1 (mod NS)
+            bool ok = true;
+            Walk8 w;
+            for (w.start(p); ok && !w.done; w.next(p)) {
+                const int ss = w.gt & 1;
+                const uint64_t ad = smem_desc_sw128(sb + L::SLOT_OFF + slot * L::SLOT, 16, 1024);
+                auto wait = [&](int which, uint32_t parity) {
+                    ok = ok && mbar_wait_bounded(bar + which, parity, p.timeout_ns, abort_flag);
+                };
+                if (qk) {
                     // S = K . q^T once q of the item and the K tile are in and the softmax has
                     // released this S slot
-                    const int ss = qk.gt & 1;
-                    if (!q_ready && mbar_test(bar + B_QFULL, qph)) {
-                        qph ^= 1u;
-                        q_ready = true;
+                    if (w.first) {
+                        wait(B_QFULL, iph);
+                        iph ^= 1u;
                     }
-                    if (q_ready && mbar_test(bar + B_FULL + kslot, kph) &&
-                        mbar_test(bar + B_SFREE + ss, ((sph >> ss) & 1u) ^ 1u)) {
-                        sph ^= 1u << ss;
-                        tc_fence_after();
-                        const uint64_t kd =
-                            smem_desc_sw128(sb + L::SLOT_OFF + kslot * L::SLOT, 16, 1024);
-                        const uint64_t qd = smem_desc_sw128(sb + L::Q_OFF, 16, 1024);
+                    wait(B_FULL + slot, ph);
+                    wait(B_SFREE + ss, ((sph >> ss) & 1u) ^ 1u);
+                    sph ^= 1u << ss;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t qd = smem_desc_sw128(sb + L::Q_OFF, 16, 1024);
 #pragma unroll
-                        for (int c = 0; c < NCH; ++c)
+                    for (int c = 0; c < NCH; ++c)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f8(tmem + ss * N, kd + (uint64_t)((c * L::CHUNK + k * 32) >> 4),
-                                       qd + (uint64_t)((c * L::QCH + k * 32) >> 4), idesc_qk,
-                                       (c | k) != 0 ? 1u : 0u);
-                        tc_commit(bar + B_SFULL + ss);
-                        tc_commit(bar + B_EMPTY + kslot);
-                        if (qk.last()) {
-                            tc_commit(bar + B_QFREE);
-                            q_ready = false;
-                        }
-                        if ((kslot += 2) >= NS) {
-                            kslot -= NS;
-                            kph ^= 1u;
-                        }
-                        progress = true;
-                        qk.next(p);
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8(tmem + ss * N, ad + (uint64_t)((c * L::CHUNK + k * 32) >> 4),
+                                   qd + (uint64_t)((c * L::QCH + k * 32) >> 4), idesc,
+                                   (c | k) != 0 ? 1u : 0u);
+                    tc_commit(bar + B_SFULL + ss);
+                    tc_commit(bar + B_EMPTY + slot);
+                    if (w.last()) tc_commit(bar + B_QFREE);
+                } else {
+                    // O^T += V^T . x^T once the V tile is in, x(t) is written and, at an item's
+                    // first tile, the previous item's epilogue has read O^T
+                    wait(B_FULL + slot, ph);
+                    if (w.first && items++ > 0) {
+                        wait(B_OFREE, iph);
+                        iph ^= 1u;
                     }
+                    wait(B_PFULL + ss, (sph >> ss) & 1u);
+                    sph ^= 1u << ss;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t pd = smem_desc_sw128(sb + L::P_OFF + ss * L::PSLOT, 16, 1024);
+#pragma unroll
+                    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+                        for (int k = 0; k < T / 32; ++k)
+                            mma_f8(tmem + 2 * N + j * N,
+                                   ad + (uint64_t)((j * L::CHUNK + k * 4096) >> 4),
+                                   pd + (uint64_t)((k * (L::PMN ? 4096 : 32)) >> 4), idesc,
+                                   (w.first && k == 0) ? 0u : 1u);
+                    tc_commit(bar + B_EMPTY + slot);
+                    tc_commit(bar + B_PFREE + ss);
+                    tc_commit(bar + B_PVDONE);
+                    if (w.last()) tc_commit(bar + B_OREADY);
                 }
-                if (progress) {
-                    last = global_ns();
-                } else if (*abort_flag || global_ns() - last > p.timeout_ns) {
-                    ok = false;
-                    break;
+                if ((slot += 2) >= NS) {
+                    slot -= NS;
+                    ph ^= 1u;
                 }
             }
-            if (!ok && !*abort_flag) {
+            if (!ok) {
                 *abort_flag = 1;
                 atomicCAS(p.status, 0, kStatusTimeoutQ8);
             }
             // no MMA may be in flight when TMEM is freed
-            tc_commit(bar + B_DRAIN);
-            (void)mbar_wait_bounded(bar + B_DRAIN, 0, p.timeout_ns, &never);
+            tc_commit(bar + (qk ? B_QKDRAIN : B_PVDRAIN));
+            (void)mbar_wait_bounded(bar + (qk ? B_QKDRAIN : B_PVDRAIN), 0, p.timeout_ns, &never);
         }
         __syncwarp();
     } else {
-        // ========================= softmax and epilogue (warps 0-3) ========================
-        const int tid = threadIdx.x; // position of the tile (TMEM lane), value column
+        // ====================== softmax and epilogue (warpgroups 0..W-1) ======================
+        const int wg = W > 1 ? warp >> 2 : 0, r00 = wg * RPW; // this warpgroup's first row
+        const int tid = threadIdx.x & 127; // position of the tile (TMEM lane), value column
+        float *red = red_sm + wg * 4 * RPW;
+        auto bar_or = [&](bool pred) { return named_bar_or(1 + wg, 128, pred); };
         const int Gh = p.hq / it.n_kv_heads, rows = Gh * p.q_len;
         const int per = (rows + it.row_groups - 1) / it.row_groups;
-        const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + r00;
         const bool causal = p.q_len > 1 && !(p.flags & DA_FLAG_NO_CAUSAL);
-        uint32_t sph = 0, pfp = 0, qfp = 0, oph = 0, scp = 0;
+        uint32_t sph = 0, pfp = 0, iph = 0, oph = 0, scp = 0; // iph: per item
         bool ab = false;
         int items = 0, gt = 0;
         int vslot = 1;
@@ -489,24 +489,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row0 = rg * per, R = min(per, rows - row0);
             const size_t wbase = ((size_t)it.split_base[b] + s) * p.n_heads + (size_t)kvh * Gh;
             if (p1 <= p0) { // an empty item: a neutral partial, no MMA took part
-                if (tid < R) {
+                if (wg == 0 && tid < R) {
                     const int tok = (row0 + tid) / Gh;
                     p.ml[wbase + tok * p.hq + (row0 + tid - tok * Gh)] = make_float2(kNeutralM, 0.f);
                 }
                 continue;
             }
-            // ---- q of this item's rows, once the previous item's QK is done with Q
+            // ---- q of this item's rows, once the previous item's QK is done with Q and every
+            // warp with its row tables
             if (items > 0) {
-                const bool okw = mbar_wait_bounded(bar + B_QFREE, qfp, p.timeout_ns, abort_flag);
+                bool okw =
+                    mbar_wait_bounded(bar + B_QFREE, iph ^ 1u, p.timeout_ns, abort_flag);
+                okw = okw &&
+                      mbar_wait_bounded(bar + B_OFREE, iph ^ 1u, p.timeout_ns, abort_flag);
                 if (bar_or(!okw)) {
                     ab = true;
                     break;
                 }
-                qfp ^= 1u;
             }
-            // a warp takes every fourth row: scaled to [128, 256), cut into terms; a lane has
+            // the warps take rows in turn: scaled to [128, 256), cut into terms; a lane has
             // 4 columns of every chunk
-            for (int r = warp; r < RP; r += 4) {
+            for (int r = warp; r < RP; r += 4 * W) {
                 float4 x[NCH];
                 float a = 0.f;
                 const int tok = (row0 + r) / Gh, g = row0 + r - tok * Gh;
@@ -548,17 +551,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (causal)
-                for (int i = tid; i < D; i += 128) nan_sm[i] = INT_MAX;
+                for (int i = threadIdx.x; i < D; i += 128 * W) nan_sm[i] = INT_MAX;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_QFULL);
-            named_bar_sync(1, 128); // the row tables
+            { // the other warps' row tables
+                const bool okw = mbar_wait_bounded(bar + B_QFULL, iph, p.timeout_ns, abort_flag);
+                if (bar_or(!okw)) {
+                    ab = true;
+                    break;
+                }
+            }
+            iph ^= 1u;
             ++items;
 
             // ---- tiles
-            float m[RP], l[RP]; // reference (uniform over the threads), this thread's share of l
+            float m[RPW], l[RPW]; // reference (uniform over the threads), this thread's share of l
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
+            for (int r = 0; r < RPW; ++r) {
                 m[r] = -INFINITY;
                 l[r] = 0.f;
             }
@@ -580,13 +590,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sph ^= 1u << ss;
                 pfp ^= 1u << ss;
                 const bool short_tile = t1 - t0 < T, new_tokens = t1 > lim0;
-                if (short_tile || new_tokens)
+                const bool fix_v = wg == 0 && (short_tile || new_tokens);
+                if (fix_v)
                     okw = okw && mbar_wait_bounded(bar + B_FULL + vslot, vph, p.timeout_ns,
                                                    abort_flag);
                 tc_fence_after();
                 const float2 sv = sc_sm[half * 32 + (gt & 3) * 8 + (tid >> 4)];
                 const int pos = t0 + tid;
-                if (okw && (short_tile || new_tokens)) {
+                if (okw && fix_v) {
                     const uint32_t vt = sb + L::SLOT_OFF + vslot * L::SLOT + tid * 128;
                     if (pos >= t1) {
                         // V rows past the tile hold whatever the pool has there: 0 * NaN would
@@ -613,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // scores of this position, with the value scale in the exponent
-                float x[RP];
+                float x[RPW];
 #pragma unroll
-                for (int r0 = 0; r0 < RP; r0 += RC) {
+                for (int r0 = 0; r0 < RPW; r0 += RC) {
                     float v[kTerms][RC];
 #pragma unroll
                     for (int j = 0; j < kTerms; ++j) tmem_ld<RC>(tl + ss * N + j * RP + r0, v[j]);
@@ -625,20 +636,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float y = v[kTerms - 1][i];
 #pragma unroll
                         for (int j = kTerms - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
-                        x[r0 + i] = y * (qf_sm[r0 + i] * sv.x);
+                        x[r0 + i] = y * (qf_sm[r00 + r0 + i] * sv.x);
                     }
                 }
                 bool ex = false;
                 if (pos >= t1) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) x[r] = -INFINITY;
+                    for (int r = 0; r < RPW; ++r) x[r] = -INFINITY;
                 } else if (new_tokens) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r)
-                        if (pos >= lim_sm[r]) x[r] = -INFINITY;
+                    for (int r = 0; r < RPW; ++r)
+                        if (pos >= lim_sm[r00 + r]) x[r] = -INFINITY;
                 }
 #pragma unroll
-                for (int r = 0; r < RP; ++r) ex |= x[r] + sv.y > m[r] + kTau;
+                for (int r = 0; r < RPW; ++r) ex |= x[r] + sv.y > m[r] + kTau;
                 if (bar_or(ex || !okw)) {
                     if (bar_or(!okw)) { // a wait ran out somewhere: leave together
                         ab = true;
@@ -646,21 +657,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // move the references that scores outgrew; rescale l and O^T
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < RPW; ++r) {
                         // as ordered integers; a NaN counts as -inf
                         const int u = __float_as_int(fmaxf(x[r] + sv.y, -INFINITY));
                         const int o = __reduce_max_sync(0xffffffffu, u ^ ((u >> 31) & 0x7fffffff));
                         if (lane == 0)
-                            red_sm[warp * RP + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
+                            red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
                     }
-                    named_bar_sync(1, 128);
+                    named_bar_sync(1 + wg, 128);
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const float tm = fmaxf(fmaxf(red_sm[r], red_sm[RP + r]),
-                                               fmaxf(red_sm[2 * RP + r], red_sm[3 * RP + r]));
+                    for (int r = 0; r < RPW; ++r) {
+                        const float tm = fmaxf(fmaxf(red[r], red[RPW + r]),
+                                               fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
                         const float mn = tm > m[r] + kTau ? tm - kHead : m[r];
                         const float al = mn == m[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
-                        if (tid == 0) alpha_sm[r] = al;
+                        if (tid == 0) alpha_sm[r00 + r] = al;
                         l[r] *= al;
                         m[r] = mn;
                     }
@@ -675,33 +686,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         for (int j = 0; j < NCH; ++j)
 #pragma unroll
-                            for (int g = 0; g < N / 16; ++g) {
-                                float o[16];
-                                const uint32_t at = tl + 2 * N + j * N + 16 * g;
-                                tmem_ld16(at, o);
-                                tmem_wait_ld();
+                            for (int k = 0; k < kTerms; ++k)
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= alpha_sm[(16 * g + i) % RP];
-                                tmem_st16(at, o);
-                            }
+                                for (int r0 = 0; r0 < RPW; r0 += RC) {
+                                    float o[RC];
+                                    const uint32_t at = tl + 2 * N + j * N + k * RP + r0;
+                                    tmem_ld<RC>(at, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < RC; ++i) o[i] *= alpha_sm[r00 + r0 + i];
+                                    tmem_st4(at, o);
+                                }
                         tmem_wait_st();
                     }
-                    named_bar_sync(1, 128); // the factors and maxima are read before they change
+                    named_bar_sync(1 + wg, 128); // the factors and maxima are read before they change
                 }
                 // weights: l, and the terms of x into the P buffer
                 const uint32_t pt = sb + L::P_OFF + ss * L::PSLOT;
+                float y[RPW];
 #pragma unroll
-                for (int r = 0; r < RP; r += 2) {
+                for (int r = 0; r < RPW; ++r) {
                     const float m0 = m[r] == -INFINITY ? 0.f : m[r];
-                    const float m1 = m[r + 1] == -INFINITY ? 0.f : m[r + 1];
                     l[r] += ex2(x[r] - m0);
-                    l[r + 1] += ex2(x[r + 1] - m1);
-                    float y0 = ex2(x[r] + sv.y - m0), y1 = ex2(x[r + 1] + sv.y - m1);
+                    y[r] = ex2(x[r] + sv.y - m0);
+                }
 #pragma unroll
-                    for (int j = 0; j < kTerms; ++j) {
-                        const uint32_t c = term2(y0, y1);
-                        sts_u8(pt + swz(j * RP + r, tid), c & 0xff);
-                        sts_u8(pt + swz(j * RP + r + 1, tid), c >> 8);
+                for (int j = 0; j < kTerms; ++j) {
+                    if constexpr (L::PMN) {
+                        const uint32_t a = term2(y[0], y[1]) | (term2(y[2], y[3]) << 16);
+                        const uint32_t c = term2(y[4], y[5]) | (term2(y[6], y[7]) << 16);
+                        sts_v2(pt + swz(tid, j * RP + r00), a, c);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < RPW; r += 2) {
+                            const uint32_t c = term2(y[r], y[r + 1]);
+                            sts_u8(pt + swz(j * RP + r, tid), c & 0xff);
+                            sts_u8(pt + swz(j * RP + r + 1, tid), c >> 8);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -720,15 +741,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ab) break;
             // ------------------------------- epilogue -------------------------------
             // l over the threads: lanes by a transposing reduce, then the four warps
-            tr_reduce<RP, 16>(l, lane);
-            if (tr_writer<RP, 16>(lane)) {
+            tr_reduce<RPW, 16>(l, lane);
+            if (tr_writer<RPW, 16>(lane)) {
 #pragma unroll
-                for (int i = 0; i < tr_out<RP, 16>(); ++i)
-                    red_sm[warp * RP + tr_base<RP, 16>(lane) + i] = l[i];
+                for (int i = 0; i < tr_out<RPW, 16>(); ++i)
+                    red[(warp & 3) * RPW + tr_base<RPW, 16>(lane) + i] = l[i];
             }
             float mr = -INFINITY; // m of row `tid`
 #pragma unroll
-            for (int r = 0; r < RP; ++r)
+            for (int r = 0; r < RPW; ++r)
                 if (tid == r) mr = m[r];
             const bool okw = mbar_wait_bounded(bar + B_OREADY, oph, p.timeout_ns, abort_flag);
             if (bar_or(!okw)) {
@@ -740,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < NCH; ++j) {
                 const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
 #pragma unroll
-                for (int r0 = 0; r0 < RP; r0 += RC) {
+                for (int r0 = 0; r0 < RPW; r0 += RC) {
                     float v[kTerms][RC];
 #pragma unroll
                     for (int k = 0; k < kTerms; ++k)
@@ -751,24 +772,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float y = v[kTerms - 1][i];
 #pragma unroll
                         for (int k = kTerms - 2; k >= 0; --k) y = fmaf(y, kTermStep, v[k][i]);
-                        if (r0 + i < R) {
-                            if (nan_from != INT_MAX && (row0 + r0 + i) / Gh >= nan_from)
+                        const int r = r00 + r0 + i;
+                        if (r < R) {
+                            if (nan_from != INT_MAX && (row0 + r) / Gh >= nan_from)
                                 y = __int_as_float(0x7fffffff);
-                            p.acc[(wbase + wrow_sm[r0 + i]) * D + 128 * j + tid] = y;
+                            p.acc[(wbase + wrow_sm[r]) * D + 128 * j + tid] = y;
                         }
                     }
                 }
             }
-            if (tid < R) {
-                const float lr = red_sm[tid] + red_sm[RP + tid] + red_sm[2 * RP + tid] +
-                                 red_sm[3 * RP + tid];
+            if (tid < RPW && r00 + tid < R) {
+                const float lr =
+                    red[tid] + red[RPW + tid] + red[2 * RPW + tid] + red[3 * RPW + tid];
                 // a NaN score makes the row NaN whatever the other splits hold
-                p.ml[wbase + wrow_sm[tid]] =
+                p.ml[wbase + wrow_sm[r00 + tid]] =
                     isnan(lr) ? make_float2(-kNeutralM, 1.f)
                               : make_float2(lr > 0.f ? mr * kLn2 : kNeutralM, lr);
             }
             tc_fence_before();
-            named_bar_sync(1, 128); // the tables are read before they change
+            named_bar_sync(1 + wg, 128); // the sums are read before they change
             if (lane == 0) mbar_arrive(bar + B_OFREE);
         }
         if (ab && tid == 0 && !*abort_flag) {
@@ -781,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMma) tmem_dealloc(tmem, 512);
+    if (warp == L::QK) tmem_dealloc(tmem, 512);
     if (threadIdx.x == 0) griddep_launch_dependents();
 }
 
@@ -793,7 +815,7 @@ cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUt
     constexpr int bytes = Layout<D, RP>::BYTES;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    fn<<<grid, kThreads, bytes, st>>>(km, vm, sc, p, e5m2);
+    fn<<<grid, (Layout<D, RP>::THREADS), bytes, st>>>(km, vm, sc, p, e5m2);
     return cudaGetLastError();
 }
 

@@ -125,6 +125,13 @@ def test_few_ctas_walk_many_items():
     run_check([600, 70], 64, 40, 2, 256, "e5m2", num_sms=2, splits=3, seed=6)
 
 
+@pytest.mark.parametrize("rows", [3, 8, 16, 32])
+@pytest.mark.parametrize("d", [128, 256])
+def test_long_items(rows, d):
+    # dozens of tiles an item, so that every slot of the ring is used again and again
+    run_check([9000, 4000], 16, rows, 1, d, "e4m3", num_sms=2, splits=1, seed=rows + d)
+
+
 def test_relative_accuracy_of_f32_output():
     # the 2-norm of the error: every source above averages over hundreds of positions;
     # 20-bit operands alone leave 2^-20 / sqrt(3) of the result
