@@ -14,114 +14,359 @@
 #include <cuda_fp8.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace skv {
 int set_error(int code, const char *phase, const char *msg); // api.cpp
 }
 
+using skv::named_bar_sync;
+
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
+struct Side { // keys or values; strides in elements
+    const void *src;
+    uint8_t *pool;
+    float *scale;
+    int64_t src_stride, src_head, block, pos, head, scale_block, scale_head;
+    int32_t units; // 16-element units of a row
+};
 struct AppendParams {
-    da_append_t a;
-    const void *src[2];
+    Side side[2];
     const int64_t *slot_map;
-    uint8_t *pool[2];
-    float *scale[2];
-    int64_t src_stride[2], src_head_stride[2];
-    int64_t block_stride[2], pos_stride[2], head_stride[2];
-    int64_t scale_block_stride[2], scale_head_stride[2];
-    int32_t dim[2];
+    int32_t tokens, heads, block_size, shift, num_blocks; // shift: log2 of block_size, or -1
+    int32_t chunk;                                        // tokens a group looks after
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+// 16 elements as they are stored
+template <typename ST> struct Unit {
+    static constexpr int V = sizeof(ST); // 16-byte vectors: 2 or 4
+    uint4 v[V];
+};
+template <typename ST> constexpr int kUnits = 8 / sizeof(ST); // units a thread holds: 128 bytes
 
-template <__nv_fp8_interpretation_t F> __device__ __forceinline__ uint8_t encode(float x)
+template <typename ST> __device__ __forceinline__ void load_unit(Unit<ST> &u, const ST *p)
 {
-    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, F);
-}
-template <__nv_fp8_interpretation_t F> __device__ __forceinline__ float decode(uint8_t c)
-{
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, F)));
+#pragma unroll
+    for (int i = 0; i < Unit<ST>::V; ++i) u.v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
 }
 
-// the least e >= -100 with a <= 1.75 * 2^(top + e), as the bits of 2^e (a >= 0, finite)
+// the largest |x| of a unit as the bits of its type, infinities and NaN included
+// (magnitudes order as integers); 16-bit types: two at a time
+__device__ __forceinline__ uint32_t top_bits(const Unit<float> &u, uint32_t m)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m = max(m, u.v[i].x & 0x7fffffffu);
+        m = max(m, u.v[i].y & 0x7fffffffu);
+        m = max(m, u.v[i].z & 0x7fffffffu);
+        m = max(m, u.v[i].w & 0x7fffffffu);
+    }
+    return m;
+}
+template <typename ST> __device__ __forceinline__ uint32_t top_bits(const Unit<ST> &u, uint32_t m)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        m = __vmaxu2(m, u.v[i].x & 0x7fff7fffu);
+        m = __vmaxu2(m, u.v[i].y & 0x7fff7fffu);
+        m = __vmaxu2(m, u.v[i].z & 0x7fff7fffu);
+        m = __vmaxu2(m, u.v[i].w & 0x7fff7fffu);
+    }
+    return m;
+}
+
+template <typename ST> struct Bits;
+template <> struct Bits<float> {
+    static constexpr uint32_t kInf = 0x7f800000u;
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return m; }
+    static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
+};
+template <> struct Bits<__half> {
+    static constexpr uint32_t kInf = 0x7c00u;
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+    static __device__ __forceinline__ float value(uint32_t b)
+    {
+        return __half2float(__ushort_as_half((unsigned short)b));
+    }
+};
+template <> struct Bits<__nv_bfloat16> {
+    static constexpr uint32_t kInf = 0x7f80u;
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+    static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
+};
+
+// a unit's elements in f32
+__device__ __forceinline__ void widen(const Unit<float> &u, float *f)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[4 * i] = __uint_as_float(u.v[i].x);
+        f[4 * i + 1] = __uint_as_float(u.v[i].y);
+        f[4 * i + 2] = __uint_as_float(u.v[i].z);
+        f[4 * i + 3] = __uint_as_float(u.v[i].w);
+    }
+}
+__device__ __forceinline__ void widen2(uint32_t w, float *f, __half)
+{
+    const float2 x = __half22float2(*reinterpret_cast<__half2 *>(&w));
+    f[0] = x.x;
+    f[1] = x.y;
+}
+__device__ __forceinline__ void widen2(uint32_t w, float *f, __nv_bfloat16)
+{
+    f[0] = __uint_as_float(w << 16);
+    f[1] = __uint_as_float(w & 0xffff0000u);
+}
+template <typename ST> __device__ __forceinline__ void widen(const Unit<ST> &u, float *f)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        widen2(u.v[i].x, f + 8 * i, ST());
+        widen2(u.v[i].y, f + 8 * i + 2, ST());
+        widen2(u.v[i].z, f + 8 * i + 4, ST());
+        widen2(u.v[i].w, f + 8 * i + 6, ST());
+    }
+}
+
+// the largest finite |x| of a unit (the rare path: something was not finite)
+template <typename ST> __device__ __noinline__ float top_finite(const Unit<ST> &u, float m)
+{
+    float f[16];
+    widen(u, f);
+    for (int i = 0; i < 16; ++i) {
+        const float a = fabsf(f[i]);
+        if (a <= 3.402823466e38f) m = fmaxf(m, a);
+    }
+    return m;
+}
+
+// 16 f32 -> 16 codes, saturating, round to nearest even
+template <__nv_fp8_interpretation_t F> __device__ __forceinline__ uint4 encode16(const float *f)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]),
+                                                    __NV_SATFINITE, F);
+        const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]),
+                                                    __NV_SATFINITE, F);
+        w[i] = a | (b << 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <__nv_fp8_interpretation_t F> __device__ __forceinline__ void decode16(uint4 c, float *f)
+{
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2 h(__nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), F));
+        const float2 x = __half22float2(h);
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+    }
+}
+
+// the least e >= -100 with a <= 1.75 * 2^(top + e), as 2^e (a >= 0, finite)
 __device__ __forceinline__ float scale_for(float a, int top)
 {
     const uint32_t u = __float_as_uint(a);
-    int e = (int)(u >> 23) - 127 - top + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = max(e, -100);
-    return __uint_as_float((uint32_t)(e + 127) << 23);
+    const int e = (int)(u >> 23) - 127 - top + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
 }
 
-template <typename ST, __nv_fp8_interpretation_t F>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
+// A group of G warps looks after `chunk` tokens of one head, keys or values: it finds the
+// runs that begin among them and writes each (a run is a page's new rows, so nobody else
+// touches that page and head). A page that fits the group's registers is read once:
+// G follows from the page's size. Every warp of a group finds the runs for itself.
+template <typename ST, __nv_fp8_interpretation_t F, int G>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
-    const int t = blockIdx.x, h = blockIdx.y, kv = blockIdx.z;
-    const int P = p.a.block_size, T = p.a.n_tokens, dim = p.dim[kv];
-    const int64_t slot = p.slot_map[t];
-    if (slot < 0 || slot / P >= p.a.num_blocks) return;
-    const int p0 = (int)(slot % P);
-    if (t > 0 && p0 > 0 && p.slot_map[t - 1] == slot - 1) return; // not a run's first row
-    // the run's length: rows at consecutive slots up to the block's end
-    __shared__ int n_s;
-    __shared__ float red[kThreads / 32];
-    if (threadIdx.x == 0) n_s = min(P - p0, T - t);
-    __syncthreads();
-    for (int i = threadIdx.x; i < min(P - p0, T - t); i += kThreads)
-        if (p.slot_map[t + i] != slot + i) {
-            atomicMin(&n_s, i);
-            break;
-        }
-    __syncthreads();
-    const int n = n_s;
-    const int64_t blk = slot / P;
-    const ST *src = static_cast<const ST *>(p.src[kv]) + (size_t)t * p.src_stride[kv] +
-                    (size_t)h * p.src_head_stride[kv];
-    uint8_t *page = p.pool[kv] + blk * p.block_stride[kv] + h * p.head_stride[kv];
-    float *sp = p.scale[kv] + blk * p.scale_block_stride[kv] + h * p.scale_head_stride[kv];
-    const float was = *sp;
+    constexpr int TG = 32 * G;
+    __shared__ uint32_t red_bits[2][kWarps];
+    __shared__ float red_f[2][kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / G, gt = threadIdx.x - group * TG; // thread of the group
+    const int P = p.block_size, T = p.tokens;
+    // tasks: head fastest, then keys and values, then chunks
+    const int64_t task = (int64_t)blockIdx.x * (kWarps / G) + group;
+    const int h = (int)(task % p.heads), kv = (int)(task / p.heads & 1);
+    const int64_t c0 = task / p.heads / 2 * p.chunk;
+    if (c0 >= T) return; // the whole group
+    const int c1 = (int)min((int64_t)T, c0 + p.chunk);
+    const Side &sd = p.side[kv];
+    const ST *src0 = static_cast<const ST *>(sd.src) + (int64_t)h * sd.src_head;
+    const int64_t slots = (int64_t)p.num_blocks * P;
+    int parity = 0; // of the reduction buffers
 
-    float amax = 0.f;
-    for (int i = threadIdx.x; i < n * dim; i += kThreads) {
-        const float a = fabsf(to_f(src[(size_t)(i / dim) * p.src_stride[kv] + i % dim]));
-        if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
-    }
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    float s = scale_for(amax, F == __NV_E4M3 ? 8 : 15);
-    if (p0 > 0) s = fmaxf(s, was);
-    if (p0 > 0 && s > was) { // the older rows move to the new scale
-        const float f = was / s;
-        for (int i = threadIdx.x; i < p0 * dim; i += kThreads) {
-            uint8_t *c = page + (int64_t)(i / dim) * p.pos_stride[kv] + i % dim;
-            *c = encode<F>(decode<F>(*c) * f);
+    for (int w0 = (int)c0; w0 < c1; w0 += 32) {
+        const int t = w0 + lane;
+        const int64_t s = t < T ? p.slot_map[t] : -1;
+        int64_t prev = __shfl_up_sync(0xffffffffu, s, 1);
+        if (lane == 0) prev = t > 0 ? p.slot_map[t - 1] : -2;
+        const bool in = s >= 0 && s < slots;
+        const int64_t blk = in ? (p.shift >= 0 ? s >> p.shift : s / P) : 0;
+        const int off = (int)(s - blk * P);
+        unsigned heads = __ballot_sync(0xffffffffu, t < c1 && in && (off == 0 || prev != s - 1));
+        while (heads) {
+            const int f = __ffs(heads) - 1;
+            heads &= heads - 1;
+            // the run: rows at consecutive slots, up to the page's end
+            const int t0 = w0 + f, p0 = __shfl_sync(0xffffffffu, off, f);
+            const int64_t s0 = __shfl_sync(0xffffffffu, s, f), b0 = __shfl_sync(0xffffffffu, blk, f);
+            const int most = min(P - p0, T - t0);
+            int n = 0;
+            for (;;) {
+                const int i = n + lane;
+                const bool cont = i < most && p.slot_map[t0 + i] == s0 + i;
+                const unsigned stop = ~__ballot_sync(0xffffffffu, cont);
+                if (stop) {
+                    n += __ffs(stop) - 1;
+                    break;
+                }
+                n += 32;
+            }
+            float *sp = sd.scale + b0 * sd.scale_block + h * sd.scale_head;
+            const float was = p0 > 0 ? *sp : 0.f;
+            const ST *src = src0 + (int64_t)t0 * sd.src_stride;
+            uint8_t *page = sd.pool + b0 * sd.block + h * sd.head;
+            // thread gt takes units gt, gt + TG, ... of the run's n * units
+            const int U = sd.units, dr = TG / U, dc = TG - dr * U;
+            const int row_first = gt / U, col_first = gt - row_first * U;
+            Unit<ST> u[kUnits<ST>];
+            uint32_t top = 0;
+            int r = row_first, c = col_first;
+            auto step = [&] {
+                r += dr;
+                c += dc;
+                if (c >= U) {
+                    c -= U;
+                    ++r;
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < kUnits<ST>; ++k) {
+                if (r < n) load_unit(u[k], src + (int64_t)r * sd.src_stride + 16 * c);
+                else
+                    for (int i = 0; i < Unit<ST>::V; ++i) u[k].v[i] = make_uint4(0, 0, 0, 0);
+                step();
+            }
+#pragma unroll
+            for (int k = 0; k < kUnits<ST>; ++k) top = top_bits(u[k], top);
+            const int r_rest = r, c_rest = c; // what does not fit the registers
+            for (; r < n; step()) {
+                Unit<ST> x;
+                load_unit(x, src + (int64_t)r * sd.src_stride + 16 * c);
+                top = top_bits(x, top);
+            }
+            top = __reduce_max_sync(0xffffffffu, Bits<ST>::join(top));
+            if constexpr (G > 1) {
+                if (lane == 0) red_bits[parity][warp] = top;
+                named_bar_sync(1 + group, TG);
+#pragma unroll
+                for (int w = 0; w < G; ++w) top = max(top, red_bits[parity][group * G + w]);
+            }
+            float amax = Bits<ST>::value(top);
+            if (top >= Bits<ST>::kInf) { // (the same for the whole group)
+                amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < kUnits<ST>; ++k) amax = top_finite(u[k], amax);
+                for (r = r_rest, c = c_rest; r < n; step()) {
+                    Unit<ST> x;
+                    load_unit(x, src + (int64_t)r * sd.src_stride + 16 * c);
+                    amax = top_finite(x, amax);
+                }
+                amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+                if constexpr (G > 1) {
+                    if (lane == 0) red_f[parity][warp] = amax;
+                    named_bar_sync(1 + group, TG);
+#pragma unroll
+                    for (int w = 0; w < G; ++w) amax = fmaxf(amax, red_f[parity][group * G + w]);
+                }
+            }
+            parity ^= 1;
+            const float sc = fmaxf(scale_for(amax, F == __NV_E4M3 ? 8 : 15), was);
+            // sc is a power of two, unless it is the scale that another quantiser gave the
+            // page's older rows
+            const bool pow2 = (__float_as_uint(sc) & 0x7fffffu) == 0;
+            const float inv = 1.f / sc;
+            auto put = [&](const Unit<ST> &x, int row, int col) {
+                float y[16];
+                widen(x, y);
+                if (pow2) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] *= inv;
+                } else {
+                    for (int i = 0; i < 16; ++i) y[i] /= sc;
+                }
+                *reinterpret_cast<uint4 *>(page + (int64_t)(p0 + row) * sd.pos + 16 * col) =
+                    encode16<F>(y);
+            };
+            r = row_first;
+            c = col_first;
+#pragma unroll
+            for (int k = 0; k < kUnits<ST>; ++k) {
+                if (r < n) put(u[k], r, c);
+                step();
+            }
+            for (; r < n; step()) {
+                Unit<ST> x;
+                load_unit(x, src + (int64_t)r * sd.src_stride + 16 * c);
+                put(x, r, c);
+            }
+            if (p0 > 0 && sc > was) { // the older rows move to the new scale
+                const float ratio = was / sc;
+#pragma unroll 4
+                for (int i = gt; i < p0 * U; i += TG) {
+                    uint4 *at = reinterpret_cast<uint4 *>(page + (int64_t)(i / U) * sd.pos +
+                                                          16 * (i % U));
+                    float y[16];
+                    decode16<F>(*at, y);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] *= ratio;
+                    *at = encode16<F>(y);
+                }
+            }
+            if (gt == 0 && sc != was) *sp = sc;
         }
     }
-    // s is a power of two, unless it is the scale that another quantiser gave the
-    // block's older rows
-    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
-    const float inv = 1.f / s;
-    auto scaled = [&](float x) { return pow2 ? x * inv : x / s; };
-    for (int i = threadIdx.x; i < n * dim; i += kThreads)
-        page[(int64_t)(p0 + i / dim) * p.pos_stride[kv] + i % dim] =
-            encode<F>(scaled(to_f(src[(size_t)(i / dim) * p.src_stride[kv] + i % dim])));
-    if (threadIdx.x == 0) *sp = s;
 }
 
 int bad(const char *msg) { return skv::set_error(DA_EINVAL, "args", msg); }
 bool off16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
-template <typename ST> void launch(const AppendParams &p, cudaStream_t st)
+template <typename ST, __nv_fp8_interpretation_t F, int G>
+void launch_g(AppendParams &p, cudaStream_t st)
 {
-    const dim3 grid(p.a.n_tokens, p.a.n_kv_heads, 2);
-    if (p.a.code_dtype == DA_E4M3) append_kernel<ST, __NV_E4M3><<<grid, kThreads, 0, st>>>(p);
-    else append_kernel<ST, __NV_E5M2><<<grid, kThreads, 0, st>>>(p);
+    // Few rows: a group per row, so that runs go side by side (a decode step's are one row
+    // each). Many rows (over two waves of warps): a group per page's worth of rows, which
+    // hold one or two runs.
+    const int64_t lanes = (int64_t)p.heads * 2;
+    p.chunk = (int64_t)p.tokens * lanes * G > 2 * 152 * 64 ? p.block_size : 1;
+    const int64_t tasks = (p.tokens + (int64_t)p.chunk - 1) / p.chunk * lanes;
+    const int64_t grid = (tasks * G + kWarps - 1) / kWarps;
+    append_kernel<ST, F, G><<<(unsigned)grid, kThreads, 0, st>>>(p);
+}
+
+template <typename ST, __nv_fp8_interpretation_t F> void launch_f(AppendParams &p, cudaStream_t st)
+{
+    // warps whose registers hold a page of one head (4 KB each)
+    const int64_t page = (int64_t)p.block_size * std::max(p.side[0].units, p.side[1].units) * 16;
+    constexpr int64_t warp = 32 * kUnits<ST> * 16;
+    if (page <= warp) launch_g<ST, F, 1>(p, st);
+    else if (page <= 4 * warp) launch_g<ST, F, 4>(p, st);
+    else launch_g<ST, F, 8>(p, st);
+}
+
+template <typename ST> void launch(AppendParams &p, int code, cudaStream_t st)
+{
+    if (code == DA_E4M3) launch_f<ST, __NV_E4M3>(p, st);
+    else launch_f<ST, __NV_E5M2>(p, st);
 }
 
 } // namespace
@@ -163,34 +408,25 @@ extern "C" int decode_attn_append_8bit(const da_append_t *a, const void *k_new, 
     const cudaError_t pre = cudaGetLastError();
     if (pre != cudaSuccess) return skv::set_error(DA_ECUDA, "before append", cudaGetErrorString(pre));
     AppendParams p;
-    p.a = *a;
+    p.side[0] = {k_new, static_cast<uint8_t *>(k_pool), k_scale, a->k_src_stride,
+                 a->k_src_head_stride, a->k_block_stride, a->k_pos_stride, a->k_head_stride,
+                 a->k_scale_block_stride, a->k_scale_head_stride, a->head_dim / 16};
+    p.side[1] = {v_new, static_cast<uint8_t *>(v_pool), v_scale, a->v_src_stride,
+                 a->v_src_head_stride, a->v_block_stride, a->v_pos_stride, a->v_head_stride,
+                 a->v_scale_block_stride, a->v_scale_head_stride, a->v_dim / 16};
     p.slot_map = slot_map;
-    p.src[0] = k_new;
-    p.src[1] = v_new;
-    p.pool[0] = static_cast<uint8_t *>(k_pool);
-    p.pool[1] = static_cast<uint8_t *>(v_pool);
-    p.scale[0] = k_scale;
-    p.scale[1] = v_scale;
-    p.src_stride[0] = a->k_src_stride;
-    p.src_stride[1] = a->v_src_stride;
-    p.src_head_stride[0] = a->k_src_head_stride;
-    p.src_head_stride[1] = a->v_src_head_stride;
-    p.block_stride[0] = a->k_block_stride;
-    p.block_stride[1] = a->v_block_stride;
-    p.pos_stride[0] = a->k_pos_stride;
-    p.pos_stride[1] = a->v_pos_stride;
-    p.head_stride[0] = a->k_head_stride;
-    p.head_stride[1] = a->v_head_stride;
-    p.scale_block_stride[0] = a->k_scale_block_stride;
-    p.scale_block_stride[1] = a->v_scale_block_stride;
-    p.scale_head_stride[0] = a->k_scale_head_stride;
-    p.scale_head_stride[1] = a->v_scale_head_stride;
-    p.dim[0] = a->head_dim;
-    p.dim[1] = a->v_dim;
+    p.tokens = a->n_tokens;
+    p.heads = a->n_kv_heads;
+    p.block_size = a->block_size;
+    p.num_blocks = a->num_blocks;
+    p.shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (a->block_size == 1 << s) p.shift = s;
+    p.chunk = 1;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a->src_dtype == DA_F32) launch<float>(p, st);
-    else if (a->src_dtype == DA_F16) launch<__half>(p, st);
-    else launch<__nv_bfloat16>(p, st);
+    if (a->src_dtype == DA_F32) launch<float>(p, a->code_dtype, st);
+    else if (a->src_dtype == DA_F16) launch<__half>(p, a->code_dtype, st);
+    else launch<__nv_bfloat16>(p, a->code_dtype, st);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "append", cudaGetErrorString(e));
     return DA_OK;
