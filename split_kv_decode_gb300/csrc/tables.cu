@@ -33,35 +33,13 @@ struct TablesParams {
     int64_t *slot_map;
     int32_t *cu_new;
     int32_t slots; // entries of slot_map
+    int32_t shift; // log2 of block_size, or -1
+    int32_t wide;  // slot_map is 16-byte aligned
 };
 
-// exclusive prefix sum of v over the block's threads; *total: the sum
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *total, int64_t *warp_sums)
+// the last i in [lo, hi] with base[i] <= x (base ascending, base[lo] <= x)
+__device__ __forceinline__ int find(const int32_t *base, int lo, int hi, int x)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        before += w < warp ? warp_sums[w] : 0;
-        all += warp_sums[w];
-    }
-    __syncthreads();
-    *total = all;
-    return before + x - v;
-}
-
-// the last i in [0, n) with base[i] <= x (base ascending, base[0] = 0)
-__device__ __forceinline__ int find(const int32_t *base, int n, int x)
-{
-    int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (base[mid] <= x) lo = mid;
@@ -70,49 +48,130 @@ __device__ __forceinline__ int find(const int32_t *base, int n, int x)
     return lo;
 }
 
+// Inclusive prefix sums of a and b over the warp's lanes.
+__device__ __forceinline__ void warp_scan(int64_t &a, int64_t &b)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+            a += x;
+            b += y;
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) grow_tables_kernel(const TablesParams p)
 {
-    __shared__ int64_t warp_sums[kThreads / 32];
-    __shared__ int32_t len_s[kThreads], have_s[kThreads], add_base[kThreads + 1],
-        need_base[kThreads + 1], given_base[kThreads + 1];
+    __shared__ int64_t sums[2][kThreads / 32];
+    __shared__ int32_t len_s[kThreads], have_s[kThreads], add_base[kThreads],
+        need_base[kThreads], given_base[kThreads];
+    __shared__ int last_s;
     const da_tables_t &t = p.t;
-    const int B = t.batch, P = t.block_size, tid = threadIdx.x;
+    const int B = t.batch, P = t.block_size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     const int32_t L = tid < B ? t.seq_lens[tid] : 0;
     const int32_t n = tid < B ? p.new_lens[tid] : 0;
     const int32_t F = t.state[0], old_status = t.state[1];
     const bool gone = n < 0;
     const int64_t end = (int64_t)L + (gone ? 0 : n);
-    bool fits = L >= 0 && end <= (int64_t)t.max_blocks_per_seq * P && end <= INT32_MAX;
-    const int have = fits ? (int)(((int64_t)L + P - 1) / P) : 0;
-    const int need = fits && !gone ? (int)((end + P - 1) / P) - have : 0;
+    const bool fits = L >= 0 && end <= (int64_t)t.max_blocks_per_seq * P && end <= INT32_MAX;
+    auto pages = [&](int x) { // ceil(x / P), x >= 0
+        return p.shift >= 0 ? (int)(((uint32_t)x + (uint32_t)P - 1) >> p.shift)
+                            : (int)(((uint32_t)x + (uint32_t)P - 1) / (uint32_t)P);
+    };
+    const int have = fits ? pages(L) : 0;
+    const int need = fits && !gone ? pages((int)end) - have : 0;
     const int given = fits && gone ? have : 0;
     const int add = fits && !gone ? n : 0;
 
-    int64_t total_need, total_given, total_add;
-    const int64_t nb = block_scan(need, &total_need, warp_sums);
-    const int64_t gb = block_scan(given, &total_given, warp_sums);
-    const int64_t ab = block_scan(add, &total_add, warp_sums);
-    fits = __syncthreads_and(fits) && F >= 0 && F + total_given <= t.num_blocks &&
-           total_add <= p.slots;
-    const bool enough = total_need <= F + total_given;
-    const bool ok = fits && enough;
+    // prefix sums of the blocks taken and given (each below 2^31: one word) and the rows
+    int64_t blocks = ((int64_t)need << 32) | (int64_t)given, rows = add;
+    const int64_t own_blocks = blocks, own_rows = rows;
+    warp_scan(blocks, rows);
+    if (lane == 31) {
+        sums[0][warp] = blocks;
+        sums[1][warp] = rows;
+    }
+    const bool all_fit = __syncthreads_and(fits);
+    int64_t total_blocks = 0, total_rows = 0;
+    blocks -= own_blocks;
+    rows -= own_rows;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        blocks += w < warp ? sums[0][w] : 0;
+        rows += w < warp ? sums[1][w] : 0;
+        total_blocks += sums[0][w];
+        total_rows += sums[1][w];
+    }
+    const int64_t total_need = total_blocks >> 32, total_given = total_blocks & 0x7fffffff;
+    const bool sound =
+        all_fit && F >= 0 && F + total_given <= t.num_blocks && total_rows <= p.slots;
+    const bool ok = sound && total_need <= F + total_given;
     len_s[tid] = L;
     have_s[tid] = have;
-    add_base[tid] = ok ? (int32_t)ab : 0;
-    need_base[tid] = ok ? (int32_t)nb : 0;
-    given_base[tid] = ok ? (int32_t)gb : 0;
-    const int adds = ok ? (int)total_add : 0, takes = ok ? (int)total_need : 0,
+    add_base[tid] = ok ? (int32_t)rows : 0;
+    need_base[tid] = ok ? (int32_t)(blocks >> 32) : 0;
+    given_base[tid] = ok ? (int32_t)(blocks & 0x7fffffff) : 0;
+    const int adds = ok ? (int)total_rows : 0, takes = ok ? (int)total_need : 0,
               gives = ok ? (int)total_given : 0;
-    // this CTA has read the lengths and the state: the last one writes them
+    // this CTA has read the lengths and the state: the last one to have writes them
     __threadfence();
-    __shared__ int last_s;
     __syncthreads();
-    if (tid == 0) {
-        last_s = 1;
-        if (gridDim.x > 1) last_s = atomicAdd(t.state_out + 2, 1) == (int)gridDim.x - 1;
+    if (tid == 0)
+        last_s = gridDim.x == 1 || atomicAdd(t.state_out + 2, 1) == (int)gridDim.x - 1;
+
+    // the k-th released block, and the k-th block taken
+    auto released = [&](int k) {
+        const int b = find(given_base, 0, B - 1, k);
+        return t.block_table[(size_t)b * t.max_blocks_per_seq + k - given_base[b]];
+    };
+    auto taken = [&](int k) {
+        return k < gives ? released(gives - 1 - k) : t.free_list[F - 1 - (k - gives)];
+    };
+    // Slots: a warp takes 64 consecutive ones, a lane two (a 16-byte store). One search
+    // finds the sequences of the first and the last, and the lanes search between them
+    // only where those differ.
+    const int gwarp = blockIdx.x * (kThreads / 32) + warp, warps = gridDim.x * (kThreads / 32);
+    for (int64_t j0 = (int64_t)gwarp * 64; j0 < p.slots; j0 += (int64_t)warps * 64) {
+        const int probe = min((int)(lane ? j0 + 63 : j0), max(adds - 1, 0));
+        const int at = find(add_base, 0, B - 1, probe);
+        const int b0 = __shfl_sync(0xffffffffu, at, 0), b1 = __shfl_sync(0xffffffffu, at, 1);
+        int64_t slot[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t j = j0 + 2 * lane + e;
+            slot[e] = -1;
+            if (j < adds) {
+                const int b = b0 == b1 ? b0 : find(add_base, b0, b1, (int)j);
+                const uint32_t pos = (uint32_t)(len_s[b] + ((int)j - add_base[b]));
+                const int i = (int)(p.shift >= 0 ? pos >> p.shift : pos / (uint32_t)P);
+                const int blk = i < have_s[b]
+                                    ? t.block_table[(size_t)b * t.max_blocks_per_seq + i]
+                                    : taken(need_base[b] + i - have_s[b]);
+                slot[e] = (int64_t)blk * P + (pos - (uint32_t)i * (uint32_t)P);
+            }
+        }
+        const int64_t j = j0 + 2 * lane;
+        if (p.wide && j + 1 < p.slots) {
+            *reinterpret_cast<longlong2 *>(p.slot_map + j) = make_longlong2(slot[0], slot[1]);
+        } else {
+            if (j < p.slots) p.slot_map[j] = slot[0];
+            if (j + 1 < p.slots) p.slot_map[j + 1] = slot[1];
+        }
     }
-    __syncthreads();
+    // table entries of the blocks taken; released blocks that nobody took
+    const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
+#pragma unroll 4
+    for (int k = first; k < takes; k += stride) {
+        const int b = find(need_base, 0, B - 1, k);
+        t.block_table[(size_t)b * t.max_blocks_per_seq + have_s[b] + k - need_base[b]] = taken(k);
+    }
+#pragma unroll 4
+    for (int k = first; k < gives - takes; k += stride) t.free_list[F + k] = released(k);
+
+    __syncthreads(); // last_s
     if (last_s) {
         if (tid < B) {
             t.seq_lens_out[tid] = ok ? (gone ? 0 : (int32_t)end) : L;
@@ -121,39 +180,10 @@ __global__ void __launch_bounds__(kThreads) grow_tables_kernel(const TablesParam
         if (tid == 0) {
             if (p.cu_new) p.cu_new[B] = adds;
             t.state_out[0] = F + gives - takes;
-            t.state_out[1] = old_status ? old_status
-                             : ok       ? 0
-                                        : (fits ? DA_ENOSPACE : DA_EINVAL);
+            t.state_out[1] = old_status ? old_status : ok ? 0 : sound ? DA_ENOSPACE : DA_EINVAL;
             t.state_out[2] = 0;
         }
     }
-
-    // the k-th released block, and the k-th block taken
-    auto released = [&](int k) {
-        const int b = find(given_base, B, k);
-        return t.block_table[(size_t)b * t.max_blocks_per_seq + k - given_base[b]];
-    };
-    auto taken = [&](int k) {
-        return k < gives ? released(gives - 1 - k) : t.free_list[F - 1 - (k - gives)];
-    };
-    const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
-    for (int j = first; j < p.slots; j += stride) {
-        int64_t slot = -1;
-        if (j < adds) {
-            const int b = find(add_base, B, j);
-            const int pos = len_s[b] + j - add_base[b], i = pos / P;
-            const int blk = i < have_s[b]
-                                ? t.block_table[(size_t)b * t.max_blocks_per_seq + i]
-                                : taken(need_base[b] + i - have_s[b]);
-            slot = (int64_t)blk * P + (pos - i * P);
-        }
-        p.slot_map[j] = slot;
-    }
-    for (int k = first; k < takes; k += stride) {
-        const int b = find(need_base, B, k);
-        t.block_table[(size_t)b * t.max_blocks_per_seq + have_s[b] + k - need_base[b]] = taken(k);
-    }
-    for (int k = first; k < gives - takes; k += stride) t.free_list[F + k] = released(k);
 }
 
 int bad(const char *msg) { return skv::set_error(DA_EINVAL, "args", msg); }
@@ -190,7 +220,15 @@ extern "C" int decode_attn_grow_tables(const da_tables_t *t, const int32_t *new_
     p.slot_map = slot_map;
     p.cu_new = cu_new;
     p.slots = (int32_t)slot_capacity;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(152 * 4, slot_capacity / kThreads));
+    p.shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (t->block_size == 1 << s) p.shift = s;
+    p.wide = reinterpret_cast<uintptr_t>(slot_map) % 16 == 0;
+    // CTAs for the most that the call may have to write: the slots, 512 a CTA, or the
+    // tables' entries (blocks taken or released), 1024 a CTA; at most four an SM
+    const int64_t most = std::max(slot_capacity / 512,
+                                  (int64_t)t->batch * t->max_blocks_per_seq / 1024);
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(152 * 4, most));
     grow_tables_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "tables", cudaGetErrorString(e));
