@@ -285,20 +285,29 @@ def decode_attn_splitk_proj(args: N.DaArgs, plan: N.DaPlan, proj: N.DaProj, q: t
 
 # ---- 8-bit paged caches ----------------------------------------------------------
 
+# These calls take a few microseconds on the GPU, so their marshalling is kept lean: raw
+# pointers and the raw current stream (3 us less than through a torch.cuda.Stream).
+
 def _on(dev: torch.device, what: str, *tensors: Optional[torch.Tensor]) -> None:
     for t in tensors:
         if t is not None and t.device != dev:
             raise ValueError(f"{what}: every tensor must be on {dev} (got one on {t.device})")
 
 
-def _launch(dev: torch.device, stream, call) -> None:
-    """call(stream handle) with `dev` current: the current stream of the tensors'
-    device, not of whichever device happens to be current."""
+def _launch(dev: torch.device, stream, fn, *args) -> None:
+    """fn(*args, stream handle) with `dev` current: by default on the current stream of
+    the tensors' device, not of whichever device happens to be current."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if dev.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(call(_stream(stream)))
+            rc = fn(*args, handle)
+    if rc:
+        _check(rc)
 
 
 def make_tables(seq_lens: torch.Tensor, block_table: torch.Tensor, free_list: torch.Tensor,
@@ -351,15 +360,17 @@ def decode_attn_grow_tables(tables: N.DaTables, new_lens: torch.Tensor,
                                or cu_new.numel() != tables.batch + 1):
         raise TypeError("cu_new must be a contiguous int32 tensor of batch + 1 entries")
     _on(dev, "decode_attn_grow_tables", slot_map, cu_new)
-    _launch(dev, stream, lambda st: N.load().decode_attn_grow_tables(
-        ctypes.byref(tables), _ptr(new_lens), _ptr(slot_map), slot_map.numel(), _ptr(cu_new), st))
+    _launch(dev, stream, N.load().decode_attn_grow_tables, ctypes.byref(tables),
+            new_lens.data_ptr(), slot_map.data_ptr(), slot_map.numel(),
+            0 if cu_new is None else cu_new.data_ptr())
 
 
 def decode_attn_tables_status(state: torch.Tensor, stream=None) -> None:
     """Synchronises; raises if a decode_attn_grow_tables call on this state failed
     since the last check (and clears the status)."""
-    _launch(state.device, stream,
-            lambda st: N.load().decode_attn_tables_status(_ptr(state), st))
+    if state.dtype != torch.int32 or not state.is_cuda:
+        raise TypeError("state must be an int32 CUDA tensor")
+    _launch(state.device, stream, N.load().decode_attn_tables_status, state.data_ptr())
 
 
 def make_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.Tensor,
@@ -410,9 +421,9 @@ def decode_attn_append_8bit(append: N.DaAppend, k_new: torch.Tensor, v_new: torc
     if dev.type != "cuda":
         raise TypeError("the pools must be CUDA tensors")
     _on(dev, "decode_attn_append_8bit", k_new, v_new, slot_map, v_pool, k_scale, v_scale)
-    _launch(dev, stream, lambda st: N.load().decode_attn_append_8bit(
-        ctypes.byref(append), _ptr(k_new), _ptr(v_new), _ptr(slot_map), _ptr(k_pool),
-        _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), st))
+    _launch(dev, stream, N.load().decode_attn_append_8bit, ctypes.byref(append),
+            k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), k_pool.data_ptr(),
+            v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def make_scales(k_scale: torch.Tensor, v_scale: torch.Tensor) -> N.DaScales:
@@ -433,10 +444,13 @@ def decode_attn_splitk_8bit(args: N.DaArgs, plan: N.DaPlan, dev: N.DaDev, scales
                             out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """decode_attn_splitk_dev over 8-bit pools with scales (make_paged_args,
     make_dev with a block table, make_scales)."""
-    _on(q.device, "decode_attn_splitk_8bit", k_pool, v_pool, out, workspace)
+    device = q.device
+    if device.type != "cuda":
+        raise TypeError("q must be a CUDA tensor")
+    _on(device, "decode_attn_splitk_8bit", k_pool, v_pool, out, workspace)
     if q.dtype != torch.float32 or not q.is_contiguous() or not out.is_contiguous():
         raise TypeError("q must be contiguous float32 and out contiguous")
-    _launch(q.device, stream, lambda st: N.load().decode_attn_splitk_8bit(
-        ctypes.byref(args), ctypes.byref(plan), ctypes.byref(dev), ctypes.byref(scales), _ptr(q),
-        _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), st))
+    _launch(device, stream, N.load().decode_attn_splitk_8bit, ctypes.byref(args),
+            ctypes.byref(plan), ctypes.byref(dev), ctypes.byref(scales), q.data_ptr(),
+            k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
