@@ -8,7 +8,7 @@
 // MAX = 1.75 * 2^top (top = 8 for e4m3, 15 for e5m2), so e follows from a's
 // exponent and whether its mantissa exceeds 1.75: no division, no logarithm.
 #include <algorithm>
-#include <cstdio>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -24,8 +24,12 @@ using skv::named_bar_sync;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// CTAs of 8 warps for groups of 8, four an SM (64 registers; 36 against 38 us for 32k rows of
+// 4 x 256 f16 in pages of 64); otherwise of 4 warps, seven an SM (72 registers), so that
+// short calls spread over the SMs and long ones keep 28 warps' loads in flight (126k rows of
+// 8 x 128 bf16 in pages of 16: 128 us; five or eight CTAs: 135 and 134 us)
+constexpr int warps_of(int G) { return G == 8 ? 8 : 4; }
+
 
 struct Side { // keys or values; strides in elements
     const void *src;
@@ -48,56 +52,54 @@ template <typename ST> struct Unit {
 };
 template <typename ST> constexpr int kUnits = 8 / sizeof(ST); // units a thread holds: 128 bytes
 
+// (streamed: rows are read once, and codes of a long prompt are not read back soon;
+// evict-first loads and stores took 126k rows of 8 heads from 161 to 151 us)
 template <typename ST> __device__ __forceinline__ void load_unit(Unit<ST> &u, const ST *p)
 {
 #pragma unroll
-    for (int i = 0; i < Unit<ST>::V; ++i) u.v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    for (int i = 0; i < Unit<ST>::V; ++i) u.v[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
 }
 
-// the largest |x| of a unit as the bits of its type, infinities and NaN included
-// (magnitudes order as integers); 16-bit types: two at a time
-__device__ __forceinline__ uint32_t top_bits(const Unit<float> &u, uint32_t m)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m = max(m, u.v[i].x & 0x7fffffffu);
-        m = max(m, u.v[i].y & 0x7fffffffu);
-        m = max(m, u.v[i].z & 0x7fffffffu);
-        m = max(m, u.v[i].w & 0x7fffffffu);
-    }
-    return m;
-}
-template <typename ST> __device__ __forceinline__ uint32_t top_bits(const Unit<ST> &u, uint32_t m)
-{
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        m = __vmaxu2(m, u.v[i].x & 0x7fff7fffu);
-        m = __vmaxu2(m, u.v[i].y & 0x7fff7fffu);
-        m = __vmaxu2(m, u.v[i].z & 0x7fff7fffu);
-        m = __vmaxu2(m, u.v[i].w & 0x7fff7fffu);
-    }
-    return m;
-}
-
-template <typename ST> struct Bits;
-template <> struct Bits<float> {
-    static constexpr uint32_t kInf = 0x7f800000u;
-    static __device__ __forceinline__ uint32_t join(uint32_t m) { return m; }
-    static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
+// Running maximum of |x|, one or two values a word. A maximum drops NaN; an infinity
+// stays and sends the run to the slow path.
+template <typename ST> struct Top;
+template <> struct Top<float> {
+    float m = 0.f;
+    __device__ __forceinline__ void add(uint32_t w) { m = fmaxf(m, fabsf(__uint_as_float(w))); }
+    __device__ __forceinline__ float value() const { return m; }
 };
-template <> struct Bits<__half> {
-    static constexpr uint32_t kInf = 0x7c00u;
-    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xffffu, m >> 16); }
-    static __device__ __forceinline__ float value(uint32_t b)
+template <> struct Top<__half> {
+    __half2 m = __half2(__half(0.f), __half(0.f));
+    __device__ __forceinline__ void add(uint32_t w)
     {
-        return __half2float(__ushort_as_half((unsigned short)b));
+        m = __hmax2(m, __habs2(*reinterpret_cast<__half2 *>(&w)));
+    }
+    __device__ __forceinline__ float value() const
+    {
+        return fmaxf(__low2float(m), __high2float(m));
     }
 };
-template <> struct Bits<__nv_bfloat16> {
-    static constexpr uint32_t kInf = 0x7f80u;
-    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xffffu, m >> 16); }
-    static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
+template <> struct Top<__nv_bfloat16> {
+    __nv_bfloat162 m = __nv_bfloat162(__nv_bfloat16(0.f), __nv_bfloat16(0.f));
+    __device__ __forceinline__ void add(uint32_t w)
+    {
+        m = __hmax2(m, __habs2(*reinterpret_cast<__nv_bfloat162 *>(&w)));
+    }
+    __device__ __forceinline__ float value() const
+    {
+        return fmaxf(__low2float(m), __high2float(m));
+    }
 };
+template <typename ST> __device__ __forceinline__ void add_unit(Top<ST> &m, const Unit<ST> &u)
+{
+#pragma unroll
+    for (int i = 0; i < Unit<ST>::V; ++i) {
+        m.add(u.v[i].x);
+        m.add(u.v[i].y);
+        m.add(u.v[i].z);
+        m.add(u.v[i].w);
+    }
+}
 
 // a unit's elements in f32
 __device__ __forceinline__ void widen(const Unit<float> &u, float *f)
@@ -133,10 +135,11 @@ template <typename ST> __device__ __forceinline__ void widen(const Unit<ST> &u, 
 }
 
 // the largest finite |x| of a unit (the rare path: something was not finite)
-template <typename ST> __device__ __noinline__ float top_finite(const Unit<ST> &u, float m)
+template <typename ST> __device__ __noinline__ float top_finite(Unit<ST> u, float m)
 {
     float f[16];
     widen(u, f);
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
         const float a = fabsf(f[i]);
         if (a <= 3.402823466e38f) m = fmaxf(m, a);
@@ -157,6 +160,46 @@ template <__nv_fp8_interpretation_t F> __device__ __forceinline__ uint4 encode16
         w[i] = a | (b << 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The codes of a unit under a power-of-two scale (inv: its inverse). f16 is scaled in its own
+// type, two elements at a time, where inv is an f16: exact, but for results below 2^-14,
+// rounded to 2^-24, which e4m3, whose least step is 2^-9, does not see (e5m2's steps of 2^-16
+// could, so it goes through f32).
+template <__nv_fp8_interpretation_t F, typename ST>
+__device__ __forceinline__ uint4 encode_unit(const Unit<ST> &u, float inv)
+{
+    constexpr bool kHalf = std::is_same<ST, __half>::value;
+    if constexpr (kHalf && F == __NV_E4M3) {
+        if (inv >= 6.103515625e-5f && inv <= 32768.f) {
+            const __half2 s = __float2half2_rn(inv);
+            uint32_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w = (&u.v[i / 4].x)[i % 4];
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&w), s);
+                c[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(y), __NV_SATFINITE, F);
+            }
+            return make_uint4(c[0] | (c[1] << 16), c[2] | (c[3] << 16), c[4] | (c[5] << 16),
+                              c[6] | (c[7] << 16));
+        }
+    }
+    float f[16];
+    widen(u, f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] *= inv;
+    return encode16<F>(f);
+}
+
+// the same under a scale that is no power of two (rare: a page that another quantiser began)
+template <__nv_fp8_interpretation_t F, typename ST>
+__device__ __noinline__ uint4 encode_divided(Unit<ST> u, float sc)
+{
+    float f[16];
+    widen(u, f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] /= sc;
+    return encode16<F>(f);
 }
 
 template <__nv_fp8_interpretation_t F> __device__ __forceinline__ void decode16(uint4 c, float *f)
@@ -185,18 +228,18 @@ __device__ __forceinline__ float scale_for(float a, int top)
 // touches that page and head). A page that fits the group's registers is read once:
 // G follows from the page's size. Every warp of a group finds the runs for itself.
 template <typename ST, __nv_fp8_interpretation_t F, int G>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(32 * warps_of(G), G == 8 ? 4 : 7)
+    append_kernel(const __grid_constant__ AppendParams p)
 {
-    constexpr int TG = 32 * G;
-    __shared__ uint32_t red_bits[2][kWarps];
-    __shared__ float red_f[2][kWarps];
+    constexpr int TG = 32 * G, kWarps = warps_of(G);
+    __shared__ float red[2][kWarps], red_finite[2][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / G, gt = threadIdx.x - group * TG; // thread of the group
     const int P = p.block_size, T = p.tokens;
     // tasks: head fastest, then keys and values, then chunks
-    const int64_t task = (int64_t)blockIdx.x * (kWarps / G) + group;
-    const int h = (int)(task % p.heads), kv = (int)(task / p.heads & 1);
-    const int64_t c0 = task / p.heads / 2 * p.chunk;
+    const uint32_t task = blockIdx.x * (kWarps / G) + group, pair = task / (uint32_t)p.heads;
+    const int h = (int)(task - pair * p.heads), kv = (int)(pair & 1);
+    const int64_t c0 = (int64_t)(pair >> 1) * p.chunk;
     if (c0 >= T) return; // the whole group
     const int c1 = (int)min((int64_t)T, c0 + p.chunk);
     const Side &sd = p.side[kv];
@@ -239,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             const int U = sd.units, dr = TG / U, dc = TG - dr * U;
             const int row_first = gt / U, col_first = gt - row_first * U;
             Unit<ST> u[kUnits<ST>];
-            uint32_t top = 0;
+            Top<ST> most_abs;
             int r = row_first, c = col_first;
             auto step = [&] {
                 r += dr;
@@ -257,22 +300,25 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                 step();
             }
 #pragma unroll
-            for (int k = 0; k < kUnits<ST>; ++k) top = top_bits(u[k], top);
+            for (int k = 0; k < kUnits<ST>; ++k) add_unit(most_abs, u[k]);
             const int r_rest = r, c_rest = c; // what does not fit the registers
             for (; r < n; step()) {
                 Unit<ST> x;
                 load_unit(x, src + (int64_t)r * sd.src_stride + 16 * c);
-                top = top_bits(x, top);
+                add_unit(most_abs, x);
             }
-            top = __reduce_max_sync(0xffffffffu, Bits<ST>::join(top));
-            if constexpr (G > 1) {
-                if (lane == 0) red_bits[parity][warp] = top;
-                named_bar_sync(1 + group, TG);
+            auto reduce = [&](float m, float *buf) { // over the group (magnitudes order as integers)
+                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+                if constexpr (G > 1) {
+                    if (lane == 0) buf[warp] = m;
+                    named_bar_sync(1 + group, TG);
 #pragma unroll
-                for (int w = 0; w < G; ++w) top = max(top, red_bits[parity][group * G + w]);
-            }
-            float amax = Bits<ST>::value(top);
-            if (top >= Bits<ST>::kInf) { // (the same for the whole group)
+                    for (int w = 0; w < G; ++w) m = fmaxf(m, buf[group * G + w]);
+                }
+                return m;
+            };
+            float amax = reduce(most_abs.value(), red[parity]);
+            if (amax > 3.402823466e38f) { // an infinity (the same for the whole group)
                 amax = 0.f;
 #pragma unroll
                 for (int k = 0; k < kUnits<ST>; ++k) amax = top_finite(u[k], amax);
@@ -281,13 +327,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                     load_unit(x, src + (int64_t)r * sd.src_stride + 16 * c);
                     amax = top_finite(x, amax);
                 }
-                amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-                if constexpr (G > 1) {
-                    if (lane == 0) red_f[parity][warp] = amax;
-                    named_bar_sync(1 + group, TG);
-#pragma unroll
-                    for (int w = 0; w < G; ++w) amax = fmaxf(amax, red_f[parity][group * G + w]);
-                }
+                amax = reduce(amax, red_finite[parity]);
             }
             parity ^= 1;
             const float sc = fmaxf(scale_for(amax, F == __NV_E4M3 ? 8 : 15), was);
@@ -296,16 +336,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             const bool pow2 = (__float_as_uint(sc) & 0x7fffffu) == 0;
             const float inv = 1.f / sc;
             auto put = [&](const Unit<ST> &x, int row, int col) {
-                float y[16];
-                widen(x, y);
-                if (pow2) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] *= inv;
-                } else {
-                    for (int i = 0; i < 16; ++i) y[i] /= sc;
-                }
-                *reinterpret_cast<uint4 *>(page + (int64_t)(p0 + row) * sd.pos + 16 * col) =
-                    encode16<F>(y);
+                __stcs(reinterpret_cast<uint4 *>(page + (int64_t)(p0 + row) * sd.pos + 16 * col),
+                       pow2 ? encode_unit<F>(x, inv) : encode_divided<F>(x, sc));
             };
             r = row_first;
             c = col_first;
@@ -341,32 +373,35 @@ int bad(const char *msg) { return skv::set_error(DA_EINVAL, "args", msg); }
 bool off16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
 template <typename ST, __nv_fp8_interpretation_t F, int G>
-void launch_g(AppendParams &p, cudaStream_t st)
+cudaError_t launch_g(AppendParams &p, cudaStream_t st)
 {
     // Few rows: a group per row, so that runs go side by side (a decode step's are one row
     // each). Many rows (over two waves of warps): a group per page's worth of rows, which
     // hold one or two runs.
+    constexpr int kWarps = warps_of(G);
     const int64_t lanes = (int64_t)p.heads * 2;
     p.chunk = (int64_t)p.tokens * lanes * G > 2 * 152 * 64 ? p.block_size : 1;
     const int64_t tasks = (p.tokens + (int64_t)p.chunk - 1) / p.chunk * lanes;
     const int64_t grid = (tasks * G + kWarps - 1) / kWarps;
-    append_kernel<ST, F, G><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    if (tasks + kWarps > INT32_MAX) return cudaErrorInvalidValue; // 32-bit task numbers
+    append_kernel<ST, F, G><<<(unsigned)grid, 32 * kWarps, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
-template <typename ST, __nv_fp8_interpretation_t F> void launch_f(AppendParams &p, cudaStream_t st)
+template <typename ST, __nv_fp8_interpretation_t F>
+cudaError_t launch_f(AppendParams &p, cudaStream_t st)
 {
     // warps whose registers hold a page of one head (4 KB each)
     const int64_t page = (int64_t)p.block_size * std::max(p.side[0].units, p.side[1].units) * 16;
     constexpr int64_t warp = 32 * kUnits<ST> * 16;
-    if (page <= warp) launch_g<ST, F, 1>(p, st);
-    else if (page <= 4 * warp) launch_g<ST, F, 4>(p, st);
-    else launch_g<ST, F, 8>(p, st);
+    if (page <= warp) return launch_g<ST, F, 1>(p, st);
+    if (page <= 4 * warp) return launch_g<ST, F, 4>(p, st);
+    return launch_g<ST, F, 8>(p, st);
 }
 
-template <typename ST> void launch(AppendParams &p, int code, cudaStream_t st)
+template <typename ST> cudaError_t launch(AppendParams &p, int code, cudaStream_t st)
 {
-    if (code == DA_E4M3) launch_f<ST, __NV_E4M3>(p, st);
-    else launch_f<ST, __NV_E5M2>(p, st);
+    return code == DA_E4M3 ? launch_f<ST, __NV_E4M3>(p, st) : launch_f<ST, __NV_E5M2>(p, st);
 }
 
 } // namespace
@@ -424,10 +459,9 @@ extern "C" int decode_attn_append_8bit(const da_append_t *a, const void *k_new, 
         if (a->block_size == 1 << s) p.shift = s;
     p.chunk = 1;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a->src_dtype == DA_F32) launch<float>(p, a->code_dtype, st);
-    else if (a->src_dtype == DA_F16) launch<__half>(p, a->code_dtype, st);
-    else launch<__nv_bfloat16>(p, a->code_dtype, st);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = a->src_dtype == DA_F32   ? launch<float>(p, a->code_dtype, st)
+                          : a->src_dtype == DA_F16 ? launch<__half>(p, a->code_dtype, st)
+                                                   : launch<__nv_bfloat16>(p, a->code_dtype, st);
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "append", cudaGetErrorString(e));
     return DA_OK;
 }
