@@ -62,6 +62,8 @@ __device__ __forceinline__ void warp_scan(int64_t &a, int64_t &b)
     }
 }
 
+// PER: consecutive slots a lane takes
+template <int PER>
 __global__ void __launch_bounds__(kThreads) grow_tables_kernel(const TablesParams p)
 {
     __shared__ int64_t sums[2][kThreads / 32];
@@ -130,44 +132,61 @@ __global__ void __launch_bounds__(kThreads) grow_tables_kernel(const TablesParam
     auto taken = [&](int k) {
         return k < gives ? released(gives - 1 - k) : t.free_list[F - 1 - (k - gives)];
     };
-    // Slots: a warp takes 64 consecutive ones, a lane two (a 16-byte store). One search
-    // finds the sequences of the first and the last, and the lanes search between them
-    // only where those differ.
+    // the block of position i * P + off of sequence b; the caller of a block's first
+    // position (a block taken begins with a new token) writes its table entry
+    auto block_of = [&](int b, int i, int off) {
+        int32_t *entry = t.block_table + (size_t)b * t.max_blocks_per_seq + i;
+        if (i < have_s[b]) return *entry;
+        const int blk = taken(need_base[b] + i - have_s[b]);
+        if (off == 0) *entry = blk;
+        return blk;
+    };
+    // Slots: a warp takes 32 * PER consecutive ones, a lane PER of them. One search finds
+    // the sequences of the first and the last, and the lanes search between them only
+    // where those differ.
+    constexpr int SPAN = 32 * PER;
     const int gwarp = blockIdx.x * (kThreads / 32) + warp, warps = gridDim.x * (kThreads / 32);
-    for (int64_t j0 = (int64_t)gwarp * 64; j0 < p.slots; j0 += (int64_t)warps * 64) {
-        const int probe = min((int)(lane ? j0 + 63 : j0), max(adds - 1, 0));
+    for (int64_t j0 = (int64_t)gwarp * SPAN; j0 < p.slots; j0 += (int64_t)warps * SPAN) {
+        const int probe = min((int)(lane ? j0 + SPAN - 1 : j0), max(adds - 1, 0));
         const int at = find(add_base, 0, B - 1, probe);
         const int b0 = __shfl_sync(0xffffffffu, at, 0), b1 = __shfl_sync(0xffffffffu, at, 1);
-        int64_t slot[2];
+        const int64_t j = j0 + PER * lane;
+        int64_t slot[PER];
+        int b = 0, i = 0, off = 0, blk = 0, left = 0; // left: rows of sequence b from here on
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int64_t j = j0 + 2 * lane + e;
+        for (int e = 0; e < PER; ++e) {
+            const int je = (int)j + e;
             slot[e] = -1;
-            if (j < adds) {
-                const int b = b0 == b1 ? b0 : find(add_base, b0, b1, (int)j);
-                const uint32_t pos = (uint32_t)(len_s[b] + ((int)j - add_base[b]));
-                const int i = (int)(p.shift >= 0 ? pos >> p.shift : pos / (uint32_t)P);
-                const int blk = i < have_s[b]
-                                    ? t.block_table[(size_t)b * t.max_blocks_per_seq + i]
-                                    : taken(need_base[b] + i - have_s[b]);
-                slot[e] = (int64_t)blk * P + (pos - (uint32_t)i * (uint32_t)P);
+            if (je < adds) {
+                if (left == 0) { // the first one, or the next sequence that has rows
+                    b = b0 == b1 ? b0 : find(add_base, e ? b : b0, b1, je);
+                    left = (b + 1 < B ? add_base[b + 1] : adds) - je;
+                    const uint32_t pos = (uint32_t)(len_s[b] + (je - add_base[b]));
+                    i = (int)(p.shift >= 0 ? pos >> p.shift : pos / (uint32_t)P);
+                    off = (int)(pos - (uint32_t)i * (uint32_t)P);
+                    blk = block_of(b, i, off);
+                } else if (off == P) {
+                    off = 0;
+                    blk = block_of(b, ++i, 0);
+                }
+                slot[e] = (int64_t)blk * P + off;
+                ++off;
+                --left;
             }
         }
-        const int64_t j = j0 + 2 * lane;
-        if (p.wide && j + 1 < p.slots) {
-            *reinterpret_cast<longlong2 *>(p.slot_map + j) = make_longlong2(slot[0], slot[1]);
+        if (PER > 1 && p.wide && j + PER <= p.slots) {
+#pragma unroll
+            for (int e = 0; e + 1 < PER; e += 2)
+                *reinterpret_cast<longlong2 *>(p.slot_map + j + e) =
+                    make_longlong2(slot[e], slot[e + 1]);
         } else {
-            if (j < p.slots) p.slot_map[j] = slot[0];
-            if (j + 1 < p.slots) p.slot_map[j + 1] = slot[1];
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (j + e < p.slots) p.slot_map[j + e] = slot[e];
         }
     }
-    // table entries of the blocks taken; released blocks that nobody took
+    // released blocks that nobody took
     const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
-#pragma unroll 4
-    for (int k = first; k < takes; k += stride) {
-        const int b = find(need_base, 0, B - 1, k);
-        t.block_table[(size_t)b * t.max_blocks_per_seq + have_s[b] + k - need_base[b]] = taken(k);
-    }
 #pragma unroll 4
     for (int k = first; k < gives - takes; k += stride) t.free_list[F + k] = released(k);
 
@@ -224,12 +243,17 @@ extern "C" int decode_attn_grow_tables(const da_tables_t *t, const int32_t *new_
     for (int s = 0; s < 31; ++s)
         if (t->block_size == 1 << s) p.shift = s;
     p.wide = reinterpret_cast<uintptr_t>(slot_map) % 16 == 0;
-    // CTAs for the most that the call may have to write: the slots, 512 a CTA, or the
-    // tables' entries (blocks taken or released), 1024 a CTA; at most four an SM
-    const int64_t most = std::max(slot_capacity / 512,
+    // Few slots: one a lane, so that their look-ups go side by side (a decode step's are of
+    // different sequences); many (over one a thread of the GPU): four, which share a look-up
+    // where they lie in one block (2.1M slots of 256 prompts: 9.1 us; one a lane 11.1). CTAs for the most that the call may have to write: the
+    // slots, or the free list's entries of released blocks, 1024 a CTA; at most four an SM.
+    const int per = slot_capacity > 152 * 4 * kThreads ? 4 : 1;
+    const int64_t most = std::max(slot_capacity / (per * kThreads),
                                   (int64_t)t->batch * t->max_blocks_per_seq / 1024);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(152 * 4, most));
-    grow_tables_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (per == 4) grow_tables_kernel<4><<<grid, kThreads, 0, st>>>(p);
+    else grow_tables_kernel<1><<<grid, kThreads, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "tables", cudaGetErrorString(e));
     return DA_OK;

@@ -66,6 +66,24 @@ def test_random_loads(batch, num_blocks, width, page, capacity, most):
     assert len(ref.free) == num_blocks and sorted(ref.free) == list(range(num_blocks))
 
 
+@pytest.mark.parametrize("page", [16, 3])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_prompts_of_a_full_batch(page, shift):
+    # over 155,648 slots a lane takes several; with an odd start they are stored one by one
+    rng = random.Random(page)
+    ref, dev = Blocks(256, 100000, 700, page), Device(256, 100000, 700, page, 200001)
+    room = torch.full((200004,), 77, dtype=torch.int64, device="cuda")
+    dev.slots = room[shift:shift + 200001]
+    for step in range(3):
+        new = [rng.choice([0, 1, 2, rng.randint(0, 700), rng.randint(400, 2000)]) for _ in range(256)]
+        if step == 1:
+            new = [-1 if b % 3 == 0 else 1 for b in range(256)]
+        status, slots, cu = ref.grow(new, 200001)
+        dev.grow(new)
+        dev.check(ref, slots, cu, status)
+    assert room[200001 + shift:].eq(77).all() and room[:shift].eq(77).all()
+
+
 def test_the_first_failure_is_kept_and_nothing_changes():
     ref, dev = Blocks(3, 4, 8, 16), Device(3, 4, 8, 16, 200)
     status, slots, cu = ref.grow([20, 5, 0], 200)
