@@ -4,7 +4,7 @@
 // stand for code * scale[i][head]. With page scales ks, vs (lv = log2 vs) and
 // scores in log2 units,
 //     s[r][pos]  = ks[page] * sum_d q[r][d] Kc[pos][d]        (q times scale * log2 e)
-//     x[r][pos]  = 2^(s + lv[page] - m[r])
+//     x[r][pos]  = 2^(s - m[r]) * vs[page],  m[r] about the largest s + lv
 //     acc[r][d]  = sum_pos x[r][pos] Vc[pos][d],   l[r] = sum_pos 2^(s - m[r])
 // so the value scales fold into the exponent and the codes go to the tensor cores
 // as they stand: TMA brings 128-position tiles of K and of V into shared memory
@@ -84,10 +84,12 @@ template <int D, int RP> struct Layout {
     static constexpr int P_OFF = Q_OFF + NCH * QCH;
     static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
     // after the slots: barriers, flags, page scales (2 batches of 4 tiles of 8 groups of
-    // 16 positions), per-row tables, warp maxima, columns with a NaN
+    // 16 positions), per-row tables (of two items), rescale factors, warp maxima, columns
+    // with a NaN (of two items)
     static constexpr int BAR = 0, MISC = BAR + B_N * 8, SC = (MISC + 16 + 15) / 16 * 16,
-                         ROW = SC + 2 * 4 * 8 * 8, RED = ROW + 4 * RP * 4, NANC = RED + 4 * RP * 4,
-                         TAIL = NANC + D * 4;
+                         ROW = SC + 2 * 4 * 8 * 16, ALPHA = ROW + 2 * 3 * RP * 4,
+                         RED = ALPHA + RP * 4, NANC = RED + 4 * RP * 4,
+                         TAIL = NANC + 2 * D * 4;
     static constexpr int SLOTS_FIT = (232448 - 1024 - SLOT_OFF - TAIL) / SLOT;
     // even: K tiles then use the even slots and V tiles the odd ones, so the two producers
     // never wait for each other's slots (a barrier's parity tells one phase back, not two)
@@ -230,13 +232,13 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(tail + L::BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + L::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + L::MISC + 4);
-    float2 *sc_sm = reinterpret_cast<float2 *>(tail + L::SC); // (ks, log2 vs) of 16 positions
-    float *qf_sm = reinterpret_cast<float *>(tail + L::ROW);  // per row: 1 / (q's scaling)
-    float *alpha_sm = qf_sm + RP;                             // rescale factor
-    int *lim_sm = reinterpret_cast<int *>(alpha_sm + RP);     // positions seen: below lim
-    int *wrow_sm = lim_sm + RP;                               // workspace row
+    float4 *sc_sm = reinterpret_cast<float4 *>(tail + L::SC); // (ks, log2 vs, vs) of 16 positions
+    // per row, of items in turn: 1 / (q's scaling), positions seen (below lim), workspace row
+    float *const qf2 = reinterpret_cast<float *>(tail + L::ROW);
+    int *const lim2 = reinterpret_cast<int *>(qf2 + 2 * RP), *const wrow2 = lim2 + 2 * RP;
+    float *alpha_sm = reinterpret_cast<float *>(tail + L::ALPHA); // rescale factor of a row
     float *red_sm = reinterpret_cast<float *>(tail + L::RED); // [4 W warps][RPW]
-    int *nan_sm = reinterpret_cast<int *>(tail + L::NANC);    // [D] first token that sees a NaN
+    int *const nan2 = reinterpret_cast<int *>(tail + L::NANC); // first token that sees a NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ItemTable &it = p.items;
     volatile int never = 0;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         Walk8 w;
         w.start(p);
         for (int batch = 0; !w.done; ++batch) {
-            float2 v = make_float2(0.f, 0.f);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             int b = -1, kvh = 0, pos = 0;
             for (int i = 0; i < 4 && !w.done; ++i, w.next(p))
                 if ((lane >> 3) == i && w.t0 + 16 * g < w.t1) {
@@ -370,7 +372,8 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     v.x = __ldg(sc.k + blk * sc.k_block + kvh * sc.k_head);
                     vs = __ldg(sc.v + blk * sc.v_block + kvh * sc.v_head);
                 }
-                v.y = __log2f(fmaxf(vs, kMinScale));
+                v.z = fmaxf(vs, kMinScale);
+                v.y = __log2f(v.z);
             }
             const int half = batch & 1;
             const bool got = mbar_wait_bounded(bar + B_SCFREE + half, ((fph >> half) & 1u) ^ 1u,
@@ -476,55 +479,73 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         const int per = (rows + it.row_groups - 1) / it.row_groups;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + r00;
         const bool causal = p.q_len > 1 && !(p.flags & DA_FLAG_NO_CAUSAL);
-        uint32_t sph = 0, pfp = 0, iph = 0, oph = 0, scp = 0; // iph: per item
+        uint32_t sph = 0, pfp = 0, iph = 0, scp = 0; // iph: item parity
         bool ab = false;
-        int items = 0, gt = 0;
+        int gt = 0;
         int vslot = 1;
         uint32_t vph = 0;
-        for (int item = blockIdx.x; !ab && item < it.n_items; item += gridDim.x) {
-            int b, kvh, s, rg;
-            decode_item(it, item, b, kvh, s, rg);
-            const int Lb = len8(p, b);
-            const int p0 = s * it.chunk[b], p1 = min(Lb, p0 + it.chunk[b]);
-            const int row0 = rg * per, R = min(per, rows - row0);
-            const size_t wbase = ((size_t)it.split_base[b] + s) * p.n_heads + (size_t)kvh * Gh;
-            if (p1 <= p0) { // an empty item: a neutral partial, no MMA took part
-                if (wg == 0 && tid < R) {
-                    const int tok = (row0 + tid) / Gh;
-                    p.ml[wbase + tok * p.hq + (row0 + tid - tok * Gh)] = make_float2(kNeutralM, 0.f);
-                }
-                continue;
-            }
-            // ---- q of this item's rows, once the previous item's QK is done with Q and every
-            // warp with its row tables
-            if (items > 0) {
-                bool okw =
-                    mbar_wait_bounded(bar + B_QFREE, iph ^ 1u, p.timeout_ns, abort_flag);
-                okw = okw &&
-                      mbar_wait_bounded(bar + B_OFREE, iph ^ 1u, p.timeout_ns, abort_flag);
-                if (bar_or(!okw)) {
-                    ab = true;
-                    break;
+        struct Item {
+            int item, b, kvh, Lb, p0, p1, row0, R;
+            size_t wbase;
+        };
+        // the CTA's next item from `item` on that has positions; the ones without get neutral
+        // partials (no MMA takes part in them)
+        auto seek = [&](int item) {
+            Item x;
+            for (; item < it.n_items; item += gridDim.x) {
+                int s, rg;
+                decode_item(it, item, x.b, x.kvh, s, rg);
+                x.Lb = len8(p, x.b);
+                x.p0 = s * it.chunk[x.b];
+                x.p1 = min(x.Lb, x.p0 + it.chunk[x.b]);
+                x.row0 = rg * per;
+                x.R = min(per, rows - x.row0);
+                x.wbase = ((size_t)it.split_base[x.b] + s) * p.n_heads + (size_t)x.kvh * Gh;
+                if (x.p1 > x.p0) break;
+                if (wg == 0 && tid < x.R) {
+                    const int tok = (x.row0 + tid) / Gh;
+                    p.ml[x.wbase + tok * p.hq + (x.row0 + tid - tok * Gh)] =
+                        make_float2(kNeutralM, 0.f);
                 }
             }
-            // the warps take rows in turn: scaled to [128, 256), cut into terms; a lane has
-            // 4 columns of every chunk
-            for (int r = warp; r < RP; r += 4 * W) {
-                float4 x[NCH];
-                float a = 0.f;
-                const int tok = (row0 + r) / Gh, g = row0 + r - tok * Gh;
-                const float *qr =
-                    p.q + ((size_t)(b * p.q_len + tok) * p.hq + (size_t)kvh * Gh + g) * D + 4 * lane;
+            x.item = item;
+            return x;
+        };
+        // q of an item: the warps take rows in turn (QR each), a lane has 4 columns of every
+        // chunk. get_q loads it, put_q writes it to shared memory, scaled to [128, 256) and
+        // cut into terms, and the row tables (buffer `buf`), then arrives on QFULL.
+        constexpr int QR = (RP + 4 * W - 1) / (4 * W);
+        float4 qv[QR][NCH];
+        auto get_q = [&](const Item &x) {
+#pragma unroll
+            for (int i = 0; i < QR; ++i) {
+                const int r = warp + 4 * W * i;
+                const int tok = (x.row0 + r) / Gh, g = x.row0 + r - tok * Gh;
+                const float *qr = p.q +
+                                  ((size_t)(x.b * p.q_len + tok) * p.hq + (size_t)x.kvh * Gh + g) * D +
+                                  4 * lane;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
-                    x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (r < R) x[c] = __ldg(reinterpret_cast<const float4 *>(qr + 128 * c));
-                    x[c].x *= p.scale_log2;
-                    x[c].y *= p.scale_log2;
-                    x[c].z *= p.scale_log2;
-                    x[c].w *= p.scale_log2;
-                    a = fmaxf(a, fmaxf(fmaxf(fabsf(x[c].x), fabsf(x[c].y)),
-                                       fmaxf(fabsf(x[c].z), fabsf(x[c].w))));
+                    qv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < x.R) qv[i][c] = __ldg(reinterpret_cast<const float4 *>(qr + 128 * c));
+                }
+            }
+        };
+        auto put_q = [&](const Item &x, int buf) {
+#pragma unroll
+            for (int i = 0; i < QR; ++i) {
+                const int r = warp + 4 * W * i;
+                float4 (&v)[NCH] = qv[i];
+                float a = 0.f;
+                const int tok = (x.row0 + r) / Gh, g = x.row0 + r - tok * Gh;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    v[c].x *= p.scale_log2;
+                    v[c].y *= p.scale_log2;
+                    v[c].z *= p.scale_log2;
+                    v[c].w *= p.scale_log2;
+                    a = fmaxf(a, fmaxf(fmaxf(fabsf(v[c].x), fabsf(v[c].y)),
+                                       fmaxf(fabsf(v[c].z), fabsf(v[c].w))));
                 }
                 a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
                 // 2^k with a * 2^k in [128, 256); k within what 2^k and 2^-k can be
@@ -532,15 +553,16 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 k = a > 0.f ? max(-120, min(120, k)) : 0;
                 const float f = __uint_as_float((uint32_t)(127 + k) << 23);
                 if (lane == 0) {
-                    qf_sm[r] = __uint_as_float((uint32_t)(127 - k) << 23);
-                    lim_sm[r] = r >= R ? 0 : causal ? Lb - p.q_len + 1 + tok : INT_MAX;
-                    wrow_sm[r] = r < R ? tok * p.hq + g : 0;
+                    qf2[buf * RP + r] = __uint_as_float((uint32_t)(127 - k) << 23);
+                    lim2[buf * RP + r] =
+                        r >= x.R ? 0 : causal ? x.Lb - p.q_len + 1 + tok : INT_MAX;
+                    wrow2[buf * RP + r] = r < x.R ? tok * p.hq + g : 0;
                 }
                 // an infinite q makes NaN scores, as infinities weighted against each other do
                 const bool nan = !(a <= 3.402823466e38f);
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
-                    float y0 = x[c].x * f, y1 = x[c].y * f, y2 = x[c].z * f, y3 = x[c].w * f;
+                    float y0 = v[c].x * f, y1 = v[c].y * f, y2 = v[c].z * f, y3 = v[c].w * f;
                     if (nan) y0 = __int_as_float(0x7fffffff);
 #pragma unroll
                     for (int j = 0; j < kTerms; ++j) {
@@ -551,10 +573,24 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
             }
             if (causal)
-                for (int i = threadIdx.x; i < D; i += 128 * W) nan_sm[i] = INT_MAX;
+                for (int i = threadIdx.x; i < D; i += 128 * W) nan2[buf * D + i] = INT_MAX;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_QFULL);
+        };
+        // narrow items have the registers to load the next item's q a tile ahead
+        constexpr bool kAhead = RP <= 8;
+        Item cur = seek(blockIdx.x);
+        if (cur.item < it.n_items) {
+            get_q(cur);
+            put_q(cur, 0);
+        }
+        for (int n = 0; !ab && cur.item < it.n_items; ++n) {
+            const int Lb = cur.Lb, p0 = cur.p0, p1 = cur.p1, row0 = cur.row0, R = cur.R;
+            const size_t wbase = cur.wbase;
+            const float *qf_sm = qf2 + iph * RP;
+            const int *lim_sm = lim2 + iph * RP, *wrow_sm = wrow2 + iph * RP;
+            int *nan_sm = nan2 + iph * D;
             { // the other warps' row tables
                 const bool okw = mbar_wait_bounded(bar + B_QFULL, iph, p.timeout_ns, abort_flag);
                 if (bar_or(!okw)) {
@@ -562,9 +598,9 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     break;
                 }
             }
-            iph ^= 1u;
-            ++items;
 
+            const Item nxt = seek(cur.item + gridDim.x);
+            const bool more = nxt.item < it.n_items;
             // ---- tiles
             float m[RPW], l[RPW]; // reference (uniform over the threads), this thread's share of l
 #pragma unroll
@@ -576,6 +612,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             bool firsttile = true;
             for (int t0 = p0, t1; t0 < p1; t0 = t1, ++gt, firsttile = false) {
                 t1 = tile_end<T>(t0, p1);
+                if (kAhead && more && t1 >= p1) get_q(nxt);
                 const int ss = gt & 1, half = (gt >> 2) & 1;
                 bool okw = true;
                 if ((gt & 3) == 0) {
@@ -595,7 +632,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     okw = okw && mbar_wait_bounded(bar + B_FULL + vslot, vph, p.timeout_ns,
                                                    abort_flag);
                 tc_fence_after();
-                const float2 sv = sc_sm[half * 32 + (gt & 3) * 8 + (tid >> 4)];
+                const float4 sv = sc_sm[half * 32 + (gt & 3) * 8 + (tid >> 4)];
                 const int pos = t0 + tid;
                 if (okw && fix_v) {
                     const uint32_t vt = sb + L::SLOT_OFF + vslot * L::SLOT + tid * 128;
@@ -684,19 +721,32 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     }
                     if (!firsttile) {
                         tc_fence_after();
+                        float al[RPW];
+#pragma unroll
+                        for (int r = 0; r < RPW; ++r) al[r] = alpha_sm[r00 + r];
+                        // the columns of two terms at a time: one round trip for each
                         for (int j = 0; j < NCH; ++j)
 #pragma unroll
-                            for (int k = 0; k < kTerms; ++k)
+                            for (int k = 0; k < kTerms; k += 2) {
+                                float o[2][RPW];
+                                const uint32_t at = tl + 2 * N + j * N + k * RP;
 #pragma unroll
                                 for (int r0 = 0; r0 < RPW; r0 += RC) {
-                                    float o[RC];
-                                    const uint32_t at = tl + 2 * N + j * N + k * RP + r0;
-                                    tmem_ld<RC>(at, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int i = 0; i < RC; ++i) o[i] *= alpha_sm[r00 + r0 + i];
-                                    tmem_st4(at, o);
+                                    tmem_ld<RC>(at + r0, o[0] + r0);
+                                    tmem_ld<RC>(at + RP + r0, o[1] + r0);
                                 }
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int r = 0; r < RPW; ++r) {
+                                    o[0][r] *= al[r];
+                                    o[1][r] *= al[r];
+                                }
+#pragma unroll
+                                for (int r0 = 0; r0 < RPW; r0 += RC) {
+                                    tmem_st4(at + r0, o[0] + r0);
+                                    tmem_st4(at + RP + r0, o[1] + r0);
+                                }
+                            }
                         tmem_wait_st();
                     }
                     named_bar_sync(1 + wg, 128); // the factors and maxima are read before they change
@@ -707,8 +757,9 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
 #pragma unroll
                 for (int r = 0; r < RPW; ++r) {
                     const float m0 = m[r] == -INFINITY ? 0.f : m[r];
-                    l[r] += ex2(x[r] - m0);
-                    y[r] = ex2(x[r] + sv.y - m0);
+                    y[r] = ex2(x[r] - m0);
+                    l[r] += y[r];
+                    y[r] *= sv.z;
                 }
 #pragma unroll
                 for (int j = 0; j < kTerms; ++j) {
@@ -739,7 +790,6 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
             }
             if (ab) break;
-            // ------------------------------- epilogue -------------------------------
             // l over the threads: lanes by a transposing reduce, then the four warps
             tr_reduce<RPW, 16>(l, lane);
             if (tr_writer<RPW, 16>(lane)) {
@@ -751,12 +801,26 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
 #pragma unroll
             for (int r = 0; r < RPW; ++r)
                 if (tid == r) mr = m[r];
-            const bool okw = mbar_wait_bounded(bar + B_OREADY, oph, p.timeout_ns, abort_flag);
+            // ---- q of the next item, while the last value MMA runs: once the last QK is done
+            // with Q, and every warp with the row tables of the item before this one
+            if (more) {
+                if (!kAhead) get_q(nxt);
+                bool okw = mbar_wait_bounded(bar + B_QFREE, iph, p.timeout_ns, abort_flag);
+                if (n > 0)
+                    okw = okw &&
+                          mbar_wait_bounded(bar + B_OFREE, iph ^ 1u, p.timeout_ns, abort_flag);
+                if (bar_or(!okw)) {
+                    ab = true;
+                    break;
+                }
+                put_q(nxt, iph ^ 1);
+            }
+            // ------------------------------- epilogue -------------------------------
+            const bool okw = mbar_wait_bounded(bar + B_OREADY, iph, p.timeout_ns, abort_flag);
             if (bar_or(!okw)) {
                 ab = true;
                 break;
             }
-            oph ^= 1u;
             tc_fence_after();
             for (int j = 0; j < NCH; ++j) {
                 const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
@@ -792,6 +856,8 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             tc_fence_before();
             named_bar_sync(1 + wg, 128); // the sums are read before they change
             if (lane == 0) mbar_arrive(bar + B_OFREE);
+            cur = nxt;
+            iph ^= 1u;
         }
         if (ab && tid == 0 && !*abort_flag) {
             *abort_flag = 1;
