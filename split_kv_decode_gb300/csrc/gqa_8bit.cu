@@ -84,11 +84,12 @@ template <int D, int RP> struct Layout {
     static constexpr int P_OFF = Q_OFF + NCH * QCH;
     static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
     // after the slots: barriers, flags, page scales (2 batches of 4 tiles of 8 groups of
-    // 16 positions), per-row tables (of two items), rescale factors, warp maxima, columns
+    // 16 positions), per-row tables (of two items), warp maxima and sums, flags, columns
     // with a NaN (of two items)
     static constexpr int BAR = 0, MISC = BAR + B_N * 8, SC = (MISC + 16 + 15) / 16 * 16,
-                         ROW = SC + 2 * 4 * 8 * 16, ALPHA = ROW + 2 * 3 * RP * 4,
-                         RED = ALPHA + RP * 4, NANC = RED + 4 * RP * 4,
+                         ROW = SC + 2 * 4 * 8 * 16,
+                         RED = ROW + 2 * 3 * RP * 4, SUM = RED + 4 * RP * 4,
+                         BAD = SUM + 4 * RP * 4, NANC = BAD + 2 * W * 4,
                          TAIL = NANC + 2 * D * 4;
     static constexpr int SLOTS_FIT = (232448 - 1024 - SLOT_OFF - TAIL) / SLOT;
     // even: K tiles then use the even slots and V tiles the odd ones, so the two producers
@@ -236,8 +237,9 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
     // per row, of items in turn: 1 / (q's scaling), positions seen (below lim), workspace row
     float *const qf2 = reinterpret_cast<float *>(tail + L::ROW);
     int *const lim2 = reinterpret_cast<int *>(qf2 + 2 * RP), *const wrow2 = lim2 + 2 * RP;
-    float *alpha_sm = reinterpret_cast<float *>(tail + L::ALPHA); // rescale factor of a row
-    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // [4 W warps][RPW]
+    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // maxima, [4 W warps][RPW]
+    float *sum_sm = reinterpret_cast<float *>(tail + L::SUM); // l, the same
+    volatile int *bad_sm = reinterpret_cast<volatile int *>(tail + L::BAD); // [W][tile parity]
     int *const nan2 = reinterpret_cast<int *>(tail + L::NANC); // first token that sees a NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ItemTable &it = p.items;
@@ -264,6 +266,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         mbar_init(bar + B_QKDRAIN, 1);
         mbar_init(bar + B_PVDRAIN, 1);
         *abort_flag = 0;
+        for (int i = 0; i < 2 * W; ++i) bad_sm[i] = 0;
         if (blockIdx.x == 0) *p.status = 0;
         fence_mbar_init();
     }
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         // ====================== softmax and epilogue (warpgroups 0..W-1) ======================
         const int wg = W > 1 ? warp >> 2 : 0, r00 = wg * RPW; // this warpgroup's first row
         const int tid = threadIdx.x & 127; // position of the tile (TMEM lane), value column
-        float *red = red_sm + wg * 4 * RPW;
+        float *red = red_sm + wg * 4 * RPW, *sum = sum_sm + wg * 4 * RPW;
         auto bar_or = [&](bool pred) { return named_bar_or(1 + wg, 128, pred); };
         const int Gh = p.hq / it.n_kv_heads, rows = Gh * p.q_len;
         const int per = (rows + it.row_groups - 1) / it.row_groups;
@@ -484,32 +487,73 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         int gt = 0;
         int vslot = 1;
         uint32_t vph = 0;
+        // The CTA's items in turn; those without positions get neutral partials and are
+        // skipped. Where registers allow, every warp works out 32 items at a time, one a lane
+        // (the look-ups of one item take 1500 cycles, as long as a tile), and reads them by
+        // shuffles.
         struct Item {
-            int item, b, kvh, Lb, p0, p1, row0, R;
-            size_t wbase;
+            int k, b, kvh, Lb, p0, p1, row0, R, slot; // k: number in the CTA, -1 past the last
         };
-        // the CTA's next item from `item` on that has positions; the ones without get neutral
-        // partials (no MMA takes part in them)
-        auto seek = [&](int item) {
+        auto look = [&](int k) { // item k by itself; k = -1 past the last
             Item x;
-            for (; item < it.n_items; item += gridDim.x) {
+            const int64_t item = blockIdx.x + (int64_t)k * gridDim.x;
+            x.k = item < it.n_items ? k : -1;
+            x.b = x.kvh = x.Lb = x.p0 = x.p1 = x.row0 = x.slot = 0;
+            if (x.k >= 0) {
                 int s, rg;
-                decode_item(it, item, x.b, x.kvh, s, rg);
+                decode_item(it, (int)item, x.b, x.kvh, s, rg);
                 x.Lb = len8(p, x.b);
                 x.p0 = s * it.chunk[x.b];
-                x.p1 = min(x.Lb, x.p0 + it.chunk[x.b]);
+                x.p1 = max(x.p0, min(x.Lb, x.p0 + it.chunk[x.b]));
                 x.row0 = rg * per;
-                x.R = min(per, rows - x.row0);
-                x.wbase = ((size_t)it.split_base[x.b] + s) * p.n_heads + (size_t)x.kvh * Gh;
-                if (x.p1 > x.p0) break;
-                if (wg == 0 && tid < x.R) {
-                    const int tok = (x.row0 + tid) / Gh;
-                    p.ml[x.wbase + tok * p.hq + (x.row0 + tid - tok * Gh)] =
-                        make_float2(kNeutralM, 0.f);
+                x.slot = it.split_base[x.b] + s;
+            }
+            x.R = min(per, rows - x.row0);
+            return x;
+        };
+        auto neutral = [&](const Item &x, int r) { // row r of an empty item
+            const int jf = x.row0 + r;
+            p.ml[(size_t)x.slot * p.n_heads + (size_t)x.kvh * Gh + jf / Gh * p.hq + jf % Gh] =
+                make_float2(kNeutralM, 0.f);
+        };
+        constexpr bool kLanes = RP <= 8;
+        int k0 = -32;
+        Item mine; // item k0 + lane
+        auto seek = [&](int k) {
+            Item x;
+            if constexpr (kLanes) {
+                for (;;) {
+                    if (k >= k0 + 32) {
+                        k0 += 32;
+                        mine = look(k0 + lane);
+                        if (mine.k >= 0 && mine.p1 == mine.p0 && warp == 0)
+                            for (int r = 0; r < mine.R; ++r) neutral(mine, r);
+                        __syncwarp();
+                    }
+                    const unsigned live =
+                        __ballot_sync(0xffffffffu, mine.p1 > mine.p0) >> (k - k0);
+                    if (live || __any_sync(0xffffffffu, mine.k < 0)) {
+                        const int i = live ? k - k0 + __ffs(live) - 1 : 0;
+                        x.k = live ? k0 + i : -1;
+                        x.b = __shfl_sync(0xffffffffu, mine.b, i);
+                        x.kvh = __shfl_sync(0xffffffffu, mine.kvh, i);
+                        x.Lb = __shfl_sync(0xffffffffu, mine.Lb, i);
+                        x.p0 = __shfl_sync(0xffffffffu, mine.p0, i);
+                        x.p1 = __shfl_sync(0xffffffffu, mine.p1, i);
+                        x.row0 = __shfl_sync(0xffffffffu, mine.row0, i);
+                        x.slot = __shfl_sync(0xffffffffu, mine.slot, i);
+                        x.R = min(per, rows - x.row0);
+                        return x;
+                    }
+                    k = k0 + 32;
+                }
+            } else {
+                for (;; ++k) {
+                    x = look(k);
+                    if (x.k < 0 || x.p1 > x.p0) return x;
+                    if (wg == 0 && tid < x.R) neutral(x, tid);
                 }
             }
-            x.item = item;
-            return x;
         };
         // q of an item: the warps take rows in turn (QR each), a lane has 4 columns of every
         // chunk. get_q loads it, put_q writes it to shared memory, scaled to [128, 256) and
@@ -580,14 +624,14 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         };
         // narrow items have the registers to load the next item's q a tile ahead
         constexpr bool kAhead = RP <= 8;
-        Item cur = seek(blockIdx.x);
-        if (cur.item < it.n_items) {
+        Item cur = seek(0);
+        if (cur.k >= 0) {
             get_q(cur);
             put_q(cur, 0);
         }
-        for (int n = 0; !ab && cur.item < it.n_items; ++n) {
+        for (int n = 0; !ab && cur.k >= 0; ++n) {
             const int Lb = cur.Lb, p0 = cur.p0, p1 = cur.p1, row0 = cur.row0, R = cur.R;
-            const size_t wbase = cur.wbase;
+            const size_t wbase = (size_t)cur.slot * p.n_heads + (size_t)cur.kvh * Gh;
             const float *qf_sm = qf2 + iph * RP;
             const int *lim_sm = lim2 + iph * RP, *wrow_sm = wrow2 + iph * RP;
             int *nan_sm = nan2 + iph * D;
@@ -599,8 +643,8 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
             }
 
-            const Item nxt = seek(cur.item + gridDim.x);
-            const bool more = nxt.item < it.n_items;
+            const Item nxt = seek(cur.k + 1);
+            const bool more = nxt.k >= 0;
             // ---- tiles
             float m[RPW], l[RPW]; // reference (uniform over the threads), this thread's share of l
 #pragma unroll
@@ -687,11 +731,11 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
 #pragma unroll
                 for (int r = 0; r < RPW; ++r) ex |= x[r] + sv.y > m[r] + kTau;
-                if (bar_or(ex || !okw)) {
-                    if (bar_or(!okw)) { // a wait ran out somewhere: leave together
-                        ab = true;
-                        break;
-                    }
+                // One vote a tile; a wait that ran out joins it through a flag of this tile's
+                // parity (written before the tile's first barrier, read after it, so the
+                // warpgroup leaves together). An item's first tile always sets references.
+                if (!okw) bad_sm[2 * wg + (gt & 1)] = 1;
+                if (firsttile || bar_or(ex || !okw)) {
                     // move the references that scores outgrew; rescale l and O^T
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
@@ -702,28 +746,28 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                             red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
                     }
                     named_bar_sync(1 + wg, 128);
+                    if (bad_sm[2 * wg + (gt & 1)]) {
+                        ab = true;
+                        break;
+                    }
+                    float al[RPW];
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
                         const float tm = fmaxf(fmaxf(red[r], red[RPW + r]),
                                                fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
                         const float mn = tm > m[r] + kTau ? tm - kHead : m[r];
-                        const float al = mn == m[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
-                        if (tid == 0) alpha_sm[r00 + r] = al;
-                        l[r] *= al;
+                        al[r] = mn == m[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
+                        l[r] *= al[r];
                         m[r] = mn;
                     }
-                    if (!firsttile) // PV(t-1) is done with O^T before it is rescaled
+                    if (!firsttile) { // PV(t-1) is done with O^T before it is rescaled
                         okw = mbar_wait_bounded(bar + B_PVDONE, (uint32_t)(gt - 1) & 1u,
                                                 p.timeout_ns, abort_flag);
-                    if (bar_or(!okw)) { // also publishes the factors
-                        ab = true;
-                        break;
-                    }
-                    if (!firsttile) {
+                        if (bar_or(!okw)) {
+                            ab = true;
+                            break;
+                        }
                         tc_fence_after();
-                        float al[RPW];
-#pragma unroll
-                        for (int r = 0; r < RPW; ++r) al[r] = alpha_sm[r00 + r];
                         // the columns of two terms at a time: one round trip for each
                         for (int j = 0; j < NCH; ++j)
 #pragma unroll
@@ -749,7 +793,6 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                             }
                         tmem_wait_st();
                     }
-                    named_bar_sync(1 + wg, 128); // the factors and maxima are read before they change
                 }
                 // weights: l, and the terms of x into the P buffer
                 const uint32_t pt = sb + L::P_OFF + ss * L::PSLOT;
@@ -795,7 +838,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             if (tr_writer<RPW, 16>(lane)) {
 #pragma unroll
                 for (int i = 0; i < tr_out<RPW, 16>(); ++i)
-                    red[(warp & 3) * RPW + tr_base<RPW, 16>(lane) + i] = l[i];
+                    sum[(warp & 3) * RPW + tr_base<RPW, 16>(lane) + i] = l[i];
             }
             float mr = -INFINITY; // m of row `tid`
 #pragma unroll
@@ -847,7 +890,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             }
             if (tid < RPW && r00 + tid < R) {
                 const float lr =
-                    red[tid] + red[RPW + tid] + red[2 * RPW + tid] + red[3 * RPW + tid];
+                    sum[tid] + sum[RPW + tid] + sum[2 * RPW + tid] + sum[3 * RPW + tid];
                 // a NaN score makes the row NaN whatever the other splits hold
                 p.ml[wbase + wrow_sm[r00 + tid]] =
                     isnan(lr) ? make_float2(-kNeutralM, 1.f)
@@ -893,6 +936,7 @@ cudaError_t launch_d(int rows, int grid, cudaStream_t st, const CUtensorMap &km,
     if (rows <= 4) return launch_t<D, 4>(grid, st, km, vm, sc, p, e5m2);
     if (rows <= 8) return launch_t<D, 8>(grid, st, km, vm, sc, p, e5m2);
     if (rows <= 16) return launch_t<D, 16>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 24) return launch_t<D, 24>(grid, st, km, vm, sc, p, e5m2);
     return launch_t<D, 32>(grid, st, km, vm, sc, p, e5m2);
 }
 
