@@ -74,7 +74,7 @@ template <int D, int RP> struct Layout {
                          SCALE = KPROD + 4;
     // weights as [row term][position] (K-major), or for wide items [position][row term]
     // (MN-major, rows of 128 bytes): there a thread stores 8 bytes at a time
-    static constexpr bool PMN = N >= 64;
+    static constexpr bool PMN = N >= 64 || D == 128;
     static constexpr int NCH = D / 128;        // 128-column chunks of a row
     static constexpr int CHUNK = T * 128;      // bytes of a chunk of a tile
     static constexpr int SLOT = NCH * CHUNK;   // a K or V tile
@@ -806,7 +806,10 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
 #pragma unroll
                 for (int j = 0; j < kTerms; ++j) {
-                    if constexpr (L::PMN) {
+                    if constexpr (L::PMN && RPW == 4) {
+                        sts_u32(pt + swz(tid, j * RP + r00),
+                                term2(y[0], y[1]) | (term2(y[2], y[3]) << 16));
+                    } else if constexpr (L::PMN) {
                         const uint32_t a = term2(y[0], y[1]) | (term2(y[2], y[3]) << 16);
                         const uint32_t c = term2(y[4], y[5]) | (term2(y[6], y[7]) << 16);
                         sts_v2(pt + swz(tid, j * RP + r00), a, c);
