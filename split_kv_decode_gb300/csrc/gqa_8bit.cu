@@ -290,16 +290,15 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         if (lane == 0) tma_prefetch_map(map);
         const uint64_t pol = l2_evict_first_policy();
         const int bs = p.block_size, h = p.box_rows, nbox = T / h;
-        // this lane's box of tile w: its block, the first slot in it
+        // this lane's box of tile w: its block as the table has it (not looked at until the tile
+        // is issued, so that the load has a tile's time), the first slot in it
         auto look_up = [&](const Walk8 &w, int &slot0) {
             int blk = p.oob_block;
             if (!w.done && lane < nbox) {
                 const int pos = w.t0 + lane * h, idx = pos / bs;
                 slot0 = pos - idx * bs;
-                if (idx < p.max_blocks) {
+                if (idx < p.max_blocks)
                     blk = __ldg(p.block_table + (size_t)w.b * p.max_blocks + idx);
-                    if (blk < 0 || blk > p.oob_block) blk = p.oob_block;
-                }
             }
             return blk;
         };
@@ -327,6 +326,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 last = (last & ~(1u << slot)) | (ph << slot);
                 uint8_t *dst = sm + L::SLOT_OFF + slot * L::SLOT + lane * h * 128;
                 if (lane == 0) mbar_arrive_expect_tx(bar + B_FULL + slot, L::SLOT);
+                if (blk < 0 || blk > p.oob_block) blk = p.oob_block; // reads as zeros
                 __syncwarp();
                 if (lane < nbox) {
 #pragma unroll
