@@ -56,9 +56,10 @@ constexpr float kMinScale = 7.8886090522101181e-31f; // 2^-100
 // barriers
 constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE = B_SFULL + 2,
               B_PFULL = B_SFREE + 2, B_PFREE = B_PFULL + 2, B_PVDONE = B_PFREE + 2,
-              B_OREADY = B_PVDONE + 1, B_OFREE = B_OREADY + 1, B_QFULL = B_OFREE + 1,
-              B_QFREE = B_QFULL + 1, B_SCFULL = B_QFREE + 1, B_SCFREE = B_SCFULL + 2,
-              B_QKDRAIN = B_SCFREE + 2, B_PVDRAIN = B_QKDRAIN + 1, B_N = B_PVDRAIN + 1;
+              B_OREADY = B_PVDONE + 2, B_OFREE = B_OREADY + 1, B_MFULL = B_OFREE + 1,
+              B_QFULL = B_MFULL + 1, B_QFREE = B_QFULL + 1, B_SCFULL = B_QFREE + 1,
+              B_SCFREE = B_SCFULL + 2, B_QKDRAIN = B_SCFREE + 2, B_PVDRAIN = B_QKDRAIN + 1,
+              B_N = B_PVDRAIN + 1;
 
 // Shape and shared memory of <D, RP>: RP rows an item at most, N = 4 RP columns. A
 // softmax warpgroup takes RPW rows of every tile (8, or 4 when there are no more): a
@@ -66,11 +67,18 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE 
 // rows in one thread took 5200 cycles against 2800.
 template <int D, int RP> struct Layout {
     static constexpr int N = kTerms * RP;
-    static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups
+    static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups a tile
     static constexpr int RPW = RP / W;
-    static constexpr int THREADS = W * 128 + 160;
+    // 5 to 16 rows of 128 columns: two sets of warpgroups take turns, each with its own
+    // references and its own O^T, joined at the item's end. There a tile's waits, vote, terms
+    // and fences add up to 1800 cycles, the memory side's share to 1400 (8 rows, 1.2M
+    // positions: 72 -> 66 us; 4 rows are no faster for it, 256 columns have twice the time,
+    // and more rows have not the registers).
+    static constexpr int X = D == 128 && (RP == 8 || RP == 16) ? 2 : 1;
+    static constexpr int WT = W * X; // softmax warpgroups
+    static constexpr int THREADS = WT * 128 + 160;
     // warps after the softmax warps
-    static constexpr int KPROD = 4 * W, VPROD = KPROD + 1, QK = KPROD + 2, PV = KPROD + 3,
+    static constexpr int KPROD = 4 * WT, VPROD = KPROD + 1, QK = KPROD + 2, PV = KPROD + 3,
                          SCALE = KPROD + 4;
     // weights as [row term][position] (K-major), or for wide items [position][row term]
     // (MN-major, rows of 128 bytes): there a thread stores 8 bytes at a time
@@ -84,12 +92,13 @@ template <int D, int RP> struct Layout {
     static constexpr int P_OFF = Q_OFF + NCH * QCH;
     static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
     // after the slots: barriers, flags, page scales (2 batches of 4 tiles of 8 groups of
-    // 16 positions), per-row tables (of two items), warp maxima and sums, flags, columns
-    // with a NaN (of two items)
+    // 16 positions), per-row tables (of two items), warp maxima, sums and references (of
+    // two items), flags, columns with a NaN (of two items)
     static constexpr int BAR = 0, MISC = BAR + B_N * 8, SC = (MISC + 16 + 15) / 16 * 16,
                          ROW = SC + 2 * 4 * 8 * 16,
-                         RED = ROW + 2 * 3 * RP * 4, SUM = RED + 4 * RP * 4,
-                         BAD = SUM + 4 * RP * 4, NANC = BAD + 2 * W * 4,
+                         RED = ROW + 2 * 3 * RP * 4, SUM = RED + 4 * RP * X * 4,
+                         REF = SUM + 2 * 4 * RP * X * 4, BAD = REF + 2 * RP * X * 4,
+                         NANC = BAD + 2 * WT * 4,
                          TAIL = NANC + 2 * D * 4;
     static constexpr int SLOTS_FIT = (232448 - 1024 - SLOT_OFF - TAIL) / SLOT;
     // even: K tiles then use the even slots and V tiles the odd ones, so the two producers
@@ -98,7 +107,7 @@ template <int D, int RP> struct Layout {
     static constexpr int TAIL_OFF = SLOT_OFF + NS * SLOT;
     static constexpr int BYTES = TAIL_OFF + TAIL + 1024;
     static_assert(NS >= 4 && NS % 2 == 0, "K and V tiles of two steps in flight");
-    static_assert((2 + NCH) * N <= 512, "TMEM columns: two S slots and O^T");
+    static_assert((2 + X * NCH) * N <= 512, "TMEM columns: two S slots and O^T");
     static_assert(QCH % 1024 == 0 && BYTES <= 232448, "swizzle atoms, shared memory");
 };
 
@@ -223,7 +232,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     const int e5m2)
 {
     using L = Layout<D, RP>;
-    constexpr int N = L::N, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW;
+    constexpr int N = L::N, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW, X = L::X, WT = L::WT;
     constexpr int RC = 4; // rows taken from TMEM at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
@@ -237,9 +246,10 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
     // per row, of items in turn: 1 / (q's scaling), positions seen (below lim), workspace row
     float *const qf2 = reinterpret_cast<float *>(tail + L::ROW);
     int *const lim2 = reinterpret_cast<int *>(qf2 + 2 * RP), *const wrow2 = lim2 + 2 * RP;
-    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // maxima, [4 W warps][RPW]
-    float *sum_sm = reinterpret_cast<float *>(tail + L::SUM); // l, the same
-    volatile int *bad_sm = reinterpret_cast<volatile int *>(tail + L::BAD); // [W][tile parity]
+    float *red_sm = reinterpret_cast<float *>(tail + L::RED); // maxima, [4 WT warps][RPW]
+    float *sum_sm = reinterpret_cast<float *>(tail + L::SUM); // l, [2 items][4 WT warps][RPW]
+    float *ref_sm = reinterpret_cast<float *>(tail + L::REF); // m, [2 items][X][RP]
+    volatile int *bad_sm = reinterpret_cast<volatile int *>(tail + L::BAD); // [WT][tile parity]
     int *const nan2 = reinterpret_cast<int *>(tail + L::NANC); // first token that sees a NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ItemTable &it = p.items;
@@ -256,17 +266,18 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             mbar_init(bar + B_PFULL + s, 4 * W);
             mbar_init(bar + B_PFREE + s, 1);
             mbar_init(bar + B_SCFULL + s, 1);
-            mbar_init(bar + B_SCFREE + s, 4 * W);
+            mbar_init(bar + B_SCFREE + s, 4 * WT);
+            mbar_init(bar + B_PVDONE + s, 1);
         }
-        mbar_init(bar + B_PVDONE, 1);
+        mbar_init(bar + B_MFULL, 4 * WT);
         mbar_init(bar + B_OREADY, 1);
-        mbar_init(bar + B_OFREE, 4 * W);
-        mbar_init(bar + B_QFULL, 4 * W);
+        mbar_init(bar + B_OFREE, 4 * WT);
+        mbar_init(bar + B_QFULL, 4 * WT);
         mbar_init(bar + B_QFREE, 1);
         mbar_init(bar + B_QKDRAIN, 1);
         mbar_init(bar + B_PVDRAIN, 1);
         *abort_flag = 0;
-        for (int i = 0; i < 2 * W; ++i) bad_sm[i] = 0;
+        for (int i = 0; i < 2 * WT; ++i) bad_sm[i] = 0;
         if (blockIdx.x == 0) *p.status = 0;
         fence_mbar_init();
     }
@@ -400,6 +411,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             const bool qk = warp == L::QK;
             const uint32_t idesc = idesc_f8(N, !qk, !qk && L::PMN, e5m2);
             uint32_t ph = 0, iph = 0, sph = 0; // phases: tile slot, item, S or P buffer
+            uint32_t begun = 0;                // O^T sets of this item that hold something
             int slot = qk ? 0 : 1, items = 0;  // slots of tile t: K 2t, V 2t + 1 (mod NS)
             bool ok = true;
             Walk8 w;
@@ -445,17 +457,21 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t pd = smem_desc_sw128(sb + L::P_OFF + ss * L::PSLOT, 16, 1024);
+                    const int x = X > 1 ? ss : 0; // the tile's O^T, and whether it has begun
+                    if (w.first) begun = 0;
+                    const uint32_t more = (begun >> x) & 1u;
+                    begun |= 1u << x;
 #pragma unroll
                     for (int j = 0; j < NCH; ++j)
 #pragma unroll
                         for (int k = 0; k < T / 32; ++k)
-                            mma_f8(tmem + 2 * N + j * N,
+                            mma_f8(tmem + 2 * N + (x * NCH + j) * N,
                                    ad + (uint64_t)((j * L::CHUNK + k * 4096) >> 4),
                                    pd + (uint64_t)((k * (L::PMN ? 4096 : 32)) >> 4), idesc,
-                                   (w.first && k == 0) ? 0u : 1u);
+                                   k == 0 ? more : 1u);
                     tc_commit(bar + B_EMPTY + slot);
                     tc_commit(bar + B_PFREE + ss);
-                    tc_commit(bar + B_PVDONE);
+                    tc_commit(bar + B_PVDONE + x);
                     if (w.last()) tc_commit(bar + B_OREADY);
                 }
                 if ((slot += 2) >= NS) {
@@ -473,10 +489,12 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         }
         __syncwarp();
     } else {
-        // ====================== softmax and epilogue (warpgroups 0..W-1) ======================
-        const int wg = W > 1 ? warp >> 2 : 0, r00 = wg * RPW; // this warpgroup's first row
+        // ===================== softmax and epilogue (warpgroups 0..WT-1) =====================
+        const int wg = WT > 1 ? warp >> 2 : 0;
+        const int turn = X > 1 ? wg / W : 0;            // tiles of this parity (X = 2)
+        const int r00 = (W > 1 ? wg % W : 0) * RPW;     // this warpgroup's first row
         const int tid = threadIdx.x & 127; // position of the tile (TMEM lane), value column
-        float *red = red_sm + wg * 4 * RPW, *sum = sum_sm + wg * 4 * RPW;
+        float *red = red_sm + wg * 4 * RPW;
         auto bar_or = [&](bool pred) { return named_bar_or(1 + wg, 128, pred); };
         const int Gh = p.hq / it.n_kv_heads, rows = Gh * p.q_len;
         const int per = (rows + it.row_groups - 1) / it.row_groups;
@@ -558,12 +576,12 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         // q of an item: the warps take rows in turn (QR each), a lane has 4 columns of every
         // chunk. get_q loads it, put_q writes it to shared memory, scaled to [128, 256) and
         // cut into terms, and the row tables (buffer `buf`), then arrives on QFULL.
-        constexpr int QR = (RP + 4 * W - 1) / (4 * W);
+        constexpr int QR = (RP + 4 * WT - 1) / (4 * WT);
         float4 qv[QR][NCH];
         auto get_q = [&](const Item &x) {
 #pragma unroll
             for (int i = 0; i < QR; ++i) {
-                const int r = warp + 4 * W * i;
+                const int r = warp + 4 * WT * i;
                 const int tok = (x.row0 + r) / Gh, g = x.row0 + r - tok * Gh;
                 const float *qr = p.q +
                                   ((size_t)(x.b * p.q_len + tok) * p.hq + (size_t)x.kvh * Gh + g) * D +
@@ -578,7 +596,8 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         auto put_q = [&](const Item &x, int buf) {
 #pragma unroll
             for (int i = 0; i < QR; ++i) {
-                const int r = warp + 4 * W * i;
+                const int r = warp + 4 * WT * i;
+                if (RP % (4 * WT) && r >= RP) break;
                 float4 (&v)[NCH] = qv[i];
                 float a = 0.f;
                 const int tok = (x.row0 + r) / Gh, g = x.row0 + r - tok * Gh;
@@ -617,7 +636,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
             }
             if (causal)
-                for (int i = threadIdx.x; i < D; i += 128 * W) nan2[buf * D + i] = INT_MAX;
+                for (int i = threadIdx.x; i < D; i += 128 * WT) nan2[buf * D + i] = INT_MAX;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_QFULL);
@@ -654,12 +673,20 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             }
             const int lim0 = causal ? Lb - p.q_len + 1 : INT_MAX; // the first token's limit
             bool firsttile = true;
-            for (int t0 = p0, t1; t0 < p1; t0 = t1, ++gt, firsttile = false) {
+            for (int t0 = p0, t1; t0 < p1; t0 = t1, ++gt) {
                 t1 = tile_end<T>(t0, p1);
                 if (kAhead && more && t1 >= p1) get_q(nxt);
                 const int ss = gt & 1, half = (gt >> 2) & 1;
+                if (X > 1 && ss != turn) { // the other set's tile
+                    if ((vslot += 2) >= NS) {
+                        vslot -= NS;
+                        vph ^= 1u;
+                    }
+                    continue;
+                }
+                const int own = X > 1 ? gt >> 1 : gt; // number of this set's tile
                 bool okw = true;
-                if ((gt & 3) == 0) {
+                if ((gt & 3) == turn) {
                     okw = mbar_wait_bounded(bar + B_SCFULL + half, (scp >> half) & 1u, p.timeout_ns,
                                             abort_flag);
                     scp ^= 1u << half;
@@ -671,7 +698,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 sph ^= 1u << ss;
                 pfp ^= 1u << ss;
                 const bool short_tile = t1 - t0 < T, new_tokens = t1 > lim0;
-                const bool fix_v = wg == 0 && (short_tile || new_tokens);
+                const bool fix_v = r00 == 0 && (short_tile || new_tokens);
                 if (fix_v)
                     okw = okw && mbar_wait_bounded(bar + B_FULL + vslot, vph, p.timeout_ns,
                                                    abort_flag);
@@ -734,7 +761,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 // One vote a tile; a wait that ran out joins it through a flag of this tile's
                 // parity (written before the tile's first barrier, read after it, so the
                 // warpgroup leaves together). An item's first tile always sets references.
-                if (!okw) bad_sm[2 * wg + (gt & 1)] = 1;
+                if (!okw) bad_sm[2 * wg + (own & 1)] = 1;
                 if (firsttile || bar_or(ex || !okw)) {
                     // move the references that scores outgrew; rescale l and O^T
 #pragma unroll
@@ -746,7 +773,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                             red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
                     }
                     named_bar_sync(1 + wg, 128);
-                    if (bad_sm[2 * wg + (gt & 1)]) {
+                    if (bad_sm[2 * wg + (own & 1)]) {
                         ab = true;
                         break;
                     }
@@ -760,8 +787,8 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                         l[r] *= al[r];
                         m[r] = mn;
                     }
-                    if (!firsttile) { // PV(t-1) is done with O^T before it is rescaled
-                        okw = mbar_wait_bounded(bar + B_PVDONE, (uint32_t)(gt - 1) & 1u,
+                    if (!firsttile) { // the set's last PV is done with O^T before it is rescaled
+                        okw = mbar_wait_bounded(bar + B_PVDONE + turn, (uint32_t)(own - 1) & 1u,
                                                 p.timeout_ns, abort_flag);
                         if (bar_or(!okw)) {
                             ab = true;
@@ -773,7 +800,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
 #pragma unroll
                             for (int k = 0; k < kTerms; k += 2) {
                                 float o[2][RPW];
-                                const uint32_t at = tl + 2 * N + j * N + k * RP;
+                                const uint32_t at = tl + 2 * N + (turn * NCH + j) * N + k * RP;
 #pragma unroll
                                 for (int r0 = 0; r0 < RPW; r0 += RC) {
                                     tmem_ld<RC>(at + r0, o[0] + r0);
@@ -825,10 +852,11 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
+                firsttile = false;
                 if (lane == 0) {
                     mbar_arrive(bar + B_SFREE + ss);
                     mbar_arrive(bar + B_PFULL + ss);
-                    if ((gt & 3) == 3) mbar_arrive(bar + B_SCFREE + half);
+                    if ((gt & 3) == (X > 1 ? 2 + turn : 3)) mbar_arrive(bar + B_SCFREE + half);
                 }
                 if ((vslot += 2) >= NS) {
                     vslot -= NS;
@@ -836,17 +864,21 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
             }
             if (ab) break;
-            // l over the threads: lanes by a transposing reduce, then the four warps
+            // l over the threads (lanes by a transposing reduce, the warps later) and m, where
+            // the other set and the epilogue find them
+            float *sum = sum_sm + iph * 4 * RP * X, *ref = ref_sm + iph * RP * X;
             tr_reduce<RPW, 16>(l, lane);
             if (tr_writer<RPW, 16>(lane)) {
 #pragma unroll
                 for (int i = 0; i < tr_out<RPW, 16>(); ++i)
-                    sum[(warp & 3) * RPW + tr_base<RPW, 16>(lane) + i] = l[i];
+                    sum[warp * RPW + tr_base<RPW, 16>(lane) + i] = l[i];
             }
-            float mr = -INFINITY; // m of row `tid`
+            if (tid == 0) {
 #pragma unroll
-            for (int r = 0; r < RPW; ++r)
-                if (tid == r) mr = m[r];
+                for (int r = 0; r < RPW; ++r) ref[turn * RP + r00 + r] = m[r];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + B_MFULL);
             // ---- q of the next item, while the last value MMA runs: once the last QK is done
             // with Q, and every warp with the row tables of the item before this one
             if (more) {
@@ -862,27 +894,59 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 put_q(nxt, iph ^ 1);
             }
             // ------------------------------- epilogue -------------------------------
-            const bool okw = mbar_wait_bounded(bar + B_OREADY, iph, p.timeout_ns, abort_flag);
+            bool okw = mbar_wait_bounded(bar + B_MFULL, iph, p.timeout_ns, abort_flag);
+            okw = okw && mbar_wait_bounded(bar + B_OREADY, iph, p.timeout_ns, abort_flag);
             if (bar_or(!okw)) {
                 ab = true;
                 break;
             }
             tc_fence_after();
-            for (int j = 0; j < NCH; ++j) {
-                const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
+            // Row r of this warpgroup: the reference M of both sets, l under it, and the factor of
+            // each set's O^T (0: the set has nothing, and its O^T may hold anything). A set whose
+            // only scores are NaN has no reference, but a NaN in l.
+            auto join = [&](int r, float *f, float &M) {
+                float l2[X], lr = 0.f;
+                M = -INFINITY;
 #pragma unroll
-                for (int r0 = 0; r0 < RPW; r0 += RC) {
-                    float v[kTerms][RC];
+                for (int x = 0; x < X; ++x) {
+                    const float *s4 = sum + (x * W + r00 / RPW) * 4 * RPW + r;
+                    l2[x] = s4[0] + s4[RPW] + s4[2 * RPW] + s4[3 * RPW];
+                    M = fmaxf(M, ref[x * RP + r00 + r]);
+                }
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k)
-                        tmem_ld<RC>(tl + 2 * N + j * N + k * RP + r0, v[k]);
+                for (int x = 0; x < X; ++x) {
+                    const float m1 = ref[x * RP + r00 + r];
+                    f[x] = X == 1 ? 1.f : m1 == -INFINITY ? l2[x] : ex2(m1 - M);
+                    lr = X == 1 ? l2[x] : fmaf(l2[x], f[x], lr);
+                }
+                return lr;
+            };
+            // the sets of warpgroups take the row chunks in turn
+#pragma unroll
+            for (int r0 = 0; r0 < RPW; r0 += RC) {
+                if (X > 1 && (r0 / RC) % X != turn) continue;
+                for (int j = 0; j < NCH; ++j) {
+                    const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
+                    float v[X][kTerms][RC];
+#pragma unroll
+                    for (int x = 0; x < X; ++x)
+#pragma unroll
+                        for (int k = 0; k < kTerms; ++k)
+                            tmem_ld<RC>(tl + 2 * N + (x * NCH + j) * N + k * RP + r0, v[x][k]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < RC; ++i) {
-                        float y = v[kTerms - 1][i];
-#pragma unroll
-                        for (int k = kTerms - 2; k >= 0; --k) y = fmaf(y, kTermStep, v[k][i]);
                         const int r = r00 + r0 + i;
+                        float f[X], M, y = 0.f;
+                        (void)join(r0 + i, f, M);
+#pragma unroll
+                        for (int x = 0; x < X; ++x) {
+                            float o = v[x][kTerms - 1][i];
+#pragma unroll
+                            for (int k = kTerms - 2; k >= 0; --k) o = fmaf(o, kTermStep, v[x][k][i]);
+                            if (X == 1) y = o;
+                            else if (f[x] != 0.f) y = fmaf(o, f[x], y);
+                        }
                         if (r < R) {
                             if (nan_from != INT_MAX && (row0 + r) / Gh >= nan_from)
                                 y = __int_as_float(0x7fffffff);
@@ -891,16 +955,16 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     }
                 }
             }
-            if (tid < RPW && r00 + tid < R) {
-                const float lr =
-                    sum[tid] + sum[RPW + tid] + sum[2 * RPW + tid] + sum[3 * RPW + tid];
+            if (turn == 0 && tid < RPW && r00 + tid < R) {
+                float f[X], M;
+                const float lr = join(tid, f, M);
                 // a NaN score makes the row NaN whatever the other splits hold
                 p.ml[wbase + wrow_sm[r00 + tid]] =
                     isnan(lr) ? make_float2(-kNeutralM, 1.f)
-                              : make_float2(lr > 0.f ? mr * kLn2 : kNeutralM, lr);
+                              : make_float2(lr > 0.f ? M * kLn2 : kNeutralM, lr);
             }
             tc_fence_before();
-            named_bar_sync(1 + wg, 128); // the sums are read before they change
+            __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_OFREE);
             cur = nxt;
             iph ^= 1u;

@@ -458,3 +458,19 @@ def test_a_wait_that_runs_out_is_reported():
             assert e.value.status == N.DA_ETIMEOUT and "8 bits" in e.value.message
     A.decode_attn_device_status(ws)
     check(o.double().cpu().numpy()[:, None], q, cache, lens, 16, "e4m3", 0.1)
+
+
+@pytest.mark.parametrize("rows", [4, 8, 16, 24])
+@pytest.mark.parametrize("where", [(0,), (200,), (5, 140, 300)])
+def test_a_nan_score_makes_the_row_nan(rows, where):
+    # in the first tile, in the second (of the other warpgroups), in all of them; lengths
+    # where a tile holds nothing but a NaN
+    L, d = 301, 128
+    cache = paged_cache(41, [L, 129], 16, 1, d, "e4m3")
+    kp, table = cache[0].view(torch.uint8), cache[4]
+    for pos in where:
+        kp[table[0, pos // 16], pos % 16, 0, 3] = 0x7F
+    kp[table[1, 8], 0, 0, 3] = 0x7F               # position 128: a tile of its own
+    q = queries(42, 2, 1, rows, d)
+    got = call(q, cache, 16, 0.1, plan_lens=[L, 129], splits=1)
+    assert np.all(np.isnan(got))
