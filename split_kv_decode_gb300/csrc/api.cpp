@@ -661,8 +661,8 @@ int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
                          dev->num_blocks, a->v_head_stride, a->v_pos_stride,
                          dev->v_block_stride, p.box_rows, true);
     if (rc) return rc;
-    const cudaError_t e = launch_gqa_8bit(a->kv_dtype, a->head_dim, split_grid(a, pl), st, km, vm,
-                                          s, p);
+    const cudaError_t e = launch_gqa_8bit(a->kv_dtype, a->out_dtype, a->head_dim, split_grid(a, pl),
+                                          st, km, vm, s, p);
     if (e != cudaSuccess) return fail(DA_ELAUNCH, "split", "%s", cudaGetErrorString(e));
     return DA_OK;
 }

@@ -61,12 +61,13 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE 
               B_SCFREE = B_SCFULL + 2, B_QKDRAIN = B_SCFREE + 2, B_PVDRAIN = B_QKDRAIN + 1,
               B_N = B_PVDRAIN + 1;
 
-// Shape and shared memory of <D, RP>: RP rows an item at most, N = 4 RP columns. A
+// Shape and shared memory of <D, RP, PT>: RP rows an item at most, 4 terms of q, PT of x. A
 // softmax warpgroup takes RPW rows of every tile (8, or 4 when there are no more): a
 // thread's share of a tile must not outlast the tile's time on the memory side, and 32
 // rows in one thread took 5200 cycles against 2800.
-template <int D, int RP> struct Layout {
-    static constexpr int N = kTerms * RP;
+template <int D, int RP, int PT> struct Layout {
+    static constexpr int N = kTerms * RP;              // columns of S
+    static constexpr int NP = (PT * RP + 15) / 16 * 16; // columns of O^T
     static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups a tile
     static constexpr int RPW = RP / W;
     // 5 to 16 rows of 128 columns: two sets of warpgroups take turns, each with its own
@@ -87,7 +88,7 @@ template <int D, int RP> struct Layout {
     static constexpr int CHUNK = T * 128;      // bytes of a chunk of a tile
     static constexpr int SLOT = NCH * CHUNK;   // a K or V tile
     static constexpr int QCH = N * 128;        // a chunk of Q
-    static constexpr int PSLOT = PMN ? T * 128 : N * 128; // one P buffer
+    static constexpr int PSLOT = PMN ? T * 128 : NP * 128; // one P buffer
     static constexpr int Q_OFF = 0;
     static constexpr int P_OFF = Q_OFF + NCH * QCH;
     static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
@@ -107,7 +108,7 @@ template <int D, int RP> struct Layout {
     static constexpr int TAIL_OFF = SLOT_OFF + NS * SLOT;
     static constexpr int BYTES = TAIL_OFF + TAIL + 1024;
     static_assert(NS >= 4 && NS % 2 == 0, "K and V tiles of two steps in flight");
-    static_assert((2 + X * NCH) * N <= 512, "TMEM columns: two S slots and O^T");
+    static_assert(2 * N + X * NCH * NP <= 512, "TMEM columns: two S slots and O^T");
     static_assert(QCH % 1024 == 0 && BYTES <= 232448, "swizzle atoms, shared memory");
 };
 
@@ -174,6 +175,19 @@ __device__ __forceinline__ uint32_t term2(float &x, float &y)
     return c;
 }
 
+// The PT terms of two values, x in the low byte of each. What is left after all but two
+// fits an f16 (11 bits for 10), so the last two are taken two values at a time.
+template <int PT> __device__ __forceinline__ void terms(float x, float y, uint32_t *c)
+{
+#pragma unroll
+    for (int j = 0; j < PT - 2; ++j) c[j] = term2(x, y);
+    const __half2 h = __floats2half2_rn(x, y);
+    c[PT - 2] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+    const __half2 f(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[PT - 2], __NV_E4M3));
+    const __half2 rest = __hmul2(__hsub2(h, f), __half2(__half(16.f), __half(16.f)));
+    c[PT - 1] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+}
+
 // the length item items of sequence b attend over: the plan's, or the device's,
 // kept within [0, the plan's]
 __device__ __forceinline__ int len8(const SplitParams &p, int b)
@@ -225,14 +239,14 @@ struct Walk8 {
     }
 };
 
-template <int D, int RP>
-__global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
+template <int D, int RP, int PT>
+__global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
     gqa_8bit_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ Scales8 sc, const __grid_constant__ SplitParams p,
                     const int e5m2)
 {
-    using L = Layout<D, RP>;
-    constexpr int N = L::N, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW, X = L::X, WT = L::WT;
+    using L = Layout<D, RP, PT>;
+    constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW, X = L::X, WT = L::WT;
     constexpr int RC = 4; // rows taken from TMEM at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
@@ -409,7 +423,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
         // Two issuers, so that neither polls for the other's inputs.
         if (lane == 0) {
             const bool qk = warp == L::QK;
-            const uint32_t idesc = idesc_f8(N, !qk, !qk && L::PMN, e5m2);
+            const uint32_t idesc = idesc_f8(qk ? N : NP, !qk, !qk && L::PMN, e5m2);
             uint32_t ph = 0, iph = 0, sph = 0; // phases: tile slot, item, S or P buffer
             uint32_t begun = 0;                // O^T sets of this item that hold something
             int slot = qk ? 0 : 1, items = 0;  // slots of tile t: K 2t, V 2t + 1 (mod NS)
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                     for (int j = 0; j < NCH; ++j)
 #pragma unroll
                         for (int k = 0; k < T / 32; ++k)
-                            mma_f8(tmem + 2 * N + (x * NCH + j) * N,
+                            mma_f8(tmem + 2 * N + (x * NCH + j) * NP,
                                    ad + (uint64_t)((j * L::CHUNK + k * 4096) >> 4),
                                    pd + (uint64_t)((k * (L::PMN ? 4096 : 32)) >> 4), idesc,
                                    k == 0 ? more : 1u);
@@ -668,7 +682,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             float m[RPW], l[RPW]; // reference (uniform over the threads), this thread's share of l
 #pragma unroll
             for (int r = 0; r < RPW; ++r) {
-                m[r] = -INFINITY;
+                m[r] = kNeutralM; // none yet
                 l[r] = 0.f;
             }
             const int lim0 = causal ? Lb - p.q_len + 1 : INT_MAX; // the first token's limit
@@ -731,43 +745,54 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                         }
                     }
                 }
-                // scores of this position, with the value scale in the exponent
-                float x[RPW];
+                // a[r]: this position's score in row r, less the row's reference (`less`), -inf
+                // where it is masked
+                float a[RPW];
+                auto scores = [&](bool less) {
 #pragma unroll
-                for (int r0 = 0; r0 < RPW; r0 += RC) {
-                    float v[kTerms][RC];
+                    for (int r0 = 0; r0 < RPW; r0 += RC) {
+                        float v[kTerms][RC];
 #pragma unroll
-                    for (int j = 0; j < kTerms; ++j) tmem_ld<RC>(tl + ss * N + j * RP + r0, v[j]);
-                    tmem_wait_ld();
+                        for (int j = 0; j < kTerms; ++j)
+                            tmem_ld<RC>(tl + ss * N + j * RP + r0, v[j]);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < RC; ++i) {
-                        float y = v[kTerms - 1][i];
+                        for (int i = 0; i < RC; ++i) {
+                            float y = v[kTerms - 1][i];
 #pragma unroll
-                        for (int j = kTerms - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
-                        x[r0 + i] = y * (qf_sm[r00 + r0 + i] * sv.x);
+                            for (int j = kTerms - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
+                            a[r0 + i] = fmaf(y, qf_sm[r00 + r0 + i] * sv.x, less ? -m[r0 + i] : 0.f);
+                        }
                     }
-                }
-                bool ex = false;
-                if (pos >= t1) {
+                    if (pos >= t1) {
 #pragma unroll
-                    for (int r = 0; r < RPW; ++r) x[r] = -INFINITY;
-                } else if (new_tokens) {
+                        for (int r = 0; r < RPW; ++r) a[r] = -INFINITY;
+                    } else if (new_tokens) {
 #pragma unroll
-                    for (int r = 0; r < RPW; ++r)
-                        if (pos >= lim_sm[r00 + r]) x[r] = -INFINITY;
-                }
-#pragma unroll
-                for (int r = 0; r < RPW; ++r) ex |= x[r] + sv.y > m[r] + kTau;
-                // One vote a tile; a wait that ran out joins it through a flag of this tile's
-                // parity (written before the tile's first barrier, read after it, so the
-                // warpgroup leaves together). An item's first tile always sets references.
+                        for (int r = 0; r < RPW; ++r)
+                            if (pos >= lim_sm[r00 + r]) a[r] = -INFINITY;
+                    }
+                };
+                // One vote a tile, whether a score outgrew its reference; a wait that ran out
+                // joins it through a flag of this tile's parity (written before the tile's first
+                // barrier, read after it, so the warpgroup leaves together). An item's first tile
+                // always sets references.
                 if (!okw) bad_sm[2 * wg + (own & 1)] = 1;
-                if (firsttile || bar_or(ex || !okw)) {
+                bool ex = firsttile;
+                if (!firsttile) {
+                    scores(true);
+                    const float most = kTau - sv.y;
+#pragma unroll
+                    for (int r = 0; r < RPW; ++r) ex |= a[r] > most;
+                    ex = bar_or(ex || !okw);
+                }
+                if (ex) {
                     // move the references that scores outgrew; rescale l and O^T
+                    scores(false);
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
                         // as ordered integers; a NaN counts as -inf
-                        const int u = __float_as_int(fmaxf(x[r] + sv.y, -INFINITY));
+                        const int u = __float_as_int(fmaxf(a[r] + sv.y, -INFINITY));
                         const int o = __reduce_max_sync(0xffffffffu, u ^ ((u >> 31) & 0x7fffffff));
                         if (lane == 0)
                             red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
@@ -783,9 +808,10 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                         const float tm = fmaxf(fmaxf(red[r], red[RPW + r]),
                                                fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
                         const float mn = tm > m[r] + kTau ? tm - kHead : m[r];
-                        al[r] = mn == m[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
+                        al[r] = ex2(m[r] - mn);
                         l[r] *= al[r];
                         m[r] = mn;
+                        a[r] -= mn;
                     }
                     if (!firsttile) { // the set's last PV is done with O^T before it is rescaled
                         okw = mbar_wait_bounded(bar + B_PVDONE + turn, (uint32_t)(own - 1) & 1u,
@@ -798,24 +824,23 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                         // the columns of two terms at a time: one round trip for each
                         for (int j = 0; j < NCH; ++j)
 #pragma unroll
-                            for (int k = 0; k < kTerms; k += 2) {
+                            for (int k = 0; k < PT; k += 2) {
                                 float o[2][RPW];
-                                const uint32_t at = tl + 2 * N + (turn * NCH + j) * N + k * RP;
+                                const uint32_t at = tl + 2 * N + (turn * NCH + j) * NP + k * RP;
+                                const int two = k + 1 < PT ? 2 : 1;
 #pragma unroll
-                                for (int r0 = 0; r0 < RPW; r0 += RC) {
-                                    tmem_ld<RC>(at + r0, o[0] + r0);
-                                    tmem_ld<RC>(at + RP + r0, o[1] + r0);
-                                }
+                                for (int e = 0; e < two; ++e)
+#pragma unroll
+                                    for (int r0 = 0; r0 < RPW; r0 += RC)
+                                        tmem_ld<RC>(at + e * RP + r0, o[e] + r0);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int r = 0; r < RPW; ++r) {
-                                    o[0][r] *= al[r];
-                                    o[1][r] *= al[r];
-                                }
+                                for (int e = 0; e < two; ++e) {
 #pragma unroll
-                                for (int r0 = 0; r0 < RPW; r0 += RC) {
-                                    tmem_st4(at + r0, o[0] + r0);
-                                    tmem_st4(at + RP + r0, o[1] + r0);
+                                    for (int r = 0; r < RPW; ++r) o[e][r] *= al[r];
+#pragma unroll
+                                    for (int r0 = 0; r0 < RPW; r0 += RC)
+                                        tmem_st4(at + e * RP + r0, o[e] + r0);
                                 }
                             }
                         tmem_wait_st();
@@ -823,29 +848,27 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 }
                 // weights: l, and the terms of x into the P buffer
                 const uint32_t pt = sb + L::P_OFF + ss * L::PSLOT;
-                float y[RPW];
 #pragma unroll
                 for (int r = 0; r < RPW; ++r) {
-                    const float m0 = m[r] == -INFINITY ? 0.f : m[r];
-                    y[r] = ex2(x[r] - m0);
-                    l[r] += y[r];
-                    y[r] *= sv.z;
+                    a[r] = ex2(a[r]);
+                    l[r] += a[r];
+                    a[r] *= sv.z;
                 }
+                uint32_t c[RPW / 2][PT]; // codes of two rows
 #pragma unroll
-                for (int j = 0; j < kTerms; ++j) {
+                for (int r = 0; r < RPW; r += 2) terms<PT>(a[r], a[r + 1], c[r / 2]);
+#pragma unroll
+                for (int j = 0; j < PT; ++j) {
+                    const uint32_t at = pt + swz(tid, j * RP + r00);
                     if constexpr (L::PMN && RPW == 4) {
-                        sts_u32(pt + swz(tid, j * RP + r00),
-                                term2(y[0], y[1]) | (term2(y[2], y[3]) << 16));
+                        sts_u32(at, c[0][j] | (c[1][j] << 16));
                     } else if constexpr (L::PMN) {
-                        const uint32_t a = term2(y[0], y[1]) | (term2(y[2], y[3]) << 16);
-                        const uint32_t c = term2(y[4], y[5]) | (term2(y[6], y[7]) << 16);
-                        sts_v2(pt + swz(tid, j * RP + r00), a, c);
+                        sts_v2(at, c[0][j] | (c[1][j] << 16), c[2][j] | (c[3][j] << 16));
                     } else {
 #pragma unroll
                         for (int r = 0; r < RPW; r += 2) {
-                            const uint32_t c = term2(y[r], y[r + 1]);
-                            sts_u8(pt + swz(j * RP + r, tid), c & 0xff);
-                            sts_u8(pt + swz(j * RP + r + 1, tid), c >> 8);
+                            sts_u8(pt + swz(j * RP + r, tid), c[r / 2][j] & 0xff);
+                            sts_u8(pt + swz(j * RP + r + 1, tid), c[r / 2][j] >> 8);
                         }
                     }
                 }
@@ -906,7 +929,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
             // only scores are NaN has no reference, but a NaN in l.
             auto join = [&](int r, float *f, float &M) {
                 float l2[X], lr = 0.f;
-                M = -INFINITY;
+                M = kNeutralM;
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
                     const float *s4 = sum + (x * W + r00 / RPW) * 4 * RPW + r;
@@ -916,7 +939,7 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
                     const float m1 = ref[x * RP + r00 + r];
-                    f[x] = X == 1 ? 1.f : m1 == -INFINITY ? l2[x] : ex2(m1 - M);
+                    f[x] = X == 1 ? 1.f : m1 == kNeutralM ? l2[x] : ex2(m1 - M);
                     lr = X == 1 ? l2[x] : fmaf(l2[x], f[x], lr);
                 }
                 return lr;
@@ -927,12 +950,12 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                 if (X > 1 && (r0 / RC) % X != turn) continue;
                 for (int j = 0; j < NCH; ++j) {
                     const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
-                    float v[X][kTerms][RC];
+                    float v[X][PT][RC];
 #pragma unroll
                     for (int x = 0; x < X; ++x)
 #pragma unroll
-                        for (int k = 0; k < kTerms; ++k)
-                            tmem_ld<RC>(tl + 2 * N + (x * NCH + j) * N + k * RP + r0, v[x][k]);
+                        for (int k = 0; k < PT; ++k)
+                            tmem_ld<RC>(tl + 2 * N + (x * NCH + j) * NP + k * RP + r0, v[x][k]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < RC; ++i) {
@@ -941,9 +964,9 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
                         (void)join(r0 + i, f, M);
 #pragma unroll
                         for (int x = 0; x < X; ++x) {
-                            float o = v[x][kTerms - 1][i];
+                            float o = v[x][PT - 1][i];
 #pragma unroll
-                            for (int k = kTerms - 2; k >= 0; --k) o = fmaf(o, kTermStep, v[x][k][i]);
+                            for (int k = PT - 2; k >= 0; --k) o = fmaf(o, kTermStep, v[x][k][i]);
                             if (X == 1) y = o;
                             else if (f[x] != 0.f) y = fmaf(o, f[x], y);
                         }
@@ -983,28 +1006,36 @@ __global__ void __launch_bounds__((Layout<D, RP>::THREADS), 1)
     if (threadIdx.x == 0) griddep_launch_dependents();
 }
 
-template <int D, int RP>
+template <int D, int RP, int PT>
 cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
                      const Scales8 &sc, const SplitParams &p, int e5m2)
 {
-    auto *fn = gqa_8bit_kernel<D, RP>;
-    constexpr int bytes = Layout<D, RP>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    using L = Layout<D, RP, PT>;
+    auto *fn = gqa_8bit_kernel<D, RP, PT>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
-    fn<<<grid, (Layout<D, RP>::THREADS), bytes, st>>>(km, vm, sc, p, e5m2);
+    fn<<<grid, L::THREADS, L::BYTES, st>>>(km, vm, sc, p, e5m2);
     return cudaGetLastError();
 }
 
+// The narrowest instantiation that holds the item's rows. Wide items are bound by the
+// instructions of the softmax warps; where the result is rounded to 16 bits anyway, they
+// take three terms of x (15 bits, 2^-14 of a weight at most, against 2^-9 and 2^-12 of the
+// output's rounding).
 template <int D>
-cudaError_t launch_d(int rows, int grid, cudaStream_t st, const CUtensorMap &km,
+cudaError_t launch_d(int rows, bool out16, int grid, cudaStream_t st, const CUtensorMap &km,
                      const CUtensorMap &vm, const Scales8 &sc, const SplitParams &p, int e5m2)
 {
-    // the narrowest instantiation that holds the item's rows
-    if (rows <= 4) return launch_t<D, 4>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 8) return launch_t<D, 8>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 16) return launch_t<D, 16>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 24) return launch_t<D, 24>(grid, st, km, vm, sc, p, e5m2);
-    return launch_t<D, 32>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 4) return launch_t<D, 4, 4>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 8) return launch_t<D, 8, 4>(grid, st, km, vm, sc, p, e5m2);
+    if (out16) {
+        if (rows <= 16) return launch_t<D, 16, 3>(grid, st, km, vm, sc, p, e5m2);
+        if (rows <= 24) return launch_t<D, 24, 3>(grid, st, km, vm, sc, p, e5m2);
+        return launch_t<D, 32, 3>(grid, st, km, vm, sc, p, e5m2);
+    }
+    if (rows <= 16) return launch_t<D, 16, 4>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 24) return launch_t<D, 24, 4>(grid, st, km, vm, sc, p, e5m2);
+    return launch_t<D, 32, 4>(grid, st, km, vm, sc, p, e5m2);
 }
 
 } // namespace
@@ -1015,15 +1046,16 @@ int q8_rows_per_item(int rows)
     return (rows + groups - 1) / groups;
 }
 
-cudaError_t launch_gqa_8bit(int code_dtype, int head_dim, int grid, cudaStream_t st,
+cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid, cudaStream_t st,
                             const CUtensorMap &km, const CUtensorMap &vm, const Scales8 &sc,
                             const SplitParams &p)
 {
     const int rows = p.n_heads / p.items.n_kv_heads;
     const int per = (rows + p.items.row_groups - 1) / p.items.row_groups;
     const int e5m2 = code_dtype == DA_E5M2;
-    if (head_dim == 128) return launch_d<128>(per, grid, st, km, vm, sc, p, e5m2);
-    return launch_d<256>(per, grid, st, km, vm, sc, p, e5m2);
+    const bool out16 = out_dtype != DA_F32;
+    if (head_dim == 128) return launch_d<128>(per, out16, grid, st, km, vm, sc, p, e5m2);
+    return launch_d<256>(per, out16, grid, st, km, vm, sc, p, e5m2);
 }
 
 } // namespace skv

@@ -256,9 +256,9 @@ cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
 constexpr int kQ8Tile = 128;
 constexpr int kQ8Rows = 32;
 int q8_rows_per_item(int rows);
-cudaError_t launch_gqa_8bit(int code_dtype, int head_dim, int grid, cudaStream_t st,
-                            const CUtensorMap &km, const CUtensorMap &vm, const Scales8 &sc,
-                            const SplitParams &p);
+cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
+                            cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
+                            const Scales8 &sc, const SplitParams &p);
 
 // TMA maps of the SIMT GQA kernel: k and v copy a whole tile of T rows; for a
 // paged pool kb and vb copy box_rows rows, the boxes of a tile that spans a

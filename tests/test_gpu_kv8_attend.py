@@ -10,6 +10,10 @@ Tolerance, per output element, from the arithmetic (u = 2^-24):
   * probabilities are held to 20 significant bits and 2^-26 of the largest, 2^x is good to
     2^-22, its f32 argument (at most 2^7 in size) to 2^-18: 2^-16.7 together; sums over
     positions and splits are f32, for the lengths here at most 2^-17: 2^-15 max|V|.
+  * groups of more than 8 rows with a 16-bit output: probabilities of 15 significant bits. A
+    term of 4 bits leaves half of its step, 2^-4 of the value's power of two; each further
+    one, of a rest in the next lower power at most, 2^-5 of that: 2^-4, 2^-9, 2^-14 of a
+    weight, of either sign, in the sum of weight times value: 2^-14 max|V|.
   * the output's rounding: half a step, eps / 2 of the value.
 """
 import math
@@ -63,6 +67,7 @@ def check(got, q, cache, lens, page, code, scale, out="f32", causal=True):
         vmax = np.abs(v[b]).max() if lens[b] else 0.0
         tol = vmax * (2.0 ** -17 * mag[b][..., None] + 2.0 ** -15)
         if out != "f32":
+            tol = tol + (2.0 ** -14 * vmax if q.shape[1] * q.shape[2] // k[b].shape[1] > 8 else 0.0)
             tol = tol + torch.finfo(OUT[out]).eps / 2 * np.abs(ref[b])
             tol = tol + (6e-8 if out == "f16" else 0.0)      # half of f16's least step
         worst = (np.abs(got[b] - ref[b]) / np.maximum(tol, 1e-300)).max()
@@ -116,8 +121,11 @@ def test_forced_splits(splits):
 
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
-def test_output_types(out):
-    run_check([777, 300], 32, 12, 2, 256, "e4m3", out=out, seed=9)
+@pytest.mark.parametrize("hq,d", [(12, 256), (3, 128), (16, 128), (24, 128), (24, 256), (44, 128),
+                                  (64, 256)])
+def test_output_types(out, hq, d):
+    run_check([777, 300], 32, hq, 1, d, "e4m3", out=out, seed=9)
+    run_check([200, 129], 32, hq // 2, 1, d, "e4m3", T=2, out=out, seed=10)
 
 
 def test_few_ctas_walk_many_items():
