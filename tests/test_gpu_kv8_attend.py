@@ -445,11 +445,12 @@ def test_codes_are_used_as_they_stand():
             np.testing.assert_allclose(got[0, 0, 0], vals[row] * 0.375, rtol=2.0 ** -19, atol=0)
 
 
-def test_a_wait_that_runs_out_is_reported():
+@pytest.mark.parametrize("rows,d", [(4, 128), (8, 128), (16, 128), (24, 256), (32, 128)])
+def test_a_wait_that_runs_out_is_reported(rows, d):
     # the copies are never issued; the next call on the same workspace is sound
     lens = [500, 2000]
-    cache = paged_cache(39, lens, 16, 2, 128, "e4m3")
-    q = queries(40, 2, 1, 8, 128)
+    cache = paged_cache(39, lens, 16, 1, d, "e4m3")
+    q = queries(40, 2, 1, rows, d)
     kp, vp, ks, vs, t = [y.cuda() for y in cache]
     x = q[:, 0].contiguous().cuda()
     dv = A.make_dev(block_table=t, k_pool=kp, v_pool=vp)
@@ -482,3 +483,78 @@ def test_a_nan_score_makes_the_row_nan(rows, where):
     q = queries(42, 2, 1, rows, d)
     got = call(q, cache, 16, 0.1, plan_lens=[L, 129], splits=1)
     assert np.all(np.isnan(got))
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("hq", [4, 24])
+def test_a_query_that_is_no_number_spoils_its_own_row_alone(bad, hq):
+    cache = paged_cache(43, [300], 16, 1, 128, "e4m3")
+    q = queries(44, 1, 1, hq, 128)
+    want = call(q, cache, 16, 0.1, plan_lens=[300])
+    x = q.clone()
+    x[0, 0, 2, 17] = bad
+    got = call(x, cache, 16, 0.1, plan_lens=[300])
+    assert np.all(np.isnan(got[0, 0, 2]))
+    keep = [h for h in range(hq) if h != 2]
+    np.testing.assert_array_equal(got[0, 0, keep], want[0, 0, keep])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30])
+def test_scales_of_the_scores(scale):
+    cache = paged_cache(45, [500, 3], 16, 2, 128, "e4m3")
+    q = queries(46, 2, 1, 8, 128)
+    got = call(q, cache, 16, scale, plan_lens=[500, 3])
+    check(got, q, cache, [500, 3], 16, "e4m3", abs(scale)) if scale >= 0 else \
+        check(got, -q, cache, [500, 3], 16, "e4m3", -scale)
+
+
+def test_queries_of_very_different_size():
+    # rows from 1e-12 to 1e3: every row is scaled for itself
+    cache = paged_cache(47, [400], 16, 1, 256, "e4m3")
+    q = queries(48, 1, 1, 8, 256) * torch.tensor([1e-12, 1e-6, 1e-3, 0.1, 1.0, 10.0, 30.0, 0.0])[:, None]
+    got = call(q, cache, 16, 1 / 16, plan_lens=[400])
+    check(got, q, cache, [400], 16, "e4m3", 1 / 16)
+
+
+def test_one_large_page_and_a_full_table():
+    # a pool of a single page of 4096 positions, of which the table has one entry
+    cache = paged_cache(49, [4096], 4096, 1, 128, "e4m3", spare=0, width_extra=0)
+    q = queries(50, 1, 1, 8, 128)
+    got = call(q, cache, 4096, 0.1, plan_lens=[4096])
+    check(got, q, cache, [4096], 4096, "e4m3", 0.1)
+
+
+def test_many_sequences():
+    # the largest batch, a third of it empty
+    lens = [(7 * b) % 200 if b % 3 else 0 for b in range(256)]
+    cache = paged_cache(51, lens, 16, 1, 128, "e4m3")
+    q = queries(52, 256, 1, 4, 128)
+    got = call(q, cache, 16, 0.1, plan_lens=[max(1, n) for n in lens], now=lens)
+    check(got, q, cache, lens, 16, "e4m3", 0.1)
+
+
+def test_a_batch_that_is_empty():
+    cache = paged_cache(53, [0, 0], 16, 2, 256, "e4m3")
+    q = queries(54, 2, 1, 16, 256)
+    got = call(q, cache, 16, 0.1, plan_lens=[20, 20], now=[0, 0])
+    assert np.all(got == 0)
+
+
+def test_refusals_of_the_binding():
+    cache = [t.cuda() for t in paged_cache(55, [30], 16, 1, 128, "e4m3")]
+    kp, vp, ks, vs, t = cache
+    x = torch.randn(1, 4, 128, device="cuda")
+    a = A.make_paged_args(x, kp, vp, 0.1, t.shape[1])
+    p = A.decode_attn_plan(a, [30])
+    dv, sc = A.make_dev(block_table=t, k_pool=kp, v_pool=vp), A.make_scales(ks, vs)
+    ws, o = A.new_workspace(p), torch.empty_like(x)
+    for q_, o_ in ((x.half(), o), (x.cpu(), o), (x.transpose(1, 2), o), (x, o.transpose(1, 2))):
+        with pytest.raises((TypeError, ValueError)):
+            A.decode_attn_splitk_8bit(a, p, dv, sc, q_, kp, vp, o_, ws)
+    with pytest.raises(ValueError):
+        A.decode_attn_splitk_8bit(a, p, dv, sc, x, kp.cpu(), vp, o, ws)
+    with pytest.raises(TypeError):
+        A.make_scales(ks.half(), vs)
+    with pytest.raises(A.DecodeAttnError) as e:
+        A.decode_attn_splitk_8bit(a, p, A.make_dev(), sc, x, kp, vp, o, ws)
+    assert e.value.status == N.DA_EINVAL and "block_table" in e.value.message
