@@ -16,7 +16,8 @@
 // terms, y = y_0 + 2^-4 y_1 + 2^-8 y_2 + 2^-12 y_3: a term rounds what the ones
 // before it left, and each takes 5 bits off (4 significant bits and the sign of
 // the rest), so four hold 20 bits; y is scaled to at most 256, so that the
-// smallest steps (e4m3's 2^-9, 2^-21 in the last term) are 2^-30 of the largest.
+// smallest steps (e4m3's 2^-9, 2^-21 in the last term) are 2^-30 of the largest. (Wide
+// items with 16-bit outputs take three terms of x, see launch_d.)
 // The terms are columns of the MMA (N = 4 x rows, at least 16), whose time for N <= 64
 // is that of reading the tile (46 to 48 cycles per 32-byte step); they are added in
 // f32 when S or O^T leave TMEM. The products are exact and the sums f32 (measured:
@@ -24,10 +25,11 @@
 //
 // An item is (sequence, KV head, split, row group), rows (query token, head). Roles, one
 // CTA per SM:
-//   softmax warpgroups (1, 2 or 4, up to 8 rows each): a thread owns one position of the
-//              tile (TMEM lane); the reference m of a row moves only when a score outgrows it
-//              by 2^8 (then O^T is rescaled), so most tiles take one vote. In the epilogue a
-//              thread owns a value column.
+//   softmax warpgroups (1 to 4, up to 8 rows each; on some shapes two sets of them take
+//              tiles in turn): a thread owns one position of the tile (TMEM lane); the
+//              reference m of a row moves only when a score outgrows it by 2^8 (then O^T is
+//              rescaled), so most tiles take one vote. In the epilogue a thread owns a value
+//              column.
 //   two warps  TMA producers, K and V tiles through one ring of slots, paged boxes as in the
 //              16-bit tensor-core kernel.
 //   two warps  MMA issue, one thread each for the scores and for the values.
@@ -246,7 +248,8 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                     const int e5m2)
 {
     using L = Layout<D, RP, PT>;
-    constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW, X = L::X, WT = L::WT;
+    constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW,
+                  X = L::X, WT = L::WT;
     constexpr int RC = 4; // rows taken from TMEM at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
             if (!w.done && lane < nbox) {
                 const int pos = w.t0 + lane * h, idx = pos / bs;
                 slot0 = pos - idx * bs;
-                if (idx < p.max_blocks)
+                if (pos < w.t1 && idx < p.max_blocks) // past the tile: zeros, nothing is read
                     blk = __ldg(p.block_table + (size_t)w.b * p.max_blocks + idx);
             }
             return blk;
