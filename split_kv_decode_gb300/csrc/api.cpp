@@ -636,9 +636,10 @@ int launch_split(const da_args_t *a, const da_plan_t *pl, const float *q, const 
 }
 
 // Launches the split kernel over 8-bit paged pools.
+// *whole: it wrote the output itself (one split a sequence), and no combine is wanted.
 int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
                 const da_scales_t *sc, const float *q, const void *k, const void *v, void *ws,
-                cudaStream_t st)
+                cudaStream_t st, void *out, bool *whole)
 {
     SplitParams p;
     split_params(a, pl, q, ws, &p);
@@ -650,6 +651,9 @@ int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
     p.box_rows = std::gcd(pl->tile, dev->block_size);
     const int G = a->n_heads / a->n_kv_heads * q_len_of(a), per = q8_rows_per_item(G);
     p.items.row_groups = (G + per - 1) / per;
+    *whole = pl->max_splits == 1 && per <= kQ8DirectRows && !(a->flags & DA_FLAG_NO_COMBINE);
+    p.fused = fused_out(a, pl, ws, out);
+    p.fused.on = *whole;
     const Scales8 s = {sc->k_scale,      sc->v_scale,       sc->k_block_stride, sc->k_head_stride,
                        sc->v_block_stride, sc->v_head_stride, dev->num_blocks};
     CUtensorMap km, vm;
@@ -975,9 +979,10 @@ int decode_attn_splitk_8bit(const da_args_t *a, const da_plan_t *plan, const da_
     if (pre != cudaSuccess)
         return fail(DA_ECUDA, "before split", "pending CUDA error: %s", cudaGetErrorString(pre));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    rc = launch_8bit(a, plan, dev, sc, q, k, v, ws, st);
+    bool whole = false;
+    rc = launch_8bit(a, plan, dev, sc, q, k, v, ws, st, out, &whole);
     if (rc) return rc;
-    if (a->flags & DA_FLAG_NO_COMBINE) return DA_OK;
+    if (whole || (a->flags & DA_FLAG_NO_COMBINE)) return DA_OK;
     return launch_combine_phase(a, plan, ws, out, st);
 }
 

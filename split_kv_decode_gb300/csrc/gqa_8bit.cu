@@ -34,9 +34,13 @@
 //              16-bit tensor-core kernel.
 //   two warps  MMA issue, one thread each for the scores and for the values.
 //   one warp   the page scales of four tiles at a time, two batches ahead.
+// Where every sequence has one split there is nothing to merge: the epilogue divides by l
+// and writes the output itself, and no combine follows (256 sequences of 40 positions, 32/8
+// heads: 60 us instead of 72). Items of more than 16 rows have not the registers for it.
 // Every wait is bounded; a wait that runs out sets the status word and the CTA drains
 // and returns.
 #include <climits>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -196,6 +200,16 @@ __device__ __forceinline__ int len8(const SplitParams &p, int b)
 {
     const int L = p.items.seq_lens[b];
     return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
+}
+
+// one output element, in the output's type
+__device__ __forceinline__ void put_out(const FusedOut &f, size_t i, float v)
+{
+    switch (f.out_dtype) {
+    case DA_F32: static_cast<float *>(f.out)[i] = v; break;
+    case DA_F16: static_cast<__half *>(f.out)[i] = __float2half_rn(v); break;
+    default: static_cast<__nv_bfloat16 *>(f.out)[i] = __float2bfloat16_rn(v); break;
+    }
 }
 
 // The (item, tile) sequence of a CTA, the same for every role: items blockIdx.x,
@@ -520,6 +534,7 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
         const int per = (rows + it.row_groups - 1) / it.row_groups;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + r00;
         const bool causal = p.q_len > 1 && !(p.flags & DA_FLAG_NO_CAUSAL);
+        const bool direct = RP <= kQ8DirectRows && p.fused.on; // writes the output itself
         uint32_t sph = 0, pfp = 0, iph = 0, scp = 0; // iph: item parity
         bool ab = false;
         int gt = 0;
@@ -549,10 +564,19 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
             x.R = min(per, rows - x.row0);
             return x;
         };
-        auto neutral = [&](const Item &x, int r) { // row r of an empty item
+        // workspace row of row r of an item (with one split a sequence: the output row)
+        auto row_of = [&](const Item &x, int r) {
             const int jf = x.row0 + r;
-            p.ml[(size_t)x.slot * p.n_heads + (size_t)x.kvh * Gh + jf / Gh * p.hq + jf % Gh] =
-                make_float2(kNeutralM, 0.f);
+            return (size_t)x.slot * p.n_heads + (size_t)x.kvh * Gh + jf / Gh * p.hq + jf % Gh;
+        };
+        // an item without positions, by thread i of n: neutral partials, or zeros in the output
+        auto empty_item = [&](const Item &x, int i, int n) {
+            if (direct) {
+                for (int r = 0; r < x.R; ++r)
+                    for (int d = i; d < D; d += n) put_out(p.fused, row_of(x, r) * D + d, 0.f);
+            } else {
+                for (int r = i; r < x.R; r += n) p.ml[row_of(x, r)] = make_float2(kNeutralM, 0.f);
+            }
         };
         constexpr bool kLanes = RP <= 8;
         int k0 = -32;
@@ -564,9 +588,17 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                     if (k >= k0 + 32) {
                         k0 += 32;
                         mine = look(k0 + lane);
-                        if (mine.k >= 0 && mine.p1 == mine.p0 && warp == 0)
-                            for (int r = 0; r < mine.R; ++r) neutral(mine, r);
-                        __syncwarp();
+                        unsigned none =
+                            __ballot_sync(0xffffffffu, mine.k >= 0 && mine.p1 == mine.p0);
+                        while (warp == 0 && none) {
+                            const int i = __ffs(none) - 1;
+                            none &= none - 1;
+                            x.kvh = __shfl_sync(0xffffffffu, mine.kvh, i);
+                            x.row0 = __shfl_sync(0xffffffffu, mine.row0, i);
+                            x.slot = __shfl_sync(0xffffffffu, mine.slot, i);
+                            x.R = min(per, rows - x.row0);
+                            empty_item(x, lane, 32);
+                        }
                     }
                     const unsigned live =
                         __ballot_sync(0xffffffffu, mine.p1 > mine.p0) >> (k - k0);
@@ -589,7 +621,7 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                 for (;; ++k) {
                     x = look(k);
                     if (x.k < 0 || x.p1 > x.p0) return x;
-                    if (wg == 0 && tid < x.R) neutral(x, tid);
+                    if (wg == 0) empty_item(x, tid, 128);
                 }
             }
         };
@@ -967,7 +999,7 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                     for (int i = 0; i < RC; ++i) {
                         const int r = r00 + r0 + i;
                         float f[X], M, y = 0.f;
-                        (void)join(r0 + i, f, M);
+                        const float lr = join(r0 + i, f, M);
 #pragma unroll
                         for (int x = 0; x < X; ++x) {
                             float o = v[x][PT - 1][i];
@@ -979,12 +1011,16 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                         if (r < R) {
                             if (nan_from != INT_MAX && (row0 + r) / Gh >= nan_from)
                                 y = __int_as_float(0x7fffffff);
-                            p.acc[(wbase + wrow_sm[r]) * D + 128 * j + tid] = y;
+                            const size_t at = (wbase + wrow_sm[r]) * D + 128 * j + tid;
+                            if (direct) // nothing seen: zero; a NaN score: NaN
+                                put_out(p.fused, at, lr == 0.f ? 0.f : y * (1.f / lr));
+                            else
+                                p.acc[at] = y;
                         }
                     }
                 }
             }
-            if (turn == 0 && tid < RPW && r00 + tid < R) {
+            if (!direct && turn == 0 && tid < RPW && r00 + tid < R) {
                 float f[X], M;
                 const float lr = join(tid, f, M);
                 // a NaN score makes the row NaN whatever the other splits hold

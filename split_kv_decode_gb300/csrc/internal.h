@@ -45,7 +45,8 @@ inline int64_t ws_total(int64_t total_splits, int n_heads, int v_dim, int64_t n_
 // A split kernel that merges its own partials (no combine launch): the last
 // partial of a (sequence, KV head) group to arrive merges the group's rows
 // (GQA kernels); every CTA merges a share of the rows once all CTAs have
-// arrived (MLA tensor-core kernel).
+// arrived (MLA tensor-core kernel). The 8-bit kernel writes the output itself when
+// every sequence has one split (no counters).
 struct FusedOut {
     void *out;                   // [B][rows][v_dim] in out_dtype
     uint32_t *ctr;               // arrival counters (workspace tail), zero at launch
@@ -255,6 +256,7 @@ cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
 // groups are cut into row groups.
 constexpr int kQ8Tile = 128;
 constexpr int kQ8Rows = 32;
+constexpr int kQ8DirectRows = 16; // items of up to so many rows may write the output themselves
 int q8_rows_per_item(int rows);
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
                             cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,

@@ -558,3 +558,31 @@ def test_refusals_of_the_binding():
     with pytest.raises(A.DecodeAttnError) as e:
         A.decode_attn_splitk_8bit(a, p, A.make_dev(), sc, x, kp, vp, o, ws)
     assert e.value.status == N.DA_EINVAL and "block_table" in e.value.message
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,T", [(8, 2, 1), (16, 2, 1), (5, 1, 4), (40, 1, 1), (24, 1, 2)])
+def test_one_split_a_sequence_writes_the_same_bits_as_the_combine(hq, hkv, T, out):
+    # lengths of zero, and tokens before the start, among them
+    now = [40, 0, 129, 2, 128, 0, 300, 1]
+    cache = paged_cache(57, now, 16, hkv, 128, "e4m3", width_extra=20)
+    kp, vp, ks, vs, t = [y.cuda() for y in cache]
+    x = queries(58, 8, T, hq, 128).cuda()
+    x = x[:, 0].contiguous() if T == 1 else x
+    lens = torch.tensor(now, dtype=torch.int32, device="cuda")
+    dv, sc = A.make_dev(seq_lens=lens, block_table=t, k_pool=kp, v_pool=vp), A.make_scales(ks, vs)
+    got = []
+    for flags in (0, N.DA_FLAG_NO_COMBINE):
+        a = A.make_paged_args(x, kp, vp, 0.1, t.shape[1], out_dtype=OUT[out], force_splits=1,
+                              flags=flags)
+        p = A.decode_attn_plan(a, [320] * 8, 3)   # 3 CTAs: many items each
+        assert p.max_splits == 1
+        ws, o = A.new_workspace(p), torch.full(x.shape, math.nan, dtype=OUT[out], device="cuda")
+        ws.fill_(0xFF)
+        A.decode_attn_splitk_8bit(a, p, dv, sc, x, kp, vp, o, ws)
+        if flags:
+            A.decode_attn_combine(a, p, ws, o)
+        got.append(o.view(torch.int32 if out == "f32" else torch.int16).clone())
+    assert torch.equal(*got)
+    check(o.double().cpu().numpy().reshape(8, T, hq, 128), queries(58, 8, T, hq, 128), cache, now,
+          16, "e4m3", 0.1, out)
