@@ -33,7 +33,8 @@
 //   two warps  TMA producers, K and V tiles through one ring of slots, paged boxes as in the
 //              16-bit tensor-core kernel.
 //   two warps  MMA issue, one thread each for the scores and for the values.
-//   one warp   the page scales of four tiles at a time, two batches ahead.
+//   one warp   the page scales of four tiles at a time, two batches ahead (the K producer does
+//              it beside many softmax warps).
 // Where every sequence has one split there is nothing to merge: the epilogue divides by l
 // and writes the output itself, and no combine follows (256 sequences of 40 positions, 32/8
 // heads: 60 us instead of 72). Items of more than 16 rows have not the registers for it.
@@ -83,10 +84,13 @@ template <int D, int RP, int PT> struct Layout {
     // and more rows have not the registers).
     static constexpr int X = D == 128 && (RP == 8 || RP == 16) ? 2 : 1;
     static constexpr int WT = W * X; // softmax warpgroups
-    static constexpr int THREADS = WT * 128 + 160;
-    // warps after the softmax warps
+    // Warps after the softmax warps. Beside three or four warpgroups the K producer fetches
+    // the page scales too: a warp less, a thread has 128 registers and not 96, or 96 and not
+    // 80, with which the tile loop spilled.
+    static constexpr bool KSCALE = WT >= 3;
     static constexpr int KPROD = 4 * WT, VPROD = KPROD + 1, QK = KPROD + 2, PV = KPROD + 3,
-                         SCALE = KPROD + 4;
+                         SCALE = KSCALE ? -1 : KPROD + 4;
+    static constexpr int THREADS = 32 * (KPROD + (KSCALE ? 4 : 5));
     // weights as [row term][position] (K-major), or for wide items [position][row term]
     // (MN-major, rows of 128 bytes): there a thread stores 8 bytes at a time
     static constexpr bool PMN = N >= 64 || D == 128;
@@ -321,6 +325,38 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
     griddep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
+    // A whole warp: the page scales of the next four tiles of w, for groups of 16 positions.
+    // Batches take two buffers in turn; false when the wait for one runs out.
+    auto scale_batch = [&](Walk8 &w, int batch) {
+        const int g = lane & 7; // group of its tile
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        int b = -1, kvh = 0, pos = 0;
+        for (int i = 0; i < 4 && !w.done; ++i, w.next(p))
+            if ((lane >> 3) == i && w.t0 + 16 * g < w.t1) {
+                b = w.b;
+                kvh = w.kvh;
+                pos = w.t0 + 16 * g;
+            }
+        if (b >= 0) {
+            const int blk = p.block_table[(size_t)b * p.max_blocks + pos / p.block_size];
+            float vs = 0.f;
+            if (blk >= 0 && blk < sc.num_blocks) {
+                v.x = __ldg(sc.k + blk * sc.k_block + kvh * sc.k_head);
+                vs = __ldg(sc.v + blk * sc.v_block + kvh * sc.v_head);
+            }
+            v.z = fmaxf(vs, kMinScale);
+            v.y = __log2f(v.z);
+        }
+        const int half = batch & 1;
+        const bool got = mbar_wait_bounded(bar + B_SCFREE + half, ((uint32_t)(batch >> 1) & 1u) ^ 1u,
+                                           p.timeout_ns, abort_flag);
+        if (__any_sync(0xffffffffu, !got)) return false;
+        sc_sm[half * 32 + lane] = v;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + B_SCFULL + half);
+        return true;
+    };
+
     if (warp == L::KPROD || warp == L::VPROD) {
         // =================== TMA producers, one for K and one for V ===================
         // box j holds positions [t0 + j*h, t0 + (j+1)*h) of a 128-column chunk, h =
@@ -353,7 +389,13 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
         Walk8 w;
         w.start(p);
         int slot0 = 0, blk = look_up(w, slot0);
+        const bool scales = L::KSCALE && !isv; // four tiles' scales before the first of them
+        Walk8 ws = w;
         while (!w.done) {
+            if (scales && (w.gt & 3) == 0 && !scale_batch(ws, w.gt >> 2)) {
+                ok = false;
+                break;
+            }
             Walk8 nx = w; // the next tile's blocks are looked up while this one is issued
             nx.next(p);
             int nslot0 = 0;
@@ -399,45 +441,16 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                     (void)mbar_wait_bounded(bar + B_FULL + s, (last >> s) & 1u, p.timeout_ns,
                                             &never);
     } else if (warp == L::SCALE) {
-        // ====================== page scales, four tiles at a time ======================
-        const int g = lane & 7; // group of 16 positions of the tile
-        uint32_t fph = 0;
         Walk8 w;
         w.start(p);
-        for (int batch = 0; !w.done; ++batch) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            int b = -1, kvh = 0, pos = 0;
-            for (int i = 0; i < 4 && !w.done; ++i, w.next(p))
-                if ((lane >> 3) == i && w.t0 + 16 * g < w.t1) {
-                    b = w.b;
-                    kvh = w.kvh;
-                    pos = w.t0 + 16 * g;
-                }
-            if (b >= 0) {
-                const int blk = p.block_table[(size_t)b * p.max_blocks + pos / p.block_size];
-                float vs = 0.f;
-                if (blk >= 0 && blk < sc.num_blocks) {
-                    v.x = __ldg(sc.k + blk * sc.k_block + kvh * sc.k_head);
-                    vs = __ldg(sc.v + blk * sc.v_block + kvh * sc.v_head);
-                }
-                v.z = fmaxf(vs, kMinScale);
-                v.y = __log2f(v.z);
-            }
-            const int half = batch & 1;
-            const bool got = mbar_wait_bounded(bar + B_SCFREE + half, ((fph >> half) & 1u) ^ 1u,
-                                               p.timeout_ns, abort_flag);
-            if (__any_sync(0xffffffffu, !got)) {
+        for (int batch = 0; !w.done; ++batch)
+            if (!scale_batch(w, batch)) {
                 if (lane == 0) {
                     *abort_flag = 1;
                     atomicCAS(p.status, 0, kStatusTimeoutQ8);
                 }
                 break;
             }
-            fph ^= 1u << half;
-            sc_sm[half * 32 + lane] = v;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar + B_SCFULL + half);
-        }
     } else if (warp == L::QK || warp == L::PV) {
         // ================ MMA issue: one thread for S, one for O^T ================
         // Two issuers, so that neither polls for the other's inputs.
