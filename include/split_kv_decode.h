@@ -609,7 +609,7 @@ typedef struct da_scales_t {
  *     < q_len); nothing is read for them.
  *   - block_table entries of positions below the length must be in
  *     [0, num_blocks); an entry outside reads as zeros.
- *   - When the plan has one split for every sequence and an item at most 16 rows,
+ *   - When the plan has one split for every sequence and an item at most 24 rows,
  *     the split kernel writes out itself and no combine is launched; otherwise the
  *     combine launch merges (DA_FLAG_ONE_LAUNCH changes nothing).
  * Codes past a sequence's length may hold anything, NaN among them. With

@@ -37,7 +37,8 @@
 //              it beside many softmax warps).
 // Where every sequence has one split there is nothing to merge: the epilogue divides by l
 // and writes the output itself, and no combine follows (256 sequences of 40 positions, 32/8
-// heads: 60 us instead of 72). Items of more than 16 rows have not the registers for it.
+// heads: 60 us instead of 72; 128 of 100, 24 heads of 256 over one: 25 instead of 38). Items of
+// more than 24 rows have not the registers for it (their long contexts would take 10% more).
 // Every wait is bounded; a wait that runs out sets the status word and the CTA drains
 // and returns.
 #include <climits>

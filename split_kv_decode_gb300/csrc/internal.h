@@ -256,7 +256,7 @@ cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
 // groups are cut into row groups.
 constexpr int kQ8Tile = 128;
 constexpr int kQ8Rows = 32;
-constexpr int kQ8DirectRows = 16; // items of up to so many rows may write the output themselves
+constexpr int kQ8DirectRows = 24; // items of up to so many rows may write the output themselves
 int q8_rows_per_item(int rows);
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
                             cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
