@@ -601,8 +601,8 @@ typedef struct da_scales_t {
  * args->kv_dtype is DA_E4M3 or DA_E5M2, v_dim == head_dim (128 or 256), and the
  * plan was made for these args; dev->block_table is required. A contiguous cache
  * is a pool with an identity table. Keys and values are used as the codes stand,
- * q and the probabilities carry 20 significant bits (the probabilities 15 in
- * groups of more than 8 rows whose output is f16 or bf16), sums are f32.
+ * q and the probabilities carry 24 significant bits for an f32 output and 20 for f16
+ * and bf16 (the probabilities 15 in groups of more than 8 rows); sums are f32.
  * Differences to decode_attn_splitk_dev:
  *   - a device length is clamped to [0, plan->seq_lens[b]]. A sequence of length 0
  *     gives zeros, and so does a new token before the sequence's start (length

@@ -184,7 +184,8 @@ int select_kernel(const da_args_t *a, KernelChoice *kc)
         kc->tile = kQ8Tile;
         kc->ctas_per_sm = 1;
         kc->cluster = 1;
-        kc->row_groups = (G + q8_rows_per_item(G) - 1) / q8_rows_per_item(G);
+        const int per = q8_rows_per_item(G, a->out_dtype);
+        kc->row_groups = (G + per - 1) / per;
         return DA_OK;
     }
     if (a->head_dim == 576 && a->v_dim == 512 && a->n_kv_heads == 1) {
@@ -649,7 +650,7 @@ int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
     p.block_size = dev->block_size;
     p.oob_block = dev->num_blocks;
     p.box_rows = std::gcd(pl->tile, dev->block_size);
-    const int G = a->n_heads / a->n_kv_heads * q_len_of(a), per = q8_rows_per_item(G);
+    const int G = a->n_heads / a->n_kv_heads * q_len_of(a), per = q8_rows_per_item(G, a->out_dtype);
     p.items.row_groups = (G + per - 1) / per;
     *whole = pl->max_splits == 1 && per <= kQ8DirectRows && !(a->flags & DA_FLAG_NO_COMBINE);
     p.fused = fused_out(a, pl, ws, out);

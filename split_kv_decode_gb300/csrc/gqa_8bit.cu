@@ -12,16 +12,18 @@
 //     S[pos][(j, r)]  = sum_d Kc[pos][d] q_j[r][d]      (M = 128 positions, K = D)
 //     O^T[d][(j, r)] += sum_pos Vc[pos][d] x_j[r][pos]  (M = 128 value columns, K = 128)
 //
-// The other operand of an 8-bit MMA is 8-bit too. q and x are split into four e4m3
-// terms, y = y_0 + 2^-4 y_1 + 2^-8 y_2 + 2^-12 y_3: a term rounds what the ones
-// before it left, and each takes 5 bits off (4 significant bits and the sign of
-// the rest), so four hold 20 bits; y is scaled to at most 256, so that the
-// smallest steps (e4m3's 2^-9, 2^-21 in the last term) are 2^-30 of the largest. (Wide
-// items with 16-bit outputs take three terms of x, see launch_d.)
-// The terms are columns of the MMA (N = 4 x rows, at least 16), whose time for N <= 64
-// is that of reading the tile (46 to 48 cycles per 32-byte step); they are added in
-// f32 when S or O^T leave TMEM. The products are exact and the sums f32 (measured:
-// relative error 1e-7 on full-range codes).
+// The other operand of an 8-bit MMA is 8-bit too. q and x are split into e4m3 terms,
+// y = y_0 + 2^-4 y_1 + 2^-8 y_2 + ...: a term rounds what the ones before it left, and
+// each takes 5 bits off (4 significant bits and the sign of the rest). f32 outputs take
+// five terms of both, 25 bits; 16-bit ones four of q, 20 bits, and four of x, or three, 15 bits,
+// in items of more than 8 rows (2^-14 of a weight at most, against 2^-9 and 2^-12 of the
+// output's rounding). Four of both
+// left an error of 0.4 to 1.4e-6 in f32 outputs, as much as or more than f32 arithmetic does.
+// y is scaled to at most 256, so that e4m3's least step, 2^-9, is 2^-25 to 2^-33 of the
+// largest in the last term. The terms are columns of the MMA (N = terms x rows, rounded to
+// 16), whose time for N <= 64 is that of reading the tile (46 to 48 cycles per 32-byte step);
+// they are added in f32 when S or O^T leave TMEM. The products are exact and the sums f32
+// (measured: relative error 1e-7 on full-range codes).
 //
 // An item is (sequence, KV head, split, row group), rows (query token, head). Roles, one
 // CTA per SM:
@@ -54,7 +56,6 @@ namespace skv {
 namespace {
 
 constexpr int T = kQ8Tile;
-constexpr int kTerms = 4;
 constexpr float kTermStep = 1.f / 16.f;
 constexpr float kHead = 4.f; // m is this much below the maximum that set it
 constexpr float kTau = 8.f;  // and moves when a score is this much above it
@@ -69,12 +70,12 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE 
               B_SCFREE = B_SCFULL + 2, B_QKDRAIN = B_SCFREE + 2, B_PVDRAIN = B_QKDRAIN + 1,
               B_N = B_PVDRAIN + 1;
 
-// Shape and shared memory of <D, RP, PT>: RP rows an item at most, 4 terms of q, PT of x. A
+// Shape and shared memory of <D, RP, QT, PT>: RP rows an item at most, QT terms of q, PT of x. A
 // softmax warpgroup takes RPW rows of every tile (8, or 4 when there are no more): a
 // thread's share of a tile must not outlast the tile's time on the memory side, and 32
 // rows in one thread took 5200 cycles against 2800.
-template <int D, int RP, int PT> struct Layout {
-    static constexpr int N = kTerms * RP;              // columns of S
+template <int D, int RP, int QT, int PT> struct Layout {
+    static constexpr int N = (QT * RP + 15) / 16 * 16;  // columns of S
     static constexpr int NP = (PT * RP + 15) / 16 * 16; // columns of O^T
     static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups a tile
     static constexpr int RPW = RP / W;
@@ -94,7 +95,7 @@ template <int D, int RP, int PT> struct Layout {
     static constexpr int THREADS = 32 * (KPROD + (KSCALE ? 4 : 5));
     // weights as [row term][position] (K-major), or for wide items [position][row term]
     // (MN-major, rows of 128 bytes): there a thread stores 8 bytes at a time
-    static constexpr bool PMN = N >= 64 || D == 128;
+    static constexpr bool PMN = RP >= 16 || D == 128;
     static constexpr int NCH = D / 128;        // 128-column chunks of a row
     static constexpr int CHUNK = T * 128;      // bytes of a chunk of a tile
     static constexpr int SLOT = NCH * CHUNK;   // a K or V tile
@@ -121,6 +122,7 @@ template <int D, int RP, int PT> struct Layout {
     static_assert(NS >= 4 && NS % 2 == 0, "K and V tiles of two steps in flight");
     static_assert(2 * N + X * NCH * NP <= 512, "TMEM columns: two S slots and O^T");
     static_assert(QCH % 1024 == 0 && BYTES <= 232448, "swizzle atoms, shared memory");
+    static_assert(!PMN || NP <= 128, "a position's weights in one row of the swizzle");
 };
 
 // byte offset of (row, byte) in a region of 128-byte rows with the 128-byte swizzle
@@ -260,13 +262,13 @@ struct Walk8 {
     }
 };
 
-template <int D, int RP, int PT>
-__global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
+template <int D, int RP, int QT, int PT>
+__global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     gqa_8bit_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ Scales8 sc, const __grid_constant__ SplitParams p,
                     const int e5m2)
 {
-    using L = Layout<D, RP, PT>;
+    using L = Layout<D, RP, QT, PT>;
     constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW,
                   X = L::X, WT = L::WT;
     constexpr int RC = 4; // rows taken from TMEM at a time
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                     float y0 = v[c].x * f, y1 = v[c].y * f, y2 = v[c].z * f, y3 = v[c].w * f;
                     if (nan) y0 = __int_as_float(0x7fffffff);
 #pragma unroll
-                    for (int j = 0; j < kTerms; ++j) {
+                    for (int j = 0; j < QT; ++j) {
                         const uint32_t lo = term2(y0, y1), hi = term2(y2, y3);
                         sts_u32(sb + L::Q_OFF + c * L::QCH + swz(j * RP + r, 4 * lane),
                                 lo | (hi << 16));
@@ -803,16 +805,16 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
                 auto scores = [&](bool less) {
 #pragma unroll
                     for (int r0 = 0; r0 < RPW; r0 += RC) {
-                        float v[kTerms][RC];
+                        float v[QT][RC];
 #pragma unroll
-                        for (int j = 0; j < kTerms; ++j)
+                        for (int j = 0; j < QT; ++j)
                             tmem_ld<RC>(tl + ss * N + j * RP + r0, v[j]);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < RC; ++i) {
-                            float y = v[kTerms - 1][i];
+                            float y = v[QT - 1][i];
 #pragma unroll
-                            for (int j = kTerms - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
+                            for (int j = QT - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
                             a[r0 + i] = fmaf(y, qf_sm[r00 + r0 + i] * sv.x, less ? -m[r0 + i] : 0.f);
                         }
                     }
@@ -1062,12 +1064,12 @@ __global__ void __launch_bounds__((Layout<D, RP, PT>::THREADS), 1)
     if (threadIdx.x == 0) griddep_launch_dependents();
 }
 
-template <int D, int RP, int PT>
+template <int D, int RP, int QT, int PT>
 cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
                      const Scales8 &sc, const SplitParams &p, int e5m2)
 {
-    using L = Layout<D, RP, PT>;
-    auto *fn = gqa_8bit_kernel<D, RP, PT>;
+    using L = Layout<D, RP, QT, PT>;
+    auto *fn = gqa_8bit_kernel<D, RP, QT, PT>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1085,31 +1087,30 @@ cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUt
     return e != cudaSuccess ? e : last;
 }
 
-// The narrowest instantiation that holds the item's rows. Wide items are bound by the
-// instructions of the softmax warps; where the result is rounded to 16 bits anyway, they
-// take three terms of x (15 bits, 2^-14 of a weight at most, against 2^-9 and 2^-12 of the
-// output's rounding).
+// The narrowest instantiation that holds the item's rows, with the terms of the output's type.
 template <int D>
 cudaError_t launch_d(int rows, bool out16, int grid, cudaStream_t st, const CUtensorMap &km,
                      const CUtensorMap &vm, const Scales8 &sc, const SplitParams &p, int e5m2)
 {
-    if (rows <= 4) return launch_t<D, 4, 4>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 8) return launch_t<D, 8, 4>(grid, st, km, vm, sc, p, e5m2);
     if (out16) {
-        if (rows <= 16) return launch_t<D, 16, 3>(grid, st, km, vm, sc, p, e5m2);
-        if (rows <= 24) return launch_t<D, 24, 3>(grid, st, km, vm, sc, p, e5m2);
-        return launch_t<D, 32, 3>(grid, st, km, vm, sc, p, e5m2);
+        if (rows <= 4) return launch_t<D, 4, 4, 4>(grid, st, km, vm, sc, p, e5m2);
+        if (rows <= 8) return launch_t<D, 8, 4, 4>(grid, st, km, vm, sc, p, e5m2);
+        if (rows <= 16) return launch_t<D, 16, 4, 3>(grid, st, km, vm, sc, p, e5m2);
+        if (rows <= 24) return launch_t<D, 24, 4, 3>(grid, st, km, vm, sc, p, e5m2);
+        return launch_t<D, 32, 4, 3>(grid, st, km, vm, sc, p, e5m2);
     }
-    if (rows <= 16) return launch_t<D, 16, 4>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 24) return launch_t<D, 24, 4>(grid, st, km, vm, sc, p, e5m2);
-    return launch_t<D, 32, 4>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 4) return launch_t<D, 4, 5, 5>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 8) return launch_t<D, 8, 5, 5>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 16) return launch_t<D, 16, 5, 5>(grid, st, km, vm, sc, p, e5m2);
+    return launch_t<D, 24, 5, 5>(grid, st, km, vm, sc, p, e5m2);
 }
 
 } // namespace
 
-int q8_rows_per_item(int rows)
+int q8_rows_per_item(int rows, int out_dtype)
 {
-    const int groups = (rows + kQ8Rows - 1) / kQ8Rows;
+    // five terms of 32 rows are more columns than TMEM and a row of weights hold
+    const int most = out_dtype == DA_F32 ? 24 : 32, groups = (rows + most - 1) / most;
     return (rows + groups - 1) / groups;
 }
 

@@ -251,13 +251,12 @@ __host__ __device__ inline TcLayout tc_layout(int D, int R)
 cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
                           const CUtensorMap &km, const CUtensorMap &vm, const SplitParams &p);
 
-// 8-bit GQA kernel: tiles of kQ8Tile positions (the 128 rows of the score MMA); at
-// most kQ8Rows query rows a work item (four terms each, 128 MMA columns), larger
-// groups are cut into row groups.
+// 8-bit GQA kernel: tiles of kQ8Tile positions (the 128 rows of the score MMA). A work
+// item holds up to 24 or 32 query rows, by the output's type; larger groups are cut
+// into row groups.
 constexpr int kQ8Tile = 128;
-constexpr int kQ8Rows = 32;
 constexpr int kQ8DirectRows = 24; // items of up to so many rows may write the output themselves
-int q8_rows_per_item(int rows);
+int q8_rows_per_item(int rows, int out_dtype);
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
                             cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
                             const Scales8 &sc, const SplitParams &p);

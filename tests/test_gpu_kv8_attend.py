@@ -2,12 +2,13 @@
 in 64 bits over what the codes stand for.
 
 Tolerance, per output element, from the arithmetic (u = 2^-24):
-  * q is held to 20 significant bits (relative error 2^-20 at most, 2^-19 counted), and a
-    score is an f32 sum of at most 4 * 256 exact products, added 32 at a time, and four
-    more f32 operations: |error of a score| <= (2^-19 + 44 u) * M, M = scale * sum |q k|
+  * q is held to 2^-20 of itself for 16-bit outputs (four terms) and 2^-25 for f32 ones
+    (five). A score is an f32 sum of at most 4 * 256 or 5 * 256 exact products, added 32 at
+    a time, and four more f32 operations: |error of a score| <= (2^-20 + 44 u) * M or
+    (2^-25 + 52 u) * M, M = scale * sum |q k|
     of the position, under 2^-18 * M (natural units). A weight is off by e^error - 1, the
     normalised output by twice that, times max |V|: 2^-17 M max|V|.
-  * probabilities are held to 20 significant bits and 2^-26 of the largest, 2^x is good to
+  * probabilities are held to 20 significant bits or more and 2^-26 of the largest, 2^x is good to
     2^-22, its f32 argument (at most 2^7 in size) to 2^-18: 2^-16.7 together; sums over
     positions and splits are f32, for the lengths here at most 2^-17: 2^-15 max|V|.
   * groups of more than 8 rows with a 16-bit output: probabilities of 15 significant bits. A
@@ -145,6 +146,22 @@ def test_relative_accuracy_of_f32_output():
     # 20-bit operands alone leave 2^-20 / sqrt(3) of the result
     got, ref = run_check([6000], 64, 16, 4, 256, "e4m3", seed=11)
     assert np.linalg.norm(got - ref) <= 2.0 ** -17 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 256), (8, 1, 128), (24, 1, 256), (40, 1, 128)])
+def test_f32_output_is_as_good_as_f32_arithmetic(hq, hkv, d):
+    # Five terms leave 2^-25 of q and of a weight, below the f32 roundings: a score's is at
+    # most 2^-24 of M a step and far less on average, its shift and 2^x another 2^-22 each.
+    # Their signs are random, so the 2-norm's ratio is one weight's error: under 2^-24 M + 2^-21.
+    cache = paged_cache(31, [5000, 700], 64, hkv, d, "e4m3", width_extra=80)
+    q = queries(32, 2, 1, hq, d)
+    got = call(q, cache, 64, 1 / math.sqrt(d), plan_lens=[5000, 700])
+    k, v = (gathered(p, s, cache[4], [5000, 700], 64, "e4m3") for p, s in
+            ((cache[0], cache[2]), (cache[1], cache[3])))
+    ref, mag = attention_reference(q.double().numpy(), k, v, [5000, 700], 1 / math.sqrt(d), True)
+    for b in range(2):
+        err = np.linalg.norm(got[b] - ref[b]) / np.linalg.norm(ref[b])
+        assert err <= 2.0 ** -24 * mag[b].max() + 2.0 ** -21, (b, err, mag[b].max())
 
 
 @pytest.mark.parametrize("now", [[0, 1000, 5], [1000, 0, 0], [16, 15, 17], [-4, 10 ** 6, 128]])
