@@ -201,11 +201,11 @@ template <int PT> __device__ __forceinline__ void terms(float x, float y, uint32
     c[PT - 1] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
 }
 
-// the length item items of sequence b attend over: the plan's, or the device's,
+// the length the items of entry e, sequence b, attend over: the plan's, or the device's,
 // kept within [0, the plan's]
-__device__ __forceinline__ int len8(const SplitParams &p, int b)
+__device__ __forceinline__ int len8(const SplitParams &p, int e, int b)
 {
-    const int L = p.items.seq_lens[b];
+    const int L = p.items.seq_lens[e];
     return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
 }
 
@@ -219,41 +219,50 @@ __device__ __forceinline__ void put_out(const FusedOut &f, size_t i, float v)
     }
 }
 
-// The (item, tile) sequence of a CTA, the same for every role: items blockIdx.x,
-// blockIdx.x + gridDim.x, ..., each in tiles of T positions, the last one cut at the
-// item's end; items without positions have no tiles and are skipped.
+// item k of this CTA
+__device__ __forceinline__ int64_t item8(int k)
+{
+    return (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// The (item, tile) sequence of a CTA, the same for every role: its items in turn, each in
+// tiles of T positions, the last one cut at the item's end; items without positions have
+// no tiles and are skipped.
 struct Walk8 {
-    int item, b, kvh, s, rg, p0, p1, t0, t1, gt, L;
+    int k, b, kvh, s, rg, p0, p1, t0, t1, gt, L;
     bool done, first;
-    __device__ __forceinline__ void load_item(const SplitParams &p)
+    __device__ __forceinline__ void load_item(const SplitParams &p, const Order8 &od)
     {
-        for (;;) {
+        for (;; ++k) {
+            const int64_t item = item8(k);
+            // in a round that is not full the CTAs at its end have none
             done = item >= p.items.n_items;
             if (done) return;
-            decode_item(p.items, item, b, kvh, s, rg);
-            p0 = s * p.items.chunk[b];
-            L = len8(p, b);
-            p1 = min(L, p0 + p.items.chunk[b]);
+            int e;
+            decode_item(p.items, (int)item, e, kvh, s, rg);
+            b = od.seq[e];
+            p0 = s * p.items.chunk[e];
+            L = len8(p, e, b);
+            p1 = min(L, p0 + p.items.chunk[e]);
             if (p1 > p0) break;
-            item += gridDim.x;
         }
         t0 = p0;
         t1 = tile_end<T>(t0, p1);
         first = true;
     }
-    __device__ __forceinline__ void start(const SplitParams &p)
+    __device__ __forceinline__ void start(const SplitParams &p, const Order8 &od)
     {
-        item = blockIdx.x;
+        k = 0;
         gt = 0;
-        load_item(p);
+        load_item(p, od);
     }
     __device__ __forceinline__ bool last() const { return t1 >= p1; }
-    __device__ __forceinline__ void next(const SplitParams &p)
+    __device__ __forceinline__ void next(const SplitParams &p, const Order8 &od)
     {
         ++gt;
         if (t1 >= p1) {
-            item += gridDim.x;
-            load_item(p);
+            ++k;
+            load_item(p, od);
         } else {
             t0 = t1;
             t1 = tile_end<T>(t0, p1);
@@ -265,7 +274,8 @@ struct Walk8 {
 template <int D, int RP, int QT, int PT>
 __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     gqa_8bit_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                    const __grid_constant__ Scales8 sc, const __grid_constant__ SplitParams p,
+                    const __grid_constant__ Scales8 sc, const __grid_constant__ Order8 od,
+                    const __grid_constant__ SplitParams p,
                     const int e5m2)
 {
     using L = Layout<D, RP, QT, PT>;
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         const int g = lane & 7; // group of its tile
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         int b = -1, kvh = 0, pos = 0;
-        for (int i = 0; i < 4 && !w.done; ++i, w.next(p))
+        for (int i = 0; i < 4 && !w.done; ++i, w.next(p, od))
             if ((lane >> 3) == i && w.t0 + 16 * g < w.t1) {
                 b = w.b;
                 kvh = w.kvh;
@@ -390,7 +400,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         int slot = isv ? 1 : 0;                // slots of tile t: K 2t, V 2t + 1 (mod NS)
         bool ok = true;
         Walk8 w;
-        w.start(p);
+        w.start(p, od);
         int slot0 = 0, blk = look_up(w, slot0);
         const bool scales = L::KSCALE && !isv; // four tiles' scales before the first of them
         Walk8 ws = w;
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 break;
             }
             Walk8 nx = w; // the next tile's blocks are looked up while this one is issued
-            nx.next(p);
+            nx.next(p, od);
             int nslot0 = 0;
             const int nblk = look_up(nx, nslot0);
             // a slot's first use finds its barrier's previous phase complete
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                                             &never);
     } else if (warp == L::SCALE) {
         Walk8 w;
-        w.start(p);
+        w.start(p, od);
         for (int batch = 0; !w.done; ++batch)
             if (!scale_batch(w, batch)) {
                 if (lane == 0) {
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
             int slot = qk ? 0 : 1, items = 0;  // slots of tile t: K 2t, V 2t + 1 (mod NS)
             bool ok = true;
             Walk8 w;
-            for (w.start(p); ok && !w.done; w.next(p)) {
+            for (w.start(p, od); ok && !w.done; w.next(p, od)) {
                 const int ss = w.gt & 1;
                 const uint64_t ad = smem_desc_sw128(sb + L::SLOT_OFF + slot * L::SLOT, 16, 1024);
                 auto wait = [&](int which, uint32_t parity) {
@@ -565,17 +575,18 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         };
         auto look = [&](int k) { // item k by itself; k = -1 past the last
             Item x;
-            const int64_t item = blockIdx.x + (int64_t)k * gridDim.x;
+            const int64_t item = item8(k);
             x.k = item < it.n_items ? k : -1;
             x.b = x.kvh = x.Lb = x.p0 = x.p1 = x.row0 = x.slot = 0;
             if (x.k >= 0) {
-                int s, rg;
-                decode_item(it, (int)item, x.b, x.kvh, s, rg);
-                x.Lb = len8(p, x.b);
-                x.p0 = s * it.chunk[x.b];
-                x.p1 = max(x.p0, min(x.Lb, x.p0 + it.chunk[x.b]));
+                int e, s, rg;
+                decode_item(it, (int)item, e, x.kvh, s, rg);
+                x.b = od.seq[e];
+                x.Lb = len8(p, e, x.b);
+                x.p0 = s * it.chunk[e];
+                x.p1 = max(x.p0, min(x.Lb, x.p0 + it.chunk[e]));
                 x.row0 = rg * per;
-                x.slot = it.split_base[x.b] + s;
+                x.slot = od.slot[e] + s;
             }
             x.R = min(per, rows - x.row0);
             return x;
@@ -1066,7 +1077,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
 
 template <int D, int RP, int QT, int PT>
 cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
-                     const Scales8 &sc, const SplitParams &p, int e5m2)
+                     const Scales8 &sc, const Order8 &od, const SplitParams &p, int e5m2)
 {
     using L = Layout<D, RP, QT, PT>;
     auto *fn = gqa_8bit_kernel<D, RP, QT, PT>;
@@ -1082,7 +1093,7 @@ cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fn, km, vm, sc, p, e5m2);
+    e = cudaLaunchKernelEx(&cfg, fn, km, vm, sc, od, p, e5m2);
     const cudaError_t last = cudaGetLastError();
     return e != cudaSuccess ? e : last;
 }
@@ -1090,19 +1101,20 @@ cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUt
 // The narrowest instantiation that holds the item's rows, with the terms of the output's type.
 template <int D>
 cudaError_t launch_d(int rows, bool out16, int grid, cudaStream_t st, const CUtensorMap &km,
-                     const CUtensorMap &vm, const Scales8 &sc, const SplitParams &p, int e5m2)
+                     const CUtensorMap &vm, const Scales8 &sc, const Order8 &od,
+                     const SplitParams &p, int e5m2)
 {
     if (out16) {
-        if (rows <= 4) return launch_t<D, 4, 4, 4>(grid, st, km, vm, sc, p, e5m2);
-        if (rows <= 8) return launch_t<D, 8, 4, 4>(grid, st, km, vm, sc, p, e5m2);
-        if (rows <= 16) return launch_t<D, 16, 4, 3>(grid, st, km, vm, sc, p, e5m2);
-        if (rows <= 24) return launch_t<D, 24, 4, 3>(grid, st, km, vm, sc, p, e5m2);
-        return launch_t<D, 32, 4, 3>(grid, st, km, vm, sc, p, e5m2);
+        if (rows <= 4) return launch_t<D, 4, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
+        if (rows <= 8) return launch_t<D, 8, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
+        if (rows <= 16) return launch_t<D, 16, 4, 3>(grid, st, km, vm, sc, od, p, e5m2);
+        if (rows <= 24) return launch_t<D, 24, 4, 3>(grid, st, km, vm, sc, od, p, e5m2);
+        return launch_t<D, 32, 4, 3>(grid, st, km, vm, sc, od, p, e5m2);
     }
-    if (rows <= 4) return launch_t<D, 4, 5, 5>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 8) return launch_t<D, 8, 5, 5>(grid, st, km, vm, sc, p, e5m2);
-    if (rows <= 16) return launch_t<D, 16, 5, 5>(grid, st, km, vm, sc, p, e5m2);
-    return launch_t<D, 24, 5, 5>(grid, st, km, vm, sc, p, e5m2);
+    if (rows <= 4) return launch_t<D, 4, 5, 5>(grid, st, km, vm, sc, od, p, e5m2);
+    if (rows <= 8) return launch_t<D, 8, 5, 5>(grid, st, km, vm, sc, od, p, e5m2);
+    if (rows <= 16) return launch_t<D, 16, 5, 5>(grid, st, km, vm, sc, od, p, e5m2);
+    return launch_t<D, 24, 5, 5>(grid, st, km, vm, sc, od, p, e5m2);
 }
 
 } // namespace
@@ -1116,14 +1128,14 @@ int q8_rows_per_item(int rows, int out_dtype)
 
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid, cudaStream_t st,
                             const CUtensorMap &km, const CUtensorMap &vm, const Scales8 &sc,
-                            const SplitParams &p)
+                            const Order8 &od, const SplitParams &p)
 {
     const int rows = p.n_heads / p.items.n_kv_heads;
     const int per = (rows + p.items.row_groups - 1) / p.items.row_groups;
     const int e5m2 = code_dtype == DA_E5M2;
     const bool out16 = out_dtype != DA_F32;
-    if (head_dim == 128) return launch_d<128>(per, out16, grid, st, km, vm, sc, p, e5m2);
-    return launch_d<256>(per, out16, grid, st, km, vm, sc, p, e5m2);
+    if (head_dim == 128) return launch_d<128>(per, out16, grid, st, km, vm, sc, od, p, e5m2);
+    return launch_d<256>(per, out16, grid, st, km, vm, sc, od, p, e5m2);
 }
 
 } // namespace skv

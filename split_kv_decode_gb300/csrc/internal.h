@@ -106,6 +106,14 @@ struct Scales8 {
     int32_t num_blocks;
 };
 
+// Its items: entry e of SplitParams::items is sequence seq[e], the entries in the order of
+// order_by_size; the partials of entry e's first split are in slot slot[e] (the plan's
+// split_base). In every other round the CTAs take items from the last to the first.
+struct Order8 {
+    uint8_t seq[DA_MAX_BATCH];
+    int32_t slot[DA_MAX_BATCH];
+};
+
 struct MlaParams {
     const float *q;          // [B][Hq][576]
     const void *cache;       // latent rows (f32, f16 or bf16): element (b, pos, d) at
@@ -259,7 +267,7 @@ constexpr int kQ8DirectRows = 24; // items of up to so many rows may write the o
 int q8_rows_per_item(int rows, int out_dtype);
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
                             cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
-                            const Scales8 &sc, const SplitParams &p);
+                            const Scales8 &sc, const Order8 &od, const SplitParams &p);
 
 // TMA maps of the SIMT GQA kernel: k and v copy a whole tile of T rows; for a
 // paged pool kb and vb copy box_rows rows, the boxes of a tile that spans a

@@ -68,6 +68,34 @@ def test_plans(lib):
             assert p.workspace_bytes == lib.decode_attn_workspace_bytes(ctypes.byref(p))
 
 
+def test_plan_cost_is_the_makespan_of_items_by_size(lib):
+    # sequences by the length of their items, the longest first; item i is the (i % grid)-th
+    # of its round, odd rounds go from the last CTA to the first
+    import random
+    rnd = random.Random(12)
+    for _ in range(60):
+        batch, hkv = rnd.choice([1, 2, 5, 16, 64, 256]), rnd.choice([1, 2, 4, 8])
+        lens = [int(2 ** rnd.uniform(0, rnd.choice([6, 13, 17]))) for _ in range(batch)]
+        a = args(hkv * 4, hkv, 128, cap=max(lens), batch=batch)
+        a.force_splits = rnd.choice([0, 0, 0, 7])
+        rc, p = plan(lib, a, lens)
+        assert rc == 0
+        load, i = [0] * p.grid, 0
+        for b in sorted(range(batch), key=lambda b: -min(p.chunk[b], lens[b])):
+            for s in range(p.n_splits[b]):
+                for _ in range(hkv):
+                    j = i % p.grid if i // p.grid % 2 == 0 else p.grid - 1 - i % p.grid
+                    load[j] += min(p.chunk[b], lens[b] - s * p.chunk[b]) + 4 * p.tile
+                    i += 1
+        assert i == p.n_items and p.est_cost == max(load)
+
+
+def test_plans_of_ragged_batches_are_balanced(lib):
+    lens = [2999, 17, 1500, 3500, 64, 2048, 777, 1]
+    rc, p = plan(lib, args(16, 16, 128, cap=4096, batch=8), lens)
+    assert rc == 0 and p.est_cost <= 1.3 * (sum(lens) * 16 / 152 + 4 * p.tile)
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(d=64), N.DA_EUNSUPPORTED), (dict(d=576), N.DA_EUNSUPPORTED),
     (dict(hq=129, hkv=1, d=128), N.DA_EUNSUPPORTED), (dict(hq=66, hkv=1, q_len=2), N.DA_EUNSUPPORTED)])
