@@ -983,78 +983,105 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
             }
             // ------------------------------- epilogue -------------------------------
             bool okw = mbar_wait_bounded(bar + B_MFULL, iph, p.timeout_ns, abort_flag);
+            // Lane r works out row r of this warpgroup (all lanes, RPW in turn), while the last
+            // value MMA runs: the reference M of both sets, l under it, and the factor of each
+            // set's O^T (0: the set has nothing, and its O^T may hold anything). A set whose
+            // only scores are NaN has no reference, but a NaN in l.
+            float fl[X], Ml = kNeutralM, ll = 0.f, inv = 1.f;
+            const int lr = lane % RPW, wl = wrow_sm[r00 + lr];
+            {
+                float l2[X];
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    const float *s4 = sum + (x * W + r00 / RPW) * 4 * RPW + lr;
+                    l2[x] = s4[0] + s4[RPW] + s4[2 * RPW] + s4[3 * RPW];
+                    Ml = fmaxf(Ml, ref[x * RP + r00 + lr]);
+                }
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    const float m1 = ref[x * RP + r00 + lr];
+                    fl[x] = X == 1 ? 1.f : m1 == kNeutralM ? l2[x] : ex2(m1 - Ml);
+                    ll = X == 1 ? l2[x] : fmaf(l2[x], fl[x], ll);
+                }
+                if (direct) inv = ll == 0.f ? 0.f : 1.f / ll; // nothing seen: zero; NaN: NaN
+            }
             okw = okw && mbar_wait_bounded(bar + B_OREADY, iph, p.timeout_ns, abort_flag);
             if (bar_or(!okw)) {
                 ab = true;
                 break;
             }
             tc_fence_after();
-            // Row r of this warpgroup: the reference M of both sets, l under it, and the factor of
-            // each set's O^T (0: the set has nothing, and its O^T may hold anything). A set whose
-            // only scores are NaN has no reference, but a NaN in l.
-            auto join = [&](int r, float *f, float &M) {
-                float l2[X], lr = 0.f;
-                M = kNeutralM;
-#pragma unroll
-                for (int x = 0; x < X; ++x) {
-                    const float *s4 = sum + (x * W + r00 / RPW) * 4 * RPW + r;
-                    l2[x] = s4[0] + s4[RPW] + s4[2 * RPW] + s4[3 * RPW];
-                    M = fmaxf(M, ref[x * RP + r00 + r]);
-                }
-#pragma unroll
-                for (int x = 0; x < X; ++x) {
-                    const float m1 = ref[x * RP + r00 + r];
-                    f[x] = X == 1 ? 1.f : m1 == kNeutralM ? l2[x] : ex2(m1 - M);
-                    lr = X == 1 ? l2[x] : fmaf(l2[x], f[x], lr);
-                }
-                return lr;
-            };
             // the sets of warpgroups take the row chunks in turn
 #pragma unroll
             for (int r0 = 0; r0 < RPW; r0 += RC) {
                 if (X > 1 && (r0 / RC) % X != turn) continue;
-                for (int j = 0; j < NCH; ++j) {
-                    const int nan_from = causal ? nan_sm[128 * j + tid] : INT_MAX;
-                    float v[X][PT][RC];
+                float v[NCH][X][PT][RC];
+#pragma unroll
+                for (int j = 0; j < NCH; ++j)
 #pragma unroll
                     for (int x = 0; x < X; ++x)
 #pragma unroll
                         for (int k = 0; k < PT; ++k)
-                            tmem_ld<RC>(tl + 2 * N + (x * NCH + j) * NP + k * RP + r0, v[x][k]);
-                    tmem_wait_ld();
+                            tmem_ld<RC>(tl + 2 * N + (x * NCH + j) * NP + k * RP + r0, v[j][x][k]);
+                tmem_wait_ld();
+                float y[NCH][RC];
+                size_t at[RC];
 #pragma unroll
-                    for (int i = 0; i < RC; ++i) {
-                        const int r = r00 + r0 + i;
-                        float f[X], M, y = 0.f;
-                        const float lr = join(r0 + i, f, M);
+                for (int i = 0; i < RC; ++i) {
+                    at[i] = (wbase + __shfl_sync(0xffffffffu, wl, r0 + i)) * D + tid;
 #pragma unroll
-                        for (int x = 0; x < X; ++x) {
-                            float o = v[x][PT - 1][i];
+                    for (int j = 0; j < NCH; ++j) y[j][i] = 0.f;
 #pragma unroll
-                            for (int k = PT - 2; k >= 0; --k) o = fmaf(o, kTermStep, v[x][k][i]);
-                            if (X == 1) y = o;
-                            else if (f[x] != 0.f) y = fmaf(o, f[x], y);
-                        }
-                        if (r < R) {
-                            if (nan_from != INT_MAX && (row0 + r) / Gh >= nan_from)
-                                y = __int_as_float(0x7fffffff);
-                            const size_t at = (wbase + wrow_sm[r]) * D + 128 * j + tid;
-                            if (direct) // nothing seen: zero; a NaN score: NaN
-                                put_out(p.fused, at, lr == 0.f ? 0.f : y * (1.f / lr));
-                            else
-                                p.acc[at] = y;
+                    for (int x = 0; x < X; ++x) {
+                        const float f = __shfl_sync(0xffffffffu, fl[x], r0 + i);
+#pragma unroll
+                        for (int j = 0; j < NCH; ++j) {
+                            float o = v[j][x][PT - 1][i];
+#pragma unroll
+                            for (int k = PT - 2; k >= 0; --k)
+                                o = fmaf(o, kTermStep, v[j][x][k][i]);
+                            if (f != 0.f) y[j][i] = fmaf(o, f, y[j][i]);
                         }
                     }
+                    if (direct) {
+                        const float n1 = __shfl_sync(0xffffffffu, inv, r0 + i);
+#pragma unroll
+                        for (int j = 0; j < NCH; ++j) y[j][i] = n1 == 0.f ? 0.f : y[j][i] * n1;
+                    }
+                }
+                if (causal)
+#pragma unroll
+                    for (int j = 0; j < NCH; ++j) {
+                        const int from = nan_sm[128 * j + tid];
+#pragma unroll
+                        for (int i = 0; i < RC; ++i)
+                            if (from != INT_MAX && (row0 + r00 + r0 + i) / Gh >= from)
+                                y[j][i] = __int_as_float(0x7fffffff);
+                    }
+                if (QT == 5 || !direct) { // five terms: the output is f32 too
+                    float *dst = direct ? static_cast<float *>(p.fused.out) : p.acc;
+#pragma unroll
+                    for (int i = 0; i < RC; ++i)
+                        if (r00 + r0 + i < R)
+#pragma unroll
+                            for (int j = 0; j < NCH; ++j) dst[at[i] + 128 * j] = y[j][i];
+                } else {
+                    const bool half = p.fused.out_dtype == DA_F16;
+#pragma unroll
+                    for (int i = 0; i < RC; ++i)
+                        if (r00 + r0 + i < R)
+#pragma unroll
+                            for (int j = 0; j < NCH; ++j)
+                                static_cast<uint16_t *>(p.fused.out)[at[i] + 128 * j] =
+                                    half ? __half_as_ushort(__float2half_rn(y[j][i]))
+                                         : __bfloat16_as_ushort(__float2bfloat16_rn(y[j][i]));
                 }
             }
-            if (!direct && turn == 0 && tid < RPW && r00 + tid < R) {
-                float f[X], M;
-                const float lr = join(tid, f, M);
+            if (!direct && turn == 0 && (warp & 3) == 0 && lane < RPW && r00 + lane < R)
                 // a NaN score makes the row NaN whatever the other splits hold
-                p.ml[wbase + wrow_sm[r00 + tid]] =
-                    isnan(lr) ? make_float2(-kNeutralM, 1.f)
-                              : make_float2(lr > 0.f ? M * kLn2 : kNeutralM, lr);
-            }
+                p.ml[wbase + wl] = isnan(ll)
+                                       ? make_float2(-kNeutralM, 1.f)
+                                       : make_float2(ll > 0.f ? Ml * kLn2 : kNeutralM, ll);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_OFREE);
