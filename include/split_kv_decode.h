@@ -609,9 +609,9 @@ typedef struct da_scales_t {
  *     < q_len); nothing is read for them.
  *   - block_table entries of positions below the length must be in
  *     [0, num_blocks); an entry outside reads as zeros.
- *   - When the plan has one split for every sequence and an item at most 24 rows,
- *     the split kernel writes out itself and no combine is launched; otherwise the
- *     combine launch merges (DA_FLAG_ONE_LAUNCH changes nothing).
+ *   - When the plan has one split for every sequence, the split kernel writes out
+ *     itself and no combine is launched; otherwise the combine launch merges
+ *     (DA_FLAG_ONE_LAUNCH changes nothing).
  * Codes past a sequence's length may hold anything, NaN among them. With
  * q_len > 1 a NaN in a new token's row reaches only the tokens that see it.
  * decode_attn_combine, _combine_ranks and _combine_proj take its partials; the

@@ -652,7 +652,7 @@ int launch_8bit(const da_args_t *a, const da_plan_t *pl, const da_dev_t *dev,
     p.box_rows = std::gcd(pl->tile, dev->block_size);
     const int G = a->n_heads / a->n_kv_heads * q_len_of(a), per = q8_rows_per_item(G, a->out_dtype);
     p.items.row_groups = (G + per - 1) / per;
-    *whole = pl->max_splits == 1 && per <= kQ8DirectRows && !(a->flags & DA_FLAG_NO_COMBINE);
+    *whole = pl->max_splits == 1 && !(a->flags & DA_FLAG_NO_COMBINE);
     p.fused = fused_out(a, pl, ws, out);
     p.fused.on = *whole;
     const Scales8 s = {sc->k_scale,      sc->v_scale,       sc->k_block_stride, sc->k_head_stride,

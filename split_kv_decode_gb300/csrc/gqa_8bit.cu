@@ -27,7 +27,7 @@
 //
 // An item is (sequence, KV head, split, row group), rows (query token, head). Roles, one
 // CTA per SM:
-//   softmax warpgroups (1 to 4, up to 8 rows each; on some shapes two sets of them take
+//   softmax warpgroups (1 to 4, up to 8 rows each; for 5 to 8 rows of 128 two of them take
 //              tiles in turn): a thread owns one position of the tile (TMEM lane); the
 //              reference m of a row moves only when a score outgrows it by 2^8 (then O^T is
 //              rescaled), so most tiles take one vote. In the epilogue a thread owns a value
@@ -39,8 +39,7 @@
 //              it beside many softmax warps).
 // Where every sequence has one split there is nothing to merge: the epilogue divides by l
 // and writes the output itself, and no combine follows (256 sequences of 40 positions, 32/8
-// heads: 60 us instead of 72; 128 of 100, 24 heads of 256 over one: 25 instead of 38). Items of
-// more than 24 rows have not the registers for it (their long contexts would take 10% more).
+// heads of 128: 38 us instead of 56; 128 of 100, 32 heads of 256 over one: 9 instead of 28).
 // Every wait is bounded; a wait that runs out sets the status word and the CTA drains
 // and returns.
 #include <climits>
@@ -79,12 +78,12 @@ template <int D, int RP, int QT, int PT> struct Layout {
     static constexpr int NP = (PT * RP + 15) / 16 * 16; // columns of O^T
     static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups a tile
     static constexpr int RPW = RP / W;
-    // 5 to 16 rows of 128 columns: two sets of warpgroups take turns, each with its own
+    // 5 to 8 rows of 128 columns: two sets of warpgroups take turns, each with its own
     // references and its own O^T, joined at the item's end. There a tile's waits, vote, terms
-    // and fences add up to 1800 cycles, the memory side's share to 1400 (8 rows, 1.2M
-    // positions: 72 -> 66 us; 4 rows are no faster for it, 256 columns have twice the time,
-    // and more rows have not the registers).
-    static constexpr int X = D == 128 && (RP == 8 || RP == 16) ? 2 : 1;
+    // and fences add up to 1800 cycles, the memory side's share to 1400 (1.2M positions: 60 us
+    // with one set, 53.6 with two; 4 rows take 52 with either, 16 rows 71 and 74 (64 and 70
+    // with bf16 outputs) for want of registers, and 256 columns have twice the time).
+    static constexpr int X = D == 128 && RP == 8 ? 2 : 1;
     static constexpr int WT = W * X; // softmax warpgroups
     // Warps after the softmax warps. Beside three or four warpgroups the K producer fetches
     // the page scales too: a warp less, a thread has 128 registers and not 96, or 96 and not
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         const int per = (rows + it.row_groups - 1) / it.row_groups;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + r00;
         const bool causal = p.q_len > 1 && !(p.flags & DA_FLAG_NO_CAUSAL);
-        const bool direct = RP <= kQ8DirectRows && p.fused.on; // writes the output itself
+        const bool direct = p.fused.on; // writes the output itself
         uint32_t sph = 0, pfp = 0, iph = 0, scp = 0; // iph: item parity
         bool ab = false;
         int gt = 0;

@@ -263,7 +263,6 @@ cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
 // item holds up to 24 or 32 query rows, by the output's type; larger groups are cut
 // into row groups.
 constexpr int kQ8Tile = 128;
-constexpr int kQ8DirectRows = 24; // items of up to so many rows may write the output themselves
 int q8_rows_per_item(int rows, int out_dtype);
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
                             cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
