@@ -548,7 +548,8 @@ int decode_attn_tables_status(int32_t *state, da_stream_t stream);
  * head_dim and v_dim: multiples of 16, at most 1024.
  */
 typedef struct da_append_t {
-    int32_t n_tokens;     /* rows of k_new, v_new and slot_map; 0: nothing to do  */
+    int32_t n_tokens;     /* rows of k_new, v_new and slot_map, at most 2^30;
+                             0: nothing to do                                    */
     int32_t n_kv_heads;
     int32_t head_dim;
     int32_t v_dim;

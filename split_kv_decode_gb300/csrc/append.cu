@@ -30,7 +30,6 @@ namespace {
 // 8 x 128 bf16 in pages of 16: 128 us; five or eight CTAs: 135 and 134 us)
 constexpr int warps_of(int G) { return G == 8 ? 8 : 4; }
 
-
 struct Side { // keys or values; strides in elements
     const void *src;
     uint8_t *pool;
@@ -411,8 +410,8 @@ extern "C" int decode_attn_append_8bit(const da_append_t *a, const void *k_new, 
                                        float *k_scale, float *v_scale, da_stream_t stream)
 {
     if (!a) return bad("shapes is NULL");
-    if (a->n_tokens < 0 || a->n_kv_heads < 1 || a->n_kv_heads > 65535)
-        return bad("n_tokens must be >= 0 and n_kv_heads in [1, 65535]");
+    if (a->n_tokens < 0 || a->n_tokens > 1 << 30 || a->n_kv_heads < 1 || a->n_kv_heads > 65535)
+        return bad("n_tokens must be in [0, 2^30] and n_kv_heads in [1, 65535]");
     for (int d : {a->head_dim, a->v_dim})
         if (d < 16 || d > 1024 || d % 16)
             return bad("head_dim and v_dim must be multiples of 16 in [16, 1024]");

@@ -237,7 +237,8 @@ def _append(**kw):
     return a
 
 
-@pytest.mark.parametrize("kw", [dict(n_tokens=-1), dict(n_kv_heads=0), dict(head_dim=24),
+@pytest.mark.parametrize("kw", [dict(n_tokens=-1), dict(n_tokens=(1 << 30) + 1),
+                                dict(n_kv_heads=0), dict(head_dim=24),
                                 dict(head_dim=0), dict(v_dim=1040), dict(block_size=0),
                                 dict(num_blocks=0), dict(src_dtype=N.DA_E4M3), dict(src_dtype=9),
                                 dict(code_dtype=N.DA_F16), dict(k_src_stride=4),
