@@ -70,13 +70,16 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE 
               B_N = B_PVDRAIN + 1;
 
 // Shape and shared memory of <D, RP, QT, PT>: RP rows an item at most, QT terms of q, PT of x. A
-// softmax warpgroup takes RPW rows of every tile (8, or 4 when there are no more): a
+// softmax warpgroup takes RPW rows of every tile, 8, or 4 where that is enough: a
 // thread's share of a tile must not outlast the tile's time on the memory side, and 32
-// rows in one thread took 5200 cycles against 2800.
+// rows in one thread took 5200 cycles against 2800. Smaller shares repeat more of a tile's
+// fixed part: 16 rows of 128 as 4 x 4 took 70 us instead of 61 (1.2M positions, bf16), 8
+// rows of 128 as 2 x 4 in one set 58 instead of 53.5; 8 rows of 256, whose tiles take
+// twice the time, 51.7 as 2 x 4 and 53.5 as one 8.
 template <int D, int RP, int QT, int PT> struct Layout {
     static constexpr int N = (QT * RP + 15) / 16 * 16;  // columns of S
     static constexpr int NP = (PT * RP + 15) / 16 * 16; // columns of O^T
-    static constexpr int W = RP > 8 ? RP / 8 : 1; // softmax warpgroups a tile
+    static constexpr int W = RP > 8 ? RP / 8 : RP == 8 && D == 256 ? 2 : 1; // per tile
     static constexpr int RPW = RP / W;
     // 5 to 8 rows of 128 columns: two sets of warpgroups take turns, each with its own
     // references and its own O^T, joined at the item's end. There a tile's waits, vote, terms
@@ -159,13 +162,19 @@ __device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn, bool b_mn, bool a
 // C consecutive 32-bit TMEM columns of this warp's lane quarter
 template <int C> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float *v)
 {
-    static_assert(C == 4, "four columns");
-    uint32_t r[4];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(taddr));
+    static_assert(C == 4 || C == 8, "four or eight columns");
+    uint32_t r[C];
+    if constexpr (C == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < C; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const float *v)
@@ -281,6 +290,9 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW,
                   X = L::X, WT = L::WT;
     constexpr int RC = 4; // rows taken from TMEM at a time
+    // and of the scores: 8 at a time save a round trip where they fit the registers (16 rows
+    // of 128, 1.2M positions: 63 -> 60.5 us; 8 and 24 rows spill and lose 1%)
+    constexpr int SC = RP == 16 ? RPW : RC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -763,16 +775,20 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                     continue;
                 }
                 const int own = X > 1 ? gt >> 1 : gt; // number of this set's tile
-                bool okw = true;
-                if ((gt & 3) == turn) {
-                    okw = mbar_wait_bounded(bar + B_SCFULL + half, (scp >> half) & 1u, p.timeout_ns,
-                                            abort_flag);
-                    scp ^= 1u << half;
-                }
-                okw = okw && mbar_wait_bounded(bar + B_SFULL + ss, (sph >> ss) & 1u, p.timeout_ns,
-                                               abort_flag);
-                okw = okw && mbar_wait_bounded(bar + B_PFREE + ss, ((pfp >> ss) & 1u) ^ 1u,
-                                               p.timeout_ns, abort_flag);
+                // the three barriers are looked at together (a look takes 110 cycles) and waited
+                // for where they are not through
+                const uint32_t sc_par = (scp >> half) & 1u, s_par = (sph >> ss) & 1u,
+                               pf_par = ((pfp >> ss) & 1u) ^ 1u;
+                const bool sc_in = (gt & 3) != turn || mbar_test(bar + B_SCFULL + half, sc_par),
+                           s_in = mbar_test(bar + B_SFULL + ss, s_par),
+                           p_free = mbar_test(bar + B_PFREE + ss, pf_par);
+                bool okw = sc_in || mbar_wait_bounded(bar + B_SCFULL + half, sc_par, p.timeout_ns,
+                                                      abort_flag);
+                okw = okw && (s_in || mbar_wait_bounded(bar + B_SFULL + ss, s_par, p.timeout_ns,
+                                                        abort_flag));
+                okw = okw && (p_free || mbar_wait_bounded(bar + B_PFREE + ss, pf_par, p.timeout_ns,
+                                                          abort_flag));
+                if ((gt & 3) == turn) scp ^= 1u << half;
                 sph ^= 1u << ss;
                 pfp ^= 1u << ss;
                 const bool short_tile = t1 - t0 < T, new_tokens = t1 > lim0;
@@ -814,14 +830,14 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 float a[RPW];
                 auto scores = [&](bool less) {
 #pragma unroll
-                    for (int r0 = 0; r0 < RPW; r0 += RC) {
-                        float v[QT][RC];
+                    for (int r0 = 0; r0 < RPW; r0 += SC) {
+                        float v[QT][SC];
 #pragma unroll
                         for (int j = 0; j < QT; ++j)
-                            tmem_ld<RC>(tl + ss * N + j * RP + r0, v[j]);
+                            tmem_ld<SC>(tl + ss * N + j * RP + r0, v[j]);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < RC; ++i) {
+                        for (int i = 0; i < SC; ++i) {
                             float y = v[QT - 1][i];
 #pragma unroll
                             for (int j = QT - 2; j >= 0; --j) y = fmaf(y, kTermStep, v[j][i]);
@@ -931,8 +947,8 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                     } else {
 #pragma unroll
                         for (int r = 0; r < RPW; r += 2) {
-                            sts_u8(pt + swz(j * RP + r, tid), c[r / 2][j] & 0xff);
-                            sts_u8(pt + swz(j * RP + r + 1, tid), c[r / 2][j] >> 8);
+                            sts_u8(pt + swz(j * RP + r00 + r, tid), c[r / 2][j] & 0xff);
+                            sts_u8(pt + swz(j * RP + r00 + r + 1, tid), c[r / 2][j] >> 8);
                         }
                     }
                 }
@@ -940,11 +956,11 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 firsttile = false;
-                if (lane == 0) {
-                    mbar_arrive(bar + B_SFREE + ss);
-                    mbar_arrive(bar + B_PFULL + ss);
-                    if ((gt & 3) == (X > 1 ? 2 + turn : 3)) mbar_arrive(bar + B_SCFREE + half);
-                }
+                // lanes 0 to 2: S and (after four tiles) the scales are read, x is written
+                if (lane < ((gt & 3) == (X > 1 ? 2 + turn : 3) ? 3 : 2))
+                    mbar_arrive(bar + (lane == 0   ? B_SFREE + ss
+                                       : lane == 1 ? B_PFULL + ss
+                                                   : B_SCFREE + half));
                 if ((vslot += 2) >= NS) {
                     vslot -= NS;
                     vph ^= 1u;
