@@ -159,6 +159,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load the built library; raises if it is missing (there is no fallback)."""
     global _lib
+    if _lib is not None:     # set once, when it is complete
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

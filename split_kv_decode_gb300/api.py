@@ -301,7 +301,7 @@ def _launch(dev: torch.device, stream, fn, *args) -> None:
         handle = torch._C._cuda_getCurrentRawStream(dev.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():    # (a CUDA tensor is there: initialised)
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
