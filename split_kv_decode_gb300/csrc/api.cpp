@@ -857,7 +857,13 @@ int decode_attn_plan(const da_args_t *a, const int32_t *lens, int num_sms, da_pl
     // 24 ragged batches, geometric mean with 2, 3, 4 and 6: 19.3, 19.2, 19.1 and 19.0 us,
     // 6 up to 5% worse for groups of 1 to 4 rows)
     const bool q8 = kc.kernel == DA_KERNEL_GQA_8BIT;
-    const PlanRule rule = {(q8 ? 4 : 3) * (int64_t)kc.tile, q8};
+    // Its one-split plans need no combine, whose 2.2 to 2.9 us are four tiles' time (4 sequences
+    // of 300 positions: 5.9 us in one split, 6.9 in three; one of 713: 7.4, and 6.7 in six), and
+    // 1 ns more for every row of the batch (24 batches of 16 to 128 sequences, geometric mean
+    // with 0, 1, 2 and 4 ns: 31.8, 31.4, 31.4 and 32.3 us).
+    const bool merged = q8 && !(a->flags & DA_FLAG_NO_COMBINE);
+    const PlanRule rule = {(q8 ? 4 : 3) * (int64_t)kc.tile, q8,
+                           merged ? 4 * kc.tile + (int64_t)a->batch * rows_of(a) / 5 : 0};
     const int prc = plan_splits(lens, a->batch, a->n_kv_heads * kc.row_groups, kc.tile, slots,
                                 a->force_splits, 1 << 22, rule, &po);
     if (prc == 1) return fail(DA_EINVAL, "plan", "invalid lengths");

@@ -175,6 +175,7 @@ int plan_splits(const int32_t *lens, int batch, int hkv, int tile, int slots, in
         cost_of[i] = simulate(lens, batch, hkv, &cand[i * (size_t)batch], slots, rule,
                               &items_of[i], diff);
         if (items_of[i] > max_items) continue;
+        if (items_of[i] > (int64_t)batch * hkv) cost_of[i] += rule.combine;
         if (min_cost < 0 || cost_of[i] < min_cost) min_cost = cost_of[i];
     }
     // the fewest items whose makespan is within 0.5% of the best one
@@ -193,6 +194,7 @@ int plan_splits(const int32_t *lens, int batch, int hkv, int tile, int slots, in
     out->n_items = (int32_t)items_of[best];
     out->grid = (int32_t)std::min<int64_t>(items_of[best], slots);
     out->est_cost = cost_of[best];
+    if (items_of[best] > (int64_t)batch * hkv) out->est_cost -= rule.combine; // the split's own
     return 0;
 }
 

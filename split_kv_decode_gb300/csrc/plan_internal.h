@@ -20,6 +20,7 @@ struct PlanRule {
     // false: sequences as they stand, item i to CTA i % grid. true: sequences in the order
     // of order_by_size, every other round of grid items from the last CTA to the first.
     bool by_size;
+    int64_t combine; // what a combine costs where some sequence has several splits, in positions
 };
 
 // The sequences by the length of their items, the longest first (equal ones as they stand).

@@ -578,7 +578,8 @@ def test_refusals_of_the_binding():
 
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("hq,hkv,T", [(8, 2, 1), (16, 2, 1), (5, 1, 4), (40, 1, 1), (24, 1, 2)])
+@pytest.mark.parametrize("hq,hkv,T", [(8, 2, 1), (16, 2, 1), (5, 1, 4), (40, 1, 1), (24, 1, 2),
+                                      (32, 1, 1)])
 def test_one_split_a_sequence_writes_the_same_bits_as_the_combine(hq, hkv, T, out):
     # lengths of zero, and tokens before the start, among them
     now = [40, 0, 129, 2, 128, 0, 300, 1]

@@ -90,6 +90,18 @@ def test_plan_cost_is_the_makespan_of_items_by_size(lib):
         assert i == p.n_items and p.est_cost == max(load)
 
 
+@pytest.mark.parametrize("lens,hkv,splits", [([256], 4, 1), ([300] * 4, 2, 1), ([713], 2, 6),
+                                             ([4096], 2, 32), ([1024] * 8, 8, 1)])
+def test_plans_count_the_combine(lib, lens, hkv, splits):
+    # four tiles for the combine that a plan of several splits needs
+    a = args(4 * hkv, hkv, 128, cap=max(lens), batch=len(lens))
+    rc, p = plan(lib, a, lens)
+    assert rc == 0 and p.max_splits == splits
+    a.flags = N.DA_FLAG_NO_COMBINE           # the partials are wanted: no call is saved
+    rc, p = plan(lib, a, lens)
+    assert rc == 0 and p.max_splits > 1
+
+
 def test_plans_of_ragged_batches_are_balanced(lib):
     lens = [2999, 17, 1500, 3500, 64, 2048, 777, 1]
     rc, p = plan(lib, args(16, 16, 128, cap=4096, batch=8), lens)
