@@ -20,6 +20,8 @@ namespace skv {
 int set_error(int code, const char *phase, const char *msg); // api.cpp
 }
 
+using skv::griddep_launch_dependents;
+using skv::griddep_wait;
 using skv::named_bar_sync;
 
 namespace {
@@ -230,6 +232,8 @@ template <typename ST, __nv_fp8_interpretation_t F, int G>
 __global__ void __launch_bounds__(32 * warps_of(G), G == 8 ? 4 : 7)
     append_kernel(const __grid_constant__ AppendParams p)
 {
+    griddep_launch_dependents(); // the attention that follows may set itself up meanwhile
+    griddep_wait();
     constexpr int TG = 32 * G, kWarps = warps_of(G);
     __shared__ float red[2][kWarps], red_finite[2][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -383,8 +387,7 @@ cudaError_t launch_g(AppendParams &p, cudaStream_t st)
     const int64_t tasks = (p.tokens + (int64_t)p.chunk - 1) / p.chunk * lanes;
     const int64_t grid = (tasks * G + kWarps - 1) / kWarps;
     if (tasks + kWarps > INT32_MAX) return cudaErrorInvalidValue; // 32-bit task numbers
-    append_kernel<ST, F, G><<<(unsigned)grid, 32 * kWarps, 0, st>>>(p);
-    return cudaGetLastError();
+    return skv::launch_after(append_kernel<ST, F, G>, (unsigned)grid, 32 * kWarps, st, p);
 }
 
 template <typename ST, __nv_fp8_interpretation_t F>

@@ -264,6 +264,27 @@ cudaError_t launch_gqa_tc(int kv_dtype, int head_dim, int grid, cudaStream_t st,
 // into row groups.
 constexpr int kQ8Tile = 128;
 int q8_rows_per_item(int rows, int out_dtype);
+
+// Launches kernel(param) so that it may start while the stream's last kernel still runs (a
+// programmatic launch): the kernel waits for that one (griddep_wait) before anything else.
+template <typename P>
+cudaError_t launch_after(void (*kernel)(P), unsigned grid, unsigned threads, cudaStream_t st,
+                         const P &param)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, param);
+    const cudaError_t last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
+}
+
 cudaError_t launch_gqa_8bit(int code_dtype, int out_dtype, int head_dim, int grid,
                             cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
                             const Scales8 &sc, const Order8 &od, const SplitParams &p);
