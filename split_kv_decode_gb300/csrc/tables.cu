@@ -248,7 +248,7 @@ extern "C" int decode_attn_grow_tables(const da_tables_t *t, const int32_t *new_
     p.wide = reinterpret_cast<uintptr_t>(slot_map) % 16 == 0;
     // Few slots: one a lane, so that their look-ups go side by side (a decode step's are of
     // different sequences); many (over one a thread of the GPU): four, which share a look-up
-    // where they lie in one block (2.1M slots of 256 prompts: 9.4 us; one a lane 11.1). CTAs
+    // where they lie in one block (2.1M slots of 256 prompts: 8.9 us; one a lane 2 more). CTAs
     // for the most that the call may have to write: the slots, or the free list's entries of
     // released blocks, 1024 a CTA; at most four an SM.
     const int per = slot_capacity > 152 * 4 * kThreads ? 4 : 1;
