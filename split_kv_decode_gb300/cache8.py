@@ -67,6 +67,7 @@ class PagedCache8:
                                         self.state, block_size)
         self.dev = A.make_dev(seq_lens=self.seq_lens, block_table=self.block_table,
                               k_pool=self.k, v_pool=self.v)
+        self._shapes = self._append = None   # of the last append's rows; shapes only
 
     def grow(self, new_lens: torch.Tensor, stream=None) -> torch.Tensor:
         """Give sequence b new_lens[b] tokens (int32 [max_batch] on the device, 0: none,
@@ -79,8 +80,14 @@ class PagedCache8:
         max_new, and at least the tokens that grow() gave (rows past them are skipped)."""
         if k_new.dim() != 3 or k_new.shape[0] > self.slot_map.numel():
             raise ValueError(f"new rows must be [T, Hkv, D] with T <= {self.slot_map.numel()}")
-        a = A.make_append(k_new, v_new, self.k, self.v, self.k_scale, self.v_scale)
-        A.decode_attn_append_8bit(a, k_new, v_new, self.slot_map[:k_new.shape[0]], self.k, self.v,
+        shapes = (k_new.shape, v_new.shape, k_new.stride(), v_new.stride(), k_new.dtype,
+                  v_new.dtype)
+        if shapes != self._shapes:
+            self._append = A.make_append(k_new, v_new, self.k, self.v, self.k_scale, self.v_scale)
+            self._shapes = shapes
+        slots, n = self.slot_map, k_new.shape[0]
+        A.decode_attn_append_8bit(self._append, k_new, v_new,
+                                  slots if n == slots.numel() else slots[:n], self.k, self.v,
                                   self.k_scale, self.v_scale, stream)
 
     def check(self, stream=None) -> None:

@@ -15,10 +15,10 @@
 // The other operand of an 8-bit MMA is 8-bit too. q and x are split into e4m3 terms,
 // y = y_0 + 2^-4 y_1 + 2^-8 y_2 + ...: a term rounds what the ones before it left, and
 // each takes 5 bits off (4 significant bits and the sign of the rest). f32 outputs take
-// five terms of both, 25 bits; 16-bit ones four of q, 20 bits, and four of x, or three, 15 bits,
-// in items of more than 8 rows (2^-14 of a weight at most, against 2^-9 and 2^-12 of the
-// output's rounding). Four of both
-// left an error of 0.4 to 1.4e-6 in f32 outputs, as much as or more than f32 arithmetic does.
+// five terms of both, 25 bits: four of both left an error of 0.4 to 1.4e-6 there, as much as
+// or more than f32 arithmetic does. 16-bit outputs take four of q, 20 bits, and four of x, or
+// three, 15 bits, in items of more than 8 rows (2^-14 of a weight at most, against 2^-9 and
+// 2^-12 of the output's rounding).
 // y is scaled to at most 256, so that e4m3's least step, 2^-9, is 2^-25 to 2^-33 of the
 // largest in the last term. The terms are columns of the MMA (N = terms x rows, rounded to
 // 16), whose time for N <= 64 is that of reading the tile (46 to 48 cycles per 32-byte step);

@@ -107,6 +107,28 @@ def test_layers_share_the_tables():
         PagedCache8(2, 10, 4, 2, 128, block_size=32, tables_of=a)
 
 
+def test_rows_of_changing_shapes_strides_and_types():
+    cache = PagedCache8(3, 24, 8, 2, 128, block_size=16, max_new=12)
+    fused = torch.randn(9, 5, 2, 128, device="cuda")
+    rows = [(fused[:, 0], fused[:, 1]), (fused[:, 1], fused[:, 3]),
+            (fused[:, 2].contiguous(), fused[:, 4].contiguous()),
+            (fused[:3, 0].half(), fused[:3, 1].half()), (fused[:3, 2], fused[:3, 0]),
+            (fused[:3, 0].bfloat16(), fused[:3, 1].bfloat16()),
+            (torch.cat([fused, fused[:3]])[:, 0], torch.cat([fused, fused[:3]])[:, 1])]
+    want = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    for k, v in rows:
+        n = k.shape[0] // 3
+        slots = cache.grow(torch.full((3,), n, dtype=torch.int32, device="cuda"))
+        cache.append(k, v)
+        A.decode_attn_append_8bit(A.make_append(k, v, *want), k, v, slots[:3 * n].clone(), *want)
+        for got, ref in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), want):
+            assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
+    with pytest.raises(ValueError):
+        cache.append(rows[0][0], rows[0][1][:3])
+    with pytest.raises(ValueError):
+        cache.append(fused[:, 0, :, ::2], fused[:, 1, :, ::2])
+
+
 def test_a_step_that_finds_no_blocks_leaves_the_cache_as_it_was():
     c = PagedCache8(2, 3, 4, 1, 128, block_size=16, max_new=64)
     x = torch.randn(64, 1, 128, device="cuda")
