@@ -349,33 +349,39 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     griddep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
-    // A whole warp: the page scales of the next four tiles of w, for groups of 16 positions.
-    // Batches take two buffers in turn; false when the wait for one runs out.
-    auto scale_batch = [&](Walk8 &w, int batch) {
-        const int g = lane & 7; // group of its tile
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        int b = -1, kvh = 0, pos = 0;
+    // A whole warp: the page scales of four tiles at a time (a batch), a lane a group of 16
+    // positions. The blocks of a batch are looked up a batch ahead of its scales, and those
+    // a batch ahead of their use, so that neither load is waited for. Batches take two buffers
+    // in turn.
+    struct Batch {
+        int blk, kvh;  // of the next batch: this lane's block (-1: none)
+        float ks, vs;  // of this batch
+    };
+    auto blocks = [&](Walk8 &w, Batch &x) {
+        int b = -1, pos = 0;
         for (int i = 0; i < 4 && !w.done; ++i, w.next(p, od))
-            if ((lane >> 3) == i && w.t0 + 16 * g < w.t1) {
+            if ((lane >> 3) == i && w.t0 + 16 * (lane & 7) < w.t1) {
                 b = w.b;
-                kvh = w.kvh;
-                pos = w.t0 + 16 * g;
+                x.kvh = w.kvh;
+                pos = w.t0 + 16 * (lane & 7);
             }
-        if (b >= 0) {
-            const int blk = p.block_table[(size_t)b * p.max_blocks + pos / p.block_size];
-            float vs = 0.f;
-            if (blk >= 0 && blk < sc.num_blocks) {
-                v.x = __ldg(sc.k + blk * sc.k_block + kvh * sc.k_head);
-                vs = __ldg(sc.v + blk * sc.v_block + kvh * sc.v_head);
-            }
-            v.z = fmaxf(vs, kMinScale);
-            v.y = __log2f(v.z);
+        x.blk = b < 0 ? -1 : p.block_table[(size_t)b * p.max_blocks + pos / p.block_size];
+    };
+    auto scales = [&](Batch &x) {
+        x.ks = x.vs = 0.f;
+        if (x.blk >= 0 && x.blk < sc.num_blocks) {
+            x.ks = __ldg(sc.k + x.blk * sc.k_block + x.kvh * sc.k_head);
+            x.vs = __ldg(sc.v + x.blk * sc.v_block + x.kvh * sc.v_head);
         }
+    };
+    // false when the wait for the buffer runs out
+    auto put_scales = [&](const Batch &x, int batch) {
         const int half = batch & 1;
         const bool got = mbar_wait_bounded(bar + B_SCFREE + half, ((uint32_t)(batch >> 1) & 1u) ^ 1u,
                                            p.timeout_ns, abort_flag);
         if (__any_sync(0xffffffffu, !got)) return false;
-        sc_sm[half * 32 + lane] = v;
+        const float vs = fmaxf(x.vs, kMinScale);
+        sc_sm[half * 32 + lane] = make_float4(x.ks, __log2f(vs), vs, 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + B_SCFULL + half);
         return true;
@@ -413,13 +419,15 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         Walk8 w;
         w.start(p, od);
         int slot0 = 0, blk = look_up(w, slot0);
-        const bool scales = L::KSCALE && !isv; // four tiles' scales before the first of them
+        const bool with_scales = L::KSCALE && !isv;
         Walk8 ws = w;
+        Batch sb = {};
+        if (with_scales) {
+            blocks(ws, sb);
+            scales(sb);
+            blocks(ws, sb);
+        }
         while (!w.done) {
-            if (scales && (w.gt & 3) == 0 && !scale_batch(ws, w.gt >> 2)) {
-                ok = false;
-                break;
-            }
             Walk8 nx = w; // the next tile's blocks are looked up while this one is issued
             nx.next(p, od);
             int nslot0 = 0;
@@ -446,6 +454,14 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                                     slot0, blk, pol);
                 }
             }
+            if (with_scales && (w.gt & 3) == 0) { // four tiles' scales, behind the first of them
+                if (!put_scales(sb, w.gt >> 2)) {
+                    ok = false;
+                    break;
+                }
+                scales(sb);
+                blocks(ws, sb);
+            }
             if ((slot += 2) >= NS) {
                 slot -= NS;
                 ph ^= 1u;
@@ -467,14 +483,23 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     } else if (warp == L::SCALE) {
         Walk8 w;
         w.start(p, od);
-        for (int batch = 0; !w.done; ++batch)
-            if (!scale_batch(w, batch)) {
+        Batch sb = {};
+        bool here = !w.done; // this batch has tiles
+        blocks(w, sb);
+        scales(sb);
+        for (int batch = 0; here; ++batch) {
+            const bool more = !w.done;
+            blocks(w, sb);
+            if (!put_scales(sb, batch)) {
                 if (lane == 0) {
                     *abort_flag = 1;
                     atomicCAS(p.status, 0, kStatusTimeoutQ8);
                 }
                 break;
             }
+            scales(sb);
+            here = more;
+        }
     } else if (warp == L::QK || warp == L::PV) {
         // ================ MMA issue: one thread for S, one for O^T ================
         // Two issuers, so that neither polls for the other's inputs.
