@@ -350,8 +350,8 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
     // A whole warp: the page scales of four tiles at a time (a batch), a lane a group of 16
-    // positions. The blocks of a batch are looked up a batch ahead of its scales, and those
-    // a batch ahead of their use, so that neither load is waited for. Batches take two buffers
+    // positions. The K producer looks the blocks of a batch up a batch ahead of its scales, and
+    // those a batch ahead of their use, so that it waits for neither. Batches take two buffers
     // in turn.
     struct Batch {
         int blk, kvh;  // of the next batch: this lane's block (-1: none)
@@ -484,12 +484,9 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         Walk8 w;
         w.start(p, od);
         Batch sb = {};
-        bool here = !w.done; // this batch has tiles
-        blocks(w, sb);
-        scales(sb);
-        for (int batch = 0; here; ++batch) {
-            const bool more = !w.done;
+        for (int batch = 0; !w.done; ++batch) { // (this warp has the time to wait for the loads)
             blocks(w, sb);
+            scales(sb);
             if (!put_scales(sb, batch)) {
                 if (lane == 0) {
                     *abort_flag = 1;
@@ -497,8 +494,6 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 }
                 break;
             }
-            scales(sb);
-            here = more;
         }
     } else if (warp == L::QK || warp == L::PV) {
         // ================ MMA issue: one thread for S, one for O^T ================
