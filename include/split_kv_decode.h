@@ -589,7 +589,10 @@ int decode_attn_append_8bit(const da_append_t *shapes, const void *k_new, const 
 
 /* The scales of 8-bit pools, strides in elements: (block, head) at base + block *
  * *_block_stride + head * *_head_stride. Any finite positive f32 from 2^-100
- * to 2^120 (smaller value scales, zero among them, count as 2^-100). */
+ * to 2^120 (smaller value scales, zero among them, count as 2^-100). Value scales of
+ * one sequence and head may differ by all of that: a page holds its share of the
+ * probabilities whatever its scale is, and values of a page more than 2^32 below
+ * another are off by 2^-50 of the other's at most. */
 typedef struct da_scales_t {
     const float *k_scale;
     const float *v_scale;

@@ -4,11 +4,15 @@
 // stand for code * scale[i][head]. With page scales ks, vs (lv = log2 vs) and
 // scores in log2 units,
 //     s[r][pos]  = ks[page] * sum_d q[r][d] Kc[pos][d]        (q times scale * log2 e)
-//     x[r][pos]  = 2^(s - m[r]) * vs[page],  m[r] about the largest s + lv
+//     x[r][pos]  = 2^(s - m[r]) * vs[page] / V,  m[r] about the largest s + lv - log2 V
 //     acc[r][d]  = sum_pos x[r][pos] Vc[pos][d],   l[r] = sum_pos 2^(s - m[r])
-// so the value scales fold into the exponent and the codes go to the tensor cores
+// so the value scales fold into the weights and the codes go to the tensor cores
 // as they stand: TMA brings 128-position tiles of K and of V into shared memory
 // in the 128-byte swizzle the MMA reads, and nothing converts or re-reads them.
+// V is about the largest value scale of the item so far, a power of two: with it l stays
+// near 1 whatever the scales are (pages of zeros have 2^-100, others up to 2^120), and
+// neither l nor x leaves the range of an f32. References and V are even powers of two, so
+// that moving them multiplies by an exact power, in two halves where one would underflow.
 //     S[pos][(j, r)]  = sum_d Kc[pos][d] q_j[r][d]      (M = 128 positions, K = D)
 //     O^T[d][(j, r)] += sum_pos Vc[pos][d] x_j[r][pos]  (M = 128 value columns, K = 128)
 //
@@ -58,6 +62,9 @@ constexpr int T = kQ8Tile;
 constexpr float kTermStep = 1.f / 16.f;
 constexpr float kHead = 4.f; // m is this much below the maximum that set it
 constexpr float kTau = 8.f;  // and moves when a score is this much above it
+constexpr float kWide = 16.f; // log2 V moves when a page's is this much above it
+constexpr float kLeast = -32.f; // and pages further below it count as this far in a reference:
+                                // 2^(s - m) stays below 2^(8 + 32)
 constexpr int kMaxSlots = 12;
 constexpr float kMinScale = 7.8886090522101181e-31f; // 2^-100
 
@@ -107,12 +114,13 @@ template <int D, int RP, int QT, int PT> struct Layout {
     static constexpr int P_OFF = Q_OFF + NCH * QCH;
     static constexpr int SLOT_OFF = (P_OFF + 2 * PSLOT + 1023) / 1024 * 1024;
     // after the slots: barriers, flags, page scales (2 batches of 4 tiles of 8 groups of
-    // 16 positions), per-row tables (of two items), warp maxima, sums and references (of
-    // two items), flags, columns with a NaN (of two items)
+    // 16 positions), per-row tables (of two items), warp maxima, sums, references and log2 V
+    // (of two items), flags, columns with a NaN (of two items)
     static constexpr int BAR = 0, MISC = BAR + B_N * 8, SC = (MISC + 16 + 15) / 16 * 16,
                          ROW = SC + 2 * 4 * 8 * 16,
                          RED = ROW + 2 * 3 * RP * 4, SUM = RED + 4 * RP * X * 4,
-                         REF = SUM + 2 * 4 * RP * X * 4, BAD = REF + 2 * RP * X * 4,
+                         REF = SUM + 2 * 4 * RP * X * 4, LGV = REF + 2 * RP * X * 4,
+                         BAD = LGV + 2 * X * 4,
                          NANC = BAD + 2 * WT * 4,
                          TAIL = NANC + 2 * D * 4;
     static constexpr int SLOTS_FIT = (232448 - 1024 - SLOT_OFF - TAIL) / SLOT;
@@ -209,6 +217,9 @@ template <int PT> __device__ __forceinline__ void terms(float x, float y, uint32
     c[PT - 1] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
 }
 
+// 2^k, k in [-126, 127]
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
+
 // the length the items of entry e, sequence b, attend over: the plan's, or the device's,
 // kept within [0, the plan's]
 __device__ __forceinline__ int len8(const SplitParams &p, int e, int b)
@@ -301,13 +312,15 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(tail + L::BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + L::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + L::MISC + 4);
-    float4 *sc_sm = reinterpret_cast<float4 *>(tail + L::SC); // (ks, log2 vs, vs) of 16 positions
+    // of 16 positions: (ks, log2 vs, vs, the largest log2 vs of the tile rounded down to even)
+    float4 *sc_sm = reinterpret_cast<float4 *>(tail + L::SC);
     // per row, of items in turn: 1 / (q's scaling), positions seen (below lim), workspace row
     float *const qf2 = reinterpret_cast<float *>(tail + L::ROW);
     int *const lim2 = reinterpret_cast<int *>(qf2 + 2 * RP), *const wrow2 = lim2 + 2 * RP;
     float *red_sm = reinterpret_cast<float *>(tail + L::RED); // maxima, [4 WT warps][RPW]
     float *sum_sm = reinterpret_cast<float *>(tail + L::SUM); // l, [2 items][4 WT warps][RPW]
     float *ref_sm = reinterpret_cast<float *>(tail + L::REF); // m, [2 items][X][RP]
+    float *lgv_sm = reinterpret_cast<float *>(tail + L::LGV); // log2 V, [2 items][X]
     volatile int *bad_sm = reinterpret_cast<volatile int *>(tail + L::BAD); // [WT][tile parity]
     int *const nan2 = reinterpret_cast<int *>(tail + L::NANC); // first token that sees a NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -380,8 +393,11 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         const bool got = mbar_wait_bounded(bar + B_SCFREE + half, ((uint32_t)(batch >> 1) & 1u) ^ 1u,
                                            p.timeout_ns, abort_flag);
         if (__any_sync(0xffffffffu, !got)) return false;
-        const float vs = fmaxf(x.vs, kMinScale);
-        sc_sm[half * 32 + lane] = make_float4(x.ks, __log2f(vs), vs, 0.f);
+        const float vs = fmaxf(x.vs, kMinScale), lv = __log2f(vs);
+        float top = lv; // over the tile's 8 lanes
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sc_sm[half * 32 + lane] = make_float4(x.ks, lv, vs, 2.f * floorf(0.5f * top));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + B_SCFULL + half);
         return true;
@@ -781,6 +797,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 m[r] = kNeutralM; // none yet
                 l[r] = 0.f;
             }
+            float lgv = 0.f, inv_v = 1.f; // log2 V, 1 / V (uniform over the warpgroup)
             const int lim0 = causal ? Lb - p.q_len + 1 : INT_MAX; // the first token's limit
             bool firsttile = true;
             for (int t0 = p0, t1; t0 < p1; t0 = t1, ++gt) {
@@ -878,10 +895,19 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 // barrier, read after it, so the warpgroup leaves together). An item's first tile
                 // always sets references.
                 if (!okw) bad_sm[2 * wg + (own & 1)] = 1;
-                bool ex = firsttile;
+                // V first: the same for the whole warpgroup
+                const bool wider = firsttile || sv.w > lgv + kWide;
+                float half_v = 1.f; // sqrt(old V / new V)
+                if (wider) {
+                    if (!firsttile) half_v = pow2(max(-126, (int)(0.5f * (lgv - sv.w))));
+                    lgv = sv.w;
+                    inv_v = pow2(-(int)lgv);
+                }
+                const float lv = fmaxf(sv.y - lgv, kLeast), vs = sv.z * inv_v;
+                bool ex = wider;
                 if (!firsttile) {
                     scores(true);
-                    const float most = kTau - sv.y;
+                    const float most = kTau - lv;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) ex |= a[r] > most;
                     ex = bar_or(ex || !okw);
@@ -892,7 +918,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
                         // as ordered integers; a NaN counts as -inf
-                        const int u = __float_as_int(fmaxf(a[r] + sv.y, -INFINITY));
+                        const int u = __float_as_int(fmaxf(a[r] + lv, -INFINITY));
                         const int o = __reduce_max_sync(0xffffffffu, u ^ ((u >> 31) & 0x7fffffff));
                         if (lane == 0)
                             red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
@@ -902,18 +928,23 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                         ab = true;
                         break;
                     }
-                    float al[RPW];
+                    float al[RPW]; // square roots of the factors, exact
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
                         const float tm = fmaxf(fmaxf(red[r], red[RPW + r]),
                                                fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
-                        const float mn = tm > m[r] + kTau ? tm - kHead : m[r];
-                        al[r] = ex2(m[r] - mn);
-                        l[r] *= al[r];
+                        const float mn = tm > m[r] + kTau ? 2.f * floorf(0.5f * (tm - kHead)) : m[r];
+                        al[r] = m[r] - mn;
                         m[r] = mn;
                         a[r] -= mn;
                     }
                     if (!firsttile) { // the set's last PV is done with O^T before it is rescaled
+#pragma unroll
+                        for (int r = 0; r < RPW; ++r) {
+                            al[r] = pow2(max(-126, (int)(0.5f * al[r])));
+                            l[r] = l[r] * al[r] * al[r];
+                            al[r] *= half_v;
+                        }
                         okw = mbar_wait_bounded(bar + B_PVDONE + turn, (uint32_t)(own - 1) & 1u,
                                                 p.timeout_ns, abort_flag);
                         if (bar_or(!okw)) {
@@ -937,7 +968,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
 #pragma unroll
                                 for (int e = 0; e < two; ++e) {
 #pragma unroll
-                                    for (int r = 0; r < RPW; ++r) o[e][r] *= al[r];
+                                    for (int r = 0; r < RPW; ++r) o[e][r] = o[e][r] * al[r] * al[r];
 #pragma unroll
                                     for (int r0 = 0; r0 < RPW; r0 += RC)
                                         tmem_st4(at + e * RP + r0, o[e] + r0);
@@ -952,7 +983,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 for (int r = 0; r < RPW; ++r) {
                     a[r] = ex2(a[r]);
                     l[r] += a[r];
-                    a[r] *= sv.z;
+                    a[r] *= vs;
                 }
                 uint32_t c[RPW / 2][PT]; // codes of two rows
 #pragma unroll
@@ -987,8 +1018,8 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 }
             }
             if (ab) break;
-            // l over the threads (lanes by a transposing reduce, the warps later) and m, where
-            // the other set and the epilogue find them
+            // l over the threads (lanes by a transposing reduce, the warps later), m and log2 V,
+            // where the other set and the epilogue find them
             float *sum = sum_sm + iph * 4 * RP * X, *ref = ref_sm + iph * RP * X;
             tr_reduce<RPW, 16>(l, lane);
             if (tr_writer<RPW, 16>(lane)) {
@@ -999,6 +1030,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
             if (tid == 0) {
 #pragma unroll
                 for (int r = 0; r < RPW; ++r) ref[turn * RP + r00 + r] = m[r];
+                if (X > 1) lgv_sm[iph * X + turn] = lgv;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + B_MFULL);
@@ -1019,27 +1051,40 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
             // ------------------------------- epilogue -------------------------------
             bool okw = mbar_wait_bounded(bar + B_MFULL, iph, p.timeout_ns, abort_flag);
             // Lane r works out row r of this warpgroup (all lanes, RPW in turn), while the last
-            // value MMA runs: the reference M of both sets, l under it, and the factor of each
-            // set's O^T (0: the set has nothing, and its O^T may hold anything). A set whose
-            // only scores are NaN has no reference, but a NaN in l.
+            // value MMA runs. A set's l is between 2^E and 2^(E + 1): the row's partial is
+            // published under the larger m + E of the sets, so that l is in [1, 4), the sums of
+            // values are about the size of a value, and merges meet the extremes of neither. A
+            // set's O^T comes under that by f = 2^(m - the row's) and V (0: the set has nothing,
+            // and its O^T may hold anything; a set whose only scores are NaN has no reference,
+            // but a NaN in l).
             float fl[X], Ml = kNeutralM, ll = 0.f, inv = 1.f;
             const int lr = lane % RPW, wl = wrow_sm[r00 + lr];
             {
-                float l2[X];
+                float me[X]; // m + E
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
                     const float *s4 = sum + (x * W + r00 / RPW) * 4 * RPW + lr;
-                    l2[x] = s4[0] + s4[RPW] + s4[2 * RPW] + s4[3 * RPW];
-                    Ml = fmaxf(Ml, ref[x * RP + r00 + lr]);
+                    const float l1 = s4[0] + s4[RPW] + s4[2 * RPW] + s4[3 * RPW];
+                    fl[x] = l1; // 0 or NaN
+                    me[x] = kNeutralM;
+                    if (l1 > 0.f) {
+                        me[x] = ref[x * RP + r00 + lr] + (float)((__float_as_int(l1) >> 23) - 127);
+                        fl[x] = __int_as_float((__float_as_int(l1) & 0x7fffff) | 0x3f800000);
+                    }
+                    Ml = fmaxf(Ml, me[x]);
                 }
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
-                    const float m1 = ref[x * RP + r00 + lr];
-                    fl[x] = X == 1 ? 1.f : m1 == kNeutralM ? l2[x] : ex2(m1 - Ml);
-                    ll = X == 1 ? l2[x] : fmaf(l2[x], fl[x], ll);
+                    ll += X == 1 || !(fl[x] > 0.f)
+                              ? fl[x]
+                              : fl[x] * pow2(max(-126, (int)(me[x] - Ml)));
+                    if (fl[x] > 0.f) fl[x] = pow2(max(-126, (int)(ref[x * RP + r00 + lr] - Ml)));
                 }
                 if (direct) inv = ll == 0.f ? 0.f : 1.f / ll; // nothing seen: zero; NaN: NaN
             }
+            float vx[X]; // V of the sets
+#pragma unroll
+            for (int x = 0; x < X; ++x) vx[x] = pow2((int)(X > 1 ? lgv_sm[iph * X + x] : lgv));
             okw = okw && mbar_wait_bounded(bar + B_OREADY, iph, p.timeout_ns, abort_flag);
             if (bar_or(!okw)) {
                 ab = true;
@@ -1075,7 +1120,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
 #pragma unroll
                             for (int k = PT - 2; k >= 0; --k)
                                 o = fmaf(o, kTermStep, v[j][x][k][i]);
-                            if (f != 0.f) y[j][i] = fmaf(o, f, y[j][i]);
+                            if (f != 0.f) y[j][i] = fmaf(o * f, vx[x], y[j][i]);
                         }
                     }
                     if (direct) {
