@@ -9,33 +9,39 @@
 // so the value scales fold into the weights and the codes go to the tensor cores
 // as they stand: TMA brings 128-position tiles of K and of V into shared memory
 // in the 128-byte swizzle the MMA reads, and nothing converts or re-reads them.
+//     S[pos][(j, r)]  = sum_d Kc[pos][d] q_j[r][d]      (M = 128 positions, K = D)
+//     O^T[d][(j, r)] += sum_pos Vc[pos][d] x_j[r][pos]  (M = 128 value columns, K = 128)
 // V is about the largest value scale of the item so far, a power of two: with it l stays
 // near 1 whatever the scales are (pages of zeros have 2^-100, others up to 2^120), and
 // neither l nor x leaves the range of an f32. References and V are even powers of two, so
 // that moving them multiplies by an exact power, in two halves where one would underflow.
-//     S[pos][(j, r)]  = sum_d Kc[pos][d] q_j[r][d]      (M = 128 positions, K = D)
-//     O^T[d][(j, r)] += sum_pos Vc[pos][d] x_j[r][pos]  (M = 128 value columns, K = 128)
 //
 // The other operand of an 8-bit MMA is 8-bit too. q and x are split into e4m3 terms,
-// y = y_0 + 2^-4 y_1 + 2^-8 y_2 + ...: a term rounds what the ones before it left, and
+// y = y_0 + 2^-5 y_1 + 2^-10 y_2 + ...: a term rounds what the ones before it left, and
 // each takes 5 bits off (4 significant bits and the sign of the rest). f32 outputs take
 // five terms of both, 25 bits: four of both left an error of 0.4 to 1.4e-6 there, as much as
-// or more than f32 arithmetic does. 16-bit outputs take four of q, 20 bits, and four of x, or
-// three, 15 bits, in items of more than 8 rows (2^-14 of a weight at most, against 2^-9 and
-// 2^-12 of the output's rounding).
-// y is scaled to at most 256, so that e4m3's least step, 2^-9, is 2^-25 to 2^-33 of the
-// largest in the last term. The terms are columns of the MMA (N = terms x rows, rounded to
-// 16), whose time for N <= 64 is that of reading the tile (46 to 48 cycles per 32-byte step);
-// they are added in f32 when S or O^T leave TMEM. The products are exact and the sums f32
-// (measured: relative error 1e-7 on full-range codes).
+// or more than f32 arithmetic does. 16-bit outputs take four of both, 20 bits (of x 16 in
+// items of more than 8 rows, where the last three come from an f16).
+// y is at most 256, and e4m3's least step, 2^-9, is 2^-24 or 2^-29 in the last term: half of
+// that is what a term of any size may be off by. Of q that is 2^-32 of the row's largest.
+// Weights differ by far more, and a small one can be one of many whose values are all there
+// is to sum (one position that holds the probability, with values near zero). So m follows
+// the largest weight of the tile both ways: it is 2^4 to 2^6 when it sets m, and when a
+// row's is above 2^8 or below 2^-10 (five terms: 2^-8) in a whole tile, m moves and l and
+// O^T are rescaled. What is off by half a step is then at most 2^-15 (2^-22) of the largest
+// weight of its tile. A fixed m lost 3.6% of 65536 equal positions beside one of 99.7% with
+// values of zero, and with three terms (x of wide items) all of 16384.
+// The terms are columns of the MMA (N = terms x rows, rounded to 16), whose time for N <= 64
+// is that of reading the tile (46 to 48 cycles per 32-byte step); they are added in f32 when S
+// or O^T leave TMEM. The products are exact and the sums f32 (measured: relative error 1e-7
+// on full-range codes).
 //
 // An item is (sequence, KV head, split, row group), rows (query token, head). Roles, one
 // CTA per SM:
 //   softmax warpgroups (1 to 4, up to 8 rows each; for 5 to 8 rows of 128 two of them take
 //              tiles in turn): a thread owns one position of the tile (TMEM lane); the
-//              reference m of a row moves only when a score outgrows it by 2^8 (then O^T is
-//              rescaled), so most tiles take one vote. In the epilogue a thread owns a value
-//              column.
+//              references stay for most tiles, which take one vote. In the epilogue a thread
+//              owns a value column.
 //   two warps  TMA producers, K and V tiles through one ring of slots, paged boxes as in the
 //              16-bit tensor-core kernel.
 //   two warps  MMA issue, one thread each for the scores and for the values.
@@ -59,9 +65,12 @@ namespace skv {
 namespace {
 
 constexpr int T = kQ8Tile;
-constexpr float kTermStep = 1.f / 16.f;
+constexpr float kTermStep = 1.f / 32.f;
 constexpr float kHead = 4.f; // m is this much below the maximum that set it
-constexpr float kTau = 8.f;  // and moves when a score is this much above it
+constexpr float kTau = 8.f;  // and moves when a score is this much above it,
+                             // or a tile's largest kLow below it
+constexpr float kDeep = 64.f; // but not further below its highest than this: l and O^T keep
+                              // the weights of before, times 2^64 at most
 constexpr float kWide = 16.f; // log2 V moves when a page's is this much above it
 constexpr float kLeast = -32.f; // and pages further below it count as this far in a reference:
                                 // 2^(s - m) stays below 2^(8 + 32)
@@ -193,28 +202,46 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const float *v)
                  : "memory");
 }
 
-// two values to e4m3 (x in the low byte); *x, *y: what is left, times 16
+// two values of at most 256 to e4m3 (x in the low byte); *x, *y: what is left, times 32 (at
+// most 256 again: a code is within 2^3 of a value below 2^8)
 __device__ __forceinline__ uint32_t term2(float &x, float &y)
 {
     const __nv_fp8x2_storage_t c =
         __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
     const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-    x = (x - f.x) * 16.f;
-    y = (y - f.y) * 16.f;
+    x = (x - f.x) * 32.f;
+    y = (y - f.y) * 32.f;
     return c;
 }
 
-// The PT terms of two values, x in the low byte of each. What is left after all but two
-// fits an f16 (11 bits for 10), so the last two are taken two values at a time.
-template <int PT> __device__ __forceinline__ void terms(float x, float y, uint32_t *c)
+// The PT terms of two values, x in the low byte of each. The last HT are taken two values at
+// a time in f16: its 11 bits hold the 10 of two terms, and of three (of which the first leaves
+// 2^-4 of the value) all but 2^-16 of the value.
+template <int PT, int HT> __device__ __forceinline__ void terms(float x, float y, uint32_t *c)
 {
 #pragma unroll
-    for (int j = 0; j < PT - 2; ++j) c[j] = term2(x, y);
-    const __half2 h = __floats2half2_rn(x, y);
-    c[PT - 2] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-    const __half2 f(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[PT - 2], __NV_E4M3));
-    const __half2 rest = __hmul2(__hsub2(h, f), __half2(__half(16.f), __half(16.f)));
-    c[PT - 1] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+    for (int j = 0; j < PT - HT; ++j) c[j] = term2(x, y);
+    __half2 h = __floats2half2_rn(x, y);
+#pragma unroll
+    for (int j = PT - HT; j < PT; ++j) {
+        c[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+        if (j + 1 < PT) {
+            const __half2 f(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[j], __NV_E4M3));
+            h = __hmul2(__hsub2(h, f), __half2(__half(32.f), __half(32.f)));
+        }
+    }
+}
+
+// how many of a barrier's threads have pred
+__device__ __forceinline__ int named_bar_count(int id, int threads, bool pred)
+{
+    int n;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+                 "barrier.cta.red.popc.aligned.u32 %0, %1, %2, p;\n\t}"
+                 : "=r"(n)
+                 : "r"(id), "r"(threads), "r"((int)pred)
+                 : "memory");
+    return n;
 }
 
 // 2^k, k in [-126, 127]
@@ -300,6 +327,10 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     using L = Layout<D, RP, QT, PT>;
     constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW,
                   X = L::X, WT = L::WT;
+    // terms of x taken in f16, three in wide items with 16-bit outputs
+    constexpr int HT = RP > 8 && PT == 4 ? 3 : 2;
+    // a tile's largest weight is 2^-kLow at least, half a step of the terms 2^-30 or 2^-25
+    constexpr float kLow = PT == 5 ? 8.f : 10.f;
     constexpr int RC = 4; // rows taken from TMEM at a time
     // and of the scores: 8 at a time save a round trip where they fit the registers (16 rows
     // of 128, 1.2M positions: 63 -> 60.5 us; 8 and 24 rows spill and lose 1%)
@@ -797,6 +828,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 m[r] = kNeutralM; // none yet
                 l[r] = 0.f;
             }
+            float high = kNeutralM; // the highest reference so far of row lane % RPW
             float lgv = 0.f, inv_v = 1.f; // log2 V, 1 / V (uniform over the warpgroup)
             const int lim0 = causal ? Lb - p.q_len + 1 : INT_MAX; // the first token's limit
             bool firsttile = true;
@@ -890,7 +922,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                             if (pos >= lim_sm[r00 + r]) a[r] = -INFINITY;
                     }
                 };
-                // One vote a tile, whether a score outgrew its reference; a wait that ran out
+                // One vote a tile, whether a row outgrew its reference or left it; a wait that ran out
                 // joins it through a flag of this tile's parity (written before the tile's first
                 // barrier, read after it, so the warpgroup leaves together). An item's first tile
                 // always sets references.
@@ -907,13 +939,25 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 bool ex = wider;
                 if (!firsttile) {
                     scores(true);
-                    const float most = kTau - lv;
+                    const float most = kTau - lv, least = -kLow - lv;
+                    float top = a[0];
+                    unsigned low = 0; // rows of which this warp's positions all lie low
 #pragma unroll
-                    for (int r = 0; r < RPW; ++r) ex |= a[r] > most;
-                    ex = bar_or(ex || !okw);
+                    for (int r = RPW - 1; r >= 0; --r) {
+                        top = fmaxf(top, a[r]);
+                        low = __funnelshift_l(__float_as_uint(a[r] - least), low, 1); // its sign
+                    }
+                    ex |= top > most;
+                    low = __reduce_and_sync(0xffffffffu, low);
+                    if (t0 + 32 * (warp & 3) >= t1) low = 0; // it has none
+                    // a row that lies low in the whole tile counts once for each warp that has
+                    // positions, and a warp with any other cause 32 times
+                    ex = __any_sync(0xffffffffu, ex || !okw);
+                    ex = named_bar_count(1 + wg, 128, ex || ((low >> lane) & 1u)) >=
+                         (t1 - t0 + 31) >> 5;
                 }
                 if (ex) {
-                    // move the references that scores outgrew; rescale l and O^T
+                    // move the references that scores outgrew or left; rescale l and O^T
                     scores(false);
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
@@ -929,16 +973,23 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                         break;
                     }
                     float al[RPW]; // square roots of the factors, exact
+                    bool moved = wider;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
                         const float tm = fmaxf(fmaxf(red[r], red[RPW + r]),
                                                fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
-                        const float mn = tm > m[r] + kTau ? 2.f * floorf(0.5f * (tm - kHead)) : m[r];
+                        const float hi = __shfl_sync(0xffffffffu, high, r);
+                        float mn = m[r];
+                        if (tm > mn + kTau || (tm < mn - kLow && tm > -INFINITY))
+                            mn = fmaxf(2.f * floorf(0.5f * (tm - kHead)), hi - kDeep);
+                        if (lane % RPW == r) high = fmaxf(hi, mn);
+                        moved |= mn != m[r];
                         al[r] = m[r] - mn;
                         m[r] = mn;
                         a[r] -= mn;
                     }
-                    if (!firsttile) { // the set's last PV is done with O^T before it is rescaled
+                    // the set's last PV is done with O^T before it is rescaled
+                    if (!firsttile && moved) {
 #pragma unroll
                         for (int r = 0; r < RPW; ++r) {
                             al[r] = pow2(max(-126, (int)(0.5f * al[r])));
@@ -987,7 +1038,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 }
                 uint32_t c[RPW / 2][PT]; // codes of two rows
 #pragma unroll
-                for (int r = 0; r < RPW; r += 2) terms<PT>(a[r], a[r + 1], c[r / 2]);
+                for (int r = 0; r < RPW; r += 2) terms<PT, HT>(a[r], a[r + 1], c[r / 2]);
 #pragma unroll
                 for (int j = 0; j < PT; ++j) {
                     const uint32_t at = pt + swz(tid, j * RP + r00);
@@ -1214,9 +1265,9 @@ cudaError_t launch_d(int rows, bool out16, int grid, cudaStream_t st, const CUte
     if (out16) {
         if (rows <= 4) return launch_t<D, 4, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
         if (rows <= 8) return launch_t<D, 8, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
-        if (rows <= 16) return launch_t<D, 16, 4, 3>(grid, st, km, vm, sc, od, p, e5m2);
-        if (rows <= 24) return launch_t<D, 24, 4, 3>(grid, st, km, vm, sc, od, p, e5m2);
-        return launch_t<D, 32, 4, 3>(grid, st, km, vm, sc, od, p, e5m2);
+        if (rows <= 16) return launch_t<D, 16, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
+        if (rows <= 24) return launch_t<D, 24, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
+        return launch_t<D, 32, 4, 4>(grid, st, km, vm, sc, od, p, e5m2);
     }
     if (rows <= 4) return launch_t<D, 4, 5, 5>(grid, st, km, vm, sc, od, p, e5m2);
     if (rows <= 8) return launch_t<D, 8, 5, 5>(grid, st, km, vm, sc, od, p, e5m2);
