@@ -13,7 +13,8 @@
 // then computes m and l over all splits itself (lanes stride the splits, warp
 // shuffles reduce), so the only block-wide step is the final sum of the 8
 // warps' vectors. Launched with programmatic stream serialization: the CTAs
-// may start while the split kernel drains and wait in griddepcontrol.wait.
+// may start while the split kernel drains and wait in griddepcontrol.wait; its
+// partials are read by ordinary loads, which the wait orders.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -60,9 +61,9 @@ __device__ __forceinline__ float4 merge_columns(const CombineParams &p, int h, i
     const float *acc0 = p.acc + (slot0 * p.n_heads + h) * p.v_dim + (live ? col : 0);
     const size_t acc_step = (size_t)p.n_heads * p.v_dim;
     auto ml_of = [&](int i) {
-        if (p.n_ranks == 1) return __ldg(ml0 + (size_t)i * p.n_heads);
+        if (p.n_ranks == 1) return ml0[(size_t)i * p.n_heads];
         const int r = i / S;
-        return __ldg(ml0 + r * p.rank_ml + (size_t)(i - r * S) * p.n_heads);
+        return ml0[r * p.rank_ml + (size_t)(i - r * S) * p.n_heads];
     };
     auto acc_of = [&](int i) {
         const float *a = acc0 + (size_t)i * acc_step;
@@ -70,7 +71,7 @@ __device__ __forceinline__ float4 merge_columns(const CombineParams &p, int h, i
             const int r = i / S;
             a = acc0 + r * p.rank_acc + (size_t)(i - r * S) * acc_step;
         }
-        return __ldg(reinterpret_cast<const float4 *>(a));
+        return *reinterpret_cast<const float4 *>(a);
     };
 
     // acc vectors of this warp's first pairs, in flight while m and l are formed
@@ -248,7 +249,7 @@ __device__ __forceinline__ float4 staged_merge(const CombineParams &p, int h, in
 #pragma unroll
             for (int i = 0; i < WB; ++i) {
                 const int s = s0 + 32 * i + lane;
-                x[i] = s < S ? __ldg(ml + (size_t)s * p.n_heads) : make_float2(kNeutralM, 0.f);
+                x[i] = s < S ? ml[(size_t)s * p.n_heads] : make_float2(kNeutralM, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < WB; ++i) {
@@ -276,7 +277,7 @@ __device__ __forceinline__ float4 staged_merge(const CombineParams &p, int h, in
             }
         } else {
             for (int s = lane; s < S; s += 32) {
-                const float2 y = __ldg(ml + (size_t)s * p.n_heads);
+                const float2 y = ml[(size_t)s * p.n_heads];
                 st.wts[s] = y.y > 0.f ? ex2((y.x - M) * kLog2e) * inv : 0.f;
             }
         }

@@ -252,7 +252,7 @@ __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) <
 __device__ __forceinline__ int len8(const SplitParams &p, int e, int b)
 {
     const int L = p.items.seq_lens[e];
-    return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
+    return p.dev_lens ? max(0, min(p.dev_lens[b], L)) : L;
 }
 
 // one output element, in the output's type
@@ -389,7 +389,9 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // The set-up above overlaps the end of the stream's last kernel (a programmatic launch:
-    // 0.25 us of 7 on short contexts); nothing of it is touched before here.
+    // 0.25 us of 7 on short contexts); nothing of it is touched before here, and what that
+    // kernel may have written (lengths, tables, scales, q) is read by ordinary loads, which
+    // the wait orders.
     griddep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
@@ -414,8 +416,8 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     auto scales = [&](Batch &x) {
         x.ks = x.vs = 0.f;
         if (x.blk >= 0 && x.blk < sc.num_blocks) {
-            x.ks = __ldg(sc.k + x.blk * sc.k_block + x.kvh * sc.k_head);
-            x.vs = __ldg(sc.v + x.blk * sc.v_block + x.kvh * sc.v_head);
+            x.ks = sc.k[x.blk * sc.k_block + x.kvh * sc.k_head];
+            x.vs = sc.v[x.blk * sc.v_block + x.kvh * sc.v_head];
         }
     };
     // false when the wait for the buffer runs out
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 const int pos = w.t0 + lane * h, idx = pos / bs;
                 slot0 = pos - idx * bs;
                 if (pos < w.t1 && idx < p.max_blocks) // past the tile: zeros, nothing is read
-                    blk = __ldg(p.block_table + (size_t)w.b * p.max_blocks + idx);
+                    blk = p.block_table[(size_t)w.b * p.max_blocks + idx];
             }
             return blk;
         };
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
                     qv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (r < x.R) qv[i][c] = __ldg(reinterpret_cast<const float4 *>(qr + 128 * c));
+                    if (r < x.R) qv[i][c] = *reinterpret_cast<const float4 *>(qr + 128 * c);
                 }
             }
         };

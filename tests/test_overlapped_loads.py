@@ -1,0 +1,31 @@
+"""Kernels that a programmatic launch starts before their predecessor ends may not read what
+it writes through the read-only path: those loads are for data that nobody writes while the
+kernel runs, and griddepcontrol.wait does not order them (CPU)."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "split_kv_decode_gb300", "csrc")
+
+
+def code(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+def overlapped():
+    """The sources with a griddep_wait: their kernels are launched ahead of time."""
+    return [f for f in sorted(os.listdir(CSRC)) if f.endswith(".cu") and "griddep_wait" in code(f)]
+
+
+def test_the_overlapped_kernels_are_known():
+    assert overlapped() == ["append.cu", "combine.cu", "gqa_8bit.cu", "tables.cu"]
+
+
+@pytest.mark.parametrize("name", overlapped())
+def test_no_read_only_loads_behind_the_wait(name):
+    found = [l.strip() for l in code(name).splitlines()
+             if re.search(r"__ldg\s*\(|ld\.global\.nc|LDG", l)]
+    assert not found, found
