@@ -448,6 +448,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
         const bool isv = warp == L::VPROD;
         const CUtensorMap *map = isv ? &vmap : &kmap;
         if (lane == 0) tma_prefetch_map(map);
+        fence_proxy_async_global(); // the pages as the append wrote them, for the copies
         const uint64_t pol = l2_evict_first_policy();
         const int bs = p.block_size, h = p.box_rows, nbox = T / h;
         // this lane's box of tile w: its block as the table has it (not looked at until the tile

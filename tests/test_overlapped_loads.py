@@ -29,3 +29,10 @@ def test_no_read_only_loads_behind_the_wait(name):
     found = [l.strip() for l in code(name).splitlines()
              if re.search(r"__ldg\s*\(|ld\.global\.nc|LDG", l)]
     assert not found, found
+
+
+def test_tma_reads_of_the_8bit_pools_are_fenced():
+    # the append writes the pools by ordinary stores; copies read them through the async proxy
+    text = code("gqa_8bit.cu")
+    wait, fence = text.index("griddep_wait();"), text.find("fence_proxy_async_global();")
+    assert wait < fence < text.index("tma_load_4d(")
