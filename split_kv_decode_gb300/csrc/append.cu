@@ -232,8 +232,10 @@ template <typename ST, __nv_fp8_interpretation_t F, int G>
 __global__ void __launch_bounds__(32 * warps_of(G), G == 8 ? 4 : 7)
     append_kernel(const __grid_constant__ AppendParams p)
 {
-    griddep_launch_dependents(); // the attention that follows may set itself up meanwhile
     griddep_wait();
+    // The attention that follows may set itself up meanwhile. Not before the wait: the kernel
+    // after that could then run beside what came before this one.
+    griddep_launch_dependents();
     constexpr int TG = 32 * G, kWarps = warps_of(G);
     __shared__ float red[2][kWarps], red_finite[2][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

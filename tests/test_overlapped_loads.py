@@ -36,3 +36,11 @@ def test_tma_reads_of_the_8bit_pools_are_fenced():
     text = code("gqa_8bit.cu")
     wait, fence = text.index("griddep_wait();"), text.find("fence_proxy_async_global();")
     assert wait < fence < text.index("tma_load_4d(")
+
+
+def test_the_append_lets_others_start_only_after_its_own_wait():
+    # a kernel two places on (a projection whose weights are fetched before its wait) may start
+    # once the append says so; what ran before the append must have ended by then
+    text = code("append.cu")
+    text = text[text.index("append_kernel("):]
+    assert text.index("griddep_wait();") < text.index("griddep_launch_dependents();")
