@@ -6,10 +6,10 @@ Tolerances, from the arithmetic (test_gpu_kv8_attend derives the first line):
     included; here that is of the positions that contribute, tau (their probability) max|V|.
   * the sum of values takes weights in steps: half a step is 2^-25 (four terms) or 2^-30
     (f32 outputs, five) where the largest weight of a tile of 128 positions is at least 2^-10
-    or 2^-8, and 2^4 when it set the row's reference. The others' weights here are alike: on
+    or 2^-8, and 2^2 when it set the row's reference. The others' weights here are alike: on
     average within 2^3 of their tile's largest, so at least 2^-13 or 2^-11, and off by
     2^-12 or 2^-19 of themselves. In the tile of the dominating position 128 half steps are
-    2^-22 or 2^-27 of its weight.
+    2^-20 or 2^-25 of its weight.
   * the output's rounding: half a step, eps / 2 of the value.
 """
 import math
@@ -66,7 +66,7 @@ def check_peaked(got, q, cache, n, d, code, where, out):
     p = np.exp(s - s.max(0))
     tau = (p[rest].sum(0) / p.sum(0))[:, None]
     rel = 2.0 ** -17 * mag[0, 0][:, None] + 2.0 ** -15 + 2.0 ** (-19 if five else -12)
-    tol = (tau * vmax + (1 - tau) * vpeak) * rel + 2.0 ** (-27 if five else -22) * vmax
+    tol = (tau * vmax + (1 - tau) * vpeak) * rel + 2.0 ** (-25 if five else -20) * vmax
     if not five:
         tol = tol + torch.finfo(OUT[out]).eps / 2 * np.abs(ref[0, 0])
         tol = tol + (6e-8 if out == "f16" else 0.0)

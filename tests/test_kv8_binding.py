@@ -1,0 +1,117 @@
+"""Refusals of the 8-bit cache's binding (CPU): stand-ins for CUDA tensors carry a type, a
+shape, strides and a device, and no call gets as far as a launch."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from split_kv_decode_gb300 import _native as N
+from split_kv_decode_gb300 import api as A
+from split_kv_decode_gb300 import cache8 as C
+
+CUDA = torch.device("cuda", 0)
+
+
+class Fake:
+    """What the binding looks at of a CUDA tensor."""
+
+    def __init__(self, shape, dtype=torch.float32, stride=None, device=CUDA):
+        self._t = torch.empty(0, dtype=dtype)
+        full = []
+        for n in reversed(shape):
+            full.insert(0, full[0] * below if full else 1)
+            below = n
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
+        self._stride = tuple(stride or full)
+        self._dense = tuple(full)
+        self.is_cuda = device.type == "cuda"
+
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self._t.element_size()
+
+    def is_contiguous(self):
+        return self._stride == self._dense
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """Launches that a call would make; none is made."""
+    got = []
+    monkeypatch.setattr(A, "_launch", lambda dev, stream, fn, *args: got.append((dev, args)))
+    monkeypatch.setattr(N, "load", lambda: SimpleNamespace(
+        decode_attn_splitk_8bit=None, decode_attn_append_8bit=None, decode_attn_grow_tables=None,
+        decode_attn_tables_status=None))
+    return got
+
+
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+POOL = (40, 16, 2, 128)
+
+
+def attend(q_shape=(3, 8, 128), out_dtype=torch.float32, pool=POOL, **kw):
+    t = dict(q=Fake(q_shape), k=Fake(pool, E4), v=Fake(pool, E4), out=Fake(q_shape, out_dtype),
+             lens=Fake((3,), torch.int32), table=Fake((3, 10), torch.int32),
+             ks=Fake(pool[::2][:2]), vs=Fake(pool[::2][:2]), ws=Fake((4096,), torch.uint8))
+    a = A.make_paged_args(t["q"], t["k"], t["v"], 0.1, 10, out_dtype=out_dtype)
+    dev = A.make_dev(seq_lens=t["lens"], block_table=t["table"], k_pool=t["k"], v_pool=t["v"])
+    t.update(kw)
+    A.decode_attn_splitk_8bit(a, N.DaPlan(), dev, A.make_scales(t["ks"], t["vs"]), t["q"], t["k"],
+                              t["v"], t["out"], t["ws"])
+
+
+@pytest.mark.parametrize("q_shape", [(3, 8, 128), (3, 2, 8, 128)])
+@pytest.mark.parametrize("out", [torch.float32, torch.float16, torch.bfloat16])
+def test_attention_takes_what_it_was_made_for(launches, q_shape, out):
+    attend(q_shape, out)
+    assert len(launches) == 1 and launches[0][0] == CUDA
+    attend(q_shape, out, out=Fake((torch.Size(q_shape).numel(),), out))   # any shape of that size
+    assert len(launches) == 2
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=Fake((3, 8, 128), torch.bfloat16)), dict(out=Fake((2, 8, 128))),
+    dict(out=Fake((3, 8, 64))), dict(q=Fake((2, 8, 128))), dict(q=Fake((3, 8, 256))),
+    dict(q=Fake((3, 8, 128), torch.float16)), dict(k=Fake(POOL, E5)), dict(v=Fake(POOL, E5)),
+    dict(k=Fake(POOL, torch.float16)), dict(v=Fake((39, 16, 2, 128), E4)),
+    dict(k=Fake((40, 32, 2, 128), E4)), dict(k=Fake((40, 16, 1, 128), E4)),
+    dict(v=Fake((40, 16, 2, 256), E4)), dict(k=Fake(POOL, E4, (4096, 128, 2048, 1))),
+    dict(out=Fake((3, 8, 128), device=torch.device("cpu")))])
+def test_attention_refuses_other_tensors_than_described(launches, kw):
+    with pytest.raises((TypeError, ValueError)):
+        attend(**kw)
+    assert not launches
+
+
+def step(q_shape=(3, 8, 128), out_dtype=torch.float32):
+    s = C.Step8.__new__(C.Step8)
+    s.cache = SimpleNamespace(k=Fake(POOL, E4), v=Fake(POOL, E4), dev=N.DaDev(), scales=N.DaScales())
+    s.shape, s.out_dtype, s.args, s.plan = q_shape, out_dtype, N.DaArgs(), N.DaPlan()
+    s.workspace = Fake((4096,), torch.uint8)
+    return s
+
+
+def test_a_step_takes_its_own_shapes_alone(launches):
+    s = step()
+    s(Fake((3, 8, 128)), Fake((3, 8, 128)))
+    assert len(launches) == 1
+    for q, out in ((Fake((2, 8, 128)), None), (Fake((3, 8, 128), torch.float16), None),
+                   (Fake((3, 8, 128), device=torch.device("cuda", 1)), None),
+                   (Fake((3, 8, 128)), Fake((3, 8, 128), torch.bfloat16)),
+                   (Fake((3, 8, 128)), Fake((2, 8, 128))),
+                   (Fake((3, 8, 128)), Fake((3, 8, 128), stride=(1, 3, 24))),
+                   (Fake((3, 8, 128)), Fake((3, 8, 128), device=torch.device("cpu")))):
+        with pytest.raises((TypeError, ValueError)):
+            s(q, out)
+    assert len(launches) == 1
