@@ -833,7 +833,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 m[r] = kNeutralM; // none yet
                 l[r] = 0.f;
             }
-            float high = kNeutralM; // the highest reference so far of row lane % RPW
+            float high = kNeutralM; // the highest reference moved to so far of row lane % RPW
             float lgv = 0.f, inv_v = 1.f; // log2 V, 1 / V (uniform over the warpgroup)
             const int lim0 = causal ? Lb - p.q_len + 1 : INT_MAX; // the first token's limit
             bool firsttile = true;
@@ -941,8 +941,43 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                     inv_v = pow2(-(int)lgv);
                 }
                 const float lv = fmaxf(sv.y - lgv, kLeast), vs = sv.z * inv_v;
+                // the tile's largest weights, from a[] as scores(false) left it; false when a wait
+                // of the warpgroup has run out
+                auto largest = [&](float *tm) {
+#pragma unroll
+                    for (int r = 0; r < RPW; ++r) {
+                        // as ordered integers; a NaN counts as -inf
+                        const int u = __float_as_int(fmaxf(a[r] + lv, -INFINITY));
+                        const int o = __reduce_max_sync(0xffffffffu, u ^ ((u >> 31) & 0x7fffffff));
+                        if (lane == 0)
+                            red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
+                    }
+                    named_bar_sync(1 + wg, 128);
+#pragma unroll
+                    for (int r = 0; r < RPW; ++r)
+                        tm[r] = fmaxf(fmaxf(red[r], red[RPW + r]),
+                                      fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
+                    return !bad_sm[2 * wg + (own & 1)];
+                };
+                // An item's first tile has a path of its own where items are narrow and often
+                // short (256 sequences of 40 positions, 4 rows of 128: 45.3 -> 40.9 us; 76 of
+                // 128, 8 rows: 19.8 -> 18.6; but 16 rows, 1.2M positions: 66 -> 69)
+                constexpr bool kFirst = RP <= 8;
                 bool ex = wider;
-                if (!firsttile) {
+                if (kFirst && firsttile) {
+                    float tm[RPW];
+                    scores(false);
+                    if (!largest(tm)) {
+                        ab = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int r = 0; r < RPW; ++r) {
+                        if (tm[r] > -INFINITY) m[r] = 2.f * floorf(0.5f * (tm[r] - kHead));
+                        a[r] -= m[r];
+                    }
+                    ex = false;
+                } else if (!firsttile) {
                     scores(true);
                     const float most = kTau - lv, least = -kLow - lv;
                     float top = a[0];
@@ -963,27 +998,18 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 }
                 if (ex) {
                     // move the references that scores outgrew or left; rescale l and O^T
+                    float al[RPW]; // the tile's largest, then square roots of the factors, exact
                     scores(false);
-#pragma unroll
-                    for (int r = 0; r < RPW; ++r) {
-                        // as ordered integers; a NaN counts as -inf
-                        const int u = __float_as_int(fmaxf(a[r] + lv, -INFINITY));
-                        const int o = __reduce_max_sync(0xffffffffu, u ^ ((u >> 31) & 0x7fffffff));
-                        if (lane == 0)
-                            red[(warp & 3) * RPW + r] = __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
-                    }
-                    named_bar_sync(1 + wg, 128);
-                    if (bad_sm[2 * wg + (own & 1)]) {
+                    if (!largest(al)) {
                         ab = true;
                         break;
                     }
-                    float al[RPW]; // square roots of the factors, exact
                     bool moved = wider;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) {
-                        const float tm = fmaxf(fmaxf(red[r], red[RPW + r]),
-                                               fmaxf(red[2 * RPW + r], red[3 * RPW + r]));
-                        const float hi = __shfl_sync(0xffffffffu, high, r);
+                        const float tm = al[r];
+                        float hi = __shfl_sync(0xffffffffu, high, r);
+                        if (kFirst) hi = fmaxf(hi, m[r]); // (the first tile's)
                         float mn = m[r];
                         if (tm > mn + kTau || (tm < mn - kLow && tm > -INFINITY))
                             mn = fmaxf(2.f * floorf(0.5f * (tm - kHead)), hi - kDeep);
@@ -1116,25 +1142,25 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
             float fl[X], Ml = kNeutralM, ll = 0.f, inv = 1.f;
             const int lr = lane % RPW, wl = wrow_sm[r00 + lr];
             {
-                float me[X]; // m + E
+                float me[X], l2[X]; // m + E, and l / 2^E (or the 0 or NaN that l is)
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
                     const float *s4 = sum + (x * W + r00 / RPW) * 4 * RPW + lr;
                     const float l1 = s4[0] + s4[RPW] + s4[2 * RPW] + s4[3 * RPW];
-                    fl[x] = l1; // 0 or NaN
-                    me[x] = kNeutralM;
-                    if (l1 > 0.f) {
-                        me[x] = ref[x * RP + r00 + lr] + (float)((__float_as_int(l1) >> 23) - 127);
-                        fl[x] = __int_as_float((__float_as_int(l1) & 0x7fffff) | 0x3f800000);
-                    }
+                    const int u = __float_as_int(l1);
+                    const bool some = l1 > 0.f;
+                    l2[x] = some ? __int_as_float((u & 0x7fffff) | 0x3f800000) : l1;
+                    fl[x] = some ? __int_as_float((254 << 23) - (u & 0x7f800000)) : l1; // 2^-E
+                    me[x] = some ? ref[x * RP + r00 + lr] + (float)((u >> 23) - 127) : kNeutralM;
                     Ml = fmaxf(Ml, me[x]);
                 }
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
-                    ll += X == 1 || !(fl[x] > 0.f)
-                              ? fl[x]
-                              : fl[x] * pow2(max(-126, (int)(me[x] - Ml)));
-                    if (fl[x] > 0.f) fl[x] = pow2(max(-126, (int)(ref[x * RP + r00 + lr] - Ml)));
+                    if (X > 1 && l2[x] > 0.f) {
+                        l2[x] *= pow2(max(-126, (int)(me[x] - Ml)));
+                        fl[x] = pow2(max(-126, (int)(ref[x * RP + r00 + lr] - Ml)));
+                    }
+                    ll += l2[x];
                 }
                 if (direct) inv = ll == 0.f ? 0.f : 1.f / ll; // nothing seen: zero; NaN: NaN
             }
