@@ -157,6 +157,7 @@ def make_paged_args(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
     a = make_args(q, k_pool, v_pool, scale, v_dim=v_dim, out_dtype=out_dtype,
                   force_splits=force_splits, flags=flags, timeout_us=timeout_us)
     a.capacity = int(max_blocks_per_seq) * k_pool.shape[1]
+    a.pools = _pools(k_pool, v_pool)      # (of this object alone, no field of the struct)
     return a
 
 
@@ -185,6 +186,7 @@ def make_dev(*, seq_lens: Optional[torch.Tensor] = None,
         d.num_blocks = k_pool.shape[0]
         d.k_block_stride = k_pool.stride(0)
         d.v_block_stride = v_pool.stride(0)
+        d.pools = _pools(k_pool, v_pool)
     return d
 
 
@@ -443,14 +445,49 @@ def decode_attn_splitk_8bit(args: N.DaArgs, plan: N.DaPlan, dev: N.DaDev, scales
                             q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
                             out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """decode_attn_splitk_dev over 8-bit pools with scales (make_paged_args,
-    make_dev with a block table, make_scales)."""
-    device = q.device
-    if device.type != "cuda":
+    make_dev with a block table, make_scales). q, out and the pools are of the shapes and
+    types that args and dev describe."""
+    index = q.get_device()
+    if index < 0:
         raise TypeError("q must be a CUDA tensor")
-    _on(device, "decode_attn_splitk_8bit", k_pool, v_pool, out, workspace)
+    if not index == k_pool.get_device() == v_pool.get_device() == out.get_device() \
+            == workspace.get_device():
+        _on(q.device, "decode_attn_splitk_8bit", k_pool, v_pool, out, workspace)
     if q.dtype != torch.float32 or not q.is_contiguous() or not out.is_contiguous():
         raise TypeError("q must be contiguous float32 and out contiguous")
-    _launch(device, stream, N.load().decode_attn_splitk_8bit, ctypes.byref(args),
+    if _DT.get(out.dtype) != args.out_dtype:
+        raise TypeError(f"out is {out.dtype}, not of the type that args were made for")
+    rows = args.batch * args.n_heads * (args.q_len or 1)
+    if q.numel() != rows * args.head_dim or out.numel() != rows * args.v_dim:
+        raise ValueError(f"q and out must hold {rows} rows, as args describe")
+    pools = _pools(k_pool, v_pool)
+    if not pools == getattr(args, "pools", None) == getattr(dev, "pools", None):
+        _check_pools(args, dev, k_pool, v_pool)
+    _splitk_8bit(args, plan, dev, scales, q, k_pool, v_pool, out, workspace, stream)
+
+
+def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor) -> tuple:
+    return (k_pool.shape, k_pool.stride(), k_pool.dtype, v_pool.shape, v_pool.stride(),
+            v_pool.dtype)
+
+
+def _check_pools(args: N.DaArgs, dev: N.DaDev, k_pool: torch.Tensor, v_pool: torch.Tensor) -> None:
+    """Raises unless the pools are what args and dev describe."""
+    if _DT.get(k_pool.dtype) != args.kv_dtype or _DT.get(v_pool.dtype) != args.kv_dtype:
+        raise TypeError("the pools are not of the type that args were made for")
+    if not dev.block_table:
+        return                # the library refuses the call
+    n, rest = dev.num_blocks, (dev.block_size, args.n_kv_heads)
+    if k_pool.shape[0] < n or k_pool.shape[1:] != rest + (args.head_dim,) or \
+            v_pool.shape[0] < n or v_pool.shape[1:] != rest + (args.v_dim,):
+        raise ValueError(f"the pools must be {(n, *rest)}, as args and dev describe")
+    if k_pool.stride() != (dev.k_block_stride, args.k_pos_stride, args.k_head_stride, 1) or \
+            v_pool.stride() != (dev.v_block_stride, args.v_pos_stride, args.v_head_stride, 1):
+        raise ValueError("the pools' strides are not those of args and dev")
+
+
+def _splitk_8bit(args, plan, dev, scales, q, k_pool, v_pool, out, workspace, stream) -> None:
+    _launch(q.device, stream, N.load().decode_attn_splitk_8bit, ctypes.byref(args),
             ctypes.byref(plan), ctypes.byref(dev), ctypes.byref(scales), q.data_ptr(),
             k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())

@@ -121,9 +121,15 @@ class Step8:
                  stream=None) -> torch.Tensor:
         if tuple(q.shape) != self.shape:
             raise ValueError(f"planned for q of shape {self.shape}")
+        c = self.cache
+        if q.dtype != torch.float32 or not q.is_contiguous() or q.device != c.k.device:
+            raise TypeError(f"q must be contiguous float32 on {c.k.device}")
         if out is None:
             out = torch.empty(self.shape, dtype=self.out_dtype, device=q.device)
-        c = self.cache
-        A.decode_attn_splitk_8bit(self.args, self.plan, c.dev, c.scales, q, c.k, c.v, out,
+        elif tuple(out.shape) != self.shape or out.dtype != self.out_dtype \
+                or not out.is_contiguous() or out.device != q.device:
+            raise TypeError(f"out must be contiguous {self.out_dtype} of shape {self.shape} "
+                            f"on {q.device}")
+        A._splitk_8bit(self.args, self.plan, c.dev, c.scales, q, c.k, c.v, out,
                                   self.workspace, stream)
         return out

@@ -26,6 +26,9 @@ class Fake:
         self._dense = tuple(full)
         self.is_cuda = device.type == "cuda"
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def stride(self, i=None):
         return self._stride if i is None else self._stride[i]
 
