@@ -407,6 +407,11 @@ def make_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.Tensor,
     a.v_block_stride, a.v_pos_stride, a.v_head_stride = v_pool.stride()[:3]
     a.k_scale_block_stride, a.k_scale_head_stride = k_scale.stride()
     a.v_scale_block_stride, a.v_scale_head_stride = v_scale.stride()
+    # (of this object alone, no field of the struct)
+    a.tensors = (k_new.shape, k_new.stride(), v_new.shape, v_new.stride(), k_new.dtype,
+                 v_new.dtype, k_pool.shape, k_pool.stride(), v_pool.shape, v_pool.stride(),
+                 k_pool.dtype, v_pool.dtype, k_scale.shape, k_scale.stride(), v_scale.shape,
+                 v_scale.stride(), k_scale.dtype, v_scale.dtype)
     return a
 
 
@@ -419,11 +424,26 @@ def decode_attn_append_8bit(append: N.DaAppend, k_new: torch.Tensor, v_new: torc
     if slot_map.dtype != torch.int64 or not slot_map.is_contiguous() \
             or slot_map.numel() != append.n_tokens:
         raise TypeError("slot_map must be a contiguous int64 tensor with a slot per row")
-    dev = k_pool.device
-    if dev.type != "cuda":
+    index = k_pool.get_device()
+    if index < 0:
         raise TypeError("the pools must be CUDA tensors")
-    _on(dev, "decode_attn_append_8bit", k_new, v_new, slot_map, v_pool, k_scale, v_scale)
-    _launch(dev, stream, N.load().decode_attn_append_8bit, ctypes.byref(append),
+    if not index == k_new.get_device() == v_new.get_device() == slot_map.get_device() \
+            == v_pool.get_device() == k_scale.get_device() == v_scale.get_device():
+        _on(k_pool.device, "decode_attn_append_8bit", k_new, v_new, slot_map, v_pool, k_scale,
+            v_scale)
+    if (k_new.shape, k_new.stride(), v_new.shape, v_new.stride(), k_new.dtype, v_new.dtype,
+            k_pool.shape, k_pool.stride(), v_pool.shape, v_pool.stride(), k_pool.dtype,
+            v_pool.dtype, k_scale.shape, k_scale.stride(), v_scale.shape, v_scale.stride(),
+            k_scale.dtype, v_scale.dtype) != getattr(append, "tensors", None):
+        # (a descriptor filled in by hand, or one for other tensors)
+        if bytes(make_append(k_new, v_new, k_pool, v_pool, k_scale, v_scale)) != bytes(append):
+            raise ValueError("append describes tensors of other shapes, strides or types")
+    _append_8bit(append, k_new, v_new, slot_map, k_pool, v_pool, k_scale, v_scale, stream)
+
+
+def _append_8bit(append, k_new, v_new, slot_map, k_pool, v_pool, k_scale, v_scale,
+                 stream) -> None:
+    _launch(k_pool.device, stream, N.load().decode_attn_append_8bit, ctypes.byref(append),
             k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), k_pool.data_ptr(),
             v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
 

@@ -85,8 +85,10 @@ class PagedCache8:
         if shapes != self._shapes:
             self._append = A.make_append(k_new, v_new, self.k, self.v, self.k_scale, self.v_scale)
             self._shapes = shapes
+        if not k_new.device == v_new.device == self.k.device:
+            raise ValueError(f"new rows must be on {self.k.device}")
         slots, n = self.slot_map, k_new.shape[0]
-        A.decode_attn_append_8bit(self._append, k_new, v_new,
+        A._append_8bit(self._append, k_new, v_new,
                                   slots if n == slots.numel() else slots[:n], self.k, self.v,
                                   self.k_scale, self.v_scale, stream)
 

@@ -118,3 +118,49 @@ def test_a_step_takes_its_own_shapes_alone(launches):
         with pytest.raises((TypeError, ValueError)):
             s(q, out)
     assert len(launches) == 1
+
+
+def append(new=(5, 2, 128), pool=POOL, src=torch.bfloat16, **kw):
+    t = dict(k_new=Fake(new, src), v_new=Fake(new, src), k=Fake(pool, E4), v=Fake(pool, E4),
+             ks=Fake(pool[::2][:2]), vs=Fake(pool[::2][:2]), slots=Fake(new[:1], torch.int64))
+    a = A.make_append(t["k_new"], t["v_new"], t["k"], t["v"], t["ks"], t["vs"])
+    t.update(kw)
+    A.decode_attn_append_8bit(t.get("append", a), t["k_new"], t["v_new"], t["slots"], t["k"],
+                              t["v"], t["ks"], t["vs"])
+    return a
+
+
+def test_append_takes_what_it_was_made_for(launches):
+    a = append()
+    by_hand = N.DaAppend.from_buffer_copy(a)
+    append(append=by_hand)
+    assert len(launches) == 2
+    with pytest.raises(ValueError):
+        append(append=by_hand, k_new=Fake((5, 2, 128), torch.float32))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_new=Fake((4, 2, 128), torch.bfloat16)), dict(v_new=Fake((5, 2, 64), torch.bfloat16)),
+    dict(k_new=Fake((5, 2, 128), torch.float32), v_new=Fake((5, 2, 128), torch.float32)),
+    dict(k_new=Fake((5, 2, 128), torch.bfloat16, (512, 128, 1))),
+    dict(k=Fake((39, 16, 2, 128), E4)), dict(v=Fake(POOL, E5)), dict(k=Fake(POOL, E5), v=Fake(POOL, E5)),
+    dict(ks=Fake((39, 2))), dict(vs=Fake((40, 2), torch.float16)), dict(vs=Fake((40, 2), stride=(1, 40))),
+    dict(slots=Fake((4,), torch.int64)), dict(slots=Fake((5,), torch.int32)),
+    dict(ks=Fake((40, 2), device=torch.device("cuda", 1)))])
+def test_append_refuses_other_tensors_than_described(launches, kw):
+    with pytest.raises((TypeError, ValueError)):
+        append(**kw)
+    assert not launches
+
+
+def test_a_cache_appends_rows_of_its_device_alone(launches):
+    c = C.PagedCache8.__new__(C.PagedCache8)
+    c.k, c.v, c.k_scale, c.v_scale = Fake(POOL, E4), Fake(POOL, E4), Fake((40, 2)), Fake((40, 2))
+    c.slot_map, c._shapes, c._append = Fake((5,), torch.int64), None, None
+    rows = [Fake((5, 2, 128), torch.float16, device=torch.device("cuda", i)) for i in (0, 0, 1)]
+    c.append(rows[0], rows[1])
+    assert len(launches) == 1
+    for k, v in ((rows[0], rows[2]), (rows[2], rows[0])):
+        with pytest.raises(ValueError):
+            c.append(k, v)
+    assert len(launches) == 1
