@@ -187,6 +187,11 @@ def make_dev(*, seq_lens: Optional[torch.Tensor] = None,
         d.k_block_stride = k_pool.stride(0)
         d.v_block_stride = v_pool.stride(0)
         d.pools = _pools(k_pool, v_pool)
+    # (of this object alone, no fields of the struct: for decode_attn_splitk_8bit)
+    given = [t for t in (seq_lens, block_table) if t is not None]
+    if given:
+        d.devices = [t.get_device() for t in given]
+        d.batch = min(t.shape[0] if t.dim() == 2 else t.numel() for t in given)
     return d
 
 
@@ -338,6 +343,7 @@ def make_tables(seq_lens: torch.Tensor, block_table: torch.Tensor, free_list: to
     if state.shape[0] != 4 or state_out.shape[0] != 4:
         raise ValueError("state must hold 4 words")
     t = N.DaTables()
+    t.device = seq_lens.get_device()          # (of this object alone, no field of the struct)
     t.seq_lens, t.seq_lens_out = seq_lens.data_ptr(), seq_lens_out.data_ptr()
     t.block_table, t.free_list = block_table.data_ptr(), free_list.data_ptr()
     t.state, t.state_out = state.data_ptr(), state_out.data_ptr()
@@ -362,6 +368,8 @@ def decode_attn_grow_tables(tables: N.DaTables, new_lens: torch.Tensor,
                                or cu_new.numel() != tables.batch + 1):
         raise TypeError("cu_new must be a contiguous int32 tensor of batch + 1 entries")
     _on(dev, "decode_attn_grow_tables", slot_map, cu_new)
+    if getattr(tables, "device", dev.index) != dev.index:
+        raise ValueError(f"the tables are on cuda:{tables.device}, new_lens on {dev}")
     _launch(dev, stream, N.load().decode_attn_grow_tables, ctypes.byref(tables),
             new_lens.data_ptr(), slot_map.data_ptr(), slot_map.numel(),
             0 if cu_new is None else cu_new.data_ptr())
@@ -454,7 +462,12 @@ def make_scales(k_scale: torch.Tensor, v_scale: torch.Tensor) -> N.DaScales:
     for t in (k_scale, v_scale):
         if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2:
             raise TypeError("scales must be 2-D float32 CUDA tensors")
+    if k_scale.get_device() != v_scale.get_device():
+        raise ValueError("scales must be on one device")
     s = N.DaScales()
+    # (of this object alone, no fields of the struct: for decode_attn_splitk_8bit)
+    s.devices = [k_scale.get_device()]
+    s.blocks, s.heads = [min(n) for n in zip(k_scale.shape, v_scale.shape)]
     s.k_scale, s.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
     s.k_block_stride, s.k_head_stride = k_scale.stride()
     s.v_block_stride, s.v_head_stride = v_scale.stride()
@@ -483,7 +496,21 @@ def decode_attn_splitk_8bit(args: N.DaArgs, plan: N.DaPlan, dev: N.DaDev, scales
     pools = _pools(k_pool, v_pool)
     if not pools == getattr(args, "pools", None) == getattr(dev, "pools", None):
         _check_pools(args, dev, k_pool, v_pool)
+    _check_descriptors(index, args, dev, scales)
     _splitk_8bit(args, plan, dev, scales, q, k_pool, v_pool, out, workspace, stream)
+
+
+def _check_descriptors(index: int, args: N.DaArgs, dev: N.DaDev, scales: N.DaScales) -> None:
+    """Raises unless the tensors behind dev and scales are on the call's device and hold its
+    batch and pages (of descriptors that make_dev and make_scales made)."""
+    for what, x in (("lengths and table", dev), ("scales", scales)):
+        if getattr(x, "devices", None) not in (None, [index], [index, index]):
+            raise ValueError(f"the {what} must be on q's device, cuda:{index}")
+    if getattr(dev, "batch", args.batch) < args.batch:
+        raise ValueError(f"the lengths and table hold {dev.batch} sequences, q {args.batch}")
+    if getattr(scales, "blocks", dev.num_blocks) < dev.num_blocks or \
+            getattr(scales, "heads", args.n_kv_heads) < args.n_kv_heads:
+        raise ValueError(f"the scales must be [{dev.num_blocks}, {args.n_kv_heads}]")
 
 
 def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor) -> tuple:

@@ -164,3 +164,52 @@ def test_a_cache_appends_rows_of_its_device_alone(launches):
         with pytest.raises(ValueError):
             c.append(k, v)
     assert len(launches) == 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lens=Fake((2,), torch.int32)), dict(table=Fake((2, 10), torch.int32)),
+    dict(ks=Fake((39, 2))), dict(vs=Fake((40, 1)))])
+def test_attention_refuses_descriptors_that_hold_too_little(launches, kw):
+    t = dict(lens=Fake((3,), torch.int32), table=Fake((3, 10), torch.int32), ks=Fake((40, 2)),
+             vs=Fake((40, 2)))
+    t.update(kw)
+    q, k, v, out = Fake((3, 8, 128)), Fake(POOL, E4), Fake(POOL, E4), Fake((3, 8, 128))
+    a = A.make_paged_args(q, k, v, 0.1, 10)
+    dev = A.make_dev(seq_lens=t["lens"], block_table=t["table"], k_pool=k, v_pool=v)
+    with pytest.raises(ValueError):
+        A.decode_attn_splitk_8bit(a, N.DaPlan(), dev, A.make_scales(t["ks"], t["vs"]), q, k, v,
+                                  out, Fake((4096,), torch.uint8))
+    assert not launches
+
+
+OTHER = torch.device("cuda", 1)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lens=Fake((3,), torch.int32, device=OTHER)),
+    dict(table=Fake((3, 10), torch.int32, device=OTHER)),
+    dict(lens=Fake((3,), torch.int32, device=OTHER), table=Fake((3, 10), torch.int32, device=OTHER)),
+    dict(ks=Fake((40, 2), device=OTHER), vs=Fake((40, 2), device=OTHER)),
+    dict(vs=Fake((40, 2), device=OTHER))])
+def test_attention_refuses_descriptors_of_another_device(launches, kw):
+    t = dict(lens=Fake((3,), torch.int32), table=Fake((3, 10), torch.int32), ks=Fake((40, 2)),
+             vs=Fake((40, 2)))
+    t.update(kw)
+    q, k, v, out = Fake((3, 8, 128)), Fake(POOL, E4), Fake(POOL, E4), Fake((3, 8, 128))
+    a = A.make_paged_args(q, k, v, 0.1, 10)
+    dev = A.make_dev(seq_lens=t["lens"], block_table=t["table"], k_pool=k, v_pool=v)
+    with pytest.raises(ValueError):
+        A.decode_attn_splitk_8bit(a, N.DaPlan(), dev, A.make_scales(t["ks"], t["vs"]), q, k, v,
+                                  out, Fake((4096,), torch.uint8))
+    assert not launches
+
+
+def test_tables_of_another_device_are_refused(launches):
+    t = A.make_tables(Fake((3,), torch.int32), Fake((3, 10), torch.int32),
+                      Fake((40,), torch.int32), Fake((4,), torch.int32), 16)
+    A.decode_attn_grow_tables(t, Fake((3,), torch.int32), Fake((9,), torch.int64))
+    assert len(launches) == 1
+    with pytest.raises(ValueError):
+        A.decode_attn_grow_tables(t, Fake((3,), torch.int32, device=OTHER),
+                                  Fake((9,), torch.int64, device=OTHER))
+    assert len(launches) == 1
