@@ -46,8 +46,14 @@ class PagedCache8:
         self.v_scale = torch.ones(num_blocks, n_kv_heads, device=device)
         self.scales = A.make_scales(self.k_scale, self.v_scale)
         if tables_of is not None:
-            if (tables_of.block_size, tables_of.free_list.numel()) != (block_size, num_blocks):
+            t = tables_of
+            if (t.block_size, t.free_list.numel()) != (block_size, num_blocks):
                 raise ValueError("caches that share tables need equal pages")
+            if tuple(t.block_table.shape) != (max_batch, max_blocks_per_seq) \
+                    or max_new not in (None, t.slot_map.numel()):
+                raise ValueError("caches that share tables need equal batches, widths and rows")
+            if t.block_table.device != self.k.device:
+                raise ValueError(f"the tables are on {t.block_table.device}, not {self.k.device}")
             for name in ("seq_lens", "block_table", "free_list", "state", "slot_map", "cu_new",
                          "tables"):
                 setattr(self, name, getattr(tables_of, name))

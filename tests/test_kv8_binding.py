@@ -213,3 +213,35 @@ def test_tables_of_another_device_are_refused(launches):
         A.decode_attn_grow_tables(t, Fake((3,), torch.int32, device=OTHER),
                                   Fake((9,), torch.int64, device=OTHER))
     assert len(launches) == 1
+
+
+class Shared:
+    """A cache whose tables another shares, as far as the other looks at it."""
+
+    def __init__(self, device=torch.device("cpu"), batch=3, width=10, rows=6):
+        self.block_size = 16
+        self.free_list = torch.zeros(40, dtype=torch.int32, device=device)
+        self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.block_table = torch.zeros(batch, width, dtype=torch.int32, device=device)
+        self.slot_map = torch.zeros(rows, dtype=torch.int64, device=device)
+        self.state, self.cu_new, self.tables = None, None, None
+
+
+def share(of, **kw):
+    """A cache on the CPU, as far as its tables; make_dev and make_scales refuse CPU tensors."""
+    args = dict(max_batch=3, num_blocks=40, max_blocks_per_seq=10, n_kv_heads=2, head_dim=128,
+                block_size=16, device="cpu")
+    args.update(kw)
+    return C.PagedCache8(tables_of=of, **args)
+
+
+@pytest.mark.parametrize("kw,of", [
+    (dict(max_batch=4), {}), (dict(max_blocks_per_seq=9), {}), (dict(max_new=5), {}),
+    (dict(block_size=32), {}), (dict(num_blocks=41), {}), ({}, dict(device="meta"))])
+def test_caches_that_share_tables_agree_in_them(monkeypatch, kw, of):
+    monkeypatch.setattr(A, "make_dev", lambda **kw: N.DaDev())
+    monkeypatch.setattr(A, "make_scales", lambda *x: N.DaScales())
+    for right in ({}, dict(max_new=6)):
+        assert share(Shared(), **right).slot_map.numel() == 6
+    with pytest.raises(ValueError):
+        share(Shared(**of), **kw)
