@@ -378,8 +378,9 @@ def decode_attn_grow_tables(tables: N.DaTables, new_lens: torch.Tensor,
 def decode_attn_tables_status(state: torch.Tensor, stream=None) -> None:
     """Synchronises; raises if a decode_attn_grow_tables call on this state failed
     since the last check (and clears the status)."""
-    if state.dtype != torch.int32 or not state.is_cuda:
-        raise TypeError("state must be an int32 CUDA tensor")
+    if state.dtype != torch.int32 or not state.is_cuda or state.numel() != 4 \
+            or not state.is_contiguous():
+        raise TypeError("state must be a contiguous int32 CUDA tensor of 4 words")
     _launch(state.device, stream, N.load().decode_attn_tables_status, state.data_ptr())
 
 

@@ -245,3 +245,14 @@ def test_caches_that_share_tables_agree_in_them(monkeypatch, kw, of):
         assert share(Shared(), **right).slot_map.numel() == 6
     with pytest.raises(ValueError):
         share(Shared(**of), **kw)
+
+
+@pytest.mark.parametrize("state", [Fake((2,), torch.int32), Fake((8,), torch.int32, (2,)),
+                                   Fake((4,), torch.int32, (2,)), Fake((4,), torch.int64),
+                                   Fake((4,), torch.int32, device=torch.device("cpu"))])
+def test_the_status_wants_a_state_of_four_words(launches, state):
+    with pytest.raises((TypeError, ValueError)):
+        A.decode_attn_tables_status(state)
+    assert not launches
+    A.decode_attn_tables_status(Fake((4,), torch.int32))
+    assert len(launches) == 1
