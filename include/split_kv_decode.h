@@ -620,8 +620,10 @@ typedef struct da_scales_t {
  *     (DA_FLAG_ONE_LAUNCH changes nothing).
  * Codes past a sequence's length may hold anything, NaN among them. With
  * q_len > 1 a NaN in a new token's row reaches only the tokens that see it.
- * decode_attn_combine, _combine_ranks and _combine_proj take its partials; the
- * other split calls refuse an 8-bit plan (DA_EUNSUPPORTED).
+ * decode_attn_combine, _combine_ranks and _combine_proj take its partials (of a plan of
+ * one split per sequence only with DA_FLAG_NO_COMBINE in args->flags of both calls; they
+ * refuse it otherwise, DA_EINVAL); the other split calls refuse an 8-bit plan
+ * (DA_EUNSUPPORTED).
  */
 int decode_attn_splitk_8bit(const da_args_t *args, const da_plan_t *plan, const da_dev_t *dev,
                             const da_scales_t *scales, const float *q, const void *k_pool,

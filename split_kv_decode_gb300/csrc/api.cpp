@@ -756,6 +756,17 @@ int refuse_8bit(const da_args_t *a)
     return DA_OK;
 }
 
+// the combines need partials, which the 8-bit kernel does not write where it writes the output
+int refuse_whole(const da_args_t *a, const da_plan_t *pl)
+{
+    if (pl->kernel == DA_KERNEL_GQA_8BIT && pl->max_splits == 1 &&
+        !(a->flags & DA_FLAG_NO_COMBINE))
+        return fail(DA_EINVAL, "args",
+                    "an 8-bit plan of one split per sequence leaves partials only with "
+                    "DA_FLAG_NO_COMBINE in args->flags");
+    return DA_OK;
+}
+
 // the block table of dev and the strides of its pools, and a plan whose chunks
 // start where a box of the tile's copies may
 int check_table(const da_args_t *a, const da_plan_t *plan, const da_dev_t *dev, bool box_chunks)
@@ -1019,6 +1030,7 @@ int decode_attn_combine_ranks(const da_args_t *a, const da_plan_t *plan, const v
     KernelChoice kc;
     rc = check_plan(a, plan, &kc);
     if (rc) return rc;
+    if ((rc = refuse_whole(a, plan))) return rc;
     if (n_ranks < 1 || n_ranks > 4096)
         return fail(DA_EINVAL, "args", "n_ranks %d outside [1, 4096]", n_ranks);
     if (!ws || !aligned(ws, 256)) return fail(DA_EINVAL, "args", "workspaces misaligned or NULL");
@@ -1039,6 +1051,7 @@ int decode_attn_combine_proj(const da_args_t *a, const da_plan_t *plan, const da
     KernelChoice kc;
     rc = check_plan(a, plan, &kc);
     if (rc) return rc;
+    if ((rc = refuse_whole(a, plan))) return rc;
     da_proj_t pj;
     rc = check_proj(a, proj, &pj);
     if (rc) return rc;
@@ -1092,6 +1105,7 @@ int decode_attn_combine(const da_args_t *a, const da_plan_t *plan, const void *w
     KernelChoice kc;
     rc = check_plan(a, plan, &kc);
     if (rc) return rc;
+    if ((rc = refuse_whole(a, plan))) return rc;
     if (!ws || !aligned(ws, 256)) return fail(DA_EINVAL, "args", "workspace misaligned or NULL");
     if (!out || !aligned(out, 16)) return fail(DA_EINVAL, "args", "out misaligned or NULL");
     cudaError_t pre = cudaGetLastError();
