@@ -606,9 +606,9 @@ typedef struct da_scales_t {
  * plan was made for these args; dev->block_table is required. A contiguous cache
  * is a pool with an identity table. Keys and values are used as the codes stand,
  * q and the probabilities carry 24 significant bits for an f32 output and 20 for f16
- * and bf16 (the probabilities 16 in groups of more than 8 rows); sums are f32. In the sum
- * of the values a probability is off by 2^-22 (f32 output) or 2^-15 of the largest of its
- * 128 positions at most, and by 2^-32 or 2^-27 of one that exceeds all before it.
+ * and bf16; sums are f32. In the sum of the values a probability is off by 2^-22 (f32
+ * output) or 2^-15 of the largest of its 128 positions at most, and by 2^-32 or 2^-27 of
+ * one that exceeds all before it.
  * Differences to decode_attn_splitk_dev:
  *   - a device length is clamped to [0, plan->seq_lens[b]]. A sequence of length 0
  *     gives zeros, and so does a new token before the sequence's start (length

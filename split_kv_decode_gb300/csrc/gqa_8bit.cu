@@ -20,8 +20,7 @@
 // y = y_0 + 2^-5 y_1 + 2^-10 y_2 + ...: a term rounds what the ones before it left, and
 // each takes 5 bits off (4 significant bits and the sign of the rest). f32 outputs take
 // five terms of both, 25 bits: four of both left an error of 0.4 to 1.4e-6 there, as much as
-// or more than f32 arithmetic does. 16-bit outputs take four of both, 20 bits (of x 16 in
-// items of more than 8 rows, where the last three come from an f16).
+// or more than f32 arithmetic does. 16-bit outputs take four of both, 20 bits.
 // y is at most 256, and e4m3's least step, 2^-9, is 2^-24 or 2^-29 in the last term: half of
 // that is what a term of any size may be off by. Of q that is 2^-32 of the row's largest.
 // Weights differ by far more, and a small one can be one of many whose values are all there
@@ -216,22 +215,17 @@ __device__ __forceinline__ uint32_t term2(float &x, float &y)
     return c;
 }
 
-// The PT terms of two values, x in the low byte of each. The last HT are taken two values at
-// a time in f16: its 11 bits hold the 10 of two terms, and of three (of which the first leaves
-// 2^-4 of the value) all but 2^-16 of the value.
-template <int PT, int HT> __device__ __forceinline__ void terms(float x, float y, uint32_t *c)
+// The PT terms of two values, x in the low byte of each. What is left after all but two
+// fits an f16 (11 bits for 10), so the last two are taken two values at a time.
+template <int PT> __device__ __forceinline__ void terms(float x, float y, uint32_t *c)
 {
 #pragma unroll
-    for (int j = 0; j < PT - HT; ++j) c[j] = term2(x, y);
-    __half2 h = __floats2half2_rn(x, y);
-#pragma unroll
-    for (int j = PT - HT; j < PT; ++j) {
-        c[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-        if (j + 1 < PT) {
-            const __half2 f(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[j], __NV_E4M3));
-            h = __hmul2(__hsub2(h, f), __half2(__half(32.f), __half(32.f)));
-        }
-    }
+    for (int j = 0; j < PT - 2; ++j) c[j] = term2(x, y);
+    const __half2 h = __floats2half2_rn(x, y);
+    c[PT - 2] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+    const __half2 f(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[PT - 2], __NV_E4M3));
+    const __half2 rest = __hmul2(__hsub2(h, f), __half2(__half(32.f), __half(32.f)));
+    c[PT - 1] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
 }
 
 // how many of a barrier's threads have pred
@@ -329,8 +323,6 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     using L = Layout<D, RP, QT, PT>;
     constexpr int N = L::N, NP = L::NP, NCH = L::NCH, NS = L::NS, W = L::W, RPW = L::RPW,
                   X = L::X, WT = L::WT;
-    // terms of x taken in f16, three in wide items with 16-bit outputs
-    constexpr int HT = RP > 8 && PT == 4 ? 3 : 2;
     // a tile's largest weight is 2^-kLow at least, half a step of the terms 2^-30 or 2^-25
     constexpr float kLow = PT == 5 ? 8.f : 10.f;
     constexpr int RC = 4; // rows taken from TMEM at a time
@@ -1069,7 +1061,7 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
                 }
                 uint32_t c[RPW / 2][PT]; // codes of two rows
 #pragma unroll
-                for (int r = 0; r < RPW; r += 2) terms<PT, HT>(a[r], a[r + 1], c[r / 2]);
+                for (int r = 0; r < RPW; r += 2) terms<PT>(a[r], a[r + 1], c[r / 2]);
 #pragma unroll
                 for (int j = 0; j < PT; ++j) {
                     const uint32_t at = pt + swz(tid, j * RP + r00);
