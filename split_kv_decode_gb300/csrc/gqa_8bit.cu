@@ -37,18 +37,18 @@
 //
 // An item is (sequence, KV head, split, row group), rows (query token, head). Roles, one
 // CTA per SM:
-//   softmax warpgroups (1 to 4, up to 8 rows each; for 5 to 8 rows of 128 two of them take
-//              tiles in turn): a thread owns one position of the tile (TMEM lane); the
+//   softmax warpgroups (1 to 4, up to 8 rows each; for 5 to 16 rows of 128 two sets of them
+//              take tiles in turn): a thread owns one position of the tile (TMEM lane); the
 //              references stay for most tiles, which take one vote. In the epilogue a thread
 //              owns a value column.
 //   two warps  TMA producers, K and V tiles through one ring of slots, paged boxes as in the
 //              16-bit tensor-core kernel.
 //   two warps  MMA issue, one thread each for the scores and for the values.
-//   one warp   the page scales of four tiles at a time, two batches ahead (the K producer does
-//              it beside many softmax warps).
+//   one warp   the page scales of four tiles at a time (beside three or four softmax
+//              warpgroups the K producer does it, looking them up two batches ahead).
 // Where every sequence has one split there is nothing to merge: the epilogue divides by l
 // and writes the output itself, and no combine follows (256 sequences of 40 positions, 32/8
-// heads of 128: 38 us instead of 56; 128 of 100, 32 heads of 256 over one: 9 instead of 28).
+// heads of 128: 41 us instead of 60; 128 of 100, 32 heads of 256 over one: 14 instead of 34).
 // Every wait is bounded; a wait that runs out sets the status word and the CTA drains
 // and returns.
 #include <climits>
@@ -90,20 +90,21 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_SFULL = 2 * kMaxSlots, B_SFREE 
 // softmax warpgroup takes RPW rows of every tile, 8, or 4 where that is enough: a
 // thread's share of a tile must not outlast the tile's time on the memory side, and 32
 // rows in one thread took 5200 cycles against 2800. Smaller shares repeat more of a tile's
-// fixed part: 16 rows of 128 as 4 x 4 took 70 us instead of 61 (1.2M positions, bf16), 8
-// rows of 128 as 2 x 4 in one set 58 instead of 53.5; 8 rows of 256, whose tiles take
-// twice the time, 51.7 as 2 x 4 and 53.5 as one 8.
+// fixed part: 8 rows of 128 as 2 x 4 in one set take 60.1 us instead of 56.9 (1.2M positions,
+// bf16), 16 as 4 x 4 69.4 instead of 68.4 as 2 x 8; 8 rows of 256, whose tiles take twice the
+// time, 54.3 as 2 x 4 and 58.3 as one 8.
 template <int D, int RP, int QT, int PT> struct Layout {
     static constexpr int N = (QT * RP + 15) / 16 * 16;  // columns of S
     static constexpr int NP = (PT * RP + 15) / 16 * 16; // columns of O^T
     static constexpr int W = RP > 8 ? RP / 8 : RP == 8 && D == 256 ? 2 : 1; // per tile
     static constexpr int RPW = RP / W;
-    // 5 to 8 rows of 128 columns: two sets of warpgroups take turns, each with its own
+    // 5 to 16 rows of 128 columns: two sets of warpgroups take turns, each with its own
     // references and its own O^T, joined at the item's end. There a tile's waits, vote, terms
-    // and fences add up to 1800 cycles, the memory side's share to 1400 (1.2M positions: 60 us
-    // with one set, 53.6 with two; 4 rows take 52 with either, 16 rows 71 and 74 (64 and 70
-    // with bf16 outputs) for want of registers, and 256 columns have twice the time).
-    static constexpr int X = D == 128 && RP == 8 ? 2 : 1;
+    // and fences add up to 1800 cycles and more, the memory side's share to 1400 (1.2M
+    // positions, bf16: 8 rows 59.9 us with one set, 56.9 with two; 16 rows 68.4 and 66.6, with
+    // f32 outputs 71.9 and 69.1; 4 rows 53.9 with either, but 256 sequences of 40 positions 41.0
+    // and 44.4; 24 rows would be 28 warps; 256 columns have twice the time).
+    static constexpr int X = D == 128 && (RP == 8 || RP == 16) ? 2 : 1;
     static constexpr int WT = W * X; // softmax warpgroups
     // Warps after the softmax warps. Beside three or four warpgroups the K producer fetches
     // the page scales too: a warp less, a thread has 128 registers and not 96, or 96 and not
@@ -326,8 +327,8 @@ __global__ void __launch_bounds__((Layout<D, RP, QT, PT>::THREADS), 1)
     // a tile's largest weight is 2^-kLow at least, half a step of the terms 2^-30 or 2^-25
     constexpr float kLow = PT == 5 ? 8.f : 10.f;
     constexpr int RC = 4; // rows taken from TMEM at a time
-    // and of the scores: 8 at a time save a round trip where they fit the registers (16 rows
-    // of 128, 1.2M positions: 63 -> 60.5 us; 8 and 24 rows spill and lose 1%)
+    // and of the scores: 8 at a time save a round trip where they fit the registers (16 rows of
+    // 128, 1.2M positions, f32: 73.5 -> 71.9 us; 24 rows 83.4 -> 87.0, 32 bf16 93.6 -> 98.4)
     constexpr int SC = RP == 16 ? RPW : RC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
