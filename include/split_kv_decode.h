@@ -462,7 +462,9 @@ int decode_attn_splitk_dev(const da_args_t *args, const da_plan_t *plan, const d
  * Pools of 8-bit floating-point codes [num_blocks][block_size][n_kv_heads][dim]
  * (any strides, as in da_dev_t) with one f32 scale per (block, KV head) for the
  * keys and one for the values: the element a code c of block i and head h
- * stands for is c * scale[i][h]. Three calls of a decode step, each
+ * stands for is c * scale[i][h]; codes are finite numbers or NaN (e5m2's infinities are no
+ * values: the append writes none, and what an attention over one gives is not specified).
+ * Three calls of a decode step, each
  * capturable in a CUDA graph:
  *   decode_attn_grow_tables   block table and slots of the new tokens
  *   decode_attn_append_8bit   the new rows, quantised into their slots
@@ -524,6 +526,9 @@ typedef struct da_tables_t {
  * holds the status, until decode_attn_tables_status reads and clears it (an
  * earlier one is kept). One launch. seq_lens, state, new_lens and free_list must
  * not change, and no second call run on the same state, while one is in flight.
+ * Between calls too, lengths change by these calls alone: which blocks a sequence holds
+ * follows from its length, so one that is lowered by hand past a block's first position
+ * loses that block for good.
  */
 int decode_attn_grow_tables(const da_tables_t *tables, const int32_t *new_lens,
                             int64_t *slot_map, int64_t slot_capacity, int32_t *cu_new,
@@ -607,8 +612,8 @@ typedef struct da_scales_t {
  * is a pool with an identity table. Keys and values are used as the codes stand,
  * q and the probabilities carry 24 significant bits for an f32 output and 20 for f16
  * and bf16; sums are f32. In the sum of the values a probability is off by 2^-22 (f32
- * output) or 2^-15 of the largest of its 128 positions at most, and by 2^-32 or 2^-27 of
- * one that exceeds all before it.
+ * output) or 2^-15 of the largest of its 128 positions at most (of 2^-64 of the largest
+ * so far, if all 128 are below that), and by 2^-32 or 2^-27 of one that exceeds all before.
  * Differences to decode_attn_splitk_dev:
  *   - a device length is clamped to [0, plan->seq_lens[b]]. A sequence of length 0
  *     gives zeros, and so does a new token before the sequence's start (length

@@ -106,7 +106,12 @@ class PagedCache8:
 class Step8:
     """Attention of q [B, Hq, D] (or [B, q_len, Hq, D]) over a PagedCache8, B at most the
     cache's max_batch: plan and workspace for sequences of up to `max_lens` positions
-    (default: the tables' width); the current lengths are the cache's, on the device."""
+    (default: the tables' width); the current lengths are the cache's, on the device.
+
+    The work is split for max_lens, whatever the lengths are then: a bound near them is
+    up to several times faster than the width of mostly empty tables. Positions past it
+    are not attended to. Calls that overlap on the GPU need steps of their own (one
+    workspace each)."""
 
     def __init__(self, cache: PagedCache8, q: torch.Tensor, scale: Optional[float] = None, *,
                  max_lens: Optional[Sequence[int]] = None,
