@@ -635,6 +635,94 @@ int decode_attn_splitk_8bit(const da_args_t *args, const da_plan_t *plan, const 
                             const void *v_pool, void *out, void *workspace,
                             size_t workspace_bytes, da_stream_t stream);
 
+/*
+ * ---- between the projections and the attention ----------------------------
+ * decode_attn_rope_append takes the new tokens' rows of a layer's projections to where
+ * the attention reads them: queries and keys normalised head by head and rotated to
+ * their positions, queries into rows of their own, keys and values into the slots of a
+ * cache of 16 or 32 bits.
+ */
+#define DA_MAX_ROT_PAIRS 128
+#define DA_MAX_ROT_AXES 8
+
+/*
+ * The rotation. Of a head's head_dim columns the first rot_dim are rot_dim / 2 pairs (a, b):
+ * columns (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved. Pair i turns by the angle
+ * position[axis[i]] * inv_freq[i]:
+ *   a' = factor (a cos - b sin),  b' = factor (b cos + a sin)
+ * Several axes (time, height and width of an image or a video) have a position each; text
+ * has one axis, or the same position on all of them.
+ *   turns  DEVICE uint64[rot_dim / 2]: inv_freq[i] / (2 pi), modulo 1, times 2^64 and rounded
+ *          (modulo 2^64). Times a position, modulo 2^64, this is the angle's fraction of a
+ *          turn, off by 2^-65 per position.
+ */
+typedef struct da_rope_t {
+    const uint64_t *turns;
+    int32_t rot_dim;      /* a multiple of 16, at most head_dim; 0: no rotation     */
+    int32_t n_axes;       /* 1 .. DA_MAX_ROT_AXES                                   */
+    int32_t interleaved;  /* 0: pairs of halves, 1: neighbours                      */
+    float factor;         /* scales the rotated columns, usually 1                  */
+    uint8_t axis[DA_MAX_ROT_PAIRS]; /* of each pair, below n_axes                   */
+} da_rope_t;
+
+/*
+ * The shapes of decode_attn_rope_append. Strides in elements; every row of a (token, head)
+ * starts 16-byte aligned.
+ *   sources  (token, head, d) at base + token * *_src_stride + head * *_src_head_stride + d,
+ *            of type src_dtype, e.g. the parts of a fused projection
+ *   q_out    (token, head, d) at base + token * q_out_stride + head * q_out_head_stride + d,
+ *            of type q_dtype; may be q itself (same type and strides)
+ *   pools    as in da_dev_t, of type cache_dtype
+ *   weights  (head, d) at base + head * *_weight_head_stride + d, of type w_dtype; stride 0: one
+ *            weight for all heads; NULL: 1
+ * Types are DA_F32, DA_F16 or DA_BF16, each on its own; head_dim and v_dim multiples of 8, at
+ * most 256.
+ */
+typedef struct da_prep_t {
+    int32_t n_tokens;     /* at most 2^30; 0: nothing to do                         */
+    int32_t n_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t v_dim;
+    int32_t block_size;   /* any positive number                                    */
+    int32_t num_blocks;
+    int32_t src_dtype;
+    int32_t q_dtype;
+    int32_t cache_dtype;
+    int32_t w_dtype;
+    int32_t norm;         /* 0: rows as they are; 1: of q and k, y = x (mean(x^2) +
+                             eps)^-1/2 (weight_offset + weight) over head_dim columns */
+    float eps;
+    float weight_offset;  /* 0, or 1 where a model stores its weights less one (not
+                             added to a NULL weight)                                */
+    const void *q_weight;
+    const void *k_weight;
+    int64_t q_weight_head_stride, k_weight_head_stride;
+    int64_t q_src_stride, q_src_head_stride;
+    int64_t k_src_stride, k_src_head_stride;
+    int64_t v_src_stride, v_src_head_stride;
+    int64_t q_out_stride, q_out_head_stride;
+    int64_t k_block_stride, k_pos_stride, k_head_stride;
+    int64_t v_block_stride, v_pos_stride, v_head_stride;
+} da_prep_t;
+
+/*
+ * decode_attn_rope_append -- one pass over the new rows.
+ *   positions  DEVICE int64[n_axes][n_tokens]: of every token, on every axis; any number
+ *              (not read if rot_dim is 0)
+ *   slot_map   DEVICE int64[n_tokens]: block * block_size + position in the block of every
+ *              token, as decode_attn_grow_tables writes it; a negative slot, or one past the
+ *              pool, leaves the pools alone (q_out is written for every token). Two tokens
+ *              must not have one slot. NULL: token t has slot t, so that rows of their
+ *              own, e.g. for decode_attn_append_8bit, are a pool of one block.
+ * Arithmetic is in f32 and each element is rounded once; values are copied. Pools and q_out
+ * must not overlap the sources, except for q_out == q. One launch.
+ */
+int decode_attn_rope_append(const da_prep_t *shapes, const da_rope_t *rope, const void *q,
+                            const void *k, const void *v, const int64_t *positions,
+                            const int64_t *slot_map, void *q_out, void *k_pool, void *v_pool,
+                            da_stream_t stream);
+
 /* Thread-local description of the last failure on this thread ("" if none). */
 const char *decode_attn_last_error(void);
 

@@ -115,6 +115,40 @@ class DaScales(ctypes.Structure):
     ]
 
 
+DA_MAX_ROT_PAIRS = 128
+DA_MAX_ROT_AXES = 8
+
+
+class DaRope(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float),
+        ("axis", ctypes.c_uint8 * DA_MAX_ROT_PAIRS),
+    ]
+
+
+class DaPrep(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("v_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32), ("src_dtype", ctypes.c_int32),
+        ("q_dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("q_weight_head_stride", ctypes.c_int64), ("k_weight_head_stride", ctypes.c_int64),
+        ("q_src_stride", ctypes.c_int64), ("q_src_head_stride", ctypes.c_int64),
+        ("k_src_stride", ctypes.c_int64), ("k_src_head_stride", ctypes.c_int64),
+        ("v_src_stride", ctypes.c_int64), ("v_src_head_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("k_block_stride", ctypes.c_int64), ("k_pos_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_block_stride", ctypes.c_int64), ("v_pos_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
 SIGNATURES = {
     "decode_attn_plan": (ctypes.c_int, [ctypes.POINTER(DaArgs), _P, ctypes.c_int,
                                         ctypes.POINTER(DaPlan)]),
@@ -147,6 +181,8 @@ SIGNATURES = {
     "decode_attn_splitk_8bit": (ctypes.c_int, [ctypes.POINTER(DaArgs), ctypes.POINTER(DaPlan),
                                                ctypes.POINTER(DaDev), ctypes.POINTER(DaScales),
                                                _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "decode_attn_rope_append": (ctypes.c_int, [ctypes.POINTER(DaPrep), ctypes.POINTER(DaRope), _P,
+                                               _P, _P, _P, _P, _P, _P, _P, _P]),
     "decode_attn_last_error": (ctypes.c_char_p, []),
     "decode_attn_release": (None, []),
     "decode_attn_version": (ctypes.c_char_p, []),

@@ -539,3 +539,135 @@ def _splitk_8bit(args, plan, dev, scales, q, k_pool, v_pool, out, workspace, str
             ctypes.byref(plan), ctypes.byref(dev), ctypes.byref(scales), q.data_ptr(),
             k_pool.data_ptr(), v_pool.data_ptr(), out.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
+
+
+# ---- between the projections and the attention ---------------------------------------
+
+_TWO_PI_TOP = 50                         # digits of 2 pi after the point
+_TWO_PI = 628318530717958647692528676655900576839433879875021
+
+
+def make_rope(inv_freq, *, axes: Optional[Sequence[int]] = None, interleaved: bool = False,
+              factor: float = 1.0, device=None) -> N.DaRope:
+    """da_rope_t for the frequencies inv_freq [rot_dim / 2] (a tensor or a sequence, taken as
+    the numbers they are): pair i of a head turns by position[axes[i]] * inv_freq[i]. axes: one
+    axis by default. interleaved: pairs are neighbouring columns, not halves. The
+    descriptor keeps its table alive."""
+    if isinstance(inv_freq, torch.Tensor):
+        if device is None and inv_freq.is_cuda:
+            device = inv_freq.device
+        inv_freq = inv_freq.detach().double().cpu().reshape(-1).tolist()
+    freqs = [float(f) for f in inv_freq]
+    n = len(freqs)
+    if n % 8 or n > N.DA_MAX_ROT_PAIRS:
+        raise ValueError(f"inv_freq must hold a multiple of 8 frequencies, at most "
+                         f"{N.DA_MAX_ROT_PAIRS}")
+    if not all(math.isfinite(f) for f in freqs):
+        raise ValueError("inv_freq must be finite")
+    axes = [0] * n if axes is None else [int(a) for a in axes]
+    if len(axes) != n or any(a < 0 or a >= N.DA_MAX_ROT_AXES for a in axes):
+        raise ValueError(f"axes must give one of {N.DA_MAX_ROT_AXES} axes for each frequency")
+    turns = []
+    for f in freqs:                      # f / (2 pi) * 2^64, rounded, in whole numbers
+        num, den = f.as_integer_ratio()
+        num, den = num * 10 ** _TWO_PI_TOP << 64, den * _TWO_PI
+        t = (2 * num + den) // (2 * den) % (1 << 64)
+        turns.append(t - (1 << 64) if t >> 63 else t)
+    r = N.DaRope()
+    r.table = torch.tensor(turns, dtype=torch.int64, device=device or "cuda")
+    r.turns = r.table.data_ptr()
+    r.rot_dim, r.n_axes = 2 * n, max(axes, default=0) + 1
+    r.interleaved, r.factor = int(bool(interleaved)), float(factor)
+    for i, a in enumerate(axes):
+        r.axis[i] = a
+    return r
+
+
+def make_prep(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_out: torch.Tensor,
+              k_pool: torch.Tensor, v_pool: torch.Tensor, rope: N.DaRope, *,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: Optional[float] = None, weight_offset: float = 0.0) -> N.DaPrep:
+    """da_prep_t for new rows q [T, Hq, D], k [T, Hkv, D] and v [T, Hkv, Dv] (any token and head
+    strides), q_out [T, Hq, D], and pools [num_blocks, block_size, Hkv, D] of f32, f16 or
+    bf16. eps: the RMS norm of q and k, with weights [D] or [heads, D] (1 without); None: no
+    norm. The descriptor keeps rope and the weights alive."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or q_out.dim() != 3 or k_pool.dim() != 4 \
+            or v_pool.dim() != 4:
+        raise ValueError("rows must be [T, heads, D] and pools [num_blocks, block_size, Hkv, D]")
+    if q.shape != q_out.shape or k.shape[:2] != v.shape[:2] or q.shape[0] != k.shape[0] \
+            or q.shape[2] != k.shape[2] or k_pool.shape[:3] != v_pool.shape[:3]:
+        raise ValueError("q, q_out, k and v must agree in their tokens, heads and widths, and the "
+                         "pools in their blocks and heads")
+    if k.shape[1:] != k_pool.shape[2:] or v.shape[1:] != v_pool.shape[2:]:
+        raise ValueError("new rows and pools must agree in heads and width")
+    if not q.dtype == k.dtype == v.dtype or k_pool.dtype != v_pool.dtype:
+        raise ValueError("q, k and v must be of one type, and the pools of one")
+    if any(t.stride(-1) != 1 for t in (q, k, v, q_out, k_pool, v_pool)):
+        raise ValueError("the last dimension must be contiguous")
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights belong to a norm: give eps")
+    a = N.DaPrep()
+    a.n_tokens, a.n_heads, a.head_dim = q.shape
+    a.n_kv_heads, a.v_dim = v.shape[1:]
+    a.num_blocks, a.block_size = k_pool.shape[:2]
+    a.src_dtype, a.q_dtype = dtype_code(q.dtype), dtype_code(q_out.dtype)
+    a.cache_dtype = dtype_code(k_pool.dtype)
+    a.norm, a.eps, a.weight_offset = int(eps is not None), float(eps or 0.0), float(weight_offset)
+    for name, w, heads in (("q", q_weight, q.shape[1]), ("k", k_weight, k.shape[1])):
+        if w is None:
+            continue
+        if tuple(w.shape) not in ((q.shape[2],), (heads, q.shape[2])) or w.stride(-1) != 1:
+            raise ValueError(f"{name}_weight must be [{q.shape[2]}] or [{heads}, {q.shape[2]}]")
+        if q_weight is not None and w.dtype != q_weight.dtype:
+            raise ValueError("the weights must be of one type")
+        _on(q.device, "make_prep", w)
+        a.w_dtype = dtype_code(w.dtype)
+        setattr(a, f"{name}_weight", w.data_ptr())
+        setattr(a, f"{name}_weight_head_stride", w.stride(0) if w.dim() == 2 else 0)
+    a.q_src_stride, a.q_src_head_stride = q.stride()[:2]
+    a.k_src_stride, a.k_src_head_stride = k.stride()[:2]
+    a.v_src_stride, a.v_src_head_stride = v.stride()[:2]
+    a.q_out_stride, a.q_out_head_stride = q_out.stride()[:2]
+    a.k_block_stride, a.k_pos_stride, a.k_head_stride = k_pool.stride()[:3]
+    a.v_block_stride, a.v_pos_stride, a.v_head_stride = v_pool.stride()[:3]
+    _on(q.device, "make_prep", rope.table)
+    # (of this object alone, no fields of the struct)
+    a.rope, a.weights = rope, (q_weight, k_weight)
+    a.tensors = _prep_tensors(q, k, v, q_out, k_pool, v_pool)
+    return a
+
+
+def _prep_tensors(q, k, v, q_out, k_pool, v_pool) -> tuple:
+    return tuple((t.shape, t.stride(), t.dtype, t.get_device())
+                 for t in (q, k, v, q_out, k_pool, v_pool))
+
+
+def decode_attn_rope_append(prep: N.DaPrep, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            positions: torch.Tensor, slot_map: Optional[torch.Tensor],
+                            q_out: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                            stream=None) -> None:
+    """Normalise and rotate the new rows' q and k; q into q_out, k and v into the slots
+    (int64 [T], negative: not cached; None: row t has slot t) of the pools. positions: int64
+    [T], or [axes, T]. `prep` describes tensors of these shapes, types and strides."""
+    T = prep.n_tokens
+    if positions.dtype != torch.int64 or not positions.is_contiguous() \
+            or positions.dim() not in (1, 2) or positions.shape[-1] != T \
+            or positions.numel() != T * prep.rope.n_axes:
+        raise TypeError(f"positions must be contiguous int64 [{T}] for each of "
+                        f"{prep.rope.n_axes} axes")
+    if slot_map is not None and (slot_map.dtype != torch.int64 or not slot_map.is_contiguous()
+                                 or slot_map.numel() != T):
+        raise TypeError("slot_map must be a contiguous int64 tensor with a slot per row")
+    if not q.is_cuda:
+        raise TypeError("the rows must be CUDA tensors")
+    if _prep_tensors(q, k, v, q_out, k_pool, v_pool) != prep.tensors:
+        raise ValueError("prep describes tensors of other shapes, strides, types or devices")
+    index = q.get_device()
+    if not index == k.get_device() == v.get_device() == q_out.get_device() \
+            == k_pool.get_device() == v_pool.get_device() == positions.get_device() \
+            or (slot_map is not None and slot_map.get_device() != index):
+        _on(q.device, "decode_attn_rope_append", k, v, q_out, k_pool, v_pool, positions, slot_map)
+    _launch(q.device, stream, N.load().decode_attn_rope_append, ctypes.byref(prep),
+            ctypes.byref(prep.rope), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            positions.data_ptr(), 0 if slot_map is None else slot_map.data_ptr(),
+            q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
