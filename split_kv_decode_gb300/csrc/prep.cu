@@ -11,10 +11,10 @@
 // so far positions lose nothing and a position costs one integer product. The top 32 bits
 // give the octant and the argument of sinpi and cospi.
 //
-// Bound by memory: each row is read and written once. A row of a head is held by 2 to 32
-// lanes, eight columns a lane (16 bytes of a 16-bit type); the sum of squares and the partner
-// columns of halved pairs come by shuffles. A CTA forms the sines of its tokens once for all
-// heads.
+// Bound by memory: each row is read and written once. A warp holds one token (or 2 to 32 of
+// narrow heads) and walks its heads, or a share of them; a lane holds both columns of four
+// pairs of every head, so that it needs four angles a token, no exchange but the sum of squares, and
+// q may be rotated in place. The loads of the next rows are in flight while one is worked on.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,9 +31,9 @@ using skv::griddep_wait;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kAhead = 4; // rows of a warp in flight
 constexpr int kMaxPairs = DA_MAX_ROT_PAIRS;
-constexpr int kMaxTokens = 8; // tokens of a CTA
 
 struct PrepParams {
     const void *q, *k, *v;
@@ -50,53 +50,64 @@ struct PrepParams {
     int32_t block_size, pairs, interleaved;
     int32_t q_dtype, cache_dtype, w_dtype;
     int32_t norm;
-    int32_t lanes, per_cta, shares; // lanes of a row; tokens of a CTA; CTAs that share them
+    int32_t lanes, shares; // lanes of a row; warps that share a token's heads
     float eps, offset, factor, inv_dim;
     uint8_t axis[kMaxPairs];
 };
 
-// eight consecutive elements, widened
-__device__ __forceinline__ void load8(const float *p, float *f)
+// twice four consecutive elements: as they are stored, and widened
+template <typename ST> struct Raw {
+    uint2 a, b;
+};
+template <> struct Raw<float> {
+    uint4 a, b;
+};
+template <typename ST>
+__device__ __forceinline__ void load(Raw<ST> &r, const ST *row, int ca, int cb)
 {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    using V = decltype(r.a);
+    r.a = *reinterpret_cast<const V *>(row + ca);
+    r.b = *reinterpret_cast<const V *>(row + cb);
 }
-__device__ __forceinline__ void load8(const __half *p, float *f)
+__device__ __forceinline__ void widen2(uint32_t w, float *f, __half)
 {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    f[0] = x.x;
+    f[1] = x.y;
+}
+__device__ __forceinline__ void widen2(uint32_t w, float *f, __nv_bfloat16)
+{
+    f[0] = __uint_as_float(w << 16);
+    f[1] = __uint_as_float(w & 0xffff0000u);
+}
+template <typename ST> __device__ __forceinline__ void widen(const Raw<ST> &r, float *f)
+{
+    widen2(r.a.x, f, ST(0.f));
+    widen2(r.a.y, f + 2, ST(0.f));
+    widen2(r.b.x, f + 4, ST(0.f));
+    widen2(r.b.y, f + 6, ST(0.f));
+}
+template <> __device__ __forceinline__ void widen<float>(const Raw<float> &r, float *f)
+{
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        f[2 * i] = x.x;
-        f[2 * i + 1] = x.y;
-    }
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f)
+template <typename WT>
+__device__ __forceinline__ void load_as(const void *base, int64_t at, int ca, int cb, float *f)
 {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void load8(const void *base, int dtype, int64_t at, float *f)
-{
-    if (dtype == DA_F32) load8(static_cast<const float *>(base) + at, f);
-    else if (dtype == DA_F16) load8(static_cast<const __half *>(base) + at, f);
-    else load8(static_cast<const __nv_bfloat16 *>(base) + at, f);
+    Raw<WT> r;
+    load(r, static_cast<const WT *>(base) + at, ca, cb);
+    widen<WT>(r, f);
 }
 
-__device__ __forceinline__ void store8(void *base, int dtype, int64_t at, const float *f)
+__device__ __forceinline__ void store(void *base, int dtype, int64_t at, int ca, int cb,
+                                      const float *f)
 {
     if (dtype == DA_F32) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        float *p = static_cast<float *>(base) + at;
+        *reinterpret_cast<float4 *>(p + ca) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(p + cb) = make_float4(f[4], f[5], f[6], f[7]);
         return;
     }
     uint32_t w[4];
@@ -110,8 +121,9 @@ __device__ __forceinline__ void store8(void *base, int dtype, int64_t at, const 
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    uint16_t *p = static_cast<uint16_t *>(base) + at;
+    *reinterpret_cast<uint2 *>(p + ca) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2 *>(p + cb) = make_uint2(w[2], w[3]);
 }
 
 // cosine and sine of `phase` * 2^-64 turns
@@ -122,123 +134,145 @@ __device__ __forceinline__ float2 unit(uint64_t phase)
     // the rest, within an eighth of a turn, in half turns
     const float x = (float)(int32_t)(top - (quarter << 30)) * 0x1p-31f;
     const float s = sinpif(x), c = cospif(x);
-    switch (quarter & 3) {
-    case 0: return make_float2(c, s);
-    case 1: return make_float2(-s, c);
-    case 2: return make_float2(-c, -s);
-    default: return make_float2(s, -c);
-    }
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+    return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
 template <typename ST>
 __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ PrepParams p)
 {
-    __shared__ float2 sm_unit[kMaxTokens][kMaxPairs];
-    __shared__ int64_t sm_k[kMaxTokens], sm_v[kMaxTokens]; // offsets of the slots' rows, or -1
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t group = w / p.shares;
+    const int share = (int)(w - group * p.shares);
+    const int64_t t = group * (32 / p.lanes) + lane / p.lanes;
+    const bool live = t < p.tokens;
+    const int sub = lane & (p.lanes - 1);
+    const int heads = p.hq + 2 * p.hkv;
+    const int h0 = (int)((int64_t)share * heads / p.shares);
+    const int h1 = (int)((int64_t)(share + 1) * heads / p.shares);
+    const int turning = p.pairs >> 2; // lanes that hold pairs
+    const bool turns = sub < turning;
+    // the lane's columns: both of four pairs, or eight in a row
+    const bool halves = turns && !p.interleaved;
+    const int ca = halves ? sub * 4 : sub * 8, cb = halves ? p.pairs + sub * 4 : sub * 8 + 4;
+    // a value row has its own columns
+    const int va = sub * 8;
 
     // Nothing is touched before the stream's last kernel has ended; the next one may set
     // itself up from then on.
     griddep_wait();
     griddep_launch_dependents();
 
-    const int group = blockIdx.x / p.shares, share = blockIdx.x - group * p.shares;
-    const int t0 = group * p.per_cta;
-    const int nt = min(p.per_cta, p.tokens - t0);
-    for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
-        const int t = i / p.pairs, j = i - t * p.pairs;
-        const int64_t pos = p.positions[(int64_t)p.axis[j] * p.tokens + t0 + t];
-        float2 u = unit((uint64_t)pos * p.turns[j]);
-        u.x *= p.factor;
-        u.y *= p.factor;
-        sm_unit[t][j] = u;
-    }
-    if (threadIdx.x < nt) {
-        const int t = t0 + threadIdx.x;
-        const int64_t slot = p.slot_map ? p.slot_map[t] : t;
-        int64_t k = -1, v = -1;
-        if (slot >= 0 && slot < p.slots) {
-            const int64_t blk = slot / p.block_size, at = slot - blk * p.block_size;
-            k = blk * p.kb + at * p.kp;
-            v = blk * p.vb + at * p.vp;
+    Raw<ST> raw[kAhead] = {};
+    auto fetch = [&](Raw<ST> &r, int h) {
+        if (!live) return;
+        if (h < p.hq) {
+            if (sub < p.units_k)
+                load(r, static_cast<const ST *>(p.q) + t * p.q_stride + h * p.q_head, ca, cb);
+        } else if (h < p.hq + p.hkv) {
+            if (sub < p.units_k)
+                load(r, static_cast<const ST *>(p.k) + t * p.k_stride + (h - p.hq) * p.k_head, ca,
+                     cb);
+        } else if (sub < p.units_v) {
+            load(r, static_cast<const ST *>(p.v) + t * p.v_stride +
+                        (h - p.hq - p.hkv) * p.v_head, va, va + 4);
         }
-        sm_k[threadIdx.x] = k;
-        sm_v[threadIdx.x] = v;
-    }
-    __syncthreads();
-
-    // rows (token, head): q heads, then k heads, then v heads
-    const int heads = p.hq + 2 * p.hkv;
-    const int sub = threadIdx.x & (p.lanes - 1), row0 = threadIdx.x / p.lanes;
-    const int step = kThreads / p.lanes;
-    const int half_units = p.pairs >> 3; // units of the first half of halved pairs
-    const int rows = nt * heads;
-    // every lane of a warp takes part in each round's shuffles
-    for (int r0 = share * step; r0 < rows; r0 += p.shares * step) {
-        const int r = r0 + row0;
-        const bool live = r < rows;
-        const int t = live ? r / heads : 0;
-        const int h = live ? r - t * heads : 0;
-        const bool is_v = h >= p.hq + p.hkv, is_k = h >= p.hq && !is_v;
-        const bool mine = live && sub < (is_v ? p.units_v : p.units_k);
-        const int hh = h - (is_v ? p.hq + p.hkv : is_k ? p.hq : 0);
-        float x[8];
+    };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        if (mine) {
-            const int64_t tt = t0 + t;
-            const ST *src = is_v   ? static_cast<const ST *>(p.v) + tt * p.v_stride + hh * p.v_head
-                            : is_k ? static_cast<const ST *>(p.k) + tt * p.k_stride + hh * p.k_head
-                                   : static_cast<const ST *>(p.q) + tt * p.q_stride + hh * p.q_head;
-            load8(src + sub * 8, x);
+    for (int i = 0; i < kAhead; ++i)
+        if (h0 + i < h1) fetch(raw[i], h0 + i);
+
+    int64_t k_at = -1, v_at = -1; // the slot's rows
+    float2 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = make_float2(1.f, 0.f);
+    if (live) {
+        const int64_t slot = p.slot_map ? p.slot_map[t] : t;
+        if (slot >= 0 && slot < p.slots) {
+            const int64_t blk = p.slots <= UINT32_MAX ? (uint32_t)slot / (uint32_t)p.block_size
+                                                      : slot / p.block_size;
+            const int64_t at = slot - blk * p.block_size;
+            k_at = blk * p.kb + at * p.kp;
+            v_at = blk * p.vb + at * p.vp;
         }
+        if (turns && h0 < p.hq + p.hkv) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = sub * 4 + i;
+                const int64_t pos = p.positions[(int64_t)p.axis[j] * p.tokens + t];
+                u[i] = unit((uint64_t)pos * p.turns[j]);
+                u[i].x *= p.factor;
+                u[i].y *= p.factor;
+            }
+        }
+    }
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.f;
+
+    auto row = [&](float *x, int h) {
+        if (h >= p.hq + p.hkv) {
+            if (sub < p.units_v && v_at >= 0)
+                store(p.v_pool, p.cache_dtype, v_at + (h - p.hq - p.hkv) * p.vh, va, va + 4, x);
+            return;
+        }
+        const bool is_k = h >= p.hq, mine = live && sub < p.units_k;
+        const int hh = is_k ? h - p.hq : h;
         if (p.norm) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
             for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (mine && !is_v) {
-                const float inv = 1.f / sqrtf(fmaf(ss, p.inv_dim, p.eps));
-                const void *w = is_k ? p.k_weight : p.q_weight;
-                float g[8];
+            const int64_t step = is_k ? p.kw_head : p.qw_head;
+            if (mine && (h == h0 || h == p.hq || step)) { // the weights of this head
+                const void *wt = is_k ? p.k_weight : p.q_weight;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) g[i] = 1.f;
-                if (w) {
-                    load8(w, p.w_dtype, hh * (is_k ? p.kw_head : p.qw_head) + sub * 8, g);
+                if (wt) {
+                    if (p.w_dtype == DA_F32) load_as<float>(wt, hh * step, ca, cb, g);
+                    else if (p.w_dtype == DA_F16) load_as<__half>(wt, hh * step, ca, cb, g);
+                    else load_as<__nv_bfloat16>(wt, hh * step, ca, cb, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] += p.offset;
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * g[i];
             }
+            const float inv = 1.f / sqrtf(fmaf(ss, p.inv_dim, p.eps));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * g[i];
         }
-        if (p.interleaved) {
-            if (mine && !is_v && sub < 2 * half_units) {
-                const float2 *u = sm_unit[t] + sub * 4;
+        if (turns) {
+            if (p.interleaved) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float a = x[2 * i], b = x[2 * i + 1];
                     x[2 * i] = a * u[i].x - b * u[i].y;
                     x[2 * i + 1] = b * u[i].x + a * u[i].y;
                 }
-            }
-        } else {
-            const bool second = sub >= half_units;
-            const bool turns = !is_v && sub < 2 * half_units;
-            const int other = (threadIdx.x & 31) + (turns ? (second ? -half_units : half_units) : 0);
-            const float2 *u = sm_unit[t] + (second ? sub - half_units : sub) * 8;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = __shfl_sync(0xffffffffu, x[i], other);
-                if (turns) x[i] = x[i] * u[i].x + (second ? y * u[i].y : -y * u[i].y);
+                for (int i = 0; i < 4; ++i) {
+                    const float a = x[i], b = x[i + 4];
+                    x[i] = a * u[i].x - b * u[i].y;
+                    x[i + 4] = b * u[i].x + a * u[i].y;
+                }
             }
         }
-        if (!mine) continue;
-        if (is_v) {
-            if (sm_v[t] >= 0) store8(p.v_pool, p.cache_dtype, sm_v[t] + hh * p.vh + sub * 8, x);
-        } else if (is_k) {
-            if (sm_k[t] >= 0) store8(p.k_pool, p.cache_dtype, sm_k[t] + hh * p.kh + sub * 8, x);
+        if (!mine) return;
+        if (is_k) {
+            if (k_at >= 0) store(p.k_pool, p.cache_dtype, k_at + hh * p.kh, ca, cb, x);
         } else {
-            store8(p.q_out, p.q_dtype, (int64_t)(t0 + t) * p.qo_stride + hh * p.qo_head + sub * 8, x);
+            store(p.q_out, p.q_dtype, t * p.qo_stride + hh * p.qo_head, ca, cb, x);
+        }
+    };
+    for (int h = h0; h < h1; h += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (h + i >= h1) break;
+            float x[8];
+            widen<ST>(raw[i], x);
+            if (h + i + kAhead < h1) fetch(raw[i], h + i + kAhead);
+            row(x, h + i);
         }
     }
 }
@@ -334,16 +368,13 @@ extern "C" int decode_attn_rope_append(const da_prep_t *a, const da_rope_t *rope
     for (int i = 0; i < kMaxPairs; ++i) p.axis[i] = i < p.pairs ? rope->axis[i] : 0;
     p.lanes = 1;
     while (p.lanes < std::max(p.units_k, p.units_v)) p.lanes *= 2;
-    // Tokens of a CTA: as many as fill its threads once. Few tokens: several CTAs share
-    // one token's heads, so that each thread has one row's unit to wait for.
-    const int step = kThreads / p.lanes, heads = p.hq + 2 * p.hkv;
-    p.per_cta = std::min(std::max(step / heads, 1), kMaxTokens);
-    p.shares = 1;
-    const int groups = (p.tokens + p.per_cta - 1) / p.per_cta;
-    const int rounds = (p.per_cta * heads + step - 1) / step;
-    while (p.shares * 2 <= rounds && (int64_t)groups * p.shares * 2 <= 1216) p.shares *= 2;
+    // Few tokens: several warps share one's heads, down to two heads each, until there are
+    // eight warps an SM.
+    const int64_t groups = ((int64_t)p.tokens * p.lanes + 31) / 32;
+    const int heads = p.hq + 2 * p.hkv;
+    p.shares = (int)std::max<int64_t>(1, std::min<int64_t>(heads / 2, 1216 / groups));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)(groups * p.shares);
+    const unsigned grid = (unsigned)((groups * p.shares + kThreads / 32 - 1) / (kThreads / 32));
     const cudaError_t e =
         a->src_dtype == DA_F32   ? skv::launch_after(prep_kernel<float>, grid, kThreads, st, p)
         : a->src_dtype == DA_F16 ? skv::launch_after(prep_kernel<__half>, grid, kThreads, st, p)
