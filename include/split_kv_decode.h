@@ -148,6 +148,9 @@ typedef enum {
 #define DA_KERNEL_GQA_8BIT 4 /* 8-bit GQA/MQA split kernel (decode_attn_splitk_8bit):
                                e4m3 or e5m2 codes with a scale per (page, KV head),
                                head_dim 128 or 256, groups of 1 to 128 query rows  */
+#define DA_KERNEL_GQA_SCORED 5 /* tcgen05/TMEM split kernel of decode_attn_splitk_scored:
+                               16-bit caches, head_dim 128 or 256, groups of 1 to
+                               128 query rows                                      */
 #define DA_KERNEL_GQA_TC 3  /* tcgen05/TMEM split kernel for GQA/MQA work items of
                                8 to 128 query rows ((n_heads / n_kv_heads) * q_len),
                                f16 or bf16 caches, head_dim 128 or 256; q and the
@@ -722,6 +725,86 @@ int decode_attn_rope_append(const da_prep_t *shapes, const da_rope_t *rope, cons
                             const void *k, const void *v, const int64_t *positions,
                             const int64_t *slot_map, void *q_out, void *k_pool, void *v_pool,
                             da_stream_t stream);
+
+/*
+ * ---- scored attention ------------------------------------------------------
+ * decode_attn_splitk_scored is split-KV decode attention over 16-bit caches whose scores are
+ * capped, biased by the distance or limited to some positions, and whose sequences may
+ * continue a common prefix, which is read and multiplied once for the whole batch.
+ *
+ * Sequence b holds S_b positions of its own behind shared_len common ones (usually 0). Its
+ * tokens i = 0 .. q_len - 1 are at o = S_b - q_len + i of its own. With x = scale q.k, token i
+ * and head h score position j (of the sequence's own) as
+ *     y = softcap tanh(x / softcap)          (softcap > 0; otherwise y = x)
+ *     y -= slopes[h] |o - j|                 (with slopes)
+ * and out = sum_j e^y v / sum_j e^y over the visible positions: all that are shared, at distance
+ * shared_len + o - j from position j of them; and of the sequence's own those with
+ *     starts[b] <= j < S_b  and  (j < keep_b  or  o - window < j <= o)
+ * where a window of 0 has no lower end, starts counts as 0 if NULL, and keep_b is keep, or
+ * min(keep_lens[b], keep). So window is a sliding window, keep the positions at the front that
+ * stay visible behind it (or, past the token, a prefix that is seen both ways), and starts[b]
+ * the first position of the document (or behind the padding) that a sequence is in.
+ * A token that sees nothing gives zeros, and so does one with o < 0 (a sequence of length 0 is an
+ * unused place in the batch, with shared positions too). What keys and values hold at
+ * positions that a token does not see has no effect on it, NaN and infinities included.
+ */
+typedef struct da_score_t {
+    const float *slopes;        /* DEVICE float[n_heads], or NULL                      */
+    const int32_t *starts;      /* DEVICE int32[batch], or NULL                        */
+    const int32_t *keep_lens;   /* DEVICE int32[batch], or NULL                        */
+    const int32_t *shared_table;/* DEVICE int32[shared_len / block_size]: the blocks of the
+                                   shared positions                                    */
+    float softcap;              /* 0: none                                             */
+    int32_t window;             /* 0: none                                             */
+    int32_t keep;               /* bound of keep_lens, or every sequence's             */
+    int32_t shared_len;         /* a multiple of dev->block_size; 0: none. Not together
+                                   with a window, keep or starts (DA_EUNSUPPORTED)     */
+    int32_t q_dtype;            /* DA_F32, or the cache's type                         */
+    int32_t reserved;           /* 0                                                   */
+} da_score_t;
+
+/* A plan of decode_attn_plan_scored. base.seq_lens are the sequences' own lengths;
+ * base.n_splits[b] counts the splits of the shared positions, then b's own. */
+typedef struct da_scored_plan_t {
+    da_plan_t base;       /* kernel DA_KERNEL_GQA_SCORED                              */
+    int32_t shared_len;
+    int32_t shared_chunk; /* positions per split of the shared ones                   */
+    int32_t shared_splits;
+    int32_t reserved;     /* 0                                                        */
+} da_scored_plan_t;
+
+/*
+ * decode_attn_plan_scored -- decode_attn_plan for these calls: seq_lens_host are the largest
+ * own lengths that a launch will see, each in [q_len, capacity]. With a window the span
+ * that is visible at most is split, not the length. Pure host code. args->kv_dtype is DA_F16
+ * or DA_BF16, v_dim == head_dim is 128 or 256, (n_heads / n_kv_heads) * q_len at most 128, and
+ * flags are 0 (or DA_FLAG_COMBINE_LOADS, DA_FLAG_TEST_*); DA_EUNSUPPORTED otherwise.
+ */
+int decode_attn_plan_scored(const da_args_t *args, const da_score_t *score,
+                            const int32_t *seq_lens_host, int num_sms, da_scored_plan_t *plan);
+
+/*
+ * decode_attn_splitk_scored -- the split kernel and, unless the plan has one split in all for
+ * every sequence, the combine.
+ *   dev    device lengths, each clamped to [0, plan->base.seq_lens[b]], and paged caches as in
+ *          decode_attn_splitk_dev; an entry of block_table or shared_table outside
+ *          [0, num_blocks) reads as zeros. NULL: the plan's lengths, contiguous caches.
+ *          shared_len needs a block_table.
+ *   score  as in the plan's call but for the pointers, which may change
+ *   q      [batch][n_heads][head_dim] or [batch][q_len][n_heads][head_dim], contiguous, of
+ *          score->q_dtype
+ *   workspace  plan->base.workspace_bytes, 256-byte aligned; calls that overlap on the GPU need
+ *          their own
+ * Keys and values are used as stored; so is a q of the cache's type. An f32 q and the weights
+ * (e^y, relative to the largest so far) carry 16 bits or more beside 16-bit outputs, 22 bits
+ * (f16 caches) or 24 (bf16) beside f32 ones; sums are f32. No host decision depends
+ * on the current lengths: the call can be captured in a CUDA graph. The partials are this call's
+ * own: the combines refuse a scored plan.
+ */
+int decode_attn_splitk_scored(const da_args_t *args, const da_scored_plan_t *plan,
+                              const da_dev_t *dev, const da_score_t *score, const void *q,
+                              const void *k_cache, const void *v_cache, void *out,
+                              void *workspace, size_t workspace_bytes, da_stream_t stream);
 
 /* Thread-local description of the last failure on this thread ("" if none). */
 const char *decode_attn_last_error(void);

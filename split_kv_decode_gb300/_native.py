@@ -28,6 +28,7 @@ DA_MLA_EXACT_BELOW = 2048
 DA_FLAG_TEST_NO_TMA = 0x100
 DA_FLAG_TEST_BAD_LAUNCH = 0x200
 DA_KERNEL_GQA_TMA, DA_KERNEL_MLA_TC, DA_KERNEL_GQA_TC, DA_KERNEL_GQA_8BIT = 1, 2, 3, 4
+DA_KERNEL_GQA_SCORED = 5
 
 
 class DaArgs(ctypes.Structure):
@@ -149,6 +150,24 @@ class DaPrep(ctypes.Structure):
     ]
 
 
+class DaScore(ctypes.Structure):
+    _fields_ = [
+        ("slopes", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+        ("keep_lens", ctypes.c_void_p), ("shared_table", ctypes.c_void_p),
+        ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("keep", ctypes.c_int32),
+        ("shared_len", ctypes.c_int32), ("q_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class DaScoredPlan(DaPlan):
+    """da_scored_plan_t: a da_plan_t (base) and the split of the shared positions."""
+    _fields_ = [
+        ("shared_len", ctypes.c_int32), ("shared_chunk", ctypes.c_int32),
+        ("shared_splits", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
 SIGNATURES = {
     "decode_attn_plan": (ctypes.c_int, [ctypes.POINTER(DaArgs), _P, ctypes.c_int,
                                         ctypes.POINTER(DaPlan)]),
@@ -183,6 +202,12 @@ SIGNATURES = {
                                                _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "decode_attn_rope_append": (ctypes.c_int, [ctypes.POINTER(DaPrep), ctypes.POINTER(DaRope), _P,
                                                _P, _P, _P, _P, _P, _P, _P, _P]),
+    "decode_attn_plan_scored": (ctypes.c_int, [ctypes.POINTER(DaArgs), ctypes.POINTER(DaScore),
+                                               _P, ctypes.c_int, ctypes.POINTER(DaScoredPlan)]),
+    "decode_attn_splitk_scored": (ctypes.c_int, [ctypes.POINTER(DaArgs),
+                                                 ctypes.POINTER(DaScoredPlan),
+                                                 ctypes.POINTER(DaDev), ctypes.POINTER(DaScore),
+                                                 _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "decode_attn_last_error": (ctypes.c_char_p, []),
     "decode_attn_release": (None, []),
     "decode_attn_version": (ctypes.c_char_p, []),

@@ -671,3 +671,110 @@ def decode_attn_rope_append(prep: N.DaPrep, q: torch.Tensor, k: torch.Tensor, v:
             ctypes.byref(prep.rope), q.data_ptr(), k.data_ptr(), v.data_ptr(),
             positions.data_ptr(), 0 if slot_map is None else slot_map.data_ptr(),
             q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
+
+
+# ---- scored attention ----------------------------------------------------------------
+
+def make_score(q: torch.Tensor, *, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+               window: int = 0, keep: int = 0, keep_lens: Optional[torch.Tensor] = None,
+               starts: Optional[torch.Tensor] = None, shared_len: int = 0,
+               shared_table: Optional[torch.Tensor] = None) -> N.DaScore:
+    """da_score_t for q [B, Hq, D] or [B, q_len, Hq, D] of f32 or of the cache's type: scores
+    softcap tanh(x / softcap) - slopes[h] * distance (slopes f32 [Hq]), over the positions that
+    starts (int32 [B]), keep (or keep_lens, int32 [B], bounded by keep) and window leave, and
+    over shared_len positions that all sequences share, in the blocks of shared_table (int32).
+    The descriptor keeps its tensors alive."""
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
+    if shared_table is None and shared_len:
+        raise ValueError("shared_len needs a shared_table")
+    s = N.DaScore()
+    for name, t, dtype, n in (("slopes", slopes, torch.float32, q.shape[-2]),
+                              ("starts", starts, torch.int32, q.shape[0]),
+                              ("keep_lens", keep_lens, torch.int32, q.shape[0]),
+                              ("shared_table", shared_table, torch.int32, None)):
+        if t is None:
+            continue
+        if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous 1-D {dtype} tensor")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name} must hold {n} elements")
+        _on(q.device, "make_score", t)
+        setattr(s, name, t.data_ptr())
+    s.softcap, s.window, s.keep = float(softcap), int(window), int(keep)
+    s.shared_len, s.q_dtype = int(shared_len), dtype_code(q.dtype)
+    # (of this object alone, no fields of the struct)
+    s.tensors = (slopes, starts, keep_lens, shared_table)
+    s.batch, s.heads, s.device = q.shape[0], q.shape[-2], q.get_device()
+    return s
+
+
+def decode_attn_plan_scored(args: N.DaArgs, score: N.DaScore, seq_lens_host: Sequence[int],
+                            num_sms: int = 0) -> N.DaScoredPlan:
+    lens = [int(x) for x in seq_lens_host]
+    if len(lens) != args.batch:
+        raise ValueError(f"seq_lens must hold {args.batch} lengths")
+    lens = (ctypes.c_int32 * max(1, args.batch))(*lens)
+    plan = N.DaScoredPlan()
+    _check(N.load().decode_attn_plan_scored(ctypes.byref(args), ctypes.byref(score),
+                                            ctypes.cast(lens, ctypes.c_void_p), int(num_sms),
+                                            ctypes.byref(plan)))
+    return plan
+
+
+def decode_attn_splitk_scored(args: N.DaArgs, plan: N.DaScoredPlan, dev: Optional[N.DaDev],
+                              score: N.DaScore, q: torch.Tensor, k_cache: torch.Tensor,
+                              v_cache: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                              stream=None) -> None:
+    """Scored split-KV attention (make_args or make_paged_args, make_dev or None, make_score,
+    decode_attn_plan_scored). q, out and the caches are of the shapes and types that the
+    descriptors were made for."""
+    index = q.get_device()
+    if index < 0:
+        raise TypeError("q must be a CUDA tensor")
+    if not index == k_cache.get_device() == v_cache.get_device() == out.get_device() \
+            == workspace.get_device():
+        _on(q.device, "decode_attn_splitk_scored", k_cache, v_cache, out, workspace)
+    if _DT.get(q.dtype) != score.q_dtype or not q.is_contiguous() or not out.is_contiguous():
+        raise TypeError("q must be contiguous and of score's type, and out contiguous")
+    if _DT.get(out.dtype) != args.out_dtype:
+        raise TypeError(f"out is {out.dtype}, not of the type that args were made for")
+    rows = args.batch * args.n_heads * (args.q_len or 1)
+    if q.numel() != rows * args.head_dim or out.numel() != rows * args.v_dim:
+        raise ValueError(f"q and out must hold {rows} rows, as args describe")
+    if (score.batch, score.heads, score.device) != (args.batch, args.n_heads, index):
+        raise ValueError("score was made for a q of another batch, number of heads or device")
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    paged = dev is not None and bool(dev.block_table)
+    if paged:
+        pools = _pools(k_cache, v_cache)
+        if not pools == getattr(args, "pools", None) == getattr(dev, "pools", None):
+            _check_pools(args, dev, k_cache, v_cache)
+        table = score.tensors[3]
+        if score.shared_len and table.numel() * dev.block_size < score.shared_len:
+            raise ValueError("shared_table holds fewer blocks than shared_len needs")
+    else:
+        _check_caches(args, k_cache, v_cache)
+    if dev is not None:
+        if getattr(dev, "devices", None) not in (None, [index], [index, index]):
+            raise ValueError(f"the lengths and table must be on q's device, cuda:{index}")
+        if getattr(dev, "batch", args.batch) < args.batch:
+            raise ValueError(f"the lengths and table hold {dev.batch} sequences, q {args.batch}")
+    _launch(q.device, stream, N.load().decode_attn_splitk_scored, ctypes.byref(args),
+            ctypes.byref(plan), None if dev is None else ctypes.byref(dev), ctypes.byref(score),
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _check_caches(args: N.DaArgs, k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    """Raises unless the contiguous caches are what args describe."""
+    for c, dim, strides in ((k_cache, args.head_dim, (args.k_batch_stride, args.k_pos_stride,
+                                                      args.k_head_stride, 1)),
+                            (v_cache, args.v_dim, (args.v_batch_stride, args.v_pos_stride,
+                                                   args.v_head_stride, 1))):
+        if _DT.get(c.dtype) != args.kv_dtype:
+            raise TypeError("the caches are not of the type that args were made for")
+        if c.dim() != 4 or c.shape[0] < args.batch or c.shape[1] < args.capacity \
+                or tuple(c.shape[2:]) != (args.n_kv_heads, dim) or c.stride() != strides:
+            raise ValueError("the caches must have the shapes and strides of args")

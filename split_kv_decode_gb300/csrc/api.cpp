@@ -18,6 +18,7 @@
 
 #include "internal.h"
 #include "plan_internal.h"
+#include "scored.h"
 
 namespace skv {
 
@@ -817,6 +818,198 @@ int check_buffers(int kernel, const float *q, const void *k, const void *v, cons
     return DA_OK;
 }
 
+// ---- scored attention -----------------------------------------------------------
+// What follows from the arguments of a scored call (see scored.h).
+struct Scored {
+    ScoredGeometry g;
+    int tile, p_terms, row_groups, row_tiles, shared_tiles;
+    int window;                     // 0 where it reaches every position
+    int32_t tiles[DA_MAX_BATCH];    // of a sequence's visible span at most
+};
+
+int check_scored(const da_args_t *a, const da_score_t *s, const int32_t *lens, Scored *out)
+{
+    if (!s) return fail(DA_EINVAL, "args", "score is NULL");
+    const int G = a->n_heads / a->n_kv_heads * q_len_of(a), es = dtype_size(a->kv_dtype);
+    if (a->kv_dtype != DA_F16 && a->kv_dtype != DA_BF16)
+        return fail(DA_EUNSUPPORTED, "args", "scored attention reads f16 and bf16 caches (got %s)",
+                    dtype_name(a->kv_dtype));
+    if (a->head_dim != a->v_dim || (a->head_dim != 128 && a->head_dim != 256) || G > 128)
+        return fail(DA_EUNSUPPORTED, "args",
+                    "scored attention serves v_dim == head_dim of 128 or 256 and groups of 1 to "
+                    "128 rows (heads per KV head x q_len; got %d, %d, %d)",
+                    a->head_dim, a->v_dim, G);
+    const int64_t st[6] = {a->k_pos_stride, a->k_head_stride, a->v_pos_stride,
+                           a->v_head_stride, a->batch > 1 ? a->k_batch_stride : 0,
+                           a->batch > 1 ? a->v_batch_stride : 0};
+    for (int i = 0; i < 6; ++i)
+        if ((st[i] * es) % 16)
+            return fail(DA_EUNSUPPORTED, "args",
+                        "cache strides must be multiples of 16 bytes for TMA tiles");
+    if (a->capacity > 1 << 30) return fail(DA_EUNSUPPORTED, "args", "capacity exceeds 2^30");
+    if (a->flags & ~(DA_FLAG_COMBINE_LOADS | DA_FLAG_TEST_NO_TMA | DA_FLAG_TEST_BAD_LAUNCH))
+        return fail(DA_EUNSUPPORTED, "args", "scored attention takes no flags (got 0x%x)", a->flags);
+    if (s->q_dtype != DA_F32 && s->q_dtype != a->kv_dtype)
+        return fail(DA_EINVAL, "args", "q_dtype must be f32 or the cache's type");
+    if (!std::isfinite(s->softcap) || s->softcap < 0.f)
+        return fail(DA_EINVAL, "args", "softcap must be finite and >= 0");
+    if (s->window < 0 || s->keep < 0 || s->shared_len < 0 || s->shared_len > 1 << 30)
+        return fail(DA_EINVAL, "args", "window and keep must be >= 0, shared_len in [0, 2^30]");
+    if (s->shared_len && (s->window || s->keep || s->starts || s->keep_lens))
+        return fail(DA_EUNSUPPORTED, "args",
+                    "shared positions do not go together with a window, keep or starts");
+    if (s->shared_len && !s->shared_table)
+        return fail(DA_EINVAL, "args", "shared_len needs a shared_table");
+    for (const void *x : {(const void *)s->slopes, (const void *)s->starts,
+                          (const void *)s->keep_lens, (const void *)s->shared_table})
+        if (!aligned(x, 4))
+            return fail(DA_EINVAL, "args", "score's pointers must be 4-byte aligned");
+    for (int b = 0; b < a->batch; ++b)
+        if (lens[b] < q_len_of(a) || lens[b] > a->capacity)
+            return fail(DA_EINVAL, "args", "seq_lens[%d] = %d outside [q_len %d, capacity %d]",
+                        b, lens[b], q_len_of(a), a->capacity);
+    out->p_terms = scored_terms(a->kv_dtype, a->out_dtype);
+    out->tile = scored_tile(a->head_dim, out->p_terms);
+    const int64_t shared_rows = s->shared_len ? (int64_t)a->batch * G : 0;
+    out->g = scored_geometry(a->head_dim, s->q_dtype == DA_F32 ? out->p_terms : 1, out->p_terms,
+                             (int)std::max<int64_t>(G, shared_rows));
+    if (out->g.slots < 3) return fail(DA_EUNSUPPORTED, "args", "no room for the tiles");
+    out->row_groups = (int)ceil_div(G, out->g.tile_rows);
+    out->row_tiles = (int)ceil_div(shared_rows, out->g.tile_rows);
+    const int T = out->tile;
+    out->shared_tiles = (int)ceil_div(s->shared_len, T);
+    out->window = s->window >= a->capacity ? 0 : s->window;
+    for (int b = 0; b < a->batch; ++b) {
+        int64_t n = ceil_div(lens[b], T);
+        if (out->window) // the window's positions may start and end inside a tile
+            n = std::min(n, ceil_div(s->keep, T) +
+                                ceil_div((int64_t)out->window + q_len_of(a) - 1, T) + 1);
+        out->tiles[b] = (int32_t)n;
+    }
+    return DA_OK;
+}
+
+// The plan's own splits of sequence b.
+int own_splits(const Scored &x, const da_plan_t &pl, int b)
+{
+    return (int)std::max<int64_t>(1, ceil_div((int64_t)x.tiles[b] * x.tile, pl.chunk[b]));
+}
+
+int check_scored_plan(const da_args_t *a, const da_score_t *s, const da_scored_plan_t *sp,
+                      const Scored &x)
+{
+    const da_plan_t &pl = sp->base;
+    if (pl.kernel != DA_KERNEL_GQA_SCORED || pl.batch != a->batch || pl.tile != x.tile ||
+        sp->shared_len != s->shared_len)
+        return fail(DA_EINVAL, "plan", "plan was made for other arguments");
+    const int T = x.tile;
+    if (sp->shared_len ? sp->shared_chunk < 1 || sp->shared_chunk % T ||
+                             sp->shared_splits != ceil_div(s->shared_len, sp->shared_chunk)
+                       : sp->shared_splits != 0)
+        return fail(DA_EINVAL, "plan", "inconsistent split of the shared positions");
+    int64_t base = 0, items = (int64_t)sp->shared_splits * a->n_kv_heads * x.row_tiles;
+    int64_t most = 0;
+    for (int b = 0; b < a->batch; ++b) {
+        if (pl.chunk[b] < 1 || pl.chunk[b] % T || pl.split_base[b] != base ||
+            pl.n_splits[b] != sp->shared_splits + own_splits(x, pl, b))
+            return fail(DA_EINVAL, "plan",
+                        "inconsistent split table at b = %d (a plan of other arguments?)", b);
+        base += pl.n_splits[b];
+        items += (int64_t)own_splits(x, pl, b) * a->n_kv_heads * x.row_groups;
+        most = std::max<int64_t>(most, pl.n_splits[b]);
+    }
+    if (pl.total_splits != base || pl.n_items != items || pl.max_splits != most || pl.grid < 1 ||
+        pl.grid > items)
+        return fail(DA_EINVAL, "plan", "inconsistent plan totals");
+    if (pl.workspace_bytes != ws_total(pl.total_splits, rows_of(a), a->v_dim,
+                                       ws_counters(a->batch, a->n_kv_heads)))
+        return fail(DA_EINVAL, "plan", "inconsistent workspace size");
+    return DA_OK;
+}
+
+int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t *dev,
+                  const da_score_t *s, const Scored &x, const void *q, const void *k,
+                  const void *v, void *ws, cudaStream_t st, void *out)
+{
+    const da_plan_t &pl = sp->base;
+    ScoredParams p;
+    std::memset(&p, 0, sizeof p);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    p.q = q;
+    p.out = out;
+    p.ml = reinterpret_cast<float2 *>(w + ws_ml_offset());
+    p.acc = reinterpret_cast<float *>(w + ws_acc_offset(pl.total_splits, rows_of(a)));
+    p.status = reinterpret_cast<int *>(w);
+    p.slopes = s->slopes;
+    p.starts = s->starts;
+    p.keep_lens = s->keep_lens;
+    p.timeout_ns = (uint64_t)(a->timeout_us > 0 ? a->timeout_us : 2000000) * 1000ull;
+    p.scale = a->scale;
+    p.softcap = s->softcap;
+    p.batch = a->batch;
+    p.rows = rows_of(a);
+    p.q_len = q_len_of(a);
+    p.hq = a->n_heads;
+    p.hkv = a->n_kv_heads;
+    p.q_f32 = s->q_dtype == DA_F32;
+    p.q_terms = x.g.q_terms;
+    p.out_dtype = a->out_dtype;
+    p.whole = pl.max_splits == 1;
+    p.flags = a->flags;
+    p.window = x.window;
+    p.keep = std::min(s->keep, a->capacity);
+    p.rpad = x.g.rpad;
+    p.tile_rows = x.g.tile_rows;
+    p.slots = x.g.slots;
+    p.q_bytes = x.g.q_bytes;
+    p.row_groups = x.row_groups;
+    p.shared_len = sp->shared_len;
+    p.shared_tiles = x.shared_tiles;
+    p.shared_chunk = sp->shared_chunk / x.tile;
+    p.shared_splits = sp->shared_splits;
+    p.row_tiles = x.row_tiles;
+    p.shared_items = sp->shared_splits * a->n_kv_heads * x.row_tiles;
+    p.n_items = pl.n_items;
+    for (int b = 0; b < a->batch; ++b) {
+        p.lens[b] = pl.seq_lens[b];
+        p.chunk[b] = pl.chunk[b] / x.tile;
+        p.slot[b] = pl.split_base[b];
+    }
+    scored_order(x.tiles, p.chunk, a->batch, p.seq);
+    for (int e = 0; e < a->batch; ++e) p.base[e + 1] = p.base[e] + own_splits(x, pl, p.seq[e]);
+    CUtensorMap km, vm;
+    int rc;
+    if (dev && dev->block_table) {
+        p.block_table = dev->block_table;
+        p.shared_table = s->shared_table;
+        p.max_blocks = dev->max_blocks_per_seq;
+        p.block_size = dev->block_size;
+        p.oob_block = dev->num_blocks;
+        p.box_rows = std::gcd(x.tile, dev->block_size);
+        rc = encode_pool_map(&km, k, a->kv_dtype, a->head_dim, a->n_kv_heads, dev->block_size,
+                             dev->num_blocks, a->k_head_stride, a->k_pos_stride,
+                             dev->k_block_stride, p.box_rows, true);
+        if (rc) return rc;
+        rc = encode_pool_map(&vm, v, a->kv_dtype, a->v_dim, a->n_kv_heads, dev->block_size,
+                             dev->num_blocks, a->v_head_stride, a->v_pos_stride,
+                             dev->v_block_stride, p.box_rows, true);
+    } else {
+        rc = encode_cache_map(&km, k, a->kv_dtype, a->head_dim, a->n_kv_heads, a->capacity,
+                              a->batch, a->k_head_stride, a->k_pos_stride, a->k_batch_stride,
+                              x.tile, true);
+        if (rc) return rc;
+        rc = encode_cache_map(&vm, v, a->kv_dtype, a->v_dim, a->n_kv_heads, a->capacity,
+                              a->batch, a->v_head_stride, a->v_pos_stride, a->v_batch_stride,
+                              x.tile, true);
+    }
+    if (rc) return rc;
+    if (dev) p.dev_lens = dev->seq_lens;
+    const cudaError_t e = launch_gqa_scored(a->kv_dtype, a->head_dim, x.p_terms, split_grid(a, &pl),
+                                            x.g.smem, st, km, vm, p);
+    if (e != cudaSuccess) return fail(DA_ELAUNCH, "split", "%s", cudaGetErrorString(e));
+    return DA_OK;
+}
+
 // short form: one workspace per device
 std::mutex g_ws_mu;
 std::vector<std::pair<void *, size_t>> g_ws;
@@ -1022,6 +1215,94 @@ int decode_attn_splitk_8bit(const da_args_t *a, const da_plan_t *plan, const da_
     return launch_combine_phase(a, plan, ws, out, st);
 }
 
+int decode_attn_plan_scored(const da_args_t *a, const da_score_t *s, const int32_t *lens,
+                            int num_sms, da_scored_plan_t *sp)
+{
+    int rc = check_args(a);
+    if (rc) return rc;
+    if (!lens || !sp) return fail(DA_EINVAL, "args", "seq_lens or plan is NULL");
+    Scored x;
+    rc = check_scored(a, s, lens, &x);
+    if (rc) return rc;
+    if (num_sms <= 0) {
+        num_sms = device_sms();
+        if (num_sms < 1) return fail(DA_ECUDA, "plan", "SM count query failed");
+    }
+    const int G = a->n_heads / a->n_kv_heads * q_len_of(a);
+    const int shared_rows = s->shared_len ? std::min(a->batch * G, x.g.tile_rows) : 0;
+    const ScoredWork w = {a->batch, a->n_kv_heads, x.row_groups, x.tiles, x.shared_tiles,
+                          x.row_tiles, shared_rows > 128 ? 2 : 1, shared_rows,
+                          std::min(G, x.g.tile_rows), x.tile, x.g.q_terms, x.p_terms, a->head_dim,
+                          num_sms, a->force_splits};
+    ScoredSplit o;
+    if (plan_scored(w, &o)) return fail(DA_EUNSUPPORTED, "plan", "too many work items");
+    std::memset(sp, 0, sizeof *sp);
+    da_plan_t *plan = &sp->base;
+    plan->kernel = DA_KERNEL_GQA_SCORED;
+    plan->num_sms = num_sms;
+    plan->ctas_per_sm = 1;
+    plan->tile = x.tile;
+    plan->grid = (int32_t)std::min<int64_t>(o.items, num_sms);
+    plan->n_items = (int32_t)o.items;
+    plan->batch = a->batch;
+    sp->shared_len = s->shared_len;
+    sp->shared_chunk = s->shared_len ? o.shared_chunk * x.tile : 0;
+    sp->shared_splits = o.shared_splits;
+    int64_t base = 0;
+    for (int b = 0; b < a->batch; ++b) {
+        plan->seq_lens[b] = lens[b];
+        plan->chunk[b] = o.chunk[b] * x.tile;
+        plan->n_splits[b] = o.shared_splits + o.n_splits[b];
+        plan->split_base[b] = (int32_t)base;
+        base += plan->n_splits[b];
+        plan->max_splits = std::max(plan->max_splits, plan->n_splits[b]);
+    }
+    plan->total_splits = (int32_t)base;
+    plan->workspace_bytes = ws_total(base, rows_of(a), a->v_dim, ws_counters(a->batch, a->n_kv_heads));
+    plan->est_cost = o.cost;
+    return DA_OK;
+}
+
+int decode_attn_splitk_scored(const da_args_t *a, const da_scored_plan_t *plan,
+                              const da_dev_t *dev, const da_score_t *score, const void *q,
+                              const void *k, const void *v, void *out, void *ws, size_t ws_bytes,
+                              da_stream_t stream)
+{
+    int rc = check_args(a);
+    if (rc) return rc;
+    if (!plan) return fail(DA_EINVAL, "args", "plan is NULL");
+    if (plan->base.batch != a->batch)
+        return fail(DA_EINVAL, "plan", "plan was made for other arguments");
+    Scored x;
+    rc = check_scored(a, score, plan->base.seq_lens, &x);
+    if (rc) return rc;
+    if ((rc = check_scored_plan(a, score, plan, x))) return rc;
+    rc = check_buffers(DA_KERNEL_GQA_SCORED, static_cast<const float *>(q), k, v, out);
+    if (rc) return rc;
+    if (dev && dev->seq_lens && !aligned(dev->seq_lens, 4))
+        return fail(DA_EINVAL, "args", "dev->seq_lens must be 4-byte aligned");
+    if (dev && dev->block_table && (rc = check_table(a, &plan->base, dev, true))) return rc;
+    if (score->shared_len) {
+        if (!dev || !dev->block_table)
+            return fail(DA_EINVAL, "args", "shared_len needs paged caches (a block_table)");
+        if (score->shared_len % dev->block_size)
+            return fail(DA_EINVAL, "args", "shared_len %d is not a multiple of block_size %d",
+                        score->shared_len, dev->block_size);
+    }
+    if (!ws || !aligned(ws, 256))
+        return fail(DA_EINVAL, "args", "workspace must be non-NULL and 256-byte aligned");
+    if ((int64_t)ws_bytes < plan->base.workspace_bytes)
+        return fail(DA_ENOSPACE, "args", "workspace %zu bytes < %lld needed", ws_bytes,
+                    (long long)plan->base.workspace_bytes);
+    cudaError_t pre = cudaGetLastError();
+    if (pre != cudaSuccess)
+        return fail(DA_ECUDA, "before split", "pending CUDA error: %s", cudaGetErrorString(pre));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    rc = launch_scored(a, plan, dev, score, x, q, k, v, ws, st, out);
+    if (rc || plan->base.max_splits == 1) return rc;
+    return launch_combine_phase(a, &plan->base, ws, out, st);
+}
+
 int decode_attn_combine_ranks(const da_args_t *a, const da_plan_t *plan, const void *ws,
                               int n_ranks, void *out, da_stream_t stream)
 {
@@ -1181,6 +1462,7 @@ int decode_attn_device_status(void *ws, da_stream_t stream)
                     kernel == DA_KERNEL_MLA_TC   ? "split (mla)"
                     : kernel == DA_KERNEL_GQA_TC ? "split (gqa, tensor cores)"
                     : kernel == DA_KERNEL_GQA_8BIT ? "split (gqa, 8 bits)"
+                    : kernel == DA_KERNEL_GQA_SCORED ? "split (gqa, scored)"
                     : kernel == (kStatusTimeoutProj >> 8) ? "combine (projection)"
                     : kernel == (kStatusTimeoutCombine >> 8) ? "combine"
                                                           : "split (gqa)",

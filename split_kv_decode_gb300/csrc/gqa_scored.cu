@@ -1,0 +1,968 @@
+// Scored attention on tcgen05 tensor cores, sm_103a: split-KV decode attention whose scores
+// are capped, biased by the distance and masked, over 16-bit caches, and over positions that
+// all sequences share.
+//
+//     y = c tanh(x / c), x = scale q.k  (or x without a cap)
+//     y -= slope_h |position of the token - j|
+//     out = sum_j 2^(y_j log2 e - m) v_j / sum_j 2^(y_j log2 e - m)   over the visible j
+//
+// An item is a slice of positions for up to 128 query rows of one KV head (256 where two row
+// tiles share the slice's tiles): the (token, head) rows of one sequence, or, for shared
+// positions, those of the whole batch, so that shared keys and values are read and multiplied
+// once. Per tile of T positions
+//     S = Q K^T       M = 128 rows, N = T, K = D          Q and K from shared memory
+//     O += P V        M = 128 rows, N = D, K = T          P from TMEM, V from shared memory
+// Row r is TMEM lane r of both, so its thread has its scores, its running maximum, its sum
+// and its rescaling to itself; no score crosses a lane.
+//
+// Operands are 16-bit, sums f32. K and V are used as they stand. A weight is the sum of two 16-bit
+// terms (three for f32 outputs of bf16 caches), so are the elements of an f32 q; the terms are
+// MMAs into one accumulator. P takes the place of its scores in TMEM: 32 scores (32 columns) become
+// two terms of 16 columns.
+//
+// What bounds it: memory. A tile of K and V takes 2800 cycles at an SM's share of the rate, its
+// MMAs 1500 (one term of q) and the softmax of a warpgroup about as much, with two
+// warpgroups taking tiles (or, for 256 rows, row tiles) in turn; 256 columns leave TMEM for
+// one. Many rows on shared positions are bound by the MMAs.
+//
+// Roles: one or two softmax warpgroups, a TMA producer warp, a warp whose first lane issues the
+// MMAs. Unit u of an item is tile u, or tile u / 2 and row tile u % 2; it has S slot u % 2 and, with
+// two warpgroups, warpgroup and accumulator u % 2. The MMA order S0 S1 O0 S2 O1 S3 ... lets each
+// unit's softmax run beside the other's MMAs, and makes P of unit u - 2 read before S of unit
+// u takes its place. Warpgroups that took tiles in turn have two states a row, which the
+// epilogue joins. Every wait is bounded: one that runs out sets the status word, and all roles
+// leave.
+#include <type_traits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "merge.cuh"
+#include "ptx.cuh"
+#include "scored.h"
+
+namespace skv {
+namespace {
+
+template <typename DT_, int D_, int TP_> struct Cfg {
+    using DT = DT_;
+    static constexpr int D = D_, TP = TP_;
+    static constexpr bool BF = std::is_same<DT, __nv_bfloat16>::value;
+    static constexpr int T = scored_tile(D, TP);
+    static constexpr int NWG = scored_groups(D);
+    static constexpr int NCH = D / 64;      // 64-column chunks of a row
+    static constexpr int CHUNK = T * 128;   // bytes of a chunk of a tile
+    static constexpr int SLOT = NCH * CHUNK;
+    static constexpr int WARPS = NWG * 4;   // softmax warps
+    static constexpr int THREADS = (WARPS + 2) * 32;
+    static constexpr int S_COL = 256;       // S slot s at S_COL + 128 s; O of warpgroup w at D w
+    // A row's reference moves when a weight passes 2^LIM, and then to 2^-OFF of the largest: an f16
+    // term keeps weights down to 2^-(24 + OFF) of it, bf16 has the exponents of f32.
+    static constexpr float LIM = BF ? 8.f : 15.f, OFF = BF ? 0.f : 7.f;
+};
+
+// barriers
+constexpr int SB_FULL = 0, SB_EMPTY = kScoredMaxSlots, SB_SFULL = 2 * kScoredMaxSlots,
+              SB_PFULL = SB_SFULL + 2, SB_PVDONE = SB_PFULL + 2, SB_OREADY = SB_PVDONE + 2,
+              SB_OFREE = SB_OREADY + 1, SB_QFULL = SB_OFREE + 1, SB_QFREE = SB_QFULL + 1,
+              SB_XCH = SB_QFREE + 1, SB_GROUP = SB_XCH + 1, SB_DRAIN = SB_GROUP + 2,
+              SB_N = SB_DRAIN + 1;
+
+// the part of shared memory behind the ring
+struct Misc {
+    uint64_t bar[SB_N];
+    uint32_t tmem;
+    int abort;
+    uint32_t bad[2][4];     // rows of a unit's V tile that hold no numbers, by its S slot
+    float2 state[2][128];   // (m, l) of a warpgroup's rows
+    float row_scale[256];   // of an f32 q beside an f16 cache
+};
+static_assert(sizeof(Misc) <= kScoredMisc, "misc");
+
+struct Item {
+    bool shared;
+    int b, kvh, split;
+    int row0, rows, nrt;    // rows of the (sequence's or batch's) KV head; row tiles
+    int tiles, v0;          // of the visible span
+    int n1, a0, w0;         // its tile v: at a0 + v T below n1, else at w0 + (v - n1) T
+    int end;                // positions from here on are not there
+    int start, keep1;       // visible to every row: [start, keep1)
+    int S, q0;              // the sequence's length, and its first token's position
+};
+
+__device__ __forceinline__ int length_of(const ScoredParams &p, int b)
+{
+    const int L = p.lens[b];
+    return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
+}
+
+// The idx-th item.
+template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
+{
+    const int per_seq = p.q_len * (p.hq / p.hkv);
+    if (idx < p.shared_items) {
+        it.shared = true;
+        const int u = idx / p.row_tiles;
+        it.row0 = (idx - u * p.row_tiles) * p.tile_rows;
+        it.split = u / p.hkv;
+        it.kvh = u - it.split * p.hkv;
+        it.rows = min(p.batch * per_seq - it.row0, p.tile_rows);
+        it.nrt = it.rows > 128 ? 2 : 1;
+        it.v0 = it.split * p.shared_chunk;
+        it.tiles = min(p.shared_tiles - it.v0, p.shared_chunk);
+        it.n1 = it.a0 = it.w0 = 0;
+        it.end = p.shared_len;
+        it.b = 0;
+        return;
+    }
+    it.shared = false;
+    int t = idx - p.shared_items;
+    int u = t / p.row_groups;
+    it.row0 = (t - u * p.row_groups) * p.tile_rows;
+    it.rows = min(per_seq - it.row0, p.tile_rows);
+    it.nrt = 1;
+    t = u / p.hkv;
+    it.kvh = u - t * p.hkv;
+    int lo = 0, hi = p.batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.base[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const int b = p.seq[lo];
+    it.b = b;
+    it.split = t - p.base[lo];
+    const int S = length_of(p, b);
+    it.S = it.end = S;
+    it.q0 = S - p.q_len;
+    it.start = p.starts ? max(0, __ldg(p.starts + b)) : 0;
+    int keep = p.keep;
+    if (p.keep_lens) keep = max(0, min(__ldg(p.keep_lens + b), keep));
+    it.keep1 = min(keep, S);
+    // the visible span: what is kept, and from the first token's window on
+    int from = it.start;
+    if (p.window) from = max(from, max(it.q0, 0) - p.window + 1);
+    it.n1 = 0;
+    it.a0 = 0;
+    it.w0 = from / T * T;
+    if (it.keep1 > it.start) {
+        it.a0 = it.start / T * T;
+        const int end1 = (it.keep1 + T - 1) / T * T;
+        if (it.w0 > end1) it.n1 = (end1 - it.a0) / T;
+        else it.w0 = it.a0;
+    }
+    const int n2 = S > from ? (S - it.w0 + T - 1) / T : 0;
+    it.v0 = it.split * p.chunk[b];
+    it.tiles = max(0, min(it.n1 + n2 - it.v0, p.chunk[b]));
+}
+
+template <int T> __device__ __forceinline__ int tile_at(const Item &it, int i)
+{
+    const int v = it.v0 + i;
+    return v < it.n1 ? it.a0 + v * T : it.w0 + (v - it.n1) * T;
+}
+
+// The items of a CTA: calls f(item) for each, until f returns false.
+template <int T, typename F> __device__ __forceinline__ void each_item(const ScoredParams &p, F &&f)
+{
+    const int g = gridDim.x;
+    for (int r = 0, first = 0; first < p.n_items; ++r, first += g) {
+        const int idx = first + (r & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (idx >= p.n_items) continue;
+        Item it;
+        get_item<T>(p, idx, it);
+        if (!f(it)) return;
+    }
+}
+
+// byte offset of (row, byte) in a chunk: 128-byte rows, 128-byte swizzle
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t byte)
+{
+    return (row >> 3) * 1024 + (row & 7) * 128 + ((((byte >> 4) ^ row) & 7) << 4) + (byte & 15);
+}
+
+template <typename DT> struct Pair;
+template <> struct Pair<__half> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t w)
+    {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+};
+template <> struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t w)
+    {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+};
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// A from TMEM (16-bit, two columns of A a word), B from shared memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                          uint32_t idesc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(bdesc), "r"(idesc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,"
+                 "%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+                 "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
+{
+    tmem_ld16(taddr, v);
+    tmem_ld16(taddr + 16, v + 16);
+}
+
+// (volatile, in program order with the other TMEM accesses)
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr)
+{
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    tmem_wait_ld();
+    return __uint_as_float(r);
+}
+
+__device__ __forceinline__ uint64_t l2_normal_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// what turns a row's raw score into y log2 e
+struct Scorer {
+    float mult;      // scale log2 e of the row (1 once the scores are transformed)
+    float cap;       // softcap log2 e; 0: none
+    float turn;      // 2 scale log2 e / softcap of the row, or scale / softcap (precise)
+    float slope;     // slope log2 e
+    bool precise;
+    // raw: the score; d: the token's position less the key's
+    __device__ __forceinline__ float operator()(float raw, float d) const
+    {
+        float y = raw * mult;
+        if (cap != 0.f) {
+            // tanh z = 1 - 2 / (1 + e^2z): off by 2^-22 of the cap, which 16-bit outputs do not
+            // see; f32 outputs take the function that is as near for small z
+            y = precise ? cap * tanhf(raw * turn)
+                        : fmaf(__fdividef(-2.f * cap, 1.f + ex2(raw * turn)), 1.f, cap);
+        }
+        return fmaf(-slope, fabsf(d), y);
+    }
+};
+
+template <typename C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    gqa_scored_kernel(const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ ScoredParams p)
+{
+    using DT = typename C::DT;
+    constexpr int D = C::D, T = C::T, NCH = C::NCH, NWG = C::NWG, TP = C::TP, CHUNK = C::CHUNK;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    const int nst = p.slots;
+    Misc *ms = reinterpret_cast<Misc *>(sm + p.q_bytes + nst * C::SLOT);
+    uint64_t *bar = ms->bar;
+    volatile int *abort_flag = &ms->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int Gh = p.hq / p.hkv; // query heads per KV head
+    const int qch = p.rpad * 128; // bytes of a Q chunk
+    volatile int never = 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < nst; ++s) {
+            mbar_init(bar + SB_FULL + s, 1);
+            mbar_init(bar + SB_EMPTY + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar + SB_SFULL + s, 1);
+            mbar_init(bar + SB_PFULL + s, 4);
+            mbar_init(bar + SB_PVDONE + s, 1);
+            mbar_init(bar + SB_GROUP + s, 4);
+        }
+        mbar_init(bar + SB_OREADY, 1);
+        mbar_init(bar + SB_OFREE, C::WARPS);
+        mbar_init(bar + SB_QFULL, C::WARPS);
+        mbar_init(bar + SB_QFREE, 1);
+        mbar_init(bar + SB_XCH, C::WARPS);
+        mbar_init(bar + SB_DRAIN, 1);
+        ms->abort = 0;
+        if (blockIdx.x == 0) *p.status = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::WARPS + 1) tmem_alloc(&ms->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms->tmem;
+    auto timed_out = [&]() {
+        *abort_flag = 1;
+        atomicCAS(p.status, 0, kStatusTimeoutScored);
+    };
+
+    if (warp == C::WARPS) {
+        // =============================== TMA producer ===============================
+        if (lane == 0) {
+            tma_prefetch_map(&kmap);
+            tma_prefetch_map(&vmap);
+        }
+        const uint64_t first = l2_evict_first_policy(), normal = l2_normal_policy();
+        const bool paged = p.block_table != nullptr;
+        int st = 0, n = 0; // slot, copies issued
+        uint32_t phase = 0;
+        const int32_t *win_tab = nullptr;
+        int win_lo = 0;
+        int32_t win_entry = 0;
+        bool ok = true;
+        each_item<T>(p, [&](const Item &it) {
+            const int32_t *tab = nullptr;
+            int width = 0;
+            if (paged) {
+                tab = it.shared ? p.shared_table : p.block_table + (size_t)it.b * p.max_blocks;
+                width = it.shared ? p.shared_len / p.block_size : p.max_blocks;
+            }
+            // shared tiles are read by every row tile's items
+            const uint64_t pol = it.shared && p.row_tiles > 1 ? normal : first;
+            for (int i = 0; i < it.tiles; ++i) {
+                const int t0 = tile_at<T>(it, i);
+                int blk = it.b, at = t0;
+                const int h = paged ? p.box_rows : T, nbox = T / h;
+                if (paged) {
+                    // box j: h rows of one block, h a divisor of the tile and of the block
+                    const int bs = p.block_size, lo = t0 / bs, hi = (t0 + T - 1) / bs;
+                    if (tab != win_tab || lo < win_lo || hi >= win_lo + 32) {
+                        win_tab = tab;
+                        win_lo = lo;
+                        win_entry = lo + lane < width ? tab[lo + lane] : p.oob_block;
+                    }
+                    const int pos = t0 + min(lane, nbox - 1) * h, e = pos / bs;
+                    blk = __shfl_sync(0xffffffffu, win_entry, e - win_lo);
+                    at = pos - e * bs;
+                    if (pos >= it.end || blk < 0) blk = p.oob_block; // reads as zeros
+                }
+                for (int kv = 0; kv < 2; ++kv) {
+                    bool got = true;
+                    if (lane == 0)
+                        got = mbar_wait_bounded(bar + SB_EMPTY + st, phase ^ 1u, p.timeout_ns,
+                                                abort_flag);
+                    if (!__shfl_sync(0xffffffffu, got, 0)) {
+                        ok = false;
+                        return false;
+                    }
+                    if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
+                        uint8_t *dst = sm + p.q_bytes + st * C::SLOT;
+                        if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + st, C::SLOT);
+                        __syncwarp();
+                        if (lane < nbox) {
+#pragma unroll
+                            for (int c = 0; c < NCH; ++c)
+                                tma_load_4d(dst + c * CHUNK + lane * h * 128, kv ? &vmap : &kmap,
+                                            bar + SB_FULL + st, c * 64, it.kvh, at, blk, pol);
+                        }
+                        ++n;
+                    }
+                    if (++st == nst) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            return true;
+        });
+        if (lane == 0) {
+            if (!ok) timed_out();
+            // nothing may be in flight when the CTA ends: the last copy into every slot
+            for (int f = max(0, n - nst); f < n; ++f)
+                (void)mbar_wait_bounded(bar + SB_FULL + f % nst, (uint32_t)(f / nst) & 1u,
+                                        p.timeout_ns, &never);
+        }
+        __syncwarp();
+    } else if (warp == C::WARPS + 1) {
+        // ============================ MMA issue (one thread) ============================
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_f16kind(128, T, 0, 0, C::BF);
+            constexpr uint32_t idesc_pv = idesc_f16kind(128, D, 0, 1, C::BF);
+            int n = 0;             // copies consumed: K of tile i at n + 2 i, V behind it
+            int items = 0;
+            uint32_t pph = 0;      // phases of PFULL, by slot
+            bool ok = true;
+            auto wait = [&](int b, uint32_t parity) {
+                ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
+                return ok;
+            };
+            each_item<T>(p, [&](const Item &it) {
+                if (it.tiles == 0) return true;
+                const int nu = it.tiles * it.nrt, sh = it.nrt - 1;
+                if (!wait(SB_QFULL, (uint32_t)items & 1u)) return false;
+                for (int v = 0; v < nu + 2; ++v) {
+                    if (v >= 2) { // O += P V of unit v - 2
+                        const int u = v - 2, tile = u >> sh, f = n + 2 * tile + 1, st = f % nst;
+                        const int s = u & 1, w = NWG == 2 ? s : 0;
+                        if (u == 0 && !wait(SB_OFREE, (uint32_t)items & 1u)) return false;
+                        if (!wait(SB_PFULL + s, (pph >> s) & 1u)) return false;
+                        pph ^= 1u << s;
+                        if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
+                        tc_fence_after();
+                        const uint64_t vd =
+                            smem_desc_sw128(sb + p.q_bytes + st * C::SLOT, CHUNK, 1024);
+                        const uint32_t a = tmem + C::S_COL + s * 128;
+#pragma unroll
+                        for (int x = 0; x < TP; ++x)
+#pragma unroll
+                            for (int k = 0; k < T / 16; ++k)
+                                tc_mma_ts(tmem + w * D,
+                                          a + (x < 2 ? 32 * (k / 2) + 16 * x + 8 * (k & 1)
+                                                     : T + 8 * k),
+                                          vd + (uint64_t)((k * 2048) >> 4), idesc_pv);
+                        if (sh == 0 || (u & 1)) tc_commit(bar + SB_EMPTY + st);
+                        tc_commit(bar + SB_PVDONE + w);
+                    }
+                    if (v < nu) { // S of unit v
+                        const int tile = v >> sh, f = n + 2 * tile, st = f % nst, s = v & 1;
+                        if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
+                        tc_fence_after();
+                        const uint32_t q0 =
+                            sb + (sh ? (v & 1) * p.q_terms * NCH * qch : 0);
+                        const uint64_t qd = smem_desc_sw128(q0, 16, 1024);
+                        const uint64_t kd = smem_desc_sw128(sb + p.q_bytes + st * C::SLOT, 16, 1024);
+                        for (int x = 0; x < p.q_terms; ++x)
+#pragma unroll
+                            for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc_mma_bf16(
+                                        tmem + C::S_COL + s * 128,
+                                        qd + (uint64_t)(((x * NCH + c) * qch + k * 32) >> 4),
+                                        kd + (uint64_t)((c * CHUNK + k * 32) >> 4), idesc_qk,
+                                        (x | c | k) != 0 ? 1u : 0u);
+                        tc_commit(bar + SB_SFULL + s);
+                        if (sh == 0 || (v & 1)) tc_commit(bar + SB_EMPTY + st);
+                        if (v == nu - 1) tc_commit(bar + SB_QFREE);
+                    }
+                }
+                tc_commit(bar + SB_OREADY);
+                n += 2 * it.tiles;
+                ++items;
+                return true;
+            });
+            if (!ok) timed_out();
+            // no MMA may be in flight when TMEM is freed
+            tc_commit(bar + SB_DRAIN);
+            (void)mbar_wait_bounded(bar + SB_DRAIN, 0, p.timeout_ns, &never);
+        }
+        __syncwarp();
+    } else {
+        // ========================= softmax and epilogue =========================
+        const int w = warp >> 2;              // warpgroup
+        const int r = threadIdx.x & 127;      // row of the row tile, TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t to = tl + w * D;       // its accumulator
+        int n = 0, items = 0;
+        uint32_t sph = 0;                     // phases of SFULL, by slot
+        int done = 0;                         // units of this warpgroup so far
+        uint32_t groups = 0;                  // uses of SB_GROUP
+        bool ok = true;
+        auto wait = [&](int b, uint32_t parity) {
+            ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            return ok;
+        };
+        auto arrive = [&](int b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + b);
+        };
+        // all warps of the warpgroup have come here
+        auto group_sync = [&]() {
+            arrive(SB_GROUP + w);
+            return wait(SB_GROUP + w, groups++ & 1u);
+        };
+        auto zero_o = [&](uint32_t addr, int cols) {
+            const float z[16] = {};
+            for (int c = 0; c < cols; c += 16) tmem_st16(addr + c, z);
+        };
+        zero_o(to, D);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(SB_OFREE);
+
+        each_item<T>(p, [&](const Item &it) {
+            // ---- this thread's row
+            const int nrt = it.nrt;
+            const int local = nrt == 2 ? w * 128 + r : r; // row of the item
+            const bool owner = local < it.rows;
+            const int per_seq = p.q_len * Gh;
+            int row = it.row0 + (owner ? local : 0), b = it.b, S, q0;
+            if (it.shared) {
+                b = row / per_seq;
+                row -= b * per_seq;
+                S = length_of(p, b);
+                q0 = S - p.q_len;
+            } else {
+                S = it.S;
+                q0 = it.q0;
+            }
+            const int tk = row / Gh, h = it.kvh * Gh + row - tk * Gh;
+            const int own = q0 + tk;               // its position behind the shared ones
+            const bool dead = !owner || own < 0;   // no such token: it sees nothing
+            const int out_row = tk * p.hq + h;
+            const size_t slot = (size_t)p.slot[b] + it.split + (it.shared ? 0 : p.shared_splits);
+            const size_t wrow = slot * p.rows + out_row;
+            // columns of this thread in the epilogue
+            const bool joint = NWG == 2 && nrt == 1;
+            const int c0 = joint ? w * (D / 2) : 0, nc = joint ? D / 2 : D;
+            auto write_cols = [&](int c, const float *x) { // 16 columns of its row, normalised or not
+                if (p.whole) {
+                    const size_t at = ((size_t)b * p.rows + out_row) * D + c;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        if (p.out_dtype == DA_F32) store4(static_cast<float *>(p.out) + at + i, f);
+                        else if (p.out_dtype == DA_F16) store4(static_cast<__half *>(p.out) + at + i, f);
+                        else store4(static_cast<__nv_bfloat16 *>(p.out) + at + i, f);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        store4(p.acc + wrow * D + c + i,
+                               make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+                }
+            };
+            if (it.tiles == 0) { // nothing to see: a neutral partial
+                if (owner && (nrt == 2 || w == 0)) {
+                    if (p.whole) {
+                        const float z[16] = {};
+                        for (int c = 0; c < D; c += 16) write_cols(c, z);
+                    } else {
+                        p.ml[wrow] = make_float2(kNeutralM, 0.f);
+                    }
+                }
+                return true;
+            }
+
+            // ---- Q, once the last item's scores are done with it
+            if (items > 0 && !wait(SB_QFREE, (uint32_t)(items - 1) & 1u)) return false;
+            {
+                constexpr int U8 = D / 8; // 8-column units of a row: a half-warp's or a warp's
+                // (rows past them give scores that nobody reads)
+                const int rows_padded = (it.rows + 7) / 8 * 8;
+                const int units = rows_padded * U8;
+                for (int u = threadIdx.x; u < units; u += C::WARPS * 32) {
+                    const int rr = u / U8, j = u - rr * U8;
+                    const bool real = rr < it.rows;
+                    int qrow = it.row0 + (real ? rr : 0), qb = it.b;
+                    if (it.shared) {
+                        qb = qrow / per_seq;
+                        qrow -= qb * per_seq;
+                    }
+                    const int qt = qrow / Gh, qh = it.kvh * Gh + qrow - qt * Gh;
+                    const size_t at = (((size_t)qb * p.q_len + qt) * p.hq + qh) * D + j * 8;
+                    const uint32_t dst = sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch +
+                                         swz(rr & 127, (j & 7) * 16);
+                    if (!p.q_f32) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (real) x = __ldg(reinterpret_cast<const uint4 *>(
+                                      static_cast<const uint16_t *>(p.q) + at));
+                        sts_v4(dst, x.x, x.y, x.z, x.w);
+                        continue;
+                    }
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+                    if (real) {
+                        const float4 *src = reinterpret_cast<const float4 *>(
+                            static_cast<const float *>(p.q) + at);
+                        const float4 x = __ldg(src), y = __ldg(src + 1);
+                        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+                        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+                    }
+                    if (!C::BF) {
+                        // f16: the row scaled to a largest element in [1, 2), so that two terms
+                        // keep 22 bits of it (every unit of a row is in this loop's same turn)
+                        float a = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
+                        for (int o = U8 / 2; o > 0; o >>= 1)
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                        // 2^-e from the exponent of a (its bits; subnormals and infinities: 1)
+                        const int e = (int)(__float_as_uint(a) >> 23);
+                        const bool plain = e < 1 || e > 253;
+                        const float down = plain ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
+                        if (j == 0)
+                            ms->row_scale[rr] = plain ? 1.f : __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] *= down;
+                    }
+                    for (int x = 0; x < p.q_terms; ++x) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] = Pair<DT>::pack(f[2 * i], f[2 * i + 1]);
+                            const float2 y = Pair<DT>::unpack(v[i]);
+                            f[2 * i] -= y.x;
+                            f[2 * i + 1] -= y.y;
+                        }
+                        sts_v4(dst + x * NCH * qch, v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            arrive(SB_QFULL);
+
+            // ---- what this row sees and how it scores
+            Scorer sc;
+            const int pos = own + (it.shared ? p.shared_len : 0); // in this item's positions
+            const float slope = p.slopes && owner ? __ldg(p.slopes + h) * kLog2e : 0.f;
+            bool scaled = false;
+            auto set_scorer = [&]() { // (an f32 q's row scale is there once all of Q is)
+                const float rs = !C::BF && p.q_f32 ? ms->row_scale[nrt == 2 ? w * 128 + r : r] : 1.f;
+                const float x = p.scale * rs;
+                sc.mult = x * kLog2e;
+                sc.precise = p.out_dtype == DA_F32;
+                sc.cap = p.softcap * kLog2e;
+                sc.turn = p.softcap == 0.f ? 0.f
+                                           : x / p.softcap * (sc.precise ? 1.f : 2.f * kLog2e);
+                sc.slope = slope;
+                scaled = true;
+            };
+            // warp-uniform: scores are transformed before the maximum is taken
+            const bool transform = p.softcap != 0.f || p.slopes || !(p.scale > 0.f);
+            const bool busy = (nrt == 2 ? w * 128 : 0) + (warp & 3) * 32 < it.rows;
+            const int x_lo = p.window ? max(it.start, own - p.window + 1) : it.start;
+            const int x_hi = dead ? 0 : own + 1;
+
+            // ---- units
+            const int nu = it.tiles * nrt;
+            float m = -INFINITY, l = 0.f;
+            int mine = 0; // units of this item so far
+            for (int u = NWG == 2 ? w : 0; u < nu; u += NWG) {
+                const int tile = nrt == 2 ? u >> 1 : u, s = u & 1;
+                const int t0 = tile_at<T>(it, tile);
+                const uint32_t ts = tl + C::S_COL + s * 128;
+                if (!wait(SB_SFULL + s, (sph >> s) & 1u)) return false;
+                sph ^= 1u << s;
+                tc_fence_after();
+                if (!scaled) set_scorer();
+
+                // which columns are visible: all, all below a border, or row by row
+                bool full = t0 + T <= it.end;
+                if (!it.shared) {
+                    const int o0 = max(it.q0, 0), o1 = it.S - 1;
+                    full = full && t0 >= it.start &&
+                           (t0 + T <= it.keep1 ||
+                            (t0 + T - 1 <= o0 && (!p.window || t0 > o1 - p.window)));
+                }
+                int k0 = 0, k1 = 0, x0 = 0, x1 = T; // visible: [k0, k1) and [x0, x1)
+                if (!full) {
+                    if (it.shared) {
+                        x1 = min(T, it.end - t0);
+                    } else {
+                        k0 = max(it.start - t0, 0);
+                        k1 = dead ? 0 : min(it.keep1 - t0, T);
+                        x0 = max(x_lo - t0, 0);
+                        x1 = min(x_hi - t0, T);
+                    }
+                }
+                // (no row, or a token that is not there, sees column 0 at least as unknown:
+                // its result is not used)
+                auto visible = [&](int c) { return (c >= x0 && c < x1) || (c >= k0 && c < k1); };
+
+                float tm = -INFINITY;
+                if (busy) {
+                    if (!transform && full) {
+#pragma unroll 1
+                        for (int c = 0; c < T; c += 32) {
+                            float x[32];
+                            tmem_ld32(ts + c, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) tm = fmaxf(tm, x[i]);
+                        }
+                        tm *= sc.mult;
+                    } else {
+                        // y (or -infinity where the row sees nothing) takes the score's place
+                        const float d0 = (float)(pos - t0);
+#pragma unroll 1
+                        for (int c = 0; c < T; c += 32) {
+                            float x[32];
+                            tmem_ld32(ts + c, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                x[i] = sc(x[i], d0 - (float)(c + i));
+                                if (!full && !visible(c + i)) x[i] = -INFINITY;
+                                tm = fmaxf(tm, x[i]);
+                            }
+                            tmem_st16(ts + c, x);
+                            tmem_st16(ts + c + 16, x + 16);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float mult = !transform && full ? sc.mult : 1.f;
+                // ---- the reference moves where a weight would pass 2^LIM
+                const bool moves = owner && tm > m + C::LIM;
+                if (__any_sync(0xffffffffu, moves)) {
+                    const float to_m = moves ? tm - C::OFF : m;
+                    const float alpha = moves && m != -INFINITY ? ex2(m - to_m) : 1.f;
+                    l *= alpha;
+                    m = to_m;
+                    if (mine > 0) { // (before, O is zero)
+                        if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(to + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st16(to + c, o);
+                            tmem_st16(to + c + 16, o + 16);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+
+                // ---- a tile that not all rows see in full: V rows that no row sees may hold
+                // anything (0 * NaN is NaN), and so may rows that some see
+                if (!full && !it.shared) {
+                    const int f = n + 2 * tile + 1, st = f % nst;
+                    if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
+                    const uint32_t vt = sb + p.q_bytes + st * C::SLOT;
+                    const int o0 = max(it.q0, 0), o1 = it.S - 1;
+                    const int ka = max(it.start - t0, 0), kb = min(it.keep1 - t0, T);
+                    const int lo_any = max(p.window ? max(it.start, o0 - p.window + 1) : it.start, 0) - t0;
+                    const int lo_all = max(p.window ? max(it.start, o1 - p.window + 1) : it.start, 0) - t0;
+                    const int hi_any = it.S - t0, hi_all = o0 + 1 - t0;
+                    auto kept = [&](int c) { return c >= ka && c < kb; };
+                    auto any = [&](int c) { return kept(c) || (c >= lo_any && c < hi_any); };
+                    auto all = [&](int c) { return kept(c) || (c >= lo_all && c < hi_all); };
+                    const bool partial = p.q_len > 1;
+                    uint32_t *bad = ms->bad[u & 1]; // (one warpgroup: its next unit's is another)
+                    if (partial) {
+                        if (r < 4) bad[r] = 0u;
+                        if (!group_sync()) return false;
+                    }
+                    // rows of D / 8 units; a thread's units are of one row each
+                    for (int i = r; i < T * (D / 8); i += 128) {
+                        const int c = i / (D / 8), j = i - c * (D / 8);
+                        const uint32_t at = vt + (j >> 3) * CHUNK + swz(c, (j & 7) * 16);
+                        if (!any(c)) {
+                            sts_v4(at, 0u, 0u, 0u, 0u);
+                        } else if (partial && !all(c)) {
+                            const uint4 x = lds_v4(at);
+                            const uint32_t e = C::BF ? 0x7f80u : 0x7c00u; // exponent of infinities, NaN
+                            bool odd = false;
+                            for (uint32_t y : {x.x, x.y, x.z, x.w})
+                                odd = odd || (y & e) == e || ((y >> 16) & e) == e;
+                            if (odd) atomicOr(bad + (c >> 5), 1u << (c & 31));
+                        }
+                    }
+                    if (partial) {
+                        if (!group_sync()) return false;
+                        uint32_t word[4];
+                        for (int i = 0; i < 4; ++i)
+                            word[i] = *reinterpret_cast<volatile uint32_t *>(bad + i);
+                        if (word[0] | word[1] | word[2] | word[3]) {
+                            // (rare) such rows are added here, to the rows that see them, and
+                            // leave the tile
+                            if (mine > 0 && !wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u))
+                                return false;
+                            tc_fence_after();
+                            for (int c = 0; c < T; ++c) {
+                                if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
+                                const float y = tmem_ld1(ts + c);
+                                const bool sees = !dead && visible(c);
+                                const float pr = ex2(y - ref);
+#pragma unroll 1
+                                for (int j = 0; j < D / 16; ++j) {
+                                    float o[16];
+                                    tmem_ld16(to + 16 * j, o);
+                                    tmem_wait_ld();
+                                    const uint32_t at = vt + (j >> 2) * CHUNK;
+                                    const uint4 a = lds_v4(at + swz(c, (j & 3) * 32));
+                                    const uint4 e = lds_v4(at + swz(c, (j & 3) * 32 + 16));
+                                    const uint32_t v[8] = {a.x, a.y, a.z, a.w, e.x, e.y, e.z, e.w};
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const float2 z = Pair<DT>::unpack(v[i]);
+                                        if (sees) {
+                                            o[2 * i] = fmaf(pr, z.x, o[2 * i]);
+                                            o[2 * i + 1] = fmaf(pr, z.y, o[2 * i + 1]);
+                                        }
+                                    }
+                                    tmem_st16(to + 16 * j, o);
+                                    tmem_wait_st();
+                                }
+                            }
+                            if (!group_sync()) return false;
+                            for (int i = r; i < T * (D / 8); i += 128) {
+                                const int c = i / (D / 8), j = i - c * (D / 8);
+                                if ((word[c >> 5] >> (c & 31)) & 1u)
+                                    sts_v4(vt + (j >> 3) * CHUNK + swz(c, (j & 7) * 16), 0u, 0u, 0u, 0u);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+
+                // ---- P: the weights, in terms, in the place of their scores
+                if (busy) {
+                    float l4[4] = {};
+#pragma unroll 1
+                    for (int c = 0; c < T; c += 32) {
+                        float x[32];
+                        tmem_ld32(ts + c, x);
+                        tmem_wait_ld();
+                        uint32_t hi[16], lo[16], lo2[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float a = ex2(fmaf(x[i], mult, -ref));
+                            const float b2 = ex2(fmaf(x[i + 1], mult, -ref));
+                            l4[i & 3] += a;
+                            l4[(i + 1) & 3] += b2;
+                            hi[i / 2] = Pair<DT>::pack(a, b2);
+                            const float2 y = Pair<DT>::unpack(hi[i / 2]);
+                            lo[i / 2] = Pair<DT>::pack(a - y.x, b2 - y.y);
+                            if (TP == 3) {
+                                const float2 z = Pair<DT>::unpack(lo[i / 2]);
+                                lo2[i / 2] = Pair<DT>::pack(a - y.x - z.x, b2 - y.y - z.y);
+                            }
+                        }
+                        tmem_st16w(ts + c, hi);
+                        tmem_st16w(ts + c + 16, lo);
+                        if (TP == 3)
+                            tmem_st16w(ts + T + c / 2, lo2);
+                    }
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                arrive(SB_PFULL + s);
+                ++done;
+                ++mine;
+            }
+
+            // ---- epilogue
+            if (!wait(SB_OREADY, (uint32_t)items & 1u)) return false;
+            tc_fence_after();
+            float f_own = 1.f, f_other = 0.f;
+            if (joint) {
+                ms->state[w][r] = make_float2(m, l);
+                arrive(SB_XCH);
+                if (!wait(SB_XCH, (uint32_t)items & 1u)) return false;
+                const float2 x = ms->state[w ^ 1][r];
+                // (a sum that is no number takes part: only an empty state does not)
+                const float ma = l == 0.f ? -INFINITY : m, mb = x.y == 0.f ? -INFINITY : x.x;
+                const float mm = fmaxf(ma, mb);
+                f_own = l == 0.f ? 0.f : ex2(m - mm);
+                f_other = x.y == 0.f ? 0.f : ex2(x.x - mm);
+                l = l * f_own + x.y * f_other;
+                m = mm;
+            }
+            if (dead) l = 0.f;
+            const bool odd = !(l - l == 0.f); // no number, or infinite
+            const float inv = p.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const bool writes = owner;
+#pragma unroll 1
+            for (int c = c0; c < c0 + nc; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+                if (joint) {
+                    float o2[16];
+                    tmem_ld16(tl + (w ^ 1) * D + c, o2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = f_own * o[i] + f_other * o2[i];
+                } else {
+                    tmem_wait_ld();
+                }
+                if (writes && (p.whole || l != 0.f)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : odd ? NAN : o[i] * inv;
+                    write_cols(c, o);
+                }
+            }
+            if (writes && !p.whole && (!joint || w == 0))
+                p.ml[wrow] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
+                             : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
+            // the next item starts from zero
+            zero_o(to + c0, nc);
+            if (joint) zero_o(tl + (w ^ 1) * D + c0, nc);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(SB_OFREE);
+            n += 2 * it.tiles;
+            ++items;
+            return true;
+        });
+        if (!ok && lane == 0) timed_out();
+    }
+
+    // ---------------------------------- teardown ----------------------------------
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::WARPS + 1) tmem_dealloc(tmem, 512);
+}
+
+template <typename C>
+cudaError_t launch(int grid, int smem, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
+                   const ScoredParams &p)
+{
+    auto *fn = gqa_scored_kernel<C>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    fn<<<grid, C::THREADS, smem, st>>>(km, vm, p);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_gqa_scored(int kv_dtype, int head_dim, int p_terms, int grid, int smem,
+                              cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
+                              const ScoredParams &p)
+{
+    if (kv_dtype == DA_F16) {
+        if (head_dim == 128) return launch<Cfg<__half, 128, 2>>(grid, smem, st, km, vm, p);
+        return launch<Cfg<__half, 256, 2>>(grid, smem, st, km, vm, p);
+    }
+    if (p_terms == 2) {
+        if (head_dim == 128) return launch<Cfg<__nv_bfloat16, 128, 2>>(grid, smem, st, km, vm, p);
+        return launch<Cfg<__nv_bfloat16, 256, 2>>(grid, smem, st, km, vm, p);
+    }
+    if (head_dim == 128) return launch<Cfg<__nv_bfloat16, 128, 3>>(grid, smem, st, km, vm, p);
+    return launch<Cfg<__nv_bfloat16, 256, 3>>(grid, smem, st, km, vm, p);
+}
+
+} // namespace skv

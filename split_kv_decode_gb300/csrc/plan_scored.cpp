@@ -1,0 +1,138 @@
+// Planner of scored attention: how the shared positions and the sequences' own spans are cut into
+// items. Pure host code, no CUDA calls.
+//
+// The kernel is persistent, one CTA an SM; item i of a round goes to CTA i, every other round
+// from the last CTA to the first, the shared items before the others and those by size. The planner
+// scores candidates by that assignment, in units of a sixteenth of the time that a K and a V
+// tile take from memory at one SM's share of the rate, and keeps the cheapest.
+#include <algorithm>
+#include <cstdint>
+#include <vector>
+
+#include "scored.h"
+
+namespace skv {
+
+namespace {
+
+constexpr int64_t kUnit = 16;
+constexpr int64_t kMaxItems = 1 << 22;
+constexpr int64_t kSimulated = 1 << 14; // items whose assignment is followed
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+} // namespace
+
+void scored_order(const int32_t *tiles, const int32_t *chunk, int batch, uint8_t *order)
+{
+    for (int b = 0; b < batch; ++b) order[b] = (uint8_t)b;
+    std::stable_sort(order, order + batch, [&](uint8_t x, uint8_t y) {
+        return std::min(tiles[x], chunk[x]) > std::min(tiles[y], chunk[y]);
+    });
+}
+
+int plan_scored(const ScoredWork &w, ScoredSplit *out)
+{
+    // costs of an item beside its tiles: q, the first tile's latency and the epilogue, and the
+    // partials that it writes and the combine reads, in units
+    const int64_t tile_bytes = (int64_t)w.tile * w.head_dim * 4;
+    const int64_t fixed = 2 * kUnit * 128 / w.tile;
+    auto partials = [&](int rows) { return (int64_t)rows * w.head_dim * 8 * kUnit / tile_bytes; };
+    // a shared tile: its MMAs take about a third of its time from memory for each term of q and of
+    // the weights and 128 rows
+    const int64_t shared_tile = std::max<int64_t>(
+        kUnit, kUnit * w.units * (w.q_terms + w.p_terms) * 10 / 30);
+
+    struct Candidate {
+        std::vector<int32_t> chunk;
+        int32_t shared;
+    };
+    std::vector<Candidate> cand;
+    int32_t most = w.shared_tiles;
+    int64_t total = (int64_t)w.shared_tiles * w.row_tiles * w.hkv;
+    for (int b = 0; b < w.batch; ++b) {
+        most = std::max(most, w.tiles[b]);
+        total += (int64_t)w.tiles[b] * w.hkv * w.row_groups;
+    }
+    auto even = [](int tiles, int64_t n) { // chunks of n splits of about one size
+        return tiles ? (int32_t)ceil_div(tiles, std::min<int64_t>(std::max<int64_t>(n, 1), tiles)) : 1;
+    };
+    if (w.force_splits > 0) {
+        Candidate c;
+        for (int b = 0; b < w.batch; ++b) c.chunk.push_back(even(w.tiles[b], w.force_splits));
+        c.shared = even(w.shared_tiles, w.force_splits);
+        cand.push_back(c);
+    } else {
+        for (double t = std::max(1.0, (double)total / (24.0 * w.slots));; t *= 1.19) {
+            for (int round = 0; round < 2; ++round) {
+                Candidate c;
+                // (a) splits of at most t tiles, (b) of about t
+                auto splits = [&](int tiles, double share) {
+                    const double n = tiles / share;
+                    return (int64_t)(round ? n + 0.5 : n + 0.999);
+                };
+                for (int b = 0; b < w.batch; ++b)
+                    c.chunk.push_back(even(w.tiles[b], splits(w.tiles[b], t)));
+                c.shared = even(w.shared_tiles, splits(w.shared_tiles, t * kUnit / shared_tile));
+                cand.push_back(c);
+            }
+            if (t > most) break;
+        }
+    }
+
+    int64_t best = -1;
+    std::vector<int64_t> load;
+    std::vector<uint8_t> order((size_t)w.batch);
+    for (const Candidate &c : cand) {
+        const int64_t ss = w.shared_tiles ? ceil_div(w.shared_tiles, c.shared) : 0;
+        int64_t items = ss * w.hkv * w.row_tiles;
+        int64_t most_splits = 1;
+        for (int b = 0; b < w.batch; ++b) {
+            const int64_t n = std::max<int64_t>(1, ceil_div(w.tiles[b], c.chunk[b]));
+            items += n * w.hkv * w.row_groups;
+            most_splits = std::max(most_splits, n + ss);
+        }
+        if (items > kMaxItems) continue;
+        // (candidates of very many items: the mean load instead of the largest)
+        const int64_t grid = std::min<int64_t>(items, w.slots);
+        const bool exact = items <= kSimulated;
+        int64_t cost = 0, sum = 0, i = 0;
+        load.assign((size_t)grid, 0);
+        auto add = [&](int64_t n, int64_t each) {
+            sum += n * each;
+            for (int64_t k = 0; exact && k < n; ++k, ++i) {
+                const int64_t r = i / grid, at = i - r * grid;
+                load[(size_t)(r & 1 ? grid - 1 - at : at)] += each;
+            }
+        };
+        const int64_t per = (int64_t)w.hkv * w.row_tiles;
+        for (int64_t s = 0; s < ss; ++s)
+            add(per, fixed + partials(w.shared_rows) +
+                         shared_tile * std::min<int64_t>(c.shared, w.shared_tiles - s * c.shared));
+        scored_order(w.tiles, c.chunk.data(), w.batch, order.data());
+        for (int b : order) {
+            const int64_t n = std::max<int64_t>(1, ceil_div(w.tiles[b], c.chunk[b]));
+            const int64_t each = fixed + partials(w.own_rows);
+            // (all splits but the last are of one size)
+            add((n - 1) * w.hkv * w.row_groups, each + kUnit * c.chunk[b]);
+            add((int64_t)w.hkv * w.row_groups,
+                each + kUnit * (w.tiles[b] - (n - 1) * c.chunk[b]));
+        }
+        cost = exact ? *std::max_element(load.begin(), load.end()) : sum / grid;
+        if (most_splits > 1) cost += 2 * kUnit * 128 / w.tile; // the combine's launch
+        if (best < 0 || cost < best) {
+            best = cost;
+            for (int b = 0; b < w.batch; ++b) {
+                out->chunk[b] = c.chunk[b];
+                out->n_splits[b] = (int32_t)std::max<int64_t>(1, ceil_div(w.tiles[b], c.chunk[b]));
+            }
+            out->shared_chunk = c.shared;
+            out->shared_splits = (int32_t)ss;
+            out->items = items;
+            out->cost = cost;
+        }
+    }
+    return best < 0 ? 1 : 0;
+}
+
+} // namespace skv

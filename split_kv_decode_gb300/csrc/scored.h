@@ -1,0 +1,112 @@
+// Scored attention (decode_attn_splitk_scored): what the host and the kernel share.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace skv {
+
+// positions of a tile, softmax warpgroups, and 16-bit terms of a weight
+__host__ __device__ constexpr int scored_tile(int D, int terms)
+{
+    return D == 128 && terms == 2 ? 128 : 64;
+}
+__host__ __device__ constexpr int scored_groups(int D) { return D == 128 ? 2 : 1; }
+// terms of a weight (and of an f32 q): f16 carries 11 bits a term, bf16 8
+constexpr int scored_terms(int kv_dtype, int out_dtype)
+{
+    return kv_dtype == DA_BF16 && out_dtype == DA_F32 ? 3 : 2;
+}
+constexpr int kScoredMaxSlots = 8;
+constexpr int kScoredMisc = 4096; // barriers, exchange of (m, l), row scales
+constexpr int kScoredSmemMax = 232448;
+
+// Shared memory: Q [row tile][term][64-column chunk][rpad rows of 128 bytes], then a ring of
+// K and V tiles, then the rest.
+struct ScoredGeometry {
+    int q_terms;   // 1: q is of the cache's type
+    int tile_rows; // query rows of an item, at most (256: two row tiles that share K and V tiles)
+    int rpad;      // rows of a Q chunk
+    int q_bytes;
+    int slots;     // of the ring
+    int smem;
+};
+
+// max_rows: query rows of the widest item that the call could have
+inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int max_rows)
+{
+    ScoredGeometry g;
+    g.q_terms = q_terms;
+    const int slot = scored_tile(D, p_terms) * D * 2;
+    // (two row tiles only for a q of one term: with more terms the ring would be too short)
+    for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
+        const int rows = max_rows < g.tile_rows ? max_rows : g.tile_rows;
+        g.rpad = rows >= 128 ? 128 : (rows + 7) / 8 * 8;
+        g.q_bytes = (rows > 128 ? 2 : 1) * q_terms * g.rpad * D * 2;
+        g.slots = (kScoredSmemMax - 1024 - kScoredMisc - g.q_bytes) / slot;
+        if (g.slots >= 3 || g.tile_rows == 64) break;
+    }
+    if (g.slots > kScoredMaxSlots) g.slots = kScoredMaxSlots;
+    // the 128-row MMA reads 128 rows from every Q chunk: past the last one, into the ring
+    g.smem = 1024 + g.q_bytes + g.slots * slot + kScoredMisc;
+    return g;
+}
+
+struct ScoredParams {
+    const void *q;
+    void *out;               // written by the kernel itself if whole
+    float2 *ml;              // workspace (m, l) per (slot, row)
+    float *acc;              // workspace acc per (slot, row, D)
+    int *status;
+    const float *slopes;     // per query head, or NULL
+    const int32_t *starts, *keep_lens;
+    const int32_t *dev_lens;
+    const int32_t *block_table, *shared_table;
+    uint64_t timeout_ns;
+    float scale, softcap;
+    int32_t batch, rows, q_len, hq, hkv; // rows: q_len * hq
+    int32_t q_f32, q_terms, out_dtype, whole, flags;
+    int32_t window, keep;
+    int32_t max_blocks, block_size, oob_block, box_rows;
+    int32_t rpad, tile_rows, slots, q_bytes;
+    int32_t row_groups;      // of a sequence's rows of one KV head
+    // items of the shared positions: (split, KV head, row tile), the row tile fastest
+    int32_t shared_len, shared_tiles, shared_chunk, shared_splits, row_tiles, shared_items;
+    // then those of the sequences: entry e is sequence seq[e], (split, KV head, row group)
+    int32_t n_items;
+    int32_t lens[DA_MAX_BATCH];      // of sequence b
+    int32_t chunk[DA_MAX_BATCH];     // tiles of a split of sequence b
+    int32_t slot[DA_MAX_BATCH];      // sequence b's first partial: the shared splits', then its own
+    int32_t base[DA_MAX_BATCH + 1];  // splits before entry e
+    uint8_t seq[DA_MAX_BATCH];
+};
+
+cudaError_t launch_gqa_scored(int kv_dtype, int head_dim, int p_terms, int grid, int smem,
+                              cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
+                              const ScoredParams &p);
+
+// Planner (plan_scored.cpp, pure host code). Lengths in tiles.
+struct ScoredWork {
+    int batch, hkv, row_groups;
+    const int32_t *tiles;   // of each sequence's visible span
+    int shared_tiles, row_tiles;
+    int units;              // row tiles of 128 rows in an item of the shared positions
+    int shared_rows;        // its rows
+    int own_rows;
+    int tile, q_terms, p_terms, head_dim;
+    int slots;              // CTAs
+    int force_splits;
+};
+struct ScoredSplit {
+    int32_t chunk[DA_MAX_BATCH], n_splits[DA_MAX_BATCH]; // of the sequences' own tiles
+    int32_t shared_chunk, shared_splits;
+    int64_t items, cost;
+};
+// Returns 0 on success, 1 if no split has an acceptable number of items.
+int plan_scored(const ScoredWork &w, ScoredSplit *out);
+// the sequences by their items' tiles, the longest first
+void scored_order(const int32_t *tiles, const int32_t *chunk, int batch, uint8_t *order);
+
+} // namespace skv
