@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int n = 0, items = 0;
         uint32_t sph = 0;                     // phases of SFULL, by slot
         int done = 0;                         // units of this warpgroup so far
-        uint32_t groups = 0;                  // uses of SB_GROUP
+        uint32_t groups = 0, joints = 0;      // uses of SB_GROUP and SB_XCH
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
             ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (joint) {
                 ms->state[w][r] = make_float2(m, l);
                 arrive(SB_XCH);
-                if (!wait(SB_XCH, (uint32_t)items & 1u)) return false;
+                if (!wait(SB_XCH, joints++ & 1u)) return false;
                 const float2 x = ms->state[w ^ 1][r];
                 // (a sum that is no number takes part: only an empty state does not)
                 const float ma = l == 0.f ? -INFINITY : m, mb = x.y == 0.f ? -INFINITY : x.x;

@@ -111,7 +111,7 @@ def test_what_is_not_seen_may_hold_anything():
 def test_rows_that_are_no_numbers_reach_the_tokens_that_see_them(d, cache, out):
     # three new tokens; the second one's key or value, or a value at a window's lower end, is
     # not a number: the tokens that do not see it are as if it were not there
-    for what, j in (("v", 298), ("k", 298), ("v", 299), ("v", 199), ("v", 200)):
+    for what, j in (("v", 298), ("k", 298), ("v", 299), ("v", 199), ("v", 198)):
         for value in (math.nan, math.inf):
             c = Case([300], 8, 2, d, q_len=3, window=100, cache=cache, out=out)
             at = (int(c.table[0, j // 16]), j % 16)
@@ -192,6 +192,19 @@ def test_shared_positions_and_unused_places():
 def test_shared_positions_in_forced_splits(splits):
     Case([300, 20], 8, 2, 128, shared=640, force_splits=splits).check()
     Case([300, 20] * 20, 8, 1, 128, shared=640, force_splits=splits, out="bf16").check()
+
+
+@pytest.mark.parametrize("sms", [1, 2, 5])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("shared", [0, 320])
+def test_many_items_of_every_kind_on_one_cta(shared, d, sms):
+    # items of two row tiles, of one, of one tile, without tiles, one after the other
+    lens = [5, 0, 300, 64, 1, 900] * 6 + [129]
+    for splits in (0, 3):
+        c = Case(lens, 16, 2, d, shared=shared, page=64, num_sms=sms, force_splits=splits,
+                 out="bf16", max_lens=[max(n, 200) for n in lens])
+        c.check()
+    Case(lens, 16, 2, d, shared=shared, page=64, num_sms=sms, q="f32").check()
 
 
 # ---- numerics
