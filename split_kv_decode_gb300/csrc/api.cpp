@@ -871,8 +871,8 @@ int check_scored(const da_args_t *a, const da_score_t *s, const int32_t *lens, S
     out->p_terms = scored_terms(a->kv_dtype, a->out_dtype);
     out->tile = scored_tile(a->head_dim, out->p_terms);
     const int64_t shared_rows = s->shared_len ? (int64_t)a->batch * G : 0;
-    out->g = scored_geometry(a->head_dim, s->q_dtype == DA_F32 ? out->p_terms : 1, out->p_terms,
-                             (int)std::max<int64_t>(G, shared_rows));
+    out->g = scored_geometry(a->head_dim, s->q_dtype == DA_F32 ? out->p_terms : 1, out->p_terms, G,
+                             shared_rows);
     if (out->g.slots < 3) return fail(DA_EUNSUPPORTED, "args", "no room for the tiles");
     out->row_groups = (int)ceil_div(G, out->g.tile_rows);
     out->row_tiles = (int)ceil_div(shared_rows, out->g.tile_rows);
@@ -1230,9 +1230,14 @@ int decode_attn_plan_scored(const da_args_t *a, const da_score_t *s, const int32
     }
     const int G = a->n_heads / a->n_kv_heads * q_len_of(a);
     const int shared_rows = s->shared_len ? std::min(a->batch * G, x.g.tile_rows) : 0;
+    const int own_rows = std::min(G, x.g.tile_rows);
     const ScoredWork w = {a->batch, a->n_kv_heads, x.row_groups, x.tiles, x.shared_tiles,
                           x.row_tiles, shared_rows > 128 ? 2 : 1, shared_rows,
-                          std::min(G, x.g.tile_rows), x.tile, x.g.q_terms, x.p_terms, a->head_dim,
+                          own_rows, x.tile, x.g.q_terms, x.p_terms, a->head_dim,
+                          scored_max_tiles(x.g, a->head_dim, x.p_terms, shared_rows,
+                                           a->out_dtype == DA_F32),
+                          scored_max_tiles(x.g, a->head_dim, x.p_terms, own_rows,
+                                           a->out_dtype == DA_F32),
                           num_sms, a->force_splits};
     ScoredSplit o;
     if (plan_scored(w, &o)) return fail(DA_EUNSUPPORTED, "plan", "too many work items");

@@ -17,8 +17,8 @@
 //
 // Operands are 16-bit, sums f32. K and V are used as they stand. A weight is the sum of two 16-bit
 // terms (three for f32 outputs of bf16 caches), so are the elements of an f32 q; the terms are
-// MMAs into one accumulator. P takes the place of its scores in TMEM: 32 scores (32 columns) become
-// two terms of 16 columns.
+// MMAs into one accumulator. P takes the place of its scores in TMEM: 16 scores (16 columns) become
+// two terms of 8 columns.
 //
 // What bounds it: memory. A tile of K and V takes 2800 cycles at an SM's share of the rate, its
 // MMAs 1500 (one term of q) and the softmax of a warpgroup about as much, with two
@@ -68,15 +68,21 @@ constexpr int SB_FULL = 0, SB_EMPTY = kScoredMaxSlots, SB_SFULL = 2 * kScoredMax
               SB_N = SB_DRAIN + 1;
 
 // the part of shared memory behind the ring
-struct Misc {
+template <int NWG> struct Misc {
     uint64_t bar[SB_N];
     uint32_t tmem;
     int abort;
-    uint32_t bad[2][4];     // rows of a unit's V tile that hold no numbers, by its S slot
-    float2 state[2][128];   // (m, l) of a warpgroup's rows
-    float row_scale[256];   // of an f32 q beside an f16 cache
+    uint32_t bad[2][4];       // rows of a unit's V tile that hold no numbers, by its S slot
+    float2 state[NWG][128];   // (m, l) of a warpgroup's lanes
+    union {
+        float row_scale[128]; // of an f32 q beside an f16 cache (at most 128 rows then)
+        struct {              // in the epilogue, of rows that several lanes share:
+            float factor[64]; // what their sum is multiplied by,
+            uint32_t to[64];  // and the row that it goes to
+        } row;
+    };
 };
-static_assert(sizeof(Misc) <= kScoredMisc, "misc");
+static_assert(sizeof(Misc<1>) <= scored_misc(256) && sizeof(Misc<2>) <= scored_misc(128), "misc");
 
 struct Item {
     bool shared;
@@ -234,6 +240,14 @@ __device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8w(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
 {
     tmem_ld16(taddr, v);
@@ -256,26 +270,34 @@ __device__ __forceinline__ uint64_t l2_normal_policy()
     return p;
 }
 
-// what turns a row's raw score into y log2 e
+// What turns a row's raw score into y log2 e.
 struct Scorer {
-    float mult;      // scale log2 e of the row (1 once the scores are transformed)
+    float mult;      // scale log2 e of the row
     float cap;       // softcap log2 e; 0: none
-    float turn;      // 2 scale log2 e / softcap of the row, or scale / softcap (precise)
+    float turn;      // scale / softcap of the row
     float slope;     // slope log2 e
-    bool precise;
-    // raw: the score; d: the token's position less the key's
-    __device__ __forceinline__ float operator()(float raw, float d) const
-    {
-        float y = raw * mult;
-        if (cap != 0.f) {
-            // tanh z = 1 - 2 / (1 + e^2z): off by 2^-22 of the cap, which 16-bit outputs do not
-            // see; f32 outputs take the function that is as near for small z
-            y = precise ? cap * tanhf(raw * turn)
-                        : fmaf(__fdividef(-2.f * cap, 1.f + ex2(raw * turn)), 1.f, cap);
-        }
-        return fmaf(-slope, fabsf(d), y);
-    }
 };
+
+// c tanh z. 16-bit outputs: tanh z = 1 - 2 / (1 + e^2z), off by a few 2^-23 of c. f32 outputs: for
+// |z| < 0.75, where that is far off relative to tanh z, Lambert's continued fraction to its fifth
+// term, z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4), off by less than 2^-26 there.
+template <bool PRECISE> __device__ __forceinline__ float capped(float z, float c)
+{
+    const float far = fmaf(-2.f * c, __fdividef(1.f, 1.f + ex2(z * (2.f * kLog2e))), c);
+    if (!PRECISE) return far;
+    const float zz = z * z;
+    const float near = c * z * __fdividef(fmaf(zz, zz + 105.f, 945.f),
+                                          fmaf(zz, fmaf(zz, 15.f, 420.f), 945.f));
+    return fabsf(z) < 0.75f ? near : far;
+}
+
+// bits i of 0 .. 15 with lo <= i < hi
+__device__ __forceinline__ uint32_t range16(int lo, int hi)
+{
+    lo = max(lo, 0);
+    hi = min(hi, 16);
+    return hi > lo ? (0xffffu >> (16 - hi)) & (0xffffu << lo) : 0u;
+}
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -290,7 +312,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
     const int nst = p.slots;
-    Misc *ms = reinterpret_cast<Misc *>(sm + p.q_bytes + nst * C::SLOT);
+    auto *ms = reinterpret_cast<Misc<NWG> *>(sm + p.q_bytes + nst * C::SLOT);
     uint64_t *bar = ms->bar;
     volatile int *abort_flag = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -440,8 +462,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < T / 16; ++k)
                                 tc_mma_ts(tmem + w * D,
-                                          a + (x < 2 ? 32 * (k / 2) + 16 * x + 8 * (k & 1)
-                                                     : T + 8 * k),
+                                          a + (x < 2 ? 16 * k + 8 * x : T + 8 * k),
                                           vd + (uint64_t)((k * 2048) >> 4), idesc_pv);
                         if (sh == 0 || (u & 1)) tc_commit(bar + SB_EMPTY + st);
                         tc_commit(bar + SB_PVDONE + w);
@@ -454,7 +475,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             sb + (sh ? (v & 1) * p.q_terms * NCH * qch : 0);
                         const uint64_t qd = smem_desc_sw128(q0, 16, 1024);
                         const uint64_t kd = smem_desc_sw128(sb + p.q_bytes + st * C::SLOT, 16, 1024);
-                        for (int x = 0; x < p.q_terms; ++x)
+                        // the small terms first: an MMA's sums are cut off at their 24th bit, so
+                        // that each addition to a large sum costs about 2^-24 of it
+                        for (int x = p.q_terms - 1; x >= 0; --x)
 #pragma unroll
                             for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                         tmem + C::S_COL + s * 128,
                                         qd + (uint64_t)(((x * NCH + c) * qch + k * 32) >> 4),
                                         kd + (uint64_t)((c * CHUNK + k * 32) >> 4), idesc_qk,
-                                        (x | c | k) != 0 ? 1u : 0u);
+                                        x != p.q_terms - 1 || (c | k) != 0 ? 1u : 0u);
                         tc_commit(bar + SB_SFULL + s);
                         if (sh == 0 || (v & 1)) tc_commit(bar + SB_EMPTY + st);
                         if (v == nu - 1) tc_commit(bar + SB_QFREE);
@@ -500,10 +523,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + b);
         };
-        // all warps of the warpgroup have come here
+        // all warps of the warpgroup, or of both, have come here
         auto group_sync = [&]() {
             arrive(SB_GROUP + w);
             return wait(SB_GROUP + w, groups++ & 1u);
+        };
+        auto all_sync = [&]() {
+            arrive(SB_XCH);
+            return wait(SB_XCH, joints++ & 1u);
         };
         auto zero_o = [&](uint32_t addr, int cols) {
             const float z[16] = {};
@@ -515,10 +542,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         arrive(SB_OFREE);
 
         each_item<T>(p, [&](const Item &it) {
-            // ---- this thread's row
+            // ---- this thread's row and its share of every tile's columns
             const int nrt = it.nrt;
-            const int local = nrt == 2 ? w * 128 + r : r; // row of the item
-            const bool owner = local < it.rows;
+            // few rows: Q has copies at lanes span, 2 span, ..., whose warps each take a share of the
+            // columns; the other weights of such a lane are zero
+            const int span = nrt == 2 || it.rows > 64 ? 128 : it.rows > 32 ? 64 : 32;
+            const int reps = nrt == 2 ? 1 : max(1, p.rpad / span);
+            const int rep = (warp & 3) * 32 / span;
+            const bool in_use = rep < reps;                    // (of this warp)
+            const int cols = T / reps, cb = in_use ? rep * cols : 0;
+            const int local = nrt == 2 ? w * 128 + r : r - rep * span; // row of the item
+            const bool owner = in_use && local < it.rows;
+            const bool busy = in_use && (local & ~31) < it.rows;
             const int per_seq = p.q_len * Gh;
             int row = it.row0 + (owner ? local : 0), b = it.b, S, q0;
             if (it.shared) {
@@ -535,35 +570,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const bool dead = !owner || own < 0;   // no such token: it sees nothing
             const int out_row = tk * p.hq + h;
             const size_t slot = (size_t)p.slot[b] + it.split + (it.shared ? 0 : p.shared_splits);
-            const size_t wrow = slot * p.rows + out_row;
-            // columns of this thread in the epilogue
-            const bool joint = NWG == 2 && nrt == 1;
-            const int c0 = joint ? w * (D / 2) : 0, nc = joint ? D / 2 : D;
-            auto write_cols = [&](int c, const float *x) { // 16 columns of its row, normalised or not
-                if (p.whole) {
-                    const size_t at = ((size_t)b * p.rows + out_row) * D + c;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 f = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                        if (p.out_dtype == DA_F32) store4(static_cast<float *>(p.out) + at + i, f);
-                        else if (p.out_dtype == DA_F16) store4(static_cast<__half *>(p.out) + at + i, f);
-                        else store4(static_cast<__nv_bfloat16 *>(p.out) + at + i, f);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        store4(p.acc + wrow * D + c + i,
-                               make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+            // its row of the output, or of the partials
+            const size_t dst_row = p.whole ? (size_t)b * p.rows + out_row : slot * p.rows + out_row;
+            auto write4 = [&](size_t row_at, int c, const float4 &f) {
+                if (!p.whole) {
+                    store4(p.acc + row_at * D + c, f);
+                    return;
                 }
+                const size_t at = row_at * D + c;
+                if (p.out_dtype == DA_F32) store4(static_cast<float *>(p.out) + at, f);
+                else if (p.out_dtype == DA_F16) store4(static_cast<__half *>(p.out) + at, f);
+                else store4(static_cast<__nv_bfloat16 *>(p.out) + at, f);
             };
             if (it.tiles == 0) { // nothing to see: a neutral partial
-                if (owner && (nrt == 2 || w == 0)) {
-                    if (p.whole) {
-                        const float z[16] = {};
-                        for (int c = 0; c < D; c += 16) write_cols(c, z);
-                    } else {
-                        p.ml[wrow] = make_float2(kNeutralM, 0.f);
-                    }
+                if (owner && rep == 0 && (nrt == 2 || w == 0)) {
+                    if (p.whole)
+                        for (int c = 0; c < D; c += 4)
+                            write4(dst_row, c, make_float4(0.f, 0.f, 0.f, 0.f));
+                    else
+                        p.ml[dst_row] = make_float2(kNeutralM, 0.f);
                 }
                 return true;
             }
@@ -573,8 +598,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             {
                 constexpr int U8 = D / 8; // 8-column units of a row: a half-warp's or a warp's
                 // (rows past them give scores that nobody reads)
-                const int rows_padded = (it.rows + 7) / 8 * 8;
-                const int units = rows_padded * U8;
+                const int units = (it.rows + 7) / 8 * 8 * U8;
                 for (int u = threadIdx.x; u < units; u += C::WARPS * 32) {
                     const int rr = u / U8, j = u - rr * U8;
                     const bool real = rr < it.rows;
@@ -585,13 +609,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     const int qt = qrow / Gh, qh = it.kvh * Gh + qrow - qt * Gh;
                     const size_t at = (((size_t)qb * p.q_len + qt) * p.hq + qh) * D + j * 8;
-                    const uint32_t dst = sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch +
-                                         swz(rr & 127, (j & 7) * 16);
+                    const uint32_t dst =
+                        sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch;
+                    auto put = [&](int x, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                        for (int k = 0; k < reps; ++k)
+                            sts_v4(dst + x * NCH * qch + swz((rr & 127) + k * span, (j & 7) * 16), a0,
+                                   a1, a2, a3);
+                    };
                     if (!p.q_f32) {
                         uint4 x = make_uint4(0, 0, 0, 0);
                         if (real) x = __ldg(reinterpret_cast<const uint4 *>(
                                       static_cast<const uint16_t *>(p.q) + at));
-                        sts_v4(dst, x.x, x.y, x.z, x.w);
+                        put(0, x.x, x.y, x.z, x.w);
                         continue;
                     }
                     float f[8];
@@ -630,32 +659,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             f[2 * i] -= y.x;
                             f[2 * i + 1] -= y.y;
                         }
-                        sts_v4(dst + x * NCH * qch, v[0], v[1], v[2], v[3]);
+                        put(x, v[0], v[1], v[2], v[3]);
                     }
                 }
             }
             fence_proxy_async_smem();
+            if (TP == 3 && reps > 1 && busy) {
+                // the third terms have columns of their own: zero but for this warp's share
+                const uint32_t z[16] = {};
+                for (int s = NWG == 2 ? w : 0; s < 2; s += NWG)
+                    for (int c = 0; c < T / 2; c += 16) tmem_st16w(tl + C::S_COL + s * 128 + T + c, z);
+                tmem_wait_st();
+            }
             arrive(SB_QFULL);
 
             // ---- what this row sees and how it scores
             Scorer sc;
             const int pos = own + (it.shared ? p.shared_len : 0); // in this item's positions
-            const float slope = p.slopes && owner ? __ldg(p.slopes + h) * kLog2e : 0.f;
-            bool scaled = false;
-            auto set_scorer = [&]() { // (an f32 q's row scale is there once all of Q is)
-                const float rs = !C::BF && p.q_f32 ? ms->row_scale[nrt == 2 ? w * 128 + r : r] : 1.f;
-                const float x = p.scale * rs;
-                sc.mult = x * kLog2e;
-                sc.precise = p.out_dtype == DA_F32;
-                sc.cap = p.softcap * kLog2e;
-                sc.turn = p.softcap == 0.f ? 0.f
-                                           : x / p.softcap * (sc.precise ? 1.f : 2.f * kLog2e);
-                sc.slope = slope;
-                scaled = true;
-            };
+            sc.slope = p.slopes && owner ? __ldg(p.slopes + h) * kLog2e : 0.f;
+            sc.cap = p.softcap * kLog2e;
+            sc.mult = sc.turn = 0.f;
+            const bool precise = p.out_dtype == DA_F32;
             // warp-uniform: scores are transformed before the maximum is taken
             const bool transform = p.softcap != 0.f || p.slopes || !(p.scale > 0.f);
-            const bool busy = (nrt == 2 ? w * 128 : 0) + (warp & 3) * 32 < it.rows;
             const int x_lo = p.window ? max(it.start, own - p.window + 1) : it.start;
             const int x_hi = dead ? 0 : own + 1;
 
@@ -670,7 +696,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (!wait(SB_SFULL + s, (sph >> s) & 1u)) return false;
                 sph ^= 1u << s;
                 tc_fence_after();
-                if (!scaled) set_scorer();
+                if (mine == 0) { // (an f32 q's row scale is there once all of Q is)
+                    const float x = p.scale * (!C::BF && p.q_f32 ? ms->row_scale[owner ? local : 0] : 1.f);
+                    sc.mult = x * kLog2e;
+                    sc.turn = p.softcap == 0.f ? 0.f : x / p.softcap;
+                }
 
                 // which columns are visible: all, all below a border, or row by row
                 bool full = t0 + T <= it.end;
@@ -691,43 +721,79 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         x1 = min(x_hi - t0, T);
                     }
                 }
-                // (no row, or a token that is not there, sees column 0 at least as unknown:
-                // its result is not used)
-                auto visible = [&](int c) { return (c >= x0 && c < x1) || (c >= k0 && c < k1); };
-
-                float tm = -INFINITY;
-                if (busy) {
-                    if (!transform && full) {
-#pragma unroll 1
-                        for (int c = 0; c < T; c += 32) {
-                            float x[32];
-                            tmem_ld32(ts + c, x);
-                            tmem_wait_ld();
+                const bool modified = transform || !full;
+                // 16 scores from column c on: y, -infinity where the row sees nothing
+                auto score16 = [&](float *x, int c) {
+                    if (p.softcap == 0.f) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) tm = fmaxf(tm, x[i]);
-                        }
-                        tm *= sc.mult;
+                        for (int i = 0; i < 16; ++i) x[i] *= sc.mult;
+                    } else if (precise) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = capped<true>(x[i] * sc.turn, sc.cap);
                     } else {
-                        // y (or -infinity where the row sees nothing) takes the score's place
-                        const float d0 = (float)(pos - t0);
-#pragma unroll 1
-                        for (int c = 0; c < T; c += 32) {
-                            float x[32];
-                            tmem_ld32(ts + c, x);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                x[i] = sc(x[i], d0 - (float)(c + i));
-                                if (!full && !visible(c + i)) x[i] = -INFINITY;
-                                tm = fmaxf(tm, x[i]);
-                            }
-                            tmem_st16(ts + c, x);
-                            tmem_st16(ts + c + 16, x + 16);
-                        }
-                        tmem_wait_st();
+                        for (int i = 0; i < 16; ++i) x[i] = capped<false>(x[i] * sc.turn, sc.cap);
                     }
+                    if (p.slopes) {
+                        const float d = (float)(pos - t0 - c);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = fmaf(-sc.slope, fabsf(d - (float)i), x[i]);
+                    }
+                    if (!full) {
+                        const uint32_t see = range16(x0 - c, x1 - c) | range16(k0 - c, k1 - c);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (!((see >> i) & 1u)) x[i] = -INFINITY;
+                    }
+                };
+                auto max16 = [&](const float *x) {
+                    float a = x[0], b2 = x[1];
+#pragma unroll
+                    for (int i = 2; i < 16; i += 2) {
+                        a = fmaxf(a, x[i]);
+                        b2 = fmaxf(b2, x[i + 1]);
+                    }
+                    return fmaxf(a, b2);
+                };
+                float tm = -INFINITY;
+                // up to 32 columns stay in registers until they are weights; more go back to TMEM
+                float xr[32];
+                const bool held = cols <= 32;
+                if (busy) {
+                    if (held) {
+                        tmem_ld16(ts + cb, xr);
+                        if (cols == 32) tmem_ld16(ts + cb + 16, xr + 16);
+                        tmem_wait_ld();
+                        if (modified) {
+                            score16(xr, cb);
+                            if (cols == 32) score16(xr + 16, cb + 16);
+                            if (!full && p.q_len > 1) { // (for the rows that are no numbers below)
+                                tmem_st16(ts + cb, xr);
+                                if (cols == 32) tmem_st16(ts + cb + 16, xr + 16);
+                                tmem_wait_st();
+                            }
+                        }
+                        tm = max16(xr);
+                        if (cols == 32) tm = fmaxf(tm, max16(xr + 16));
+                    } else {
+#pragma unroll 1
+                        for (int c = cb; c < cb + cols; c += 32) {
+                            tmem_ld32(ts + c, xr);
+                            tmem_wait_ld();
+                            if (modified) {
+                                score16(xr, c);
+                                tmem_st16(ts + c, xr);
+                                score16(xr + 16, c + 16);
+                                tmem_st16(ts + c + 16, xr + 16);
+                            }
+                            tm = fmaxf(tm, fmaxf(max16(xr), max16(xr + 16)));
+                        }
+                        if (modified) tmem_wait_st();
+                    }
+                    if (!modified) tm *= sc.mult;
                 }
-                const float mult = !transform && full ? sc.mult : 1.f;
+                const float mult = modified ? 1.f : sc.mult;
                 // ---- the reference moves where a weight would pass 2^LIM
                 const bool moves = owner && tm > m + C::LIM;
                 if (__any_sync(0xffffffffu, moves)) {
@@ -802,7 +868,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             for (int c = 0; c < T; ++c) {
                                 if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
                                 const float y = tmem_ld1(ts + c);
-                                const bool sees = !dead && visible(c);
+                                const bool sees = !dead && c >= cb && c < cb + cols &&
+                                                  ((c >= x0 && c < x1) || (c >= k0 && c < k1));
                                 const float pr = ex2(y - ref);
 #pragma unroll 1
                                 for (int j = 0; j < D / 16; ++j) {
@@ -839,30 +906,46 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // ---- P: the weights, in terms, in the place of their scores
                 if (busy) {
                     float l4[4] = {};
-#pragma unroll 1
-                    for (int c = 0; c < T; c += 32) {
-                        float x[32];
-                        tmem_ld32(ts + c, x);
-                        tmem_wait_ld();
-                        uint32_t hi[16], lo[16], lo2[16];
+                    auto weigh16 = [&](const float *x, int c) {
+                        uint32_t t16[16], third[8];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             const float a = ex2(fmaf(x[i], mult, -ref));
                             const float b2 = ex2(fmaf(x[i + 1], mult, -ref));
                             l4[i & 3] += a;
                             l4[(i + 1) & 3] += b2;
-                            hi[i / 2] = Pair<DT>::pack(a, b2);
-                            const float2 y = Pair<DT>::unpack(hi[i / 2]);
-                            lo[i / 2] = Pair<DT>::pack(a - y.x, b2 - y.y);
+                            t16[i / 2] = Pair<DT>::pack(a, b2);
+                            const float2 y = Pair<DT>::unpack(t16[i / 2]);
+                            t16[8 + i / 2] = Pair<DT>::pack(a - y.x, b2 - y.y);
                             if (TP == 3) {
-                                const float2 z = Pair<DT>::unpack(lo[i / 2]);
-                                lo2[i / 2] = Pair<DT>::pack(a - y.x - z.x, b2 - y.y - z.y);
+                                const float2 z = Pair<DT>::unpack(t16[8 + i / 2]);
+                                third[i / 2] = Pair<DT>::pack(a - y.x - z.x, b2 - y.y - z.y);
                             }
                         }
-                        tmem_st16w(ts + c, hi);
-                        tmem_st16w(ts + c + 16, lo);
-                        if (TP == 3)
-                            tmem_st16w(ts + T + c / 2, lo2);
+                        tmem_st16w(ts + c, t16);
+                        if (TP == 3) tmem_st8w(ts + T + c / 2, third);
+                    };
+                    if (held) {
+                        weigh16(xr, cb);
+                        if (cols == 32) weigh16(xr + 16, cb + 16);
+                        const uint32_t z[16] = {};
+#pragma unroll 1
+                        for (int c = 0; c < T; c += 16)
+                            if (c < cb || c >= cb + cols) tmem_st16w(ts + c, z);
+                    } else {
+#pragma unroll 1
+                        for (int c = cb; c < cb + cols; c += 32) {
+                            tmem_ld32(ts + c, xr);
+                            tmem_wait_ld();
+                            weigh16(xr, c);
+                            weigh16(xr + 16, c + 16);
+                        }
+                        if (reps > 1) {
+                            const uint32_t z[16] = {};
+#pragma unroll 1
+                            for (int c = 0; c < T; c += 16)
+                                if (c < cb || c >= cb + cols) tmem_st16w(ts + c, z);
+                        }
                     }
                     l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tmem_wait_st();
@@ -873,30 +956,44 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 ++mine;
             }
 
-            // ---- epilogue
+            // ---- epilogue: a row's states, of the warpgroups that took tiles in turn and of the
+            // copies of its lane, are joined
             if (!wait(SB_OREADY, (uint32_t)items & 1u)) return false;
             tc_fence_after();
+            const bool joint = NWG == 2 && nrt == 1;
+            const int c0 = joint ? w * (D / 2) : 0, nc = joint ? D / 2 : D; // this thread's columns
             float f_own = 1.f, f_other = 0.f;
-            if (joint) {
+            if (joint || reps > 1) {
                 ms->state[w][r] = make_float2(m, l);
-                arrive(SB_XCH);
-                if (!wait(SB_XCH, joints++ & 1u)) return false;
-                const float2 x = ms->state[w ^ 1][r];
+                if (!all_sync()) return false;
                 // (a sum that is no number takes part: only an empty state does not)
-                const float ma = l == 0.f ? -INFINITY : m, mb = x.y == 0.f ? -INFINITY : x.x;
-                const float mm = fmaxf(ma, mb);
+                const int first = owner ? local : 0;
+                float mm = -INFINITY, ll = 0.f;
+                for (int k = 0; k < reps * NWG; ++k) {
+                    const float2 x = ms->state[k % NWG][first + k / NWG * span];
+                    if (x.y != 0.f) mm = fmaxf(mm, x.x);
+                }
+                for (int k = 0; k < reps * NWG; ++k) {
+                    const float2 x = ms->state[k % NWG][first + k / NWG * span];
+                    if (x.y != 0.f) ll += x.y * ex2(x.x - mm);
+                }
                 f_own = l == 0.f ? 0.f : ex2(m - mm);
-                f_other = x.y == 0.f ? 0.f : ex2(x.x - mm);
-                l = l * f_own + x.y * f_other;
+                if (joint) {
+                    const float2 x = ms->state[NWG - 1 - w][r];
+                    f_other = x.y == 0.f ? 0.f : ex2(x.x - mm);
+                }
                 m = mm;
+                l = ll;
             }
             if (dead) l = 0.f;
             const bool odd = !(l - l == 0.f); // no number, or infinite
-            const float inv = p.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const bool writes = owner;
-#pragma unroll 1
-            for (int c = c0; c < c0 + nc; c += 16) {
-                float o[16];
+            const float factor = l == 0.f ? 0.f : odd ? NAN : p.whole ? 1.f / l : 1.f;
+            const bool writes = owner && rep == 0;
+            if (writes && !p.whole && (!joint || w == 0))
+                p.ml[dst_row] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
+                                : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
+            // 16 columns of the lane, its warpgroups' joined
+            auto lane16 = [&](int c, float *o) {
                 tmem_ld16(to + c, o);
                 if (joint) {
                     float o2[16];
@@ -906,16 +1003,73 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int i = 0; i < 16; ++i) o[i] = f_own * o[i] + f_other * o2[i];
                 } else {
                     tmem_wait_ld();
-                }
-                if (writes && (p.whole || l != 0.f)) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : odd ? NAN : o[i] * inv;
-                    write_cols(c, o);
+                    for (int i = 0; i < 16; ++i) o[i] *= f_own;
+                }
+            };
+            if (reps == 1) {
+#pragma unroll 1
+                for (int c = c0; c < c0 + nc; c += 16) {
+                    float o[16];
+                    lane16(c, o);
+                    if (writes && (p.whole || l != 0.f)) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = factor == 0.f ? 0.f : o[i] * factor;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            write4(dst_row, c + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+                    }
+                }
+            } else {
+                // the copies' sums meet in the place of Q, whose MMAs are done: [copy][row][columns
+                // of a pass], in one pass or two
+                const int rows8 = (it.rows + 7) / 8 * 8;
+                const int passes = reps * rows8 * D * 4 <= p.q_bytes ? 1 : 2, width = nc / passes;
+                const int stride = D / passes; // columns of a row: of all warpgroups
+                if (writes && w == 0) {
+                    ms->row.factor[local] = factor;
+                    ms->row.to[local] = (uint32_t)dst_row;
+                }
+                float *xs = reinterpret_cast<float *>(sm);
+                for (int ps = 0; ps < passes; ++ps) {
+                    if (busy) {
+                        float *to_row = xs + (rep * rows8 + local) * stride + (joint ? w * width : 0);
+#pragma unroll 1
+                        for (int c = 0; c < width; c += 16) {
+                            float o[16];
+                            lane16(c0 + ps * width + c, o);
+                            if (owner) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4)
+                                    *reinterpret_cast<float4 *>(to_row + c + i) =
+                                        make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            }
+                        }
+                    }
+                    if (!all_sync()) return false;
+                    const int units = it.rows * stride / 4;
+                    for (int u = threadIdx.x; u < units; u += C::WARPS * 32) {
+                        const int rr = u / (stride / 4), c = (u - rr * (stride / 4)) * 4;
+                        const float fac = ms->row.factor[rr];
+                        if (fac == 0.f && !p.whole) continue;
+                        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < reps; ++k) {
+                            const float4 x = *reinterpret_cast<const float4 *>(
+                                xs + (k * rows8 + rr) * stride + c);
+                            sum.x += x.x;
+                            sum.y += x.y;
+                            sum.z += x.z;
+                            sum.w += x.w;
+                        }
+                        sum = fac == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                         : make_float4(sum.x * fac, sum.y * fac, sum.z * fac, sum.w * fac);
+                        // column c of the pass: of the warpgroup whose half it is in
+                        const int g = c / width;
+                        write4((size_t)ms->row.to[rr], g * nc + ps * width + c - g * width, sum);
+                    }
+                    if (!all_sync()) return false; // the place may be written again
                 }
             }
-            if (writes && !p.whole && (!joint || w == 0))
-                p.ml[wrow] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
-                             : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
             // the next item starts from zero
             zero_o(to + c0, nc);
             if (joint) zero_o(tl + (w ^ 1) * D + c0, nc);

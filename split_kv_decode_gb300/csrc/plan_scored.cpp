@@ -54,16 +54,27 @@ int plan_scored(const ScoredWork &w, ScoredSplit *out)
         most = std::max(most, w.tiles[b]);
         total += (int64_t)w.tiles[b] * w.hkv * w.row_groups;
     }
-    auto even = [](int tiles, int64_t n) { // chunks of n splits of about one size
-        return tiles ? (int32_t)ceil_div(tiles, std::min<int64_t>(std::max<int64_t>(n, 1), tiles)) : 1;
+    // chunks of n splits of about one size, of `most` tiles at most
+    auto even = [](int tiles, int64_t n, int most) {
+        if (!tiles) return (int32_t)1;
+        n = std::max(n, ceil_div(tiles, most));
+        return (int32_t)ceil_div(tiles, std::min<int64_t>(n, tiles));
     };
     if (w.force_splits > 0) {
         Candidate c;
-        for (int b = 0; b < w.batch; ++b) c.chunk.push_back(even(w.tiles[b], w.force_splits));
-        c.shared = even(w.shared_tiles, w.force_splits);
+        for (int b = 0; b < w.batch; ++b) c.chunk.push_back(even(w.tiles[b], w.force_splits, w.own_max));
+        c.shared = even(w.shared_tiles, w.force_splits, w.shared_max);
         cand.push_back(c);
     } else {
+        // targets: the even share of a number of rounds, and steps of a quarter octave
+        std::vector<double> targets;
+        for (int r = 1; r <= 12; ++r) targets.push_back((double)total / ((double)r * w.slots));
         for (double t = std::max(1.0, (double)total / (24.0 * w.slots));; t *= 1.19) {
+            targets.push_back(t);
+            if (t > most) break;
+        }
+        for (double t : targets) {
+            if (t < 0.25) continue;
             for (int round = 0; round < 2; ++round) {
                 Candidate c;
                 // (a) splits of at most t tiles, (b) of about t
@@ -72,11 +83,11 @@ int plan_scored(const ScoredWork &w, ScoredSplit *out)
                     return (int64_t)(round ? n + 0.5 : n + 0.999);
                 };
                 for (int b = 0; b < w.batch; ++b)
-                    c.chunk.push_back(even(w.tiles[b], splits(w.tiles[b], t)));
-                c.shared = even(w.shared_tiles, splits(w.shared_tiles, t * kUnit / shared_tile));
+                    c.chunk.push_back(even(w.tiles[b], splits(w.tiles[b], t), w.own_max));
+                c.shared = even(w.shared_tiles, splits(w.shared_tiles, t * kUnit / shared_tile),
+                                w.shared_max);
                 cand.push_back(c);
             }
-            if (t > most) break;
         }
     }
 

@@ -20,7 +20,9 @@ constexpr int scored_terms(int kv_dtype, int out_dtype)
     return kv_dtype == DA_BF16 && out_dtype == DA_F32 ? 3 : 2;
 }
 constexpr int kScoredMaxSlots = 8;
-constexpr int kScoredMisc = 4096; // barriers, exchange of (m, l), row scales
+// barriers, exchange of (m, l), row scales (at 256 columns beside 128 rows of two terms and three
+// tiles of the ring)
+__host__ __device__ constexpr int scored_misc(int D) { return D == 128 ? 3072 : 2048; }
 constexpr int kScoredSmemMax = 232448;
 
 // Shared memory: Q [row tile][term][64-column chunk][rpad rows of 128 bytes], then a ring of
@@ -34,24 +36,50 @@ struct ScoredGeometry {
     int smem;
 };
 
-// max_rows: query rows of the widest item that the call could have
-inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int max_rows)
+// own_rows: a sequence's query rows of a KV head; shared_rows: those of the batch, or 0
+inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_rows,
+                                      int64_t shared_rows)
 {
     ScoredGeometry g;
     g.q_terms = q_terms;
     const int slot = scored_tile(D, p_terms) * D * 2;
+    const int64_t most = shared_rows > own_rows ? shared_rows : own_rows;
     // (two row tiles only for a q of one term: with more terms the ring would be too short)
     for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
-        const int rows = max_rows < g.tile_rows ? max_rows : g.tile_rows;
-        g.rpad = rows >= 128 ? 128 : (rows + 7) / 8 * 8;
-        g.q_bytes = (rows > 128 ? 2 : 1) * q_terms * g.rpad * D * 2;
-        g.slots = (kScoredSmemMax - 1024 - kScoredMisc - g.q_bytes) / slot;
+        const int rows = (int)(most < g.tile_rows ? most : g.tile_rows);
+        // 128 lanes, with copies of few rows, where that leaves a ring of two tiles; a ring
+        // shorter than a tile and a half takes smaller items
+        for (g.rpad = 128;; g.rpad /= 2) {
+            g.q_bytes = (rows > 128 ? 2 : 1) * q_terms * g.rpad * D * 2;
+            g.slots = (kScoredSmemMax - 1024 - scored_misc(D) - g.q_bytes) / slot;
+            if (g.slots >= 4 || g.rpad / 2 < rows || g.rpad == 32) break;
+        }
         if (g.slots >= 3 || g.tile_rows == 64) break;
     }
     if (g.slots > kScoredMaxSlots) g.slots = kScoredMaxSlots;
     // the 128-row MMA reads 128 rows from every Q chunk: past the last one, into the ring
-    g.smem = 1024 + g.q_bytes + g.slots * slot + kScoredMisc;
+    g.smem = 1024 + g.q_bytes + g.slots * slot + scored_misc(D);
     return g;
+}
+
+// Copies of the lanes of an item of that many rows.
+inline int scored_reps(const ScoredGeometry &g, int rows)
+{
+    const int span = rows > 64 ? 128 : rows > 32 ? 64 : 32;
+    return rows > 128 || g.rpad < span ? 1 : g.rpad / span;
+}
+
+// Tiles of an item at most. An MMA's sums are cut off at their 24th bit, so that a lane's accumulator
+// loses up to 2^-24 of itself at every addition of a term of 16 positions (measured, 1024
+// additions: 6e-5 of values of one sign, 2e-5 of N(0, 1) ones). 16-bit outputs do not see that;
+// f32 ones start a partial after at most 128 additions, which the combine adds in f32.
+inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int rows, bool f32_out)
+{
+    if (!f32_out) return 1 << 24;
+    const int T = scored_tile(D, p_terms);
+    const int per = T / 16 * p_terms / scored_reps(g, rows); // additions to a lane by a unit
+    const int units = 128 / (per > 1 ? per : 1);
+    return rows > 128 || scored_groups(D) == 1 ? units : 2 * units;
 }
 
 struct ScoredParams {
@@ -96,6 +124,7 @@ struct ScoredWork {
     int shared_rows;        // its rows
     int own_rows;
     int tile, q_terms, p_terms, head_dim;
+    int shared_max, own_max; // tiles of an item at most
     int slots;              // CTAs
     int force_splits;
 };
