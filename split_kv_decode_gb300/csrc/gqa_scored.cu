@@ -20,6 +20,12 @@
 // MMAs into one accumulator. P takes the place of its scores in TMEM: 16 scores (16 columns) become
 // two terms of 8 columns.
 //
+// Few rows leave most of the 128 lanes free. Up to 64 rows have copies at lanes 32 or 64 apart (Q
+// rows stored several times), whose warps each take a share of a tile's columns; their other weights
+// are zero. Up to 16 rows (8 with three terms) are also packed: the terms of q and of the
+// weights lie in different lanes of a warp instead of different MMAs, a score is the sum over
+// those lanes (one or two shuffles), and the epilogue adds their results.
+//
 // What bounds it: memory. A tile of K and V takes 2800 cycles at an SM's share of the rate, its
 // MMAs 1500 (one term of q) and the softmax of a warpgroup about as much, with two
 // warpgroups taking tiles (or, for 256 rows, row tiles) in turn; 256 columns leave TMEM for
@@ -93,6 +99,7 @@ struct Item {
     int end;                // positions from here on are not there
     int start, keep1;       // visible to every row: [start, keep1)
     int S, q0;              // the sequence's length, and its first token's position
+    int parts;              // lanes of a row that hold a term each (1: terms are MMAs)
 };
 
 __device__ __forceinline__ int length_of(const ScoredParams &p, int b)
@@ -101,8 +108,16 @@ __device__ __forceinline__ int length_of(const ScoredParams &p, int b)
     return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
 }
 
+// Lanes of a row's terms in a warp: 2 for up to 16 rows of two terms, 4 for up to 8 of three.
+template <int TP> __device__ __forceinline__ int parts_of(int rows)
+{
+    constexpr int most = TP == 2 ? 2 : 4;
+    return rows <= 32 / most ? most : 1;
+}
+
 // The idx-th item.
-template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
+template <int T, int TP>
+__device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
 {
     const int per_seq = p.q_len * (p.hq / p.hkv);
     if (idx < p.shared_items) {
@@ -113,6 +128,7 @@ template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p,
         it.kvh = u - it.split * p.hkv;
         it.rows = min(p.batch * per_seq - it.row0, p.tile_rows);
         it.nrt = it.rows > 128 ? 2 : 1;
+        it.parts = parts_of<TP>(it.rows);
         it.v0 = it.split * p.shared_chunk;
         it.tiles = min(p.shared_tiles - it.v0, p.shared_chunk);
         it.n1 = it.a0 = it.w0 = 0;
@@ -126,6 +142,7 @@ template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p,
     it.row0 = (t - u * p.row_groups) * p.tile_rows;
     it.rows = min(per_seq - it.row0, p.tile_rows);
     it.nrt = 1;
+    it.parts = parts_of<TP>(it.rows);
     t = u / p.hkv;
     it.kvh = u - t * p.hkv;
     int lo = 0, hi = p.batch - 1;
@@ -168,14 +185,15 @@ template <int T> __device__ __forceinline__ int tile_at(const Item &it, int i)
 }
 
 // The items of a CTA: calls f(item) for each, until f returns false.
-template <int T, typename F> __device__ __forceinline__ void each_item(const ScoredParams &p, F &&f)
+template <int T, int TP, typename F>
+__device__ __forceinline__ void each_item(const ScoredParams &p, F &&f)
 {
     const int g = gridDim.x;
     for (int r = 0, first = 0; first < p.n_items; ++r, first += g) {
         const int idx = first + (r & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
         if (idx >= p.n_items) continue;
         Item it;
-        get_item<T>(p, idx, it);
+        get_item<T, TP>(p, idx, it);
         if (!f(it)) return;
     }
 }
@@ -365,7 +383,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int win_lo = 0;
         int32_t win_entry = 0;
         bool ok = true;
-        each_item<T>(p, [&](const Item &it) {
+        each_item<T, TP>(p, [&](const Item &it) {
             const int32_t *tab = nullptr;
             int width = 0;
             if (paged) {
@@ -433,7 +451,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (lane == 0) {
             constexpr uint32_t idesc_qk = idesc_f16kind(128, T, 0, 0, C::BF);
             constexpr uint32_t idesc_pv = idesc_f16kind(128, D, 0, 1, C::BF);
-            int n = 0;             // copies consumed: K of tile i at n + 2 i, V behind it
             int items = 0;
             uint32_t pph = 0;      // phases of PFULL, by slot
             bool ok = true;
@@ -441,43 +458,56 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
                 return ok;
             };
-            each_item<T>(p, [&](const Item &it) {
+            // ring positions of the next K and the next V tile (K and V take turns)
+            struct Place {
+                int st;
+                uint32_t ph;
+            } kp = {0, 0u}, vp = {1, 0u};
+            auto advance = [&](Place &x) {
+                x.st += 2;
+                if (x.st >= nst) {
+                    x.st -= nst;
+                    x.ph ^= 1u;
+                }
+            };
+            const uint32_t ring = sb + p.q_bytes;
+            each_item<T, TP>(p, [&](const Item &it) {
                 if (it.tiles == 0) return true;
                 const int nu = it.tiles * it.nrt, sh = it.nrt - 1;
+                const bool packed = it.parts > 1;
+                const int q_terms = packed ? 1 : p.q_terms, p_terms = packed ? 1 : TP;
                 if (!wait(SB_QFULL, (uint32_t)items & 1u)) return false;
                 for (int v = 0; v < nu + 2; ++v) {
                     if (v >= 2) { // O += P V of unit v - 2
-                        const int u = v - 2, tile = u >> sh, f = n + 2 * tile + 1, st = f % nst;
-                        const int s = u & 1, w = NWG == 2 ? s : 0;
+                        const int u = v - 2, s = u & 1, w = NWG == 2 ? s : 0;
                         if (u == 0 && !wait(SB_OFREE, (uint32_t)items & 1u)) return false;
                         if (!wait(SB_PFULL + s, (pph >> s) & 1u)) return false;
                         pph ^= 1u << s;
-                        if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
+                        if ((sh == 0 || !(u & 1)) && !wait(SB_FULL + vp.st, vp.ph)) return false;
                         tc_fence_after();
-                        const uint64_t vd =
-                            smem_desc_sw128(sb + p.q_bytes + st * C::SLOT, CHUNK, 1024);
+                        const uint64_t vd = smem_desc_sw128(ring + vp.st * C::SLOT, CHUNK, 1024);
                         const uint32_t a = tmem + C::S_COL + s * 128;
-#pragma unroll
-                        for (int x = 0; x < TP; ++x)
+                        for (int x = 0; x < p_terms; ++x)
 #pragma unroll
                             for (int k = 0; k < T / 16; ++k)
-                                tc_mma_ts(tmem + w * D,
-                                          a + (x < 2 ? 16 * k + 8 * x : T + 8 * k),
+                                tc_mma_ts(tmem + w * D, a + (x < 2 ? 16 * k + 8 * x : T + 8 * k),
                                           vd + (uint64_t)((k * 2048) >> 4), idesc_pv);
-                        if (sh == 0 || (u & 1)) tc_commit(bar + SB_EMPTY + st);
+                        if (sh == 0 || (u & 1)) {
+                            tc_commit(bar + SB_EMPTY + vp.st);
+                            advance(vp);
+                        }
                         tc_commit(bar + SB_PVDONE + w);
                     }
                     if (v < nu) { // S of unit v
-                        const int tile = v >> sh, f = n + 2 * tile, st = f % nst, s = v & 1;
-                        if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
+                        const int s = v & 1;
+                        if ((sh == 0 || !(v & 1)) && !wait(SB_FULL + kp.st, kp.ph)) return false;
                         tc_fence_after();
-                        const uint32_t q0 =
-                            sb + (sh ? (v & 1) * p.q_terms * NCH * qch : 0);
-                        const uint64_t qd = smem_desc_sw128(q0, 16, 1024);
-                        const uint64_t kd = smem_desc_sw128(sb + p.q_bytes + st * C::SLOT, 16, 1024);
+                        const uint64_t qd = smem_desc_sw128(
+                            sb + (sh ? (v & 1) * p.q_terms * NCH * qch : 0), 16, 1024);
+                        const uint64_t kd = smem_desc_sw128(ring + kp.st * C::SLOT, 16, 1024);
                         // the small terms first: an MMA's sums are cut off at their 24th bit, so
                         // that each addition to a large sum costs about 2^-24 of it
-                        for (int x = p.q_terms - 1; x >= 0; --x)
+                        for (int x = q_terms - 1; x >= 0; --x)
 #pragma unroll
                             for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -486,14 +516,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                         tmem + C::S_COL + s * 128,
                                         qd + (uint64_t)(((x * NCH + c) * qch + k * 32) >> 4),
                                         kd + (uint64_t)((c * CHUNK + k * 32) >> 4), idesc_qk,
-                                        x != p.q_terms - 1 || (c | k) != 0 ? 1u : 0u);
+                                        x != q_terms - 1 || (c | k) != 0 ? 1u : 0u);
                         tc_commit(bar + SB_SFULL + s);
-                        if (sh == 0 || (v & 1)) tc_commit(bar + SB_EMPTY + st);
+                        if (sh == 0 || (v & 1)) {
+                            tc_commit(bar + SB_EMPTY + kp.st);
+                            advance(kp);
+                        }
                         if (v == nu - 1) tc_commit(bar + SB_QFREE);
                     }
                 }
                 tc_commit(bar + SB_OREADY);
-                n += 2 * it.tiles;
                 ++items;
                 return true;
             });
@@ -541,17 +573,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_fence_before();
         arrive(SB_OFREE);
 
-        each_item<T>(p, [&](const Item &it) {
-            // ---- this thread's row and its share of every tile's columns
-            const int nrt = it.nrt;
-            // few rows: Q has copies at lanes span, 2 span, ..., whose warps each take a share of the
-            // columns; the other weights of such a lane are zero
+        each_item<T, TP>(p, [&](const Item &it) {
+            // ---- this thread's row and its share of every tile's columns (see above)
+            const int nrt = it.nrt, parts = it.parts;
             const int span = nrt == 2 || it.rows > 64 ? 128 : it.rows > 32 ? 64 : 32;
-            const int reps = nrt == 2 ? 1 : max(1, p.rpad / span);
+            const int reps = nrt == 2 ? 1 : max(1, p.rpad / span), copies = reps * parts;
             const int rep = (warp & 3) * 32 / span;
+            const int part = parts == 1 ? 0 : lane / (32 / parts);
             const bool in_use = rep < reps;                    // (of this warp)
             const int cols = T / reps, cb = in_use ? rep * cols : 0;
-            const int local = nrt == 2 ? w * 128 + r : r - rep * span; // row of the item
+            const int local = nrt == 2     ? w * 128 + r       // row of the item
+                              : parts == 1 ? r - rep * span
+                                           : lane & (32 / parts - 1);
             const bool owner = in_use && local < it.rows;
             const bool busy = in_use && (local & ~31) < it.rows;
             const int per_seq = p.q_len * Gh;
@@ -583,7 +616,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 else store4(static_cast<__nv_bfloat16 *>(p.out) + at, f);
             };
             if (it.tiles == 0) { // nothing to see: a neutral partial
-                if (owner && rep == 0 && (nrt == 2 || w == 0)) {
+                if (owner && rep == 0 && part == 0 && (nrt == 2 || w == 0)) {
                     if (p.whole)
                         for (int c = 0; c < D; c += 4)
                             write4(dst_row, c, make_float4(0.f, 0.f, 0.f, 0.f));
@@ -596,75 +629,112 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // ---- Q, once the last item's scores are done with it
             if (items > 0 && !wait(SB_QFREE, (uint32_t)(items - 1) & 1u)) return false;
             {
-                constexpr int U8 = D / 8; // 8-column units of a row: a half-warp's or a warp's
-                // (rows past them give scores that nobody reads)
+                // 8-column units, a half-warp's or a warp's to a row; four of a thread in flight
+                // (rows past the last eight give scores that nobody reads)
+                constexpr int U8 = D / 8, STEP = C::WARPS * 32;
                 const int units = (it.rows + 7) / 8 * 8 * U8;
-                for (int u = threadIdx.x; u < units; u += C::WARPS * 32) {
-                    const int rr = u / U8, j = u - rr * U8;
-                    const bool real = rr < it.rows;
-                    int qrow = it.row0 + (real ? rr : 0), qb = it.b;
+                const int j = threadIdx.x % U8; // (the step is a multiple of a row)
+                auto source = [&](int rr) { // element of q, or -1
+                    if (rr >= it.rows) return (int64_t)-1;
+                    int qrow = it.row0 + rr, qb = it.b;
                     if (it.shared) {
                         qb = qrow / per_seq;
                         qrow -= qb * per_seq;
                     }
                     const int qt = qrow / Gh, qh = it.kvh * Gh + qrow - qt * Gh;
-                    const size_t at = (((size_t)qb * p.q_len + qt) * p.hq + qh) * D + j * 8;
-                    const uint32_t dst =
-                        sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch;
-                    auto put = [&](int x, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    return (((int64_t)qb * p.q_len + qt) * p.hq + qh) * D + j * 8;
+                };
+                // unit j of row rr: term x, at all copies of the row
+                auto put = [&](int rr, int x, const uint32_t *v) {
+                    const uint32_t dst = sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch;
+                    if (parts == 1) {
                         for (int k = 0; k < reps; ++k)
-                            sts_v4(dst + x * NCH * qch + swz((rr & 127) + k * span, (j & 7) * 16), a0,
-                                   a1, a2, a3);
-                    };
-                    if (!p.q_f32) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (real) x = __ldg(reinterpret_cast<const uint4 *>(
-                                      static_cast<const uint16_t *>(p.q) + at));
-                        put(0, x.x, x.y, x.z, x.w);
-                        continue;
+                            sts_v4(dst + x * NCH * qch + swz((rr & 127) + k * span, (j & 7) * 16), v[0],
+                                   v[1], v[2], v[3]);
+                    } else {
+                        for (int k = 0; k < reps; ++k)
+                            sts_v4(dst + swz(k * 32 + x * (32 / parts) + rr, (j & 7) * 16), v[0], v[1],
+                                   v[2], v[3]);
                     }
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = 0.f;
-                    if (real) {
-                        const float4 *src = reinterpret_cast<const float4 *>(
-                            static_cast<const float *>(p.q) + at);
-                        const float4 x = __ldg(src), y = __ldg(src + 1);
-                        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-                        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-                    }
-                    if (!C::BF) {
-                        // f16: the row scaled to a largest element in [1, 2), so that two terms
-                        // keep 22 bits of it (every unit of a row is in this loop's same turn)
-                        float a = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
-                        for (int o = U8 / 2; o > 0; o >>= 1)
-                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                        // 2^-e from the exponent of a (its bits; subnormals and infinities: 1)
-                        const int e = (int)(__float_as_uint(a) >> 23);
-                        const bool plain = e < 1 || e > 253;
-                        const float down = plain ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
-                        if (j == 0)
-                            ms->row_scale[rr] = plain ? 1.f : __uint_as_float((uint32_t)e << 23);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] *= down;
-                    }
-                    for (int x = 0; x < p.q_terms; ++x) {
-                        uint32_t v[4];
+                };
+                const uint32_t none[4] = {0u, 0u, 0u, 0u};
+                if (!p.q_f32) {
+                    for (int u0 = threadIdx.x; u0 < units; u0 += 4 * STEP) {
+                        uint4 x[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            v[i] = Pair<DT>::pack(f[2 * i], f[2 * i + 1]);
-                            const float2 y = Pair<DT>::unpack(v[i]);
-                            f[2 * i] -= y.x;
-                            f[2 * i + 1] -= y.y;
+                            const int u = u0 + i * STEP;
+                            const int64_t at = u < units ? source(u / U8) : -1;
+                            x[i] = make_uint4(0, 0, 0, 0);
+                            if (at >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                             static_cast<const uint16_t *>(p.q) + at));
                         }
-                        put(x, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int u = u0 + i * STEP;
+                            if (u >= units) break;
+                            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                            for (int k = 0; k < parts; ++k) put(u / U8, k, v); // (every lane's score)
+                        }
+                    }
+                } else {
+                    for (int u0 = threadIdx.x; u0 < units; u0 += 4 * STEP) {
+                        float4 xa[4], xb[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int u = u0 + i * STEP;
+                            const int64_t at = u < units ? source(u / U8) : -1;
+                            xa[i] = xb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (at >= 0) {
+                                const float4 *src = reinterpret_cast<const float4 *>(
+                                    static_cast<const float *>(p.q) + at);
+                                xa[i] = __ldg(src);
+                                xb[i] = __ldg(src + 1);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int u = u0 + i * STEP;
+                            if (u >= units) break; // (whole warps: units is a multiple of 128)
+                            float f[8] = {xa[i].x, xa[i].y, xa[i].z, xa[i].w,
+                                          xb[i].x, xb[i].y, xb[i].z, xb[i].w};
+                            if (!C::BF) {
+                                // f16: the row scaled to a largest element in [1, 2), so that two
+                                // terms keep 22 bits of it
+                                float a = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
+                                for (int o = U8 / 2; o > 0; o >>= 1)
+                                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                                // 2^-e from the exponent of a (its bits; subnormals, infinities: 1)
+                                const int e = (int)(__float_as_uint(a) >> 23);
+                                const bool plain = e < 1 || e > 253;
+                                const float down =
+                                    plain ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
+                                if (j == 0)
+                                    ms->row_scale[u / U8] =
+                                        plain ? 1.f : __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) f[k] *= down;
+                            }
+                            for (int x = 0; x < p.q_terms; ++x) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    v[k] = Pair<DT>::pack(f[2 * k], f[2 * k + 1]);
+                                    const float2 y = Pair<DT>::unpack(v[k]);
+                                    f[2 * k] -= y.x;
+                                    f[2 * k + 1] -= y.y;
+                                }
+                                put(u / U8, x, v);
+                            }
+                            if (parts > p.q_terms) put(u / U8, 3, none); // (of four lanes, three terms)
+                        }
                     }
                 }
             }
             fence_proxy_async_smem();
-            if (TP == 3 && reps > 1 && busy) {
+            if (TP == 3 && parts == 1 && reps > 1 && busy) {
                 // the third terms have columns of their own: zero but for this warp's share
                 const uint32_t z[16] = {};
                 for (int s = NWG == 2 ? w : 0; s < 2; s += NWG)
@@ -721,79 +791,65 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         x1 = min(x_hi - t0, T);
                     }
                 }
-                const bool modified = transform || !full;
-                // 16 scores from column c on: y, -infinity where the row sees nothing
-                auto score16 = [&](float *x, int c) {
-                    if (p.softcap == 0.f) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] *= sc.mult;
-                    } else if (precise) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = capped<true>(x[i] * sc.turn, sc.cap);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = capped<false>(x[i] * sc.turn, sc.cap);
-                    }
-                    if (p.slopes) {
-                        const float d = (float)(pos - t0 - c);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            x[i] = fmaf(-sc.slope, fabsf(d - (float)i), x[i]);
-                    }
-                    if (!full) {
-                        const uint32_t see = range16(x0 - c, x1 - c) | range16(k0 - c, k1 - c);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!((see >> i) & 1u)) x[i] = -INFINITY;
-                    }
-                };
-                auto max16 = [&](const float *x) {
-                    float a = x[0], b2 = x[1];
-#pragma unroll
-                    for (int i = 2; i < 16; i += 2) {
-                        a = fmaxf(a, x[i]);
-                        b2 = fmaxf(b2, x[i + 1]);
-                    }
-                    return fmaxf(a, b2);
-                };
+                const bool adds = parts > 1 && p.q_f32; // a score is the sum over a row's lanes
+                // what the scores become takes their place (one granule that needs no other pass
+                // stays in registers)
+                const bool modified = adds || transform || !full;
                 float tm = -INFINITY;
-                // up to 32 columns stay in registers until they are weights; more go back to TMEM
-                float xr[32];
-                const bool held = cols <= 32;
+                float x[16];
                 if (busy) {
-                    if (held) {
-                        tmem_ld16(ts + cb, xr);
-                        if (cols == 32) tmem_ld16(ts + cb + 16, xr + 16);
-                        tmem_wait_ld();
-                        if (modified) {
-                            score16(xr, cb);
-                            if (cols == 32) score16(xr + 16, cb + 16);
-                            if (!full && p.q_len > 1) { // (for the rows that are no numbers below)
-                                tmem_st16(ts + cb, xr);
-                                if (cols == 32) tmem_st16(ts + cb + 16, xr + 16);
-                                tmem_wait_st();
-                            }
-                        }
-                        tm = max16(xr);
-                        if (cols == 32) tm = fmaxf(tm, max16(xr + 16));
-                    } else {
 #pragma unroll 1
-                        for (int c = cb; c < cb + cols; c += 32) {
-                            tmem_ld32(ts + c, xr);
-                            tmem_wait_ld();
-                            if (modified) {
-                                score16(xr, c);
-                                tmem_st16(ts + c, xr);
-                                score16(xr + 16, c + 16);
-                                tmem_st16(ts + c + 16, xr + 16);
+                    for (int c = cb; c < cb + cols; c += 16) {
+                        tmem_ld16(ts + c, x);
+                        tmem_wait_ld();
+                        if (adds) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+                                if (TP == 3) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 8);
                             }
-                            tm = fmaxf(tm, fmaxf(max16(xr), max16(xr + 16)));
                         }
-                        if (modified) tmem_wait_st();
+                        if (transform || !full) {
+                            // y, -infinity where the row sees nothing
+                            if (p.softcap == 0.f) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) x[i] *= sc.mult;
+                            } else if (precise) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    x[i] = capped<true>(x[i] * sc.turn, sc.cap);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    x[i] = capped<false>(x[i] * sc.turn, sc.cap);
+                            }
+                            if (p.slopes) {
+                                const float d = (float)(pos - t0 - c);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    x[i] = fmaf(-sc.slope, fabsf(d - (float)i), x[i]);
+                            }
+                            if (!full) {
+                                const uint32_t see =
+                                    range16(x0 - c, x1 - c) | range16(k0 - c, k1 - c);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (!((see >> i) & 1u)) x[i] = -INFINITY;
+                            }
+                        }
+                        if (modified) tmem_st16(ts + c, x);
+                        float a = x[0], b2 = x[1];
+#pragma unroll
+                        for (int i = 2; i < 16; i += 2) {
+                            a = fmaxf(a, x[i]);
+                            b2 = fmaxf(b2, x[i + 1]);
+                        }
+                        tm = fmaxf(tm, fmaxf(a, b2));
                     }
-                    if (!modified) tm *= sc.mult;
+                    if (modified) tmem_wait_st();
+                    if (!transform && full) tm *= sc.mult;
                 }
-                const float mult = modified ? 1.f : sc.mult;
+                const float mult = transform || !full ? 1.f : sc.mult;
                 // ---- the reference moves where a weight would pass 2^LIM
                 const bool moves = owner && tm > m + C::LIM;
                 if (__any_sync(0xffffffffu, moves)) {
@@ -868,7 +924,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             for (int c = 0; c < T; ++c) {
                                 if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
                                 const float y = tmem_ld1(ts + c);
-                                const bool sees = !dead && c >= cb && c < cb + cols &&
+                                const bool sees = !dead && part == 0 && c >= cb && c < cb + cols &&
                                                   ((c >= x0 && c < x1) || (c >= k0 && c < k1));
                                 const float pr = ex2(y - ref);
 #pragma unroll 1
@@ -906,8 +962,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // ---- P: the weights, in terms, in the place of their scores
                 if (busy) {
                     float l4[4] = {};
-                    auto weigh16 = [&](const float *x, int c) {
-                        uint32_t t16[16], third[8];
+                    const bool one = cols == 16; // (still in registers)
+#pragma unroll 1
+                    for (int c = cb; c < cb + cols; c += 16) {
+                        if (!one) {
+                            tmem_ld16(ts + c, x);
+                            tmem_wait_ld();
+                        }
+                        uint32_t t16[16];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const float a = ex2(fmaf(x[i], mult, -ref));
@@ -916,36 +978,34 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             l4[(i + 1) & 3] += b2;
                             t16[i / 2] = Pair<DT>::pack(a, b2);
                             const float2 y = Pair<DT>::unpack(t16[i / 2]);
-                            t16[8 + i / 2] = Pair<DT>::pack(a - y.x, b2 - y.y);
-                            if (TP == 3) {
-                                const float2 z = Pair<DT>::unpack(t16[8 + i / 2]);
-                                third[i / 2] = Pair<DT>::pack(a - y.x - z.x, b2 - y.y - z.y);
-                            }
+                            x[i] = a - y.x;
+                            x[i + 1] = b2 - y.y;
+                            t16[8 + i / 2] = Pair<DT>::pack(x[i], x[i + 1]);
                         }
-                        tmem_st16w(ts + c, t16);
-                        if (TP == 3) tmem_st8w(ts + T + c / 2, third);
-                    };
-                    if (held) {
-                        weigh16(xr, cb);
-                        if (cols == 32) weigh16(xr + 16, cb + 16);
+                        if (TP == 3) {
+                            uint32_t third[8];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 z = Pair<DT>::unpack(t16[8 + i / 2]);
+                                third[i / 2] = Pair<DT>::pack(x[i] - z.x, x[i + 1] - z.y);
+                                if (part >= 2) t16[i / 2] = part == 2 ? third[i / 2] : 0u;
+                            }
+                            if (parts == 1) tmem_st8w(ts + T + c / 2, third);
+                        }
+                        if (parts == 1) {
+                            tmem_st16w(ts + c, t16);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (part == 1) t16[i] = t16[8 + i];
+                            tmem_st8w(ts + c, t16);
+                        }
+                    }
+                    if (reps > 1) {
                         const uint32_t z[16] = {};
 #pragma unroll 1
                         for (int c = 0; c < T; c += 16)
                             if (c < cb || c >= cb + cols) tmem_st16w(ts + c, z);
-                    } else {
-#pragma unroll 1
-                        for (int c = cb; c < cb + cols; c += 32) {
-                            tmem_ld32(ts + c, xr);
-                            tmem_wait_ld();
-                            weigh16(xr, c);
-                            weigh16(xr + 16, c + 16);
-                        }
-                        if (reps > 1) {
-                            const uint32_t z[16] = {};
-#pragma unroll 1
-                            for (int c = 0; c < T; c += 16)
-                                if (c < cb || c >= cb + cols) tmem_st16w(ts + c, z);
-                        }
                     }
                     l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tmem_wait_st();
@@ -963,7 +1023,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const bool joint = NWG == 2 && nrt == 1;
             const int c0 = joint ? w * (D / 2) : 0, nc = joint ? D / 2 : D; // this thread's columns
             float f_own = 1.f, f_other = 0.f;
-            if (joint || reps > 1) {
+            if (joint || copies > 1) {
                 ms->state[w][r] = make_float2(m, l);
                 if (!all_sync()) return false;
                 // (a sum that is no number takes part: only an empty state does not)
@@ -988,7 +1048,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (dead) l = 0.f;
             const bool odd = !(l - l == 0.f); // no number, or infinite
             const float factor = l == 0.f ? 0.f : odd ? NAN : p.whole ? 1.f / l : 1.f;
-            const bool writes = owner && rep == 0;
+            const bool writes = owner && rep == 0 && part == 0;
             if (writes && !p.whole && (!joint || w == 0))
                 p.ml[dst_row] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
                                 : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
@@ -1007,7 +1067,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int i = 0; i < 16; ++i) o[i] *= f_own;
                 }
             };
-            if (reps == 1) {
+            if (copies == 1) {
 #pragma unroll 1
                 for (int c = c0; c < c0 + nc; c += 16) {
                     float o[16];
@@ -1021,54 +1081,54 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
             } else {
-                // the copies' sums meet in the place of Q, whose MMAs are done: [copy][row][columns
-                // of a pass], in one pass or two
+                // the copies' sums meet in the place of Q, whose MMAs are done: [warpgroup][copy]
+                // [row][W columns], as many columns at once as there is room for; 16-byte units
+                // swizzled so that lanes hit other banks
                 const int rows8 = (it.rows + 7) / 8 * 8;
-                const int passes = reps * rows8 * D * 4 <= p.q_bytes ? 1 : 2, width = nc / passes;
-                const int stride = D / passes; // columns of a row: of all warpgroups
+                int W = nc;
+                while ((joint ? 2 : 1) * copies * rows8 * W * 4 > p.q_bytes) W >>= 1;
+                const int w4 = W / 4;
                 if (writes && w == 0) {
                     ms->row.factor[local] = factor;
                     ms->row.to[local] = (uint32_t)dst_row;
                 }
-                float *xs = reinterpret_cast<float *>(sm);
-                for (int ps = 0; ps < passes; ++ps) {
+                float4 *xs = reinterpret_cast<float4 *>(sm) + (joint ? w * copies * rows8 * w4 : 0);
+                for (int at = 0; at < nc; at += W) {
                     if (busy) {
-                        float *to_row = xs + (rep * rows8 + local) * stride + (joint ? w * width : 0);
+                        float4 *to_row = xs + ((rep * parts + part) * rows8 + local) * w4;
 #pragma unroll 1
-                        for (int c = 0; c < width; c += 16) {
+                        for (int c = 0; c < W; c += 16) {
                             float o[16];
-                            lane16(c0 + ps * width + c, o);
+                            lane16(c0 + at + c, o);
                             if (owner) {
 #pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    *reinterpret_cast<float4 *>(to_row + c + i) =
-                                        make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                for (int i = 0; i < 4; ++i)
+                                    to_row[(c / 4 + i) ^ (local & 3)] = make_float4(
+                                        o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                             }
                         }
                     }
-                    if (!all_sync()) return false;
-                    const int units = it.rows * stride / 4;
-                    for (int u = threadIdx.x; u < units; u += C::WARPS * 32) {
-                        const int rr = u / (stride / 4), c = (u - rr * (stride / 4)) * 4;
+                    if (!(at == 0 ? all_sync() : group_sync())) return false;
+                    // w4 threads to a row
+                    const int lw = 31 - __clz(w4), c = r & (w4 - 1);
+                    for (int rr = r >> lw; rr < it.rows; rr += 128 >> lw) {
                         const float fac = ms->row.factor[rr];
                         if (fac == 0.f && !p.whole) continue;
                         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int k = 0; k < reps; ++k) {
-                            const float4 x = *reinterpret_cast<const float4 *>(
-                                xs + (k * rows8 + rr) * stride + c);
-                            sum.x += x.x;
-                            sum.y += x.y;
-                            sum.z += x.z;
-                            sum.w += x.w;
+                        for (int k = 0; k < copies; ++k) {
+                            const float4 y = xs[(k * rows8 + rr) * w4 + (c ^ (rr & 3))];
+                            sum.x += y.x;
+                            sum.y += y.y;
+                            sum.z += y.z;
+                            sum.w += y.w;
                         }
                         sum = fac == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                                          : make_float4(sum.x * fac, sum.y * fac, sum.z * fac, sum.w * fac);
-                        // column c of the pass: of the warpgroup whose half it is in
-                        const int g = c / width;
-                        write4((size_t)ms->row.to[rr], g * nc + ps * width + c - g * width, sum);
+                        write4((size_t)ms->row.to[rr], c0 + at + 4 * c, sum);
                     }
-                    if (!all_sync()) return false; // the place may be written again
+                    if (at + W < nc && !group_sync()) return false;
                 }
+                if (!all_sync()) return false; // the place may be written again
             }
             // the next item starts from zero
             zero_o(to + c0, nc);

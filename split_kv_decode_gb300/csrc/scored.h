@@ -36,21 +36,25 @@ struct ScoredGeometry {
     int smem;
 };
 
+// Rows up to which an item's terms lie in the lanes of one warp.
+constexpr int scored_packed(int p_terms) { return p_terms == 2 ? 16 : 8; }
+
 // own_rows: a sequence's query rows of a KV head; shared_rows: those of the batch, or 0
 inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_rows,
                                       int64_t shared_rows)
 {
     ScoredGeometry g;
-    g.q_terms = q_terms;
     const int slot = scored_tile(D, p_terms) * D * 2;
     const int64_t most = shared_rows > own_rows ? shared_rows : own_rows;
+    g.q_terms = q_terms;
+    const int held = most <= scored_packed(p_terms) ? 1 : q_terms; // of the widest item
     // (two row tiles only for a q of one term: with more terms the ring would be too short)
     for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
         const int rows = (int)(most < g.tile_rows ? most : g.tile_rows);
         // 128 lanes, with copies of few rows, where that leaves a ring of two tiles; a ring
         // shorter than a tile and a half takes smaller items
         for (g.rpad = 128;; g.rpad /= 2) {
-            g.q_bytes = (rows > 128 ? 2 : 1) * q_terms * g.rpad * D * 2;
+            g.q_bytes = (rows > 128 ? 2 : 1) * held * g.rpad * D * 2;
             g.slots = (kScoredSmemMax - 1024 - scored_misc(D) - g.q_bytes) / slot;
             if (g.slots >= 4 || g.rpad / 2 < rows || g.rpad == 32) break;
         }
@@ -62,23 +66,19 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
     return g;
 }
 
-// Copies of the lanes of an item of that many rows.
-inline int scored_reps(const ScoredGeometry &g, int rows)
-{
-    const int span = rows > 64 ? 128 : rows > 32 ? 64 : 32;
-    return rows > 128 || g.rpad < span ? 1 : g.rpad / span;
-}
-
 // Tiles of an item at most. An MMA's sums are cut off at their 24th bit, so that a lane's accumulator
 // loses up to 2^-24 of itself at every addition of a term of 16 positions (measured, 1024
 // additions: 6e-5 of values of one sign, 2e-5 of N(0, 1) ones). 16-bit outputs do not see that;
-// f32 ones start a partial after at most 128 additions, which the combine adds in f32.
+// f32 ones start a partial after at most 48 additions, which the combine adds in f32.
 inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int rows, bool f32_out)
 {
     if (!f32_out) return 1 << 24;
     const int T = scored_tile(D, p_terms);
-    const int per = T / 16 * p_terms / scored_reps(g, rows); // additions to a lane by a unit
-    const int units = 128 / (per > 1 ? per : 1);
+    const int span = rows > 64 ? 128 : rows > 32 ? 64 : 32;
+    const int reps = rows > 128 || g.rpad < span ? 1 : g.rpad / span;
+    // additions of a unit to a lane (packed: a term has a lane of its own)
+    const int per = T / 16 / reps * (rows <= scored_packed(p_terms) ? 1 : p_terms);
+    const int units = 48 / (per > 1 ? per : 1);
     return rows > 128 || scored_groups(D) == 1 ? units : 2 * units;
 }
 
