@@ -22,22 +22,27 @@
 //
 // Few rows leave most of the 128 lanes free. Up to 64 rows have copies at lanes 32 or 64 apart (Q
 // rows stored several times), whose warps each take a share of a tile's columns; their other weights
-// are zero. Up to 16 rows (8 with three terms) are also packed: the terms of q and of the
-// weights lie in different lanes of a warp instead of different MMAs, a score is the sum over
-// those lanes (one or two shuffles), and the epilogue adds their results.
+// are zero. Half of the copies take the second term of the weights, so that O += P V is one set of
+// MMAs. Up to 16 rows (8 with three terms) are packed instead: the terms of q and of the weights
+// lie in different lanes of a warp, and a score is the sum over those lanes (one or two
+// shuffles). The epilogue adds the copies' results.
 //
-// What bounds it: memory. A tile of K and V takes 2800 cycles at an SM's share of the rate, its
-// MMAs 1500 (one term of q) and the softmax of a warpgroup about as much, with two
-// warpgroups taking tiles (or, for 256 rows, row tiles) in turn; 256 columns leave TMEM for
-// one. Many rows on shared positions are bound by the MMAs.
+// 256 columns: one term of Q lies in TMEM (128 columns), beside O (256) and two S slots of 64: the
+// MMAs of S then read half as much shared memory, and the ring has room for three tiles.
+//
+// What bounds it: memory. A tile of K and V (64 KB) takes 1.43 us at an SM's share of the rate; its MMAs
+// take 1.0 to 1.3, and the softmax of a warpgroup about 1, with two warpgroups taking tiles (or, for
+// 256 rows, row tiles) in turn; 256 columns leave TMEM for one. Many rows on shared
+// positions are bound by the MMAs.
 //
 // Roles: one or two softmax warpgroups, a TMA producer warp, a warp whose first lane issues the
-// MMAs. Unit u of an item is tile u, or tile u / 2 and row tile u % 2; it has S slot u % 2 and, with
-// two warpgroups, warpgroup and accumulator u % 2. The MMA order S0 S1 O0 S2 O1 S3 ... lets each
-// unit's softmax run beside the other's MMAs, and makes P of unit u - 2 read before S of unit
-// u takes its place. Warpgroups that took tiles in turn have two states a row, which the
-// epilogue joins. Every wait is bounded: one that runs out sets the status word, and all roles
-// leave.
+// MMAs. The producer also works the items out and passes them on through a queue. Unit u of an
+// item is tile u, or tile u / 2 and row tile u % 2; it has S slot u % 2 and, with two warpgroups,
+// warpgroup and accumulator u % 2. The MMA order S0 S1 O0 S2 O1 S3 ... lets each unit's softmax
+// run beside the other's MMAs, and makes P of unit u - 2 read before S of unit u takes its
+// place; K and V tiles come through the ring in that order. Warpgroups that took tiles in turn have
+// two states a row, which the epilogue joins. Every wait is bounded: one that runs out sets the
+// status word, and all roles leave.
 #include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -60,7 +65,10 @@ template <typename DT_, int D_, int TP_> struct Cfg {
     static constexpr int SLOT = NCH * CHUNK;
     static constexpr int WARPS = NWG * 4;   // softmax warps
     static constexpr int THREADS = (WARPS + 2) * 32;
-    static constexpr int S_COL = 256;       // S slot s at S_COL + 128 s; O of warpgroup w at D w
+    static constexpr int G = T / 4;         // columns that a warp takes at a time
+    // TMEM columns: O of warpgroup w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
+    static constexpr bool QTM = scored_q_in_tmem(D, TP);
+    static constexpr int S_COL = 256, S_SLOT = QTM ? 64 : 128, Q_COL = 384;
     // A row's reference moves when a weight passes 2^LIM, and then to 2^-OFF of the largest: an f16
     // term keeps weights down to 2^-(24 + OFF) of it, bf16 has the exponents of f32.
     static constexpr float LIM = BF ? 8.f : 15.f, OFF = BF ? 0.f : 7.f;
@@ -71,10 +79,27 @@ constexpr int SB_FULL = 0, SB_EMPTY = kScoredMaxSlots, SB_SFULL = 2 * kScoredMax
               SB_PFULL = SB_SFULL + 2, SB_PVDONE = SB_PFULL + 2, SB_OREADY = SB_PVDONE + 2,
               SB_OFREE = SB_OREADY + 1, SB_QFULL = SB_OFREE + 1, SB_QFREE = SB_QFULL + 1,
               SB_XCH = SB_QFREE + 1, SB_GROUP = SB_XCH + 1, SB_DRAIN = SB_GROUP + 2,
-              SB_N = SB_DRAIN + 1;
+              SB_ITEM = SB_DRAIN + 1, SB_TAKEN = SB_ITEM + 2, SB_N = SB_TAKEN + 2;
+
+struct Item {
+    int tiles;              // of the visible span; < 0: no more items
+    int b;                  // sequence, or -1: shared positions
+    int kvh, split;
+    int row0, rows;         // of the (sequence's or batch's) rows of the KV head
+    int v0;                 // first tile of the span
+    int n1, a0, w0;         // its tile v: at a0 + v T below n1, else at w0 + (v - n1) T
+    int end;                // positions from here on are not there
+    int start, keep1;       // visible to every row: [start, keep1)
+    int S;                  // the sequence's length
+    int pad[2];
+    __device__ __forceinline__ bool shared() const { return b < 0; }
+    __device__ __forceinline__ int row_tiles() const { return rows > 128 ? 2 : 1; }
+};
+static_assert(sizeof(Item) == 64, "item");
 
 // the part of shared memory behind the ring
-template <int NWG> struct Misc {
+template <int NWG> struct alignas(16) Misc {
+    Item item[2];             // the queue
     uint64_t bar[SB_N];
     uint32_t tmem;
     int abort;
@@ -90,18 +115,6 @@ template <int NWG> struct Misc {
 };
 static_assert(sizeof(Misc<1>) <= scored_misc(256) && sizeof(Misc<2>) <= scored_misc(128), "misc");
 
-struct Item {
-    bool shared;
-    int b, kvh, split;
-    int row0, rows, nrt;    // rows of the (sequence's or batch's) KV head; row tiles
-    int tiles, v0;          // of the visible span
-    int n1, a0, w0;         // its tile v: at a0 + v T below n1, else at w0 + (v - n1) T
-    int end;                // positions from here on are not there
-    int start, keep1;       // visible to every row: [start, keep1)
-    int S, q0;              // the sequence's length, and its first token's position
-    int parts;              // lanes of a row that hold a term each (1: terms are MMAs)
-};
-
 __device__ __forceinline__ int length_of(const ScoredParams &p, int b)
 {
     const int L = p.lens[b];
@@ -115,34 +128,44 @@ template <int TP> __device__ __forceinline__ int parts_of(int rows)
     return rows <= 32 / most ? most : 1;
 }
 
+// Lanes from one copy of a row tile to the next, and copies.
+__device__ __forceinline__ int span_of(int rows)
+{
+    return rows > 64 ? 128 : rows > 32 ? 64 : 32;
+}
+__device__ __forceinline__ int reps_of(const ScoredParams &p, int rows)
+{
+    return rows > 128 ? 1 : max(1, p.rpad / span_of(rows));
+}
+// Copies of a row by the weights' terms: with two terms, half of the copies take the second.
+template <int TP> __device__ __forceinline__ int shares_of_terms(int parts, int reps)
+{
+    return TP == 2 && parts == 1 && reps > 1 ? 2 : 1;
+}
+
 // The idx-th item.
-template <int T, int TP>
-__device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
+template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
 {
     const int per_seq = p.q_len * (p.hq / p.hkv);
+    it.pad[0] = it.pad[1] = 0;
     if (idx < p.shared_items) {
-        it.shared = true;
+        it.b = -1;
         const int u = idx / p.row_tiles;
         it.row0 = (idx - u * p.row_tiles) * p.tile_rows;
         it.split = u / p.hkv;
         it.kvh = u - it.split * p.hkv;
         it.rows = min(p.batch * per_seq - it.row0, p.tile_rows);
-        it.nrt = it.rows > 128 ? 2 : 1;
-        it.parts = parts_of<TP>(it.rows);
         it.v0 = it.split * p.shared_chunk;
         it.tiles = min(p.shared_tiles - it.v0, p.shared_chunk);
         it.n1 = it.a0 = it.w0 = 0;
         it.end = p.shared_len;
-        it.b = 0;
+        it.start = it.keep1 = it.S = 0;
         return;
     }
-    it.shared = false;
     int t = idx - p.shared_items;
     int u = t / p.row_groups;
     it.row0 = (t - u * p.row_groups) * p.tile_rows;
     it.rows = min(per_seq - it.row0, p.tile_rows);
-    it.nrt = 1;
-    it.parts = parts_of<TP>(it.rows);
     t = u / p.hkv;
     it.kvh = u - t * p.hkv;
     int lo = 0, hi = p.batch - 1;
@@ -156,14 +179,13 @@ __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &i
     it.split = t - p.base[lo];
     const int S = length_of(p, b);
     it.S = it.end = S;
-    it.q0 = S - p.q_len;
     it.start = p.starts ? max(0, __ldg(p.starts + b)) : 0;
     int keep = p.keep;
     if (p.keep_lens) keep = max(0, min(__ldg(p.keep_lens + b), keep));
     it.keep1 = min(keep, S);
     // the visible span: what is kept, and from the first token's window on
     int from = it.start;
-    if (p.window) from = max(from, max(it.q0, 0) - p.window + 1);
+    if (p.window) from = max(from, max(S - p.q_len, 0) - p.window + 1);
     it.n1 = 0;
     it.a0 = 0;
     it.w0 = from / T * T;
@@ -182,20 +204,6 @@ template <int T> __device__ __forceinline__ int tile_at(const Item &it, int i)
 {
     const int v = it.v0 + i;
     return v < it.n1 ? it.a0 + v * T : it.w0 + (v - it.n1) * T;
-}
-
-// The items of a CTA: calls f(item) for each, until f returns false.
-template <int T, int TP, typename F>
-__device__ __forceinline__ void each_item(const ScoredParams &p, F &&f)
-{
-    const int g = gridDim.x;
-    for (int r = 0, first = 0; first < p.n_items; ++r, first += g) {
-        const int idx = first + (r & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        if (idx >= p.n_items) continue;
-        Item it;
-        get_item<T, TP>(p, idx, it);
-        if (!f(it)) return;
-    }
 }
 
 // byte offset of (row, byte) in a chunk: 128-byte rows, 128-byte swizzle
@@ -240,11 +248,11 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t a)
 
 // A from TMEM (16-bit, two columns of A a word), B from shared memory
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t idesc)
+                                          uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(bdesc), "r"(idesc)
+                 "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 
@@ -309,12 +317,45 @@ template <bool PRECISE> __device__ __forceinline__ float capped(float z, float c
     return fabsf(z) < 0.75f ? near : far;
 }
 
-// bits i of 0 .. 15 with lo <= i < hi
-__device__ __forceinline__ uint32_t range16(int lo, int hi)
+// bits i of 0 .. 31 with lo <= i < hi
+__device__ __forceinline__ uint32_t range32(int lo, int hi)
 {
     lo = max(lo, 0);
-    hi = min(hi, 16);
-    return hi > lo ? (0xffffu >> (16 - hi)) & (0xffffu << lo) : 0u;
+    hi = min(hi, 32);
+    return hi > lo ? (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo) : 0u;
+}
+
+// the x-th 16-bit term of a pair
+template <typename DT> __device__ __forceinline__ uint32_t term(float a, float b, int x)
+{
+    uint32_t v = Pair<DT>::pack(a, b);
+    for (int i = 0; i < x; ++i) {
+        const float2 y = Pair<DT>::unpack(v);
+        a -= y.x;
+        b -= y.y;
+        v = Pair<DT>::pack(a, b);
+    }
+    return v;
+}
+
+// the power of two at or below a, from its exponent's bits (subnormals, infinities: 1)
+__device__ __forceinline__ float pow2_of(float a)
+{
+    const uint32_t e = __float_as_uint(a) >> 23;
+    return e < 1 || e > 253 ? 1.f : __uint_as_float(e << 23);
+}
+
+// largest |q| of the f32 row at `at`
+template <int D> __device__ __forceinline__ float row_max(const void *q, int64_t at)
+{
+    const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + at);
+    float a = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < D / 4; ++i) {
+        const float4 y = __ldg(src + i);
+        a = fmaxf(a, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+    }
+    return a;
 }
 
 template <typename C>
@@ -355,6 +396,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_init(bar + SB_QFREE, 1);
         mbar_init(bar + SB_XCH, C::WARPS);
         mbar_init(bar + SB_DRAIN, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar + SB_ITEM + s, 1);
+            mbar_init(bar + SB_TAKEN + s, C::WARPS + 1);
+        }
         ms->abort = 0;
         if (blockIdx.x == 0) *p.status = 0;
         fence_mbar_init();
@@ -383,61 +428,97 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int win_lo = 0;
         int32_t win_entry = 0;
         bool ok = true;
-        each_item<T, TP>(p, [&](const Item &it) {
+        auto wait = [&](int b, uint32_t parity) {
+            bool got = true;
+            if (lane == 0) got = mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
+            ok = ok && __shfl_sync(0xffffffffu, got, 0);
+            return ok;
+        };
+        auto copies = [&](const Item &it) {
             const int32_t *tab = nullptr;
             int width = 0;
             if (paged) {
-                tab = it.shared ? p.shared_table : p.block_table + (size_t)it.b * p.max_blocks;
-                width = it.shared ? p.shared_len / p.block_size : p.max_blocks;
+                tab = it.shared() ? p.shared_table : p.block_table + (size_t)it.b * p.max_blocks;
+                width = it.shared() ? p.shared_len / p.block_size : p.max_blocks;
             }
             // shared tiles are read by every row tile's items
-            const uint64_t pol = it.shared && p.row_tiles > 1 ? normal : first;
-            for (int i = 0; i < it.tiles; ++i) {
-                const int t0 = tile_at<T>(it, i);
+            const uint64_t pol = it.shared() && p.row_tiles > 1 ? normal : first;
+            // the order in which the MMAs take them: K0 K1 V0 K2 V1 ..., or K0 V0 K1 V1 ...
+            const int ahead = it.row_tiles() == 1 && it.tiles > 1 ? 1 : 0;
+            const int h = paged ? p.box_rows : T, nbox = T / h;
+            for (int i = 0; i < 2 * it.tiles; ++i) {
+                int kv, tile;
+                if (!ahead) {
+                    kv = i & 1;
+                    tile = i >> 1;
+                } else if (i == 0) {
+                    kv = tile = 0;
+                } else if (i == 2 * it.tiles - 1) {
+                    kv = 1;
+                    tile = it.tiles - 1;
+                } else {
+                    kv = (i & 1) ^ 1;
+                    tile = kv ? (i >> 1) - 1 : (i + 1) >> 1;
+                }
+                const int t0 = tile_at<T>(it, tile);
                 int blk = it.b, at = t0;
-                const int h = paged ? p.box_rows : T, nbox = T / h;
                 if (paged) {
                     // box j: h rows of one block, h a divisor of the tile and of the block
                     const int bs = p.block_size, lo = t0 / bs, hi = (t0 + T - 1) / bs;
                     if (tab != win_tab || lo < win_lo || hi >= win_lo + 32) {
+                        // (the V tile of the tile before comes after this K tile)
                         win_tab = tab;
-                        win_lo = lo;
-                        win_entry = lo + lane < width ? tab[lo + lane] : p.oob_block;
+                        win_lo = max(0, lo - (T + bs - 1) / bs - 1);
+                        if (hi >= win_lo + 32) win_lo = lo;
+                        win_entry = win_lo + lane < width ? tab[win_lo + lane] : p.oob_block;
                     }
                     const int pos = t0 + min(lane, nbox - 1) * h, e = pos / bs;
                     blk = __shfl_sync(0xffffffffu, win_entry, e - win_lo);
                     at = pos - e * bs;
                     if (pos >= it.end || blk < 0) blk = p.oob_block; // reads as zeros
                 }
-                for (int kv = 0; kv < 2; ++kv) {
-                    bool got = true;
-                    if (lane == 0)
-                        got = mbar_wait_bounded(bar + SB_EMPTY + st, phase ^ 1u, p.timeout_ns,
-                                                abort_flag);
-                    if (!__shfl_sync(0xffffffffu, got, 0)) {
-                        ok = false;
-                        return false;
-                    }
-                    if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
-                        uint8_t *dst = sm + p.q_bytes + st * C::SLOT;
-                        if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + st, C::SLOT);
-                        __syncwarp();
-                        if (lane < nbox) {
+                if (!wait(SB_EMPTY + st, phase ^ 1u)) return false;
+                if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
+                    uint8_t *dst = sm + p.q_bytes + st * C::SLOT;
+                    if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + st, C::SLOT);
+                    __syncwarp();
+                    if (lane < nbox) {
 #pragma unroll
-                            for (int c = 0; c < NCH; ++c)
-                                tma_load_4d(dst + c * CHUNK + lane * h * 128, kv ? &vmap : &kmap,
-                                            bar + SB_FULL + st, c * 64, it.kvh, at, blk, pol);
-                        }
-                        ++n;
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_4d(dst + c * CHUNK + lane * h * 128, kv ? &vmap : &kmap,
+                                        bar + SB_FULL + st, c * 64, it.kvh, at, blk, pol);
                     }
-                    if (++st == nst) {
-                        st = 0;
-                        phase ^= 1u;
-                    }
+                    ++n;
+                }
+                if (++st == nst) {
+                    st = 0;
+                    phase ^= 1u;
                 }
             }
             return true;
-        });
+        };
+        // items: every other round of them from the last CTA to the first
+        int passed = 0; // items put in the queue
+        auto pass_on = [&](const Item &it) {
+            const int s = passed & 1;
+            if (!wait(SB_TAKEN + s, ((uint32_t)(passed >> 1) & 1u) ^ 1u)) return false;
+            if (lane == 0) {
+                ms->item[s] = it;
+                mbar_arrive(bar + SB_ITEM + s);
+            }
+            ++passed;
+            return true;
+        };
+        const int g = gridDim.x;
+        Item it;
+        for (int r = 0, at = 0; ok && at < p.n_items; ++r, at += g) {
+            const int idx = at + (r & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+            if (idx >= p.n_items) continue;
+            get_item<T>(p, idx, it);
+            if (pass_on(it)) (void)copies(it);
+        }
+        it.tiles = -1;
+        if (ok) (void)pass_on(it);
         if (lane == 0) {
             if (!ok) timed_out();
             // nothing may be in flight when the CTA ends: the last copy into every slot
@@ -451,84 +532,105 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (lane == 0) {
             constexpr uint32_t idesc_qk = idesc_f16kind(128, T, 0, 0, C::BF);
             constexpr uint32_t idesc_pv = idesc_f16kind(128, D, 0, 1, C::BF);
-            int items = 0;
             uint32_t pph = 0;      // phases of PFULL, by slot
             bool ok = true;
             auto wait = [&](int b, uint32_t parity) {
                 ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
                 return ok;
             };
-            // ring positions of the next K and the next V tile (K and V take turns)
-            struct Place {
-                int st;
-                uint32_t ph;
-            } kp = {0, 0u}, vp = {1, 0u};
-            auto advance = [&](Place &x) {
-                x.st += 2;
-                if (x.st >= nst) {
-                    x.st -= nst;
-                    x.ph ^= 1u;
+            int st = 0;            // the next slot of the ring, and its phase
+            uint32_t ph = 0u;
+            auto take = [&](int &slot) { // waits for the next tile
+                slot = st;
+                if (!wait(SB_FULL + st, ph)) return false;
+                if (++st == nst) {
+                    st = 0;
+                    ph ^= 1u;
                 }
+                return true;
             };
             const uint32_t ring = sb + p.q_bytes;
-            each_item<T, TP>(p, [&](const Item &it) {
-                if (it.tiles == 0) return true;
-                const int nu = it.tiles * it.nrt, sh = it.nrt - 1;
-                const bool packed = it.parts > 1;
-                const int q_terms = packed ? 1 : p.q_terms, p_terms = packed ? 1 : TP;
-                if (!wait(SB_QFULL, (uint32_t)items & 1u)) return false;
+            auto item = [&](int tiles, int rows, uint32_t nth) {
+                const int sh = rows > 128 ? 1 : 0, nu = tiles << sh;
+                const int parts = parts_of<TP>(rows);
+                const bool one_p = parts > 1 || shares_of_terms<TP>(parts, reps_of(p, rows)) > 1;
+                const int q_terms = parts > 1 ? 1 : p.q_terms;
+                int ks = 0, vs = 0;
+                if (!wait(SB_QFULL, nth & 1u)) return false;
                 for (int v = 0; v < nu + 2; ++v) {
                     if (v >= 2) { // O += P V of unit v - 2
                         const int u = v - 2, s = u & 1, w = NWG == 2 ? s : 0;
-                        if (u == 0 && !wait(SB_OFREE, (uint32_t)items & 1u)) return false;
+                        if (u == 0 && !wait(SB_OFREE, nth & 1u)) return false;
                         if (!wait(SB_PFULL + s, (pph >> s) & 1u)) return false;
                         pph ^= 1u << s;
-                        if ((sh == 0 || !(u & 1)) && !wait(SB_FULL + vp.st, vp.ph)) return false;
+                        if ((sh == 0 || !(u & 1)) && !take(vs)) return false;
                         tc_fence_after();
-                        const uint64_t vd = smem_desc_sw128(ring + vp.st * C::SLOT, CHUNK, 1024);
-                        const uint32_t a = tmem + C::S_COL + s * 128;
-                        for (int x = 0; x < p_terms; ++x)
+                        const uint64_t vd = smem_desc_sw128(ring + vs * C::SLOT, CHUNK, 1024);
+                        const uint32_t a = tmem + C::S_COL + s * C::S_SLOT;
+                        if (one_p) {
 #pragma unroll
                             for (int k = 0; k < T / 16; ++k)
-                                tc_mma_ts(tmem + w * D, a + (x < 2 ? 16 * k + 8 * x : T + 8 * k),
-                                          vd + (uint64_t)((k * 2048) >> 4), idesc_pv);
-                        if (sh == 0 || (u & 1)) {
-                            tc_commit(bar + SB_EMPTY + vp.st);
-                            advance(vp);
+                                tc_mma_ts(tmem + w * D, a + 8 * k, vd + (uint64_t)((k * 2048) >> 4),
+                                          idesc_pv, 1u);
+                        } else {
+#pragma unroll 1
+                            for (int x = 0; x < TP; ++x)
+#pragma unroll
+                                for (int k = 0; k < T / 16; ++k)
+                                    tc_mma_ts(tmem + w * D,
+                                              x < 2 ? a + 16 * k + 8 * x : a + T + 8 * k,
+                                              vd + (uint64_t)((k * 2048) >> 4), idesc_pv, 1u);
                         }
+                        if (sh == 0 || (u & 1)) tc_commit(bar + SB_EMPTY + vs);
                         tc_commit(bar + SB_PVDONE + w);
                     }
                     if (v < nu) { // S of unit v
                         const int s = v & 1;
-                        if ((sh == 0 || !(v & 1)) && !wait(SB_FULL + kp.st, kp.ph)) return false;
+                        if ((sh == 0 || !(v & 1)) && !take(ks)) return false;
                         tc_fence_after();
+                        const uint32_t sd = tmem + C::S_COL + s * C::S_SLOT;
                         const uint64_t qd = smem_desc_sw128(
                             sb + (sh ? (v & 1) * p.q_terms * NCH * qch : 0), 16, 1024);
-                        const uint64_t kd = smem_desc_sw128(ring + kp.st * C::SLOT, 16, 1024);
+                        const uint64_t kd = smem_desc_sw128(ring + ks * C::SLOT, 16, 1024);
                         // the small terms first: an MMA's sums are cut off at their 24th bit, so
                         // that each addition to a large sum costs about 2^-24 of it
-                        for (int x = q_terms - 1; x >= 0; --x)
+                        constexpr int tm = C::QTM ? 1 : 0; // terms in TMEM
+#pragma unroll 1
+                        for (int x = q_terms - 1; x >= tm; --x)
 #pragma unroll
                             for (int c = 0; c < NCH; ++c)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     tc_mma_bf16(
-                                        tmem + C::S_COL + s * 128,
-                                        qd + (uint64_t)(((x * NCH + c) * qch + k * 32) >> 4),
+                                        sd, qd + (uint64_t)((((x - tm) * NCH + c) * qch + k * 32) >> 4),
                                         kd + (uint64_t)((c * CHUNK + k * 32) >> 4), idesc_qk,
                                         x != q_terms - 1 || (c | k) != 0 ? 1u : 0u);
-                        tc_commit(bar + SB_SFULL + s);
-                        if (sh == 0 || (v & 1)) {
-                            tc_commit(bar + SB_EMPTY + kp.st);
-                            advance(kp);
+                        if (C::QTM) {
+#pragma unroll
+                            for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc_mma_ts(sd, tmem + C::Q_COL + (c * 4 + k) * 8,
+                                              kd + (uint64_t)((c * CHUNK + k * 32) >> 4), idesc_qk,
+                                              q_terms > 1 || (c | k) != 0 ? 1u : 0u);
                         }
+                        tc_commit(bar + SB_SFULL + s);
+                        if (sh == 0 || (v & 1)) tc_commit(bar + SB_EMPTY + ks);
                         if (v == nu - 1) tc_commit(bar + SB_QFREE);
                     }
                 }
                 tc_commit(bar + SB_OREADY);
-                ++items;
                 return true;
-            });
+            };
+            uint32_t live = 0;     // items with tiles so far
+            for (int i = 0; ok; ++i) {
+                const int q = i & 1;
+                if (!wait(SB_ITEM + q, (uint32_t)(i >> 1) & 1u)) break;
+                const int tiles = ms->item[q].tiles, rows = ms->item[q].rows;
+                mbar_arrive(bar + SB_TAKEN + q);
+                if (tiles < 0) break;
+                if (tiles > 0) (void)item(tiles, rows, live++);
+            }
             if (!ok) timed_out();
             // no MMA may be in flight when TMEM is freed
             tc_commit(bar + SB_DRAIN);
@@ -541,7 +643,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int r = threadIdx.x & 127;      // row of the row tile, TMEM lane
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t to = tl + w * D;       // its accumulator
-        int n = 0, items = 0;
+        int n = 0, items = 0;                 // copies and items with tiles before this item
         uint32_t sph = 0;                     // phases of SFULL, by slot
         int done = 0;                         // units of this warpgroup so far
         uint32_t groups = 0, joints = 0;      // uses of SB_GROUP and SB_XCH
@@ -573,36 +675,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_fence_before();
         arrive(SB_OFREE);
 
-        each_item<T, TP>(p, [&](const Item &it) {
+        auto work = [&](const Item &it) {
             // ---- this thread's row and its share of every tile's columns (see above)
-            const int nrt = it.nrt, parts = it.parts;
-            const int span = nrt == 2 || it.rows > 64 ? 128 : it.rows > 32 ? 64 : 32;
-            const int reps = nrt == 2 ? 1 : max(1, p.rpad / span), copies = reps * parts;
+            const int nrt = it.row_tiles(), parts = parts_of<TP>(it.rows);
+            const int span = span_of(it.rows), reps = reps_of(p, it.rows), copies = reps * parts;
+            const int terms = shares_of_terms<TP>(parts, reps), shares = reps / terms;
             const int rep = (warp & 3) * 32 / span;
-            const int part = parts == 1 ? 0 : lane / (32 / parts);
             const bool in_use = rep < reps;                    // (of this warp)
-            const int cols = T / reps, cb = in_use ? rep * cols : 0;
+            const int share = in_use ? rep % shares : 0;
+            // its term of the weights
+            const int part = parts > 1 ? lane / (32 / parts) : in_use ? rep / shares : 0;
+            const bool one_p = parts * terms > 1;              // (a lane holds one term)
+            const int cols = T / shares, cb = share * cols;
             const int local = nrt == 2     ? w * 128 + r       // row of the item
                               : parts == 1 ? r - rep * span
                                            : lane & (32 / parts - 1);
             const bool owner = in_use && local < it.rows;
             const bool busy = in_use && (local & ~31) < it.rows;
             const int per_seq = p.q_len * Gh;
-            int row = it.row0 + (owner ? local : 0), b = it.b, S, q0;
-            if (it.shared) {
+            int row = it.row0 + (owner ? local : 0), b = it.b, S = it.S;
+            if (it.shared()) {
                 b = row / per_seq;
                 row -= b * per_seq;
                 S = length_of(p, b);
-                q0 = S - p.q_len;
-            } else {
-                S = it.S;
-                q0 = it.q0;
             }
+            const int q0 = it.S - p.q_len;         // of a sequence's own item: its first token
             const int tk = row / Gh, h = it.kvh * Gh + row - tk * Gh;
-            const int own = q0 + tk;               // its position behind the shared ones
+            const int own = S - p.q_len + tk;      // its position behind the shared ones
             const bool dead = !owner || own < 0;   // no such token: it sees nothing
             const int out_row = tk * p.hq + h;
-            const size_t slot = (size_t)p.slot[b] + it.split + (it.shared ? 0 : p.shared_splits);
+            const size_t slot = (size_t)p.slot[b] + it.split + (it.shared() ? 0 : p.shared_splits);
             // its row of the output, or of the partials
             const size_t dst_row = p.whole ? (size_t)b * p.rows + out_row : slot * p.rows + out_row;
             auto write4 = [&](size_t row_at, int c, const float4 &f) {
@@ -617,27 +719,67 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             };
             if (it.tiles == 0) { // nothing to see: a neutral partial
                 if (owner && rep == 0 && part == 0 && (nrt == 2 || w == 0)) {
-                    if (p.whole)
+                    if (p.whole) {
+#pragma unroll 1
                         for (int c = 0; c < D; c += 4)
                             write4(dst_row, c, make_float4(0.f, 0.f, 0.f, 0.f));
-                    else
+                    } else {
                         p.ml[dst_row] = make_float2(kNeutralM, 0.f);
+                    }
                 }
                 return true;
             }
 
             // ---- Q, once the last item's scores are done with it
             if (items > 0 && !wait(SB_QFREE, (uint32_t)(items - 1) & 1u)) return false;
-            {
+            const int64_t q_at = (((int64_t)b * p.q_len + tk) * p.hq + h) * D; // of this row
+            float row_scale = 1.f;
+            if (C::QTM) {
+                // a lane's own row: the first term, or its part's, 32 columns at a time
+                if (p.q_f32 && !C::BF && busy) row_scale = pow2_of(row_max<D>(p.q, q_at));
+                const float down = 1.f / row_scale;
+                if (busy) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[16];
+                        if (!p.q_f32) {
+                            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                static_cast<const uint16_t *>(p.q) + q_at + c);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 y = __ldg(src + i);
+                                v[4 * i] = y.x;
+                                v[4 * i + 1] = y.y;
+                                v[4 * i + 2] = y.z;
+                                v[4 * i + 3] = y.w;
+                            }
+                        } else {
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                static_cast<const float *>(p.q) + q_at + c);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 y = __ldg(src + i);
+                                v[2 * i] = term<DT>(y.x * down, y.y * down, parts > 1 ? part : 0);
+                                v[2 * i + 1] = term<DT>(y.z * down, y.w * down, parts > 1 ? part : 0);
+                            }
+                        }
+                        tmem_st16w(tl + C::Q_COL + c / 2, v);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+            }
+            // the other terms, or all, in shared memory
+            if (!C::QTM || (p.q_f32 && parts == 1)) {
                 // 8-column units, a half-warp's or a warp's to a row; four of a thread in flight
                 // (rows past the last eight give scores that nobody reads)
-                constexpr int U8 = D / 8, STEP = C::WARPS * 32;
+                constexpr int U8 = D / 8, STEP = C::WARPS * 32, TM = C::QTM ? 1 : 0;
                 const int units = (it.rows + 7) / 8 * 8 * U8;
                 const int j = threadIdx.x % U8; // (the step is a multiple of a row)
                 auto source = [&](int rr) { // element of q, or -1
                     if (rr >= it.rows) return (int64_t)-1;
                     int qrow = it.row0 + rr, qb = it.b;
-                    if (it.shared) {
+                    if (it.shared()) {
                         qb = qrow / per_seq;
                         qrow -= qb * per_seq;
                     }
@@ -646,19 +788,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 };
                 // unit j of row rr: term x, at all copies of the row
                 auto put = [&](int rr, int x, const uint32_t *v) {
-                    const uint32_t dst = sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch;
-                    if (parts == 1) {
-                        for (int k = 0; k < reps; ++k)
-                            sts_v4(dst + x * NCH * qch + swz((rr & 127) + k * span, (j & 7) * 16), v[0],
-                                   v[1], v[2], v[3]);
-                    } else {
-                        for (int k = 0; k < reps; ++k)
-                            sts_v4(dst + swz(k * 32 + x * (32 / parts) + rr, (j & 7) * 16), v[0], v[1],
-                                   v[2], v[3]);
-                    }
+                    const uint32_t dst = sb + (rr >> 7) * p.q_terms * NCH * qch + (j >> 3) * qch +
+                                         (parts == 1 ? x * NCH * qch : 0);
+                    const int first = (rr & 127) + (parts == 1 ? 0 : x * (32 / parts));
+#pragma unroll 1
+                    for (int k = 0; k < reps; ++k)
+                        sts_v4(dst + swz(first + k * span, (j & 7) * 16), v[0], v[1], v[2], v[3]);
                 };
-                const uint32_t none[4] = {0u, 0u, 0u, 0u};
                 if (!p.q_f32) {
+#pragma unroll 1
                     for (int u0 = threadIdx.x; u0 < units; u0 += 4 * STEP) {
                         uint4 x[4];
 #pragma unroll
@@ -678,6 +816,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                 } else {
+#pragma unroll 1
                     for (int u0 = threadIdx.x; u0 < units; u0 += 4 * STEP) {
                         float4 xa[4], xb[4];
 #pragma unroll
@@ -704,20 +843,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 float a = 0.f;
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
+#pragma unroll
                                 for (int o = U8 / 2; o > 0; o >>= 1)
                                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                                // 2^-e from the exponent of a (its bits; subnormals, infinities: 1)
-                                const int e = (int)(__float_as_uint(a) >> 23);
-                                const bool plain = e < 1 || e > 253;
-                                const float down =
-                                    plain ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
-                                if (j == 0)
-                                    ms->row_scale[u / U8] =
-                                        plain ? 1.f : __uint_as_float((uint32_t)e << 23);
+                                const float up = pow2_of(a);
+                                if (j == 0) ms->row_scale[u / U8] = up;
+                                const float down = 1.f / up;
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) f[k] *= down;
                             }
-                            for (int x = 0; x < p.q_terms; ++x) {
+#pragma unroll 1
+                            for (int x = 0; x < (parts > 1 ? parts : p.q_terms); ++x) {
                                 uint32_t v[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
@@ -725,27 +861,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     const float2 y = Pair<DT>::unpack(v[k]);
                                     f[2 * k] -= y.x;
                                     f[2 * k + 1] -= y.y;
+                                    if (x >= p.q_terms) v[k] = 0u; // (four lanes, three terms)
                                 }
-                                put(u / U8, x, v);
+                                if (x >= TM) put(u / U8, x - TM, v);
                             }
-                            if (parts > p.q_terms) put(u / U8, 3, none); // (of four lanes, three terms)
                         }
                     }
                 }
+                fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
-            if (TP == 3 && parts == 1 && reps > 1 && busy) {
+            if (TP == 3 && !one_p && reps > 1 && busy) {
                 // the third terms have columns of their own: zero but for this warp's share
                 const uint32_t z[16] = {};
                 for (int s = NWG == 2 ? w : 0; s < 2; s += NWG)
-                    for (int c = 0; c < T / 2; c += 16) tmem_st16w(tl + C::S_COL + s * 128 + T + c, z);
+                    for (int c = 0; c < T / 2; c += 16)
+                        tmem_st16w(tl + C::S_COL + s * C::S_SLOT + T + c, z);
                 tmem_wait_st();
             }
             arrive(SB_QFULL);
 
             // ---- what this row sees and how it scores
             Scorer sc;
-            const int pos = own + (it.shared ? p.shared_len : 0); // in this item's positions
+            const int pos = own + (it.shared() ? p.shared_len : 0); // in this item's positions
             sc.slope = p.slopes && owner ? __ldg(p.slopes + h) * kLog2e : 0.f;
             sc.cap = p.softcap * kLog2e;
             sc.mult = sc.turn = 0.f;
@@ -759,30 +896,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int nu = it.tiles * nrt;
             float m = -INFINITY, l = 0.f;
             int mine = 0; // units of this item so far
+#pragma unroll 1
             for (int u = NWG == 2 ? w : 0; u < nu; u += NWG) {
                 const int tile = nrt == 2 ? u >> 1 : u, s = u & 1;
                 const int t0 = tile_at<T>(it, tile);
-                const uint32_t ts = tl + C::S_COL + s * 128;
+                const uint32_t ts = tl + C::S_COL + s * C::S_SLOT;
                 if (!wait(SB_SFULL + s, (sph >> s) & 1u)) return false;
                 sph ^= 1u << s;
                 tc_fence_after();
                 if (mine == 0) { // (an f32 q's row scale is there once all of Q is)
-                    const float x = p.scale * (!C::BF && p.q_f32 ? ms->row_scale[owner ? local : 0] : 1.f);
+                    if (!C::QTM && !C::BF && p.q_f32) row_scale = ms->row_scale[owner ? local : 0];
+                    const float x = p.scale * row_scale;
                     sc.mult = x * kLog2e;
                     sc.turn = p.softcap == 0.f ? 0.f : x / p.softcap;
                 }
 
                 // which columns are visible: all, all below a border, or row by row
                 bool full = t0 + T <= it.end;
-                if (!it.shared) {
-                    const int o0 = max(it.q0, 0), o1 = it.S - 1;
+                if (!it.shared()) {
+                    const int o0 = max(q0, 0), o1 = it.S - 1;
                     full = full && t0 >= it.start &&
                            (t0 + T <= it.keep1 ||
                             (t0 + T - 1 <= o0 && (!p.window || t0 > o1 - p.window)));
                 }
                 int k0 = 0, k1 = 0, x0 = 0, x1 = T; // visible: [k0, k1) and [x0, x1)
                 if (!full) {
-                    if (it.shared) {
+                    if (it.shared()) {
                         x1 = min(T, it.end - t0);
                     } else {
                         k0 = max(it.start - t0, 0);
@@ -792,19 +931,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
                 const bool adds = parts > 1 && p.q_f32; // a score is the sum over a row's lanes
-                // what the scores become takes their place (one granule that needs no other pass
-                // stays in registers)
-                const bool modified = adds || transform || !full;
+                // what the scores become takes their place; a share of one granule also stays in
+                // registers until it is weights
+                const bool modified = adds || transform || !full, one = cols == C::G;
+                const bool back = modified && (!one || !full);
                 float tm = -INFINITY;
-                float x[16];
+                float x[C::G];
                 if (busy) {
 #pragma unroll 1
-                    for (int c = cb; c < cb + cols; c += 16) {
-                        tmem_ld16(ts + c, x);
+                    for (int c = cb; c < cb + cols; c += C::G) {
+#pragma unroll
+                        for (int i = 0; i < C::G; i += 16) tmem_ld16(ts + c + i, x + i);
                         tmem_wait_ld();
                         if (adds) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
+                            for (int i = 0; i < C::G; ++i) {
                                 x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
                                 if (TP == 3) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 8);
                             }
@@ -813,40 +954,43 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             // y, -infinity where the row sees nothing
                             if (p.softcap == 0.f) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) x[i] *= sc.mult;
+                                for (int i = 0; i < C::G; ++i) x[i] *= sc.mult;
                             } else if (precise) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
+                                for (int i = 0; i < C::G; ++i)
                                     x[i] = capped<true>(x[i] * sc.turn, sc.cap);
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
+                                for (int i = 0; i < C::G; ++i)
                                     x[i] = capped<false>(x[i] * sc.turn, sc.cap);
                             }
                             if (p.slopes) {
                                 const float d = (float)(pos - t0 - c);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
+                                for (int i = 0; i < C::G; ++i)
                                     x[i] = fmaf(-sc.slope, fabsf(d - (float)i), x[i]);
                             }
                             if (!full) {
                                 const uint32_t see =
-                                    range16(x0 - c, x1 - c) | range16(k0 - c, k1 - c);
+                                    range32(x0 - c, x1 - c) | range32(k0 - c, k1 - c);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
+                                for (int i = 0; i < C::G; ++i)
                                     if (!((see >> i) & 1u)) x[i] = -INFINITY;
                             }
                         }
-                        if (modified) tmem_st16(ts + c, x);
+                        if (back) {
+#pragma unroll
+                            for (int i = 0; i < C::G; i += 16) tmem_st16(ts + c + i, x + i);
+                        }
                         float a = x[0], b2 = x[1];
 #pragma unroll
-                        for (int i = 2; i < 16; i += 2) {
+                        for (int i = 2; i < C::G; i += 2) {
                             a = fmaxf(a, x[i]);
                             b2 = fmaxf(b2, x[i + 1]);
                         }
                         tm = fmaxf(tm, fmaxf(a, b2));
                     }
-                    if (modified) tmem_wait_st();
+                    if (back) tmem_wait_st();
                     if (!transform && full) tm *= sc.mult;
                 }
                 const float mult = transform || !full ? 1.f : sc.mult;
@@ -877,11 +1021,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
                 // ---- a tile that not all rows see in full: V rows that no row sees may hold
                 // anything (0 * NaN is NaN), and so may rows that some see
-                if (!full && !it.shared) {
-                    const int f = n + 2 * tile + 1, st = f % nst;
+                if (!full && !it.shared()) {
+                    // (the copies of a sequence's item: K0 K1 V0 K2 V1 ...)
+                    const int f = n + min(2 * tile + 2, 2 * it.tiles - 1), st = f % nst;
                     if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
                     const uint32_t vt = sb + p.q_bytes + st * C::SLOT;
-                    const int o0 = max(it.q0, 0), o1 = it.S - 1;
+                    const int o0 = max(q0, 0), o1 = it.S - 1;
                     const int ka = max(it.start - t0, 0), kb = min(it.keep1 - t0, T);
                     const int lo_any = max(p.window ? max(it.start, o0 - p.window + 1) : it.start, 0) - t0;
                     const int lo_all = max(p.window ? max(it.start, o1 - p.window + 1) : it.start, 0) - t0;
@@ -896,17 +1041,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (!group_sync()) return false;
                     }
                     // rows of D / 8 units; a thread's units are of one row each
+#pragma unroll 1
                     for (int i = r; i < T * (D / 8); i += 128) {
                         const int c = i / (D / 8), j = i - c * (D / 8);
                         const uint32_t at = vt + (j >> 3) * CHUNK + swz(c, (j & 7) * 16);
                         if (!any(c)) {
                             sts_v4(at, 0u, 0u, 0u, 0u);
                         } else if (partial && !all(c)) {
-                            const uint4 x = lds_v4(at);
+                            const uint4 y = lds_v4(at);
                             const uint32_t e = C::BF ? 0x7f80u : 0x7c00u; // exponent of infinities, NaN
                             bool odd = false;
-                            for (uint32_t y : {x.x, x.y, x.z, x.w})
-                                odd = odd || (y & e) == e || ((y >> 16) & e) == e;
+                            for (uint32_t z : {y.x, y.y, y.z, y.w})
+                                odd = odd || (z & e) == e || ((z >> 16) & e) == e;
                             if (odd) atomicOr(bad + (c >> 5), 1u << (c & 31));
                         }
                     }
@@ -921,6 +1067,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             if (mine > 0 && !wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u))
                                 return false;
                             tc_fence_after();
+#pragma unroll 1
                             for (int c = 0; c < T; ++c) {
                                 if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
                                 const float y = tmem_ld1(ts + c);
@@ -949,6 +1096,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 }
                             }
                             if (!group_sync()) return false;
+#pragma unroll 1
                             for (int i = r; i < T * (D / 8); i += 128) {
                                 const int c = i / (D / 8), j = i - c * (D / 8);
                                 if ((word[c >> 5] >> (c & 31)) & 1u)
@@ -959,53 +1107,66 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     fence_proxy_async_smem();
                 }
 
-                // ---- P: the weights, in terms, in the place of their scores
+                // ---- P: the weights, in terms, in the place of their scores. One term of 16
+                // positions takes 8 columns: those of a lane's one term lie side by side, of several
+                // 16 apart (16 k: the first term, 16 k + 8: the second, T + 8 k: the third)
                 if (busy) {
                     float l4[4] = {};
-                    const bool one = cols == 16; // (still in registers)
 #pragma unroll 1
-                    for (int c = cb; c < cb + cols; c += 16) {
+                    for (int c = cb; c < cb + cols; c += C::G) {
                         if (!one) {
-                            tmem_ld16(ts + c, x);
+#pragma unroll
+                            for (int i = 0; i < C::G; i += 16) tmem_ld16(ts + c + i, x + i);
                             tmem_wait_ld();
                         }
-                        uint32_t t16[16];
+                        uint32_t first[C::G / 2], second[C::G / 2];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
+                        for (int i = 0; i < C::G; i += 2) {
                             const float a = ex2(fmaf(x[i], mult, -ref));
                             const float b2 = ex2(fmaf(x[i + 1], mult, -ref));
                             l4[i & 3] += a;
                             l4[(i + 1) & 3] += b2;
-                            t16[i / 2] = Pair<DT>::pack(a, b2);
-                            const float2 y = Pair<DT>::unpack(t16[i / 2]);
+                            first[i / 2] = Pair<DT>::pack(a, b2);
+                            const float2 y = Pair<DT>::unpack(first[i / 2]);
                             x[i] = a - y.x;
                             x[i + 1] = b2 - y.y;
-                            t16[8 + i / 2] = Pair<DT>::pack(x[i], x[i + 1]);
+                            second[i / 2] = Pair<DT>::pack(x[i], x[i + 1]);
                         }
                         if (TP == 3) {
                             uint32_t third[8];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float2 z = Pair<DT>::unpack(t16[8 + i / 2]);
+                                const float2 z = Pair<DT>::unpack(second[i / 2]);
                                 third[i / 2] = Pair<DT>::pack(x[i] - z.x, x[i + 1] - z.y);
-                                if (part >= 2) t16[i / 2] = part == 2 ? third[i / 2] : 0u;
+                                if (part >= 2) first[i / 2] = part == 2 ? third[i / 2] : 0u;
                             }
-                            if (parts == 1) tmem_st8w(ts + T + c / 2, third);
+                            if (!one_p) tmem_st8w(ts + T + c / 2, third);
                         }
-                        if (parts == 1) {
-                            tmem_st16w(ts + c, t16);
+                        if (one_p) {
+#pragma unroll
+                            for (int i = 0; i < C::G / 2; ++i)
+                                if (part == 1) first[i] = second[i];
+                            if (C::G == 32) tmem_st16w(ts + c / 2, first);
+                            else tmem_st8w(ts + c / 2, first);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (part == 1) t16[i] = t16[8 + i];
-                            tmem_st8w(ts + c, t16);
+                            for (int i = 0; i < C::G; i += 16) {
+                                tmem_st8w(ts + c + i, first + i / 2);
+                                tmem_st8w(ts + c + i + 8, second + i / 2);
+                            }
                         }
                     }
-                    if (reps > 1) {
+                    if (shares > 1) { // the other shares' weights of these lanes
                         const uint32_t z[16] = {};
+                        const int each = one_p ? C::G / 2 : C::G;
 #pragma unroll 1
-                        for (int c = 0; c < T; c += 16)
-                            if (c < cb || c >= cb + cols) tmem_st16w(ts + c, z);
+                        for (int c = 0; c < T; c += C::G) {
+                            if (c >= cb && c < cb + cols) continue;
+                            const int at = c / C::G * each;
+                            if (each >= 16) tmem_st16w(ts + at, z);
+                            else tmem_st8w(ts + at, z);
+                            if (each == 32) tmem_st16w(ts + at + 16, z);
+                        }
                     }
                     l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tmem_wait_st();
@@ -1029,18 +1190,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // (a sum that is no number takes part: only an empty state does not)
                 const int first = owner ? local : 0;
                 float mm = -INFINITY, ll = 0.f;
-                for (int k = 0; k < reps * NWG; ++k) {
-                    const float2 x = ms->state[k % NWG][first + k / NWG * span];
-                    if (x.y != 0.f) mm = fmaxf(mm, x.x);
+                for (int k = 0; k < shares * NWG; ++k) {
+                    const float2 y = ms->state[k % NWG][first + k / NWG * span];
+                    if (y.y != 0.f) mm = fmaxf(mm, y.x);
                 }
-                for (int k = 0; k < reps * NWG; ++k) {
-                    const float2 x = ms->state[k % NWG][first + k / NWG * span];
-                    if (x.y != 0.f) ll += x.y * ex2(x.x - mm);
+                for (int k = 0; k < shares * NWG; ++k) {
+                    const float2 y = ms->state[k % NWG][first + k / NWG * span];
+                    if (y.y != 0.f) ll += y.y * ex2(y.x - mm);
                 }
                 f_own = l == 0.f ? 0.f : ex2(m - mm);
                 if (joint) {
-                    const float2 x = ms->state[NWG - 1 - w][r];
-                    f_other = x.y == 0.f ? 0.f : ex2(x.x - mm);
+                    const float2 y = ms->state[NWG - 1 - w][r];
+                    f_other = y.y == 0.f ? 0.f : ex2(y.x - mm);
                 }
                 m = mm;
                 l = ll;
@@ -1052,31 +1213,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (writes && !p.whole && (!joint || w == 0))
                 p.ml[dst_row] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
                                 : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
-            // 16 columns of the lane, its warpgroups' joined
-            auto lane16 = [&](int c, float *o) {
-                tmem_ld16(to + c, o);
+            // 32 columns of the lane, its warpgroups' joined
+            auto lane32 = [&](int c, float *o) {
+                tmem_ld32(to + c, o);
                 if (joint) {
-                    float o2[16];
-                    tmem_ld16(tl + (w ^ 1) * D + c, o2);
+                    float o2[32];
+                    tmem_ld32(tl + (NWG - 1 - w) * D + c, o2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = f_own * o[i] + f_other * o2[i];
+                    for (int i = 0; i < 32; ++i) o[i] = f_own * o[i] + f_other * o2[i];
                 } else {
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] *= f_own;
+                    for (int i = 0; i < 32; ++i) o[i] *= f_own;
                 }
             };
             if (copies == 1) {
 #pragma unroll 1
-                for (int c = c0; c < c0 + nc; c += 16) {
-                    float o[16];
-                    lane16(c, o);
+                for (int c = c0; c < c0 + nc; c += 32) {
+                    float o[32];
+                    lane32(c, o);
                     if (writes && (p.whole || l != 0.f)) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = factor == 0.f ? 0.f : o[i] * factor;
+                        for (int i = 0; i < 32; ++i) o[i] = factor == 0.f ? 0.f : o[i] * factor;
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
+                        for (int i = 0; i < 32; i += 4)
                             write4(dst_row, c + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
                     }
                 }
@@ -1087,36 +1248,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int rows8 = (it.rows + 7) / 8 * 8;
                 int W = nc;
                 while ((joint ? 2 : 1) * copies * rows8 * W * 4 > p.q_bytes) W >>= 1;
-                const int w4 = W / 4;
+                const int w4 = W / 4, lw = 31 - __clz(w4);
                 if (writes && w == 0) {
                     ms->row.factor[local] = factor;
                     ms->row.to[local] = (uint32_t)dst_row;
                 }
                 float4 *xs = reinterpret_cast<float4 *>(sm) + (joint ? w * copies * rows8 * w4 : 0);
+#pragma unroll 1
                 for (int at = 0; at < nc; at += W) {
                     if (busy) {
-                        float4 *to_row = xs + ((rep * parts + part) * rows8 + local) * w4;
+                        const int copy = parts > 1 ? rep * parts + part : rep;
+                        float4 *to_row = xs + (copy * rows8 + local) * w4;
 #pragma unroll 1
-                        for (int c = 0; c < W; c += 16) {
-                            float o[16];
-                            lane16(c0 + at + c, o);
+                        for (int c = 0; c < W; c += 32) {
+                            float o[32];
+                            lane32(c0 + at + c, o);
                             if (owner) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    to_row[(c / 4 + i) ^ (local & 3)] = make_float4(
+                                for (int i = 0; i < 8; ++i)
+                                    to_row[(c / 4 + i) ^ (local & 7)] = make_float4(
                                         o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                             }
                         }
                     }
                     if (!(at == 0 ? all_sync() : group_sync())) return false;
                     // w4 threads to a row
-                    const int lw = 31 - __clz(w4), c = r & (w4 - 1);
+                    const int c = r & (w4 - 1);
+#pragma unroll 1
                     for (int rr = r >> lw; rr < it.rows; rr += 128 >> lw) {
                         const float fac = ms->row.factor[rr];
                         if (fac == 0.f && !p.whole) continue;
                         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (int k = 0; k < copies; ++k) {
-                            const float4 y = xs[(k * rows8 + rr) * w4 + (c ^ (rr & 3))];
+                            const float4 y = xs[(k * rows8 + rr) * w4 + (c ^ (rr & 7))];
                             sum.x += y.x;
                             sum.y += y.y;
                             sum.z += y.z;
@@ -1132,14 +1296,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             // the next item starts from zero
             zero_o(to + c0, nc);
-            if (joint) zero_o(tl + (w ^ 1) * D + c0, nc);
+            if (joint) zero_o(tl + (NWG - 1 - w) * D + c0, nc);
             tmem_wait_st();
             tc_fence_before();
             arrive(SB_OFREE);
             n += 2 * it.tiles;
             ++items;
             return true;
-        });
+        };
+#pragma unroll 1
+        for (int i = 0;; ++i) {
+            const int q = i & 1;
+            if (!wait(SB_ITEM + q, (uint32_t)(i >> 1) & 1u)) break;
+            const Item it = ms->item[q];
+            arrive(SB_TAKEN + q);
+            if (it.tiles < 0 || !work(it)) break;
+        }
         if (!ok && lane == 0) timed_out();
     }
 

@@ -14,6 +14,8 @@ __host__ __device__ constexpr int scored_tile(int D, int terms)
     return D == 128 && terms == 2 ? 128 : 64;
 }
 __host__ __device__ constexpr int scored_groups(int D) { return D == 128 ? 2 : 1; }
+// 256 columns, two terms: TMEM has room for a term of Q beside O and the scores
+__host__ __device__ constexpr bool scored_q_in_tmem(int D, int terms) { return D == 256 && terms == 2; }
 // terms of a weight (and of an f32 q): f16 carries 11 bits a term, bf16 8
 constexpr int scored_terms(int kv_dtype, int out_dtype)
 {
@@ -22,11 +24,11 @@ constexpr int scored_terms(int kv_dtype, int out_dtype)
 constexpr int kScoredMaxSlots = 8;
 // barriers, exchange of (m, l), row scales (at 256 columns beside 128 rows of two terms and three
 // tiles of the ring)
-__host__ __device__ constexpr int scored_misc(int D) { return D == 128 ? 3072 : 2048; }
+__host__ __device__ constexpr int scored_misc(int D) { return D == 128 ? 3328 : 2048; }
 constexpr int kScoredSmemMax = 232448;
 
-// Shared memory: Q [row tile][term][64-column chunk][rpad rows of 128 bytes], then a ring of
-// K and V tiles, then the rest.
+// Shared memory: the terms of Q that TMEM does not hold, [row tile][term][64-column chunk][rpad rows
+// of 128 bytes], then a ring of K and V tiles, then the rest.
 struct ScoredGeometry {
     int q_terms;   // 1: q is of the cache's type
     int tile_rows; // query rows of an item, at most (256: two row tiles that share K and V tiles)
@@ -47,7 +49,10 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
     const int slot = scored_tile(D, p_terms) * D * 2;
     const int64_t most = shared_rows > own_rows ? shared_rows : own_rows;
     g.q_terms = q_terms;
-    const int held = most <= scored_packed(p_terms) ? 1 : q_terms; // of the widest item
+    // terms in shared memory, and the least that the join of copies has to have
+    const bool tm = scored_q_in_tmem(D, p_terms);
+    const int held = (most <= scored_packed(p_terms) ? 1 : q_terms) - (tm ? 1 : 0);
+    const int least = tm ? 32768 : 0;
     // (two row tiles only for a q of one term: with more terms the ring would be too short)
     for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
         const int rows = (int)(most < g.tile_rows ? most : g.tile_rows);
@@ -55,6 +60,7 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
         // shorter than a tile and a half takes smaller items
         for (g.rpad = 128;; g.rpad /= 2) {
             g.q_bytes = (rows > 128 ? 2 : 1) * held * g.rpad * D * 2;
+            if (g.q_bytes < least) g.q_bytes = least;
             g.slots = (kScoredSmemMax - 1024 - scored_misc(D) - g.q_bytes) / slot;
             if (g.slots >= 4 || g.rpad / 2 < rows || g.rpad == 32) break;
         }
@@ -76,7 +82,8 @@ inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int row
     const int T = scored_tile(D, p_terms);
     const int span = rows > 64 ? 128 : rows > 32 ? 64 : 32;
     const int reps = rows > 128 || g.rpad < span ? 1 : g.rpad / span;
-    // additions of a unit to a lane (packed: a term has a lane of its own)
+    // additions of a unit to a lane (packed: a term has a lane of its own; or copies of its own, and
+    // then half as many share the columns)
     const int per = T / 16 / reps * (rows <= scored_packed(p_terms) ? 1 : p_terms);
     const int units = 48 / (per > 1 ? per : 1);
     return rows > 128 || scored_groups(D) == 1 ? units : 2 * units;
