@@ -65,7 +65,6 @@ template <typename DT_, int D_, int TP_> struct Cfg {
     static constexpr int SLOT = NCH * CHUNK;
     static constexpr int WARPS = NWG * 4;   // softmax warps
     static constexpr int THREADS = (WARPS + 2) * 32;
-    static constexpr int G = T / 4;         // columns that a warp takes at a time
     // TMEM columns: O of warpgroup w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
     static constexpr bool QTM = scored_q_in_tmem(D, TP);
     static constexpr int S_COL = 256, S_SLOT = QTM ? 64 : 128, Q_COL = 384;
@@ -91,7 +90,8 @@ struct Item {
     int end;                // positions from here on are not there
     int start, keep1;       // visible to every row: [start, keep1)
     int S;                  // the sequence's length
-    int pad[2];
+    int last;               // of its CTA
+    int pad;
     __device__ __forceinline__ bool shared() const { return b < 0; }
     __device__ __forceinline__ int row_tiles() const { return rows > 128 ? 2 : 1; }
 };
@@ -147,7 +147,7 @@ template <int TP> __device__ __forceinline__ int shares_of_terms(int parts, int 
 template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
 {
     const int per_seq = p.q_len * (p.hq / p.hkv);
-    it.pad[0] = it.pad[1] = 0;
+    it.last = it.pad = 0;
     if (idx < p.shared_items) {
         it.b = -1;
         const int u = idx / p.row_tiles;
@@ -424,9 +424,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const bool paged = p.block_table != nullptr;
         int st = 0, n = 0; // slot, copies issued
         uint32_t phase = 0;
-        const int32_t *win_tab = nullptr;
-        int win_lo = 0;
-        int32_t win_entry = 0;
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
             bool got = true;
@@ -434,68 +431,78 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ok = ok && __shfl_sync(0xffffffffu, got, 0);
             return ok;
         };
+        // lanes hold the 64 table entries from `base` on, the second half ahead of its use
+        const int32_t *tab = nullptr;
+        int width = 0, base = -1;
+        int32_t near = 0, next = 0;
+        auto entry = [&](int i) { return i >= 0 && i < width ? __ldg(tab + i) : p.oob_block; };
+        struct At { // of this lane's box of a tile: block (or sequence) and position in it
+            int blk, pos;
+        };
+        const int h = paged ? p.box_rows : T, nbox = T / h;
+        auto locate = [&](const Item &it, int tile) {
+            const int t0 = tile_at<T>(it, tile);
+            if (!paged) return At{it.b, t0};
+            // box j: h rows of one block, h a divisor of the tile and of the block
+            const int bs = p.block_size, pos = t0 + min(lane, nbox - 1) * h, e = pos / bs;
+            const int lo = __shfl_sync(0xffffffffu, e, 0);
+            if (base < 0 || lo < base || lo >= base + 64) {
+                base = lo;
+                near = entry(base + lane);
+                next = entry(base + 32 + lane);
+            } else if (lo >= base + 32) {
+                base += 32;
+                near = next;
+                next = entry(base + 32 + lane);
+            }
+            // (a tile lies in at most 9 blocks)
+            const int i = e - base;
+            const int x = __shfl_sync(0xffffffffu, near, i & 31);
+            const int y = __shfl_sync(0xffffffffu, next, i & 31);
+            int blk = i < 32 ? x : y;
+            if (pos >= it.end || blk < 0) blk = p.oob_block; // reads as zeros
+            return At{blk, pos - e * bs};
+        };
+        auto copy = [&](const CUtensorMap *map, const Item &it, const At &at, uint64_t pol) {
+            if (!wait(SB_EMPTY + st, phase ^ 1u)) return;
+            if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
+                uint8_t *dst = sm + p.q_bytes + st * C::SLOT;
+                if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + st, C::SLOT);
+                __syncwarp();
+                if (lane < nbox) {
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_4d(dst + c * CHUNK + lane * h * 128, map, bar + SB_FULL + st, c * 64,
+                                    it.kvh, at.pos, at.blk, pol);
+                }
+                ++n;
+            }
+            if (++st == nst) {
+                st = 0;
+                phase ^= 1u;
+            }
+        };
         auto copies = [&](const Item &it) {
-            const int32_t *tab = nullptr;
-            int width = 0;
+            if (it.tiles == 0) return;
             if (paged) {
                 tab = it.shared() ? p.shared_table : p.block_table + (size_t)it.b * p.max_blocks;
                 width = it.shared() ? p.shared_len / p.block_size : p.max_blocks;
+                base = -1;
             }
             // shared tiles are read by every row tile's items
             const uint64_t pol = it.shared() && p.row_tiles > 1 ? normal : first;
             // the order in which the MMAs take them: K0 K1 V0 K2 V1 ..., or K0 V0 K1 V1 ...
-            const int ahead = it.row_tiles() == 1 && it.tiles > 1 ? 1 : 0;
-            const int h = paged ? p.box_rows : T, nbox = T / h;
-            for (int i = 0; i < 2 * it.tiles; ++i) {
-                int kv, tile;
-                if (!ahead) {
-                    kv = i & 1;
-                    tile = i >> 1;
-                } else if (i == 0) {
-                    kv = tile = 0;
-                } else if (i == 2 * it.tiles - 1) {
-                    kv = 1;
-                    tile = it.tiles - 1;
-                } else {
-                    kv = (i & 1) ^ 1;
-                    tile = kv ? (i >> 1) - 1 : (i + 1) >> 1;
-                }
-                const int t0 = tile_at<T>(it, tile);
-                int blk = it.b, at = t0;
-                if (paged) {
-                    // box j: h rows of one block, h a divisor of the tile and of the block
-                    const int bs = p.block_size, lo = t0 / bs, hi = (t0 + T - 1) / bs;
-                    if (tab != win_tab || lo < win_lo || hi >= win_lo + 32) {
-                        // (the V tile of the tile before comes after this K tile)
-                        win_tab = tab;
-                        win_lo = max(0, lo - (T + bs - 1) / bs - 1);
-                        if (hi >= win_lo + 32) win_lo = lo;
-                        win_entry = win_lo + lane < width ? tab[win_lo + lane] : p.oob_block;
-                    }
-                    const int pos = t0 + min(lane, nbox - 1) * h, e = pos / bs;
-                    blk = __shfl_sync(0xffffffffu, win_entry, e - win_lo);
-                    at = pos - e * bs;
-                    if (pos >= it.end || blk < 0) blk = p.oob_block; // reads as zeros
-                }
-                if (!wait(SB_EMPTY + st, phase ^ 1u)) return false;
-                if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
-                    uint8_t *dst = sm + p.q_bytes + st * C::SLOT;
-                    if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + st, C::SLOT);
-                    __syncwarp();
-                    if (lane < nbox) {
-#pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tma_load_4d(dst + c * CHUNK + lane * h * 128, kv ? &vmap : &kmap,
-                                        bar + SB_FULL + st, c * 64, it.kvh, at, blk, pol);
-                    }
-                    ++n;
-                }
-                if (++st == nst) {
-                    st = 0;
-                    phase ^= 1u;
-                }
+            const bool ahead = it.row_tiles() == 1;
+            At at = locate(it, 0);
+            copy(&kmap, it, at, pol);
+#pragma unroll 1
+            for (int i = 1; ok && i < it.tiles; ++i) {
+                const At after = locate(it, i);
+                copy(ahead ? &kmap : &vmap, it, ahead ? after : at, pol);
+                copy(ahead ? &vmap : &kmap, it, ahead ? at : after, pol);
+                at = after;
             }
-            return true;
+            copy(&vmap, it, at, pol);
         };
         // items: every other round of them from the last CTA to the first
         int passed = 0; // items put in the queue
@@ -510,12 +517,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             return true;
         };
         const int g = gridDim.x;
+        auto nth = [&](int round) { // this CTA's item of a round
+            const int idx = round * g + (round & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+            return round * (int64_t)g < p.n_items && idx < p.n_items ? idx : -1;
+        };
         Item it;
-        for (int r = 0, at = 0; ok && at < p.n_items; ++r, at += g) {
-            const int idx = at + (r & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
-            if (idx >= p.n_items) continue;
+        // (a round without an item for this CTA is the last one)
+        for (int r = 0, idx = nth(0); ok && idx >= 0; ++r) {
+            const int then = nth(r + 1);
             get_item<T>(p, idx, it);
-            if (pass_on(it)) (void)copies(it);
+            it.last = then < 0;
+            if (pass_on(it)) copies(it);
+            idx = then;
         }
         it.tiles = -1;
         if (ok) (void)pass_on(it);
@@ -931,64 +944,82 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
                 const bool adds = parts > 1 && p.q_f32; // a score is the sum over a row's lanes
-                // what the scores become takes their place; a share of one granule also stays in
-                // registers until it is weights
-                const bool modified = adds || transform || !full, one = cols == C::G;
+                // what the scores become takes their place; up to 32 columns stay in registers until
+                // they are weights
+                const bool modified = adds || transform || !full, one = cols <= 32;
+                const bool wide = T == 128 || cols > 16; // 32 at a time
                 const bool back = modified && (!one || !full);
                 float tm = -INFINITY;
-                float x[C::G];
+                float x[32];
+                auto load = [&](int c) {
+                    tmem_ld16(ts + c, x);
+                    if (wide) tmem_ld16(ts + c + 16, x + 16);
+                    tmem_wait_ld();
+                };
+                // f(16 of x, their first column)
+                auto halves = [&](int c, auto &&f) {
+                    f(x, c);
+                    if (wide) f(x + 16, c + 16);
+                };
                 if (busy) {
 #pragma unroll 1
-                    for (int c = cb; c < cb + cols; c += C::G) {
+                    for (int c = cb; c < cb + cols; c += 32) {
+                        load(c);
+                        if (adds)
+                            halves(c, [&](float *y, int) {
 #pragma unroll
-                        for (int i = 0; i < C::G; i += 16) tmem_ld16(ts + c + i, x + i);
-                        tmem_wait_ld();
-                        if (adds) {
-#pragma unroll
-                            for (int i = 0; i < C::G; ++i) {
-                                x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
-                                if (TP == 3) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 8);
-                            }
-                        }
+                                for (int i = 0; i < 16; ++i) {
+                                    y[i] += __shfl_xor_sync(0xffffffffu, y[i], 16);
+                                    if (TP == 3) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 8);
+                                }
+                            });
                         if (transform || !full) {
                             // y, -infinity where the row sees nothing
-                            if (p.softcap == 0.f) {
+                            if (p.softcap == 0.f)
+                                halves(c, [&](float *y, int) {
 #pragma unroll
-                                for (int i = 0; i < C::G; ++i) x[i] *= sc.mult;
-                            } else if (precise) {
+                                    for (int i = 0; i < 16; ++i) y[i] *= sc.mult;
+                                });
+                            else if (precise)
+                                halves(c, [&](float *y, int) {
 #pragma unroll
-                                for (int i = 0; i < C::G; ++i)
-                                    x[i] = capped<true>(x[i] * sc.turn, sc.cap);
-                            } else {
+                                    for (int i = 0; i < 16; ++i)
+                                        y[i] = capped<true>(y[i] * sc.turn, sc.cap);
+                                });
+                            else
+                                halves(c, [&](float *y, int) {
 #pragma unroll
-                                for (int i = 0; i < C::G; ++i)
-                                    x[i] = capped<false>(x[i] * sc.turn, sc.cap);
-                            }
+                                    for (int i = 0; i < 16; ++i)
+                                        y[i] = capped<false>(y[i] * sc.turn, sc.cap);
+                                });
                             if (p.slopes) {
                                 const float d = (float)(pos - t0 - c);
+                                halves(0, [&](float *y, int e) {
 #pragma unroll
-                                for (int i = 0; i < C::G; ++i)
-                                    x[i] = fmaf(-sc.slope, fabsf(d - (float)i), x[i]);
+                                    for (int i = 0; i < 16; ++i)
+                                        y[i] = fmaf(-sc.slope, fabsf(d - (float)(e + i)), y[i]);
+                                });
                             }
                             if (!full) {
                                 const uint32_t see =
                                     range32(x0 - c, x1 - c) | range32(k0 - c, k1 - c);
+                                halves(0, [&](float *y, int e) {
 #pragma unroll
-                                for (int i = 0; i < C::G; ++i)
-                                    if (!((see >> i) & 1u)) x[i] = -INFINITY;
+                                    for (int i = 0; i < 16; ++i)
+                                        if (!((see >> (e + i)) & 1u)) y[i] = -INFINITY;
+                                });
                             }
                         }
-                        if (back) {
+                        if (back) halves(c, [&](float *y, int e) { tmem_st16(ts + e, y); });
+                        halves(c, [&](float *y, int) {
+                            float a = y[0], b2 = y[1];
 #pragma unroll
-                            for (int i = 0; i < C::G; i += 16) tmem_st16(ts + c + i, x + i);
-                        }
-                        float a = x[0], b2 = x[1];
-#pragma unroll
-                        for (int i = 2; i < C::G; i += 2) {
-                            a = fmaxf(a, x[i]);
-                            b2 = fmaxf(b2, x[i + 1]);
-                        }
-                        tm = fmaxf(tm, fmaxf(a, b2));
+                            for (int i = 2; i < 16; i += 2) {
+                                a = fmaxf(a, y[i]);
+                                b2 = fmaxf(b2, y[i + 1]);
+                            }
+                            tm = fmaxf(tm, fmaxf(a, b2));
+                        });
                     }
                     if (back) tmem_wait_st();
                     if (!transform && full) tm *= sc.mult;
@@ -1113,60 +1144,48 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (busy) {
                     float l4[4] = {};
 #pragma unroll 1
-                    for (int c = cb; c < cb + cols; c += C::G) {
-                        if (!one) {
-#pragma unroll
-                            for (int i = 0; i < C::G; i += 16) tmem_ld16(ts + c + i, x + i);
-                            tmem_wait_ld();
-                        }
-                        uint32_t first[C::G / 2], second[C::G / 2];
-#pragma unroll
-                        for (int i = 0; i < C::G; i += 2) {
-                            const float a = ex2(fmaf(x[i], mult, -ref));
-                            const float b2 = ex2(fmaf(x[i + 1], mult, -ref));
-                            l4[i & 3] += a;
-                            l4[(i + 1) & 3] += b2;
-                            first[i / 2] = Pair<DT>::pack(a, b2);
-                            const float2 y = Pair<DT>::unpack(first[i / 2]);
-                            x[i] = a - y.x;
-                            x[i + 1] = b2 - y.y;
-                            second[i / 2] = Pair<DT>::pack(x[i], x[i + 1]);
-                        }
-                        if (TP == 3) {
-                            uint32_t third[8];
+                    for (int c = cb; c < cb + cols; c += 32) {
+                        if (!one) load(c);
+                        halves(c, [&](float *y, int e) {
+                            uint32_t v[16]; // first terms, second terms
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float2 z = Pair<DT>::unpack(second[i / 2]);
-                                third[i / 2] = Pair<DT>::pack(x[i] - z.x, x[i + 1] - z.y);
-                                if (part >= 2) first[i / 2] = part == 2 ? third[i / 2] : 0u;
+                                const float a = ex2(fmaf(y[i], mult, -ref));
+                                const float b2 = ex2(fmaf(y[i + 1], mult, -ref));
+                                l4[i & 3] += a;
+                                l4[(i + 1) & 3] += b2;
+                                v[i / 2] = Pair<DT>::pack(a, b2);
+                                const float2 z = Pair<DT>::unpack(v[i / 2]);
+                                y[i] = a - z.x;
+                                y[i + 1] = b2 - z.y;
+                                v[8 + i / 2] = Pair<DT>::pack(y[i], y[i + 1]);
                             }
-                            if (!one_p) tmem_st8w(ts + T + c / 2, third);
-                        }
-                        if (one_p) {
+                            if (TP == 3) {
+                                uint32_t third[8];
 #pragma unroll
-                            for (int i = 0; i < C::G / 2; ++i)
-                                if (part == 1) first[i] = second[i];
-                            if (C::G == 32) tmem_st16w(ts + c / 2, first);
-                            else tmem_st8w(ts + c / 2, first);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < C::G; i += 16) {
-                                tmem_st8w(ts + c + i, first + i / 2);
-                                tmem_st8w(ts + c + i + 8, second + i / 2);
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float2 z = Pair<DT>::unpack(v[8 + i / 2]);
+                                    third[i / 2] = Pair<DT>::pack(y[i] - z.x, y[i + 1] - z.y);
+                                    if (part >= 2) v[i / 2] = part == 2 ? third[i / 2] : 0u;
+                                }
+                                if (!one_p) tmem_st8w(ts + T + e / 2, third);
                             }
-                        }
+                            if (one_p) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (part == 1) v[i] = v[8 + i];
+                                tmem_st8w(ts + e / 2, v);
+                            } else {
+                                tmem_st16w(ts + e, v);
+                            }
+                        });
                     }
                     if (shares > 1) { // the other shares' weights of these lanes
                         const uint32_t z[16] = {};
-                        const int each = one_p ? C::G / 2 : C::G;
+                        const int half = one_p ? 2 : 1; // columns of TMEM to 16 positions: 8 or 16
 #pragma unroll 1
-                        for (int c = 0; c < T; c += C::G) {
-                            if (c >= cb && c < cb + cols) continue;
-                            const int at = c / C::G * each;
-                            if (each >= 16) tmem_st16w(ts + at, z);
-                            else tmem_st8w(ts + at, z);
-                            if (each == 32) tmem_st16w(ts + at + 16, z);
-                        }
+                        for (int c = 0; c < T / half; c += 8)
+                            if (c * half < cb || c * half >= cb + cols) tmem_st8w(ts + c, z);
                     }
                     l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tmem_wait_st();
@@ -1247,7 +1266,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // swizzled so that lanes hit other banks
                 const int rows8 = (it.rows + 7) / 8 * 8;
                 int W = nc;
-                while ((joint ? 2 : 1) * copies * rows8 * W * 4 > p.q_bytes) W >>= 1;
+                // (a CTA's last item finds the ring empty)
+                const int room = p.q_bytes + (it.last ? nst * C::SLOT : 0);
+                while ((joint ? 2 : 1) * copies * rows8 * W * 4 > room) W >>= 1;
                 const int w4 = W / 4, lw = 31 - __clz(w4);
                 if (writes && w == 0) {
                     ms->row.factor[local] = factor;
