@@ -91,7 +91,7 @@ struct Item {
     int start, keep1;       // visible to every row: [start, keep1)
     int S;                  // the sequence's length
     int last;               // of its CTA
-    int pad;
+    int back;               // tiles from the last to the first
     __device__ __forceinline__ bool shared() const { return b < 0; }
     __device__ __forceinline__ int row_tiles() const { return rows > 128 ? 2 : 1; }
 };
@@ -147,7 +147,9 @@ template <int TP> __device__ __forceinline__ int shares_of_terms(int parts, int 
 template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
 {
     const int per_seq = p.q_len * (p.hq / p.hkv);
-    it.last = it.pad = 0;
+    it.last = 0;
+    // (a bias by distance favours the last positions: the references are set at once)
+    it.back = p.slopes != nullptr;
     if (idx < p.shared_items) {
         it.b = -1;
         const int u = idx / p.row_tiles;
@@ -202,7 +204,7 @@ template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p,
 
 template <int T> __device__ __forceinline__ int tile_at(const Item &it, int i)
 {
-    const int v = it.v0 + i;
+    const int v = it.v0 + (it.back ? it.tiles - 1 - i : i);
     return v < it.n1 ? it.a0 + v * T : it.w0 + (v - it.n1) * T;
 }
 
@@ -276,8 +278,13 @@ __device__ __forceinline__ void tmem_st8w(uint32_t taddr, const uint32_t *r)
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
 {
-    tmem_ld16(taddr, v);
-    tmem_ld16(taddr + 16, v + 16);
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // (volatile, in program order with the other TMEM accesses)
@@ -325,19 +332,6 @@ __device__ __forceinline__ uint32_t range32(int lo, int hi)
     return hi > lo ? (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo) : 0u;
 }
 
-// the x-th 16-bit term of a pair
-template <typename DT> __device__ __forceinline__ uint32_t term(float a, float b, int x)
-{
-    uint32_t v = Pair<DT>::pack(a, b);
-    for (int i = 0; i < x; ++i) {
-        const float2 y = Pair<DT>::unpack(v);
-        a -= y.x;
-        b -= y.y;
-        v = Pair<DT>::pack(a, b);
-    }
-    return v;
-}
-
 // the power of two at or below a, from its exponent's bits (subnormals, infinities: 1)
 __device__ __forceinline__ float pow2_of(float a)
 {
@@ -350,7 +344,7 @@ template <int D> __device__ __forceinline__ float row_max(const void *q, int64_t
 {
     const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + at);
     float a = 0.f;
-#pragma unroll 8
+#pragma unroll 32
     for (int i = 0; i < D / 4; ++i) {
         const float4 y = __ldg(src + i);
         a = fmaxf(a, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
@@ -748,45 +742,69 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int64_t q_at = (((int64_t)b * p.q_len + tk) * p.hq + h) * D; // of this row
             float row_scale = 1.f;
             if (C::QTM) {
-                // a lane's own row: the first term, or its part's, 32 columns at a time
-                if (p.q_f32 && !C::BF && busy) row_scale = pow2_of(row_max<D>(p.q, q_at));
-                const float down = 1.f / row_scale;
-                if (busy) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t v[16];
-                        if (!p.q_f32) {
-                            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                static_cast<const uint16_t *>(p.q) + q_at + c);
+                // each lane its own row: one term into TMEM, the second of an f32 q that is not
+                // packed into shared memory; half a row (128 columns) or more in flight
+                if (busy && !p.q_f32) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(p.q) + q_at);
+                    uint4 y[D / 8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 y = __ldg(src + i);
-                                v[4 * i] = y.x;
-                                v[4 * i + 1] = y.y;
-                                v[4 * i + 2] = y.z;
-                                v[4 * i + 3] = y.w;
-                            }
-                        } else {
-                            const float4 *src = reinterpret_cast<const float4 *>(
-                                static_cast<const float *>(p.q) + q_at + c);
+                    for (int i = 0; i < D / 8; ++i) y[i] = __ldg(src + i);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 y = __ldg(src + i);
-                                v[2 * i] = term<DT>(y.x * down, y.y * down, parts > 1 ? part : 0);
-                                v[2 * i + 1] = term<DT>(y.z * down, y.w * down, parts > 1 ? part : 0);
-                            }
-                        }
-                        tmem_st16w(tl + C::Q_COL + c / 2, v);
+                    for (int i = 0; i < D / 8; i += 4) {
+                        const uint32_t v[16] = {
+                            y[i].x,     y[i].y,     y[i].z,     y[i].w,     y[i + 1].x, y[i + 1].y,
+                            y[i + 1].z, y[i + 1].w, y[i + 2].x, y[i + 2].y, y[i + 2].z, y[i + 2].w,
+                            y[i + 3].x, y[i + 3].y, y[i + 3].z, y[i + 3].w};
+                        tmem_st16w(tl + C::Q_COL + i * 4, v);
                     }
                     tmem_wait_st();
+                } else if (busy) {
+                    if (!C::BF) row_scale = pow2_of(row_max<D>(p.q, q_at));
+                    const float down = 1.f / row_scale;
+                    const float4 *src = reinterpret_cast<const float4 *>(
+                        static_cast<const float *>(p.q) + q_at);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 128) {
+                        float4 y[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] = __ldg(src + c / 4 + i);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t v[16], second[16];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float f[4] = {y[i + k].x * down, y[i + k].y * down,
+                                                    y[i + k].z * down, y[i + k].w * down};
+#pragma unroll
+                                for (int e = 0; e < 4; e += 2) {
+                                    const uint32_t a = Pair<DT>::pack(f[e], f[e + 1]);
+                                    const float2 z = Pair<DT>::unpack(a);
+                                    const uint32_t a2 = Pair<DT>::pack(f[e] - z.x, f[e + 1] - z.y);
+                                    v[2 * k + e / 2] = parts > 1 && part == 1 ? a2 : a;
+                                    second[2 * k + e / 2] = a2;
+                                }
+                            }
+                            tmem_st16w(tl + C::Q_COL + c / 2 + i * 2, v);
+                            if (parts == 1) {
+                                const int col = c + 4 * i; // of the row, 32 of them
+                                const uint32_t at = sb + (col >> 6) * qch;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    sts_v4(at + swz(r, (col & 63) * 2 + 16 * k), second[4 * k],
+                                           second[4 * k + 1], second[4 * k + 2], second[4 * k + 3]);
+                            }
+                        }
+                    }
+                    tmem_wait_st();
+                    if (parts == 1) fence_proxy_async_smem();
                 }
                 tc_fence_before();
             }
-            // the other terms, or all, in shared memory
-            if (!C::QTM || (p.q_f32 && parts == 1)) {
+            if (!C::QTM) { // all terms in shared memory
                 // 8-column units, a half-warp's or a warp's to a row; four of a thread in flight
                 // (rows past the last eight give scores that nobody reads)
-                constexpr int U8 = D / 8, STEP = C::WARPS * 32, TM = C::QTM ? 1 : 0;
+                constexpr int U8 = D / 8, STEP = C::WARPS * 32;
                 const int units = (it.rows + 7) / 8 * 8 * U8;
                 const int j = threadIdx.x % U8; // (the step is a multiple of a row)
                 auto source = [&](int rr) { // element of q, or -1
@@ -876,7 +894,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     f[2 * k + 1] -= y.y;
                                     if (x >= p.q_terms) v[k] = 0u; // (four lanes, three terms)
                                 }
-                                if (x >= TM) put(u / U8, x - TM, v);
+                                put(u / U8, x, v);
                             }
                         }
                     }
@@ -952,21 +970,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 float tm = -INFINITY;
                 float x[32];
                 auto load = [&](int c) {
-                    tmem_ld16(ts + c, x);
-                    if (wide) tmem_ld16(ts + c + 16, x + 16);
+                    if (wide) tmem_ld32(ts + c, x);
+                    else tmem_ld16(ts + c, x);
                     tmem_wait_ld();
                 };
-                // f(16 of x, their first column)
+                // f(16 of x, their first column, which half)
                 auto halves = [&](int c, auto &&f) {
-                    f(x, c);
-                    if (wide) f(x + 16, c + 16);
+                    f(x, c, std::integral_constant<int, 0>());
+                    if (wide) f(x + 16, c + 16, std::integral_constant<int, 1>());
                 };
                 if (busy) {
 #pragma unroll 1
                     for (int c = cb; c < cb + cols; c += 32) {
                         load(c);
                         if (adds)
-                            halves(c, [&](float *y, int) {
+                            halves(c, [&](float *y, int, auto) {
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
                                     y[i] += __shfl_xor_sync(0xffffffffu, y[i], 16);
@@ -976,25 +994,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (transform || !full) {
                             // y, -infinity where the row sees nothing
                             if (p.softcap == 0.f)
-                                halves(c, [&](float *y, int) {
+                                halves(c, [&](float *y, int, auto) {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) y[i] *= sc.mult;
                                 });
                             else if (precise)
-                                halves(c, [&](float *y, int) {
+                                halves(c, [&](float *y, int, auto) {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i)
                                         y[i] = capped<true>(y[i] * sc.turn, sc.cap);
                                 });
                             else
-                                halves(c, [&](float *y, int) {
+                                halves(c, [&](float *y, int, auto) {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i)
                                         y[i] = capped<false>(y[i] * sc.turn, sc.cap);
                                 });
                             if (p.slopes) {
                                 const float d = (float)(pos - t0 - c);
-                                halves(0, [&](float *y, int e) {
+                                halves(0, [&](float *y, int e, auto) {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i)
                                         y[i] = fmaf(-sc.slope, fabsf(d - (float)(e + i)), y[i]);
@@ -1003,15 +1021,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             if (!full) {
                                 const uint32_t see =
                                     range32(x0 - c, x1 - c) | range32(k0 - c, k1 - c);
-                                halves(0, [&](float *y, int e) {
+                                halves(0, [&](float *y, int e, auto) {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i)
                                         if (!((see >> (e + i)) & 1u)) y[i] = -INFINITY;
                                 });
                             }
                         }
-                        if (back) halves(c, [&](float *y, int e) { tmem_st16(ts + e, y); });
-                        halves(c, [&](float *y, int) {
+                        if (back) halves(c, [&](float *y, int e, auto) { tmem_st16(ts + e, y); });
+                        halves(c, [&](float *y, int, auto) {
                             float a = y[0], b2 = y[1];
 #pragma unroll
                             for (int i = 2; i < 16; i += 2) {
@@ -1146,7 +1164,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
                     for (int c = cb; c < cb + cols; c += 32) {
                         if (!one) load(c);
-                        halves(c, [&](float *y, int e) {
+                        uint32_t words[16];
+                        halves(c, [&](float *y, int e, auto half) {
                             uint32_t v[16]; // first terms, second terms
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
@@ -1171,16 +1190,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 if (!one_p) tmem_st8w(ts + T + e / 2, third);
                             }
                             if (one_p) {
+                                uint32_t *to_w = words + 8 * half.value;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (part == 1) v[i] = v[8 + i];
-                                tmem_st8w(ts + e / 2, v);
+                                for (int i = 0; i < 8; ++i) to_w[i] = part == 1 ? v[8 + i] : v[i];
                             } else {
                                 tmem_st16w(ts + e, v);
                             }
                         });
+                        if (one_p && one) {
+                            // the lane's whole row: its share's weights, zeros for the others'
+#pragma unroll
+                            for (int k = 0; k < T / 32; ++k) {
+                                uint32_t v[16];
+                                if (wide) { // 32 positions
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) v[i] = share == k ? words[i] : 0u;
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        v[i] = share == 2 * k + i / 8 ? words[i & 7] : 0u;
+                                }
+                                tmem_st16w(ts + 16 * k, v);
+                            }
+                        } else if (one_p) {
+                            tmem_st16w(ts + c / 2, words);
+                        }
                     }
-                    if (shares > 1) { // the other shares' weights of these lanes
+                    if (shares > 1 && !(one_p && one)) { // zeros for the other shares' positions
                         const uint32_t z[16] = {};
                         const int half = one_p ? 2 : 1; // columns of TMEM to 16 positions: 8 or 16
 #pragma unroll 1
@@ -1315,10 +1351,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 if (!all_sync()) return false; // the place may be written again
             }
-            // the next item starts from zero
-            zero_o(to + c0, nc);
-            if (joint) zero_o(tl + (NWG - 1 - w) * D + c0, nc);
-            tmem_wait_st();
+            if (!it.last) { // the next item starts from zero
+                zero_o(to + c0, nc);
+                if (joint) zero_o(tl + (NWG - 1 - w) * D + c0, nc);
+                tmem_wait_st();
+            }
             tc_fence_before();
             arrive(SB_OFREE);
             n += 2 * it.tiles;

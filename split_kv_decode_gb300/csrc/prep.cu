@@ -20,14 +20,10 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
-#include "ptx.cuh"
 
 namespace skv {
 int set_error(int code, const char *phase, const char *msg); // api.cpp
 }
-
-using skv::griddep_launch_dependents;
-using skv::griddep_wait;
 
 namespace {
 
@@ -158,11 +154,6 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
     const int ca = halves ? sub * 4 : sub * 8, cb = halves ? p.pairs + sub * 4 : sub * 8 + 4;
     // a value row has its own columns
     const int va = sub * 8;
-
-    // Nothing is touched before the stream's last kernel has ended; the next one may set
-    // itself up from then on.
-    griddep_wait();
-    griddep_launch_dependents();
 
     Raw<ST> raw[kAhead] = {};
     auto fetch = [&](Raw<ST> &r, int h) {
@@ -375,10 +366,10 @@ extern "C" int decode_attn_rope_append(const da_prep_t *a, const da_rope_t *rope
     p.shares = (int)std::max<int64_t>(1, std::min<int64_t>(heads / 2, 1216 / groups));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)((groups * p.shares + kThreads / 32 - 1) / (kThreads / 32));
-    const cudaError_t e =
-        a->src_dtype == DA_F32   ? skv::launch_after(prep_kernel<float>, grid, kThreads, st, p)
-        : a->src_dtype == DA_F16 ? skv::launch_after(prep_kernel<__half>, grid, kThreads, st, p)
-                                 : skv::launch_after(prep_kernel<__nv_bfloat16>, grid, kThreads, st, p);
+    if (a->src_dtype == DA_F32) prep_kernel<float><<<grid, kThreads, 0, st>>>(p);
+    else if (a->src_dtype == DA_F16) prep_kernel<__half><<<grid, kThreads, 0, st>>>(p);
+    else prep_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "rope_append", cudaGetErrorString(e));
     return DA_OK;
 }
