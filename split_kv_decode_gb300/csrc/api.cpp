@@ -962,6 +962,7 @@ int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t
     p.tile_rows = x.g.tile_rows;
     p.slots = x.g.slots;
     p.q_bytes = x.g.q_bytes;
+    p.join_bytes = x.g.join_bytes;
     p.row_groups = x.row_groups;
     p.shared_len = sp->shared_len;
     p.shared_tiles = x.shared_tiles;

@@ -105,13 +105,12 @@ template <int NWG> struct alignas(16) Misc {
     int abort;
     uint32_t bad[2][4];       // rows of a unit's V tile that hold no numbers, by its S slot
     float2 state[NWG][128];   // (m, l) of a warpgroup's lanes
-    union {
-        float row_scale[128]; // of an f32 q beside an f16 cache (at most 128 rows then)
-        struct {              // in the epilogue, of rows that several lanes share:
-            float factor[64]; // what their sum is multiplied by,
-            uint32_t to[64];  // and the row that it goes to
-        } row;
-    };
+    struct {                  // in the epilogue, of rows that several lanes share:
+        float factor[64];     // what their sum is multiplied by,
+        uint32_t to[64];      // and the row that it goes to
+    } row;
+    // of an f32 q beside an f16 cache, 128 columns (at most 128 rows then), of every other item
+    float row_scale[2][NWG == 2 ? 128 : 1];
 };
 static_assert(sizeof(Misc<1>) <= scored_misc(256) && sizeof(Misc<2>) <= scored_misc(128), "misc");
 
@@ -142,6 +141,50 @@ template <int TP> __device__ __forceinline__ int shares_of_terms(int parts, int 
 {
     return TP == 2 && parts == 1 && reps > 1 ? 2 : 1;
 }
+
+// What a softmax thread holds of an item: a row of it, and a share of its columns.
+template <int T, int TP> struct Lane {
+    int nrt, parts, span, reps, copies, shares;
+    int rep, share, part;   // copy of the row tile, share of the columns, term of the weights
+    int local;              // row of the item
+    bool in_use, owner, busy; // (of its warp: in_use, busy)
+    bool one_p;             // a lane holds one term of the weights
+    int b, tk, h, own, S;   // sequence, token, head, the token's position, the sequence's length
+    int out_row;
+    __device__ __forceinline__ Lane(const ScoredParams &p, const Item &it, int w, int warp4, int lane)
+    {
+        nrt = it.row_tiles();
+        parts = parts_of<TP>(it.rows);
+        span = span_of(it.rows);
+        reps = reps_of(p, it.rows);
+        copies = reps * parts;
+        const int terms = shares_of_terms<TP>(parts, reps);
+        shares = reps / terms;
+        one_p = parts * terms > 1;
+        rep = warp4 * 32 / span;
+        in_use = rep < reps;
+        share = in_use ? rep % shares : 0;
+        part = parts > 1 ? lane / (32 / parts) : in_use ? rep / shares : 0;
+        local = nrt == 2     ? w * 128 + warp4 * 32 + lane
+                : parts == 1 ? warp4 * 32 + lane - rep * span
+                             : lane & (32 / parts - 1);
+        owner = in_use && local < it.rows;
+        busy = in_use && (local & ~31) < it.rows;
+        const int Gh = p.hq / p.hkv, per_seq = p.q_len * Gh;
+        int row = it.row0 + (owner ? local : 0);
+        b = it.b;
+        S = it.S;
+        if (it.shared()) {
+            b = row / per_seq;
+            row -= b * per_seq;
+            S = length_of(p, b);
+        }
+        tk = row / Gh;
+        h = it.kvh * Gh + row - tk * Gh;
+        own = S - p.q_len + tk;
+        out_row = tk * p.hq + h;
+    }
+};
 
 // The idx-th item.
 template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
@@ -365,7 +408,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
     const int nst = p.slots;
-    auto *ms = reinterpret_cast<Misc<NWG> *>(sm + p.q_bytes + nst * C::SLOT);
+    auto *ms = reinterpret_cast<Misc<NWG> *>(sm + p.q_bytes + nst * C::SLOT + p.join_bytes);
     uint64_t *bar = ms->bar;
     volatile int *abort_flag = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -682,65 +725,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_fence_before();
         arrive(SB_OFREE);
 
-        auto work = [&](const Item &it) {
-            // ---- this thread's row and its share of every tile's columns (see above)
-            const int nrt = it.row_tiles(), parts = parts_of<TP>(it.rows);
-            const int span = span_of(it.rows), reps = reps_of(p, it.rows), copies = reps * parts;
-            const int terms = shares_of_terms<TP>(parts, reps), shares = reps / terms;
-            const int rep = (warp & 3) * 32 / span;
-            const bool in_use = rep < reps;                    // (of this warp)
-            const int share = in_use ? rep % shares : 0;
-            // its term of the weights
-            const int part = parts > 1 ? lane / (32 / parts) : in_use ? rep / shares : 0;
-            const bool one_p = parts * terms > 1;              // (a lane holds one term)
-            const int cols = T / shares, cb = share * cols;
-            const int local = nrt == 2     ? w * 128 + r       // row of the item
-                              : parts == 1 ? r - rep * span
-                                           : lane & (32 / parts - 1);
-            const bool owner = in_use && local < it.rows;
-            const bool busy = in_use && (local & ~31) < it.rows;
+        // Q of an item with tiles, once the last one's scores are done with it; returns false after a
+        // timeout. scale: of this lane's row (256 columns, an f32 q beside an f16 cache)
+        auto load_q = [&](const Item &it, int nth, float &row_scale) {
+            const Lane<T, TP> me(p, it, w, warp & 3, lane);
+            const int parts = me.parts, part = me.part, reps = me.reps, span = me.span;
+            const bool busy = me.busy;
             const int per_seq = p.q_len * Gh;
-            int row = it.row0 + (owner ? local : 0), b = it.b, S = it.S;
-            if (it.shared()) {
-                b = row / per_seq;
-                row -= b * per_seq;
-                S = length_of(p, b);
-            }
-            const int q0 = it.S - p.q_len;         // of a sequence's own item: its first token
-            const int tk = row / Gh, h = it.kvh * Gh + row - tk * Gh;
-            const int own = S - p.q_len + tk;      // its position behind the shared ones
-            const bool dead = !owner || own < 0;   // no such token: it sees nothing
-            const int out_row = tk * p.hq + h;
-            const size_t slot = (size_t)p.slot[b] + it.split + (it.shared() ? 0 : p.shared_splits);
-            // its row of the output, or of the partials
-            const size_t dst_row = p.whole ? (size_t)b * p.rows + out_row : slot * p.rows + out_row;
-            auto write4 = [&](size_t row_at, int c, const float4 &f) {
-                if (!p.whole) {
-                    store4(p.acc + row_at * D + c, f);
-                    return;
-                }
-                const size_t at = row_at * D + c;
-                if (p.out_dtype == DA_F32) store4(static_cast<float *>(p.out) + at, f);
-                else if (p.out_dtype == DA_F16) store4(static_cast<__half *>(p.out) + at, f);
-                else store4(static_cast<__nv_bfloat16 *>(p.out) + at, f);
-            };
-            if (it.tiles == 0) { // nothing to see: a neutral partial
-                if (owner && rep == 0 && part == 0 && (nrt == 2 || w == 0)) {
-                    if (p.whole) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 4)
-                            write4(dst_row, c, make_float4(0.f, 0.f, 0.f, 0.f));
-                    } else {
-                        p.ml[dst_row] = make_float2(kNeutralM, 0.f);
-                    }
-                }
-                return true;
-            }
-
-            // ---- Q, once the last item's scores are done with it
-            if (items > 0 && !wait(SB_QFREE, (uint32_t)(items - 1) & 1u)) return false;
-            const int64_t q_at = (((int64_t)b * p.q_len + tk) * p.hq + h) * D; // of this row
-            float row_scale = 1.f;
+            if (nth > 0 && !wait(SB_QFREE, (uint32_t)(nth - 1) & 1u)) return false;
+            tc_fence_after();
+            const int64_t q_at = (((int64_t)me.b * p.q_len + me.tk) * p.hq + me.h) * D;
+            row_scale = 1.f;
             if (C::QTM) {
                 // each lane its own row: one term into TMEM, the second of an f32 q that is not
                 // packed into shared memory; half a row (128 columns) or more in flight
@@ -878,7 +873,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 for (int o = U8 / 2; o > 0; o >>= 1)
                                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
                                 const float up = pow2_of(a);
-                                if (j == 0) ms->row_scale[u / U8] = up;
+                                if (j == 0) ms->row_scale[nth & 1][u / U8] = up;
                                 const float down = 1.f / up;
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) f[k] *= down;
@@ -901,6 +896,50 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 fence_proxy_async_smem();
             }
+            arrive(SB_QFULL);
+            return true;
+        };
+        // An item without positions to see: neutral partials.
+        auto neutral = [&](const Item &it) {
+            const Lane<T, TP> me(p, it, w, warp & 3, lane);
+            if (!me.owner || me.rep || me.part || (me.nrt == 1 && w)) return;
+            const size_t slot = (size_t)p.slot[me.b] + it.split + (it.shared() ? 0 : p.shared_splits);
+            const size_t row = p.whole ? (size_t)me.b * p.rows + me.out_row : slot * p.rows + me.out_row;
+            if (!p.whole) {
+                p.ml[row] = make_float2(kNeutralM, 0.f);
+                return;
+            }
+            const int bytes = D * (p.out_dtype == DA_F32 ? 4 : 2);
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row * bytes);
+#pragma unroll 1
+            for (int i = 0; i < bytes / 16; ++i) out[i] = make_uint4(0, 0, 0, 0);
+        };
+        // The units and the epilogue of an item (of one without tiles: neither). before_join is called
+        // between them, once this warp's scores of the item are done with.
+        auto work = [&](const Item &it, float row_scale, auto &&before_join) {
+            const Lane<T, TP> me(p, it, w, warp & 3, lane);
+            const int nrt = me.nrt, parts = me.parts, part = me.part, span = me.span, reps = me.reps;
+            const int copies = me.copies, shares = me.shares, rep = me.rep, share = me.share;
+            const int local = me.local, b = me.b, h = me.h, own = me.own;
+            const bool owner = me.owner, busy = me.busy, one_p = me.one_p;
+            const int cols = T / shares, cb = share * cols;
+            const int q0 = it.S - p.q_len;         // of a sequence's own item: its first token
+            const bool dead = !owner || own < 0;   // no such token: it sees nothing
+            const size_t slot = (size_t)p.slot[b] + it.split + (it.shared() ? 0 : p.shared_splits);
+            // its row of the output, or of the partials
+            const size_t dst_row =
+                p.whole ? (size_t)b * p.rows + me.out_row : slot * p.rows + me.out_row;
+            auto write4 = [&](size_t row_at, int c, const float4 &f) {
+                if (!p.whole) {
+                    store4(p.acc + row_at * D + c, f);
+                    return;
+                }
+                const size_t at = row_at * D + c;
+                if (p.out_dtype == DA_F32) store4(static_cast<float *>(p.out) + at, f);
+                else if (p.out_dtype == DA_F16) store4(static_cast<__half *>(p.out) + at, f);
+                else store4(static_cast<__nv_bfloat16 *>(p.out) + at, f);
+            };
+
             if (TP == 3 && !one_p && reps > 1 && busy) {
                 // the third terms have columns of their own: zero but for this warp's share
                 const uint32_t z[16] = {};
@@ -909,7 +948,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         tmem_st16w(tl + C::S_COL + s * C::S_SLOT + T + c, z);
                 tmem_wait_st();
             }
-            arrive(SB_QFULL);
 
             // ---- what this row sees and how it scores
             Scorer sc;
@@ -936,8 +974,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 sph ^= 1u << s;
                 tc_fence_after();
                 if (mine == 0) { // (an f32 q's row scale is there once all of Q is)
-                    if (!C::QTM && !C::BF && p.q_f32) row_scale = ms->row_scale[owner ? local : 0];
-                    const float x = p.scale * row_scale;
+                    const float x = p.scale * (!C::QTM && !C::BF && p.q_f32
+                                                   ? ms->row_scale[items & 1][owner ? local : 0]
+                                                   : row_scale);
                     sc.mult = x * kLog2e;
                     sc.turn = p.softcap == 0.f ? 0.f : x / p.softcap;
                 }
@@ -1068,9 +1107,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
 
-                // ---- a tile that not all rows see in full: V rows that no row sees may hold
-                // anything (0 * NaN is NaN), and so may rows that some see
-                if (!full && !it.shared()) {
+                // A tile that not all rows see in full: V rows that no row sees may hold anything (0 * NaN
+                // is NaN), and so may rows that some see, which are looked for where there are
+                // several tokens; then this comes before the weights take the scores' place.
+                auto clean_v = [&]() {
                     // (the copies of a sequence's item: K0 K1 V0 K2 V1 ...)
                     const int f = n + min(2 * tile + 2, 2 * it.tiles - 1), st = f % nst;
                     if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
@@ -1154,7 +1194,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                     fence_proxy_async_smem();
-                }
+                    return true;
+                };
+                const bool edge = !full && !it.shared();
+                if (edge && p.q_len > 1 && !clean_v()) return false;
 
                 // ---- P: the weights, in terms, in the place of their scores. One term of 16
                 // positions takes 8 columns: those of a lane's one term lie side by side, of several
@@ -1226,11 +1269,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tmem_wait_st();
                 }
+                if (edge && p.q_len == 1 && !clean_v()) return false;
                 tc_fence_before();
                 arrive(SB_PFULL + s);
                 ++done;
                 ++mine;
             }
+
+            if (!before_join()) return false;
+            if (it.tiles == 0) return true;
 
             // ---- epilogue: a row's states, of the warpgroups that took tiles in turn and of the
             // copies of its lane, are joined
@@ -1268,62 +1315,63 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (writes && !p.whole && (!joint || w == 0))
                 p.ml[dst_row] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
                                 : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
-            // 32 columns of the lane, its warpgroups' joined
-            auto lane32 = [&](int c, float *o) {
-                tmem_ld32(to + c, o);
+            // 16 columns of the lane, its warpgroups' joined
+            auto lane16 = [&](int c, float *o) {
+                tmem_ld16(to + c, o);
                 if (joint) {
-                    float o2[32];
-                    tmem_ld32(tl + (NWG - 1 - w) * D + c, o2);
+                    float o2[16];
+                    tmem_ld16(tl + (NWG - 1 - w) * D + c, o2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = f_own * o[i] + f_other * o2[i];
+                    for (int i = 0; i < 16; ++i) o[i] = f_own * o[i] + f_other * o2[i];
                 } else {
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] *= f_own;
+                    for (int i = 0; i < 16; ++i) o[i] *= f_own;
                 }
             };
             if (copies == 1) {
 #pragma unroll 1
-                for (int c = c0; c < c0 + nc; c += 32) {
-                    float o[32];
-                    lane32(c, o);
+                for (int c = c0; c < c0 + nc; c += 16) {
+                    float o[16];
+                    lane16(c, o);
                     if (writes && (p.whole || l != 0.f)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = factor == 0.f ? 0.f : o[i] * factor;
+                        for (int i = 0; i < 16; ++i) o[i] = factor == 0.f ? 0.f : o[i] * factor;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
+                        for (int i = 0; i < 16; i += 4)
                             write4(dst_row, c + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
                     }
                 }
             } else {
-                // the copies' sums meet in the place of Q, whose MMAs are done: [warpgroup][copy]
-                // [row][W columns], as many columns at once as there is room for; 16-byte units
-                // swizzled so that lanes hit other banks
+                // the copies' sums meet in shared memory: [warpgroup][copy][row][W columns], as many
+                // columns at once as there is room for; 16-byte units swizzled so that lanes hit
+                // other banks
                 const int rows8 = (it.rows + 7) / 8 * 8;
                 int W = nc;
                 // (a CTA's last item finds the ring empty)
-                const int room = p.q_bytes + (it.last ? nst * C::SLOT : 0);
+                const int room = it.last ? nst * C::SLOT : p.join_bytes;
                 while ((joint ? 2 : 1) * copies * rows8 * W * 4 > room) W >>= 1;
                 const int w4 = W / 4, lw = 31 - __clz(w4);
                 if (writes && w == 0) {
                     ms->row.factor[local] = factor;
                     ms->row.to[local] = (uint32_t)dst_row;
                 }
-                float4 *xs = reinterpret_cast<float4 *>(sm) + (joint ? w * copies * rows8 * w4 : 0);
+                float4 *xs = reinterpret_cast<float4 *>(sm + p.q_bytes + (it.last ? 0 : nst * C::SLOT)) +
+                             (joint ? w * copies * rows8 * w4 : 0);
 #pragma unroll 1
                 for (int at = 0; at < nc; at += W) {
                     if (busy) {
                         const int copy = parts > 1 ? rep * parts + part : rep;
                         float4 *to_row = xs + (copy * rows8 + local) * w4;
 #pragma unroll 1
-                        for (int c = 0; c < W; c += 32) {
-                            float o[32];
-                            lane32(c0 + at + c, o);
+                        for (int c = 0; c < W; c += 16) {
+                            float o[16];
+                            lane16(c0 + at + c, o);
                             if (owner) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    to_row[(c / 4 + i) ^ (local & 7)] = make_float4(
+                                for (int i = 0; i < 4; ++i)
+                                    to_row[(c / 4 + i) ^ (local & 3)] = make_float4(
                                         o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                             }
                         }
@@ -1337,7 +1385,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (fac == 0.f && !p.whole) continue;
                         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (int k = 0; k < copies; ++k) {
-                            const float4 y = xs[(k * rows8 + rr) * w4 + (c ^ (rr & 7))];
+                            const float4 y = xs[(k * rows8 + rr) * w4 + (c ^ (rr & 3))];
                             sum.x += y.x;
                             sum.y += y.y;
                             sum.z += y.z;
@@ -1362,13 +1410,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ++items;
             return true;
         };
+        int taken = 0; // items from the queue
+        // The next item with tiles (or the end), its Q on the way; those without are dealt with.
+        auto next_item = [&](Item &it, int nth, float &row_scale) {
+            for (;;) {
+                const int q = taken & 1;
+                if (!wait(SB_ITEM + q, (uint32_t)(taken >> 1) & 1u)) return false;
+                it = ms->item[q];
+                arrive(SB_TAKEN + q);
+                ++taken;
+                if (it.tiles < 0) return true;
+                if (it.tiles > 0) return load_q(it, nth, row_scale);
+                neutral(it);
+            }
+        };
+        Item it = {};   // (before the first: an item without tiles, of one row)
+        it.rows = 1;
+        float row_scale = 1.f;
 #pragma unroll 1
-        for (int i = 0;; ++i) {
-            const int q = i & 1;
-            if (!wait(SB_ITEM + q, (uint32_t)(i >> 1) & 1u)) break;
-            const Item it = ms->item[q];
-            arrive(SB_TAKEN + q);
-            if (it.tiles < 0 || !work(it)) break;
+        while (it.tiles >= 0) {
+            // the next item's Q goes out before this one's epilogue, so that its first scores are
+            // there when the epilogue is done
+            Item then;
+            float then_scale = 1.f;
+            if (!work(it, row_scale, [&]() {
+                    return next_item(then, items + (it.tiles > 0 ? 1 : 0), then_scale);
+                }))
+                break;
+            it = then;
+            row_scale = then_scale;
         }
         if (!ok && lane == 0) timed_out();
     }

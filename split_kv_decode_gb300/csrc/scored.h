@@ -24,17 +24,19 @@ constexpr int scored_terms(int kv_dtype, int out_dtype)
 constexpr int kScoredMaxSlots = 8;
 // barriers, exchange of (m, l), row scales (at 256 columns beside 128 rows of two terms and three
 // tiles of the ring)
-__host__ __device__ constexpr int scored_misc(int D) { return D == 128 ? 3328 : 2048; }
+__host__ __device__ constexpr int scored_misc(int D) { return D == 128 ? 4096 : 2048; }
 constexpr int kScoredSmemMax = 232448;
 
 // Shared memory: the terms of Q that TMEM does not hold, [row tile][term][64-column chunk][rpad rows
-// of 128 bytes], then a ring of K and V tiles, then the rest.
+// of 128 bytes], then a ring of K and V tiles, then the place where the copies of an item's rows are
+// joined, then the rest.
 struct ScoredGeometry {
     int q_terms;   // 1: q is of the cache's type
     int tile_rows; // query rows of an item, at most (256: two row tiles that share K and V tiles)
     int rpad;      // rows of a Q chunk
     int q_bytes;
     int slots;     // of the ring
+    int join_bytes;
     int smem;
 };
 
@@ -49,10 +51,8 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
     const int slot = scored_tile(D, p_terms) * D * 2;
     const int64_t most = shared_rows > own_rows ? shared_rows : own_rows;
     g.q_terms = q_terms;
-    // terms in shared memory, and the least that the join of copies has to have
     const bool tm = scored_q_in_tmem(D, p_terms);
-    const int held = (most <= scored_packed(p_terms) ? 1 : q_terms) - (tm ? 1 : 0);
-    const int least = tm ? 32768 : 0;
+    const int held = (most <= scored_packed(p_terms) ? 1 : q_terms) - (tm ? 1 : 0); // in shared memory
     // (two row tiles only for a q of one term: with more terms the ring would be too short)
     for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
         const int rows = (int)(most < g.tile_rows ? most : g.tile_rows);
@@ -60,15 +60,20 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
         // shorter than a tile and a half takes smaller items
         for (g.rpad = 128;; g.rpad /= 2) {
             g.q_bytes = (rows > 128 ? 2 : 1) * held * g.rpad * D * 2;
-            if (g.q_bytes < least) g.q_bytes = least;
-            g.slots = (kScoredSmemMax - 1024 - scored_misc(D) - g.q_bytes) / slot;
+            // copies of up to 64 rows are joined at least 16 columns at a time
+            auto narrow = [&](int64_t all) { // has an item of up to 64 rows
+                const int64_t rest = all % g.tile_rows;
+                return all > 0 && (all <= 64 || g.tile_rows == 64 || (rest > 0 && rest <= 64));
+            };
+            g.join_bytes = narrow(own_rows) || narrow(shared_rows) ? scored_groups(D) * g.rpad * 64 : 0;
+            g.slots = (kScoredSmemMax - 1024 - scored_misc(D) - g.q_bytes - g.join_bytes) / slot;
             if (g.slots >= 4 || g.rpad / 2 < rows || g.rpad == 32) break;
         }
         if (g.slots >= 3 || g.tile_rows == 64) break;
     }
     if (g.slots > kScoredMaxSlots) g.slots = kScoredMaxSlots;
     // the 128-row MMA reads 128 rows from every Q chunk: past the last one, into the ring
-    g.smem = 1024 + g.q_bytes + g.slots * slot + scored_misc(D);
+    g.smem = 1024 + g.q_bytes + g.slots * slot + g.join_bytes + scored_misc(D);
     return g;
 }
 
@@ -105,7 +110,7 @@ struct ScoredParams {
     int32_t q_f32, q_terms, out_dtype, whole, flags;
     int32_t window, keep;
     int32_t max_blocks, block_size, oob_block, box_rows;
-    int32_t rpad, tile_rows, slots, q_bytes;
+    int32_t rpad, tile_rows, slots, q_bytes, join_bytes;
     int32_t row_groups;      // of a sequence's rows of one KV head
     // items of the shared positions: (split, KV head, row tile), the row tile fastest
     int32_t shared_len, shared_tiles, shared_chunk, shared_splits, row_tiles, shared_items;
