@@ -103,6 +103,7 @@ template <int NWG> struct alignas(16) Misc {
     uint64_t bar[SB_N];
     uint32_t tmem;
     int abort;
+    int started[2];           // a warpgroup's accumulator holds something before its first MMA
     uint32_t bad[2][4];       // rows of a unit's V tile that hold no numbers, by its S slot
     float2 state[NWG][128];   // (m, l) of a warpgroup's lanes
     struct {                  // in the epilogue, of rows that several lanes share:
@@ -354,17 +355,27 @@ struct Scorer {
     float slope;     // slope log2 e
 };
 
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // c tanh z. 16-bit outputs: tanh z = 1 - 2 / (1 + e^2z), off by a few 2^-23 of c. f32 outputs: for
 // |z| < 0.75, where that is far off relative to tanh z, Lambert's continued fraction to its fifth
-// term, z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4), off by less than 2^-26 there.
+// term, z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4), off by less than 2^-26 there, and
+// (e^2z - 1) / (e^2z + 1) beyond; both are one quotient. (Comparisons that keep a NaN.)
 template <bool PRECISE> __device__ __forceinline__ float capped(float z, float c)
 {
-    const float far = fmaf(-2.f * c, __fdividef(1.f, 1.f + ex2(z * (2.f * kLog2e))), c);
-    if (!PRECISE) return far;
-    const float zz = z * z;
-    const float near = c * z * __fdividef(fmaf(zz, zz + 105.f, 945.f),
-                                          fmaf(zz, fmaf(zz, 15.f, 420.f), 945.f));
-    return fabsf(z) < 0.75f ? near : far;
+    if (!PRECISE) return fmaf(-2.f * c, rcp(1.f + ex2(z * (2.f * kLog2e))), c);
+    z = z > 10.f ? 10.f : z;
+    z = z < -10.f ? -10.f : z;
+    const float t = ex2(z * (2.f * kLog2e)), zz = z * z;
+    const bool near = fabsf(z) < 0.75f;
+    const float num = near ? z * fmaf(zz, zz + 105.f, 945.f) : t - 1.f;
+    const float den = near ? fmaf(zz, fmaf(zz, 15.f, 420.f), 945.f) : t + 1.f;
+    return c * num * rcp(den);
 }
 
 // bits i of 0 .. 31 with lo <= i < hi
@@ -617,11 +628,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         tc_fence_after();
                         const uint64_t vd = smem_desc_sw128(ring + vs * C::SLOT, CHUNK, 1024);
                         const uint32_t a = tmem + C::S_COL + s * C::S_SLOT;
+                        const bool more = u >= (NWG == 2 ? 2 : 1) ||
+                                          *static_cast<volatile int *>(ms->started + w);
                         if (one_p) {
 #pragma unroll
                             for (int k = 0; k < T / 16; ++k)
                                 tc_mma_ts(tmem + w * D, a + 8 * k, vd + (uint64_t)((k * 2048) >> 4),
-                                          idesc_pv, 1u);
+                                          idesc_pv, k || more ? 1u : 0u);
                         } else {
 #pragma unroll 1
                             for (int x = 0; x < TP; ++x)
@@ -629,7 +642,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 for (int k = 0; k < T / 16; ++k)
                                     tc_mma_ts(tmem + w * D,
                                               x < 2 ? a + 16 * k + 8 * x : a + T + 8 * k,
-                                              vd + (uint64_t)((k * 2048) >> 4), idesc_pv, 1u);
+                                              vd + (uint64_t)((k * 2048) >> 4), idesc_pv,
+                                              x || k || more ? 1u : 0u);
                         }
                         if (sh == 0 || (u & 1)) tc_commit(bar + SB_EMPTY + vs);
                         tc_commit(bar + SB_PVDONE + w);
@@ -716,13 +730,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             arrive(SB_XCH);
             return wait(SB_XCH, joints++ & 1u);
         };
-        auto zero_o = [&](uint32_t addr, int cols) {
-            const float z[16] = {};
-            for (int c = 0; c < cols; c += 16) tmem_st16(addr + c, z);
-        };
-        zero_o(to, D);
-        tmem_wait_st();
-        tc_fence_before();
         arrive(SB_OFREE);
 
         // Q of an item with tiles, once the last one's scores are done with it; returns false after a
@@ -974,6 +981,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 sph ^= 1u << s;
                 tc_fence_after();
                 if (mine == 0) { // (an f32 q's row scale is there once all of Q is)
+                    if (r == 0) ms->started[w] = 0; // (before this warp's arrival, or a group_sync)
                     const float x = p.scale * (!C::QTM && !C::BF && p.q_f32
                                                    ? ms->row_scale[items & 1][owner ? local : 0]
                                                    : row_scale);
@@ -1089,7 +1097,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const float alpha = moves && m != -INFINITY ? ex2(m - to_m) : 1.f;
                     l *= alpha;
                     m = to_m;
-                    if (mine > 0) { // (before, O is zero)
+                    if (mine > 0) { // (before, there is no O)
                         if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
                         tc_fence_after();
 #pragma unroll 1
@@ -1120,6 +1128,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const int lo_any = max(p.window ? max(it.start, o0 - p.window + 1) : it.start, 0) - t0;
                     const int lo_all = max(p.window ? max(it.start, o1 - p.window + 1) : it.start, 0) - t0;
                     const int hi_any = it.S - t0, hi_all = o0 + 1 - t0;
+                    // (boxes of a paged cache past the end read as zeros)
+                    const int top = p.block_table
+                                        ? min(T, (max(hi_any, 0) + p.box_rows - 1) / p.box_rows * p.box_rows)
+                                        : T;
+                    const int low = min(max(lo_all, 0), T), high = max(min(hi_all, hi_any), low);
                     auto kept = [&](int c) { return c >= ka && c < kb; };
                     auto any = [&](int c) { return kept(c) || (c >= lo_any && c < hi_any); };
                     auto all = [&](int c) { return kept(c) || (c >= lo_all && c < hi_all); };
@@ -1129,10 +1142,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (r < 4) bad[r] = 0u;
                         if (!group_sync()) return false;
                     }
-                    // rows of D / 8 units; a thread's units are of one row each
+                    // rows 0 .. low - 1 and high .. top - 1, D / 8 units each
 #pragma unroll 1
-                    for (int i = r; i < T * (D / 8); i += 128) {
-                        const int c = i / (D / 8), j = i - c * (D / 8);
+                    for (int i = r; i < (low + max(top - high, 0)) * (D / 8); i += 128) {
+                        const int nth = i / (D / 8), j = i - nth * (D / 8);
+                        const int c = nth < low ? nth : nth - low + high;
                         const uint32_t at = vt + (j >> 3) * CHUNK + swz(c, (j & 7) * 16);
                         if (!any(c)) {
                             sts_v4(at, 0u, 0u, 0u, 0u);
@@ -1153,9 +1167,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (word[0] | word[1] | word[2] | word[3]) {
                             // (rare) such rows are added here, to the rows that see them, and
                             // leave the tile
-                            if (mine > 0 && !wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u))
-                                return false;
-                            tc_fence_after();
+                            if (mine > 0) {
+                                if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
+                                tc_fence_after();
+                            } else { // the accumulator starts here
+                                const float z[16] = {};
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) tmem_st16(to + c, z);
+                                tmem_wait_st();
+                                ms->started[w] = 1;
+                            }
 #pragma unroll 1
                             for (int c = 0; c < T; ++c) {
                                 if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
@@ -1291,19 +1312,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (!all_sync()) return false;
                 // (a sum that is no number takes part: only an empty state does not)
                 const int first = owner ? local : 0;
+                float2 y[8];
                 float mm = -INFINITY, ll = 0.f;
-                for (int k = 0; k < shares * NWG; ++k) {
-                    const float2 y = ms->state[k % NWG][first + k / NWG * span];
-                    if (y.y != 0.f) mm = fmaxf(mm, y.x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    y[k] = make_float2(-INFINITY, 0.f);
+                    if (k < shares * NWG) y[k] = ms->state[k % NWG][first + k / NWG * span];
                 }
-                for (int k = 0; k < shares * NWG; ++k) {
-                    const float2 y = ms->state[k % NWG][first + k / NWG * span];
-                    if (y.y != 0.f) ll += y.y * ex2(y.x - mm);
-                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (y[k].y != 0.f) mm = fmaxf(mm, y[k].x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (y[k].y != 0.f) ll += y[k].y * ex2(y[k].x - mm);
                 f_own = l == 0.f ? 0.f : ex2(m - mm);
                 if (joint) {
-                    const float2 y = ms->state[NWG - 1 - w][r];
-                    f_other = y.y == 0.f ? 0.f : ex2(y.x - mm);
+                    const float2 other = ms->state[NWG - 1 - w][r];
+                    f_other = other.y == 0.f ? 0.f : ex2(other.x - mm);
                 }
                 m = mm;
                 l = ll;
@@ -1322,8 +1347,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     float o2[16];
                     tmem_ld16(tl + (NWG - 1 - w) * D + c, o2);
                     tmem_wait_ld();
+                    // (an accumulator that no unit went to holds anything)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = f_own * o[i] + f_other * o2[i];
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = (f_own != 0.f ? f_own * o[i] : 0.f) +
+                               (f_other != 0.f ? f_other * o2[i] : 0.f);
                 } else {
                     tmem_wait_ld();
 #pragma unroll
@@ -1347,23 +1375,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // the copies' sums meet in shared memory: [warpgroup][copy][row][W columns], as many
                 // columns at once as there is room for; 16-byte units swizzled so that lanes hit
                 // other banks
-                const int rows8 = (it.rows + 7) / 8 * 8;
+                const int rows4 = (it.rows + 3) / 4 * 4;
                 int W = nc;
                 // (a CTA's last item finds the ring empty)
                 const int room = it.last ? nst * C::SLOT : p.join_bytes;
-                while ((joint ? 2 : 1) * copies * rows8 * W * 4 > room) W >>= 1;
+                while ((joint ? 2 : 1) * copies * rows4 * W * 4 > room) W >>= 1;
                 const int w4 = W / 4, lw = 31 - __clz(w4);
                 if (writes && w == 0) {
                     ms->row.factor[local] = factor;
                     ms->row.to[local] = (uint32_t)dst_row;
                 }
                 float4 *xs = reinterpret_cast<float4 *>(sm + p.q_bytes + (it.last ? 0 : nst * C::SLOT)) +
-                             (joint ? w * copies * rows8 * w4 : 0);
+                             (joint ? w * copies * rows4 * w4 : 0);
 #pragma unroll 1
                 for (int at = 0; at < nc; at += W) {
                     if (busy) {
                         const int copy = parts > 1 ? rep * parts + part : rep;
-                        float4 *to_row = xs + (copy * rows8 + local) * w4;
+                        float4 *to_row = xs + (copy * rows4 + local) * w4;
 #pragma unroll 1
                         for (int c = 0; c < W; c += 16) {
                             float o[16];
@@ -1385,7 +1413,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (fac == 0.f && !p.whole) continue;
                         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (int k = 0; k < copies; ++k) {
-                            const float4 y = xs[(k * rows8 + rr) * w4 + (c ^ (rr & 3))];
+                            const float4 y = xs[(k * rows4 + rr) * w4 + (c ^ (rr & 3))];
                             sum.x += y.x;
                             sum.y += y.y;
                             sum.z += y.z;
@@ -1398,11 +1426,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (at + W < nc && !group_sync()) return false;
                 }
                 if (!all_sync()) return false; // the place may be written again
-            }
-            if (!it.last) { // the next item starts from zero
-                zero_o(to + c0, nc);
-                if (joint) zero_o(tl + (NWG - 1 - w) * D + c0, nc);
-                tmem_wait_st();
             }
             tc_fence_before();
             arrive(SB_OFREE);
