@@ -1005,8 +1005,10 @@ int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t
     }
     if (rc) return rc;
     if (dev) p.dev_lens = dev->seq_lens;
-    const cudaError_t e = launch_gqa_scored(a->kv_dtype, a->head_dim, x.p_terms, split_grid(a, &pl),
-                                            x.g.smem, st, km, vm, p);
+    const auto launch = a->kv_dtype == DA_F16 ? launch_gqa_scored_f16
+                        : x.p_terms == 2      ? launch_gqa_scored_bf16
+                                              : launch_gqa_scored_bf16_f32;
+    const cudaError_t e = launch(a->head_dim, split_grid(a, &pl), x.g.smem, st, km, vm, p);
     if (e != cudaSuccess) return fail(DA_ELAUNCH, "split", "%s", cudaGetErrorString(e));
     return DA_OK;
 }

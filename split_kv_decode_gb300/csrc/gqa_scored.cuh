@@ -43,6 +43,7 @@
 // place; K and V tiles come through the ring in that order. Warpgroups that took tiles in turn have
 // two states a row, which the epilogue joins. Every wait is bounded: one that runs out sets the
 // status word, and all roles leave.
+#pragma once
 #include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,9 +55,10 @@
 namespace skv {
 namespace {
 
-template <typename DT_, int D_, int TP_> struct Cfg {
+template <typename DT_, int D_, int TP_, bool XF_> struct Cfg {
     using DT = DT_;
     static constexpr int D = D_, TP = TP_;
+    static constexpr bool XF = XF_; // scores are transformed before the maximum is taken
     static constexpr bool BF = std::is_same<DT, __nv_bfloat16>::value;
     static constexpr int T = scored_tile(D, TP);
     static constexpr int NWG = scored_groups(D);
@@ -256,6 +258,22 @@ template <int T> __device__ __forceinline__ int tile_at(const Item &it, int i)
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t byte)
 {
     return (row >> 3) * 1024 + (row & 7) * 128 + ((((byte >> 4) ^ row) & 7) << 4) + (byte & 15);
+}
+
+// Waits for a phase as mbar_wait_bounded does, but looks at the clock and the flag now and then
+// only (the loop is in many places, and has to be short).
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                           volatile int *abort)
+{
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 31u) continue;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (*abort || t - t0 > limit_ns) return false;
+    }
+    return true;
 }
 
 template <typename DT> struct Pair;
@@ -475,7 +493,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
             bool got = true;
-            if (lane == 0) got = mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
+            if (lane == 0) got = wait_phase(bar + b, parity, p.timeout_ns, abort_flag);
             ok = ok && __shfl_sync(0xffffffffu, got, 0);
             return ok;
         };
@@ -584,7 +602,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (!ok) timed_out();
             // nothing may be in flight when the CTA ends: the last copy into every slot
             for (int f = max(0, n - nst); f < n; ++f)
-                (void)mbar_wait_bounded(bar + SB_FULL + f % nst, (uint32_t)(f / nst) & 1u,
+                (void)wait_phase(bar + SB_FULL + f % nst, (uint32_t)(f / nst) & 1u,
                                         p.timeout_ns, &never);
         }
         __syncwarp();
@@ -596,7 +614,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             uint32_t pph = 0;      // phases of PFULL, by slot
             bool ok = true;
             auto wait = [&](int b, uint32_t parity) {
-                ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
+                ok = ok && wait_phase(bar + b, parity, p.timeout_ns, abort_flag);
                 return ok;
             };
             int st = 0;            // the next slot of the ring, and its phase
@@ -698,7 +716,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (!ok) timed_out();
             // no MMA may be in flight when TMEM is freed
             tc_commit(bar + SB_DRAIN);
-            (void)mbar_wait_bounded(bar + SB_DRAIN, 0, p.timeout_ns, &never);
+            (void)wait_phase(bar + SB_DRAIN, 0, p.timeout_ns, &never);
         }
         __syncwarp();
     } else {
@@ -713,8 +731,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         uint32_t groups = 0, joints = 0;      // uses of SB_GROUP and SB_XCH
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
-            ok = ok && mbar_wait_bounded(bar + b, parity, p.timeout_ns, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, wait_phase(bar + b, parity, p.timeout_ns, abort_flag));
             return ok;
         };
         auto arrive = [&](int b) {
@@ -963,8 +980,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             sc.cap = p.softcap * kLog2e;
             sc.mult = sc.turn = 0.f;
             const bool precise = p.out_dtype == DA_F32;
-            // warp-uniform: scores are transformed before the maximum is taken
-            const bool transform = p.softcap != 0.f || p.slopes || !(p.scale > 0.f);
             const int x_lo = p.window ? max(it.start, own - p.window + 1) : it.start;
             const int x_hi = dead ? 0 : own + 1;
 
@@ -998,7 +1013,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             (t0 + T - 1 <= o0 && (!p.window || t0 > o1 - p.window)));
                 }
                 int k0 = 0, k1 = 0, x0 = 0, x1 = T; // visible: [k0, k1) and [x0, x1)
-                if (!full) {
+                if (__builtin_expect(!full, 0)) {
                     if (it.shared()) {
                         x1 = min(T, it.end - t0);
                     } else {
@@ -1011,7 +1026,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const bool adds = parts > 1 && p.q_f32; // a score is the sum over a row's lanes
                 // what the scores become takes their place; up to 32 columns stay in registers until
                 // they are weights
-                const bool modified = adds || transform || !full, one = cols <= 32;
+                const bool modified = adds || C::XF || !full, one = cols <= 32;
                 const bool wide = T == 128 || cols > 16; // 32 at a time
                 const bool back = modified && (!one || !full);
                 float tm = -INFINITY;
@@ -1038,12 +1053,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     if (TP == 3) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 8);
                                 }
                             });
-                        if (transform || !full) {
+                        if (C::XF || !full) {
                             // y, -infinity where the row sees nothing
-                            if (p.softcap == 0.f)
+                            if (!C::XF || p.softcap == 0.f)
                                 halves(c, [&](float *y, int, auto) {
+                                    const float2 k = make_float2(sc.mult, sc.mult);
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) y[i] *= sc.mult;
+                                    for (int i = 0; i < 16; i += 2) {
+                                        const float2 z = __fmul2_rn(make_float2(y[i], y[i + 1]), k);
+                                        y[i] = z.x;
+                                        y[i + 1] = z.y;
+                                    }
                                 });
                             else if (precise)
                                 halves(c, [&](float *y, int, auto) {
@@ -1057,7 +1077,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     for (int i = 0; i < 16; ++i)
                                         y[i] = capped<false>(y[i] * sc.turn, sc.cap);
                                 });
-                            if (p.slopes) {
+                            if (C::XF && p.slopes) {
                                 const float d = (float)(pos - t0 - c);
                                 halves(0, [&](float *y, int e, auto) {
 #pragma unroll
@@ -1065,7 +1085,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                         y[i] = fmaf(-sc.slope, fabsf(d - (float)(e + i)), y[i]);
                                 });
                             }
-                            if (!full) {
+                            if (__builtin_expect(!full, 0)) {
                                 const uint32_t see =
                                     range32(x0 - c, x1 - c) | range32(k0 - c, k1 - c);
                                 halves(0, [&](float *y, int e, auto) {
@@ -1087,12 +1107,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         });
                     }
                     if (back) tmem_wait_st();
-                    if (!transform && full) tm *= sc.mult;
+                    if (!C::XF && full) tm *= sc.mult;
                 }
-                const float mult = transform || !full ? 1.f : sc.mult;
+                const float mult = C::XF || !full ? 1.f : sc.mult;
                 // ---- the reference moves where a weight would pass 2^LIM
                 const bool moves = owner && tm > m + C::LIM;
-                if (__any_sync(0xffffffffu, moves)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, moves), 0)) {
                     const float to_m = moves ? tm - C::OFF : m;
                     const float alpha = moves && m != -INFINITY ? ex2(m - to_m) : 1.f;
                     l *= alpha;
@@ -1217,14 +1237,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     fence_proxy_async_smem();
                     return true;
                 };
-                const bool edge = !full && !it.shared();
+                const bool edge = __builtin_expect(!full, 0) && !it.shared();
                 if (edge && p.q_len > 1 && !clean_v()) return false;
 
                 // ---- P: the weights, in terms, in the place of their scores. One term of 16
                 // positions takes 8 columns: those of a lane's one term lie side by side, of several
                 // 16 apart (16 k: the first term, 16 k + 8: the second, T + 8 k: the third)
                 if (busy) {
-                    float l4[4] = {};
+                    float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
+                    const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll 1
                     for (int c = cb; c < cb + cols; c += 32) {
                         if (!one) load(c);
@@ -1233,15 +1255,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             uint32_t v[16]; // first terms, second terms
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float a = ex2(fmaf(y[i], mult, -ref));
-                                const float b2 = ex2(fmaf(y[i + 1], mult, -ref));
-                                l4[i & 3] += a;
-                                l4[(i + 1) & 3] += b2;
-                                v[i / 2] = Pair<DT>::pack(a, b2);
-                                const float2 z = Pair<DT>::unpack(v[i / 2]);
-                                y[i] = a - z.x;
-                                y[i + 1] = b2 - z.y;
-                                v[8 + i / 2] = Pair<DT>::pack(y[i], y[i + 1]);
+                                const float2 e2 = __ffma2_rn(make_float2(y[i], y[i + 1]), mult2, ref2);
+                                const float2 a = make_float2(ex2(e2.x), ex2(e2.y));
+                                l2[i / 2 & 1] = __fadd2_rn(l2[i / 2 & 1], a);
+                                v[i / 2] = Pair<DT>::pack(a.x, a.y);
+                                const float2 z = __ffma2_rn(Pair<DT>::unpack(v[i / 2]), minus, a);
+                                y[i] = z.x;
+                                y[i + 1] = z.y;
+                                v[8 + i / 2] = Pair<DT>::pack(z.x, z.y);
                             }
                             if (TP == 3) {
                                 uint32_t third[8];
@@ -1287,7 +1308,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         for (int c = 0; c < T / half; c += 8)
                             if (c * half < cb || c * half >= cb + cols) tmem_st8w(ts + c, z);
                     }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
                     tmem_wait_st();
                 }
                 if (edge && p.q_len == 1 && !clean_v()) return false;
@@ -1486,20 +1507,16 @@ cudaError_t launch(int grid, int smem, cudaStream_t st, const CUtensorMap &km, c
 
 } // namespace
 
-cudaError_t launch_gqa_scored(int kv_dtype, int head_dim, int p_terms, int grid, int smem,
-                              cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
-                              const ScoredParams &p)
+template <typename DT, int TP>
+static cudaError_t launch_d(int head_dim, int grid, int smem, cudaStream_t st, const CUtensorMap &km,
+                            const CUtensorMap &vm, const ScoredParams &p)
 {
-    if (kv_dtype == DA_F16) {
-        if (head_dim == 128) return launch<Cfg<__half, 128, 2>>(grid, smem, st, km, vm, p);
-        return launch<Cfg<__half, 256, 2>>(grid, smem, st, km, vm, p);
-    }
-    if (p_terms == 2) {
-        if (head_dim == 128) return launch<Cfg<__nv_bfloat16, 128, 2>>(grid, smem, st, km, vm, p);
-        return launch<Cfg<__nv_bfloat16, 256, 2>>(grid, smem, st, km, vm, p);
-    }
-    if (head_dim == 128) return launch<Cfg<__nv_bfloat16, 128, 3>>(grid, smem, st, km, vm, p);
-    return launch<Cfg<__nv_bfloat16, 256, 3>>(grid, smem, st, km, vm, p);
+    const bool xf = p.softcap != 0.f || p.slopes || !(p.scale > 0.f);
+    if (head_dim == 128)
+        return xf ? launch<Cfg<DT, 128, TP, true>>(grid, smem, st, km, vm, p)
+                  : launch<Cfg<DT, 128, TP, false>>(grid, smem, st, km, vm, p);
+    return xf ? launch<Cfg<DT, 256, TP, true>>(grid, smem, st, km, vm, p)
+              : launch<Cfg<DT, 256, TP, false>>(grid, smem, st, km, vm, p);
 }
 
 } // namespace skv

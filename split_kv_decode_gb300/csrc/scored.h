@@ -123,9 +123,16 @@ struct ScoredParams {
     uint8_t seq[DA_MAX_BATCH];
 };
 
-cudaError_t launch_gqa_scored(int kv_dtype, int head_dim, int p_terms, int grid, int smem,
-                              cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
-                              const ScoredParams &p);
+// by the cache's type and the output's (f32 outputs of bf16 caches take three terms)
+cudaError_t launch_gqa_scored_f16(int head_dim, int grid, int smem, cudaStream_t st,
+                                  const CUtensorMap &km, const CUtensorMap &vm,
+                                  const ScoredParams &p);
+cudaError_t launch_gqa_scored_bf16(int head_dim, int grid, int smem, cudaStream_t st,
+                                   const CUtensorMap &km, const CUtensorMap &vm,
+                                   const ScoredParams &p);
+cudaError_t launch_gqa_scored_bf16_f32(int head_dim, int grid, int smem, cudaStream_t st,
+                                       const CUtensorMap &km, const CUtensorMap &vm,
+                                       const ScoredParams &p);
 
 // Planner (plan_scored.cpp, pure host code). Lengths in tiles.
 struct ScoredWork {
