@@ -145,6 +145,23 @@ template <int TP> __device__ __forceinline__ int shares_of_terms(int parts, int 
     return TP == 2 && parts == 1 && reps > 1 ? 2 : 1;
 }
 
+// Sequence, head and (own) position of a row of an item.
+__device__ __forceinline__ void row_of(const ScoredParams &p, const Item &it, int row, int &b, int &h,
+                                       int &own)
+{
+    const int Gh = p.hq / p.hkv, per_seq = p.q_len * Gh;
+    int rr = it.row0 + row, S = it.S;
+    b = it.b;
+    if (it.shared()) {
+        b = rr / per_seq;
+        rr -= b * per_seq;
+        S = length_of(p, b);
+    }
+    const int tk = rr / Gh;
+    h = it.kvh * Gh + rr - tk * Gh;
+    own = S - p.q_len + tk;
+}
+
 // What a softmax thread holds of an item: a row of it, and a share of its columns.
 template <int T, int TP> struct Lane {
     int nrt, parts, span, reps, copies, shares;
@@ -347,6 +364,86 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
                  : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The scores of few rows, spread over a warp: lanes 0 - 15 (or 16 - 31, of taddr) of 8 N columns.
+// Thread t gets row t / 4 (r[4 g], r[4 g + 1]) and row t / 4 + 8 (r[4 g + 2], r[4 g + 3]) of columns
+// 8 g + 2 (t % 4) and the one behind it.
+template <int N> __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float *v)
+{
+    static_assert(N == 2 || N == 4, "groups of 8 columns");
+    uint32_t r[4 * N];
+    if constexpr (N == 2) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                     "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,"
+                     "%11,%12,%13,%14,%15}, [%16];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                     "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                     "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                     : "r"(taddr));
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N> __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const float *v)
+{
+    static_assert(N == 2 || N == 4, "groups of 8 columns");
+    uint32_t r[4 * N];
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) r[i] = __float_as_uint(v[i]);
+    if constexpr (N == 2) {
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,"
+                     "%8};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7])
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,"
+                     "%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                     "r"(r[13]), "r"(r[14]), "r"(r[15])
+                     : "memory");
+    }
+}
+// 16-bit pairs of the same rows and positions: 4 N columns, thread t's word of group g is column
+// 4 g + t % 4 of row t / 4 (r[2 g]) and of row t / 4 + 8 (r[2 g + 1]).
+template <int N> __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t *r)
+{
+    static_assert(N == 2 || N == 4 || N == 8 || N == 16, "groups of 4 columns");
+    if constexpr (N == 2) {
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                     : "memory");
+    } else if constexpr (N == 4) {
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,"
+                     "%8};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7])
+                     : "memory");
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,"
+                     "%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                     "r"(r[13]), "r"(r[14]), "r"(r[15])
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,"
+                     "%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+                     "%28,%29,%30,%31,%32};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                     "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+                     "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                     "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+                     "r"(r[31])
+                     : "memory");
+    }
 }
 
 // (volatile, in program order with the other TMEM accesses)
@@ -973,19 +1070,46 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tmem_wait_st();
             }
 
-            // ---- what this row sees and how it scores
-            Scorer sc;
-            const int pos = own + (it.shared() ? p.shared_len : 0); // in this item's positions
-            sc.slope = p.slopes && owner ? __ldg(p.slopes + h) * kLog2e : 0.f;
-            sc.cap = p.softcap * kLog2e;
-            sc.mult = sc.turn = 0.f;
+            // ---- what rows see and how they score: of unpacked items this lane's row (the first of
+            // two), of packed ones rows lane / 4 and lane / 4 + 8, four lanes to a row
+            const bool packed = parts > 1;
+            constexpr int PR = TP == 2 ? 2 : 1; // rows of a thread in packed items
+            struct Row {
+                bool real;
+                int pos, x_lo, x_hi;
+                Scorer sc;
+                float m, l;
+            } rows[PR];
             const bool precise = p.out_dtype == DA_F32;
-            const int x_lo = p.window ? max(it.start, own - p.window + 1) : it.start;
-            const int x_hi = dead ? 0 : own + 1;
+#pragma unroll
+            for (int k = 0; k < PR; ++k) {
+                Row &y = rows[k];
+                int rr = local, rb = b, rh = h, at = own;
+                y.real = owner;
+                if (packed) {
+                    rr = (lane >> 2) + 8 * k;
+                    y.real = me.in_use && rr < it.rows;
+                    row_of(p, it, y.real ? rr : 0, rb, rh, at);
+                }
+                y.pos = at + (it.shared() ? p.shared_len : 0); // in this item's positions
+                y.x_lo = p.window ? max(it.start, at - p.window + 1) : it.start;
+                y.x_hi = !y.real || at < 0 ? 0 : at + 1;
+                y.sc.slope = C::XF && p.slopes && y.real ? __ldg(p.slopes + rh) * kLog2e : 0.f;
+                y.sc.cap = p.softcap * kLog2e;
+                y.sc.mult = y.sc.turn = 0.f;
+                y.m = -INFINITY;
+                y.l = 0.f;
+            }
+            // a value of a packed item's row, for the lanes that hold a term of it
+            auto of_lane = [&](float first, float second) {
+                const int src = (local & 7) * 4;
+                const float x = __shfl_sync(0xffffffffu, first, src);
+                const float y = __shfl_sync(0xffffffffu, second, src);
+                return local >= 8 ? y : x;
+            };
 
             // ---- units
             const int nu = it.tiles * nrt;
-            float m = -INFINITY, l = 0.f;
             int mine = 0; // units of this item so far
 #pragma unroll 1
             for (int u = NWG == 2 ? w : 0; u < nu; u += NWG) {
@@ -997,14 +1121,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_fence_after();
                 if (mine == 0) { // (an f32 q's row scale is there once all of Q is)
                     if (r == 0) ms->started[w] = 0; // (before this warp's arrival, or a group_sync)
-                    const float x = p.scale * (!C::QTM && !C::BF && p.q_f32
-                                                   ? ms->row_scale[items & 1][owner ? local : 0]
-                                                   : row_scale);
-                    sc.mult = x * kLog2e;
-                    sc.turn = p.softcap == 0.f ? 0.f : x / p.softcap;
+#pragma unroll
+                    for (int k = 0; k < PR; ++k) {
+                        Row &y = rows[k];
+                        const int rr = packed ? (lane >> 2) + 8 * k : local;
+                        float scale = row_scale;
+                        if (packed) scale = __shfl_sync(0xffffffffu, row_scale, rr);
+                        if (!C::QTM && !C::BF && p.q_f32)
+                            scale = ms->row_scale[items & 1][y.real ? rr : 0];
+                        scale *= p.scale;
+                        y.sc.mult = scale * kLog2e;
+                        y.sc.turn = p.softcap == 0.f ? 0.f : scale / p.softcap;
+                    }
                 }
 
-                // which columns are visible: all, all below a border, or row by row
+                // does every row see all columns?
                 bool full = t0 + T <= it.end;
                 if (!it.shared()) {
                     const int o0 = max(q0, 0), o1 = it.S - 1;
@@ -1012,24 +1143,78 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                            (t0 + T <= it.keep1 ||
                             (t0 + T - 1 <= o0 && (!p.window || t0 > o1 - p.window)));
                 }
-                int k0 = 0, k1 = 0, x0 = 0, x1 = T; // visible: [k0, k1) and [x0, x1)
-                if (__builtin_expect(!full, 0)) {
-                    if (it.shared()) {
-                        x1 = min(T, it.end - t0);
+                // otherwise a row sees columns [k0, k1) and [x0, x1)
+                const int k0 = max(it.start - t0, 0), k1 = min(it.keep1 - t0, T);
+                auto x0_of = [&](const Row &y) { return it.shared() ? 0 : max(y.x_lo - t0, 0); };
+                auto x1_of = [&](const Row &y) {
+                    return min((it.shared() ? it.end : y.x_hi) - t0, T);
+                };
+                auto k1_of = [&](const Row &y) { return y.x_hi > 0 && !it.shared() ? k1 : 0; };
+                // y of N scores of a row (c: their first columns less each one's own)
+                auto transform = [&](const Row &y, float *x, auto count, auto &&col) {
+                    constexpr int N = decltype(count)::value;
+                    if (!C::XF || p.softcap == 0.f) {
+                        const float2 k = make_float2(y.sc.mult, y.sc.mult);
+#pragma unroll
+                        for (int i = 0; i < N; i += 2) {
+                            const float2 z = __fmul2_rn(make_float2(x[i], x[i + 1]), k);
+                            x[i] = z.x;
+                            x[i + 1] = z.y;
+                        }
+                    } else if (precise) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) x[i] = capped<true>(x[i] * y.sc.turn, y.sc.cap);
                     } else {
-                        k0 = max(it.start - t0, 0);
-                        k1 = dead ? 0 : min(it.keep1 - t0, T);
-                        x0 = max(x_lo - t0, 0);
-                        x1 = min(x_hi - t0, T);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) x[i] = capped<false>(x[i] * y.sc.turn, y.sc.cap);
                     }
-                }
-                const bool adds = parts > 1 && p.q_f32; // a score is the sum over a row's lanes
-                // what the scores become takes their place; up to 32 columns stay in registers until
-                // they are weights
-                const bool modified = adds || C::XF || !full, one = cols <= 32;
-                const bool wide = T == 128 || cols > 16; // 32 at a time
+                    if (C::XF && p.slopes) {
+                        const float d = (float)(y.pos - t0 - col(0));
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            x[i] = fmaf(-y.sc.slope, fabsf(d - (float)(col(i) - col(0))), x[i]);
+                    }
+                };
+                const float2 minus = make_float2(-1.f, -1.f);
+                bool moves = false;
+                float alpha = 1.f; // of this lane's row
+                // where a row's reference goes when its largest score of the tile is tm: it moves
+                // when a weight would pass 2^LIM
+                auto refer = [&](Row &y, float tm) {
+                    const bool on = y.real && tm > y.m + C::LIM;
+                    moves = moves || on;
+                    const float to_m = on ? tm - C::OFF : y.m;
+                    const float f = on && y.m != -INFINITY ? ex2(y.m - to_m) : 1.f;
+                    y.l *= f;
+                    y.m = to_m;
+                    return f;
+                };
+                const bool adds = packed && p.q_f32; // a score is the sum of its terms'
+                const bool modified = adds || C::XF || !full, one = shares == 4;
                 const bool back = modified && (!one || !full);
-                float tm = -INFINITY;
+                // packed: G columns of a warp at a time, 2 of every 8 a thread
+                constexpr int NG = T / 32, G = 8 * NG;
+                constexpr bool ROWS = T == 64; // weights of whole rows at once (registers)
+                float pk[PR][2 * NG];
+                auto load_packed = [&](int c, bool sums) {
+                    float v[4 * NG], v2[4 * NG];
+                    tmem_ld_rows<NG>(ts + c, v);
+                    if (sums) tmem_ld_rows<NG>(ts + (16u << 16) + c, v2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float y = v[4 * g + e];
+                            if (sums) y += v2[4 * g + e] + (TP == 3 ? v[4 * g + 2 + e] : 0.f);
+                            pk[0][2 * g + e] = y;
+                            if (PR == 2)
+                                pk[PR - 1][2 * g + e] =
+                                    v[4 * g + 2 + e] + (sums ? v2[4 * g + 2 + e] : 0.f);
+                        }
+                };
+                // unpacked: 32 columns of this lane's row, or 16
+                const bool wide = T == 128 || cols > 16; // 32 at a time
                 float x[32];
                 auto load = [&](int c) {
                     if (wide) tmem_ld32(ts + c, x);
@@ -1041,61 +1226,79 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     f(x, c, std::integral_constant<int, 0>());
                     if (wide) f(x + 16, c + 16, std::integral_constant<int, 1>());
                 };
-                if (busy) {
+                if (packed && busy) {
+                    float tm[PR];
+#pragma unroll
+                    for (int k = 0; k < PR; ++k) tm[k] = -INFINITY;
+#pragma unroll 1
+                    for (int c = cb; c < cb + cols; c += G) {
+                        load_packed(c, adds);
+                        const int c2 = c + 2 * (lane & 3);
+#pragma unroll
+                        for (int k = 0; k < PR; ++k) {
+                            if (k == 1 && it.rows <= 8) continue;
+                            if (C::XF || !full) {
+                                transform(rows[k], pk[k], std::integral_constant<int, 2 * NG>(),
+                                          [&](int i) { return c2 + 8 * (i >> 1) + (i & 1); });
+                                if (__builtin_expect(!full, 0)) {
+                                    const uint32_t see =
+                                        range32(x0_of(rows[k]) - c, x1_of(rows[k]) - c) |
+                                        range32(k0 - c, k1_of(rows[k]) - c);
+#pragma unroll
+                                    for (int i = 0; i < 2 * NG; ++i)
+                                        if (!((see >> (c2 - c + 8 * (i >> 1) + (i & 1))) & 1u))
+                                            pk[k][i] = -INFINITY;
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2 * NG; ++i) tm[k] = fmaxf(tm[k], pk[k][i]);
+                        }
+                        if (back) {
+                            float v[4 * NG];
+#pragma unroll
+                            for (int i = 0; i < 4 * NG; ++i)
+                                v[i] = pk[PR == 2 && (i & 2) ? 1 : 0][(i >> 2) * 2 + (i & 1)];
+                            tmem_st_rows<NG>(ts + c, v);
+                        }
+                    }
+                    if (back) tmem_wait_st();
+                    float f[PR];
+#pragma unroll
+                    for (int k = 0; k < PR; ++k) {
+                        float y = tm[k];
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                        if (!C::XF && full) y *= rows[k].sc.mult;
+                        f[k] = refer(rows[k], y);
+                    }
+                    if (__any_sync(0xffffffffu, moves)) {
+                        moves = true;
+                        alpha = of_lane(f[0], f[PR - 1]);
+                    }
+                } else if (busy) {
+                    const bool back32 = modified && (cols > 32 || !full);
+                    float tm = -INFINITY;
 #pragma unroll 1
                     for (int c = cb; c < cb + cols; c += 32) {
                         load(c);
-                        if (adds)
-                            halves(c, [&](float *y, int, auto) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    y[i] += __shfl_xor_sync(0xffffffffu, y[i], 16);
-                                    if (TP == 3) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 8);
-                                }
-                            });
                         if (C::XF || !full) {
                             // y, -infinity where the row sees nothing
-                            if (!C::XF || p.softcap == 0.f)
-                                halves(c, [&](float *y, int, auto) {
-                                    const float2 k = make_float2(sc.mult, sc.mult);
-#pragma unroll
-                                    for (int i = 0; i < 16; i += 2) {
-                                        const float2 z = __fmul2_rn(make_float2(y[i], y[i + 1]), k);
-                                        y[i] = z.x;
-                                        y[i + 1] = z.y;
-                                    }
-                                });
-                            else if (precise)
-                                halves(c, [&](float *y, int, auto) {
+                            const uint32_t see =
+                                full ? 0u
+                                     : range32(x0_of(rows[0]) - c, x1_of(rows[0]) - c) |
+                                           range32(k0 - c, k1_of(rows[0]) - c);
+                            halves(c, [&](float *y, int e, auto) {
+                                transform(rows[0], y, std::integral_constant<int, 16>(),
+                                          [&](int i) { return e + i; });
+                                if (__builtin_expect(!full, 0)) {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i)
-                                        y[i] = capped<true>(y[i] * sc.turn, sc.cap);
-                                });
-                            else
-                                halves(c, [&](float *y, int, auto) {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        y[i] = capped<false>(y[i] * sc.turn, sc.cap);
-                                });
-                            if (C::XF && p.slopes) {
-                                const float d = (float)(pos - t0 - c);
-                                halves(0, [&](float *y, int e, auto) {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        y[i] = fmaf(-sc.slope, fabsf(d - (float)(e + i)), y[i]);
-                                });
-                            }
-                            if (__builtin_expect(!full, 0)) {
-                                const uint32_t see =
-                                    range32(x0 - c, x1 - c) | range32(k0 - c, k1 - c);
-                                halves(0, [&](float *y, int e, auto) {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        if (!((see >> (e + i)) & 1u)) y[i] = -INFINITY;
-                                });
-                            }
+                                        if (!((see >> (e - c + i)) & 1u)) y[i] = -INFINITY;
+                                }
+                            });
                         }
-                        if (back) halves(c, [&](float *y, int e, auto) { tmem_st16(ts + e, y); });
+                        if (back32)
+                            halves(c, [&](float *y, int e, auto) { tmem_st16(ts + e, y); });
                         halves(c, [&](float *y, int, auto) {
                             float a = y[0], b2 = y[1];
 #pragma unroll
@@ -1106,34 +1309,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             tm = fmaxf(tm, fmaxf(a, b2));
                         });
                     }
-                    if (back) tmem_wait_st();
-                    if (!C::XF && full) tm *= sc.mult;
+                    if (back32) tmem_wait_st();
+                    if (!C::XF && full) tm *= rows[0].sc.mult;
+                    alpha = refer(rows[0], tm);
+                    moves = __any_sync(0xffffffffu, moves);
                 }
-                const float mult = C::XF || !full ? 1.f : sc.mult;
-                // ---- the reference moves where a weight would pass 2^LIM
-                const bool moves = owner && tm > m + C::LIM;
-                if (__builtin_expect(__any_sync(0xffffffffu, moves), 0)) {
-                    const float to_m = moves ? tm - C::OFF : m;
-                    const float alpha = moves && m != -INFINITY ? ex2(m - to_m) : 1.f;
-                    l *= alpha;
-                    m = to_m;
-                    if (mine > 0) { // (before, there is no O)
-                        if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
-                        tc_fence_after();
+                if (__builtin_expect(moves, 0) && mine > 0) { // (before, there is no O)
+                    if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(to + c, o);
-                            tmem_wait_ld();
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(to + c, o);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                            tmem_st16(to + c, o);
-                            tmem_st16(to + c + 16, o + 16);
-                        }
-                        tmem_wait_st();
+                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                        tmem_st16(to + c, o);
+                        tmem_st16(to + c + 16, o + 16);
                     }
+                    tmem_wait_st();
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
+                auto ref_of = [&](const Row &y) { return y.m == -INFINITY ? 0.f : y.m; };
 
                 // A tile that not all rows see in full: V rows that no row sees may hold anything (0 * NaN
                 // is NaN), and so may rows that some see, which are looked for where there are
@@ -1197,12 +1393,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 tmem_wait_st();
                                 ms->started[w] = 1;
                             }
+                            const float ref = packed ? of_lane(ref_of(rows[0]), ref_of(rows[PR - 1]))
+                                                     : ref_of(rows[0]);
+                            const int k1r = dead ? 0 : k1, x1r = dead ? 0 : min(own + 1 - t0, T);
+                            const int x0r =
+                                max((p.window ? max(it.start, own - p.window + 1) : it.start) - t0, 0);
 #pragma unroll 1
                             for (int c = 0; c < T; ++c) {
                                 if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
                                 const float y = tmem_ld1(ts + c);
                                 const bool sees = !dead && part == 0 && c >= cb && c < cb + cols &&
-                                                  ((c >= x0 && c < x1) || (c >= k0 && c < k1));
+                                                  ((c >= x0r && c < x1r) || (c >= k0 && c < k1r));
                                 const float pr = ex2(y - ref);
 #pragma unroll 1
                                 for (int j = 0; j < D / 16; ++j) {
@@ -1243,13 +1444,70 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // ---- P: the weights, in terms, in the place of their scores. One term of 16
                 // positions takes 8 columns: those of a lane's one term lie side by side, of several
                 // 16 apart (16 k: the first term, 16 k + 8: the second, T + 8 k: the third)
-                if (busy) {
+                if (packed && busy) {
+#pragma unroll 1
+                    for (int c = cb; c < cb + cols; c += G) {
+                        if (!one) load_packed(c, !modified && adds);
+                        // pairs of G positions: first, second and third terms
+                        uint32_t v[3][PR][NG];
+#pragma unroll
+                        for (int k = 0; k < PR; ++k) {
+                            const float mult = C::XF || !full ? 1.f : rows[k].sc.mult;
+                            const float2 mult2 = make_float2(mult, mult);
+                            const float2 ref2 = make_float2(-ref_of(rows[k]), -ref_of(rows[k]));
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                v[0][k][g] = v[1][k][g] = v[2][k][g] = 0u;
+                                if (k == 1 && it.rows <= 8) continue;
+                                const float2 e2 = __ffma2_rn(
+                                    make_float2(pk[k][2 * g], pk[k][2 * g + 1]), mult2, ref2);
+                                const float2 a = make_float2(ex2(e2.x), ex2(e2.y));
+                                rows[k].l += a.x + a.y;
+                                v[0][k][g] = Pair<DT>::pack(a.x, a.y);
+                                const float2 z = __ffma2_rn(Pair<DT>::unpack(v[0][k][g]), minus, a);
+                                v[1][k][g] = Pair<DT>::pack(z.x, z.y);
+                                if (TP == 3) {
+                                    const float2 y =
+                                        __ffma2_rn(Pair<DT>::unpack(v[1][k][g]), minus, z);
+                                    v[2][k][g] = Pair<DT>::pack(y.x, y.y);
+                                }
+                            }
+                        }
+                        // lanes 0 - 15 and 16 - 31: two terms of 16 rows, or three of 8 and none
+                        if (ROWS && one) {
+                            // whole rows: this share's weights, zeros for the others'
+                            uint32_t lo[4 * T / 16], hi[4 * T / 16];
+#pragma unroll
+                            for (int q = 0; q < T / 8; ++q) {
+                                const bool on = q / NG == share;
+                                lo[2 * q] = on ? v[0][0][q % NG] : 0u;
+                                lo[2 * q + 1] =
+                                    on ? (TP == 2 ? v[0][PR - 1][q % NG] : v[1][0][q % NG]) : 0u;
+                                hi[2 * q] = on ? (TP == 2 ? v[1][0][q % NG] : v[2][0][q % NG]) : 0u;
+                                hi[2 * q + 1] = on && TP == 2 ? v[1][PR - 1][q % NG] : 0u;
+                            }
+                            tmem_st_pairs<T / 8>(ts, lo);
+                            tmem_st_pairs<T / 8>(ts + (16u << 16), hi);
+                        } else {
+                            uint32_t lo[2 * NG], hi[2 * NG];
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                lo[2 * g] = v[0][0][g];
+                                lo[2 * g + 1] = TP == 2 ? v[0][PR - 1][g] : v[1][0][g];
+                                hi[2 * g] = TP == 2 ? v[1][0][g] : v[2][0][g];
+                                hi[2 * g + 1] = TP == 2 ? v[1][PR - 1][g] : 0u;
+                            }
+                            tmem_st_pairs<NG>(ts + c / 2, lo);
+                            tmem_st_pairs<NG>(ts + (16u << 16) + c / 2, hi);
+                        }
+                    }
+                } else if (busy) {
+                    const float mult = C::XF || !full ? 1.f : rows[0].sc.mult, ref = ref_of(rows[0]);
                     float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
-                    const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll 1
                     for (int c = cb; c < cb + cols; c += 32) {
-                        if (!one) load(c);
+                        if (cols > 32) load(c);
                         uint32_t words[16];
                         halves(c, [&](float *y, int e, auto half) {
                             uint32_t v[16]; // first terms, second terms
@@ -1270,11 +1528,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 for (int i = 0; i < 16; i += 2) {
                                     const float2 z = Pair<DT>::unpack(v[8 + i / 2]);
                                     third[i / 2] = Pair<DT>::pack(y[i] - z.x, y[i + 1] - z.y);
-                                    if (part >= 2) v[i / 2] = part == 2 ? third[i / 2] : 0u;
                                 }
-                                if (!one_p) tmem_st8w(ts + T + e / 2, third);
+                                tmem_st8w(ts + T + e / 2, third);
                             }
-                            if (one_p) {
+                            if (TP == 2 && one_p) {
                                 uint32_t *to_w = words + 8 * half.value;
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) to_w[i] = part == 1 ? v[8 + i] : v[i];
@@ -1282,33 +1539,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 tmem_st16w(ts + e, v);
                             }
                         });
-                        if (one_p && one) {
-                            // the lane's whole row: its share's weights, zeros for the others'
-#pragma unroll
-                            for (int k = 0; k < T / 32; ++k) {
-                                uint32_t v[16];
-                                if (wide) { // 32 positions
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) v[i] = share == k ? words[i] : 0u;
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        v[i] = share == 2 * k + i / 8 ? words[i & 7] : 0u;
-                                }
-                                tmem_st16w(ts + 16 * k, v);
+                        if (TP == 2 && one_p) {
+                            if (wide) {
+                                tmem_st16w(ts + c / 2, words);
+                            } else {
+                                tmem_st8w(ts + c / 2, words);
                             }
-                        } else if (one_p) {
-                            tmem_st16w(ts + c / 2, words);
                         }
                     }
-                    if (shares > 1 && !(one_p && one)) { // zeros for the other shares' positions
+                    rows[0].l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+                }
+                if (busy) {
+                    if (shares > 1 && !(ROWS && packed && one)) { // zeros for the other shares' positions
                         const uint32_t z[16] = {};
                         const int half = one_p ? 2 : 1; // columns of TMEM to 16 positions: 8 or 16
 #pragma unroll 1
-                        for (int c = 0; c < T / half; c += 8)
-                            if (c * half < cb || c * half >= cb + cols) tmem_st8w(ts + c, z);
+                        for (int c = 0; c < T / half; c += 16) {
+                            // (shares are 16 positions and more: 8 columns, or 16)
+                            const bool lo = c * half < cb || c * half >= cb + cols;
+                            const bool hi = (c + 8) * half < cb || (c + 8) * half >= cb + cols;
+                            if (lo && hi) {
+                                tmem_st16w(ts + c, z);
+                            } else {
+                                if (lo) tmem_st8w(ts + c, z);
+                                if (hi) tmem_st8w(ts + c + 8, z);
+                            }
+                        }
                     }
-                    l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
                     tmem_wait_st();
                 }
                 if (edge && p.q_len == 1 && !clean_v()) return false;
@@ -1320,6 +1577,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
             if (!before_join()) return false;
             if (it.tiles == 0) return true;
+            float m = rows[0].m, l = rows[0].l;
+            if (packed) {
+#pragma unroll
+                for (int k = 0; k < PR; ++k) {
+                    rows[k].l += __shfl_xor_sync(0xffffffffu, rows[k].l, 1);
+                    rows[k].l += __shfl_xor_sync(0xffffffffu, rows[k].l, 2);
+                }
+                m = of_lane(rows[0].m, rows[PR - 1].m);
+                l = of_lane(rows[0].l, rows[PR - 1].l);
+            }
 
             // ---- epilogue: a row's states, of the warpgroups that took tiles in turn and of the
             // copies of its lane, are joined
