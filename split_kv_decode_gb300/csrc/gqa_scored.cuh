@@ -35,12 +35,13 @@
 // 256 rows, row tiles) in turn; 256 columns leave TMEM for one. Many rows on shared
 // positions are bound by the MMAs.
 //
-// Roles: one or two softmax warpgroups, a TMA producer warp, a warp whose first lane issues the
-// MMAs. The producer also works the items out and passes them on through a queue. Unit u of an
+// Roles: one or two softmax warpgroups, a warp for the copies of K, one for those of V (pages of 16
+// positions are 16 boxes a tile, which take one warp 0.8 us to issue), a warp whose first lane issues
+// the MMAs. The K warp also works the items out and passes them on through a queue. Unit u of an
 // item is tile u, or tile u / 2 and row tile u % 2; it has S slot u % 2 and, with two warpgroups,
 // warpgroup and accumulator u % 2. The MMA order S0 S1 O0 S2 O1 S3 ... lets each unit's softmax
 // run beside the other's MMAs, and makes P of unit u - 2 read before S of unit u takes its
-// place; K and V tiles come through the ring in that order. Warpgroups that took tiles in turn have
+// place. Warpgroups that took tiles in turn have
 // two states a row, which the epilogue joins. Every wait is bounded: one that runs out sets the
 // status word, and all roles leave.
 #pragma once
@@ -65,8 +66,13 @@ template <typename DT_, int D_, int TP_, bool XF_> struct Cfg {
     static constexpr int NCH = D / 64;      // 64-column chunks of a row
     static constexpr int CHUNK = T * 128;   // bytes of a chunk of a tile
     static constexpr int SLOT = NCH * CHUNK;
-    static constexpr int WARPS = NWG * 4;   // softmax warps
-    static constexpr int THREADS = (WARPS + 2) * 32;
+    // softmax warps, then those of the K copies, the V copies and the MMAs, and one without work
+    static constexpr int WARPS = NWG * 4, K_WARP = WARPS, V_WARP = WARPS + 1, MMA_WARP = WARPS + 2;
+    static constexpr int THREADS = (WARPS + 4) * 32;
+    // registers (two softmax warpgroups: 168 a thread at launch, of which the last four warps
+    // leave some to the others: 8 * 200 + 4 * 104 = 12 * 168)
+    static constexpr bool SPLIT = NWG == 2;
+    static constexpr int SOFTMAX_REGS = 200, OTHER_REGS = 104;
     // TMEM columns: O of warpgroup w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
     static constexpr bool QTM = scored_q_in_tmem(D, TP);
     static constexpr int S_COL = 256, S_SLOT = QTM ? 64 : 128, Q_COL = 384;
@@ -446,6 +452,15 @@ template <int N> __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, c
     }
 }
 
+template <int N> __device__ __forceinline__ void setmaxnreg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void setmaxnreg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // (volatile, in program order with the other TMEM accesses)
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr)
 {
@@ -561,13 +576,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_init(bar + SB_DRAIN, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar + SB_ITEM + s, 1);
-            mbar_init(bar + SB_TAKEN + s, C::WARPS + 1);
+            mbar_init(bar + SB_TAKEN + s, C::WARPS + 2); // softmax warps, V copies, MMAs
         }
         ms->abort = 0;
         if (blockIdx.x == 0) *p.status = 0;
         fence_mbar_init();
     }
-    if (warp == C::WARPS + 1) tmem_alloc(&ms->tmem, 512);
+    if (warp == C::MMA_WARP) tmem_alloc(&ms->tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -577,16 +592,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         atomicCAS(p.status, 0, kStatusTimeoutScored);
     };
 
-    if (warp == C::WARPS) {
-        // =============================== TMA producer ===============================
-        if (lane == 0) {
-            tma_prefetch_map(&kmap);
-            tma_prefetch_map(&vmap);
+    // slots 0 .. nk - 1 of the ring are for K tiles, the others for V tiles (which are held longer)
+    const int nk = nst / 2;
+    // a walk through slots first .. last - 1 and the phases of their barriers
+    struct Ring {
+        int first, last, slot;
+        uint32_t phase;
+        __device__ __forceinline__ void advance()
+        {
+            if (++slot == last) {
+                slot = first;
+                phase ^= 1u;
+            }
         }
-        const uint64_t first = l2_evict_first_policy(), normal = l2_normal_policy();
+    };
+    int taken = 0; // items from the queue
+
+    if (warp == C::K_WARP || warp == C::V_WARP) {
+        // ============================ copies of K, or of V ============================
+        if constexpr (C::SPLIT) setmaxnreg_dec<C::OTHER_REGS>();
+        const bool is_v = warp == C::V_WARP;
+        const CUtensorMap *map = is_v ? &vmap : &kmap;
+        if (lane == 0) tma_prefetch_map(map);
+        const uint64_t once = l2_evict_first_policy(), normal = l2_normal_policy();
         const bool paged = p.block_table != nullptr;
-        int st = 0, n = 0; // slot, copies issued
-        uint32_t phase = 0;
+        Ring ring = {is_v ? nk : 0, is_v ? nst : nk, is_v ? nk : 0, 0u};
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
             bool got = true;
@@ -626,25 +656,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (pos >= it.end || blk < 0) blk = p.oob_block; // reads as zeros
             return At{blk, pos - e * bs};
         };
-        auto copy = [&](const CUtensorMap *map, const Item &it, const At &at, uint64_t pol) {
-            if (!wait(SB_EMPTY + st, phase ^ 1u)) return;
-            if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
-                uint8_t *dst = sm + p.q_bytes + st * C::SLOT;
-                if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + st, C::SLOT);
-                __syncwarp();
-                if (lane < nbox) {
-#pragma unroll
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_4d(dst + c * CHUNK + lane * h * 128, map, bar + SB_FULL + st, c * 64,
-                                    it.kvh, at.pos, at.blk, pol);
-                }
-                ++n;
-            }
-            if (++st == nst) {
-                st = 0;
-                phase ^= 1u;
-            }
-        };
         auto copies = [&](const Item &it) {
             if (it.tiles == 0) return;
             if (paged) {
@@ -653,58 +664,86 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 base = -1;
             }
             // shared tiles are read by every row tile's items
-            const uint64_t pol = it.shared() && p.row_tiles > 1 ? normal : first;
-            // the order in which the MMAs take them: K0 K1 V0 K2 V1 ..., or K0 V0 K1 V1 ...
-            const bool ahead = it.row_tiles() == 1;
+            const uint64_t pol = it.shared() && p.row_tiles > 1 ? normal : once;
             At at = locate(it, 0);
-            copy(&kmap, it, at, pol);
 #pragma unroll 1
-            for (int i = 1; ok && i < it.tiles; ++i) {
-                const At after = locate(it, i);
-                copy(ahead ? &kmap : &vmap, it, ahead ? after : at, pol);
-                copy(ahead ? &vmap : &kmap, it, ahead ? at : after, pol);
-                at = after;
+            for (int i = 0; i < it.tiles; ++i) {
+                if (!wait(SB_EMPTY + ring.slot, ring.phase ^ 1u)) return;
+                if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
+                    uint8_t *dst = sm + p.q_bytes + ring.slot * C::SLOT + lane * h * 128;
+                    if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + ring.slot, C::SLOT);
+                    __syncwarp();
+                    if (lane < nbox) {
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_4d(dst + c * CHUNK, map, bar + SB_FULL + ring.slot, c * 64,
+                                        it.kvh, at.pos, at.blk, pol);
+                    }
+                    __syncwarp();
+                }
+                ring.advance();
+                if (i + 1 < it.tiles) at = locate(it, i + 1);
             }
-            copy(&vmap, it, at, pol);
         };
-        // items: every other round of them from the last CTA to the first
-        int passed = 0; // items put in the queue
-        auto pass_on = [&](const Item &it) {
-            const int s = passed & 1;
-            if (!wait(SB_TAKEN + s, ((uint32_t)(passed >> 1) & 1u) ^ 1u)) return false;
-            if (lane == 0) {
-                ms->item[s] = it;
-                mbar_arrive(bar + SB_ITEM + s);
+        if (!is_v) {
+            // this warp works the items out: every other round from the last CTA to the first
+            int passed = 0; // items put in the queue
+            auto pass_on = [&](const Item &it) {
+                const int s = passed & 1;
+                if (!wait(SB_TAKEN + s, ((uint32_t)(passed >> 1) & 1u) ^ 1u)) return false;
+                if (lane == 0) {
+                    ms->item[s] = it;
+                    mbar_arrive(bar + SB_ITEM + s);
+                }
+                ++passed;
+                return true;
+            };
+            const int g = gridDim.x;
+            auto nth = [&](int round) { // this CTA's item of a round
+                const int idx = round * g + (round & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+                return round * (int64_t)g < p.n_items && idx < p.n_items ? idx : -1;
+            };
+            Item it;
+            // (a round without an item for this CTA is the last one)
+#pragma unroll 1
+            for (int r = 0, idx = nth(0); ok && idx >= 0; ++r) {
+                const int then = nth(r + 1);
+                get_item<T>(p, idx, it);
+                it.last = then < 0;
+                if (pass_on(it)) copies(it);
+                idx = then;
             }
-            ++passed;
-            return true;
-        };
-        const int g = gridDim.x;
-        auto nth = [&](int round) { // this CTA's item of a round
-            const int idx = round * g + (round & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
-            return round * (int64_t)g < p.n_items && idx < p.n_items ? idx : -1;
-        };
-        Item it;
-        // (a round without an item for this CTA is the last one)
-        for (int r = 0, idx = nth(0); ok && idx >= 0; ++r) {
-            const int then = nth(r + 1);
-            get_item<T>(p, idx, it);
-            it.last = then < 0;
-            if (pass_on(it)) copies(it);
-            idx = then;
+            it.tiles = -1;
+            if (ok) (void)pass_on(it);
+        } else {
+#pragma unroll 1
+            for (;; ++taken) {
+                const int q = taken & 1;
+                if (!wait(SB_ITEM + q, (uint32_t)(taken >> 1) & 1u)) break;
+                const Item it = ms->item[q];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + SB_TAKEN + q);
+                if (it.tiles < 0) break;
+                copies(it);
+                if (!ok) break;
+            }
         }
-        it.tiles = -1;
-        if (ok) (void)pass_on(it);
         if (lane == 0) {
             if (!ok) timed_out();
-            // nothing may be in flight when the CTA ends: the last copy into every slot
-            for (int f = max(0, n - nst); f < n; ++f)
-                (void)wait_phase(bar + SB_FULL + f % nst, (uint32_t)(f / nst) & 1u,
-                                        p.timeout_ns, &never);
+            // Nothing may be in flight when the CTA ends: the last copy into every slot, those of
+            // the current round up to this slot and the round's before behind it.
+            if (!(p.flags & DA_FLAG_TEST_NO_TMA))
+                for (int s = ring.first; s < ring.last; ++s) {
+                    const uint32_t ph = s < ring.slot ? ring.phase : ring.phase ^ 1u;
+                    // (a slot that has not been used is in its first phase: the one before it
+                    // counts as complete)
+                    (void)wait_phase(bar + SB_FULL + s, ph, p.timeout_ns, &never);
+                }
         }
         __syncwarp();
-    } else if (warp == C::WARPS + 1) {
+    } else if (warp == C::MMA_WARP) {
         // ============================ MMA issue (one thread) ============================
+        if constexpr (C::SPLIT) setmaxnreg_dec<C::OTHER_REGS>();
         if (lane == 0) {
             constexpr uint32_t idesc_qk = idesc_f16kind(128, T, 0, 0, C::BF);
             constexpr uint32_t idesc_pv = idesc_f16kind(128, D, 0, 1, C::BF);
@@ -714,15 +753,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 ok = ok && wait_phase(bar + b, parity, p.timeout_ns, abort_flag);
                 return ok;
             };
-            int st = 0;            // the next slot of the ring, and its phase
-            uint32_t ph = 0u;
-            auto take = [&](int &slot) { // waits for the next tile
-                slot = st;
-                if (!wait(SB_FULL + st, ph)) return false;
-                if (++st == nst) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+            Ring kr = {0, nk, 0, 0u}, vr = {nk, nst, nk, 0u};
+            auto take = [&](Ring &x, int &slot) { // waits for the next tile
+                slot = x.slot;
+                if (!wait(SB_FULL + x.slot, x.phase)) return false;
+                x.advance();
                 return true;
             };
             const uint32_t ring = sb + p.q_bytes;
@@ -739,21 +774,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (u == 0 && !wait(SB_OFREE, nth & 1u)) return false;
                         if (!wait(SB_PFULL + s, (pph >> s) & 1u)) return false;
                         pph ^= 1u << s;
-                        if ((sh == 0 || !(u & 1)) && !take(vs)) return false;
+                        if ((sh == 0 || !(u & 1)) && !take(vr, vs)) return false;
                         tc_fence_after();
                         const uint64_t vd = smem_desc_sw128(ring + vs * C::SLOT, CHUNK, 1024);
                         const uint32_t a = tmem + C::S_COL + s * C::S_SLOT;
                         const bool more = u >= (NWG == 2 ? 2 : 1) ||
                                           *static_cast<volatile int *>(ms->started + w);
                         if (one_p) {
-#pragma unroll
+#pragma unroll 4
                             for (int k = 0; k < T / 16; ++k)
                                 tc_mma_ts(tmem + w * D, a + 8 * k, vd + (uint64_t)((k * 2048) >> 4),
                                           idesc_pv, k || more ? 1u : 0u);
                         } else {
 #pragma unroll 1
                             for (int x = 0; x < TP; ++x)
-#pragma unroll
+#pragma unroll 4
                                 for (int k = 0; k < T / 16; ++k)
                                     tc_mma_ts(tmem + w * D,
                                               x < 2 ? a + 16 * k + 8 * x : a + T + 8 * k,
@@ -765,7 +800,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     if (v < nu) { // S of unit v
                         const int s = v & 1;
-                        if ((sh == 0 || !(v & 1)) && !take(ks)) return false;
+                        if ((sh == 0 || !(v & 1)) && !take(kr, ks)) return false;
                         tc_fence_after();
                         const uint32_t sd = tmem + C::S_COL + s * C::S_SLOT;
                         const uint64_t qd = smem_desc_sw128(
@@ -776,7 +811,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         constexpr int tm = C::QTM ? 1 : 0; // terms in TMEM
 #pragma unroll 1
                         for (int x = q_terms - 1; x >= tm; --x)
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < NCH; ++c)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
@@ -785,7 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                         kd + (uint64_t)((c * CHUNK + k * 32) >> 4), idesc_qk,
                                         x != q_terms - 1 || (c | k) != 0 ? 1u : 0u);
                         if (C::QTM) {
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < NCH; ++c)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
@@ -816,13 +851,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             (void)wait_phase(bar + SB_DRAIN, 0, p.timeout_ns, &never);
         }
         __syncwarp();
-    } else {
+    } else if (warp < C::WARPS) {
         // ========================= softmax and epilogue =========================
+        if constexpr (C::SPLIT) setmaxnreg_inc<C::SOFTMAX_REGS>();
         const int w = warp >> 2;              // warpgroup
         const int r = threadIdx.x & 127;      // row of the row tile, TMEM lane
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t to = tl + w * D;       // its accumulator
-        int n = 0, items = 0;                 // copies and items with tiles before this item
+        int n = 0, items = 0;                 // V tiles and items with tiles before this item
         uint32_t sph = 0;                     // phases of SFULL, by slot
         int done = 0;                         // units of this warpgroup so far
         uint32_t groups = 0, joints = 0;      // uses of SB_GROUP and SB_XCH
@@ -1335,9 +1371,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // is NaN), and so may rows that some see, which are looked for where there are
                 // several tokens; then this comes before the weights take the scores' place.
                 auto clean_v = [&]() {
-                    // (the copies of a sequence's item: K0 K1 V0 K2 V1 ...)
-                    const int f = n + min(2 * tile + 2, 2 * it.tiles - 1), st = f % nst;
-                    if (!wait(SB_FULL + st, (uint32_t)(f / nst) & 1u)) return false;
+                    const int f = n + tile, nv = nst - nk, st = nk + f % nv;
+                    if (!wait(SB_FULL + st, (uint32_t)(f / nv) & 1u)) return false;
                     const uint32_t vt = sb + p.q_bytes + st * C::SLOT;
                     const int o0 = max(q0, 0), o1 = it.S - 1;
                     const int ka = max(it.start - t0, 0), kb = min(it.keep1 - t0, T);
@@ -1717,11 +1752,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             tc_fence_before();
             arrive(SB_OFREE);
-            n += 2 * it.tiles;
+            n += it.tiles;
             ++items;
             return true;
         };
-        int taken = 0; // items from the queue
         // The next item with tiles (or the end), its Q on the way; those without are dealt with.
         auto next_item = [&](Item &it, int nth, float &row_scale) {
             for (;;) {
@@ -1752,13 +1786,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             row_scale = then_scale;
         }
         if (!ok && lane == 0) timed_out();
+    } else if constexpr (C::SPLIT) {
+        setmaxnreg_dec<C::OTHER_REGS>();
     }
 
     // ---------------------------------- teardown ----------------------------------
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == C::WARPS + 1) tmem_dealloc(tmem, 512);
+    if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
 template <typename C>
