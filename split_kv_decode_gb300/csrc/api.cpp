@@ -963,6 +963,7 @@ int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t
     p.slots = x.g.slots;
     p.q_bytes = x.g.q_bytes;
     p.join_bytes = x.g.join_bytes;
+    p.kind = x.g.kind;
     p.row_groups = x.row_groups;
     p.shared_len = sp->shared_len;
     p.shared_tiles = x.shared_tiles;
@@ -1005,10 +1006,12 @@ int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t
     }
     if (rc) return rc;
     if (dev) p.dev_lens = dev->seq_lens;
-    const auto launch = a->kv_dtype == DA_F16 ? launch_gqa_scored_f16
-                        : x.p_terms == 2      ? launch_gqa_scored_bf16
-                                              : launch_gqa_scored_bf16_f32;
-    const cudaError_t e = launch(a->head_dim, split_grid(a, &pl), x.g.smem, st, km, vm, p);
+    const bool narrow = a->head_dim == 128;
+    const auto launch =
+        a->kv_dtype == DA_F16 ? (narrow ? launch_gqa_scored_f16_128 : launch_gqa_scored_f16_256)
+        : x.p_terms == 2      ? (narrow ? launch_gqa_scored_bf16_128 : launch_gqa_scored_bf16_256)
+                              : (narrow ? launch_gqa_scored_bf16_f32_128 : launch_gqa_scored_bf16_f32_256);
+    const cudaError_t e = launch(split_grid(a, &pl), x.g.smem, st, km, vm, p);
     if (e != cudaSuccess) return fail(DA_ELAUNCH, "split", "%s", cudaGetErrorString(e));
     return DA_OK;
 }

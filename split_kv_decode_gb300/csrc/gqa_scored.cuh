@@ -56,10 +56,14 @@
 namespace skv {
 namespace {
 
-template <typename DT_, int D_, int TP_, bool XF_> struct Cfg {
+template <typename DT_, int D_, int TP_, bool XF_, int KIND_> struct Cfg {
     using DT = DT_;
     static constexpr int D = D_, TP = TP_;
     static constexpr bool XF = XF_; // scores are transformed before the maximum is taken
+    static constexpr bool PK = KIND_ == kScoredPacked;
+    static constexpr bool SH = KIND_ == kScoredShared;
+    // lanes of a row's terms in a warp: 2 for up to 16 rows of two terms, 4 for up to 8 of three
+    static constexpr int PARTS = !PK ? 1 : TP == 2 ? 2 : 4;
     static constexpr bool BF = std::is_same<DT, __nv_bfloat16>::value;
     static constexpr int T = scored_tile(D, TP);
     static constexpr int NWG = scored_groups(D);
@@ -70,9 +74,9 @@ template <typename DT_, int D_, int TP_, bool XF_> struct Cfg {
     static constexpr int WARPS = NWG * 4, K_WARP = WARPS, V_WARP = WARPS + 1, MMA_WARP = WARPS + 2;
     static constexpr int THREADS = (WARPS + 4) * 32;
     // registers (two softmax warpgroups: 168 a thread at launch, of which the last four warps
-    // leave some to the others: 8 * 200 + 4 * 104 = 12 * 168)
+    // leave some to the others: 8 * 192 + 4 * 120 = 12 * 168)
     static constexpr bool SPLIT = NWG == 2;
-    static constexpr int SOFTMAX_REGS = 200, OTHER_REGS = 104;
+    static constexpr int SOFTMAX_REGS = 192, OTHER_REGS = 120;
     // TMEM columns: O of warpgroup w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
     static constexpr bool QTM = scored_q_in_tmem(D, TP);
     static constexpr int S_COL = 256, S_SLOT = QTM ? 64 : 128, Q_COL = 384;
@@ -100,7 +104,6 @@ struct Item {
     int S;                  // the sequence's length
     int last;               // of its CTA
     int back;               // tiles from the last to the first
-    __device__ __forceinline__ bool shared() const { return b < 0; }
     __device__ __forceinline__ int row_tiles() const { return rows > 128 ? 2 : 1; }
 };
 static_assert(sizeof(Item) == 64, "item");
@@ -129,13 +132,6 @@ __device__ __forceinline__ int length_of(const ScoredParams &p, int b)
     return p.dev_lens ? max(0, min(__ldg(p.dev_lens + b), L)) : L;
 }
 
-// Lanes of a row's terms in a warp: 2 for up to 16 rows of two terms, 4 for up to 8 of three.
-template <int TP> __device__ __forceinline__ int parts_of(int rows)
-{
-    constexpr int most = TP == 2 ? 2 : 4;
-    return rows <= 32 / most ? most : 1;
-}
-
 // Lanes from one copy of a row tile to the next, and copies.
 __device__ __forceinline__ int span_of(int rows)
 {
@@ -146,19 +142,25 @@ __device__ __forceinline__ int reps_of(const ScoredParams &p, int rows)
     return rows > 128 ? 1 : max(1, p.rpad / span_of(rows));
 }
 // Copies of a row by the weights' terms: with two terms, half of the copies take the second.
-template <int TP> __device__ __forceinline__ int shares_of_terms(int parts, int reps)
+template <typename C> __device__ __forceinline__ int shares_of_terms(int reps)
 {
-    return TP == 2 && parts == 1 && reps > 1 ? 2 : 1;
+    return C::TP == 2 && !C::PK && reps > 1 ? 2 : 1;
+}
+// An item of the shared positions (known at compile time where there are none).
+template <typename C> __device__ __forceinline__ bool of_all(const Item &it)
+{
+    return C::SH && it.b < 0;
 }
 
 // Sequence, head and (own) position of a row of an item.
+template <typename C>
 __device__ __forceinline__ void row_of(const ScoredParams &p, const Item &it, int row, int &b, int &h,
                                        int &own)
 {
     const int Gh = p.hq / p.hkv, per_seq = p.q_len * Gh;
     int rr = it.row0 + row, S = it.S;
     b = it.b;
-    if (it.shared()) {
+    if (of_all<C>(it)) {
         b = rr / per_seq;
         rr -= b * per_seq;
         S = length_of(p, b);
@@ -169,8 +171,8 @@ __device__ __forceinline__ void row_of(const ScoredParams &p, const Item &it, in
 }
 
 // What a softmax thread holds of an item: a row of it, and a share of its columns.
-template <int T, int TP> struct Lane {
-    int nrt, parts, span, reps, copies, shares;
+template <typename C> struct Lane {
+    int nrt, span, reps, copies, shares;
     int rep, share, part;   // copy of the row tile, share of the columns, term of the weights
     int local;              // row of the item
     bool in_use, owner, busy; // (of its warp: in_use, busy)
@@ -180,11 +182,11 @@ template <int T, int TP> struct Lane {
     __device__ __forceinline__ Lane(const ScoredParams &p, const Item &it, int w, int warp4, int lane)
     {
         nrt = it.row_tiles();
-        parts = parts_of<TP>(it.rows);
+        constexpr int parts = C::PARTS;
         span = span_of(it.rows);
         reps = reps_of(p, it.rows);
         copies = reps * parts;
-        const int terms = shares_of_terms<TP>(parts, reps);
+        const int terms = shares_of_terms<C>(reps);
         shares = reps / terms;
         one_p = parts * terms > 1;
         rep = warp4 * 32 / span;
@@ -200,7 +202,7 @@ template <int T, int TP> struct Lane {
         int row = it.row0 + (owner ? local : 0);
         b = it.b;
         S = it.S;
-        if (it.shared()) {
+        if (of_all<C>(it)) {
             b = row / per_seq;
             row -= b * per_seq;
             S = length_of(p, b);
@@ -213,13 +215,15 @@ template <int T, int TP> struct Lane {
 };
 
 // The idx-th item.
-template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
+template <typename C>
+__device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
 {
+    constexpr int T = C::T;
     const int per_seq = p.q_len * (p.hq / p.hkv);
     it.last = 0;
     // (a bias by distance favours the last positions: the references are set at once)
     it.back = p.slopes != nullptr;
-    if (idx < p.shared_items) {
+    if (C::SH && idx < p.shared_items) {
         it.b = -1;
         const int u = idx / p.row_tiles;
         it.row0 = (idx - u * p.row_tiles) * p.tile_rows;
@@ -233,7 +237,7 @@ template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p,
         it.start = it.keep1 = it.S = 0;
         return;
     }
-    int t = idx - p.shared_items;
+    int t = C::SH ? idx - p.shared_items : idx;
     int u = t / p.row_groups;
     it.row0 = (t - u * p.row_groups) * p.tile_rows;
     it.rows = min(per_seq - it.row0, p.tile_rows);
@@ -250,6 +254,12 @@ template <int T> __device__ __forceinline__ void get_item(const ScoredParams &p,
     it.split = t - p.base[lo];
     const int S = length_of(p, b);
     it.S = it.end = S;
+    if (C::SH) { // (neither windows nor starts nor a kept prefix)
+        it.start = it.keep1 = it.n1 = it.a0 = it.w0 = 0;
+        it.v0 = it.split * p.chunk[b];
+        it.tiles = max(0, min((S + T - 1) / T - it.v0, p.chunk[b]));
+        return;
+    }
     it.start = p.starts ? max(0, __ldg(p.starts + b)) : 0;
     int keep = p.keep;
     if (p.keep_lens) keep = max(0, min(__ldg(p.keep_lens + b), keep));
@@ -295,6 +305,23 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint6
         const uint64_t t = global_ns();
         if (t0 == 0) t0 = t;
         if (*abort || t - t0 > limit_ns) return false;
+    }
+    return true;
+}
+
+// The same for a whole warp. Its branches depend on votes only: lanes that left such a loop at different
+// times would run what follows apart from each other, joining at every exchange (measured on the
+// warps of the copies: five times slower until their next wait).
+__device__ __forceinline__ bool wait_phase_warp(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                                volatile int *abort)
+{
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++n) {
+        if (n & 31u) continue;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (__any_sync(0xffffffffu, *abort || t - t0 > limit_ns)) return false;
     }
     return true;
 }
@@ -450,6 +477,15 @@ template <int N> __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, c
                      "r"(r[31])
                      : "memory");
     }
+}
+
+// one lane of a whole warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(on));
+    return on != 0;
 }
 
 template <int N> __device__ __forceinline__ void setmaxnreg_inc()
@@ -612,16 +648,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // ============================ copies of K, or of V ============================
         if constexpr (C::SPLIT) setmaxnreg_dec<C::OTHER_REGS>();
         const bool is_v = warp == C::V_WARP;
-        const CUtensorMap *map = is_v ? &vmap : &kmap;
-        if (lane == 0) tma_prefetch_map(map);
+        if (lane == 0) tma_prefetch_map(is_v ? &vmap : &kmap);
         const uint64_t once = l2_evict_first_policy(), normal = l2_normal_policy();
         const bool paged = p.block_table != nullptr;
         Ring ring = {is_v ? nk : 0, is_v ? nst : nk, is_v ? nk : 0, 0u};
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
-            bool got = true;
-            if (lane == 0) got = wait_phase(bar + b, parity, p.timeout_ns, abort_flag);
-            ok = ok && __shfl_sync(0xffffffffu, got, 0);
+            ok = ok && wait_phase_warp(bar + b, parity, p.timeout_ns, abort_flag);
             return ok;
         };
         // lanes hold the 64 table entries from `base` on, the second half ahead of its use
@@ -656,28 +689,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (pos >= it.end || blk < 0) blk = p.oob_block; // reads as zeros
             return At{blk, pos - e * bs};
         };
-        auto copies = [&](const Item &it) {
+        auto copies = [&](const Item &it, const CUtensorMap *map) {
             if (it.tiles == 0) return;
             if (paged) {
-                tab = it.shared() ? p.shared_table : p.block_table + (size_t)it.b * p.max_blocks;
-                width = it.shared() ? p.shared_len / p.block_size : p.max_blocks;
+                tab = of_all<C>(it) ? p.shared_table : p.block_table + (size_t)it.b * p.max_blocks;
+                width = of_all<C>(it) ? p.shared_len / p.block_size : p.max_blocks;
                 base = -1;
             }
             // shared tiles are read by every row tile's items
-            const uint64_t pol = it.shared() && p.row_tiles > 1 ? normal : once;
+            const uint64_t pol = C::SH && p.row_tiles > 1 && it.b < 0 ? normal : once;
             At at = locate(it, 0);
 #pragma unroll 1
             for (int i = 0; i < it.tiles; ++i) {
                 if (!wait(SB_EMPTY + ring.slot, ring.phase ^ 1u)) return;
                 if (!(p.flags & DA_FLAG_TEST_NO_TMA)) {
-                    uint8_t *dst = sm + p.q_bytes + ring.slot * C::SLOT + lane * h * 128;
-                    if (lane == 0) mbar_arrive_expect_tx(bar + SB_FULL + ring.slot, C::SLOT);
-                    __syncwarp();
-                    if (lane < nbox) {
+                    uint8_t *dst = sm + p.q_bytes + ring.slot * C::SLOT;
+                    uint64_t *full = bar + SB_FULL + ring.slot;
+                    if (elect_one()) mbar_arrive_expect_tx(full, C::SLOT);
+#pragma unroll 1
+                    for (int j = 0; j < nbox; ++j, dst += h * 128) {
+                        const int blk = __shfl_sync(0xffffffffu, at.blk, j);
+                        const int pos = __shfl_sync(0xffffffffu, at.pos, j);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tma_load_4d(dst + c * CHUNK, map, bar + SB_FULL + ring.slot, c * 64,
-                                        it.kvh, at.pos, at.blk, pol);
+                            for (int c = 0; c < NCH; ++c)
+                                tma_load_4d(dst + c * CHUNK, map, full, c * 64, it.kvh, pos, blk, pol);
+                        }
                     }
                     __syncwarp();
                 }
@@ -708,9 +745,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
             for (int r = 0, idx = nth(0); ok && idx >= 0; ++r) {
                 const int then = nth(r + 1);
-                get_item<T>(p, idx, it);
+                get_item<C>(p, idx, it);
                 it.last = then < 0;
-                if (pass_on(it)) copies(it);
+                if (pass_on(it)) copies(it, &kmap);
                 idx = then;
             }
             it.tiles = -1;
@@ -724,7 +761,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + SB_TAKEN + q);
                 if (it.tiles < 0) break;
-                copies(it);
+                copies(it, &vmap);
                 if (!ok) break;
             }
         }
@@ -763,9 +800,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const uint32_t ring = sb + p.q_bytes;
             auto item = [&](int tiles, int rows, uint32_t nth) {
                 const int sh = rows > 128 ? 1 : 0, nu = tiles << sh;
-                const int parts = parts_of<TP>(rows);
-                const bool one_p = parts > 1 || shares_of_terms<TP>(parts, reps_of(p, rows)) > 1;
-                const int q_terms = parts > 1 ? 1 : p.q_terms;
+                const bool one_p = C::PK || shares_of_terms<C>(reps_of(p, rows)) > 1;
+                const int q_terms = C::PK ? 1 : p.q_terms;
                 int ks = 0, vs = 0;
                 if (!wait(SB_QFULL, nth & 1u)) return false;
                 for (int v = 0; v < nu + 2; ++v) {
@@ -864,7 +900,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         uint32_t groups = 0, joints = 0;      // uses of SB_GROUP and SB_XCH
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, wait_phase(bar + b, parity, p.timeout_ns, abort_flag));
+            ok = wait_phase_warp(bar + b, parity, p.timeout_ns, abort_flag);
             return ok;
         };
         auto arrive = [&](int b) {
@@ -885,8 +921,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // Q of an item with tiles, once the last one's scores are done with it; returns false after a
         // timeout. scale: of this lane's row (256 columns, an f32 q beside an f16 cache)
         auto load_q = [&](const Item &it, int nth, float &row_scale) {
-            const Lane<T, TP> me(p, it, w, warp & 3, lane);
-            const int parts = me.parts, part = me.part, reps = me.reps, span = me.span;
+            const Lane<C> me(p, it, w, warp & 3, lane);
+            constexpr int parts = C::PARTS;
+            const int part = me.part, reps = me.reps, span = me.span;
             const bool busy = me.busy;
             const int per_seq = p.q_len * Gh;
             if (nth > 0 && !wait(SB_QFREE, (uint32_t)(nth - 1) & 1u)) return false;
@@ -962,7 +999,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 auto source = [&](int rr) { // element of q, or -1
                     if (rr >= it.rows) return (int64_t)-1;
                     int qrow = it.row0 + rr, qb = it.b;
-                    if (it.shared()) {
+                    if (of_all<C>(it)) {
                         qb = qrow / per_seq;
                         qrow -= qb * per_seq;
                     }
@@ -1058,9 +1095,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
         // An item without positions to see: neutral partials.
         auto neutral = [&](const Item &it) {
-            const Lane<T, TP> me(p, it, w, warp & 3, lane);
+            const Lane<C> me(p, it, w, warp & 3, lane);
             if (!me.owner || me.rep || me.part || (me.nrt == 1 && w)) return;
-            const size_t slot = (size_t)p.slot[me.b] + it.split + (it.shared() ? 0 : p.shared_splits);
+            const size_t slot = (size_t)p.slot[me.b] + it.split + (of_all<C>(it) ? 0 : p.shared_splits);
             const size_t row = p.whole ? (size_t)me.b * p.rows + me.out_row : slot * p.rows + me.out_row;
             if (!p.whole) {
                 p.ml[row] = make_float2(kNeutralM, 0.f);
@@ -1074,15 +1111,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // The units and the epilogue of an item (of one without tiles: neither). before_join is called
         // between them, once this warp's scores of the item are done with.
         auto work = [&](const Item &it, float row_scale, auto &&before_join) {
-            const Lane<T, TP> me(p, it, w, warp & 3, lane);
-            const int nrt = me.nrt, parts = me.parts, part = me.part, span = me.span, reps = me.reps;
+            const Lane<C> me(p, it, w, warp & 3, lane);
+            constexpr int parts = C::PARTS;
+            const int nrt = me.nrt, part = me.part, span = me.span, reps = me.reps;
             const int copies = me.copies, shares = me.shares, rep = me.rep, share = me.share;
             const int local = me.local, b = me.b, h = me.h, own = me.own;
             const bool owner = me.owner, busy = me.busy, one_p = me.one_p;
             const int cols = T / shares, cb = share * cols;
             const int q0 = it.S - p.q_len;         // of a sequence's own item: its first token
             const bool dead = !owner || own < 0;   // no such token: it sees nothing
-            const size_t slot = (size_t)p.slot[b] + it.split + (it.shared() ? 0 : p.shared_splits);
+            const size_t slot = (size_t)p.slot[b] + it.split + (of_all<C>(it) ? 0 : p.shared_splits);
             // its row of the output, or of the partials
             const size_t dst_row =
                 p.whole ? (size_t)b * p.rows + me.out_row : slot * p.rows + me.out_row;
@@ -1106,10 +1144,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tmem_wait_st();
             }
 
+            const int window = C::SH ? 0 : p.window, start = C::SH ? 0 : it.start;
+            const int keep1 = C::SH ? 0 : it.keep1;
+
             // ---- what rows see and how they score: of unpacked items this lane's row (the first of
             // two), of packed ones rows lane / 4 and lane / 4 + 8, four lanes to a row
-            const bool packed = parts > 1;
-            constexpr int PR = TP == 2 ? 2 : 1; // rows of a thread in packed items
+            constexpr bool packed = C::PK;
+            constexpr int PR = C::PK && TP == 2 ? 2 : 1; // rows of a thread in packed items
             struct Row {
                 bool real;
                 int pos, x_lo, x_hi;
@@ -1125,10 +1166,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (packed) {
                     rr = (lane >> 2) + 8 * k;
                     y.real = me.in_use && rr < it.rows;
-                    row_of(p, it, y.real ? rr : 0, rb, rh, at);
+                    row_of<C>(p, it, y.real ? rr : 0, rb, rh, at);
                 }
-                y.pos = at + (it.shared() ? p.shared_len : 0); // in this item's positions
-                y.x_lo = p.window ? max(it.start, at - p.window + 1) : it.start;
+                y.pos = at + (of_all<C>(it) ? p.shared_len : 0); // in this item's positions
+                y.x_lo = window ? max(start, at - window + 1) : start;
                 y.x_hi = !y.real || at < 0 ? 0 : at + 1;
                 y.sc.slope = C::XF && p.slopes && y.real ? __ldg(p.slopes + rh) * kLog2e : 0.f;
                 y.sc.cap = p.softcap * kLog2e;
@@ -1173,19 +1214,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
                 // does every row see all columns?
                 bool full = t0 + T <= it.end;
-                if (!it.shared()) {
+                if (!of_all<C>(it)) {
                     const int o0 = max(q0, 0), o1 = it.S - 1;
-                    full = full && t0 >= it.start &&
-                           (t0 + T <= it.keep1 ||
-                            (t0 + T - 1 <= o0 && (!p.window || t0 > o1 - p.window)));
+                    full = full && t0 >= start &&
+                           (t0 + T <= keep1 ||
+                            (t0 + T - 1 <= o0 && (!window || t0 > o1 - window)));
                 }
                 // otherwise a row sees columns [k0, k1) and [x0, x1)
-                const int k0 = max(it.start - t0, 0), k1 = min(it.keep1 - t0, T);
-                auto x0_of = [&](const Row &y) { return it.shared() ? 0 : max(y.x_lo - t0, 0); };
+                const int k0 = max(start - t0, 0), k1 = min(keep1 - t0, T);
+                auto x0_of = [&](const Row &y) { return of_all<C>(it) ? 0 : max(y.x_lo - t0, 0); };
                 auto x1_of = [&](const Row &y) {
-                    return min((it.shared() ? it.end : y.x_hi) - t0, T);
+                    return min((of_all<C>(it) ? it.end : y.x_hi) - t0, T);
                 };
-                auto k1_of = [&](const Row &y) { return y.x_hi > 0 && !it.shared() ? k1 : 0; };
+                auto k1_of = [&](const Row &y) { return y.x_hi > 0 && !of_all<C>(it) ? k1 : 0; };
                 // y of N scores of a row (c: their first columns less each one's own)
                 auto transform = [&](const Row &y, float *x, auto count, auto &&col) {
                     constexpr int N = decltype(count)::value;
@@ -1375,9 +1416,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!wait(SB_FULL + st, (uint32_t)(f / nv) & 1u)) return false;
                     const uint32_t vt = sb + p.q_bytes + st * C::SLOT;
                     const int o0 = max(q0, 0), o1 = it.S - 1;
-                    const int ka = max(it.start - t0, 0), kb = min(it.keep1 - t0, T);
-                    const int lo_any = max(p.window ? max(it.start, o0 - p.window + 1) : it.start, 0) - t0;
-                    const int lo_all = max(p.window ? max(it.start, o1 - p.window + 1) : it.start, 0) - t0;
+                    const int ka = max(start - t0, 0), kb = min(keep1 - t0, T);
+                    const int lo_any = max(window ? max(start, o0 - window + 1) : start, 0) - t0;
+                    const int lo_all = max(window ? max(start, o1 - window + 1) : start, 0) - t0;
                     const int hi_any = it.S - t0, hi_all = o0 + 1 - t0;
                     // (boxes of a paged cache past the end read as zeros)
                     const int top = p.block_table
@@ -1432,7 +1473,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                                      : ref_of(rows[0]);
                             const int k1r = dead ? 0 : k1, x1r = dead ? 0 : min(own + 1 - t0, T);
                             const int x0r =
-                                max((p.window ? max(it.start, own - p.window + 1) : it.start) - t0, 0);
+                                max((window ? max(start, own - window + 1) : start) - t0, 0);
 #pragma unroll 1
                             for (int c = 0; c < T; ++c) {
                                 if (!((word[c >> 5] >> (c & 31)) & 1u)) continue;
@@ -1473,7 +1514,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     fence_proxy_async_smem();
                     return true;
                 };
-                const bool edge = __builtin_expect(!full, 0) && !it.shared();
+                const bool edge = __builtin_expect(!full, 0) && !of_all<C>(it);
                 if (edge && p.q_len > 1 && !clean_v()) return false;
 
                 // ---- P: the weights, in terms, in the place of their scores. One term of 16
@@ -1808,18 +1849,24 @@ cudaError_t launch(int grid, int smem, cudaStream_t st, const CUtensorMap &km, c
     return cudaGetLastError();
 }
 
-} // namespace
-
-template <typename DT, int TP>
-static cudaError_t launch_d(int head_dim, int grid, int smem, cudaStream_t st, const CUtensorMap &km,
-                            const CUtensorMap &vm, const ScoredParams &p)
+template <typename DT, int D, int TP, int KIND>
+cudaError_t launch_x(int grid, int smem, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm,
+                     const ScoredParams &p)
 {
     const bool xf = p.softcap != 0.f || p.slopes || !(p.scale > 0.f);
-    if (head_dim == 128)
-        return xf ? launch<Cfg<DT, 128, TP, true>>(grid, smem, st, km, vm, p)
-                  : launch<Cfg<DT, 128, TP, false>>(grid, smem, st, km, vm, p);
-    return xf ? launch<Cfg<DT, 256, TP, true>>(grid, smem, st, km, vm, p)
-              : launch<Cfg<DT, 256, TP, false>>(grid, smem, st, km, vm, p);
+    return xf ? launch<Cfg<DT, D, TP, true, KIND>>(grid, smem, st, km, vm, p)
+              : launch<Cfg<DT, D, TP, false, KIND>>(grid, smem, st, km, vm, p);
+}
+
+} // namespace
+
+template <typename DT, int D, int TP>
+static cudaError_t launch_kind(int grid, int smem, cudaStream_t st, const CUtensorMap &km,
+                               const CUtensorMap &vm, const ScoredParams &p)
+{
+    return p.kind == kScoredPacked ? launch_x<DT, D, TP, kScoredPacked>(grid, smem, st, km, vm, p)
+           : p.kind == kScoredOwn  ? launch_x<DT, D, TP, kScoredOwn>(grid, smem, st, km, vm, p)
+                                   : launch_x<DT, D, TP, kScoredShared>(grid, smem, st, km, vm, p);
 }
 
 } // namespace skv

@@ -31,6 +31,7 @@ constexpr int kScoredSmemMax = 232448;
 // of 128 bytes], then a ring of K and V tiles, then the place where the copies of an item's rows are
 // joined, then the rest.
 struct ScoredGeometry {
+    int kind;
     int q_terms;   // 1: q is of the cache's type
     int tile_rows; // query rows of an item, at most (256: two row tiles that share K and V tiles)
     int rpad;      // rows of a Q chunk
@@ -40,7 +41,13 @@ struct ScoredGeometry {
     int smem;
 };
 
-// Rows up to which an item's terms lie in the lanes of one warp.
+// Kernels by what their items are, so that each has the code of its own tiles only (the softmax warps
+// run straight code, and wait for instructions as long as they compute: with both forms in one
+// kernel a tile of packed rows took 1.25 us, without the other 0.98): sequences' items whose few
+// rows' terms lie in the lanes of a warp, other items of sequences, items of shared positions and of
+// sequences.
+enum : int { kScoredPacked = 0, kScoredOwn = 1, kScoredShared = 2 };
+// Rows up to which items are packed.
 constexpr int scored_packed(int p_terms) { return p_terms == 2 ? 16 : 8; }
 
 // own_rows: a sequence's query rows of a KV head; shared_rows: those of the batch, or 0
@@ -51,8 +58,11 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
     const int slot = scored_tile(D, p_terms) * D * 2;
     const int64_t most = shared_rows > own_rows ? shared_rows : own_rows;
     g.q_terms = q_terms;
+    g.kind = shared_rows > 0                      ? kScoredShared
+             : own_rows <= scored_packed(p_terms) ? kScoredPacked
+                                                  : kScoredOwn;
     const bool tm = scored_q_in_tmem(D, p_terms);
-    const int held = (most <= scored_packed(p_terms) ? 1 : q_terms) - (tm ? 1 : 0); // in shared memory
+    const int held = (g.kind == kScoredPacked ? 1 : q_terms) - (tm ? 1 : 0); // in shared memory
     // (two row tiles only for a q of one term: with more terms the ring would be too short)
     for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
         const int rows = (int)(most < g.tile_rows ? most : g.tile_rows);
@@ -89,7 +99,7 @@ inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int row
     const int reps = rows > 128 || g.rpad < span ? 1 : g.rpad / span;
     // additions of a unit to a lane (packed: a term has a lane of its own; or copies of its own, and
     // then half as many share the columns)
-    const int per = T / 16 / reps * (rows <= scored_packed(p_terms) ? 1 : p_terms);
+    const int per = T / 16 / reps * (g.kind == kScoredPacked ? 1 : p_terms);
     const int units = 48 / (per > 1 ? per : 1);
     return rows > 128 || scored_groups(D) == 1 ? units : 2 * units;
 }
@@ -111,6 +121,7 @@ struct ScoredParams {
     int32_t window, keep;
     int32_t max_blocks, block_size, oob_block, box_rows;
     int32_t rpad, tile_rows, slots, q_bytes, join_bytes;
+    int32_t kind;
     int32_t row_groups;      // of a sequence's rows of one KV head
     // items of the shared positions: (split, KV head, row tile), the row tile fastest
     int32_t shared_len, shared_tiles, shared_chunk, shared_splits, row_tiles, shared_items;
@@ -124,16 +135,15 @@ struct ScoredParams {
 };
 
 // by the cache's type and the output's (f32 outputs of bf16 caches take three terms)
-cudaError_t launch_gqa_scored_f16(int head_dim, int grid, int smem, cudaStream_t st,
-                                  const CUtensorMap &km, const CUtensorMap &vm,
-                                  const ScoredParams &p);
-cudaError_t launch_gqa_scored_bf16(int head_dim, int grid, int smem, cudaStream_t st,
-                                   const CUtensorMap &km, const CUtensorMap &vm,
-                                   const ScoredParams &p);
-cudaError_t launch_gqa_scored_bf16_f32(int head_dim, int grid, int smem, cudaStream_t st,
-                                       const CUtensorMap &km, const CUtensorMap &vm,
-                                       const ScoredParams &p);
-
+#define SKV_SCORED_LAUNCH(name) \
+    cudaError_t name(int grid, int smem, cudaStream_t st, const CUtensorMap &km, const CUtensorMap &vm, \
+                     const ScoredParams &p)
+SKV_SCORED_LAUNCH(launch_gqa_scored_f16_128);
+SKV_SCORED_LAUNCH(launch_gqa_scored_f16_256);
+SKV_SCORED_LAUNCH(launch_gqa_scored_bf16_128);
+SKV_SCORED_LAUNCH(launch_gqa_scored_bf16_256);
+SKV_SCORED_LAUNCH(launch_gqa_scored_bf16_f32_128);
+SKV_SCORED_LAUNCH(launch_gqa_scored_bf16_f32_256);
 // Planner (plan_scored.cpp, pure host code). Lengths in tiles.
 struct ScoredWork {
     int batch, hkv, row_groups;
