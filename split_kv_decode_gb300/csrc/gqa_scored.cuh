@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else if (warp == C::MMA_WARP) {
         // ============================ MMA issue (one thread) ============================
         if constexpr (C::SPLIT) setmaxnreg_dec<C::OTHER_REGS>();
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_qk = idesc_f16kind(128, T, 0, 0, C::BF);
             constexpr uint32_t idesc_pv = idesc_f16kind(128, D, 0, 1, C::BF);
             uint32_t pph = 0;      // phases of PFULL, by slot
