@@ -66,18 +66,18 @@ template <typename DT_, int D_, int TP_, bool XF_, int KIND_> struct Cfg {
     static constexpr int PARTS = !PK ? 1 : TP == 2 ? 2 : 4;
     static constexpr bool BF = std::is_same<DT, __nv_bfloat16>::value;
     static constexpr int T = scored_tile(D, TP);
-    static constexpr int NWG = scored_groups(D);
+    static constexpr int NWG = 2;           // softmax warpgroups
+    static constexpr int NACC = scored_accs(D);
     static constexpr int NCH = D / 64;      // 64-column chunks of a row
     static constexpr int CHUNK = T * 128;   // bytes of a chunk of a tile
     static constexpr int SLOT = NCH * CHUNK;
     // softmax warps, then those of the K copies, the V copies and the MMAs, and one without work
     static constexpr int WARPS = NWG * 4, K_WARP = WARPS, V_WARP = WARPS + 1, MMA_WARP = WARPS + 2;
     static constexpr int THREADS = (WARPS + 4) * 32;
-    // registers (two softmax warpgroups: 168 a thread at launch, of which the last four warps
-    // leave some to the others: 8 * 192 + 4 * 120 = 12 * 168)
-    static constexpr bool SPLIT = NWG == 2;
+    // registers (168 a thread at launch, of which the last four warps leave some to the others:
+    // 8 * 192 + 4 * 120 = 12 * 168)
     static constexpr int SOFTMAX_REGS = 192, OTHER_REGS = 120;
-    // TMEM columns: O of warpgroup w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
+    // TMEM columns: accumulator w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
     static constexpr bool QTM = scored_q_in_tmem(D, TP);
     static constexpr int S_COL = 256, S_SLOT = QTM ? 64 : 128, Q_COL = 384;
     // A row's reference moves when a weight passes 2^LIM, and then to 2^-OFF of the largest: an f16
@@ -90,7 +90,8 @@ constexpr int SB_FULL = 0, SB_EMPTY = kScoredMaxSlots, SB_SFULL = 2 * kScoredMax
               SB_PFULL = SB_SFULL + 2, SB_PVDONE = SB_PFULL + 2, SB_OREADY = SB_PVDONE + 2,
               SB_OFREE = SB_OREADY + 1, SB_QFULL = SB_OFREE + 1, SB_QFREE = SB_QFULL + 1,
               SB_XCH = SB_QFREE + 1, SB_GROUP = SB_XCH + 1, SB_DRAIN = SB_GROUP + 2,
-              SB_ITEM = SB_DRAIN + 1, SB_TAKEN = SB_ITEM + 2, SB_N = SB_TAKEN + 2;
+              SB_ITEM = SB_DRAIN + 1, SB_TAKEN = SB_ITEM + 2, SB_REF = SB_TAKEN + 2,
+              SB_N = SB_REF + 2;
 
 struct Item {
     int tiles;              // of the visible span; < 0: no more items
@@ -109,22 +110,32 @@ struct Item {
 static_assert(sizeof(Item) == 64, "item");
 
 // the part of shared memory behind the ring
-template <int NWG> struct alignas(16) Misc {
+template <int NACC> struct Sums;
+template <> struct Sums<2> {
+    float2 state[2][128];     // (m, l) of a warpgroup's lanes
+    float row_scale[2][128];  // of an f32 q beside an f16 cache (at most 128 rows), every other item
+};
+template <> struct Sums<1> {
+    float ref[128];           // m of a lane, passed from unit to unit
+    float sum[2][128];        // l of a warpgroup's lanes
+};
+template <int NACC> struct alignas(16) Misc {
     Item item[2];             // the queue
     uint64_t bar[SB_N];
     uint32_t tmem;
     int abort;
-    int started[2];           // a warpgroup's accumulator holds something before its first MMA
+    int started[2];           // an accumulator holds something before its first MMA
     uint32_t bad[2][4];       // rows of a unit's V tile that hold no numbers, by its S slot
-    float2 state[NWG][128];   // (m, l) of a warpgroup's lanes
-    struct {                  // in the epilogue, of rows that several lanes share:
-        float factor[64];     // what their sum is multiplied by,
-        uint32_t to[64];      // and the row that it goes to
-    } row;
-    // of an f32 q beside an f16 cache, 128 columns (at most 128 rows then), of every other item
-    float row_scale[2][NWG == 2 ? 128 : 1];
+    Sums<NACC> of;
 };
 static_assert(sizeof(Misc<1>) <= scored_misc(256) && sizeof(Misc<2>) <= scored_misc(128), "misc");
+// in the epilogue, of rows that several lanes share: what their sum is multiplied by, and the row that
+// it goes to
+struct JoinRows {
+    float factor[64];
+    uint32_t to[64];
+};
+static_assert(sizeof(JoinRows) == kScoredRowBytes, "rows");
 
 __device__ __forceinline__ int length_of(const ScoredParams &p, int b)
 {
@@ -579,13 +590,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                       const __grid_constant__ ScoredParams p)
 {
     using DT = typename C::DT;
-    constexpr int D = C::D, T = C::T, NCH = C::NCH, NWG = C::NWG, TP = C::TP, CHUNK = C::CHUNK;
+    constexpr int D = C::D, T = C::T, NCH = C::NCH, NACC = C::NACC, TP = C::TP, CHUNK = C::CHUNK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
     const int nst = p.slots;
-    auto *ms = reinterpret_cast<Misc<NWG> *>(sm + p.q_bytes + nst * C::SLOT + p.join_bytes);
+    auto *ms = reinterpret_cast<Misc<NACC> *>(sm + p.q_bytes + nst * C::SLOT + p.join_bytes);
     uint64_t *bar = ms->bar;
     volatile int *abort_flag = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -603,6 +614,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(bar + SB_PFULL + s, 4);
             mbar_init(bar + SB_PVDONE + s, 1);
             mbar_init(bar + SB_GROUP + s, 4);
+            mbar_init(bar + SB_REF + s, 4);
         }
         mbar_init(bar + SB_OREADY, 1);
         mbar_init(bar + SB_OFREE, C::WARPS);
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     if (warp == C::K_WARP || warp == C::V_WARP) {
         // ============================ copies of K, or of V ============================
-        if constexpr (C::SPLIT) setmaxnreg_dec<C::OTHER_REGS>();
+        setmaxnreg_dec<C::OTHER_REGS>();
         const bool is_v = warp == C::V_WARP;
         if (lane == 0) tma_prefetch_map(is_v ? &vmap : &kmap);
         const uint64_t once = l2_evict_first_policy(), normal = l2_normal_policy();
@@ -780,7 +792,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
     } else if (warp == C::MMA_WARP) {
         // ============================ MMA issue (one thread) ============================
-        if constexpr (C::SPLIT) setmaxnreg_dec<C::OTHER_REGS>();
+        setmaxnreg_dec<C::OTHER_REGS>();
         if (elect_one()) {
             constexpr uint32_t idesc_qk = idesc_f16kind(128, T, 0, 0, C::BF);
             constexpr uint32_t idesc_pv = idesc_f16kind(128, D, 0, 1, C::BF);
@@ -806,7 +818,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (!wait(SB_QFULL, nth & 1u)) return false;
                 for (int v = 0; v < nu + 2; ++v) {
                     if (v >= 2) { // O += P V of unit v - 2
-                        const int u = v - 2, s = u & 1, w = NWG == 2 ? s : 0;
+                        const int u = v - 2, s = u & 1, w = NACC == 2 ? s : 0;
                         if (u == 0 && !wait(SB_OFREE, nth & 1u)) return false;
                         if (!wait(SB_PFULL + s, (pph >> s) & 1u)) return false;
                         pph ^= 1u << s;
@@ -814,7 +826,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         tc_fence_after();
                         const uint64_t vd = smem_desc_sw128(ring + vs * C::SLOT, CHUNK, 1024);
                         const uint32_t a = tmem + C::S_COL + s * C::S_SLOT;
-                        const bool more = u >= (NWG == 2 ? 2 : 1) ||
+                        const bool more = u >= NACC ||
                                           *static_cast<volatile int *>(ms->started + w);
                         if (one_p) {
 #pragma unroll 4
@@ -889,14 +901,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
     } else if (warp < C::WARPS) {
         // ========================= softmax and epilogue =========================
-        if constexpr (C::SPLIT) setmaxnreg_inc<C::SOFTMAX_REGS>();
+        setmaxnreg_inc<C::SOFTMAX_REGS>();
         const int w = warp >> 2;              // warpgroup
         const int r = threadIdx.x & 127;      // row of the row tile, TMEM lane
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t to = tl + w * D;       // its accumulator
+        const uint32_t to = tl + (NACC == 2 ? w : 0) * D; // its accumulator
         int n = 0, items = 0;                 // V tiles and items with tiles before this item
         uint32_t sph = 0;                     // phases of SFULL, by slot
-        int done = 0;                         // units of this warpgroup so far
+        int done = 0;                         // units of its accumulator so far
+        int handed = 0;                       // units of the other warpgroup before this item
         uint32_t groups = 0, joints = 0;      // uses of SB_GROUP and SB_XCH
         bool ok = true;
         auto wait = [&](int b, uint32_t parity) {
@@ -931,21 +944,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int64_t q_at = (((int64_t)me.b * p.q_len + me.tk) * p.hq + me.h) * D;
             row_scale = 1.f;
             if (C::QTM) {
-                // each lane its own row: one term into TMEM, the second of an f32 q that is not
-                // packed into shared memory; half a row (128 columns) or more in flight
+                // each lane half of its own row: one term into TMEM, the second of an f32 q that is
+                // not packed into shared memory
                 if (busy && !p.q_f32) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const uint16_t *>(p.q) + q_at);
-                    uint4 y[D / 8];
+                        static_cast<const uint16_t *>(p.q) + q_at + w * (D / 2));
+                    uint4 y[D / 16];
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) y[i] = __ldg(src + i);
+                    for (int i = 0; i < D / 16; ++i) y[i] = __ldg(src + i);
 #pragma unroll
-                    for (int i = 0; i < D / 8; i += 4) {
+                    for (int i = 0; i < D / 16; i += 4) {
                         const uint32_t v[16] = {
                             y[i].x,     y[i].y,     y[i].z,     y[i].w,     y[i + 1].x, y[i + 1].y,
                             y[i + 1].z, y[i + 1].w, y[i + 2].x, y[i + 2].y, y[i + 2].z, y[i + 2].w,
                             y[i + 3].x, y[i + 3].y, y[i + 3].z, y[i + 3].w};
-                        tmem_st16w(tl + C::Q_COL + i * 4, v);
+                        tmem_st16w(tl + C::Q_COL + w * (D / 4) + i * 4, v);
                     }
                     tmem_wait_st();
                 } else if (busy) {
@@ -953,8 +966,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const float down = 1.f / row_scale;
                     const float4 *src = reinterpret_cast<const float4 *>(
                         static_cast<const float *>(p.q) + q_at);
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 128) {
+                    {
+                        const int c = w * (D / 2);
                         float4 y[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) y[i] = __ldg(src + c / 4 + i);
@@ -1067,7 +1080,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 for (int o = U8 / 2; o > 0; o >>= 1)
                                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
                                 const float up = pow2_of(a);
-                                if (j == 0) ms->row_scale[nth & 1][u / U8] = up;
+                                if constexpr (NACC == 2) {
+                                    if (j == 0) ms->of.row_scale[nth & 1][u / U8] = up;
+                                }
                                 const float down = 1.f / up;
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) f[k] *= down;
@@ -1112,7 +1127,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // between them, once this warp's scores of the item are done with.
         auto work = [&](const Item &it, float row_scale, auto &&before_join) {
             const Lane<C> me(p, it, w, warp & 3, lane);
-            constexpr int parts = C::PARTS;
             const int nrt = me.nrt, part = me.part, span = me.span, reps = me.reps;
             const int copies = me.copies, shares = me.shares, rep = me.rep, share = me.share;
             const int local = me.local, b = me.b, h = me.h, own = me.own;
@@ -1138,9 +1152,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (TP == 3 && !one_p && reps > 1 && busy) {
                 // the third terms have columns of their own: zero but for this warp's share
                 const uint32_t z[16] = {};
-                for (int s = NWG == 2 ? w : 0; s < 2; s += NWG)
-                    for (int c = 0; c < T / 2; c += 16)
-                        tmem_st16w(tl + C::S_COL + s * C::S_SLOT + T + c, z);
+                for (int c = 0; c < T / 2; c += 16)
+                    tmem_st16w(tl + C::S_COL + w * C::S_SLOT + T + c, z);
                 tmem_wait_st();
             }
 
@@ -1185,27 +1198,49 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 return local >= 8 ? y : x;
             };
 
+            // where a lane's state is exchanged (packed: that of a row, by its warp)
+            auto state_at = [&](int k) {
+                return packed ? (warp & 3) * 32 + (lane >> 2) + 8 * k : r;
+            };
+            // the references as unit u left them, one of the other warpgroup (if there is one)
+            auto take = [&](int u) {
+                if constexpr (NACC == 1) {
+                    if (u < 0) return true;
+                    if (!wait(SB_REF + 1 - w, (uint32_t)(handed + (u >> 1)) & 1u)) return false;
+#pragma unroll
+                    for (int k = 0; k < PR; ++k) {
+                        const float m = ms->of.ref[state_at(k)];
+                        if (rows[k].l != 0.f && m != rows[k].m) rows[k].l *= ex2(rows[k].m - m);
+                        rows[k].m = m;
+                    }
+                }
+                return true;
+            };
+
             // ---- units
             const int nu = it.tiles * nrt;
             int mine = 0; // units of this item so far
 #pragma unroll 1
-            for (int u = NWG == 2 ? w : 0; u < nu; u += NWG) {
-                const int tile = nrt == 2 ? u >> 1 : u, s = u & 1;
+            for (int u = w; u < nu; u += 2) {
+                const int tile = nrt == 2 ? u >> 1 : u, s = w;
                 const int t0 = tile_at<T>(it, tile);
                 const uint32_t ts = tl + C::S_COL + s * C::S_SLOT;
                 if (!wait(SB_SFULL + s, (sph >> s) & 1u)) return false;
                 sph ^= 1u << s;
                 tc_fence_after();
+                const bool begun = NACC == 2 ? mine > 0 : u > 0; // there is an O
                 if (mine == 0) { // (an f32 q's row scale is there once all of Q is)
-                    if (r == 0) ms->started[w] = 0; // (before this warp's arrival, or a group_sync)
+                    // (before this warp's arrival, or a group_sync)
+                    if (r == 0 && !begun) ms->started[NACC == 2 ? w : 0] = 0;
 #pragma unroll
                     for (int k = 0; k < PR; ++k) {
                         Row &y = rows[k];
                         const int rr = packed ? (lane >> 2) + 8 * k : local;
                         float scale = row_scale;
                         if (packed) scale = __shfl_sync(0xffffffffu, row_scale, rr);
-                        if (!C::QTM && !C::BF && p.q_f32)
-                            scale = ms->row_scale[items & 1][y.real ? rr : 0];
+                        if constexpr (NACC == 2 && !C::BF) {
+                            if (p.q_f32) scale = ms->of.row_scale[items & 1][y.real ? rr : 0];
+                        }
                         scale *= p.scale;
                         y.sc.mult = scale * kLog2e;
                         y.sc.turn = p.softcap == 0.f ? 0.f : scale / p.softcap;
@@ -1265,6 +1300,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     y.l *= f;
                     y.m = to_m;
                     return f;
+                };
+                // one accumulator: a lane's reference is its last unit's, of the other warpgroup
+                auto take_refs = [&]() { return take(u - 1); };
+                auto pass_refs = [&]() {
+                    if constexpr (NACC == 1) {
+#pragma unroll
+                        for (int k = 0; k < PR; ++k)
+                            if (!packed || (lane & 3) == 0) ms->of.ref[state_at(k)] = rows[k].m;
+                        arrive(SB_REF + w);
+                    }
                 };
                 const bool adds = packed && p.q_f32; // a score is the sum of its terms'
                 const bool modified = adds || C::XF || !full, one = shares == 4;
@@ -1339,6 +1384,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                     if (back) tmem_wait_st();
+                    if (!take_refs()) return false;
                     float f[PR];
 #pragma unroll
                     for (int k = 0; k < PR; ++k) {
@@ -1348,6 +1394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (!C::XF && full) y *= rows[k].sc.mult;
                         f[k] = refer(rows[k], y);
                     }
+                    pass_refs();
                     if (__any_sync(0xffffffffu, moves)) {
                         moves = true;
                         alpha = of_lane(f[0], f[PR - 1]);
@@ -1388,12 +1435,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     if (back32) tmem_wait_st();
                     if (!C::XF && full) tm *= rows[0].sc.mult;
+                    if (!take_refs()) return false;
                     alpha = refer(rows[0], tm);
+                    pass_refs();
                     moves = __any_sync(0xffffffffu, moves);
+                } else {
+                    // (a warp without rows passes nothing on, but in turn)
+                    if (!take_refs()) return false;
+                    pass_refs();
                 }
-                if (__builtin_expect(moves, 0) && mine > 0) { // (before, there is no O)
-                    if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
+                const int before = NACC == 2 ? done : done + u; // units of the accumulator
+                auto last_done = [&]() { // O holds all of them
+                    if (!wait(SB_PVDONE + (NACC == 2 ? w : 0), (uint32_t)(before - 1) & 1u))
+                        return false;
                     tc_fence_after();
+                    return true;
+                };
+                if (__builtin_expect(moves, 0) && begun) { // (before, there is no O)
+                    if (!last_done()) return false;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
@@ -1459,15 +1518,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (word[0] | word[1] | word[2] | word[3]) {
                             // (rare) such rows are added here, to the rows that see them, and
                             // leave the tile
-                            if (mine > 0) {
-                                if (!wait(SB_PVDONE + w, (uint32_t)(done - 1) & 1u)) return false;
-                                tc_fence_after();
+                            if (begun) {
+                                if (!last_done()) return false;
                             } else { // the accumulator starts here
                                 const float z[16] = {};
 #pragma unroll 1
                                 for (int c = 0; c < D; c += 16) tmem_st16(to + c, z);
                                 tmem_wait_st();
-                                ms->started[w] = 1;
+                                ms->started[NACC == 2 ? w : 0] = 1;
                             }
                             const float ref = packed ? of_lane(ref_of(rows[0]), ref_of(rows[PR - 1]))
                                                      : ref_of(rows[0]);
@@ -1647,55 +1705,87 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (edge && p.q_len == 1 && !clean_v()) return false;
                 tc_fence_before();
                 arrive(SB_PFULL + s);
-                ++done;
+                if (NACC == 2) ++done;
                 ++mine;
             }
 
             if (!before_join()) return false;
             if (it.tiles == 0) return true;
-            float m = rows[0].m, l = rows[0].l;
+            if constexpr (NACC == 1) {
+                if (((nu - 1) & 1) != w && !take(nu - 1)) return false;
+                done += nu;
+                handed += w == 0 ? nu / 2 : (nu + 1) / 2;
+            }
             if (packed) {
 #pragma unroll
                 for (int k = 0; k < PR; ++k) {
                     rows[k].l += __shfl_xor_sync(0xffffffffu, rows[k].l, 1);
                     rows[k].l += __shfl_xor_sync(0xffffffffu, rows[k].l, 2);
                 }
-                m = of_lane(rows[0].m, rows[PR - 1].m);
-                l = of_lane(rows[0].l, rows[PR - 1].l);
             }
 
             // ---- epilogue: a row's states, of the warpgroups that took tiles in turn and of the
-            // copies of its lane, are joined
+            // copies of its lane, are joined; each warpgroup writes half of the columns
             if (!wait(SB_OREADY, (uint32_t)items & 1u)) return false;
             tc_fence_after();
-            const bool joint = NWG == 2 && nrt == 1;
+            const bool joint = nrt == 1;
             const int c0 = joint ? w * (D / 2) : 0, nc = joint ? D / 2 : D; // this thread's columns
-            float f_own = 1.f, f_other = 0.f;
-            if (joint || copies > 1) {
-                ms->state[w][r] = make_float2(m, l);
-                if (!all_sync()) return false;
-                // (a sum that is no number takes part: only an empty state does not)
-                const int first = owner ? local : 0;
+            const bool few = copies > 1 && it.rows <= 16; // rows lane / 4 and lane / 4 + 8 here too
+            float m = rows[0].m, l = rows[0].l;
+            float f_acc[NACC][2]; // what the accumulators of this copy of the rows are multiplied by
+#pragma unroll
+            for (int x = 0; x < NACC; ++x) f_acc[x][0] = f_acc[x][1] = x == 0 || joint ? 1.f : 0.f;
+            auto state = [&](int x, int at) { // of a warpgroup
+                if constexpr (NACC == 2) return ms->of.state[x][at];
+                else return make_float2(ms->of.ref[at], ms->of.sum[x][at]);
+            };
+            // (a sum that is no number takes part: only an empty state does not)
+            auto join_states = [&](int first, int here, int k, float &mm, float &ll) {
                 float2 y[8];
-                float mm = -INFINITY, ll = 0.f;
+                mm = -INFINITY;
+                ll = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    y[k] = make_float2(-INFINITY, 0.f);
-                    if (k < shares * NWG) y[k] = ms->state[k % NWG][first + k / NWG * span];
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = make_float2(-INFINITY, 0.f);
+                    if (i < shares * 2) y[i] = state(i & 1, first + (i >> 1) * span);
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (y[k].y != 0.f) mm = fmaxf(mm, y[k].x);
+                for (int i = 0; i < 8; ++i)
+                    if (y[i].y != 0.f) mm = fmaxf(mm, y[i].x);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (y[k].y != 0.f) ll += y[k].y * ex2(y[k].x - mm);
-                f_own = l == 0.f ? 0.f : ex2(m - mm);
-                if (joint) {
-                    const float2 other = ms->state[NWG - 1 - w][r];
-                    f_other = other.y == 0.f ? 0.f : ex2(other.x - mm);
+                for (int i = 0; i < 8; ++i)
+                    if (y[i].y != 0.f) ll += y[i].y * ex2(y[i].x - mm);
+                const float2 s0 = state(0, here), s1 = state(1, here);
+                if constexpr (NACC == 2) {
+                    f_acc[0][k] = s0.y == 0.f ? 0.f : ex2(s0.x - mm);
+                    f_acc[1][k] = s1.y == 0.f ? 0.f : ex2(s1.x - mm);
+                } else {
+                    f_acc[0][k] = s0.y == 0.f && s1.y == 0.f ? 0.f : ex2(s0.x - mm);
                 }
-                m = mm;
-                l = ll;
+            };
+            if (joint) {
+#pragma unroll
+                for (int k = 0; k < PR; ++k) {
+                    if (packed && (lane & 3)) continue;
+                    if constexpr (NACC == 2)
+                        ms->of.state[w][state_at(k)] = make_float2(rows[k].m, rows[k].l);
+                    else
+                        ms->of.sum[w][state_at(k)] = rows[k].l;
+                }
+                if (!all_sync()) return false;
+                if (packed || few) {
+                    float mm[2], ll[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int rr = (lane >> 2) + 8 * k;
+                        const bool on = rr < it.rows;
+                        join_states(on ? rr : 0, on ? (warp & 3) * 32 + rr : 0, k, mm[k], ll[k]);
+                    }
+                    m = of_lane(mm[0], mm[1]);
+                    l = of_lane(ll[0], ll[1]);
+                } else {
+                    join_states(owner ? local : 0, r, 0, m, l);
+                }
             }
             if (dead) l = 0.f;
             const bool odd = !(l - l == 0.f); // no number, or infinite
@@ -1704,22 +1794,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (writes && !p.whole && (!joint || w == 0))
                 p.ml[dst_row] = odd ? make_float2(-kNeutralM, 1.f) // outweighs every other partial
                                 : l == 0.f ? make_float2(kNeutralM, 0.f) : make_float2(m * kLn2, l);
-            // 16 columns of the lane, its warpgroups' joined
+            // (an accumulator that no unit went to holds anything)
+            auto times = [](float f, float x) { return f != 0.f ? f * x : 0.f; };
+            // 16 columns of the lane, of all accumulators
             auto lane16 = [&](int c, float *o) {
-                tmem_ld16(to + c, o);
-                if (joint) {
+                if (NACC == 2 && joint) {
                     float o2[16];
-                    tmem_ld16(tl + (NWG - 1 - w) * D + c, o2);
+                    tmem_ld16(tl + c, o);
+                    tmem_ld16(tl + D + c, o2);
                     tmem_wait_ld();
-                    // (an accumulator that no unit went to holds anything)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        o[i] = (f_own != 0.f ? f_own * o[i] : 0.f) +
-                               (f_other != 0.f ? f_other * o2[i] : 0.f);
+                        o[i] = times(f_acc[0][0], o[i]) + times(f_acc[NACC - 1][0], o2[i]);
                 } else {
+                    tmem_ld16(to + c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] *= f_own;
+                    for (int i = 0; i < 16; ++i) o[i] = times(f_acc[0][0], o[i]);
                 }
             };
             if (copies == 1) {
@@ -1737,25 +1828,67 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
             } else {
                 // the copies' sums meet in shared memory: [warpgroup][copy][row][W columns], as many
-                // columns at once as there is room for; 16-byte units swizzled so that lanes hit
-                // other banks
+                // columns at once as there is room for
                 const int rows4 = (it.rows + 3) / 4 * 4;
                 int W = nc;
                 // (a CTA's last item finds the ring empty)
-                const int room = it.last ? nst * C::SLOT : p.join_bytes;
-                while ((joint ? 2 : 1) * copies * rows4 * W * 4 > room) W >>= 1;
+                const int room = it.last ? nst * C::SLOT : p.join_bytes - kScoredRowBytes;
+                const int lanes = few ? reps : copies; // (those of a row's terms are added here)
+                while (2 * lanes * rows4 * W * 4 > room) W >>= 1;
                 const int w4 = W / 4, lw = 31 - __clz(w4);
+                uint8_t *place = sm + p.q_bytes + nst * C::SLOT;
+                auto *jr = reinterpret_cast<JoinRows *>(place);
                 if (writes && w == 0) {
-                    ms->row.factor[local] = factor;
-                    ms->row.to[local] = (uint32_t)dst_row;
+                    jr->factor[local] = factor;
+                    jr->to[local] = (uint32_t)dst_row;
                 }
-                float4 *xs = reinterpret_cast<float4 *>(sm + p.q_bytes + (it.last ? 0 : nst * C::SLOT)) +
-                             (joint ? w * copies * rows4 * w4 : 0);
+                float *xs = reinterpret_cast<float *>(it.last ? sm + p.q_bytes : place + kScoredRowBytes) +
+                            w * lanes * rows4 * W;
+                // units of 8 columns (few rows), of 4 otherwise, swizzled so that lanes hit other banks
+                const int mask8 = W / 8 - 1;
 #pragma unroll 1
                 for (int at = 0; at < nc; at += W) {
-                    if (busy) {
-                        const int copy = parts > 1 ? rep * parts + part : rep;
-                        float4 *to_row = xs + (copy * rows4 + local) * w4;
+                    if (few && busy) {
+                        // rows lane / 4 and lane / 4 + 8, two of every 8 columns, 32 columns at a time
+#pragma unroll 1
+                        for (int c = 0; c < W; c += 32) {
+                            float o[NACC][16], o2[NACC][16];
+#pragma unroll
+                            for (int x = 0; x < NACC; ++x) {
+                                tmem_ld_rows<4>(tl + x * D + c0 + at + c, o[x]);
+                                if (packed) tmem_ld_rows<4>(tl + (16u << 16) + x * D + c0 + at + c, o2[x]);
+                            }
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < (packed ? PR : 2); ++k) {
+                                const int rr = (lane >> 2) + 8 * k;
+                                if (rr >= it.rows) continue;
+                                float *to_row = xs + (rep * rows4 + rr) * W;
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                                    for (int x = 0; x < NACC; ++x) {
+                                        const int i = 4 * g + 2 * k;
+                                        float a = o[x][i], b2 = o[x][i + 1];
+                                        if (packed) {
+                                            a += o2[x][i];
+                                            b2 += o2[x][i + 1];
+                                        }
+                                        if (packed && TP == 3) {
+                                            a += o[x][4 * g + 2];
+                                            b2 += o[x][4 * g + 3];
+                                        }
+                                        sum.x += times(f_acc[x][k], a);
+                                        sum.y += times(f_acc[x][k], b2);
+                                    }
+                                    const int u8 = (c / 8 + g) ^ (rr & mask8);
+                                    *reinterpret_cast<float2 *>(to_row + u8 * 8 + 2 * (lane & 3)) = sum;
+                                }
+                            }
+                        }
+                    } else if (busy) {
+                        float4 *to_row = reinterpret_cast<float4 *>(xs) + (rep * rows4 + local) * w4;
 #pragma unroll 1
                         for (int c = 0; c < W; c += 16) {
                             float o[16];
@@ -1773,11 +1906,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const int c = r & (w4 - 1);
 #pragma unroll 1
                     for (int rr = r >> lw; rr < it.rows; rr += 128 >> lw) {
-                        const float fac = ms->row.factor[rr];
+                        const float fac = jr->factor[rr];
                         if (fac == 0.f && !p.whole) continue;
+                        const int at4 = few ? c ^ ((rr & mask8) << 1) : c ^ (rr & 3);
                         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int k = 0; k < copies; ++k) {
-                            const float4 y = xs[(k * rows4 + rr) * w4 + (c ^ (rr & 3))];
+#pragma unroll 4
+                        for (int k = 0; k < lanes; ++k) {
+                            const float4 y = reinterpret_cast<const float4 *>(xs)[(k * rows4 + rr) * w4 + at4];
                             sum.x += y.x;
                             sum.y += y.y;
                             sum.z += y.z;
@@ -1785,12 +1920,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                         sum = fac == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                                          : make_float4(sum.x * fac, sum.y * fac, sum.z * fac, sum.w * fac);
-                        write4((size_t)ms->row.to[rr], c0 + at + 4 * c, sum);
+                        write4((size_t)jr->to[rr], c0 + at + 4 * c, sum);
                     }
                     if (at + W < nc && !group_sync()) return false;
                 }
-                if (!all_sync()) return false; // the place may be written again
+                // (the place, and the states, are written again behind the next item's exchange)
             }
+            // (one accumulator: the next item's first unit passes references on)
+            if (NACC == 1 && copies == 1 && !all_sync()) return false;
             tc_fence_before();
             arrive(SB_OFREE);
             n += it.tiles;
@@ -1827,7 +1964,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             row_scale = then_scale;
         }
         if (!ok && lane == 0) timed_out();
-    } else if constexpr (C::SPLIT) {
+    } else {
         setmaxnreg_dec<C::OTHER_REGS>();
     }
 

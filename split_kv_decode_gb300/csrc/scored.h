@@ -8,12 +8,13 @@
 
 namespace skv {
 
-// positions of a tile, softmax warpgroups, and 16-bit terms of a weight
+// positions of a tile, accumulators (two softmax warpgroups take tiles in turn; TMEM has room for an
+// accumulator each at 128 columns), and 16-bit terms of a weight
 __host__ __device__ constexpr int scored_tile(int D, int terms)
 {
     return D == 128 && terms == 2 ? 128 : 64;
 }
-__host__ __device__ constexpr int scored_groups(int D) { return D == 128 ? 2 : 1; }
+__host__ __device__ constexpr int scored_accs(int D) { return D == 128 ? 2 : 1; }
 // 256 columns, two terms: TMEM has room for a term of Q beside O and the scores
 __host__ __device__ constexpr bool scored_q_in_tmem(int D, int terms) { return D == 256 && terms == 2; }
 // terms of a weight (and of an f32 q): f16 carries 11 bits a term, bf16 8
@@ -22,9 +23,10 @@ constexpr int scored_terms(int kv_dtype, int out_dtype)
     return kv_dtype == DA_BF16 && out_dtype == DA_F32 ? 3 : 2;
 }
 constexpr int kScoredMaxSlots = 8;
-// barriers, exchange of (m, l), row scales (at 256 columns beside 128 rows of two terms and three
-// tiles of the ring)
+// barriers, exchange of (m, l), row scales (at 256 columns beside 128 rows of two terms and five tiles
+// of the ring)
 __host__ __device__ constexpr int scored_misc(int D) { return D == 128 ? 4096 : 2048; }
+constexpr int kScoredRowBytes = 512; // of the place where copies are joined: a row's factor and place
 constexpr int kScoredSmemMax = 232448;
 
 // Shared memory: the terms of Q that TMEM does not hold, [row tile][term][64-column chunk][rpad rows
@@ -64,7 +66,7 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
     const bool tm = scored_q_in_tmem(D, p_terms);
     const int held = (g.kind == kScoredPacked ? 1 : q_terms) - (tm ? 1 : 0); // in shared memory
     // (two row tiles only for a q of one term: with more terms the ring would be too short)
-    for (g.tile_rows = scored_groups(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
+    for (g.tile_rows = scored_accs(D) == 2 && q_terms == 1 ? 256 : 128;; g.tile_rows /= 2) {
         const int rows = (int)(most < g.tile_rows ? most : g.tile_rows);
         // 128 lanes, with copies of few rows, where that leaves a ring of two tiles; a ring
         // shorter than a tile and a half takes smaller items
@@ -75,7 +77,7 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
                 const int64_t rest = all % g.tile_rows;
                 return all > 0 && (all <= 64 || g.tile_rows == 64 || (rest > 0 && rest <= 64));
             };
-            g.join_bytes = narrow(own_rows) || narrow(shared_rows) ? scored_groups(D) * g.rpad * 64 : 0;
+            g.join_bytes = narrow(own_rows) || narrow(shared_rows) ? kScoredRowBytes + g.rpad * 128 : 0;
             g.slots = (kScoredSmemMax - 1024 - scored_misc(D) - g.q_bytes - g.join_bytes) / slot;
             if (g.slots >= 4 || g.rpad / 2 < rows || g.rpad == 32) break;
         }
@@ -101,7 +103,7 @@ inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int row
     // then half as many share the columns)
     const int per = T / 16 / reps * (g.kind == kScoredPacked ? 1 : p_terms);
     const int units = 48 / (per > 1 ? per : 1);
-    return rows > 128 || scored_groups(D) == 1 ? units : 2 * units;
+    return rows > 128 || scored_accs(D) == 1 ? units : 2 * units;
 }
 
 struct ScoredParams {
