@@ -38,10 +38,10 @@ int plan_scored(const ScoredWork &w, ScoredSplit *out)
     const int64_t tile_bytes = (int64_t)w.tile * w.head_dim * 4;
     const int64_t fixed = 2 * kUnit * 128 / w.tile;
     auto partials = [&](int rows) { return (int64_t)rows * w.head_dim * 8 * kUnit / tile_bytes; };
-    // a shared tile: its MMAs take about a third of its time from memory for each term of q and of
+    // a shared tile: its MMAs take about a quarter of its time from memory for each term of q and of
     // the weights and 128 rows
     const int64_t shared_tile = std::max<int64_t>(
-        kUnit, kUnit * w.units * (w.q_terms + w.p_terms) * 10 / 30);
+        kUnit, kUnit * w.units * (w.q_terms + w.p_terms) * 10 / 40);
 
     struct Candidate {
         std::vector<int32_t> chunk;

@@ -14,8 +14,13 @@
 // Bound by memory: each row is read and written once. A warp holds one token (or 2 to 32 of
 // narrow heads) and walks its heads, or a share of them; a lane holds both columns of four
 // pairs of every head, so that it needs four angles a token, no exchange but the sum of squares, and
-// q may be rotated in place. The loads of the next rows are in flight while one is worked on.
+// q may be rotated in place. The loads of the next four rows are in flight while two are worked on side
+// by side: a row is a chain of a sum over the lanes, a root and two products, and the instructions of
+// a row (about 120) bound it beside the memory. (32768 tokens of 16/4 heads of 256 columns, f16: 174
+// us, 4.6 TB/s; a row at a time with the branches of each row 200; six or eight rows in flight 186 to
+// 275, as their registers leave room for fewer warps.)
 #include <algorithm>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -45,7 +50,7 @@ struct PrepParams {
     int32_t tokens, hq, hkv, units_k, units_v; // 8-column units of a q/k and of a v row
     int32_t block_size, pairs, interleaved;
     int32_t q_dtype, cache_dtype, w_dtype;
-    int32_t norm;
+    int32_t q_size, cache_size; // bytes of an element
     int32_t lanes, shares; // lanes of a row; warps that share a token's heads
     float eps, offset, factor, inv_dim;
     uint8_t axis[kMaxPairs];
@@ -59,11 +64,11 @@ template <> struct Raw<float> {
     uint4 a, b;
 };
 template <typename ST>
-__device__ __forceinline__ void load(Raw<ST> &r, const ST *row, int ca, int cb)
+__device__ __forceinline__ void load(Raw<ST> &r, const ST *first, int second)
 {
     using V = decltype(r.a);
-    r.a = *reinterpret_cast<const V *>(row + ca);
-    r.b = *reinterpret_cast<const V *>(row + cb);
+    r.a = *reinterpret_cast<const V *>(first);
+    r.b = *reinterpret_cast<const V *>(first + second);
 }
 __device__ __forceinline__ void widen2(uint32_t w, float *f, __half)
 {
@@ -90,36 +95,45 @@ template <> __device__ __forceinline__ void widen<float>(const Raw<float> &r, fl
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
 }
 template <typename WT>
-__device__ __forceinline__ void load_as(const void *base, int64_t at, int ca, int cb, float *f)
+__device__ __forceinline__ void load_as(const void *base, int64_t at, int second, float *f)
 {
     Raw<WT> r;
-    load(r, static_cast<const WT *>(base) + at, ca, cb);
+    load(r, static_cast<const WT *>(base) + at, second);
     widen<WT>(r, f);
 }
 
-__device__ __forceinline__ void store(void *base, int dtype, int64_t at, int ca, int cb,
-                                      const float *f)
+// f, rounded, to `first` and to `second` elements behind it
+__device__ __forceinline__ void store(uint8_t *first, int dtype, int second, const float *f)
 {
     if (dtype == DA_F32) {
-        float *p = static_cast<float *>(base) + at;
-        *reinterpret_cast<float4 *>(p + ca) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(p + cb) = make_float4(f[4], f[5], f[6], f[7]);
+        *reinterpret_cast<float4 *>(first) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(first + second * 4) = make_float4(f[4], f[5], f[6], f[7]);
         return;
     }
     uint32_t w[4];
+    if (dtype == DA_F16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (dtype == DA_F16) {
+        for (int i = 0; i < 4; ++i) {
             const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    uint16_t *p = static_cast<uint16_t *>(base) + at;
-    *reinterpret_cast<uint2 *>(p + ca) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2 *>(p + cb) = make_uint2(w[2], w[3]);
+    *reinterpret_cast<uint2 *>(first) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2 *>(first + second * 2) = make_uint2(w[2], w[3]);
+}
+
+// a^-1/2: the special function's, and one Newton step, which leaves the last rounding
+__device__ __forceinline__ float inv_root(float a)
+{
+    const float y = rsqrtf(a);
+    const float z = fmaf(0.5f * y, fmaf(-a * y, y, 1.f), y);
+    return a > 0.f && a < INFINITY ? z : y;
 }
 
 // cosine and sine of `phase` * 2^-64 turns
@@ -134,7 +148,7 @@ __device__ __forceinline__ float2 unit(uint64_t phase)
     return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
-template <typename ST>
+template <typename ST, bool NORM>
 __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ PrepParams p)
 {
     const int lane = threadIdx.x & 31;
@@ -144,40 +158,51 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
     const int64_t t = group * (32 / p.lanes) + lane / p.lanes;
     const bool live = t < p.tokens;
     const int sub = lane & (p.lanes - 1);
-    const int heads = p.hq + 2 * p.hkv;
+    const int hk = p.hq, hv = p.hq + p.hkv, heads = hv + p.hkv; // the first k and v row
     const int h0 = (int)((int64_t)share * heads / p.shares);
     const int h1 = (int)((int64_t)(share + 1) * heads / p.shares);
     const int turning = p.pairs >> 2; // lanes that hold pairs
     const bool turns = sub < turning;
-    // the lane's columns: both of four pairs, or eight in a row
+    // the lane's columns: both of four pairs, or eight in a row (those of a value row always)
     const bool halves = turns && !p.interleaved;
-    const int ca = halves ? sub * 4 : sub * 8, cb = halves ? p.pairs + sub * 4 : sub * 8 + 4;
-    // a value row has its own columns
-    const int va = sub * 8;
+    const int ca = halves ? sub * 4 : sub * 8, apart = halves ? p.pairs : 4, va = sub * 8;
+    const bool has_k = live && sub < p.units_k, has_v = live && sub < p.units_v;
 
-    Raw<ST> raw[kAhead] = {};
-    auto fetch = [&](Raw<ST> &r, int h) {
-        if (!live) return;
-        if (h < p.hq) {
-            if (sub < p.units_k)
-                load(r, static_cast<const ST *>(p.q) + t * p.q_stride + h * p.q_head, ca, cb);
-        } else if (h < p.hq + p.hkv) {
-            if (sub < p.units_k)
-                load(r, static_cast<const ST *>(p.k) + t * p.k_stride + (h - p.hq) * p.k_head, ca,
-                     cb);
-        } else if (sub < p.units_v) {
-            load(r, static_cast<const ST *>(p.v) + t * p.v_stride +
-                        (h - p.hq - p.hkv) * p.v_head, va, va + 4);
+    // the next row to load: the lane's first columns, and where a row ends and another tensor starts
+    const ST *src;
+    int64_t step;
+    int f = h0, second = apart;
+    bool has = has_k;
+    auto source = [&](int h) {
+        if (h >= hv) {
+            src = static_cast<const ST *>(p.v) + t * p.v_stride + (h - hv) * p.v_head + va;
+            step = p.v_head;
+            second = 4;
+            has = has_v;
+        } else if (h >= hk) {
+            src = static_cast<const ST *>(p.k) + t * p.k_stride + (h - hk) * p.k_head + ca;
+            step = p.k_head;
+        } else {
+            src = static_cast<const ST *>(p.q) + t * p.q_stride + h * p.q_head + ca;
+            step = p.q_head;
         }
+    };
+    source(h0);
+    Raw<ST> raw[kAhead] = {};
+    auto fetch = [&](Raw<ST> &r) {
+        if (has) load(r, src, second);
+        ++f;
+        src += step;
+        if (f == hk || f == hv) source(f);
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (h0 + i < h1) fetch(raw[i], h0 + i);
+        if (h0 + i < h1) fetch(raw[i]);
 
     int64_t k_at = -1, v_at = -1; // the slot's rows
-    float2 u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = make_float2(1.f, 0.f);
+    float2 cs[2], sn[2];          // cosines and sines of two pairs each
+    cs[0] = cs[1] = make_float2(1.f, 1.f);
+    sn[0] = sn[1] = make_float2(0.f, 0.f);
     if (live) {
         const int64_t slot = p.slot_map ? p.slot_map[t] : t;
         if (slot >= 0 && slot < p.slots) {
@@ -187,7 +212,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
             k_at = blk * p.kb + at * p.kp;
             v_at = blk * p.vb + at * p.vp;
         }
-        if (turns && h0 < p.hq + p.hkv) {
+        if (turns && h0 < hv) {
+            float2 u[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = sub * 4 + i;
@@ -196,74 +222,171 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
                 u[i].x *= p.factor;
                 u[i].y *= p.factor;
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                cs[i] = make_float2(u[2 * i].x, u[2 * i + 1].x);
+                sn[i] = make_float2(u[2 * i].y, u[2 * i + 1].y);
+            }
         }
     }
-    float g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = 1.f;
-
-    auto row = [&](float *x, int h) {
-        if (h >= p.hq + p.hkv) {
-            if (sub < p.units_v && v_at >= 0)
-                store(p.v_pool, p.cache_dtype, v_at + (h - p.hq - p.hkv) * p.vh, va, va + 4, x);
-            return;
-        }
-        const bool is_k = h >= p.hq, mine = live && sub < p.units_k;
-        const int hh = is_k ? h - p.hq : h;
-        if (p.norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const int64_t step = is_k ? p.kw_head : p.qw_head;
-            if (mine && (h == h0 || h == p.hq || step)) { // the weights of this head
-                const void *wt = is_k ? p.k_weight : p.q_weight;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = 1.f;
-                if (wt) {
-                    if (p.w_dtype == DA_F32) load_as<float>(wt, hh * step, ca, cb, g);
-                    else if (p.w_dtype == DA_F16) load_as<__half>(wt, hh * step, ca, cb, g);
-                    else load_as<__nv_bfloat16>(wt, hh * step, ca, cb, g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] += p.offset;
-                }
-            }
-            const float inv = 1.f / sqrtf(fmaf(ss, p.inv_dim, p.eps));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * g[i];
-        }
-        if (turns) {
-            if (p.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[2 * i], b = x[2 * i + 1];
-                    x[2 * i] = a * u[i].x - b * u[i].y;
-                    x[2 * i + 1] = b * u[i].x + a * u[i].y;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[i], b = x[i + 4];
-                    x[i] = a * u[i].x - b * u[i].y;
-                    x[i + 4] = b * u[i].x + a * u[i].y;
-                }
-            }
-        }
-        if (!mine) return;
-        if (is_k) {
-            if (k_at >= 0) store(p.k_pool, p.cache_dtype, k_at + hh * p.kh, ca, cb, x);
+    // the row to write, in bytes
+    uint8_t *dst;
+    int64_t to_next;
+    int dtype, apart_to;
+    bool writes;
+    auto target = [&](int h) {
+        if (h < hk) {
+            dst = static_cast<uint8_t *>(p.q_out) + (t * p.qo_stride + h * p.qo_head + ca) * p.q_size;
+            to_next = p.qo_head * p.q_size;
+            dtype = p.q_dtype;
+            writes = has_k;
+        } else if (h < hv) {
+            dst = static_cast<uint8_t *>(p.k_pool) + (k_at + (h - hk) * p.kh + ca) * p.cache_size;
+            to_next = p.kh * p.cache_size;
+            dtype = p.cache_dtype;
+            writes = has_k && k_at >= 0;
         } else {
-            store(p.q_out, p.q_dtype, t * p.qo_stride + hh * p.qo_head, ca, cb, x);
+            dst = static_cast<uint8_t *>(p.v_pool) + (v_at + (h - hv) * p.vh + va) * p.cache_size;
+            to_next = p.vh * p.cache_size;
+            dtype = p.cache_dtype;
+            writes = has_v && v_at >= 0;
+        }
+        apart_to = h < hv ? apart : 4;
+    };
+    // the norm's weights of a head
+    float2 g[4];
+    const void *weight = nullptr;
+    int64_t weight_at = 0, weight_step = 0;
+    auto weights = [&]() {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = 1.f;
+        if (weight && has_k) {
+            if (p.w_dtype == DA_F32) load_as<float>(weight, weight_at, apart, y);
+            else if (p.w_dtype == DA_F16) load_as<__half>(weight, weight_at, apart, y);
+            else load_as<__nv_bfloat16>(weight, weight_at, apart, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += p.offset;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = make_float2(y[2 * i], y[2 * i + 1]);
+    };
+    auto norm_of = [&](int h) { // from row h on
+        const bool is_k = h >= hk;
+        weight = is_k ? p.k_weight : p.q_weight;
+        weight_step = is_k ? p.kw_head : p.qw_head;
+        weight_at = (is_k ? h - hk : h) * weight_step + ca;
+        weights();
+    };
+
+    // normalised and turned: N rows' columns (0 1), (2 3) of the lane's first four and its second four
+    auto turn = [&](auto count, float2 (*x)[4]) {
+        constexpr int N = decltype(count)::value;
+        if (NORM) {
+            float sum[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                float2 ss = __fmul2_rn(x[k][0], x[k][0]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) ss = __ffma2_rn(x[k][i], x[k][i], ss);
+                sum[k] = ss.x + ss.y;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                if (o >= p.lanes) continue;
+#pragma unroll
+                for (int k = 0; k < N; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float inv = inv_root(fmaf(sum[k], p.inv_dim, p.eps));
+                const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[k][i] = __fmul2_rn(__fmul2_rn(x[k][i], inv2), g[i]);
+            }
+        }
+        if (!turns) return;
+        if (p.interleaved) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 z = x[k][i];
+                    const float c = i & 1 ? cs[i / 2].y : cs[i / 2].x;
+                    const float s = i & 1 ? sn[i / 2].y : sn[i / 2].x;
+                    x[k][i] = make_float2(z.x * c - z.y * s, z.y * c + z.x * s);
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 y = x[k][i], z = x[k][i + 2], minus = make_float2(-sn[i].x, -sn[i].y);
+                    x[k][i] = __ffma2_rn(z, minus, __fmul2_rn(y, cs[i]));
+                    x[k][i + 2] = __ffma2_rn(y, sn[i], __fmul2_rn(z, cs[i]));
+                }
         }
     };
+    auto widened = [&](const Raw<ST> &r, float2 *y) {
+        float x[8];
+        widen<ST>(r, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
+    };
+    auto put = [&](uint8_t *to, const float2 *y) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = y[i].x;
+            x[2 * i + 1] = y[i].y;
+        }
+        store(to, dtype, apart_to, x);
+    };
+    // behind `row` and before the next one
+    auto advance = [&](int row) {
+        dst += to_next;
+        const int next = row + 1;
+        if (next == hk || next == hv) {
+            target(next);
+            if (NORM && next == hk && next < h1) norm_of(next);
+        } else if (NORM && weight_step && next < hv) {
+            weight_at += weight_step;
+            weights();
+        }
+    };
+
+    target(h0);
+    if (NORM && h0 < hv) norm_of(h0);
     for (int h = h0; h < h1; h += kAhead) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (h + i >= h1) break;
-            float x[8];
-            widen<ST>(raw[i], x);
-            if (h + i + kAhead < h1) fetch(raw[i], h + i + kAhead);
-            row(x, h + i);
+        for (int i = 0; i < kAhead; i += 2) {
+            const int row = h + i;
+            if (row >= h1) break;
+            float2 y[2][4];
+            widened(raw[i], y[0]);
+            widened(raw[i + 1], y[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (f < h1) fetch(raw[i + k]);
+            const bool pair = row + 1 < h1 && row + 1 != hk && row + 1 != hv && !(NORM && weight_step);
+            if (pair) { // two rows of a tensor: their steps side by side
+                if (row < hv) turn(std::integral_constant<int, 2>(), y);
+                if (writes) {
+                    put(dst, y[0]);
+                    put(dst + to_next, y[1]);
+                }
+                dst += to_next;
+                advance(row + 1);
+                continue;
+            }
+#pragma unroll 1
+            for (int k = row; k < min(row + 2, h1); ++k) {
+                if (k < hv) turn(std::integral_constant<int, 1>(), y);
+                if (writes) put(dst, y[0]);
+                advance(k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[0][e] = y[1][e];
+            }
         }
     }
 }
@@ -353,7 +476,7 @@ extern "C" int decode_attn_rope_append(const da_prep_t *a, const da_rope_t *rope
     p.pairs = rope->rot_dim / 2;
     p.interleaved = rope->interleaved != 0;
     p.q_dtype = a->q_dtype; p.cache_dtype = a->cache_dtype; p.w_dtype = a->w_dtype;
-    p.norm = a->norm;
+    p.q_size = qs; p.cache_size = cs;
     p.eps = a->eps; p.offset = a->weight_offset; p.factor = rope->factor;
     p.inv_dim = 1.f / (float)a->head_dim;
     for (int i = 0; i < kMaxPairs; ++i) p.axis[i] = i < p.pairs ? rope->axis[i] : 0;
@@ -366,9 +489,14 @@ extern "C" int decode_attn_rope_append(const da_prep_t *a, const da_rope_t *rope
     p.shares = (int)std::max<int64_t>(1, std::min<int64_t>(heads / 2, 1216 / groups));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)((groups * p.shares + kThreads / 32 - 1) / (kThreads / 32));
-    if (a->src_dtype == DA_F32) prep_kernel<float><<<grid, kThreads, 0, st>>>(p);
-    else if (a->src_dtype == DA_F16) prep_kernel<__half><<<grid, kThreads, 0, st>>>(p);
-    else prep_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
+    auto launch = [&](auto type) {
+        using ST = decltype(type);
+        if (a->norm) prep_kernel<ST, true><<<grid, kThreads, 0, st>>>(p);
+        else prep_kernel<ST, false><<<grid, kThreads, 0, st>>>(p);
+    };
+    if (a->src_dtype == DA_F32) launch(0.f);
+    else if (a->src_dtype == DA_F16) launch(__half());
+    else launch(__nv_bfloat16());
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "rope_append", cudaGetErrorString(e));
     return DA_OK;
