@@ -23,6 +23,40 @@ import torch
 from . import api as A
 
 
+def _init_tables(cache, max_batch: int, num_blocks: int, max_blocks_per_seq: int,
+                 block_size: int, max_new: Optional[int], tables_of, device,
+                 taken: int = 0) -> None:
+    """Gives a cache with pools `k` its block tables, those of another cache (tables_of), or its
+    own, whose free list leaves out the first `taken` blocks."""
+    if tables_of is not None:
+        t = tables_of
+        if (t.block_size, t.free_list.numel(), getattr(t, "shared_blocks", 0)) != \
+                (block_size, num_blocks - taken, taken):
+            raise ValueError("caches that share tables need equal pages")
+        if tuple(t.block_table.shape) != (max_batch, max_blocks_per_seq) \
+                or max_new not in (None, t.slot_map.numel()):
+            raise ValueError("caches that share tables need equal batches, widths and rows")
+        if t.block_table.device != cache.k.device:
+            raise ValueError(f"the tables are on {t.block_table.device}, not {cache.k.device}")
+        for name in ("seq_lens", "block_table", "free_list", "state", "slot_map", "cu_new",
+                     "tables"):
+            setattr(cache, name, getattr(tables_of, name))
+        return
+
+    def ints(*size):
+        return torch.zeros(*size, dtype=torch.int32, device=device)
+    cache.seq_lens = ints(max_batch)
+    cache.block_table = ints(max_batch, max_blocks_per_seq)
+    # popped from the end: the lowest block first
+    cache.free_list = torch.arange(num_blocks - 1, taken - 1, -1, dtype=torch.int32, device=device)
+    cache.state = ints(4)
+    cache.state[0] = num_blocks - taken
+    cache.slot_map = torch.full((max_new or max_batch,), -1, dtype=torch.int64, device=device)
+    cache.cu_new = ints(max_batch + 1)
+    cache.tables = A.make_tables(cache.seq_lens, cache.block_table, cache.free_list, cache.state,
+                                 block_size)
+
+
 class PagedCache8:
     """One layer's 8-bit cache for up to `max_batch` sequences of up to
     `max_blocks_per_seq * block_size` positions in `num_blocks` shared pages.
@@ -45,32 +79,8 @@ class PagedCache8:
         self.k_scale = torch.ones(num_blocks, n_kv_heads, device=device)
         self.v_scale = torch.ones(num_blocks, n_kv_heads, device=device)
         self.scales = A.make_scales(self.k_scale, self.v_scale)
-        if tables_of is not None:
-            t = tables_of
-            if (t.block_size, t.free_list.numel()) != (block_size, num_blocks):
-                raise ValueError("caches that share tables need equal pages")
-            if tuple(t.block_table.shape) != (max_batch, max_blocks_per_seq) \
-                    or max_new not in (None, t.slot_map.numel()):
-                raise ValueError("caches that share tables need equal batches, widths and rows")
-            if t.block_table.device != self.k.device:
-                raise ValueError(f"the tables are on {t.block_table.device}, not {self.k.device}")
-            for name in ("seq_lens", "block_table", "free_list", "state", "slot_map", "cu_new",
-                         "tables"):
-                setattr(self, name, getattr(tables_of, name))
-        else:
-            def ints(*size):
-                return torch.zeros(*size, dtype=torch.int32, device=device)
-            self.seq_lens = ints(max_batch)
-            self.block_table = ints(max_batch, max_blocks_per_seq)
-            # popped from the end: block 0 first
-            self.free_list = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device)
-            self.state = ints(4)
-            self.state[0] = num_blocks
-            self.slot_map = torch.full((max_new or max_batch,), -1, dtype=torch.int64,
-                                       device=device)
-            self.cu_new = ints(max_batch + 1)
-            self.tables = A.make_tables(self.seq_lens, self.block_table, self.free_list,
-                                        self.state, block_size)
+        _init_tables(self, max_batch, num_blocks, max_blocks_per_seq, block_size, max_new,
+                     tables_of, device)
         self.dev = A.make_dev(seq_lens=self.seq_lens, block_table=self.block_table,
                               k_pool=self.k, v_pool=self.v)
         self._shapes = self._append = None   # of the last append's rows; shapes only

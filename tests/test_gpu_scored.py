@@ -242,6 +242,32 @@ def test_scores_that_rise_and_fall():
             c.check()
 
 
+@pytest.mark.parametrize("hq,q_len,shared", [(4, 1, 0), (20, 1, 0), (24, 4, 0), (4, 1, 512)])
+@pytest.mark.parametrize("cache,out", [("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("d", [128, 256])
+def test_references_that_move_in_some_tiles(d, cache, out, hq, q_len, shared):
+    # the largest score of a tile jumps up and down by up to 60, for each half of the heads at other
+    # tiles, so that every warpgroup raises references that the other one goes on with
+    rng = np.random.default_rng(d + hq)
+    for slopes in (False, True):
+        c = Case([1100, 129], hq, 1, d, q_len=q_len, shared=shared, cache=cache, out=out, scale=1.0,
+                 force_splits=1, slopes=slopes)
+        c.q.normal_(generator=c.g).mul_(0.05)
+        c.q[:, :, ::2, 0], c.q[:, :, 1::2, 0] = 1.0, 0.0
+        c.q[:, :, 1::2, 1], c.q[:, :, ::2, 1] = 1.0, 0.0
+        for column in (0, 1):
+            height = rng.permutation(np.linspace(0, 60, 40))
+            c.k[..., column] = 0.0
+            for b, n in enumerate(c.lens):
+                for j in range(n):
+                    if rng.random() < 0.1:
+                        at = (int(c.table[b, j // 16]), j % 16)
+                        c.k[at][..., column] = float(height[j // 32 % 40])
+            for j in range(0, shared, 9):
+                c.k[int(c.shared_table[j // 16]), j % 16, :, column] = float(height[j // 32])
+        c.check()
+
+
 def test_negative_and_zero_scales():
     Case([300, 5], 4, 2, 128, scale=-0.1).check()
     Case([300, 5], 4, 2, 128, scale=0.0).check()
@@ -260,6 +286,22 @@ def test_equal_results_in_every_run():
     first = c.run()
     for _ in range(3):
         np.testing.assert_array_equal(c.run(), first)
+
+
+@pytest.mark.parametrize("cache,out", [("f16", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("cap", [0.5, 4.0, 1000.0])
+def test_caps_near_and_far_in_one_tile(cap, cache, out):
+    # scores of 2^-20 to 2^3 of the cap, in one tile and in tiles of their own: the series and
+    # the quotient on both sides of a quarter
+    c = Case([520], 4, 1, 128, cap=cap, cache=cache, q="f32", out=out, scale=1.0)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.k[..., 1:] = 0.0
+    for j in range(520):
+        at = (int(c.table[0, j // 16]), j % 16)
+        step = j % 24 if j < 256 else (j // 64) % 8 * 3
+        c.k[at][..., 0] = cap * 2.0 ** (step - 20) * (-1) ** j
+    c.check()
 
 
 # ---- streams, graphs, errors
