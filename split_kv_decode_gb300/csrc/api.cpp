@@ -13,6 +13,7 @@
 #include <cstring>
 #include <numeric>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -1246,7 +1247,11 @@ int decode_attn_plan_scored(const da_args_t *a, const da_score_t *s, const int32
                                            a->out_dtype == DA_F32),
                           num_sms, a->force_splits};
     ScoredSplit o;
-    if (plan_scored(w, &o)) return fail(DA_EUNSUPPORTED, "plan", "too many work items");
+    try {
+        if (plan_scored(w, &o)) return fail(DA_EUNSUPPORTED, "plan", "too many work items");
+    } catch (const std::bad_alloc &) { // (the candidates' lists)
+        return fail(DA_ENOSPACE, "plan", "out of host memory");
+    }
     std::memset(sp, 0, sizeof *sp);
     da_plan_t *plan = &sp->base;
     plan->kernel = DA_KERNEL_GQA_SCORED;
