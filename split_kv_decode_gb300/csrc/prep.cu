@@ -12,14 +12,15 @@
 // give the octant and the argument of sinpi and cospi.
 //
 // Bound by memory: each row is read and written once. A warp holds one token (or 2 to 32 of
-// narrow heads) and walks its heads, or a share of them; a lane holds both columns of four
-// pairs of every head, so that it needs four angles a token, no exchange but the sum of squares, and
-// q may be rotated in place. The loads of the next four rows are in flight while two are worked on side
-// by side: a row is a chain of a sum over the lanes, a root and two products, and the instructions of
-// a row (about 120) bound it beside the memory. (32768 tokens of 16/4 heads of 256 columns, f16: 174
-// us, 4.6 TB/s; a row at a time with the branches of each row 200; six or eight rows in flight 186 to
-// 275, as their registers leave room for fewer warps.)
+// narrow heads) and walks its heads, or a share of them; a lane holds both columns of four or eight
+// pairs of every head, so that it needs four or eight angles a token, no exchange but the sum of
+// squares, and q may be rotated in place. Two rows are worked on side by side while the next two are
+// in flight: a row is a chain of a sum over the lanes, a root and two products, and its instructions
+// bound it beside the memory. (32768 tokens of 16/4 heads of 256 columns, f16: 141 us, 5.7 TB/s; with 8
+// columns a lane instead of 16 174, one row at a time 200; four rows in flight 146, fewer registers
+// 212 and more. 9999 tokens of 8/2 heads of 128, f32: 26 us, 4.3 TB/s; with four rows in flight 30.)
 #include <algorithm>
+#include <cstring>
 #include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,7 +34,7 @@ int set_error(int code, const char *phase, const char *msg); // api.cpp
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4; // rows of a warp in flight
+constexpr int kAhead = 2; // rows of a warp in flight
 constexpr int kMaxPairs = DA_MAX_ROT_PAIRS;
 
 struct PrepParams {
@@ -47,7 +48,7 @@ struct PrepParams {
     int64_t kb, kp, kh, vb, vp, vh;
     int64_t qw_head, kw_head;
     int64_t slots; // of the pools
-    int32_t tokens, hq, hkv, units_k, units_v; // 8-column units of a q/k and of a v row
+    int32_t tokens, hq, hkv, units_k, units_v; // lanes of a q/k and of a v row
     int32_t block_size, pairs, interleaved;
     int32_t q_dtype, cache_dtype, w_dtype;
     int32_t q_size, cache_size; // bytes of an element
@@ -56,76 +57,101 @@ struct PrepParams {
     uint8_t axis[kMaxPairs];
 };
 
-// twice four consecutive elements: as they are stored, and widened
-template <typename ST> struct Raw {
-    uint2 a, b;
+// twice H consecutive elements, as they are stored
+template <typename ST, int H> struct Raw {
+    static constexpr int WORDS = H * (int)sizeof(ST) / 4; // of a half: 2 or 4
+    using V = typename std::conditional<WORDS == 2, uint2, uint4>::type;
+    V a, b;
 };
-template <> struct Raw<float> {
-    uint4 a, b;
-};
-template <typename ST>
-__device__ __forceinline__ void load(Raw<ST> &r, const ST *first, int second)
+template <typename ST, int H>
+__device__ __forceinline__ void load(Raw<ST, H> &r, const ST *first, int second)
 {
-    using V = decltype(r.a);
+    using V = typename Raw<ST, H>::V;
     r.a = *reinterpret_cast<const V *>(first);
     r.b = *reinterpret_cast<const V *>(first + second);
 }
-__device__ __forceinline__ void widen2(uint32_t w, float *f, __half)
+// a word's elements (two, or one f32)
+template <typename ST> __device__ __forceinline__ float2 widen2(uint32_t w);
+template <> __device__ __forceinline__ float2 widen2<__half>(uint32_t w)
 {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    f[0] = x.x;
-    f[1] = x.y;
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
-__device__ __forceinline__ void widen2(uint32_t w, float *f, __nv_bfloat16)
+template <> __device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w)
 {
-    f[0] = __uint_as_float(w << 16);
-    f[1] = __uint_as_float(w & 0xffff0000u);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <typename ST> __device__ __forceinline__ void widen(const Raw<ST> &r, float *f)
+// N elements from `at` on
+template <typename ST, int N> __device__ __forceinline__ void widen(const uint32_t *w, float2 *f)
 {
-    widen2(r.a.x, f, ST(0.f));
-    widen2(r.a.y, f + 2, ST(0.f));
-    widen2(r.b.x, f + 4, ST(0.f));
-    widen2(r.b.y, f + 6, ST(0.f));
-}
-template <> __device__ __forceinline__ void widen<float>(const Raw<float> &r, float *f)
-{
-    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if constexpr (sizeof(ST) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+        for (int i = 0; i < N / 2; ++i)
+            f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) f[i] = widen2<ST>(w[i]);
+    }
 }
-template <typename WT>
-__device__ __forceinline__ void load_as(const void *base, int64_t at, int second, float *f)
+template <typename ST, int H> __device__ __forceinline__ void widen(const Raw<ST, H> &r, float2 *f)
 {
-    Raw<WT> r;
-    load(r, static_cast<const WT *>(base) + at, second);
-    widen<WT>(r, f);
+    uint32_t a[Raw<ST, H>::WORDS], b[Raw<ST, H>::WORDS];
+    memcpy(a, &r.a, sizeof a);
+    memcpy(b, &r.b, sizeof b);
+    widen<ST, H>(a, f);
+    widen<ST, H>(b, f + H / 2);
+}
+// four elements at a time
+template <typename WT, int H>
+__device__ __forceinline__ void load_as(const void *base, int64_t at, int second, float2 *f)
+{
+    const WT *w = static_cast<const WT *>(base) + at;
+#pragma unroll
+    for (int i = 0; i < H; i += 4)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t x[sizeof(WT)];
+            typename Raw<WT, 4>::V v =
+                *reinterpret_cast<const typename Raw<WT, 4>::V *>(w + (k ? second : 0) + i);
+            memcpy(x, &v, sizeof x);
+            widen<WT, 4>(x, f + k * (H / 2) + i / 2);
+        }
 }
 
-// f, rounded, to `first` and to `second` elements behind it
-__device__ __forceinline__ void store(uint8_t *first, int dtype, int second, const float *f)
+// twice H elements, rounded, to `first` and to `second` elements behind it
+template <int H>
+__device__ __forceinline__ void store(uint8_t *first, int dtype, int second, const float2 *f)
 {
     if (dtype == DA_F32) {
-        *reinterpret_cast<float4 *>(first) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(first + second * 4) = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < H; i += 4) {
+                const float2 x = f[k * (H / 2) + i / 2], y = f[k * (H / 2) + i / 2 + 1];
+                *reinterpret_cast<float4 *>(first + ((k ? second : 0) + i) * 4) =
+                    make_float4(x.x, x.y, y.x, y.y);
+            }
         return;
     }
-    uint32_t w[4];
+    uint32_t w[H];
     if (dtype == DA_F16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        for (int i = 0; i < H; ++i) {
+            const __half2 h = __floats2half2_rn(f[i].x, f[i].y);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        for (int i = 0; i < H; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].x, f[i].y);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    *reinterpret_cast<uint2 *>(first) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2 *>(first + second * 2) = make_uint2(w[2], w[3]);
+    using V = typename std::conditional<H == 4, uint2, uint4>::type;
+    V x, y;
+    memcpy(&x, w, sizeof x);
+    memcpy(&y, w + H / 2, sizeof y);
+    *reinterpret_cast<V *>(first) = x;
+    *reinterpret_cast<V *>(first + second * 2) = y;
 }
 
 // a^-1/2: the special function's, and one Newton step, which leaves the last rounding
@@ -148,8 +174,8 @@ __device__ __forceinline__ float2 unit(uint64_t phase)
     return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
-template <typename ST, bool NORM>
-__global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ PrepParams p)
+template <typename ST, bool NORM, int H>
+__global__ void __launch_bounds__(kThreads, H == 4 ? 5 : 4) prep_kernel(const __grid_constant__ PrepParams p)
 {
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -161,11 +187,11 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
     const int hk = p.hq, hv = p.hq + p.hkv, heads = hv + p.hkv; // the first k and v row
     const int h0 = (int)((int64_t)share * heads / p.shares);
     const int h1 = (int)((int64_t)(share + 1) * heads / p.shares);
-    const int turning = p.pairs >> 2; // lanes that hold pairs
+    const int turning = p.pairs / H; // lanes that hold pairs
     const bool turns = sub < turning;
-    // the lane's columns: both of four pairs, or eight in a row (those of a value row always)
+    // the lane's columns: both of H pairs, or 2 H in a row (those of a value row always)
     const bool halves = turns && !p.interleaved;
-    const int ca = halves ? sub * 4 : sub * 8, apart = halves ? p.pairs : 4, va = sub * 8;
+    const int ca = halves ? sub * H : sub * 2 * H, apart = halves ? p.pairs : H, va = sub * 2 * H;
     const bool has_k = live && sub < p.units_k, has_v = live && sub < p.units_v;
 
     // the next row to load: the lane's first columns, and where a row ends and another tensor starts
@@ -177,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
         if (h >= hv) {
             src = static_cast<const ST *>(p.v) + t * p.v_stride + (h - hv) * p.v_head + va;
             step = p.v_head;
-            second = 4;
+            second = H;
             has = has_v;
         } else if (h >= hk) {
             src = static_cast<const ST *>(p.k) + t * p.k_stride + (h - hk) * p.k_head + ca;
@@ -188,8 +214,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
         }
     };
     source(h0);
-    Raw<ST> raw[kAhead] = {};
-    auto fetch = [&](Raw<ST> &r) {
+    Raw<ST, H> raw[kAhead] = {};
+    auto fetch = [&](Raw<ST, H> &r) {
         if (has) load(r, src, second);
         ++f;
         src += step;
@@ -200,9 +226,12 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
         if (h0 + i < h1) fetch(raw[i]);
 
     int64_t k_at = -1, v_at = -1; // the slot's rows
-    float2 cs[2], sn[2];          // cosines and sines of two pairs each
-    cs[0] = cs[1] = make_float2(1.f, 1.f);
-    sn[0] = sn[1] = make_float2(0.f, 0.f);
+    float2 cs[H / 2], sn[H / 2];  // cosines and sines of two pairs each
+#pragma unroll
+    for (int i = 0; i < H / 2; ++i) {
+        cs[i] = make_float2(1.f, 1.f);
+        sn[i] = make_float2(0.f, 0.f);
+    }
     if (live) {
         const int64_t slot = p.slot_map ? p.slot_map[t] : t;
         if (slot >= 0 && slot < p.slots) {
@@ -213,19 +242,16 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
             v_at = blk * p.vb + at * p.vp;
         }
         if (turns && h0 < hv) {
-            float2 u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = sub * 4 + i;
+            auto turn_of = [&](int j) {
                 const int64_t pos = p.positions[(int64_t)p.axis[j] * p.tokens + t];
-                u[i] = unit((uint64_t)pos * p.turns[j]);
-                u[i].x *= p.factor;
-                u[i].y *= p.factor;
-            }
+                const float2 u = unit((uint64_t)pos * p.turns[j]);
+                return make_float2(u.x * p.factor, u.y * p.factor);
+            };
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                cs[i] = make_float2(u[2 * i].x, u[2 * i + 1].x);
-                sn[i] = make_float2(u[2 * i].y, u[2 * i + 1].y);
+            for (int i = 0; i < H / 2; ++i) {
+                const float2 x = turn_of(sub * H + 2 * i), y = turn_of(sub * H + 2 * i + 1);
+                cs[i] = make_float2(x.x, y.x);
+                sn[i] = make_float2(x.y, y.y);
             }
         }
     }
@@ -251,25 +277,23 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
             dtype = p.cache_dtype;
             writes = has_v && v_at >= 0;
         }
-        apart_to = h < hv ? apart : 4;
+        apart_to = h < hv ? apart : H;
     };
     // the norm's weights of a head
-    float2 g[4];
+    float2 g[H];
     const void *weight = nullptr;
     int64_t weight_at = 0, weight_step = 0;
     auto weights = [&]() {
-        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 1.f;
+        for (int i = 0; i < H; ++i) g[i] = make_float2(1.f, 1.f);
         if (weight && has_k) {
-            if (p.w_dtype == DA_F32) load_as<float>(weight, weight_at, apart, y);
-            else if (p.w_dtype == DA_F16) load_as<__half>(weight, weight_at, apart, y);
-            else load_as<__nv_bfloat16>(weight, weight_at, apart, y);
+            if (p.w_dtype == DA_F32) load_as<float, H>(weight, weight_at, apart, g);
+            else if (p.w_dtype == DA_F16) load_as<__half, H>(weight, weight_at, apart, g);
+            else load_as<__nv_bfloat16, H>(weight, weight_at, apart, g);
+            const float2 offset = make_float2(p.offset, p.offset);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += p.offset;
+            for (int i = 0; i < H; ++i) g[i] = __fadd2_rn(g[i], offset);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] = make_float2(y[2 * i], y[2 * i + 1]);
     };
     auto norm_of = [&](int h) { // from row h on
         const bool is_k = h >= hk;
@@ -279,8 +303,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
         weights();
     };
 
-    // normalised and turned: N rows' columns (0 1), (2 3) of the lane's first four and its second four
-    auto turn = [&](auto count, float2 (*x)[4]) {
+    // normalised and turned: N rows' columns (0 1), (2 3) .. of the lane's first H and its second H
+    auto turn = [&](auto count, float2 (*x)[H]) {
         constexpr int N = decltype(count)::value;
         if (NORM) {
             float sum[N];
@@ -288,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
             for (int k = 0; k < N; ++k) {
                 float2 ss = __fmul2_rn(x[k][0], x[k][0]);
 #pragma unroll
-                for (int i = 1; i < 4; ++i) ss = __ffma2_rn(x[k][i], x[k][i], ss);
+                for (int i = 1; i < H; ++i) ss = __ffma2_rn(x[k][i], x[k][i], ss);
                 sum[k] = ss.x + ss.y;
             }
 #pragma unroll
@@ -302,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
                 const float inv = inv_root(fmaf(sum[k], p.inv_dim, p.eps));
                 const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[k][i] = __fmul2_rn(__fmul2_rn(x[k][i], inv2), g[i]);
+                for (int i = 0; i < H; ++i) x[k][i] = __fmul2_rn(__fmul2_rn(x[k][i], inv2), g[i]);
             }
         }
         if (!turns) return;
@@ -310,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < N; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < H; ++i) {
                     const float2 z = x[k][i];
                     const float c = i & 1 ? cs[i / 2].y : cs[i / 2].x;
                     const float s = i & 1 ? sn[i / 2].y : sn[i / 2].x;
@@ -320,27 +344,12 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < N; ++k)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 y = x[k][i], z = x[k][i + 2], minus = make_float2(-sn[i].x, -sn[i].y);
+                for (int i = 0; i < H / 2; ++i) {
+                    const float2 y = x[k][i], z = x[k][i + H / 2], minus = make_float2(-sn[i].x, -sn[i].y);
                     x[k][i] = __ffma2_rn(z, minus, __fmul2_rn(y, cs[i]));
-                    x[k][i + 2] = __ffma2_rn(y, sn[i], __fmul2_rn(z, cs[i]));
+                    x[k][i + H / 2] = __ffma2_rn(y, sn[i], __fmul2_rn(z, cs[i]));
                 }
         }
-    };
-    auto widened = [&](const Raw<ST> &r, float2 *y) {
-        float x[8];
-        widen<ST>(r, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
-    };
-    auto put = [&](uint8_t *to, const float2 *y) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = y[i].x;
-            x[2 * i + 1] = y[i].y;
-        }
-        store(to, dtype, apart_to, x);
     };
     // behind `row` and before the next one
     auto advance = [&](int row) {
@@ -362,9 +371,9 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
         for (int i = 0; i < kAhead; i += 2) {
             const int row = h + i;
             if (row >= h1) break;
-            float2 y[2][4];
-            widened(raw[i], y[0]);
-            widened(raw[i + 1], y[1]);
+            float2 y[2][H];
+            widen<ST, H>(raw[i], y[0]);
+            widen<ST, H>(raw[i + 1], y[1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 if (f < h1) fetch(raw[i + k]);
@@ -372,8 +381,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
             if (pair) { // two rows of a tensor: their steps side by side
                 if (row < hv) turn(std::integral_constant<int, 2>(), y);
                 if (writes) {
-                    put(dst, y[0]);
-                    put(dst + to_next, y[1]);
+                    store<H>(dst, dtype, apart_to, y[0]);
+                    store<H>(dst + to_next, dtype, apart_to, y[1]);
                 }
                 dst += to_next;
                 advance(row + 1);
@@ -382,10 +391,10 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
 #pragma unroll 1
             for (int k = row; k < min(row + 2, h1); ++k) {
                 if (k < hv) turn(std::integral_constant<int, 1>(), y);
-                if (writes) put(dst, y[0]);
+                if (writes) store<H>(dst, dtype, apart_to, y[0]);
                 advance(k);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[0][e] = y[1][e];
+                for (int e = 0; e < H; ++e) y[0][e] = y[1][e];
             }
         }
     }
@@ -471,7 +480,11 @@ extern "C" int decode_attn_rope_append(const da_prep_t *a, const da_rope_t *rope
     p.qw_head = a->q_weight_head_stride; p.kw_head = a->k_weight_head_stride;
     p.slots = (int64_t)a->num_blocks * a->block_size;
     p.tokens = a->n_tokens; p.hq = a->n_heads; p.hkv = a->n_kv_heads;
-    p.units_k = a->head_dim / 8; p.units_v = a->v_dim / 8;
+    // 16 columns a lane (16-byte accesses, and the steps of a row half as often) where rows have
+    // whole ones and are of 16 bits; 8 otherwise
+    const bool wide = a->src_dtype != DA_F32 && a->head_dim % 16 == 0 && a->v_dim % 16 == 0;
+    const int columns = wide ? 16 : 8;
+    p.units_k = a->head_dim / columns; p.units_v = a->v_dim / columns;
     p.block_size = a->block_size;
     p.pairs = rope->rot_dim / 2;
     p.interleaved = rope->interleaved != 0;
@@ -489,14 +502,19 @@ extern "C" int decode_attn_rope_append(const da_prep_t *a, const da_rope_t *rope
     p.shares = (int)std::max<int64_t>(1, std::min<int64_t>(heads / 2, 1216 / groups));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)((groups * p.shares + kThreads / 32 - 1) / (kThreads / 32));
-    auto launch = [&](auto type) {
+    auto launch = [&](auto type, auto half) {
         using ST = decltype(type);
-        if (a->norm) prep_kernel<ST, true><<<grid, kThreads, 0, st>>>(p);
-        else prep_kernel<ST, false><<<grid, kThreads, 0, st>>>(p);
+        constexpr int H = decltype(half)::value;
+        if (a->norm) prep_kernel<ST, true, H><<<grid, kThreads, 0, st>>>(p);
+        else prep_kernel<ST, false, H><<<grid, kThreads, 0, st>>>(p);
     };
-    if (a->src_dtype == DA_F32) launch(0.f);
-    else if (a->src_dtype == DA_F16) launch(__half());
-    else launch(__nv_bfloat16());
+    const auto four = std::integral_constant<int, 4>();
+    const auto eight = std::integral_constant<int, 8>();
+    if (a->src_dtype == DA_F32) launch(0.f, four);
+    else if (a->src_dtype == DA_F16 && wide) launch(__half(), eight);
+    else if (a->src_dtype == DA_F16) launch(__half(), four);
+    else if (wide) launch(__nv_bfloat16(), eight);
+    else launch(__nv_bfloat16(), four);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return skv::set_error(DA_ELAUNCH, "rope_append", cudaGetErrorString(e));
     return DA_OK;
