@@ -120,6 +120,21 @@ def test_widths_and_partial_rotation(d, rot, interleaved):
          seed=d + rot).check()
 
 
+@pytest.mark.parametrize("T,hq,hkv,d,dv,rot,kw", [
+    (1301, 2, 1, 256, 256, 256, dict(src="f16", cache="f16", q_out="f16")),
+    (1216, 1, 3, 256, 256, 0, dict(src="bf16", cache="f32", q_out="f32", norm=False)),
+    (1250, 1, 1, 208, 256, 16, dict(src="f16", cache="bf16", q_out="f32", w="bf16", offset=1.0)),
+    (2435, 3, 2, 128, 128, 64, dict(interleaved=True, cache="bf16", q_out="f32", weights="heads")),
+    (4901, 2, 1, 48, 64, 32, dict(src="f16", cache="f32", q_out="bf16", weights="none")),
+    (4870, 1, 1, 56, 56, 48, dict(src="f16", cache="f16", q_out="f16")),   # half a lane over: narrow
+])
+def test_long_prompts(T, hq, hkv, d, dv, rot, kw):
+    # enough rows of 16 bits that a lane takes 16 columns
+    slots = torch.randperm(T + 32, generator=torch.Generator().manual_seed(T))[:T].tolist()
+    slots[T // 2] = -1
+    Case(T, hq, hkv, d, dv=dv, rot=rot, slots=slots, seed=rot, **kw).check()
+
+
 @pytest.mark.parametrize("norm,weights,offset,w", [(False, "none", 0.0, "f32"),
                                                    (True, "none", 1.0, "f32"),
                                                    (True, "row", 1.0, "bf16"),
