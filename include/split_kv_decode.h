@@ -746,7 +746,8 @@ int decode_attn_rope_append(const da_prep_t *shapes, const da_rope_t *rope, cons
  * the first position of the document (or behind the padding) that a sequence is in.
  * A token that sees nothing gives zeros, and so does one with o < 0 (a sequence of length 0 is an
  * unused place in the batch, with shared positions too). What keys and values hold at
- * positions that a token does not see has no effect on it, NaN and infinities included.
+ * positions that a token does not see has no effect on it, NaN and infinities included. A NaN score
+ * makes a token's head NaN; a value that is NaN or infinite and seen makes its column NaN or infinite.
  */
 typedef struct da_score_t {
     const float *slopes;        /* DEVICE float[n_heads], or NULL                      */

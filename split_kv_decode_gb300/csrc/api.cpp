@@ -1504,7 +1504,8 @@ void decode_attn_release(void)
 
 const char *decode_attn_version(void)
 {
-    return "split_kv_decode_gb300 0.3 (sm_103a: SIMT and tcgen05 GQA, 8-bit paged GQA, tcgen05 MLA, combine with projection)";
+    return "split_kv_decode_gb300 0.4 (sm_103a: SIMT and tcgen05 GQA, 8-bit paged GQA, tcgen05 MLA, combine with projection, "
+           "rotated append, scored GQA)";
 }
 
 } // extern "C"

@@ -23,27 +23,37 @@
 // Few rows leave most of the 128 lanes free. Up to 64 rows have copies at lanes 32 or 64 apart (Q
 // rows stored several times), whose warps each take a share of a tile's columns; their other weights
 // are zero. Half of the copies take the second term of the weights, so that O += P V is one set of
-// MMAs. Up to 16 rows (8 with three terms) are packed instead: the terms of q and of the weights
-// lie in different lanes of a warp, and a score is the sum over those lanes (one or two
-// shuffles). The epilogue adds the copies' results.
+// MMAs. Without shared positions up to 16 rows (8 with three terms) are packed instead: the terms of q and of the
+// weights lie in different lanes of a warp, a score is the sum over those lanes, and four threads
+// share a row. The epilogue adds the copies' results, of up to 16 rows as fragments of 16 rows, two
+// columns of every eight a thread.
 //
-// 256 columns: one term of Q lies in TMEM (128 columns), beside O (256) and two S slots of 64: the
-// MMAs of S then read half as much shared memory, and the ring has room for three tiles.
+// 256 columns, two terms: one term of Q lies in TMEM (128 columns), beside O (256) and two S slots of 64: the
+// MMAs of S then read half as much shared memory, and the ring has room for four tiles or more.
 //
-// What bounds it: memory. A tile of K and V (64 KB) takes 1.43 us at an SM's share of the rate; its MMAs
-// take 1.0 to 1.3, and the softmax of a warpgroup about 1, with two warpgroups taking tiles (or, for
-// 256 rows, row tiles) in turn; 256 columns leave TMEM for one. Many rows on shared
-// positions are bound by the MMAs.
+// What bounds it: memory, where the rows are one sequence's. A tile of K and V (64 KB) takes 1.43 us
+// at an SM's share of the rate; its MMAs take 0.6 to 1.1 and the softmax of a warpgroup 1.0 to 1.7,
+// with two warpgroups taking tiles (or, for 256 rows, row tiles) in turn. 151552 positions of 16/4 heads
+// of 256, capped, f32 q and output: 107 us, 5.8 TB/s. 32 sequences with a window of 4096, 32/8 heads
+// of 128: 102 us, 5.3 TB/s (256 equal items on 152 SMs). Four tokens under a bias, 24/4 heads of 256: 153
+// us, 5.9 TB/s. Many rows on shared positions are bound by the way of a unit of 128 rows through
+// softmax (1.7 us for 128 positions of 128 columns, 2.3 for 64 capped ones of 256) and MMAs (0.9 and
+// 1.2), of which two units overlap; the softmax warps issue an instruction every five cycles, waiting
+// for instructions and for their last results (two warps a scheduler). Measured and not kept: the next
+// columns on their way from TMEM meanwhile (70 -> 80 us for one document), 64 columns in
+// registers between the two passes (224 -> 286 for drafts), halves of 16 columns in a loop (241), caps
+// between the passes (235), one kernel for packed and other items (71 -> 76), a launch of its own for
+// the shared positions (71 -> 82), and one warpgroup at 256 columns (262 -> 252).
 //
-// Roles: one or two softmax warpgroups, a warp for the copies of K, one for those of V (pages of 16
-// positions are 16 boxes a tile, which take one warp 0.8 us to issue), a warp whose first lane issues
-// the MMAs. The K warp also works the items out and passes them on through a queue. Unit u of an
-// item is tile u, or tile u / 2 and row tile u % 2; it has S slot u % 2 and, with two warpgroups,
-// warpgroup and accumulator u % 2. The MMA order S0 S1 O0 S2 O1 S3 ... lets each unit's softmax
-// run beside the other's MMAs, and makes P of unit u - 2 read before S of unit u takes its
-// place. Warpgroups that took tiles in turn have
-// two states a row, which the epilogue joins. Every wait is bounded: one that runs out sets the
-// status word, and all roles leave.
+// Roles: two softmax warpgroups, a warp for the copies of K, one for those of V, a warp of which one
+// elected lane issues the MMAs. The K warp also works the items out and passes them on through a queue.
+// Unit u of an item is tile u, or tile u / 2 and row tile u % 2; it has S slot and warpgroup u % 2. At
+// 128 columns a warpgroup has an accumulator of its own, and a row as many states, which the
+// epilogue joins. At 256 there is one: a row's reference is handed from unit to unit through
+// shared memory, so that a unit waits for the last one's maximum but not for its weights, and
+// whichever warpgroup raises a reference rescales O. The MMA order S0 S1 O0 S2 O1 S3 ... lets each
+// unit's softmax run beside the other's MMAs, and makes P of unit u - 2 read before S of unit u takes
+// its place. Every wait is bounded: one that runs out sets the status word, and all roles leave.
 #pragma once
 #include <type_traits>
 #include <cuda_bf16.h>
