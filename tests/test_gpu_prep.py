@@ -201,6 +201,14 @@ def test_q_in_place():
     near(c.q.double().cpu().numpy(), zq, mq, "bf16")
 
 
+def test_q_in_place_of_a_long_prompt():
+    c = Case(2433, 3, 1, 128, src="f16", q_out="f16")
+    zq, mq = c.want(c.q, c.qw)
+    c.qo = c.q
+    c.run()
+    near(c.q.double().cpu().numpy(), zq, mq, "f16")
+
+
 def test_without_a_slot_map_rows_go_to_plain_buffers():
     c = Case(32, 4, 2, 128, page=32)
     c.slots = None

@@ -153,6 +153,35 @@ def test_many_sequences():
     Case(rng.integers(1, 200, 100).tolist(), 16, 16, 128, cache="f16", out="f16").check()
 
 
+@pytest.mark.parametrize("bad", [-1, 10 ** 9, "num_blocks"])
+@pytest.mark.parametrize("d,shared", [(128, 0), (256, 0), (128, 64)])
+def test_blocks_that_do_not_exist_read_as_zeros(d, shared, bad):
+    c = Case([300, 50], 8, 2, d, shared=shared)
+    o = c.setup()
+    if bad == "num_blocks":
+        bad = o.k.shape[0]
+    o.table[0, 3] = o.table[1, 1] = bad
+    if shared:
+        o.shared_table[2] = bad
+    ws, out = A.new_workspace(o.plan), torch.empty(o.q.shape, device="cuda")
+    A.decode_attn_splitk_scored(o.args, o.plan, o.dev, o.score, o.q, o.k, o.v, out, ws)
+    A.decode_attn_device_status(ws)
+    for b, i in ((0, 3), (1, 1)):
+        c.k[int(c.table[b, i])], c.v[int(c.table[b, i])] = 0.0, 0.0
+    if shared:
+        c.k[int(c.shared_table[2])], c.v[int(c.shared_table[2])] = 0.0, 0.0
+    want, mag, top = c.want()
+    near(out.double().cpu().numpy()[:, None], want, c.bound(want, mag, top))
+
+
+def test_bounds_that_reach_past_everything():
+    top = 2 ** 31 - 1
+    for kw in (dict(window=top, keep=top), dict(keep=top), dict(window=1, keep=top, keep_lens=[-5, 0, top]),
+               dict(window=1), dict(starts=[top, 0, 299], window=5), dict(starts=[-top, 300, 0], keep=9)):
+        c = Case([300, 301, 300], 8, 2, 128, q_len=2, **kw)
+        c.check()
+
+
 # ---- shared positions
 
 @pytest.mark.parametrize("shared,page", [(16, 16), (64, 32), (128, 64), (144, 48), (1024, 16),
@@ -336,6 +365,24 @@ def test_captured_steps_follow_lengths_tables_and_inputs():
         c.shared_table = torch.zeros(0, dtype=torch.int32)
         want, mag, top = c.want()
         near(out.double().cpu().numpy()[:, None], want, c.bound(want, mag, top))
+
+
+def test_two_graphs_share_a_workspace():
+    cs = [Case([500, 60], 8, 2, 256, seed=i, q_len=2) for i in range(2)]
+    ons, outs, graphs = [c.setup() for c in cs], [], []
+    ws = A.new_workspace(ons[0].plan)
+    for o in ons:
+        out = torch.empty(o.q.shape, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            A.decode_attn_splitk_scored(o.args, o.plan, o.dev, o.score, o.q, o.k, o.v, out, ws)
+        outs.append(out), graphs.append(graph)
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for c, out in zip(cs, outs):
+        want, mag, top = c.want()
+        near(out.double().cpu().numpy().reshape(want.shape), want, c.bound(want, mag, top))
 
 
 def test_two_streams_with_workspaces_of_their_own():

@@ -182,6 +182,17 @@ def test_layers_share_the_tables():
             PagedCache16(2, 10, 4, 2, 128, tables_of=a, **other)
 
 
+def test_steps_without_rows():
+    c = PagedCache16(2, 10, 4, 2, 128, block_size=16, max_new=4)
+    none = torch.zeros(0, 2, 128, device="cuda").bfloat16()
+    c.grow(torch.zeros(2, dtype=torch.int32, device="cuda"))
+    q = c.append(torch.zeros(0, 4, 128, device="cuda").bfloat16(), none, none,
+                 torch.zeros(0, dtype=torch.int64, device="cuda"))
+    assert q.shape == (0, 4, 128) and (c.k == 0).all()
+    one = torch.randn(2, 4, 128, device="cuda").bfloat16()
+    assert (ScoredStep(c, one)(one) == 0).all()  # nothing to see
+
+
 def test_refusals():
     with pytest.raises(TypeError):
         PagedCache16(2, 10, 4, 2, 128, dtype=torch.float32)
