@@ -43,7 +43,9 @@
 // columns on their way from TMEM meanwhile (70 -> 80 us for one document), 64 columns in
 // registers between the two passes (224 -> 286 for drafts), halves of 16 columns in a loop (241), caps
 // between the passes (235), one kernel for packed and other items (71 -> 76), a launch of its own for
-// the shared positions (71 -> 82), and one warpgroup at 256 columns (262 -> 252).
+// the shared positions (71 -> 82), tiles of 64 with four slots of scores and a warp for each product
+// (70 -> 71: the softmax of half a tile takes more than half as long), and one warpgroup at 256
+// columns (252 -> 262).
 //
 // Roles: two softmax warpgroups, a warp for the copies of K, one for those of V, a warp of which one
 // elected lane issues the MMAs. The K warp also works the items out and passes them on through a queue.
