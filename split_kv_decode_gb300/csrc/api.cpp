@@ -952,6 +952,10 @@ int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t
     p.q_len = q_len_of(a);
     p.hq = a->n_heads;
     p.hkv = a->n_kv_heads;
+    p.group = a->n_heads / a->n_kv_heads;
+    p.per_seq = p.group * p.q_len;
+    p.inv_group = scored_inverse(p.group);
+    p.inv_seq = scored_inverse(p.per_seq);
     p.q_f32 = s->q_dtype == DA_F32;
     p.q_terms = x.g.q_terms;
     p.out_dtype = a->out_dtype;

@@ -87,8 +87,8 @@ template <typename DT_, int D_, int TP_, bool XF_, int KIND_> struct Cfg {
     static constexpr int WARPS = NWG * 4, K_WARP = WARPS, V_WARP = WARPS + 1, MMA_WARP = WARPS + 2;
     static constexpr int THREADS = (WARPS + 4) * 32;
     // registers (168 a thread at launch, of which the last four warps leave some to the others:
-    // 8 * 192 + 4 * 120 = 12 * 168)
-    static constexpr int SOFTMAX_REGS = 192, OTHER_REGS = 120;
+    // 8 * 184 + 4 * 136 = 12 * 168)
+    static constexpr int SOFTMAX_REGS = 184, OTHER_REGS = 136;
     // TMEM columns: accumulator w at D w, S slot s at S_COL + S_SLOT s, a term of Q at Q_COL
     static constexpr bool QTM = scored_q_in_tmem(D, TP);
     static constexpr int S_COL = 256, S_SLOT = QTM ? 64 : 128, Q_COL = 384;
@@ -149,6 +149,16 @@ struct JoinRows {
 };
 static_assert(sizeof(JoinRows) == kScoredRowBytes, "rows");
 
+// rows by their group of heads, or by their sequence (see scored_inverse)
+__device__ __forceinline__ int over_group(const ScoredParams &p, int row)
+{
+    return p.group == 1 ? row : (int)__umulhi((uint32_t)row, p.inv_group);
+}
+__device__ __forceinline__ int over_seq(const ScoredParams &p, int row)
+{
+    return p.per_seq == 1 ? row : (int)__umulhi((uint32_t)row, p.inv_seq);
+}
+
 __device__ __forceinline__ int length_of(const ScoredParams &p, int b)
 {
     const int L = p.lens[b];
@@ -180,15 +190,15 @@ template <typename C>
 __device__ __forceinline__ void row_of(const ScoredParams &p, const Item &it, int row, int &b, int &h,
                                        int &own)
 {
-    const int Gh = p.hq / p.hkv, per_seq = p.q_len * Gh;
+    const int Gh = p.group, per_seq = p.per_seq;
     int rr = it.row0 + row, S = it.S;
     b = it.b;
     if (of_all<C>(it)) {
-        b = rr / per_seq;
+        b = over_seq(p, rr);
         rr -= b * per_seq;
         S = length_of(p, b);
     }
-    const int tk = rr / Gh;
+    const int tk = over_group(p, rr);
     h = it.kvh * Gh + rr - tk * Gh;
     own = S - p.q_len + tk;
 }
@@ -221,16 +231,16 @@ template <typename C> struct Lane {
                              : lane & (32 / parts - 1);
         owner = in_use && local < it.rows;
         busy = in_use && (local & ~31) < it.rows;
-        const int Gh = p.hq / p.hkv, per_seq = p.q_len * Gh;
+        const int Gh = p.group, per_seq = p.per_seq;
         int row = it.row0 + (owner ? local : 0);
         b = it.b;
         S = it.S;
         if (of_all<C>(it)) {
-            b = row / per_seq;
+            b = over_seq(p, row);
             row -= b * per_seq;
             S = length_of(p, b);
         }
-        tk = row / Gh;
+        tk = over_group(p, row);
         h = it.kvh * Gh + row - tk * Gh;
         own = S - p.q_len + tk;
         out_row = tk * p.hq + h;
@@ -242,7 +252,7 @@ template <typename C>
 __device__ __forceinline__ void get_item(const ScoredParams &p, int idx, Item &it)
 {
     constexpr int T = C::T;
-    const int per_seq = p.q_len * (p.hq / p.hkv);
+    const int per_seq = p.per_seq;
     it.last = 0;
     // (a bias by distance favours the last positions: the references are set at once)
     it.back = p.slopes != nullptr;
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint64_t *bar = ms->bar;
     volatile int *abort_flag = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int Gh = p.hq / p.hkv; // query heads per KV head
+    const int Gh = p.group;
     const int qch = p.rpad * 128; // bytes of a Q chunk
     volatile int never = 0;
 
@@ -966,7 +976,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             constexpr int parts = C::PARTS;
             const int part = me.part, reps = me.reps, span = me.span;
             const bool busy = me.busy;
-            const int per_seq = p.q_len * Gh;
+            const int per_seq = p.per_seq;
             if (nth > 0 && !wait(SB_QFREE, (uint32_t)(nth - 1) & 1u)) return false;
             tc_fence_after();
             const int64_t q_at = (((int64_t)me.b * p.q_len + me.tk) * p.hq + me.h) * D;
@@ -1041,10 +1051,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (rr >= it.rows) return (int64_t)-1;
                     int qrow = it.row0 + rr, qb = it.b;
                     if (of_all<C>(it)) {
-                        qb = qrow / per_seq;
+                        qb = over_seq(p, qrow);
                         qrow -= qb * per_seq;
                     }
-                    const int qt = qrow / Gh, qh = it.kvh * Gh + qrow - qt * Gh;
+                    const int qt = over_group(p, qrow), qh = it.kvh * Gh + qrow - qt * Gh;
                     return (((int64_t)qb * p.q_len + qt) * p.hq + qh) * D + j * 8;
                 };
                 // unit j of row rr: term x, at all copies of the row

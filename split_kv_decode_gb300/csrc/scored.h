@@ -119,6 +119,8 @@ struct ScoredParams {
     uint64_t timeout_ns;
     float scale, softcap;
     int32_t batch, rows, q_len, hq, hkv; // rows: q_len * hq
+    int32_t group, per_seq;              // query heads of a KV head; rows of a sequence: times q_len
+    uint32_t inv_group, inv_seq;         // scored_inverse of these
     int32_t q_f32, q_terms, out_dtype, whole, flags;
     int32_t window, keep;
     int32_t max_blocks, block_size, oob_block, box_rows;
@@ -135,6 +137,10 @@ struct ScoredParams {
     int32_t base[DA_MAX_BATCH + 1];  // splits before entry e
     uint8_t seq[DA_MAX_BATCH];
 };
+
+// x / d for x < 2^15 and d up to 128 is the upper word of x times ceil(2^32 / d): too much by x / 2^32 at
+// most, less than 1 / d. (d = 1: x itself)
+inline uint32_t scored_inverse(int d) { return (uint32_t)(((1ull << 32) + d - 1) / (uint64_t)d); }
 
 // by the cache's type and the output's (f32 outputs of bf16 caches take three terms)
 #define SKV_SCORED_LAUNCH(name) \
