@@ -561,13 +561,11 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
-// c tanh z. 16-bit outputs: tanh z = 1 - 2 / (1 + e^2z), off by a few 2^-23 of c. f32 outputs: for
-// |z| < 0.75, where that is far off relative to tanh z, Lambert's continued fraction to its fifth
-// term, z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4), off by less than 2^-26 there, and
-// (e^2z - 1) / (e^2z + 1) beyond; both are one quotient. (Comparisons that keep a NaN.)
-template <bool PRECISE> __device__ __forceinline__ float capped(float z, float c)
+// c tanh z. For |z| < 0.75, where (e^2z - 1) / (e^2z + 1) is far off relative to tanh z, Lambert's
+// continued fraction to its fifth term, z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4), off by less
+// than 2^-26 there; both are one quotient. (Comparisons that keep a NaN.)
+__device__ __forceinline__ float capped(float z, float c)
 {
-    if (!PRECISE) return fmaf(-2.f * c, rcp(1.f + ex2(z * (2.f * kLog2e))), c);
     z = z > 10.f ? 10.f : z;
     z = z < -10.f ? -10.f : z;
     const float t = ex2(z * (2.f * kLog2e)), zz = z * z;
@@ -1208,7 +1206,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 Scorer sc;
                 float m, l;
             } rows[PR];
-            const bool precise = p.out_dtype == DA_F32;
 #pragma unroll
             for (int k = 0; k < PR; ++k) {
                 Row &y = rows[k];
@@ -1328,12 +1325,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 x[i] = z.x;
                                 x[i + 1] = z.y;
                             }
-                        } else if (precise) {
-#pragma unroll
-                            for (int i = 0; i < N; ++i) x[i] = capped<true>(x[i], y.sc.cap);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < N; ++i) x[i] = capped<false>(x[i], y.sc.cap);
+                            for (int i = 0; i < N; ++i) x[i] = capped(x[i], y.sc.cap);
                         }
                     }
                     if (C::XF && p.slopes) {
