@@ -35,14 +35,15 @@
 // at an SM's share of the rate; its MMAs take 0.6 to 1.1 and the softmax of a warpgroup 1.0 to 1.7,
 // with two warpgroups taking tiles (or, for 256 rows, row tiles) in turn. 151552 positions of 16/4 heads
 // of 256, capped, f32 q and output: 107 us, 5.8 TB/s. 32 sequences with a window of 4096, 32/8 heads
-// of 128: 102 us, 5.3 TB/s (256 equal items on 152 SMs). Four tokens under a bias, 24/4 heads of 256: 153
-// us, 5.9 TB/s. Many rows on shared positions are bound by the way of a unit of 128 rows through
+// of 128: 101 us, 5.4 TB/s (256 equal items on 152 SMs). Four tokens under a bias, 24/4 heads of 256: 152
+// us, 6.0 TB/s. Many rows on shared positions are bound by the way of a unit of 128 rows through
 // softmax (1.7 us for 128 positions of 128 columns, 2.3 for 64 capped ones of 256) and MMAs (0.9 and
 // 1.2), of which two units overlap; the softmax warps issue an instruction every five cycles, waiting
-// for instructions and for their last results (two warps a scheduler). Measured and not kept: the next
+// for instructions and for their last results (two warps a scheduler). Measured and not kept, at the
+// figures of the time: the next
 // columns on their way from TMEM meanwhile (70 -> 80 us for one document), 64 columns in
 // registers between the two passes (224 -> 286 for drafts), halves of 16 columns in a loop (241), caps
-// between the passes (235), one kernel for packed and other items (71 -> 76), a launch of its own for
+// between the passes (235, later 209 -> 214), one kernel for packed and other items (71 -> 76), a launch of its own for
 // the shared positions (71 -> 82), tiles of 64 with four slots of scores and a warp for each product
 // (70 -> 71: the softmax of half a tile takes more than half as long), and one warpgroup at 256
 // columns (252 -> 262).
