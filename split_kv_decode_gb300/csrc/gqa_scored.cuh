@@ -39,14 +39,13 @@
 // us, 6.0 TB/s. Many rows on shared positions are bound by the way of a unit of 128 rows through
 // softmax (1.7 us for 128 positions of 128 columns, 2.3 for 64 capped ones of 256) and MMAs (0.9 and
 // 1.2), of which two units overlap; the softmax warps issue an instruction every five cycles, waiting
-// for instructions and for their last results (two warps a scheduler). Measured and not kept, at the
-// figures of the time: the next
-// columns on their way from TMEM meanwhile (70 -> 80 us for one document), 64 columns in
-// registers between the two passes (224 -> 286 for drafts), halves of 16 columns in a loop (241), caps
-// between the passes (235, later 209 -> 214), one kernel for packed and other items (71 -> 76), a launch of its own for
-// the shared positions (71 -> 82), tiles of 64 with four slots of scores and a warp for each product
-// (70 -> 71: the softmax of half a tile takes more than half as long), and one warpgroup at 256
-// columns (252 -> 262).
+// for instructions and for their last results (two warps a scheduler). Measured and not kept, in the
+// figures of the time: the next columns on their way from TMEM meanwhile (70 -> 80 us for one
+// document), 64 columns in registers between the two passes (224 -> 286 for drafts), halves of 16
+// columns in a loop (241), caps between the passes (209 -> 214), one kernel for packed and other items
+// (71 -> 76), a launch of its own for the shared positions (71 -> 82), tiles of 64 with four slots of
+// scores and a warp for each product (70 -> 71: the softmax of half a tile takes more than half as
+// long), and one warpgroup at 256 columns (252 -> 262).
 //
 // Roles: two softmax warpgroups, a warp for the copies of K, one for those of V, a warp of which one
 // elected lane issues the MMAs. The K warp also works the items out and passes them on through a queue.
