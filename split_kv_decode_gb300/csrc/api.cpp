@@ -890,6 +890,20 @@ int check_scored(const da_args_t *a, const da_score_t *s, const int32_t *lens, S
     return DA_OK;
 }
 
+ScoredWork scored_work(const da_args_t *a, const Scored &x, int num_sms)
+{
+    const int G = a->n_heads / a->n_kv_heads * q_len_of(a);
+    const int shared_rows = x.shared_tiles ? std::min(a->batch * G, x.g.tile_rows) : 0;
+    const int own_rows = std::min(G, x.g.tile_rows);
+    const bool f32 = a->out_dtype == DA_F32;
+    return {a->batch, a->n_kv_heads, x.row_groups, x.tiles, x.shared_tiles,
+            x.row_tiles, shared_rows > 128 ? 2 : 1, shared_rows,
+            own_rows, x.tile, x.g.q_terms, x.p_terms, a->head_dim,
+            scored_max_tiles(x.g, a->head_dim, x.p_terms, shared_rows, f32),
+            scored_max_tiles(x.g, a->head_dim, x.p_terms, own_rows, f32),
+            num_sms, a->force_splits};
+}
+
 // The plan's own splits of sequence b.
 int own_splits(const Scored &x, const da_plan_t &pl, int b)
 {
@@ -977,6 +991,7 @@ int launch_scored(const da_args_t *a, const da_scored_plan_t *sp, const da_dev_t
     p.row_tiles = x.row_tiles;
     p.shared_items = sp->shared_splits * a->n_kv_heads * x.row_tiles;
     p.n_items = pl.n_items;
+    p.lead = scored_lead(scored_work(a, x, pl.num_sms), p.shared_chunk, p.n_items - p.shared_items);
     for (int b = 0; b < a->batch; ++b) {
         p.lens[b] = pl.seq_lens[b];
         p.chunk[b] = pl.chunk[b] / x.tile;
@@ -1239,17 +1254,7 @@ int decode_attn_plan_scored(const da_args_t *a, const da_score_t *s, const int32
         num_sms = device_sms();
         if (num_sms < 1) return fail(DA_ECUDA, "plan", "SM count query failed");
     }
-    const int G = a->n_heads / a->n_kv_heads * q_len_of(a);
-    const int shared_rows = s->shared_len ? std::min(a->batch * G, x.g.tile_rows) : 0;
-    const int own_rows = std::min(G, x.g.tile_rows);
-    const ScoredWork w = {a->batch, a->n_kv_heads, x.row_groups, x.tiles, x.shared_tiles,
-                          x.row_tiles, shared_rows > 128 ? 2 : 1, shared_rows,
-                          own_rows, x.tile, x.g.q_terms, x.p_terms, a->head_dim,
-                          scored_max_tiles(x.g, a->head_dim, x.p_terms, shared_rows,
-                                           a->out_dtype == DA_F32),
-                          scored_max_tiles(x.g, a->head_dim, x.p_terms, own_rows,
-                                           a->out_dtype == DA_F32),
-                          num_sms, a->force_splits};
+    const ScoredWork w = scored_work(a, x, num_sms);
     ScoredSplit o;
     try {
         if (plan_scored(w, &o)) return fail(DA_EUNSUPPORTED, "plan", "too many work items");

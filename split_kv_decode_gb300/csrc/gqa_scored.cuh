@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
         };
         if (!is_v) {
-            // this warp works the items out: every other round from the last CTA to the first
+            // this warp works the items out
             int passed = 0; // items put in the queue
             auto pass_on = [&](const Item &it) {
                 const int s = passed & 1;
@@ -790,12 +790,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 return true;
             };
             const int g = gridDim.x;
-            auto nth = [&](int round) { // this CTA's item of a round
-                const int idx = round * g + (round & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
-                return round * (int64_t)g < p.n_items && idx < p.n_items ? idx : -1;
+            const ScoredOrder order = {g, C::SH ? p.shared_items : 0, p.lead};
+            auto nth = [&](int r) { // this CTA's items
+                const int64_t idx = order.item(blockIdx.x, r);
+                return idx < p.n_items ? (int)idx : -1;
             };
             Item it;
-            // (a round without an item for this CTA is the last one)
+            // (behind the first that is not there there are none)
 #pragma unroll 1
             for (int r = 0, idx = nth(0); ok && idx >= 0; ++r) {
                 const int then = nth(r + 1);

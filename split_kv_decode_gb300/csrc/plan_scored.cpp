@@ -2,7 +2,7 @@
 // items. Pure host code, no CUDA calls.
 //
 // The kernel is persistent, one CTA an SM; item i of a round goes to CTA i, every other round
-// from the last CTA to the first, the shared items before the others and those by size. The planner
+// from the last CTA to the first, the shared items before the others and those by size (ScoredOrder). The planner
 // scores candidates by that assignment, in units of a sixteenth of the time that a K and a V
 // tile take from memory at one SM's share of the rate, and keeps the cheapest.
 #include <algorithm>
@@ -31,17 +31,34 @@ void scored_order(const int32_t *tiles, const int32_t *chunk, int batch, uint8_t
     });
 }
 
+// a shared tile: its softmax and MMAs take 0.38 of its time from memory for each term of q and of the
+// weights and 128 rows
+static int64_t shared_tile_cost(int units, int terms)
+{
+    return std::max<int64_t>(kUnit, kUnit * units * terms * 5 / 13);
+}
+// of an item beside its tiles: q, the first tile's latency and the epilogue, in which copies of more
+// than 16 rows are joined in several passes; and the partials that it writes and the combine reads
+static int64_t item_cost(int tile, int head_dim, int rows)
+{
+    const int64_t fixed = (rows > 16 && rows <= 64 ? 4 : 2) * kUnit * 128 / tile;
+    return fixed + (int64_t)rows * head_dim * 8 * kUnit / ((int64_t)tile * head_dim * 4);
+}
+
+int scored_lead(const ScoredWork &w, int shared, int64_t own)
+{
+    if (own < 1) return 1;
+    int64_t tiles = 0;
+    for (int b = 0; b < w.batch; ++b) tiles += (int64_t)w.tiles[b] * w.hkv * w.row_groups;
+    const int64_t each = item_cost(w.tile, w.head_dim, w.own_rows) + kUnit * tiles / own;
+    const int64_t all = item_cost(w.tile, w.head_dim, w.shared_rows) +
+                        shared_tile_cost(w.units, w.q_terms + w.p_terms) * shared;
+    return (int)std::max<int64_t>(1, std::min<int64_t>((all + each / 2) / each, 1024));
+}
+
 int plan_scored(const ScoredWork &w, ScoredSplit *out)
 {
-    // costs of an item beside its tiles: q, the first tile's latency and the epilogue, and the
-    // partials that it writes and the combine reads, in units
-    const int64_t tile_bytes = (int64_t)w.tile * w.head_dim * 4;
-    const int64_t fixed = 2 * kUnit * 128 / w.tile;
-    auto partials = [&](int rows) { return (int64_t)rows * w.head_dim * 8 * kUnit / tile_bytes; };
-    // a shared tile: its MMAs take about a quarter of its time from memory for each term of q and of
-    // the weights and 128 rows
-    const int64_t shared_tile = std::max<int64_t>(
-        kUnit, kUnit * w.units * (w.q_terms + w.p_terms) * 10 / 40);
+    const int64_t shared_tile = shared_tile_cost(w.units, w.q_terms + w.p_terms);
 
     struct Candidate {
         std::vector<int32_t> chunk;
@@ -97,6 +114,7 @@ int plan_scored(const ScoredWork &w, ScoredSplit *out)
     for (const Candidate &c : cand) {
         const int64_t ss = w.shared_tiles ? ceil_div(w.shared_tiles, c.shared) : 0;
         int64_t items = ss * w.hkv * w.row_tiles;
+        const int64_t all = items; // of the shared positions
         int64_t most_splits = 1;
         for (int b = 0; b < w.batch; ++b) {
             const int64_t n = std::max<int64_t>(1, ceil_div(w.tiles[b], c.chunk[b]));
@@ -109,21 +127,20 @@ int plan_scored(const ScoredWork &w, ScoredSplit *out)
         const bool exact = items <= kSimulated;
         int64_t cost = 0, sum = 0, i = 0;
         load.assign((size_t)grid, 0);
+        const int lead = scored_lead(w, c.shared, items - all);
+        const ScoredOrder order_of = {(int32_t)grid, (int32_t)all, lead};
         auto add = [&](int64_t n, int64_t each) {
             sum += n * each;
-            for (int64_t k = 0; exact && k < n; ++k, ++i) {
-                const int64_t r = i / grid, at = i - r * grid;
-                load[(size_t)(r & 1 ? grid - 1 - at : at)] += each;
-            }
+            for (int64_t k = 0; exact && k < n; ++k, ++i) load[(size_t)order_of.cta((int32_t)i)] += each;
         };
         const int64_t per = (int64_t)w.hkv * w.row_tiles;
         for (int64_t s = 0; s < ss; ++s)
-            add(per, fixed + partials(w.shared_rows) +
+            add(per, item_cost(w.tile, w.head_dim, w.shared_rows) +
                          shared_tile * std::min<int64_t>(c.shared, w.shared_tiles - s * c.shared));
         scored_order(w.tiles, c.chunk.data(), w.batch, order.data());
         for (int b : order) {
             const int64_t n = std::max<int64_t>(1, ceil_div(w.tiles[b], c.chunk[b]));
-            const int64_t each = fixed + partials(w.own_rows);
+            const int64_t each = item_cost(w.tile, w.head_dim, w.own_rows);
             // (all splits but the last are of one size)
             add((n - 1) * w.hkv * w.row_groups, each + kUnit * c.chunk[b]);
             add((int64_t)w.hkv * w.row_groups,

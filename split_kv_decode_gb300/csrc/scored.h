@@ -131,6 +131,7 @@ struct ScoredParams {
     int32_t shared_len, shared_tiles, shared_chunk, shared_splits, row_tiles, shared_items;
     // then those of the sequences: entry e is sequence seq[e], (split, KV head, row group)
     int32_t n_items;
+    int32_t lead;            // items of CTAs without a shared one beside the last shared items
     int32_t lens[DA_MAX_BATCH];      // of sequence b
     int32_t chunk[DA_MAX_BATCH];     // tiles of a split of sequence b
     int32_t slot[DA_MAX_BATCH];      // sequence b's first partial: the shared splits', then its own
@@ -141,6 +142,53 @@ struct ScoredParams {
 // x / d for x < 2^15 and d up to 128 is the upper word of x times ceil(2^32 / d): too much by x / 2^32 at
 // most, less than 1 / d. (d = 1: x itself)
 inline uint32_t scored_inverse(int d) { return (uint32_t)(((1ull << 32) + d - 1) / (uint64_t)d); }
+
+// Which CTA works on which item: rounds from the first CTA to the last and back. Where the shared items
+// end inside a round, the CTAs without one work on `lead` items of sequences meanwhile.
+struct ScoredOrder {
+    int32_t grid, all, lead; // CTAs, shared items
+    // CTA c's r-th item, if there are so many
+    __host__ __device__ int64_t item(int c, int r) const
+    {
+        const int full = all / grid, rest = all - full * grid;
+        if (r < full) return (int64_t)r * grid + (r & 1 ? grid - 1 - c : c);
+        if (rest == 0) {
+            const int64_t first = (int64_t)r * grid;
+            return first + (r & 1 ? grid - 1 - c : c);
+        }
+        const int pos = full & 1 ? grid - 1 - c : c, free = grid - rest;
+        int later = r - full - 1;
+        if (pos < rest) {
+            if (later < 0) return (int64_t)full * grid + pos;
+        } else {
+            const int e = r - full, j = pos - rest;
+            if (e < lead) return (int64_t)all + (int64_t)e * free + (e & 1 ? free - 1 - j : j);
+            later = e - lead;
+        }
+        const int64_t first = (int64_t)all + (int64_t)lead * free + (int64_t)later * grid;
+        return first + ((full + 1 + later) & 1 ? grid - 1 - c : c);
+    }
+    // the CTA of item i
+    __host__ __device__ int cta(int64_t i) const
+    {
+        const int full = all / grid, rest = all - full * grid, free = grid - rest;
+        if (rest == 0 || i < all) {
+            const int64_t r = i / grid;
+            const int at = (int)(i - r * grid);
+            return r & 1 ? grid - 1 - at : at;
+        }
+        int64_t e = i - all;
+        if (e < (int64_t)lead * free) {
+            const int64_t r = e / free;
+            const int j = (int)(e - r * free), pos = rest + (r & 1 ? free - 1 - j : j);
+            return full & 1 ? grid - 1 - pos : pos;
+        }
+        e -= (int64_t)lead * free;
+        const int64_t r = e / grid;
+        const int at = (int)(e - r * grid);
+        return (full + 1 + r) & 1 ? grid - 1 - at : at;
+    }
+};
 
 // by the cache's type and the output's (f32 outputs of bf16 caches take three terms)
 #define SKV_SCORED_LAUNCH(name) \
@@ -172,6 +220,9 @@ struct ScoredSplit {
 };
 // Returns 0 on success, 1 if no split has an acceptable number of items.
 int plan_scored(const ScoredWork &w, ScoredSplit *out);
+// Items of sequences that a CTA without one of the last, partial round of shared items works on
+// meanwhile: by their costs, `own` items of sequences beside shared ones of `shared` tiles
+int scored_lead(const ScoredWork &w, int shared, int64_t own);
 // the sequences by their items' tiles, the longest first
 void scored_order(const int32_t *tiles, const int32_t *chunk, int batch, uint8_t *order);
 
