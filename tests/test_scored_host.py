@@ -250,6 +250,48 @@ def test_struct_layout_matches_the_c_compiler():
     assert got == want
 
 
+ORDER = r"""
+#include <cassert>
+#include <vector>
+#include "scored.h"
+int main()
+{
+    using namespace skv;
+    for (int grid : {1, 2, 3, 7, 152})
+        for (int all : {0, 1, 2, 5, 6, 7, 14, 128, 152, 153, 300, 304})
+            for (int lead : {1, 2, 3, 5, 1024})
+                for (int own : {1, 4, 64, 500, 2048}) {
+                    const ScoredOrder o = {grid, all, lead};
+                    const int n = all + own;
+                    std::vector<int> seen(n, 0);
+                    for (int c = 0; c < grid; ++c)
+                        for (int r = 0;; ++r) {
+                            const int64_t i = o.item(c, r);
+                            assert(i >= 0);
+                            if (i >= n) { // and none behind it
+                                for (int k = 1; k < 6; ++k) assert(o.item(c, r + k) >= n);
+                                break;
+                            }
+                            ++seen[i];
+                            assert(o.cta(i) == c);
+                        }
+                    for (int x : seen) assert(x == 1);
+                }
+    return 0;
+}
+"""
+
+
+def test_every_item_has_one_cta():
+    nvcc = B._nvcc()
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "t.cpp"), os.path.join(d, "t")
+        open(c, "w").write(ORDER)
+        subprocess.run([nvcc, "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I", B.SRC, c, "-o",
+                        exe], check=True)
+        subprocess.run([exe], check=True)
+
+
 # ---- the binding
 
 def test_make_score_refuses():
