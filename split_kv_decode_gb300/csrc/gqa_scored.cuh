@@ -1578,6 +1578,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             if (begun) {
                                 if (!last_done()) return false;
                             } else { // the accumulator starts here
+                                // (the other warpgroup may still read the last item's from it)
+                                if (!wait(SB_OFREE, (uint32_t)items & 1u)) return false;
+                                tc_fence_after();
                                 const float z[16] = {};
 #pragma unroll 1
                                 for (int c = 0; c < D; c += 16) tmem_st16(to + c, z);

@@ -136,6 +136,34 @@ def test_rows_that_are_no_numbers_reach_the_tokens_that_see_them(d, cache, out):
                         assert np.isnan(got[0, i, h]).all()
 
 
+@pytest.mark.parametrize("hq,q_len", [(2, 3), (4, 10), (30, 3)])
+@pytest.mark.parametrize("d,cache,out", [(128, "bf16", "bf16"), (128, "bf16", "f32"), (128, "f16", "f16"),
+                                         (256, "bf16", "bf16"), (256, "f16", "f32")])
+def test_rows_that_are_no_numbers_stay_with_their_sequence(d, cache, out, hq, q_len):
+    # one CTA works on sequences one after the other, packed rows, rows in copies and one copy of the
+    # rows: where an item's first tile (and that of its other warpgroup) starts its sums with a value
+    # that some of the tokens see, the last item's results are still read from there
+    lens = [260, 40, 129, 140, 64, 250, 33, 131, 70, 200] * 3
+    kw = dict(q_len=q_len, cache=cache, out=out, num_sms=1, force_splits=1, seed=d + hq)
+    clean = Case(lens, hq, 1, d, **kw)
+    tol = clean.bound(*clean.want())
+    for value in (math.nan, math.inf):
+        c = Case(lens, hq, 1, d, **kw)
+        for b, n in enumerate(lens):
+            if b % 3 == 2:                      # (numbers all through: nothing reaches them)
+                continue
+            for j in {n - 1, max(n - q_len + 1, 0)}:
+                c.v[int(c.table[b, j // 16]), j % 16, 0, (5 * b) % d] = value
+        with np.errstate(all="ignore"):
+            want = c.want()[0]
+        fine = np.isfinite(want)
+        assert not fine.all() and fine[2::3].all()
+        for _ in range(4):
+            got = c.run()
+            assert np.array_equal(np.isfinite(got), fine), np.argwhere(np.isfinite(got) != fine)[:5]
+            near(np.where(fine, got, 0.0), np.where(fine, want, 0.0), tol)
+
+
 def test_device_lengths_below_the_plan_and_unused_places():
     for kw in (dict(), dict(window=64, keep=16), dict(slopes=True, cap=9.0)):
         for q_len in (1, 3):
