@@ -52,6 +52,9 @@ class PagedCache16:
         _init_tables(self, max_batch, num_blocks, max_blocks_per_seq, block_size, max_new,
                      tables_of, device, shared_blocks)
         self.shared_table = torch.arange(shared_blocks, dtype=torch.int32, device=device)
+        # (made once: a slot map of a call's own would be written on torch's current stream, not on
+        # the call's, and its memory given to others while the call is pending)
+        self.shared_slots = torch.arange(shared_blocks * block_size, device=device)
         self.dev = A.make_dev(seq_lens=self.seq_lens, block_table=self.block_table,
                               k_pool=self.k, v_pool=self.v)
         self.rope = A.make_rope([], device=device) if rope is None else rope
@@ -82,8 +85,8 @@ class PagedCache16:
         room = self.shared_blocks * self.block_size
         if k.dim() != 3 or not 0 <= first <= room - k.shape[0]:
             raise ValueError(f"the shared blocks hold {room} positions")
-        slots = None if first == 0 else torch.arange(first, first + k.shape[0], device=k.device)
-        return self._write(q, k, v, positions, slots, q_out, stream)
+        return self._write(q, k, v, positions, self.shared_slots[first:first + k.shape[0]], q_out,
+                           stream)
 
     def _write(self, q, k, v, positions, slots, q_out, stream) -> torch.Tensor:
         if q_out is None:

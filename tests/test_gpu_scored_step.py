@@ -162,6 +162,30 @@ def test_the_8_bit_cache_takes_rotated_rows():
     assert torch.equal(Step8(cache, q_out)(q_out), Step8(other, q_out)(q_out))
 
 
+def test_shared_rows_on_a_stream_beside_a_busy_one():
+    # the call's stream is ordered behind its inputs alone, and the current one has work for longer
+    gen = torch.Generator().manual_seed(4)
+    c = PagedCache16(2, 10, 4, 2, 128, block_size=16, shared_blocks=4)
+    side = torch.cuda.Stream()
+    parts, at = [], 0
+    for n in (7, 20, 1, 36):
+        q, k, v = (torch.randn(n, h, 128, generator=gen).bfloat16().cuda() for h in (4, 2, 2))
+        parts.append((at, q, k, v, torch.arange(at, at + n, device="cuda"), torch.empty_like(q)))
+        at += n
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    for first, q, k, v, pos, q_out in parts:
+        c.append_shared(q, k, v, pos, first, q_out, stream=side)
+        torch.full((n,), 9, device="cuda")           # (takes what a call gave back)
+    side.synchronize()
+    got = [x.clone() for x in (c.k, c.v)]
+    torch.cuda.synchronize()
+    for x, i in zip(got, (2, 3)):
+        assert torch.equal(x.view(-1, 2, 128)[:64], torch.cat([p[i] for p in parts]))
+        assert (x[4:] == 0).all()
+    assert all(torch.equal(p[5], p[1]) for p in parts)
+
+
 def test_layers_share_the_tables():
     kw = dict(block_size=16, max_new=8, shared_blocks=2)
     a = PagedCache16(2, 10, 4, 2, 128, **kw)
