@@ -283,6 +283,28 @@ CUtensorMapDataType tma_dtype(int dt)
     }
 }
 
+// A 4-D map with boxes of `box`. The driver wants a context on the calling thread, which a host thread
+// that has made no CUDA call yet has none of: it takes that of its current device then, as the launch
+// behind this call would.
+CUresult encode_tiled(EncodeTiledFn enc, CUtensorMap *map, int dt, const void *base,
+                      const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                      bool sw128)
+{
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    auto encode = [&]() {
+        return enc(map, tma_dtype(dt), 4, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    int device = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess &&
+        cudaSetDevice(device) == cudaSuccess)
+        r = encode();
+    return r;
+}
+
 // 4-D map over (d, kv head, position, batch) with box (box_d, 1, rows, 1):
 // box_d = D unswizzled (SIMT kernel), or 64 columns landing 128-byte-swizzled
 // (tensor-core kernel, sw128 = true).
@@ -298,11 +320,7 @@ int encode_cache_map(CUtensorMap *map, const void *base, int dt, int D, int hkv,
     cuuint64_t strides[3] = {(cuuint64_t)(head_st * es), (cuuint64_t)(pos_st * es),
                              (cuuint64_t)(batch_st * es)};
     cuuint32_t box[4] = {(cuuint32_t)(sw128 ? 64 : D), 1, (cuuint32_t)rows, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = enc(map, tma_dtype(dt), 4, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode_tiled(enc, map, dt, base, dims, strides, box, sw128);
     if (r != CUDA_SUCCESS)
         return fail(DA_EUNSUPPORTED, "tma", "cuTensorMapEncodeTiled rejected the cache layout (%d)",
                     (int)r);
@@ -323,11 +341,7 @@ int encode_pool_map(CUtensorMap *map, const void *base, int dt, int D, int hkv, 
     cuuint64_t strides[3] = {(cuuint64_t)(head_st * es), (cuuint64_t)(pos_st * es),
                              (cuuint64_t)(block_st * es)};
     cuuint32_t box[4] = {(cuuint32_t)(sw128 ? 128 / es : D), 1, (cuuint32_t)rows, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = enc(map, tma_dtype(dt), 4, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode_tiled(enc, map, dt, base, dims, strides, box, sw128);
     if (r != CUDA_SUCCESS)
         return fail(DA_EUNSUPPORTED, "tma", "cuTensorMapEncodeTiled rejected the paged pool (%d)",
                     (int)r);

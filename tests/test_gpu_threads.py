@@ -1,0 +1,67 @@
+"""Calls from host threads other than the main one."""
+import threading
+
+import pytest
+import torch
+
+from split_kv_decode_gb300 import api as A
+from split_kv_decode_gb300.cache8 import PagedCache8, Step8
+from tests.scored_util import Case, near
+
+pytestmark = pytest.mark.gpu
+
+
+def in_a_new_thread(call):
+    """call() in a thread that has made no CUDA call; raises what it raises."""
+    failed = []
+
+    def body():
+        try:
+            call()
+        except Exception as e:                  # (to the thread that waits)
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    t = threading.Thread(target=body)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    if failed:
+        raise failed[0]
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("shared", [0, 32])
+def test_a_threads_first_call_is_scored(page, shared):
+    if shared and not page:
+        return
+    c = Case([300, 41], 8, 2, 128, page=page, shared=shared)
+    o = c.setup()
+    ws, out = A.new_workspace(o.plan), torch.empty(o.q.shape, device="cuda")
+    in_a_new_thread(lambda: A.decode_attn_splitk_scored(o.args, o.plan, o.dev, o.score, o.q, o.k,
+                                                        o.v, out, ws))
+    want, mag, top = c.want()
+    near(out.double().cpu().numpy().reshape(want.shape), want, c.bound(want, mag, top))
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_a_threads_first_call_of_the_other_kernels(dt, hq):
+    g = torch.Generator().manual_seed(hq)
+    q = torch.randn(2, hq, 128, generator=g).cuda()
+    k, v = (torch.randn(2, 500, 1, 128, generator=g).to(dt).cuda() for _ in range(2))
+    da = A.DecodeAttention(q, k, v, [500, 77])
+    out = da.new_out("cuda")
+    in_a_new_thread(lambda: da(q, k, v, out))
+    assert torch.equal(out, da(q, k, v))
+
+
+def test_a_threads_first_call_is_over_an_8_bit_cache():
+    g = torch.Generator().manual_seed(3)
+    cache = PagedCache8(2, 12, 4, 2, 128, block_size=16, max_new=40)
+    q, k, v = (torch.randn(n, h, 128, generator=g).cuda() for n, h in ((2, 8), (40, 2), (40, 2)))
+    cache.grow(torch.tensor([30, 10], dtype=torch.int32, device="cuda"))
+    cache.append(k, v)
+    step, out = Step8(cache, q), torch.empty_like(q)
+    in_a_new_thread(lambda: step(q, out))
+    assert torch.equal(out, step(q))
