@@ -509,8 +509,11 @@ template <typename OT>
 static cudaError_t launch_staged(cudaLaunchConfig_t &cfg, const CombineParams &p, int max_splits)
 {
     const int smem = combine_staged_smem_bytes(max_splits);
+    // (the same limit in every call, whatever this one needs: another host thread's call that sets a
+    // lower one in between would have the launch refused)
     cudaError_t e = cudaFuncSetAttribute(combine_staged_kernel<OT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         combine_staged_smem_bytes(kStagedMaxSplits));
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = smem;
     return cudaLaunchKernelEx(&cfg, combine_staged_kernel<OT>, p, max_splits);

@@ -2040,7 +2040,10 @@ cudaError_t launch(int grid, int smem, cudaStream_t st, const CUtensorMap &km, c
                    const ScoredParams &p)
 {
     auto *fn = gqa_scored_kernel<C>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the same limit in every call, whatever this one needs: another host thread's call that sets a
+    // lower one in between would have the launch refused)
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kScoredSmemMax);
     if (e != cudaSuccess) return e;
     fn<<<grid, C::THREADS, smem, st>>>(km, vm, p);
     return cudaGetLastError();

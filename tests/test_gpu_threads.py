@@ -6,7 +6,7 @@ import torch
 
 from split_kv_decode_gb300 import api as A
 from split_kv_decode_gb300.cache8 import PagedCache8, Step8
-from tests.scored_util import Case, near
+from tests.scored_util import DT, Case, near
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,48 @@ def test_a_threads_first_call_is_over_an_8_bit_cache():
     step, out = Step8(cache, q), torch.empty_like(q)
     in_a_new_thread(lambda: step(q, out))
     assert torch.equal(out, step(q))
+
+
+def at_once(calls, times):
+    """Each call in a thread of its own, `times` times; raises what one of them raised."""
+    start, failed = threading.Barrier(len(calls)), []
+
+    def loop(call, stream):
+        start.wait()
+        try:
+            for i in range(times):
+                call(stream)
+                if i % 500 == 499:
+                    stream.synchronize()
+        except Exception as e:                  # (to the thread that waits)
+            failed.append(e)
+
+    threads = [threading.Thread(target=loop, args=(c, torch.cuda.Stream())) for c in calls]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if failed:
+        raise failed[0]
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_scored_calls_of_other_rows_and_splits(d):
+    # 20 and 100 rows of a sequence take rings of other lengths, 4 and 40 splits other combines
+    cs = [Case([300], 20, 1, d, out="bf16", num_sms=4, force_splits=1),
+          Case([300], 100, 1, d, out="bf16", num_sms=4, force_splits=1),
+          Case([400], 4, 1, d, out="bf16", force_splits=4),
+          Case([6000], 4, 1, d, out="bf16", force_splits=40)]
+    calls, outs = [], []
+    for c in cs:
+        o = c.setup()
+        ws, out = A.new_workspace(o.plan), torch.empty(o.q.shape, dtype=DT[c.out], device="cuda")
+        calls.append(lambda s, o=o, ws=ws, out=out: A.decode_attn_splitk_scored(
+            o.args, o.plan, o.dev, o.score, o.q, o.k, o.v, out, ws, s))
+        outs.append(out)
+    at_once(calls, 5000)
+    for c, out in zip(cs, outs):
+        want, mag, top = c.want()
+        near(out.double().cpu().numpy().reshape(want.shape), want, c.bound(want, mag, top))
