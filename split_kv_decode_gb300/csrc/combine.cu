@@ -566,8 +566,11 @@ cudaError_t launch_proj_t(const CombineParams &p, int grid_x, int grid_y, cudaSt
         max_splits = 0;
     const int smem = combine_proj_smem_bytes(std::is_same<WT, float>::value ? DA_F32 : DA_BF16,
                                              p.out_dim, max_splits);
-    cudaError_t e = cudaFuncSetAttribute(combine_proj_kernel<OT, WT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the same limit in every call, as above)
+    cudaError_t e = cudaFuncSetAttribute(
+        combine_proj_kernel<OT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        combine_proj_smem_bytes(std::is_same<WT, float>::value ? DA_F32 : DA_BF16, kProjMaxOut,
+                                kStagedMaxSplits));
     if (e != cudaSuccess) return e;
     const int Z = (p.v_dim + kCombineCols - 1) / kCombineCols;
     cudaLaunchConfig_t cfg = {};

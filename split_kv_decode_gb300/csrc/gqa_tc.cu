@@ -654,7 +654,9 @@ cudaError_t launch_t(int grid, cudaStream_t st, const CUtensorMap &km, const CUt
                      const SplitParams &p, int smem)
 {
     auto *fn = gqa_tc_kernel<DT, D>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the same limit in every call, whatever this one needs: another host thread's call that sets a
+    // lower one in between would have the launch refused)
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemMax);
     if (e != cudaSuccess) return e;
     fn<<<grid, kTcThreads, smem, st>>>(km, vm, p);
     return cudaGetLastError();

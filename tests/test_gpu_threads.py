@@ -110,3 +110,24 @@ def test_scored_calls_of_other_rows_and_splits(d):
     for c, out in zip(cs, outs):
         want, mag, top = c.want()
         near(out.double().cpu().numpy().reshape(want.shape), want, c.bound(want, mag, top))
+
+
+@pytest.mark.parametrize("out_dims", [(16, 256), (256, 8)])
+def test_tensor_core_and_projected_calls_of_other_rows(out_dims):
+    # 8 and 128 rows of a KV head, and projections of other widths behind other numbers of splits
+    g = torch.Generator().manual_seed(7)
+    calls, outs, want = [], [], []
+    for (hq, splits), width in zip(((8, 40), (128, 4)), out_dims):
+        q = torch.randn(1, hq, 128, generator=g).cuda()
+        k, v = (torch.randn(1, 6000, 1, 128, generator=g).bfloat16().cuda() for _ in range(2))
+        w = torch.randn(hq, width, 128, generator=g).cuda()
+        da = A.DecodeAttention(q, k, v, [6000], force_splits=splits)
+        proj, out = A.make_proj(w), torch.empty(1, hq, width, device="cuda")
+        call = lambda s, da=da, proj=proj, q=q, k=k, v=v, w=w, out=out: A.decode_attn_splitk_proj(
+            da.args, da.plan, proj, q, k, v, out, da.workspace, s)
+        call(None)
+        calls.append(call), outs.append(out), want.append(out.clone())
+    for out in outs:
+        out.zero_()
+    at_once(calls, 5000)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
