@@ -909,12 +909,11 @@ ScoredWork scored_work(const da_args_t *a, const Scored &x, int num_sms)
     const int G = a->n_heads / a->n_kv_heads * q_len_of(a);
     const int shared_rows = x.shared_tiles ? std::min(a->batch * G, x.g.tile_rows) : 0;
     const int own_rows = std::min(G, x.g.tile_rows);
-    const bool f32 = a->out_dtype == DA_F32;
     return {a->batch, a->n_kv_heads, x.row_groups, x.tiles, x.shared_tiles,
             x.row_tiles, shared_rows > 128 ? 2 : 1, shared_rows,
             own_rows, x.tile, x.g.q_terms, x.p_terms, a->head_dim,
-            scored_max_tiles(x.g, a->head_dim, x.p_terms, shared_rows, f32),
-            scored_max_tiles(x.g, a->head_dim, x.p_terms, own_rows, f32),
+            scored_max_tiles(x.g, a->head_dim, x.p_terms, shared_rows, a->out_dtype),
+            scored_max_tiles(x.g, a->head_dim, x.p_terms, own_rows, a->out_dtype),
             num_sms, a->force_splits};
 }
 

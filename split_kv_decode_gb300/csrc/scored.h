@@ -91,18 +91,21 @@ inline ScoredGeometry scored_geometry(int D, int q_terms, int p_terms, int own_r
 
 // Tiles of an item at most. An MMA's sums are cut off at their 24th bit, so that a lane's accumulator
 // loses up to 2^-24 of itself at every addition of a term of 16 positions (measured, 1024
-// additions: 6e-5 of values of one sign, 2e-5 of N(0, 1) ones). 16-bit outputs do not see that;
-// f32 ones start a partial after at most 48 additions, which the combine adds in f32.
-inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int rows, bool f32_out)
+// additions: 6e-5 of values of one sign, 2e-5 of N(0, 1) ones). f32 outputs start a partial after at
+// most 48 additions, which the combine adds in f32; f16 ones after 1024 and bf16 ones after 8192, a
+// quarter of the output's half step. (131072 positions of 96 rows and 256 columns in one item, 16384
+// additions: 9e-4 off, more than three half steps of f16. 152 sequences of 32768 such positions take
+// 712 us as one item each, 4096 additions, and 846 as four.)
+inline int scored_max_tiles(const ScoredGeometry &g, int D, int p_terms, int rows, int out_dtype)
 {
-    if (!f32_out) return 1 << 24;
     const int T = scored_tile(D, p_terms);
     const int span = rows > 64 ? 128 : rows > 32 ? 64 : 32;
     const int reps = rows > 128 || g.rpad < span ? 1 : g.rpad / span;
     // additions of a unit to a lane (packed: a term has a lane of its own; or copies of its own, and
     // then half as many share the columns)
     const int per = T / 16 / reps * (g.kind == kScoredPacked ? 1 : p_terms);
-    const int units = 48 / (per > 1 ? per : 1);
+    const int most = out_dtype == DA_F32 ? 48 : out_dtype == DA_F16 ? 1024 : 8192;
+    const int units = most / (per > 1 ? per : 1);
     return rows > 128 || scored_accs(D) == 1 ? units : 2 * units;
 }
 

@@ -159,6 +159,70 @@ def test_plans_cover_what_is_visible(lib, kw, skw, splits, sms):
         assert max(p.chunk[:5]) // 16 <= 48 * 2 * 4
 
 
+GEOMETRY = r"""
+#include <cstdio>
+#include "scored.h"
+int main()
+{
+    int d, q, w, own;
+    long long shared;
+    while (std::scanf("%d %d %d %d %lld", &d, &q, &w, &own, &shared) == 5) {
+        const skv::ScoredGeometry g = skv::scored_geometry(d, q, w, own, shared);
+        std::printf("%d %d %d\n", g.tile_rows, g.rpad, g.kind == skv::kScoredPacked);
+    }
+    return 0;
+}
+"""
+
+
+def test_no_accumulator_takes_more_additions_than_its_output_bears(lib):
+    # the longest slices that the planner makes: one CTA, one split wanted, long contexts. A lane adds a
+    # term of 16 positions at a time; copies of its row share a tile's positions, the two
+    # accumulators of 128 columns the tiles, and packed rows' terms lie in lanes of their own
+    cases = [(d, kv, out, q, rows, shared)
+             for d in (128, 256) for kv in (N.DA_F16, N.DA_BF16)
+             for out in (N.DA_F32, N.DA_F16, N.DA_BF16) for q in (N.DA_F32, kv)
+             for rows, shared in ((1, 0), (8, 0), (9, 0), (16, 0), (20, 0), (33, 0), (40, 0), (65, 0),
+                                  (100, 0), (128, 0), (4, 1), (40, 1), (128, 1))]
+    batch, cap = 3, 1 << 20
+    given, plans = "", []
+    for d, kv, out, q, rows, shared in cases:
+        a = args(batch=batch, hq=rows, hkv=1, d=d, cap=cap, kv=kv, out=out, force_splits=1)
+        s = score(q_dtype=q, shared_len=cap * shared, shared_table=P)
+        rc, p = plan(lib, a, s, [cap, 5, cap], 1)
+        assert rc == N.DA_OK, lib.decode_attn_last_error()
+        plans.append(p)
+        terms = 3 if kv == N.DA_BF16 and out == N.DA_F32 else 2
+        given += f"{d} {terms if q == N.DA_F32 else 1} {terms} {rows} {batch * rows * shared}\n"
+    with tempfile.TemporaryDirectory() as folder:
+        c, exe = os.path.join(folder, "t.cpp"), os.path.join(folder, "t")
+        open(c, "w").write(GEOMETRY)
+        subprocess.run([B._nvcc(), "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I", B.SRC, c,
+                        "-o", exe], check=True)
+        lines = subprocess.run([exe], input=given, capture_output=True, text=True,
+                               check=True).stdout.splitlines()
+    assert len(lines) == len(cases)
+    for (d, kv, out, q, rows, shared), p, line in zip(cases, plans, lines):
+        tile_rows, rpad, packed = map(int, line.split())
+        terms = 3 if kv == N.DA_BF16 and out == N.DA_F32 else 2
+        assert p.tile == (128 if d == 128 and terms == 2 else 64)
+
+        def additions(positions, of):
+            of = min(of, tile_rows)
+            span = 32 if of <= 32 else 64 if of <= 64 else 128
+            copies = 1 if of > 128 else max(1, rpad // span)
+            own = 2 if d == 128 and of <= 128 else 1     # accumulators that take the tiles in turn
+            tiles = -(-(positions // p.tile) // own)
+            return tiles * max(1, p.tile // 16 * (1 if packed else terms) // copies)
+
+        most = {N.DA_F32: 48, N.DA_F16: 1024, N.DA_BF16: 8192}[out]
+        slices = [(p.chunk[0], rows)] + [(p.shared_chunk, batch * rows)] * shared
+        for positions, of in slices:
+            n = additions(positions, of)
+            # (and not far fewer, so that long contexts are not cut up for nothing)
+            assert most // 3 < n <= most, (d, kv, out, q, rows, shared, positions, n)
+
+
 def test_refuses_plans_of_other_arguments(lib):
     a, s = args(), score()
     rc, p = plan(lib, a, s, [4000, 100])
