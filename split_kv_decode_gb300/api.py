@@ -38,6 +38,20 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(handle)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A new tensor that a call on `stream` (None: the current one) writes. Its memory is of that
+    stream's: what the allocator gives out for another one may still be used there, by work that
+    the call is not ordered behind."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        # (0 and 1: the legacy default stream, which is torch's)
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1 \
+            else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
@@ -241,15 +255,15 @@ class DecodeAttention:
                                      device=q.device)
         self.out_dtype = out_dtype
 
-    def new_out(self, device) -> torch.Tensor:
+    def new_out(self, device, stream=None) -> torch.Tensor:
         a = self.args
         shape = (a.batch, a.n_heads, a.v_dim) if a.q_len <= 1 else \
             (a.batch, a.q_len, a.n_heads, a.v_dim)
-        return torch.empty(shape, dtype=self.out_dtype, device=device)
+        return _empty(shape, self.out_dtype, device, stream)
 
     def __call__(self, q, k_cache, v_cache, out=None, stream=None) -> torch.Tensor:
         if out is None:
-            out = self.new_out(q.device)
+            out = self.new_out(q.device, stream)
         decode_attn_splitk_ex(self.args, self.plan, q, k_cache, v_cache, out, self.workspace,
                               stream)
         return out

@@ -90,7 +90,7 @@ class PagedCache16:
 
     def _write(self, q, k, v, positions, slots, q_out, stream) -> torch.Tensor:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = A._empty(q.shape, q.dtype, q.device, stream)
         rows = (q, k, v, q_out, self.k, self.v)
         if self._prep is None or self._prep.tensors != A._prep_tensors(*rows):
             self._prep = A.make_prep(*rows, self.rope, **self._norm)
@@ -143,7 +143,7 @@ class ScoredStep:
         if tuple(q.shape) != self.shape or q.dtype != self.q_dtype:
             raise ValueError(f"planned for q of shape {self.shape} and type {self.q_dtype}")
         if out is None:
-            out = torch.empty(self.shape, dtype=self.out_dtype, device=q.device)
+            out = A._empty(self.shape, self.out_dtype, q.device, stream)
         elif tuple(out.shape) != self.shape:
             raise ValueError(f"out must be of shape {self.shape}")
         A.decode_attn_splitk_scored(self.args, self.plan, self.cache.dev, self.score, q,

@@ -148,7 +148,7 @@ class Step8:
         if q.dtype != torch.float32 or not q.is_contiguous() or q.device != c.k.device:
             raise TypeError(f"q must be contiguous float32 on {c.k.device}")
         if out is None:
-            out = torch.empty(self.shape, dtype=self.out_dtype, device=q.device)
+            out = A._empty(self.shape, self.out_dtype, q.device, stream)
         elif tuple(out.shape) != self.shape or out.dtype != self.out_dtype \
                 or not out.is_contiguous() or out.device != q.device:
             raise TypeError(f"out must be contiguous {self.out_dtype} of shape {self.shape} "

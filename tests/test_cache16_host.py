@@ -1,11 +1,15 @@
-"""PagedCache16 and ScoredStep on the host: what a call does besides its launch (no GPU)."""
+"""What calls of the caches and their steps do besides their launches (no GPU)."""
+from contextlib import contextmanager
+from types import SimpleNamespace
+
 import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
 from split_kv_decode_gb300 import _native as N
 from split_kv_decode_gb300 import api as A
-from split_kv_decode_gb300.cache16 import PagedCache16
+from split_kv_decode_gb300.cache8 import Step8
+from split_kv_decode_gb300.cache16 import PagedCache16, ScoredStep
 
 
 class Ops(TorchDispatchMode):
@@ -53,3 +57,58 @@ def test_shared_rows_bring_no_work_of_their_own(appended):
         q, k, v = rows(n)
         with pytest.raises(ValueError):
             c.append_shared(q, k, v, torch.arange(n), first)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The streams that are made current, and on which of them torch.empty makes its tensors."""
+    now, made, empty = [None], [], torch.empty
+
+    @contextmanager
+    def stream(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    def new(*args, **kw):
+        made.append(now[-1])
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: ("external", h))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch, "empty", new)
+    return made
+
+
+def test_new_outputs_are_of_the_calls_stream(appended, streams, monkeypatch):
+    # (of the current one's memory they could be written while earlier work there still uses it)
+    cache = PagedCache16(2, 10, 4, 2, 128, block_size=16, shared_blocks=3, device="cpu")
+    q, k, v = rows(2)
+    pos = torch.arange(2)
+    monkeypatch.setattr(A, "decode_attn_splitk_scored", lambda *x: None)
+    monkeypatch.setattr(A, "_splitk_8bit", lambda *x: None)
+    monkeypatch.setattr(A, "decode_attn_splitk_ex", lambda *x: None)
+    scored = ScoredStep.__new__(ScoredStep)
+    scored.shape, scored.q_dtype, scored.out_dtype = tuple(q.shape), q.dtype, torch.float32
+    scored.cache = cache
+    scored.args = scored.plan = scored.score = scored.workspace = None
+    eight = Step8.__new__(Step8)
+    eight.shape, eight.out_dtype = tuple(q.shape), torch.float16
+    eight.cache = SimpleNamespace(k=k, v=v, dev=None, scales=None)
+    eight.args = eight.plan = eight.workspace = None
+    plain = A.DecodeAttention.__new__(A.DecodeAttention)
+    plain.args, plain.out_dtype = SimpleNamespace(batch=2, n_heads=4, v_dim=128, q_len=0), torch.float32
+    plain.plan = plain.workspace = None
+    calls = [(lambda s: cache.append(q, k, v, pos, stream=s), q.dtype),
+             (lambda s: cache.append_shared(q, k, v, pos, 7, stream=s), q.dtype),
+             (lambda s: scored(q, stream=s), torch.float32),
+             (lambda s: eight(q.float(), stream=s), torch.float16),
+             (lambda s: plain(q, k, v, stream=s), torch.float32)]
+    own = SimpleNamespace(cuda_stream=99)
+    for call, dtype in calls:
+        for given, used in ((None, None), (own, own), (4096, ("external", 4096)), (0, "default"),
+                            (1, "default")):
+            streams.clear()
+            out = call(given)
+            assert streams == [used] and out.shape == q.shape and out.dtype == dtype

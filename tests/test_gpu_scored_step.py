@@ -186,6 +186,34 @@ def test_shared_rows_on_a_stream_beside_a_busy_one():
     assert all(torch.equal(p[5], p[1]) for p in parts)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_new_outputs_on_a_stream_beside_a_busy_one(handle):
+    # memory that the current stream has given back but still writes is not what a call on another
+    # stream gets for its output
+    gen = torch.Generator().manual_seed(6)
+    c = PagedCache16(2, 10, 4, 2, 128, block_size=16, max_new=32)
+    q, k, v = (torch.randn(32, h, 128, generator=gen).bfloat16().cuda() for h in (512, 2, 2))
+    c.grow(torch.tensor([20, 12], dtype=torch.int32, device="cuda"))
+    pos = torch.arange(32, device="cuda")
+    c.append(q, k, v, pos)
+    now = q[:2].contiguous()
+    step = ScoredStep(c, now[:, :8].contiguous(), out_dtype=torch.float32)
+    one = now[:, :8].contiguous()
+    want = step(one)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = [torch.empty_like(q), torch.empty_like(want)]
+    torch.cuda._sleep(50_000_000)
+    for x in held:
+        x.fill_(math.nan)
+    x = None
+    del held
+    on = side.cuda_stream if handle else side
+    rotated, got = c.append(q, k, v, pos, stream=on), step(one, stream=on)
+    torch.cuda.synchronize()
+    assert torch.equal(rotated, q) and torch.equal(got, want)
+
+
 def test_layers_share_the_tables():
     kw = dict(block_size=16, max_new=8, shared_blocks=2)
     a = PagedCache16(2, 10, 4, 2, 128, **kw)
