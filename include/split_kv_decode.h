@@ -755,7 +755,7 @@ typedef struct da_score_t {
     const int32_t *keep_lens;   /* DEVICE int32[batch], or NULL                        */
     const int32_t *shared_table;/* DEVICE int32[shared_len / block_size]: the blocks of the
                                    shared positions                                    */
-    float softcap;              /* 0: none                                             */
+    float softcap;              /* 0: none; otherwise in [2^-60, 2^60]                 */
     int32_t window;             /* 0: none                                             */
     int32_t keep;               /* bound of keep_lens, or every sequence's             */
     int32_t shared_len;         /* a multiple of dev->block_size; 0: none. Not together

@@ -694,10 +694,10 @@ def make_score(q: torch.Tensor, *, softcap: float = 0.0, slopes: Optional[torch.
                starts: Optional[torch.Tensor] = None, shared_len: int = 0,
                shared_table: Optional[torch.Tensor] = None) -> N.DaScore:
     """da_score_t for q [B, Hq, D] or [B, q_len, Hq, D] of f32 or of the cache's type: scores
-    softcap tanh(x / softcap) - slopes[h] * distance (slopes f32 [Hq]), over the positions that
-    starts (int32 [B]), keep (or keep_lens, int32 [B], bounded by keep) and window leave, and
-    over shared_len positions that all sequences share, in the blocks of shared_table (int32).
-    The descriptor keeps its tensors alive."""
+    softcap tanh(x / softcap) (softcap in [2^-60, 2^60]; 0: none) - slopes[h] * distance (slopes
+    f32 [Hq]), over the positions that starts (int32 [B]), keep (or keep_lens, int32 [B], bounded
+    by keep) and window leave, and over shared_len positions that all sequences share, in the
+    blocks of shared_table (int32). The descriptor keeps its tensors alive."""
     if q.dim() not in (3, 4):
         raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
     if shared_table is None and shared_len:

@@ -866,8 +866,10 @@ int check_scored(const da_args_t *a, const da_score_t *s, const int32_t *lens, S
         return fail(DA_EUNSUPPORTED, "args", "scored attention takes no flags (got 0x%x)", a->flags);
     if (s->q_dtype != DA_F32 && s->q_dtype != a->kv_dtype)
         return fail(DA_EINVAL, "args", "q_dtype must be f32 or the cache's type");
-    if (!std::isfinite(s->softcap) || s->softcap < 0.f)
-        return fail(DA_EINVAL, "args", "softcap must be finite and >= 0");
+    // (so that its products with a quotient's terms, and those of the scores with its inverse, stay
+    // within f32's range)
+    if (s->softcap != 0.f && !(s->softcap >= 0x1p-60f && s->softcap <= 0x1p60f))
+        return fail(DA_EINVAL, "args", "softcap must be 0 (none) or in [2^-60, 2^60]");
     if (s->window < 0 || s->keep < 0 || s->shared_len < 0 || s->shared_len > 1 << 30)
         return fail(DA_EINVAL, "args", "window and keep must be >= 0, shared_len in [0, 2^30]");
     if (s->shared_len && (s->window || s->keep || s->starts || s->keep_lens))

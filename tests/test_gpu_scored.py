@@ -361,6 +361,21 @@ def test_caps_near_and_far_in_one_tile(cap, cache, out):
     c.check()
 
 
+@pytest.mark.parametrize("cap", [2.0 ** -60, 2.0 ** -20, 2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("cache,out", [("f16", "f32"), ("bf16", "bf16")])
+def test_caps_of_every_size(cap, cache, out):
+    # (the smallest leave no score, the largest all of them; a query of zeros has scores of zero)
+    c = Case([300, 40], 4, 1, 128, cap=cap, cache=cache, q="f32", out=out)
+    c.q[:, :, 0] = 0.0
+    if cap > 1:                                 # within 2^-40 of none: of that call's precision
+        got = c.run()
+        c.cap = 0.0
+        want, mag, top = c.want()
+        near(got, want, c.bound(want, mag, top))
+    else:
+        c.check()
+
+
 # ---- streams, graphs, errors
 
 def test_captured_steps_follow_lengths_tables_and_inputs():

@@ -105,6 +105,16 @@ def test_refuses_scores(lib, kw, word):
         lib.decode_attn_last_error()
 
 
+@pytest.mark.parametrize("cap,fine", [
+    (0.0, True), (2.0 ** -60, True), (2.0 ** 60, True), (30.0, True), (-0.0, True),
+    (2.0 ** -61, False), (1e-39, False), (2.0 ** 61, False), (3e38, False)])
+def test_caps_whose_products_leave_the_range_are_refused(lib, cap, fine):
+    # (times log2 e 3e38 is infinite, and so is a score over 1e-39)
+    rc, _ = plan(lib, args(), score(softcap=cap), [8, 8])
+    assert (rc == N.DA_OK) == fine
+    assert fine or "softcap" in lib.decode_attn_last_error().decode()
+
+
 def test_refuses_lengths_and_null(lib):
     for lens in ([0, 8], [8, 4097], [-1, 8]):
         assert plan(lib, args(), score(), lens)[0] == N.DA_EINVAL
