@@ -107,8 +107,9 @@ class ScoredStep:
     """Scored attention of q [B, Hq, D] (or [B, q_len, Hq, D]; f32 or of the cache's type) over a
     PagedCache16, B at most the cache's max_batch: plan and workspace for sequences of up to
     `max_lens` positions of their own (default: the tables' width); the current lengths are the
-    cache's, on the device. softcap, slopes, window, keep, keep_lens and starts are make_score's;
-    shared_len positions of the cache's shared blocks come before every sequence's own.
+    cache's, on the device. softcap, slopes, window, keep, keep_lens and starts are make_score's
+    (keep_lens needs keep, its upper bound); shared_len positions of the cache's shared blocks come
+    before every sequence's own.
 
     The work is split for max_lens, whatever the lengths are then: a bound near them is several
     times faster than the width of mostly empty tables. Positions past it are not attended to.
@@ -124,6 +125,8 @@ class ScoredStep:
         width = cache.block_table.shape[1]
         if q.shape[0] > cache.seq_lens.numel():
             raise ValueError("q has more sequences than the cache")
+        if keep_lens is not None and keep < 1:
+            raise ValueError("keep_lens keeps nothing without keep, its upper bound")
         if shared_len > cache.shared_blocks * cache.block_size:
             raise ValueError("shared_len is more than the cache's shared blocks hold")
         sc = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)

@@ -112,3 +112,12 @@ def test_new_outputs_are_of_the_calls_stream(appended, streams, monkeypatch):
             streams.clear()
             out = call(given)
             assert streams == [used] and out.shape == q.shape and out.dtype == dtype
+
+
+@pytest.mark.parametrize("keep", [0, -1])
+def test_kept_lengths_without_their_bound_are_refused(keep):
+    # (they are bounded by keep, so that nothing would be kept)
+    cache = SimpleNamespace(k=torch.zeros(4, 16, 2, 128), block_table=torch.zeros(2, 4),
+                            seq_lens=torch.zeros(2))
+    with pytest.raises(ValueError, match="keep_lens"):
+        ScoredStep(cache, rows(2)[0], keep=keep, keep_lens=torch.zeros(2, dtype=torch.int32))
