@@ -697,7 +697,11 @@ def make_score(q: torch.Tensor, *, softcap: float = 0.0, slopes: Optional[torch.
     softcap tanh(x / softcap) (softcap in [2^-60, 2^60]; 0: none) - slopes[h] * distance (slopes
     f32 [Hq]), over the positions that starts (int32 [B]), keep (or keep_lens, int32 [B], bounded
     by keep) and window leave, and over shared_len positions that all sequences share, in the
-    blocks of shared_table (int32). The descriptor keeps its tensors alive."""
+    blocks of shared_table (int32). The descriptor keeps its tensors alive.
+
+    Kept positions are a prefix that is seen both ways: token o sees j < keep past itself too. That
+    matters where several new tokens lie among them. For kept positions that are causal there (sinks
+    behind a window of q_len positions or more), pass keep_lens of at most S_b - q_len + 1."""
     if q.dim() not in (3, 4):
         raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
     if shared_table is None and shared_len:

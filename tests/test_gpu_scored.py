@@ -90,6 +90,22 @@ def test_starts_and_kept_lengths(window, keep, q_len):
     assert (got[3] == 0).all() and (got[5] == 0).all()        # nothing left to see
 
 
+@pytest.mark.parametrize("q_len", [1, 2, 4])
+def test_kept_positions_that_are_causal(q_len):
+    # as make_score says: with keep_lens of at most S - q_len + 1 and a window of q_len or more no token
+    # sees past itself, and every one the first `keep` positions up to itself
+    keep, window = 8, 16
+
+    class Causal(Case):
+        def sees(self, b, i):
+            j, o = np.arange(self.lens[b]), self.lens[b] - self.q_len + i
+            return (j <= o) & ((j < keep) | (j > o - window))
+
+    lens = [q_len, q_len + 1, 8, 9, 10, 11, 12, 40, 300]
+    Causal(lens, 8, 2, 128, q_len=q_len, window=window, keep=keep,
+           keep_lens=[n - q_len + 1 for n in lens]).check()
+
+
 def test_what_is_not_seen_may_hold_anything():
     # evicted positions between the kept ones and the window, padding before the start
     for kw, spoil in ((dict(window=70, keep=20), range(20, 300 - 70 - 3)),
