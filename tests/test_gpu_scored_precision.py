@@ -1,9 +1,11 @@
 """The precision that scored attention promises, where a term or a bound that is lost would show."""
+import numpy as np
 import pytest
 import torch
 
 from split_kv_decode_gb300 import api as A
-from tests.scored_util import DT
+from tests import scored_terms as S
+from tests.scored_util import DT, near
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +64,21 @@ def test_long_items_beside_16_bit_outputs(cache, d, shape, shared):
     got, want = attend(q, k, v, "f16", shared)
     tol = 2.0 * (1024 * 2.0 ** -23 + 2 * (2.0 ** -16 + 2.0 ** -20)) + 2.0 ** -11
     assert (got - want).abs().max() <= tol, ((got - want).abs().max(), tol)
+
+
+@pytest.mark.parametrize("layout", S.LAYOUTS)
+@pytest.mark.parametrize("cache,out,terms", S.TYPES)
+@pytest.mark.parametrize("d", [128, 256])
+def test_every_term_of_a_query_counts(d, cache, out, terms, layout):
+    c = S.query_case(cache, out, terms, layout, d)
+    want = c.want()[0]
+    near(c.run(), want, np.full_like(want, S.query_bound(c, terms)))
+
+
+@pytest.mark.parametrize("layout", S.LAYOUTS)
+@pytest.mark.parametrize("cache,out,terms", S.WEIGHT_TYPES)
+@pytest.mark.parametrize("d", [128, 256])
+def test_every_term_of_a_weight_counts(d, cache, out, terms, layout):
+    c = S.weight_case(cache, out, terms, layout, d)
+    want = c.want()[0]
+    near(c.run() / want, np.ones_like(want), np.full_like(want, S.weight_bound(c, terms)))
