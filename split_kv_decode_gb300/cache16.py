@@ -92,10 +92,10 @@ class PagedCache16:
         if q_out is None:
             q_out = A._empty(q.shape, q.dtype, q.device, stream)
         rows = (q, k, v, q_out, self.k, self.v)
-        if self._prep is None or self._prep.tensors != A._prep_tensors(*rows):
-            self._prep = A.make_prep(*rows, self.rope, **self._norm)
-        A.decode_attn_rope_append(self._prep, q, k, v, positions, slots, q_out, self.k, self.v,
-                                  stream)
+        prep = self._prep                    # (another host thread's call may replace it)
+        if prep is None or prep.tensors != A._prep_tensors(*rows):
+            prep = self._prep = A.make_prep(*rows, self.rope, **self._norm)
+        A.decode_attn_rope_append(prep, q, k, v, positions, slots, q_out, self.k, self.v, stream)
         return q_out
 
     def check(self, stream=None) -> None:

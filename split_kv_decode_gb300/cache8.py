@@ -83,7 +83,7 @@ class PagedCache8:
                      tables_of, device)
         self.dev = A.make_dev(seq_lens=self.seq_lens, block_table=self.block_table,
                               k_pool=self.k, v_pool=self.v)
-        self._shapes = self._append = None   # of the last append's rows; shapes only
+        self._append = None                  # of the last rows, and their shapes only
 
     def grow(self, new_lens: torch.Tensor, stream=None) -> torch.Tensor:
         """Give sequence b new_lens[b] tokens (int32 [max_batch] on the device, 0: none,
@@ -98,15 +98,16 @@ class PagedCache8:
             raise ValueError(f"new rows must be [T, Hkv, D] with T <= {self.slot_map.numel()}")
         shapes = (k_new.shape, v_new.shape, k_new.stride(), v_new.stride(), k_new.dtype,
                   v_new.dtype)
-        if shapes != self._shapes:
-            self._append = A.make_append(k_new, v_new, self.k, self.v, self.k_scale, self.v_scale)
-            self._shapes = shapes
+        append = self._append                # (another host thread's call may replace it)
+        if append is None or append.shapes != shapes:
+            append = A.make_append(k_new, v_new, self.k, self.v, self.k_scale, self.v_scale)
+            append.shapes = shapes           # (of this object alone, no field of the struct)
+            self._append = append
         if not k_new.device == v_new.device == self.k.device:
             raise ValueError(f"new rows must be on {self.k.device}")
         slots, n = self.slot_map, k_new.shape[0]
-        A._append_8bit(self._append, k_new, v_new,
-                                  slots if n == slots.numel() else slots[:n], self.k, self.v,
-                                  self.k_scale, self.v_scale, stream)
+        A._append_8bit(append, k_new, v_new, slots if n == slots.numel() else slots[:n], self.k,
+                       self.v, self.k_scale, self.v_scale, stream)
 
     def check(self, stream=None) -> None:
         """Synchronises; raises if a grow() since the last check could not be served."""

@@ -8,7 +8,7 @@ from torch.utils._python_dispatch import TorchDispatchMode
 
 from split_kv_decode_gb300 import _native as N
 from split_kv_decode_gb300 import api as A
-from split_kv_decode_gb300.cache8 import Step8
+from split_kv_decode_gb300.cache8 import PagedCache8, Step8
 from split_kv_decode_gb300.cache16 import PagedCache16, ScoredStep
 
 
@@ -121,3 +121,48 @@ def test_kept_lengths_without_their_bound_are_refused(keep):
                             seq_lens=torch.zeros(2))
     with pytest.raises(ValueError, match="keep_lens"):
         ScoredStep(cache, rows(2)[0], keep=keep, keep_lens=torch.zeros(2, dtype=torch.int32))
+
+
+def test_a_call_keeps_its_descriptor_when_another_one_comes_between(appended, monkeypatch):
+    # as another host thread's call does, between this one's look at the last descriptor and its launch
+    few, more = rows(2), rows(3)
+    pos = torch.arange(3)
+    cache = PagedCache16(4, 10, 4, 2, 128, block_size=16, device="cpu")
+    cache.append(*few, pos[:2])
+    between, look = [], A._prep_tensors
+
+    def look_and_meet(*x):
+        got = look(*x)
+        if between:
+            between.pop()()
+        return got
+
+    monkeypatch.setattr(A, "_prep_tensors", look_and_meet)
+    between.append(lambda: cache.append(*more, pos))
+    appended.clear()
+    cache.append(*few, pos[:2])
+    assert sorted((x[0].n_tokens, x[1].shape[0]) for x in appended) == [(2, 2), (3, 3)]
+
+    calls = []
+    monkeypatch.setattr(A, "make_scales", lambda *x: N.DaScales())
+    monkeypatch.setattr(A, "_append_8bit", lambda *x: calls.append((x[0].n_tokens, x[1].shape[0])))
+    eight = PagedCache8(4, 10, 4, 2, 128, block_size=16, device="cpu")
+    eight.append(*few[1:])
+
+    class Meets:                                # (the slots are looked up behind the descriptor)
+        def __get__(self, cache, _):
+            if between:
+                between.pop()()
+            return torch.zeros(4, dtype=torch.int64)
+
+    kept = eight.__dict__.pop("slot_map")
+    monkeypatch.setattr(PagedCache8, "slot_map", Meets(), raising=False)
+    calls.clear()
+
+    def meet():
+        # the first look at the slots is before the descriptor's
+        between.append(lambda: eight.append(*more[1:]))
+
+    between.append(meet)
+    eight.append(*few[1:])
+    assert kept.numel() == 4 and sorted(calls) == [(2, 2), (3, 3)]
