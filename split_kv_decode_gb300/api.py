@@ -44,9 +44,10 @@ def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     the call is not ordered behind."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        # (0 and 1: the legacy default stream, which is torch's)
-        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1 \
+    if not isinstance(stream, torch.cuda.Stream):
+        # a raw handle, or what holds one (0 and 1: the legacy default stream, which is torch's)
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 \
             else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)

@@ -105,10 +105,9 @@ def test_new_outputs_are_of_the_calls_stream(appended, streams, monkeypatch):
              (lambda s: scored(q, stream=s), torch.float32),
              (lambda s: eight(q.float(), stream=s), torch.float16),
              (lambda s: plain(q, k, v, stream=s), torch.float32)]
-    own = SimpleNamespace(cuda_stream=99)
     for call, dtype in calls:
-        for given, used in ((None, None), (own, own), (4096, ("external", 4096)), (0, "default"),
-                            (1, "default")):
+        for given, used in ((None, None), (SimpleNamespace(cuda_stream=96), ("external", 96)),
+                            (4096, ("external", 4096)), (0, "default"), (1, "default")):
             streams.clear()
             out = call(given)
             assert streams == [used] and out.shape == q.shape and out.dtype == dtype
