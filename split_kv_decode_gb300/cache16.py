@@ -111,9 +111,11 @@ class ScoredStep:
     (keep_lens needs keep, its upper bound); shared_len positions of the cache's shared blocks come
     before every sequence's own.
 
-    The work is split for max_lens, whatever the lengths are then: a bound near them is several
-    times faster than the width of mostly empty tables. Positions past it are not attended to.
-    Calls that overlap on the GPU need steps of their own (one workspace each)."""
+    The work is split for max_lens, whatever the lengths are then: a bound near them is up to three
+    times faster than the width of mostly empty tables (a sequence of 4096 positions under a bound
+    of 32 times that: 39 us instead of 12.5; 32 of them: 98 instead of 89). Positions past it are
+    not attended to. Calls that overlap on the GPU need steps of their own (one workspace each). A
+    new output is memory of the call's stream."""
 
     def __init__(self, cache: PagedCache16, q: torch.Tensor, scale: Optional[float] = None, *,
                  max_lens: Optional[Sequence[int]] = None, out_dtype: Optional[torch.dtype] = None,
