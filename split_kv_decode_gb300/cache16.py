@@ -115,7 +115,8 @@ class ScoredStep:
     times faster than the width of mostly empty tables (a sequence of 4096 positions under a bound
     of 32 times that: 39 us instead of 12.5; 32 of them: 98 instead of 89). Positions past it are
     not attended to. Calls that overlap on the GPU need steps of their own (one workspace each). A
-    new output is memory of the call's stream."""
+    new output is memory of the call's stream; the cache and the step are made on the current one,
+    behind which another stream's first call has to be ordered."""
 
     def __init__(self, cache: PagedCache16, q: torch.Tensor, scale: Optional[float] = None, *,
                  max_lens: Optional[Sequence[int]] = None, out_dtype: Optional[torch.dtype] = None,
